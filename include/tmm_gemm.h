@@ -392,6 +392,130 @@ size_t sum_f32_workspace_size(int64_t n);
 int softmax_rows_f32(int64_t rows, int64_t cols, const float *x, int64_t ldx, float *y,
                      int64_t ldy, tmm_stream_t stream);
 
+/*
+ * The grouped operators: products whose right-hand matrix is chosen row by row
+ * (the experts of a mixture, the adapters of many requests).  The pages have no
+ * counterpart; the tiling is that of gemm_f32_tc3, on the same tensor cores.
+ *
+ * Element types (dtype): every matrix of a call has the same one.  FP32 sums
+ * throughout; results are rounded once.  FP32 operands are split into three
+ * bf16 parts each (exact) and six of the nine part products are added, the
+ * leading ones in FP32 registers every 128 values of the sum: normwise error
+ * below 1e-6 at any K.  An infinite FP32 entry gives NaN or an infinity in the
+ * results it enters (its lower parts are zero, and infinity times zero is NaN);
+ * 16-bit types follow IEEE.
+ *
+ * Groups: `offsets` is a DEVICE array of groups + 1 int32; group g owns the
+ * rows p with offsets[g] <= p < offsets[g+1].  Values are clamped to
+ * [0, rows], and an offset below an earlier one counts as that one, so no
+ * content of the array is unsafe.  `row_index` is a DEVICE array of `rows`
+ * int32 naming the row of x that row p reads, or NULL (row p reads x's row p);
+ * a number outside [0, x_rows) reads a row of zeros.  The groups' sizes are
+ * read on the GPU only: no call synchronises.  1 <= groups <= 512;
+ * rows, x_rows, N and K are below 2^29.
+ *
+ * Alignment: operands whose rows (and matrices) start on 16-byte boundaries
+ * are read in place in the 16-bit types; others, and every FP32 operand, are
+ * first restaged into the workspace (FP32: 6 bytes a value).
+ *
+ * workspace: DEVICE memory, 256-byte aligned, of at least the bytes that the
+ * matching *_workspace_size call gives for the same arguments (0: none needed,
+ * it may be NULL), contents scratch; calls sharing one must not overlap on the
+ * GPU.  Asynchronous on `stream`, no allocation, capturable into a graph.
+ * Results are deterministic.  Outputs must not overlap any input or the
+ * workspace (TMM_ERR_ALIAS).  Waits inside the kernels are bounded (see
+ * tmm_check_device).
+ */
+#define TMM_F32 0
+#define TMM_BF16 1
+#define TMM_F16 2
+#define TMM_MAX_GROUPS 512
+#define TMM_MAX_RANK 1024
+
+/*
+ * group_rows -- stable grouping of tokens x fan numbers.  Slot s = t*fan + j
+ * has the number index[s] (index_bits: 32 or 64, signed integers), its group
+ * when 0 <= index[s] < groups; other slots belong to no group and come last.
+ *   offsets[g]   number of slots in groups below g, g = 0 .. groups;
+ *   order[p]     the slot at place p: sorted by group, in slot order within one;
+ *   rows[p]      order[p] / fan, the token of that slot (NULL: not written);
+ *   position[s]  the place of slot s.
+ * offsets and rows are what the products below read.  DEVICE arrays of int32
+ * (index: int32 or int64), naturally aligned, caller-owned; tokens * fan below
+ * 2^31, 1 <= groups <= 512.  workspace: group_rows_workspace_size bytes,
+ * 16-byte aligned.
+ */
+int group_rows(int64_t tokens, int64_t fan, int64_t groups, const void *index, int index_bits,
+               int32_t *offsets, int32_t *order, int32_t *rows, int32_t *position,
+               void *workspace, size_t workspace_bytes, tmm_stream_t stream);
+size_t group_rows_workspace_size(int64_t tokens, int64_t fan, int64_t groups);
+
+/*
+ * gemm_grouped -- for every group g and its rows p
+ *     y[p, n] = sum_k x[r(p), k] w[g, k, n],     r(p) = row_index[p] or p.
+ * x: x_rows x K, ldx.  w: matrices stride_w elements apart, K x N each with
+ * leading dimension ldw >= N (transw = 0) or N x K with ldw >= K (transw = 1,
+ * the layout the gradient with respect to x reads: dx[p] = dy[p] w[g]^T);
+ * stride_w = 0 uses one matrix for all groups.  y: rows x N, ldy.  Rows of y
+ * that belong to no group are zero.  rows == 0 or N == 0 is a no-op, K == 0
+ * writes zeros.
+ */
+int gemm_grouped(int dtype, int transw, int64_t groups, int64_t rows, int64_t N, int64_t K,
+                 const void *x, int64_t x_rows, int64_t ldx,
+                 const int32_t *offsets, const int32_t *row_index,
+                 const void *w, int64_t ldw, int64_t stride_w,
+                 void *y, int64_t ldy,
+                 void *workspace, size_t workspace_bytes, tmm_stream_t stream);
+size_t gemm_grouped_workspace_size(int dtype, int transw, int64_t groups, int64_t rows, int64_t N,
+                                   int64_t K, const void *x, int64_t x_rows, int64_t ldx,
+                                   const void *w, int64_t ldw, int64_t stride_w);
+
+/*
+ * gemm_grouped_wgrad -- the gradient of gemm_grouped with respect to w:
+ *     dw[g, k, n] = sum_{p in group g} x[r(p), k] dy[p, n].
+ * x and row_index as there, dy: rows x N, lddy; dw: `groups` K x N matrices,
+ * lddw >= N, stride_dw >= K lddw elements apart (any value when groups == 1).
+ * A group without rows gets zeros.
+ */
+int gemm_grouped_wgrad(int dtype, int64_t groups, int64_t rows, int64_t N, int64_t K,
+                       const void *x, int64_t x_rows, int64_t ldx,
+                       const int32_t *offsets, const int32_t *row_index,
+                       const void *dy, int64_t lddy,
+                       void *dw, int64_t lddw, int64_t stride_dw,
+                       void *workspace, size_t workspace_bytes, tmm_stream_t stream);
+size_t gemm_grouped_wgrad_workspace_size(int dtype, int64_t groups, int64_t rows, int64_t N,
+                                         int64_t K, const void *x, int64_t x_rows, int64_t ldx,
+                                         const void *dy, int64_t lddy);
+
+/*
+ * gemm_lora -- a shared projection with a low-rank adapter per row:
+ *     y[t, :] = x[t, :] w + scale[g] (x[t, :] a[g]) b[g],
+ * g the group of row t.  x: rows x K, y: rows x N.  w: K x N (transw = 1:
+ * stored N x K).  a: `groups` matrices K x rank (transa = 1: rank x K), b:
+ * rank x N (transb = 1: N x rank), leading dimensions and strides as for
+ * gemm_grouped; scale: DEVICE array of `groups` FP32.  row_index names the row
+ * that place p holds, all `rows` of them once (order of group_rows), or NULL:
+ * the rows are in group order as they are.  Rows of no group get the shared
+ * projection alone, and a row that row_index does not name is not written.
+ * The product with a is rounded to dtype (FP32: kept to 24 bits) before the one
+ * with b; everything else is summed in FP32 and rounded once.  With
+ * a = w = b transposed and a and b exchanged it is the gradient with respect
+ * to x.  1 <= rank <= 1024.
+ */
+int gemm_lora(int dtype, int transw, int transa, int transb, int64_t groups, int64_t rows,
+              int64_t N, int64_t K, int64_t rank,
+              const void *x, int64_t ldx, const int32_t *offsets, const int32_t *row_index,
+              const void *w, int64_t ldw,
+              const void *a, int64_t lda, int64_t stride_a,
+              const void *b, int64_t ldb, int64_t stride_b,
+              const float *scale, void *y, int64_t ldy,
+              void *workspace, size_t workspace_bytes, tmm_stream_t stream);
+size_t gemm_lora_workspace_size(int dtype, int transw, int transa, int transb, int64_t groups,
+                                int64_t rows, int64_t N, int64_t K, int64_t rank,
+                                const void *x, int64_t ldx, const void *w, int64_t ldw,
+                                const void *a, int64_t lda, int64_t stride_a,
+                                const void *b, int64_t ldb, int64_t stride_b);
+
 /* One-line description of the calling thread's last failed call ("" if none).
  * The string is owned by the library and valid until the thread's next call. */
 const char *tmm_last_error_string(void);

@@ -12,17 +12,21 @@ one-output-per-thread contrast kernel; ``gemm_f32_tc3`` runs the product on the
 tensor cores with split-TF32 operands (it needs a workspace, allocated here
 through torch unless one is passed).  ``window_sum_f32``, ``sum_f32`` and
 ``softmax_rows_f32`` are the other tiled workloads of the same pages (sliding
-window sums, the array reduction, the two-pass row softmax).  All are
+window sums, the array reduction, the two-pass row softmax).  ``group_rows``,
+``gemm_grouped``, ``gemm_grouped_wgrad`` and ``gemm_lora`` (``grouped.py``) are
+products whose right-hand matrix is chosen row by row.  All are
 asynchronous on the current torch stream of the operands' device.
 """
 from __future__ import annotations
 
 from ._abi import (TMM_ERR_ALIAS, TMM_ERR_CUDA, TMM_ERR_INVALID_ARG,  # noqa: F401
                    TMM_ERR_UNSUPPORTED_DEVICE, TMM_OK, TmmError)
+from .grouped import (RowGroups, gemm_grouped, gemm_grouped_wgrad, gemm_lora,  # noqa: F401
+                      group_rows)
 
 __all__ = ["gemm_f32", "gemm_f32_naive", "gemm_f32_tc3", "tc3_workspace_bytes",
-           "window_sum_f32", "sum_f32", "softmax_rows_f32", "check_device", "raw_call",
-           "TmmError"]
+           "window_sum_f32", "sum_f32", "softmax_rows_f32", "group_rows", "RowGroups", "gemm_grouped",
+           "gemm_grouped_wgrad", "gemm_lora", "check_device", "raw_call", "TmmError"]
 
 
 def _matrix(x, name, allow_transposed=False):

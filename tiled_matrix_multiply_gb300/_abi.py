@@ -38,6 +38,11 @@ STATUS_NAMES = {
     TMM_ERR_BOUNDS: "TMM_ERR_BOUNDS",
 }
 
+# Element types of the grouped operators.
+TMM_F32, TMM_BF16, TMM_F16 = 0, 1, 2
+TMM_MAX_GROUPS = 512
+TMM_MAX_RANK = 1024
+
 # Entry points with the common product signature
 # (M, N, K, A, lda, B, ldb, C, ldc, stream) -> int.
 GEMM_ENTRY_POINTS = ("gemm_f32", "gemm_f32_naive")
@@ -46,6 +51,10 @@ EXPORTED = GEMM_ENTRY_POINTS + ("gemm_f32_ex", "gemm_f32_tc3", "gemm_f32_tc3_ex"
                                  "gemm_f32_tc3_workspace_size", "gemm_f32_tc3_noalloc",
                                  "window_sum_f32", "sum_f32", "sum_f32_workspace_size",
                                  "softmax_rows_f32",
+                                 "group_rows", "group_rows_workspace_size",
+                                 "gemm_grouped", "gemm_grouped_workspace_size",
+                                 "gemm_grouped_wgrad", "gemm_grouped_wgrad_workspace_size",
+                                 "gemm_lora", "gemm_lora_workspace_size",
                                  "tmm_check_device", "tmm_testing_set_wait_hooks",
                                  "tmm_testing_simt_plan", "tmm_testing_tc3_plan",
                                  "tmm_last_error_string", "tmm_version",
@@ -105,6 +114,29 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.sum_f32_workspace_size.restype = ctypes.c_size_t
         lib.softmax_rows_f32.argtypes = [i64, i64, ptr, i64, ptr, i64, ptr]
         lib.softmax_rows_f32.restype = ctypes.c_int
+        size = ctypes.c_size_t
+        lib.group_rows.argtypes = [i64, i64, i64, ptr, ci, ptr, ptr, ptr, ptr, ptr, size, ptr]
+        lib.group_rows.restype = ci
+        lib.group_rows_workspace_size.argtypes = [i64, i64, i64]
+        lib.group_rows_workspace_size.restype = size
+        lib.gemm_grouped.argtypes = [ci, ci, i64, i64, i64, i64, ptr, i64, i64, ptr, ptr, ptr, i64,
+                                     i64, ptr, i64, ptr, size, ptr]
+        lib.gemm_grouped.restype = ci
+        lib.gemm_grouped_workspace_size.argtypes = [ci, ci, i64, i64, i64, i64, ptr, i64, i64, ptr,
+                                                    i64, i64]
+        lib.gemm_grouped_workspace_size.restype = size
+        lib.gemm_grouped_wgrad.argtypes = [ci, i64, i64, i64, i64, ptr, i64, i64, ptr, ptr, ptr,
+                                           i64, ptr, i64, i64, ptr, size, ptr]
+        lib.gemm_grouped_wgrad.restype = ci
+        lib.gemm_grouped_wgrad_workspace_size.argtypes = [ci, i64, i64, i64, i64, ptr, i64, i64,
+                                                          ptr, i64]
+        lib.gemm_grouped_wgrad_workspace_size.restype = size
+        lib.gemm_lora.argtypes = [ci, ci, ci, ci, i64, i64, i64, i64, i64, ptr, i64, ptr, ptr, ptr,
+                                  i64, ptr, i64, i64, ptr, i64, i64, ptr, ptr, i64, ptr, size, ptr]
+        lib.gemm_lora.restype = ci
+        lib.gemm_lora_workspace_size.argtypes = [ci, ci, ci, ci, i64, i64, i64, i64, i64, ptr, i64,
+                                                 ptr, i64, ptr, i64, i64, ptr, i64, i64]
+        lib.gemm_lora_workspace_size.restype = size
         lib.tmm_check_device.argtypes = [ptr]
         lib.tmm_check_device.restype = ctypes.c_int
         lib.tmm_testing_set_wait_hooks.argtypes = [ctypes.c_int, i64]

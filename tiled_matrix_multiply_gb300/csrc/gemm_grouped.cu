@@ -1,0 +1,1348 @@
+// gemm_grouped.cu -- products whose right-hand matrix is chosen row by row, on the tcgen05
+// tensor cores: the grouped product, its weight gradient, and adapters beside a shared product.
+//
+//   forward   y[p, n]  = sum_k x[r(p), k] w[g, k, n]           rows p of group g
+//   gradient  dw[g, k, n] = sum_{p in g} x[r(p), k] dy[p, n]
+//   adapters  y[r(p), n] = sum_k x[r(p), k] w[k, n] + sum_j u[p, j] b[g, j, n],
+//             u[p, j] = scale[g] sum_k x[r(p), k] a[g, k, j]   (a forward product of its own)
+//
+// One kernel serves all three.  It computes tiles of D[n, q] = sum_k P[n, k] Q[q, k], with the
+// dimension that is contiguous in the result (n) on the 128 tensor-memory lanes of a block and
+// the result's rows (q) on its columns.  The columns of a tile are the ragged side: a
+// tcgen05.mma takes any multiple of 16 of them, so a group of few rows costs few columns, not a
+// whole tile, and the weights -- the larger operand when rows are few -- fill the lanes.
+//   forward:  P = w[g] (stored K x N or N x K: both majors are read in place),  Q = rows of x
+//   gradient: P = dy^T,  Q = x^T, the sum running over the group's rows
+//   adapters: the forward product with one group, its sum extended by `rank` values for every
+//             adapter that has rows in the tile: P = b[g], Q = u with the other adapters' rows
+//             read as zeros
+// Rows are fetched through the row index by the copy engine itself (four rows a copy); a row
+// number outside the matrix makes it deliver zeros, which also masks the rows past a group's
+// end in the gradient and the other adapters' rows: no operand value of another group, not even
+// a NaN, meets this group's sums.
+//
+// Single precision: every operand x is split into three bf16 parts, x = x0 + x1 + x2 exactly
+// (split3), by a pre-pass (planes).  Of the nine part products the three smallest (2^-24 of the
+// term and less) are dropped.  x0 y0 goes to one accumulator, the five smaller ones
+// (2^-8 of it and less) to another; the tensor core's additions do not round to nearest, and
+// the error of a sum grows with the number of additions made in tensor memory (16 values of K
+// each), so the first accumulator is taken out every kChunk slices and added in FP32 registers.
+// For 16-bit operands the whole sum stays in tensor memory: its error (2^-24 of the partial sum
+// per addition) is far below the result's rounding.
+//
+// Two shapes:
+//   pairs  (CG = 2): two blocks on two SMs share 256 lanes x up to 256 columns
+//          (cta_group::2): each stages half of the columns, which halves their
+//          shared-memory traffic.  For many rows per group.
+//   single (CG = 1): 128 lanes x up to 64 columns, and for few tiles a cluster of up to eight
+//          blocks that share the sum over K: each leaves its part in its shared memory, and the
+//          blocks add the parts in block order through distributed shared memory (no global
+//          scratch, no atomics: results are deterministic).  For few rows per group, where
+//          reading w is the bound and more blocks read it faster.
+// Both are persistent: the tile list is made in every block from the group offsets, which only
+// the GPU knows.  Roles: warp 0 copies, one thread of warp 1 issues the products, eight warps
+// take results out.  Every wait is bounded (globaltimer); on timeout bit 1 of the status word
+// is set and the kernel runs to its end.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+
+#include "bounds_check.cuh"
+#include "grouped.h"
+#include "tmm_gemm.h"
+
+namespace tmm {
+
+__device__ unsigned int g_grouped_status;
+
+namespace {
+
+constexpr int kForward = 0, kWgrad = 1, kLora = 2;
+constexpr int kBK = 64;                  // 16-bit values per K slice: one 128-byte swizzle row
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kChunk = 2;                // slices per tensor-memory sum of split operands
+constexpr uint32_t kPTile = 128 * 128;   // 128 lanes x 64 values: 16 KiB
+constexpr uint32_t kMaxSmem = 232448;    // 227 KiB
+
+// How the results are written.
+constexpr int kOutF32 = 0, kOutBF16 = 1, kOutF16 = 2, kOutPlanes = 3;   // planes: split3
+
+template <int CG, int PLANES>
+struct Shape {
+  static constexpr int kBN = PLANES == 3 ? (CG == 2 ? 128 : 64) : (CG == 2 ? 256 : 64);
+  static constexpr int kUnit = CG == 2 ? 64 : 16;    // columns are rounded up to this
+  static constexpr int kBox = kUnit / CG;            // rows of one copy of Q
+  static constexpr uint32_t kQTile = uint32_t(kBN / CG) * 128;
+  static constexpr uint32_t kStage = PLANES * (kPTile + kQTile);
+  static constexpr int kStages = PLANES == 3 ? (CG == 2 ? 3 : 2) : (CG == 2 ? 6 : 7);
+  static constexpr uint32_t kTmemCols =
+      PLANES == 3 ? 4 * kBN : 2 * kBN;               // two accumulators (of each kind)
+  static constexpr uint32_t kRed = CG == 1 ? 128 * kBN * 4 : 0;
+  static constexpr uint32_t kTable = (kMaxGroups + 1) * 4 * 3;
+  static constexpr uint32_t kBars = 8 * (2 * kStages + 5) + 32;
+  static constexpr uint32_t kSmem = 1024 + kStages * kStage + kRed + kTable + kBars;
+  static_assert(kSmem <= kMaxSmem, "one block's shared memory");
+  static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory columns");
+};
+
+struct Params {
+  int rows;              // p runs over [0, rows)
+  int groups;
+  const int *offsets;    // groups + 1
+  const int *row_index;  // r(p), or NULL
+  int q_rows;            // rows of x
+  int K;                 // forward, adapters: length of the sum
+  int N;                 // extent of the lanes' dimension
+  int q_cols;            // gradient: columns of x
+  int rank;              // adapters
+  int panels;            // tiles along N
+  int p_mn, e_mn;        // P (and b) stored with n contiguous
+  int p_shared, e_shared;   // one P (one b) for all groups
+  uint32_t idesc;        // types; majors and sizes are added in the kernel
+  void *out;
+  int64_t ld_out, stride_out;   // stride: of dw's matrices, or of the result's planes
+  int out_type;
+  const float *scale;    // per group, or NULL
+  int ksplit;            // blocks of a cluster that share a tile's sum (CG = 1)
+  int64_t wait_limit_ns;
+  int drop_block;        // testing hook: this block waits for bytes that never come (-1: none)
+};
+
+// ---- primitives -------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint64_t timer_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int64_t limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (int64_t(timer_ns() - t0) > limit_ns) return false;
+  return true;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// Every thread of every block of the cluster.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Tensor copies into this block's shared memory; `bar` counts their bytes (a shared::cluster
+// address, in pairs the leader's).
+template <int CG>
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                       uint32_t bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                       uint32_t bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+// Four rows y[0..3] of 64 values from column x.
+template <int CG>
+__device__ __forceinline__ void tma_rows4(uint32_t dst, const CUtensorMap *map, int x,
+                                          const int (&y)[4], uint32_t bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
+        "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
+        "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                    bool accumulate) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %4, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(uint32_t(accumulate)), "r"(idesc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(uint32_t(accumulate)), "r"(idesc)
+        : "memory");
+}
+// Arrive on `bar` (of both blocks of a pair, with `both`) once the products issued so far by
+// this thread have completed.
+template <int CG>
+__device__ __forceinline__ void mma_commit(uint32_t bar, bool both) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar),
+        "h"(uint16_t(both ? 3 : 1))
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+}
+// 16 consecutive FP32 columns of this thread's lane.
+__device__ __forceinline__ void tmem_load_16(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11,"
+      " %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle: start address >> 4 (bits 0-13), leading
+// byte offset >> 4 (16-29), stride byte offset >> 4 (32-45), version 1 (46-47), swizzle 2
+// (61-63).  A tile stored with K contiguous has rows of 64 values (128 bytes), eight of them
+// 1024 bytes apart (stride); 16 values of K are 32 bytes on.  A tile stored with n contiguous
+// is made of blocks of 64 n (128 bytes) x 64 k, 8 KiB apart (leading), eight k 1024 bytes
+// apart (stride); 16 values of K are 2048 bytes on.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, bool mn) {
+  return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t(mn ? 512 : 1) << 16) | (uint64_t(64) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// ---- tiles ------------------------------------------------------------------------------
+
+// What a tile covers.  Forward, adapters: columns are rows p in [q0, q0 + qn); gradient: they
+// are columns of x, and the sum runs over the rows [k0, k0 + klen).
+struct Tile {
+  int g;          // group (adapters: 0)
+  int n0;         // first n
+  int q0, qn;     // columns of the tile
+  int bn;         // qn rounded up for the tensor core
+  int k0, klen;
+  int e0, en;     // adapters with rows in the tile: list entries [e0, e0 + en)
+};
+
+// The tables in shared memory: the groups that have rows (every group in the gradient): number,
+// first row (one more entry: the end of the last), first tile.
+struct Table {
+  const int *gid, *row, *tile;
+  int count, tiles;
+};
+
+template <int CG, int MODE, int PLANES>
+__device__ __forceinline__ Tile tile_at(const Params &p, const Table &tab, int t) {
+  using S = Shape<CG, PLANES>;
+  Tile r;
+  r.e0 = r.en = r.k0 = 0;
+  if (MODE == kWgrad) {
+    const int qt = (p.q_cols + S::kBN - 1) / S::kBN;
+    const int per = qt * p.panels;
+    r.g = t / per;
+    const int i = t - r.g * per;
+    const int panel = i / qt;
+    r.n0 = panel * 128 * CG;
+    r.q0 = (i - panel * qt) * S::kBN;
+    r.qn = min(S::kBN, p.q_cols - r.q0);
+    r.bn = (r.qn + 64 * CG - 1) / (64 * CG) * (64 * CG);
+    r.k0 = tab.row[r.g];
+    r.klen = tab.row[r.g + 1] - r.k0;
+    return r;
+  }
+  int lo, hi, i;
+  if (MODE == kLora) {
+    r.g = 0;
+    lo = 0;
+    hi = p.rows;
+    i = t;
+  } else {
+    int a = 0, b = tab.count;      // the last entry whose first tile is <= t
+    while (b - a > 1) {
+      const int m = (a + b) >> 1;
+      if (tab.tile[m] <= t) a = m;
+      else b = m;
+    }
+    r.g = tab.gid[a];
+    lo = tab.row[a];
+    hi = tab.row[a + 1];
+    i = t - tab.tile[a];
+  }
+  const int qt = (hi - lo + S::kBN - 1) / S::kBN;
+  const int panel = i / qt;
+  r.n0 = panel * 128 * CG;
+  r.q0 = lo + (i - panel * qt) * S::kBN;
+  r.qn = min(S::kBN, hi - r.q0);
+  r.bn = (r.qn + S::kUnit - 1) / S::kUnit * S::kUnit;
+  r.klen = p.K;
+  if (MODE == kLora) {
+    // Entries whose rows overlap [q0, q0 + qn): first with an end past q0, up to a start past it.
+    int a = 0, b = tab.count;
+    while (a < b) {
+      const int m = (a + b) >> 1;
+      if (tab.row[m + 1] > r.q0) b = m;
+      else a = m + 1;
+    }
+    r.e0 = a;
+    b = tab.count;
+    int c = a;
+    while (c < b) {
+      const int m = (c + b) >> 1;
+      if (tab.row[m] >= r.q0 + r.qn) b = m;
+      else c = m + 1;
+    }
+    r.en = c - a;
+  }
+  return r;
+}
+
+// This block's K slices [s0, s1) of a tile: the slices of the base sum, then those of the
+// adapters in the tile; blocks that share a tile take equal runs of them.
+template <int MODE>
+__device__ __forceinline__ void slices_of(const Params &p, const Tile &t, int rank, int &base,
+                                          int &s0, int &s1) {
+  base = (t.klen + kBK - 1) / kBK;
+  int n = base;
+  if (MODE == kLora) n += t.en * ((p.rank + kBK - 1) / kBK);
+  if (p.ksplit == 1) {
+    s0 = 0;
+    s1 = n;
+  } else {
+    s0 = int(int64_t(n) * rank / p.ksplit);
+    s1 = int(int64_t(n) * (rank + 1) / p.ksplit);
+  }
+}
+
+// The bf16 nearest an FP32 value (ties away from zero), as its bits; in the top binade, where
+// rounding could reach infinity, the value truncated.
+__device__ __forceinline__ uint32_t nearest_bf16(uint32_t b) {
+  return (b & 0x7F800000u) == 0x7F000000u ? b & 0xFFFF0000u : (b + 0x8000u) & 0xFFFF0000u;
+}
+// The three bf16 parts of an FP32 value: each the nearest to what the ones before leave, so
+// |x1| <= 2^-8 |x| and |x2| <= 2^-16 |x|, and x = x0 + x1 + x2 exactly (for |x| >= 2^-102;
+// below, what falls under the smallest subnormal is dropped).  An infinity or a NaN is its own
+// first part.
+__device__ __forceinline__ void split3(float x, uint16_t (&h)[3]) {
+  const uint32_t b = __float_as_uint(x);
+  if ((b & 0x7F800000u) == 0x7F800000u) {
+    h[0] = uint16_t((b >> 16) | ((b & 0x007FFFFFu) ? 0x0040u : 0u));
+    h[1] = h[2] = 0;
+    return;
+  }
+  const uint32_t b0 = nearest_bf16(b);
+  const float r = x - __uint_as_float(b0);
+  const uint32_t b1 = nearest_bf16(__float_as_uint(r));
+  const float s = r - __uint_as_float(b1);
+  h[0] = uint16_t(b0 >> 16);
+  h[1] = uint16_t(b1 >> 16);
+  h[2] = uint16_t(nearest_bf16(__float_as_uint(s)) >> 16);
+}
+
+// One result at element offset `o` of the output.  Split operands (PLANES = 3) give FP32 or
+// planes, 16-bit operands their own type.
+template <int PLANES>
+__device__ __forceinline__ void store_out(const Params &p, int64_t o, float v) {
+  if constexpr (PLANES == 3) {
+    if (p.out_type == kOutF32) {
+      static_cast<float *>(p.out)[o] = v;
+    } else {
+      uint16_t h[3];
+      split3(v, h);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) static_cast<uint16_t *>(p.out)[o + i * p.stride_out] = h[i];
+    }
+  } else if (p.out_type == kOutBF16) {
+    static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(v);
+  } else {
+    static_cast<__half *>(p.out)[o] = __float2half_rn(v);
+  }
+}
+
+// Offset of the result row that column `col` of the tile goes to; -1: none.
+template <int MODE>
+__device__ __forceinline__ int64_t out_row(const Params &p, const Tile &t, int col) {
+  if (MODE == kWgrad) return int64_t(t.g) * p.stride_out + int64_t(t.q0 + col) * p.ld_out;
+  int r = t.q0 + col;
+  if (MODE == kLora && p.row_index) {
+    r = p.row_index[r];
+    if (r < 0 || r >= p.q_rows) return -1;
+  }
+  return int64_t(r) * p.ld_out;
+}
+
+// 16 consecutive columns of the tile from c0 on, for this lane's n: 32 lanes write 64 (128)
+// consecutive bytes of each result row.
+template <int MODE, int PLANES>
+__device__ __forceinline__ void store_columns(const Params &p, const Tile &t, int c0, int n,
+                                              const float (&v)[16], float scale) {
+  const int count = min(16, t.qn - c0);
+  int row = 0;      // adapters: the row of column c0 + lane % 16
+  const bool by_row = MODE == kLora && p.row_index;
+  if (by_row) {
+    const int lane = threadIdx.x & 15;
+    row = lane < count ? p.row_index[t.q0 + c0 + lane] : -1;
+    if (row >= p.q_rows) row = -1;
+  }
+  const bool in = n < p.N;
+  int64_t o = out_row<kForward>(p, t, c0) + n;
+  if (MODE == kWgrad) o += int64_t(t.g) * p.stride_out;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (by_row) {
+      const int r = __shfl_sync(~0u, row, j);
+      if (in && r >= 0) store_out<PLANES>(p, int64_t(r) * p.ld_out + n, v[j] * scale);
+    } else {
+      if (in && j < count) store_out<PLANES>(p, o, v[j] * scale);
+      o += p.ld_out;
+    }
+  }
+}
+
+// ---- kernel -----------------------------------------------------------------------------
+
+template <int CG, int MODE, int PLANES>
+__global__ void __launch_bounds__(kThreads, 1)
+grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
+               const __grid_constant__ CUtensorMap map_q,    // Q tiles
+               const __grid_constant__ CUtensorMap map_qr,   // rows of x
+               const __grid_constant__ CUtensorMap map_e,    // b tiles; gradient: rows of dy
+               const __grid_constant__ CUtensorMap map_u,    // rows of u
+               const Params p) {
+  using S = Shape<CG, PLANES>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;    // the same offset in every block
+  uint8_t *const smem = smem_raw + (base - raw);
+  const uint32_t red = base + S::kStages * S::kStage;
+  const uint32_t table = red + S::kRed;
+  const uint32_t bar_full = (table + S::kTable + 7u) & ~7u;
+  const uint32_t bar_empty = bar_full + 8 * S::kStages;
+  const uint32_t bar_tfull = bar_empty + 8 * S::kStages;
+  const uint32_t bar_tempty = bar_tfull + 16;      // pairs: used in the leader
+  const uint32_t bar_drain = bar_tempty + 16;
+  const uint32_t slot = bar_drain + 8;             // tensor memory address; then the counts
+
+  int *const tab_gid = reinterpret_cast<int *>(smem + (table - base));
+  int *const tab_row = tab_gid + (kMaxGroups + 1);
+  int *const tab_tile = tab_row + (kMaxGroups + 1);
+  volatile uint32_t *const slot_ptr = reinterpret_cast<volatile uint32_t *>(smem + (slot - base));
+  float *const red_ptr = reinterpret_cast<float *>(smem + (red - base));
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int cluster_size = CG == 2 ? 2 : p.ksplit;
+  const int cluster = int(blockIdx.x) / cluster_size;
+  const int clusters = int(gridDim.x) / cluster_size;
+  const bool leader = CG == 1 || rank == 0;
+  const int half_rank = CG == 2 ? int(rank) : 0;   // which 128 lanes, which half of the columns
+
+  // Group offsets, clamped, into the (still unused) ring; barriers; tensor memory.
+  int *const offs = reinterpret_cast<int *>(smem);
+  for (int g = threadIdx.x; g <= p.groups; g += kThreads)
+    offs[g] = max(0, min(p.offsets[g], p.rows));
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar_tfull + 8 * b, 1);
+      mbar_init(bar_tempty + 8 * b, CG * kEpiWarps);
+    }
+    mbar_init(bar_drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    if constexpr (CG == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
+                   "r"(S::kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
+                   "r"(S::kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // Group bounds are the running maximum of the offsets: offsets that step back make an
+    // empty group, never an overlap.  Groups without rows are left out of the list (kept in
+    // the gradient, whose result has a matrix for each).
+    int carry = offs[0], count = 0, tiles = 0;
+    if (lane == 0) slot_ptr[3] = uint32_t(carry);       // first row of any group
+    if (MODE == kWgrad && lane == 0) tab_row[0] = carry;
+    for (int g0 = 0; g0 < p.groups; g0 += 32) {
+      const int g = g0 + lane;
+      int hi = g < p.groups ? offs[g + 1] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(~0u, hi, d);
+        if (lane >= d) hi = max(hi, o);
+      }
+      hi = max(hi, carry);
+      int lo = __shfl_up_sync(~0u, hi, 1);
+      if (lane == 0) lo = carry;
+      carry = __shfl_sync(~0u, hi, 31);
+      if (MODE == kWgrad) {
+        if (g < p.groups) tab_row[g + 1] = hi;
+      } else {
+        const int n = g < p.groups ? hi - lo : 0;
+        const unsigned have = __ballot_sync(~0u, n > 0);
+        const int at = count + __popc(have & ((1u << lane) - 1));
+        const int mine = (n + S::kBN - 1) / S::kBN * p.panels;
+        int sum = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(~0u, sum, d);
+          if (lane >= d) sum += o;
+        }
+        if (n > 0) {
+          tab_gid[at] = g;
+          tab_row[at] = lo;
+          tab_tile[at] = tiles + sum - mine;
+        }
+        tiles += __shfl_sync(~0u, sum, 31);
+        count += __popc(have);
+      }
+    }
+    if (lane == 0) {
+      if (MODE != kWgrad) tab_row[count] = carry;
+      if (MODE == kWgrad) tiles = p.groups * p.panels * ((p.q_cols + S::kBN - 1) / S::kBN);
+      if (MODE == kLora) tiles = p.panels * ((p.rows + S::kBN - 1) / S::kBN);
+      slot_ptr[1] = uint32_t(count);
+      slot_ptr[2] = uint32_t(tiles);
+      slot_ptr[4] = uint32_t(carry);                    // end of the last group
+    }
+    // The ring is written by the copy engine from here on.
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2 || p.ksplit > 1) cluster_sync();   // barriers exist before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem = slot_ptr[0];
+  const Table tab = {tab_gid, tab_row, tab_tile, int(slot_ptr[1]), int(slot_ptr[2])};
+
+  bool timed_out = false;
+  uint32_t r = 0;      // ring position: slices so far
+  uint32_t q = 0;      // tensor-memory sums so far
+  uint32_t done = 0;   // tiles with a sum so far
+
+  // Forward: rows of the result that belong to no group are zero.
+  if (MODE == kForward && warp >= 2) {
+    const int lo = int(slot_ptr[3]), hi = int(slot_ptr[4]);
+    for (int64_t i = blockIdx.x; i < int64_t(lo) + (p.rows - hi); i += gridDim.x) {
+      const int64_t row = i < lo ? i : hi + (i - lo);
+      for (int n = int(threadIdx.x) - 64; n < p.N; n += 32 * kEpiWarps)
+        store_out<PLANES>(p, row * p.ld_out + n, 0.0f);
+    }
+  }
+
+  for (int t = cluster; t < tab.tiles; t += clusters) {
+    const Tile tile = tile_at<CG, MODE, PLANES>(p, tab, t);
+    int nbase, s0, s1;
+    slices_of<MODE>(p, tile, CG == 2 ? 0 : int(rank), nbase, s0, s1);
+    const int per_rank = MODE == kLora ? (p.rank + kBK - 1) / kBK : 1;
+
+    if (warp == 0) {
+      // ---- copies ----
+      const int hr = tile.bn / CG;                      // columns staged by this block
+      const int qf = tile.q0 + half_rank * hr;          // the first of them
+      const int n0 = tile.n0 + half_rank * 128;
+      const int pg = (p.p_shared ? 0 : tile.g);
+      const int pcount = p.p_shared ? 1 : p.groups;
+      // Rows of x this lane fetches, four of them (forward, adapters: columns 4 lane .. + 3 of
+      // this block's; gradient: rows 4 (lane % 16) .. + 3 of the next slice); -1 is a zero row.
+      int mine[4];
+      auto fetch_rows = [&](int first, int limit) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = first + i;
+          int row = -1;
+          if (at < limit) {
+            row = p.row_index ? p.row_index[at] : at;
+            if (row < 0 || row >= p.q_rows) row = -1;
+          }
+          mine[i] = row;
+        }
+      };
+      const bool by_row = p.row_index != nullptr;
+      if (MODE != kWgrad && by_row) fetch_rows(qf + 4 * lane, tile.q0 + tile.qn);
+      if (MODE == kWgrad && s0 < s1)
+        fetch_rows(tile.k0 + s0 * kBK + 4 * (lane & 15), tile.k0 + tile.klen);
+      for (int s = s0; s < s1 && !timed_out; ++s, ++r) {
+        const uint32_t st_i = r % S::kStages;
+        bool ok = true;
+        if (lane == 0 && r >= S::kStages)
+          ok = mbar_wait(bar_empty + 8 * st_i, ((r / S::kStages) - 1) & 1u, p.wait_limit_ns);
+        if (!__all_sync(~0u, ok)) {
+          timed_out = true;
+          break;
+        }
+        const uint32_t st = base + st_i * S::kStage;
+        const uint32_t sq = st + PLANES * kPTile;
+        const uint32_t full_local = bar_full + 8 * st_i;
+        const uint32_t full = CG == 2 ? map_rank(full_local, 0) : full_local;
+        uint32_t bytes;
+        int cnt = kBK;
+        if (MODE == kWgrad) {
+          cnt = min(kBK, tile.klen - s * kBK);
+          bytes = uint32_t((cnt + 15) & ~15) * 128u * uint32_t(2 + hr / 64) * PLANES;
+        } else {
+          bytes = PLANES * (kPTile + uint32_t(hr) * 128u);
+        }
+        if (lane == 0 && leader) {
+          bytes *= CG;
+          if (int(blockIdx.x) == p.drop_block && r == 0) bytes += 16;
+          mbar_expect(full_local, bytes);
+        }
+        __syncwarp();
+        if (MODE == kWgrad) {
+          const int p0 = tile.k0 + s * kBK;
+          const int quads = (cnt + 15) / 16 * 4;        // groups of four rows copied
+          const int quad = lane & 15, part = lane >> 4;
+          const int qblocks = hr / 64;
+          if (cnt == kBK) {
+            if (lane < 2 * PLANES)
+              tma_2d<CG>(st + lane * 8192, &map_p, n0 + (lane & 1) * 64,
+                         p0 + (lane >> 1) * p.rows, full);
+          } else if (quad < quads) {
+#pragma unroll
+            for (int pl = 0; pl < PLANES; ++pl) {
+              int y[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                y[i] = 4 * quad + i < cnt ? p0 + 4 * quad + i + pl * p.rows : PLANES * p.rows;
+              tma_rows4<CG>(st + pl * kPTile + part * 8192 + quad * 512, &map_e, n0 + part * 64, y,
+                            full);
+            }
+          }
+          if (cnt == kBK && !by_row) {
+            if (lane < qblocks * PLANES) {
+              const int pl = lane / qblocks, b = lane - pl * qblocks;
+              tma_2d<CG>(sq + pl * S::kQTile + b * 8192, &map_q, qf + b * 64, p0 + pl * p.q_rows,
+                         full);
+            }
+          } else if (quad < quads) {
+#pragma unroll
+            for (int pl = 0; pl < PLANES; ++pl) {
+              int y[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                y[i] = mine[i] < 0 ? PLANES * p.q_rows : mine[i] + pl * p.q_rows;
+              for (int b = part; b < qblocks; b += 2)
+                tma_rows4<CG>(sq + pl * S::kQTile + b * 8192 + quad * 512, &map_qr, qf + b * 64, y,
+                              full);
+            }
+          }
+          if (s + 1 < s1)
+            fetch_rows(tile.k0 + (s + 1) * kBK + 4 * quad, tile.k0 + tile.klen);
+        } else {
+          const bool ext = MODE == kLora && s >= nbase;
+          int k0 = s * kBK, g = pg, gcount = pcount, lo = 0, hi = 0;
+          if (ext) {
+            const int e = (s - nbase) / per_rank;
+            k0 = (s - nbase - e * per_rank) * kBK;
+            g = p.e_shared ? 0 : tab.gid[tile.e0 + e];
+            gcount = p.e_shared ? 1 : p.groups;
+            lo = tab.row[tile.e0 + e];
+            hi = tab.row[tile.e0 + e + 1];
+          }
+          const CUtensorMap *mp = ext ? &map_e : &map_p;
+          if (ext ? p.e_mn : p.p_mn) {
+            if (lane < 2 * PLANES)
+              tma_3d<CG>(st + lane * 8192, mp, n0 + (lane & 1) * 64, k0, g + (lane >> 1) * gcount,
+                         full);
+          } else if (lane < PLANES) {
+            tma_3d<CG>(st + lane * kPTile, mp, k0, n0, g + lane * gcount, full);
+          }
+          if (ext || by_row) {
+            if (lane < hr / 4) {
+#pragma unroll
+              for (int pl = 0; pl < PLANES; ++pl) {
+                int y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  if (ext) {
+                    const int at = qf + 4 * lane + i;
+                    y[i] = at >= lo && at < hi && at < tile.q0 + tile.qn ? at + pl * p.rows
+                                                                         : PLANES * p.rows;
+                  } else {
+                    y[i] = mine[i] < 0 ? PLANES * p.q_rows : mine[i] + pl * p.q_rows;
+                  }
+                }
+                tma_rows4<CG>(sq + pl * S::kQTile + lane * 512, ext ? &map_u : &map_qr, k0, y,
+                              full);
+              }
+            }
+          } else {
+            const int boxes = hr / S::kBox;
+            if (lane < boxes * PLANES) {
+              const int pl = lane / boxes, b = lane - pl * boxes;
+              tma_2d<CG>(sq + pl * S::kQTile + b * (S::kBox * 128), &map_q, k0,
+                         qf + b * S::kBox + pl * p.q_rows, full);
+            }
+          }
+        }
+      }
+    } else if (warp == 1) {
+      // ---- products ----
+      if (lane == 0 && leader) {
+        const uint32_t sizes = (uint32_t(tile.bn >> 3) << 17) | (uint32_t(128 * CG >> 4) << 24) |
+                               (MODE == kWgrad ? 1u << 16 : 0u);
+        const int n = s1 - s0;
+        for (int i = 0; i < n && !timed_out; ++i, ++r) {
+          const int s = s0 + i;
+          const bool first = PLANES == 3 ? i % kChunk == 0 : i == 0;
+          if (first) {
+            if (q >= 2 && !mbar_wait(bar_tempty + 8 * (q & 1), ((q >> 1) - 1) & 1u,
+                                     p.wait_limit_ns)) {
+              timed_out = true;
+              break;
+            }
+            ++q;
+          }
+          const uint32_t buf = (q - 1) & 1;
+          const uint32_t st_i = r % S::kStages;
+          if (!mbar_wait(bar_full + 8 * st_i, (r / S::kStages) & 1u, p.wait_limit_ns)) {
+            timed_out = true;
+            break;
+          }
+          tc_fence_after();
+          const bool ext = MODE == kLora && s >= nbase;
+          const int left = ext ? p.rank - (s - nbase) % per_rank * kBK : tile.klen - s * kBK;
+          const int steps = (min(left, kBK) + 15) / 16;
+          const bool pmn = MODE == kWgrad || (ext ? p.e_mn : p.p_mn);
+          const uint32_t idesc = p.idesc | sizes | (pmn ? 1u << 15 : 0u);
+          const uint32_t st = base + st_i * S::kStage;
+          const uint64_t dp = tile_desc(st, pmn);
+          const uint64_t dq = tile_desc(st + PLANES * kPTile, MODE == kWgrad);
+          const uint32_t pstep = pmn ? 128 : 2, qstep = MODE == kWgrad ? 128 : 2;   // 16 bytes
+          const uint32_t d = tmem + buf * S::kBN;
+          for (int k = 0; k < steps; ++k) {
+            const uint64_t a = dp + k * pstep, b = dq + k * qstep;
+            mma<CG>(d, a, b, idesc, !(first && k == 0));
+            if constexpr (PLANES == 3) {
+              constexpr uint64_t pa = kPTile >> 4, qa = S::kQTile >> 4;
+              const uint32_t ds = tmem + (2 + (done & 1)) * S::kBN;
+              mma<CG>(ds, a + 2 * pa, b, idesc, !(i == 0 && k == 0));
+              mma<CG>(ds, a, b + 2 * qa, idesc, true);
+              mma<CG>(ds, a + pa, b + qa, idesc, true);
+              mma<CG>(ds, a + pa, b, idesc, true);
+              mma<CG>(ds, a, b + qa, idesc, true);
+            }
+          }
+          mma_commit<CG>(bar_empty + 8 * st_i, true);
+          if (i == n - 1 || (PLANES == 3 && i % kChunk == kChunk - 1))
+            mma_commit<CG>(bar_tfull + 8 * buf, true);
+        }
+        if (n > 0) ++done;
+      }
+    } else {
+      // ---- results ----
+      const int quarter = warp & 3, half = (warp - 2) >> 2;
+      const int n = s1 - s0;
+      const uint32_t lanes = tmem + (uint32_t(32 * quarter) << 16);
+      const uint32_t tempty = CG == 2 ? map_rank(bar_tempty, 0) : bar_tempty;
+      const int nn = tile.n0 + half_rank * 128 + 32 * quarter + lane;
+      const float scale = MODE == kForward && p.scale ? p.scale[tile.g] : 1.0f;
+      constexpr int kBlocks = S::kBN / 32;     // 16-column blocks of a warp, every other one
+      auto put = [&](int c0, const float (&v)[16]) {
+        if (CG == 1 && p.ksplit > 1) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) red_ptr[(c0 + j) * 128 + 32 * quarter + lane] = v[j];
+        } else {
+          store_columns<MODE, PLANES>(p, tile, c0, nn, v, scale);
+        }
+      };
+      if constexpr (PLANES == 1) {
+        if (n == 0) {
+          const float v[16] = {};
+          for (int c0 = 16 * half; c0 < tile.bn; c0 += 32) put(c0, v);
+        } else {
+          const uint32_t buf = q & 1;
+          const bool ready = mbar_wait(bar_tfull + 8 * buf, (q >> 1) & 1u, p.wait_limit_ns);
+          ++q;
+          if (!__all_sync(~0u, ready)) timed_out = true;
+          tc_fence_after();
+          if (!timed_out) {
+            for (int c0 = 16 * half; c0 < tile.bn; c0 += 32) {
+              float v[16];
+              __syncwarp();
+              tmem_load_16(lanes + buf * S::kBN + c0, v);
+              put(c0, v);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tempty + 8 * buf);
+        }
+      } else {
+        float acc[kBlocks][16];
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[b][j] = 0.0f;
+        const int chunks = (n + kChunk - 1) / kChunk;
+        for (int c = 0; c < chunks && !timed_out; ++c, ++q) {
+          const uint32_t buf = q & 1;
+          const bool ready = mbar_wait(bar_tfull + 8 * buf, (q >> 1) & 1u, p.wait_limit_ns);
+          if (!__all_sync(~0u, ready)) {
+            timed_out = true;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) {
+            const int c0 = 32 * b + 16 * half;
+            if (c0 >= tile.bn) break;
+            float v[16];
+            __syncwarp();
+            tmem_load_16(lanes + buf * S::kBN + c0, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[b][j] += v[j];
+            if (c == chunks - 1) {
+              tmem_load_16(lanes + (2 + (done & 1)) * S::kBN + c0, v);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) acc[b][j] += v[j];
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tempty + 8 * buf);
+        }
+        if (n > 0) ++done;
+        if (!timed_out) {
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) {
+            const int c0 = 32 * b + 16 * half;
+            if (c0 >= tile.bn) break;
+            put(c0, acc[b]);
+          }
+        }
+      }
+    }
+    if (CG == 1 && p.ksplit > 1) {
+      // Every block holds its part of the sum in `red`: block c adds the columns of its share,
+      // in block order, and stores them.
+      __syncwarp();
+      cluster_sync();
+      if (warp >= 2) {
+        const int c0 = tile.qn * int(rank) / p.ksplit, c1 = tile.qn * int(rank + 1) / p.ksplit;
+        const float scale = MODE == kForward && p.scale ? p.scale[tile.g] : 1.0f;
+        for (int i = int(threadIdx.x) - 64; i < 128 * (c1 - c0); i += 32 * kEpiWarps) {
+          const int l = i & 127, col = c0 + (i >> 7);
+          const uint32_t at = red + uint32_t(col * 128 + l) * 4;
+          float v = 0.0f;
+          for (int b = 0; b < p.ksplit; ++b) v += ld_cluster(map_rank(at, uint32_t(b)));
+          const int64_t o = out_row<MODE>(p, tile, col);
+          if (o >= 0 && tile.n0 + l < p.N) store_out<PLANES>(p, o + tile.n0 + l, v * scale);
+        }
+      }
+      __syncwarp();
+      cluster_sync();
+    }
+  }
+
+  if (warp == 0 && timed_out && leader && lane == 0) {
+    // Let the copies in flight land before the block goes away (the leader's barriers count
+    // both blocks' copies).
+    for (uint32_t i = r > S::kStages ? r - S::kStages : 0; i < r; ++i)
+      mbar_wait(bar_full + 8 * (i % S::kStages), (i / S::kStages) & 1u, p.wait_limit_ns);
+  }
+  if (warp == 1 && lane == 0 && leader) {
+    mma_commit<CG>(bar_drain, false);
+    if (!mbar_wait(bar_drain, 0u, p.wait_limit_ns)) timed_out = true;
+  }
+  __syncwarp();
+  if (timed_out) atomicOr(&g_grouped_status, 2u);
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync();   // remote arrivals have landed; neither block uses tensor memory
+  tc_fence_after();
+  if (warp == 1) {
+    if constexpr (CG == 2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(S::kTmemCols)
+                   : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(S::kTmemCols)
+                   : "memory");
+  }
+}
+
+// ---- operand planes -----------------------------------------------------------------------
+
+// Copies a stack of matrices into 16-bit planes whose rows start on 16-byte boundaries: FP32
+// values into their three bf16 parts (planes), 16-bit values as they are (one plane).  Layout:
+// [plane][matrix][row][ld8].  Matrices of groups without rows are left out.  Bound by memory:
+// each thread moves eight values.
+template <bool F32>
+__global__ void planes_kernel(const void *__restrict__ src, int64_t count, int64_t rows,
+                              int64_t cols, int64_t ld, int64_t stride, int vec,
+                              const int *__restrict__ offsets, uint16_t *__restrict__ dst,
+                              int64_t ld8) {
+  const int64_t per_row = ld8 / 8;
+  const int64_t total = rows * per_row;
+  const int64_t plane = count * rows * ld8;
+  for (int64_t m = blockIdx.y; m < count; m += gridDim.y) {
+    if (offsets && offsets[m + 1] <= offsets[m]) continue;
+    for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < total;
+         i += int64_t(gridDim.x) * blockDim.x) {
+      const int64_t row = i / per_row, c = (i - row * per_row) * 8;
+      const int64_t so = m * stride + row * ld + c;
+      const int64_t to = (m * rows + row) * ld8 + c;
+      if constexpr (F32) {
+        const float *s = static_cast<const float *>(src) + so;
+        float x[8];
+        if (vec && c + 8 <= cols) {
+          const float4 a = *reinterpret_cast<const float4 *>(s);
+          const float4 b = *reinterpret_cast<const float4 *>(s + 4);
+          x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+          x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = c + j < cols ? s[j] : 0.0f;
+        }
+        uint16_t h[8][3];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) split3(x[j], h[j]);
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) {
+          uint4 v;
+          v.x = h[0][pl] | (uint32_t(h[1][pl]) << 16);
+          v.y = h[2][pl] | (uint32_t(h[3][pl]) << 16);
+          v.z = h[4][pl] | (uint32_t(h[5][pl]) << 16);
+          v.w = h[6][pl] | (uint32_t(h[7][pl]) << 16);
+          *reinterpret_cast<uint4 *>(dst + pl * plane + to) = v;
+        }
+      } else {
+        const uint16_t *s = static_cast<const uint16_t *>(src) + so;
+        uint32_t x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = c + j < cols ? s[j] : 0u;
+        *reinterpret_cast<uint4 *>(dst + to) =
+            make_uint4(x[0] | (x[1] << 16), x[2] | (x[3] << 16), x[4] | (x[5] << 16),
+                       x[6] | (x[7] << 16));
+      }
+    }
+  }
+}
+
+// ---- host -------------------------------------------------------------------------------
+
+std::atomic<int64_t> g_wait_limit_ns{int64_t(10) * 1000 * 1000 * 1000};
+std::atomic<int> g_drop_block{-1};
+
+int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
+
+// Whether the copy engine can read the matrices in place: 16-bit values, rows and matrices on
+// 16-byte boundaries.
+bool in_place(const Stack &s, int dtype) {
+  return dtype != TMM_F32 && (reinterpret_cast<uintptr_t>(s.data) & 15u) == 0 && s.ld % 8 == 0 &&
+         (s.count == 1 || s.stride % 8 == 0);
+}
+
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+// Bytes of an operand's planes in the workspace (0: read in place), or SIZE_MAX.
+size_t plane_bytes(const Stack &s, int dtype) {
+  if (in_place(s, dtype)) return 0;
+  const __int128 n = __int128(dtype == TMM_F32 ? 6 : 2) * s.count * s.rows * round8(s.cols);
+  return n > __int128(INT64_MAX / 4) ? SIZE_MAX : round256(size_t(n));
+}
+
+size_t add_sizes(std::initializer_list<size_t> sizes) {
+  size_t t = 0;
+  for (size_t s : sizes) {
+    if (s == SIZE_MAX) return SIZE_MAX;
+    t += s;      // each is at most 2^61, and there are at most five
+  }
+  return t;
+}
+
+// An operand as the copy engine reads it: `planes` stacks of 16-bit matrices after each other.
+struct Planes {
+  const void *data;
+  int64_t count, rows, cols, ld, stride;   // count: matrices of all planes
+};
+
+// The operand in place, or its planes made in *ws (which advances past them); matrices of
+// groups without rows (by `offsets`, a matrix per group) are not made.
+cudaError_t make_planes(const Stack &s, int dtype, const int32_t *offsets, char **ws,
+                        const DeviceInfo &dev, cudaStream_t stream, Planes *out) {
+  if (in_place(s, dtype)) {
+    *out = {s.data, s.count, s.rows, s.cols, s.ld, s.count > 1 ? s.stride : s.rows * s.ld};
+    return cudaSuccess;
+  }
+  const int64_t ld8 = round8(s.cols);
+  const int planes = dtype == TMM_F32 ? 3 : 1;
+  uint16_t *dst = reinterpret_cast<uint16_t *>(*ws);
+  *ws += plane_bytes(s, dtype);
+  const int64_t work = (s.rows * (ld8 / 8) + 255) / 256;
+  const dim3 grid(unsigned(std::min<int64_t>(work, 8 * dev.sm_count)),
+                  unsigned(std::min<int64_t>(s.count, 1024)));
+  const int vec = (reinterpret_cast<uintptr_t>(s.data) & 15u) == 0 && s.ld % 4 == 0 &&
+                  (s.count == 1 || s.stride % 4 == 0);
+  if (s.count == 1) offsets = nullptr;      // one matrix may serve every group
+  if (dtype == TMM_F32)
+    planes_kernel<true><<<grid, 256, 0, stream>>>(s.data, s.count, s.rows, s.cols, s.ld, s.stride,
+                                                  vec, offsets, dst, ld8);
+  else
+    planes_kernel<false><<<grid, 256, 0, stream>>>(s.data, s.count, s.rows, s.cols, s.ld,
+                                                   s.stride, 0, offsets, dst, ld8);
+  *out = {dst, planes * s.count, s.rows, s.cols, ld8, s.rows * ld8};
+  return cudaGetLastError();
+}
+
+// Maps of an operand: tiles of `box_rows` rows x 64 values in matrix z, or of the rows of all
+// matrices under one another (which are contiguous or only one), singly with box_rows = 1.
+cudaError_t tile_map(CUtensorMap *map, const Planes &o, uint32_t box_rows) {
+  const uint64_t size[3] = {uint64_t(o.cols), uint64_t(o.rows), uint64_t(o.count)};
+  const uint64_t stride[2] = {uint64_t(o.ld), uint64_t(o.stride)};
+  const uint32_t box[3] = {kBK, box_rows, 1};
+  return encode_16bit(map, o.data, 3, size, stride, box);
+}
+cudaError_t row_map(CUtensorMap *map, const Planes &o, uint32_t box_rows) {
+  const uint64_t size[2] = {uint64_t(o.cols), uint64_t(o.rows) * uint64_t(o.count)};
+  const uint64_t stride[1] = {uint64_t(o.ld)};
+  const uint32_t box[2] = {kBK, box_rows};
+  return encode_16bit(map, o.data, 2, size, stride, box);
+}
+
+struct Maps {
+  CUtensorMap p, q, qr, e, u;
+};
+
+template <int CG, int MODE, int PLANES>
+cudaError_t launch_shape(const Maps &m, Params &prm, int64_t tiles, const DeviceInfo &dev,
+                         cudaStream_t stream) {
+  using S = Shape<CG, PLANES>;
+  static std::atomic<uint64_t> configured{0};
+  auto kernel = grouped_kernel<CG, MODE, PLANES>;
+  const uint64_t bit = uint64_t(1) << (dev.id & 63);
+  if (!(configured.load(std::memory_order_acquire) & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(S::kSmem));
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_release);
+  }
+  const int cluster = CG == 2 ? 2 : prm.ksplit;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = stream;
+  // Persistent: a cluster for every tile there can be, at most one per resident slot.
+  const int64_t slots = std::max(1, dev.sm_count / cluster);
+  cfg.gridDim = dim3(unsigned(cluster * std::max<int64_t>(1, std::min(tiles, slots))), 1, 1);
+  return cudaLaunchKernelEx(&cfg, kernel, m.p, m.q, m.qr, m.e, m.u, prm);
+}
+
+template <int CG, int PLANES>
+cudaError_t launch_mode(int mode, const Maps &m, Params &prm, int64_t tiles,
+                        const DeviceInfo &dev, cudaStream_t stream) {
+  if (mode == kForward) return launch_shape<CG, kForward, PLANES>(m, prm, tiles, dev, stream);
+  if (mode == kWgrad) return launch_shape<CG, kWgrad, PLANES>(m, prm, tiles, dev, stream);
+  return launch_shape<CG, kLora, PLANES>(m, prm, tiles, dev, stream);
+}
+
+cudaError_t launch_any(int cg, int planes, int mode, const Maps &m, Params &prm, int64_t tiles,
+                       const DeviceInfo &dev, cudaStream_t stream) {
+  prm.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  prm.drop_block = g_drop_block.load(std::memory_order_relaxed);
+  if (cg == 2)
+    return planes == 3 ? launch_mode<2, 3>(mode, m, prm, tiles, dev, stream)
+                       : launch_mode<2, 1>(mode, m, prm, tiles, dev, stream);
+  return planes == 3 ? launch_mode<1, 3>(mode, m, prm, tiles, dev, stream)
+                     : launch_mode<1, 1>(mode, m, prm, tiles, dev, stream);
+}
+
+// Instruction descriptor of kind::f16 without majors and sizes: D FP32 (bit 4), A and B bf16
+// (1 in bits 7-9 and 10-12) or FP16 (0).
+uint32_t type_desc(int dtype) {
+  return (1u << 4) | (dtype == TMM_F16 ? 0u : (1u << 7) | (1u << 10));
+}
+int out_type(int dtype) {
+  return dtype == TMM_F32 ? kOutF32 : dtype == TMM_BF16 ? kOutBF16 : kOutF16;
+}
+int box_of(int cg) { return cg == 2 ? 32 : 16; }
+int columns_of(int cg, int planes) { return cg == 1 ? 64 : planes == 3 ? 128 : 256; }
+
+// Blocks that share a tile's sum: the largest power of two up to eight that still leaves every
+// block four slices and the cluster's blocks resident together.
+int split_of(int64_t tiles, int64_t slices, const DeviceInfo &dev) {
+  int s = 1;
+  while (s < 8 && tiles * (2 * s) <= dev.sm_count && slices >= 4 * (2 * s)) s *= 2;
+  return s;
+}
+
+// Forward product on prepared operands.
+cudaError_t run_forward(const Planes &x, int64_t x_rows, const Planes &w, bool shared_w,
+                        bool trans_w, int planes, Params prm, const DeviceInfo &dev,
+                        cudaStream_t stream) {
+  // Pairs from 64 rows per group on average.
+  const int cg = prm.rows > 64 * int64_t(prm.groups) ? 2 : 1;
+  const int bn = columns_of(cg, planes);
+  prm.panels = int((prm.N + 128 * cg - 1) / (128 * cg));
+  const int64_t tiles =
+      prm.panels * (std::min<int64_t>(prm.groups, prm.rows) + prm.rows / bn);
+  if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
+  prm.ksplit = cg == 2 ? 1 : split_of(tiles, (prm.K + kBK - 1) / kBK, dev);
+  prm.q_rows = int(x_rows);
+  prm.p_mn = trans_w ? 0 : 1;
+  prm.p_shared = shared_w ? 1 : 0;
+  Maps m;
+  cudaError_t e;
+  if ((e = tile_map(&m.p, w, trans_w ? 128 : 64)) != cudaSuccess ||
+      (e = row_map(&m.q, x, uint32_t(box_of(cg)))) != cudaSuccess ||
+      (e = row_map(&m.qr, x, 1)) != cudaSuccess)
+    return e;
+  m.e = m.p;
+  m.u = m.qr;
+  return launch_any(cg, planes, kForward, m, prm, tiles, dev, stream);
+}
+
+}  // namespace
+
+size_t grouped_workspace_bytes(const GroupedProblem &p) {
+  return add_sizes({plane_bytes(p.x, p.dtype), plane_bytes(p.w, p.dtype)});
+}
+
+cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void *workspace,
+                           cudaStream_t stream) {
+  char *ws = static_cast<char *>(workspace);
+  const bool shared = p.groups > 1 && p.w.count == 1;
+  Planes x, w;
+  cudaError_t e;
+  if ((e = make_planes(p.x, p.dtype, nullptr, &ws, dev, stream, &x)) != cudaSuccess ||
+      (e = make_planes(p.w, p.dtype, p.offsets, &ws, dev, stream, &w)) != cudaSuccess)
+    return e;
+  const int planes = p.dtype == TMM_F32 ? 3 : 1;
+  Params prm = {};
+  prm.rows = int(p.rows);
+  prm.groups = int(p.groups);
+  prm.offsets = p.offsets;
+  prm.row_index = p.row_index;
+  prm.K = int(p.K);
+  prm.N = int(p.N);
+  prm.idesc = type_desc(p.dtype);
+  prm.out = p.y;
+  prm.ld_out = p.ldy;
+  prm.out_type = out_type(p.dtype);
+  return run_forward(x, p.x.rows, w, shared, p.trans_w != 0, planes, prm, dev, stream);
+}
+
+size_t wgrad_workspace_bytes(const WgradProblem &p) {
+  return add_sizes({plane_bytes(p.x, p.dtype), plane_bytes(p.dy, p.dtype)});
+}
+
+cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *workspace,
+                         cudaStream_t stream) {
+  char *ws = static_cast<char *>(workspace);
+  Planes x, dy;
+  cudaError_t e;
+  if ((e = make_planes(p.x, p.dtype, nullptr, &ws, dev, stream, &x)) != cudaSuccess ||
+      (e = make_planes(p.dy, p.dtype, nullptr, &ws, dev, stream, &dy)) != cudaSuccess)
+    return e;
+  const int planes = p.dtype == TMM_F32 ? 3 : 1;
+  Params prm = {};
+  prm.rows = int(p.rows);
+  prm.groups = int(p.groups);
+  prm.offsets = p.offsets;
+  prm.row_index = p.row_index;
+  prm.q_rows = int(p.x.rows);
+  prm.q_cols = int(p.K);
+  prm.N = int(p.N);
+  prm.idesc = type_desc(p.dtype);
+  prm.out = p.dw;
+  prm.ld_out = p.lddw;
+  prm.stride_out = p.stride_dw;
+  prm.out_type = out_type(p.dtype);
+  prm.ksplit = 1;
+  const int cg = p.N > 128 ? 2 : 1;
+  const int bn = columns_of(cg, planes);
+  prm.panels = int((p.N + 128 * cg - 1) / (128 * cg));
+  const int64_t tiles = p.groups * prm.panels * ((p.K + bn - 1) / bn);
+  if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
+  if (cg == 1) prm.ksplit = split_of(tiles, (p.rows / p.groups + kBK - 1) / kBK, dev);
+  Maps m;
+  if ((e = row_map(&m.p, dy, kBK)) != cudaSuccess || (e = row_map(&m.e, dy, 1)) != cudaSuccess ||
+      (e = row_map(&m.q, x, kBK)) != cudaSuccess || (e = row_map(&m.qr, x, 1)) != cudaSuccess)
+    return e;
+  m.u = m.qr;
+  return launch_any(cg, planes, kWgrad, m, prm, tiles, dev, stream);
+}
+
+// The workspace holds u (a row for every p, in planes) and the planes of the operands.
+size_t lora_workspace_bytes(const LoraProblem &p) {
+  const __int128 u = __int128(p.dtype == TMM_F32 ? 6 : 2) * p.rows * round8(p.rank);
+  return add_sizes({u > __int128(INT64_MAX / 4) ? SIZE_MAX : round256(size_t(u)),
+                    plane_bytes(p.x, p.dtype), plane_bytes(p.w, p.dtype),
+                    plane_bytes(p.a, p.dtype), plane_bytes(p.b, p.dtype)});
+}
+
+cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *workspace,
+                        cudaStream_t stream) {
+  char *ws = static_cast<char *>(workspace);
+  const int planes = p.dtype == TMM_F32 ? 3 : 1;
+  const int64_t ldu = round8(p.rank);
+  uint16_t *u = reinterpret_cast<uint16_t *>(ws);
+  ws += round256(size_t(planes) * 2 * p.rows * ldu);
+  Planes x, w, a, b;
+  cudaError_t e;
+  if ((e = make_planes(p.x, p.dtype, nullptr, &ws, dev, stream, &x)) != cudaSuccess ||
+      (e = make_planes(p.w, p.dtype, nullptr, &ws, dev, stream, &w)) != cudaSuccess ||
+      (e = make_planes(p.a, p.dtype, p.offsets, &ws, dev, stream, &a)) != cudaSuccess ||
+      (e = make_planes(p.b, p.dtype, p.offsets, &ws, dev, stream, &b)) != cudaSuccess)
+    return e;
+  Params prm = {};
+  prm.rows = int(p.rows);
+  prm.groups = int(p.groups);
+  prm.offsets = p.offsets;
+  prm.row_index = p.row_index;
+  prm.K = int(p.K);
+  prm.N = int(p.rank);
+  prm.idesc = type_desc(p.dtype);
+  prm.out = u;
+  prm.ld_out = ldu;
+  prm.stride_out = p.rows * ldu;
+  prm.out_type = p.dtype == TMM_F32 ? kOutPlanes : out_type(p.dtype);
+  prm.scale = p.scale;
+  if ((e = run_forward(x, p.x.rows, a, p.groups > 1 && p.a.count == 1, p.trans_a != 0, planes, prm,
+                       dev, stream)) !=
+      cudaSuccess)
+    return e;
+
+  const int cg = p.rows > 64 ? 2 : 1;
+  const int bn = columns_of(cg, planes);
+  prm.N = int(p.N);
+  prm.q_rows = int(p.x.rows);
+  prm.rank = int(p.rank);
+  prm.panels = int((p.N + 128 * cg - 1) / (128 * cg));
+  const int64_t tiles = prm.panels * ((p.rows + bn - 1) / bn);
+  if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
+  prm.ksplit = cg == 2 ? 1 : split_of(tiles, (p.K + kBK - 1) / kBK, dev);
+  prm.p_mn = p.trans_w ? 0 : 1;
+  prm.p_shared = 1;
+  prm.e_mn = p.trans_b ? 0 : 1;
+  prm.e_shared = p.groups > 1 && p.b.count == 1;
+  prm.scale = nullptr;
+  prm.out = p.y;
+  prm.ld_out = p.ldy;
+  prm.stride_out = 0;
+  prm.out_type = out_type(p.dtype);
+  const Planes up = {u, planes, p.rows, p.rank, ldu, p.rows * ldu};
+  Maps m;
+  if ((e = tile_map(&m.p, w, p.trans_w ? 128 : 64)) != cudaSuccess ||
+      (e = row_map(&m.q, x, uint32_t(box_of(cg)))) != cudaSuccess ||
+      (e = row_map(&m.qr, x, 1)) != cudaSuccess ||
+      (e = tile_map(&m.e, b, p.trans_b ? 128 : 64)) != cudaSuccess ||
+      (e = row_map(&m.u, up, 1)) != cudaSuccess)
+    return e;
+  return launch_any(cg, planes, kLora, m, prm, tiles, dev, stream);
+}
+
+cudaError_t grouped_device_status(unsigned int *status, bool clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(status, g_grouped_status, sizeof(unsigned int));
+  if (e != cudaSuccess || !clear) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_grouped_status, &zero, sizeof(unsigned int));
+}
+
+void grouped_set_test_hooks(int drop_block, int64_t wait_limit_ns) {
+  g_drop_block.store(drop_block, std::memory_order_relaxed);
+  g_wait_limit_ns.store(wait_limit_ns > 0 ? wait_limit_ns : int64_t(10) * 1000 * 1000 * 1000,
+                        std::memory_order_relaxed);
+}
+
+}  // namespace tmm

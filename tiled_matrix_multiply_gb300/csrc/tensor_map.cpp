@@ -7,6 +7,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "grouped.h"
 #include "tmm_internal.h"
 
 namespace tmm {
@@ -43,6 +44,26 @@ cudaError_t encode_f32_2d(CUtensorMap *map, const float *base, int64_t rows, int
   const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float *>(base),
                               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t encode_16bit(CUtensorMap *map, const void *base, int dims, const uint64_t *size,
+                         const uint64_t *stride, const uint32_t *box) {
+  cudaError_t e = tensor_map_encoder_ready();
+  if (e != cudaSuccess) return e;
+  cuuint64_t size_[3], bytes_[2];
+  cuuint32_t box_[3];
+  const cuuint32_t estr[3] = {1, 1, 1};
+  for (int i = 0; i < dims; ++i) {
+    size_[i] = size[i];
+    box_[i] = box[i];
+    if (i + 1 < dims) bytes_[i] = stride[i] * 2;
+  }
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, cuuint32_t(dims),
+                              const_cast<void *>(base), size_, bytes_, box_, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

@@ -1,0 +1,254 @@
+"""Grouped operators: products whose right-hand matrix is chosen row by row.
+
+``group_rows`` sorts rows by a number each carries (its expert, its adapter);
+``gemm_grouped`` multiplies every group's rows by that group's matrix (and, with
+transposed views of the matrices, is the gradient with respect to the rows);
+``gemm_grouped_wgrad`` is the gradient with respect to the matrices;
+``gemm_lora`` adds every row's low-rank adapter to a shared projection.  Types
+are bfloat16, float16 and float32, the same for all matrices of a call.
+
+    plan = tmm.group_rows(experts, 8)               # experts: (tokens, k) integers
+    h = tmm.gemm_grouped(x, w, plan.offsets, rows=plan.rows)        # (tokens * k, N)
+    dw = tmm.gemm_grouped_wgrad(x, dh, plan.offsets, rows=plan.rows)
+    dx_rows = tmm.gemm_grouped(dh, w.transpose(1, 2), plan.offsets)
+    out = h[plan.position.view(tokens, k)]          # back in token order
+
+Everything is asynchronous on the current torch stream of the operands' device;
+no call reads a group's size on the host.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple
+
+
+class RowGroups(NamedTuple):
+    """Slots sorted by group (see ``group_rows``), int32 CUDA tensors."""
+    offsets: object     # (groups + 1): group g owns places offsets[g] .. offsets[g + 1] - 1
+    order: object       # (slots): the slot at each place
+    rows: object        # (slots): its token, order // k
+    position: object    # (slots): the place of each slot
+
+
+def _dtype_code(x, name):
+    import torch
+    from . import _abi
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    codes = {torch.float32: _abi.TMM_F32, torch.bfloat16: _abi.TMM_BF16,
+             torch.float16: _abi.TMM_F16}
+    if x.dtype not in codes:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {x.dtype}")
+    return codes[x.dtype]
+
+
+def _operand(x, name, like, dims, transposable=False):
+    """(rows, cols, ld, stride, trans) of a matrix or a stack of matrices (dims = 3).
+
+    stride: elements between matrices (0: one matrix, or an expanded one); trans = 1: every
+    matrix is the transposed view of a row-major one, whose ld this is.
+    """
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dim() != dims:
+        raise ValueError(f"{name} must be {dims}-D, got shape {tuple(x.shape)}")
+    if x.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype} like the first operand, got {x.dtype}")
+    if x.device != like.device:
+        raise ValueError(f"{name} is on {x.device}, the first operand on {like.device}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    rows, cols = x.shape[-2:]
+    s0, s1 = x.stride(-2), x.stride(-1)
+    stride = x.stride(0) if dims == 3 and x.shape[0] > 1 else 0
+    if x.numel() == 0:
+        return rows, cols, max(cols, 1), max(stride, 0), 0
+    if (cols <= 1 or s1 == 1) and (rows <= 1 or s0 >= cols):
+        return rows, cols, max(s0 if rows > 1 else cols, cols, 1), stride, 0
+    if transposable and (rows <= 1 or s0 == 1) and (cols <= 1 or s1 >= rows):
+        return rows, cols, max(s1 if cols > 1 else rows, rows, 1), stride, 1
+    raise ValueError(f"{name} must be row-major (unit column stride)"
+                     + (" or a transposed row-major view" if transposable else ""))
+
+
+def _index_tensor(t, name, like, length):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+        raise TypeError(f"{name} must be an int32 tensor")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, the operands on {like.device}")
+    if t.dim() != 1 or (length is not None and t.numel() != length) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-D tensor"
+                         + (f" of {length} values" if length is not None else ""))
+    return t
+
+
+def _workspace(given, need, like):
+    """A workspace of `need` bytes: the given tensor, or a new one (torch's start 256-byte
+    aligned at least)."""
+    import torch
+    if given is None:
+        if need == 0:
+            return 0, 0, None
+        given = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif given.device != like.device or not given.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the operands' device")
+    return given.data_ptr(), given.numel() * given.element_size(), given
+
+
+def _run(name, rc):
+    from . import _abi
+    if rc != _abi.TMM_OK:
+        raise _abi.TmmError(name, rc, _abi.last_error())
+
+
+def _on(like, stream):
+    import torch
+    return stream if stream is not None else torch.cuda.current_stream(like.device)
+
+
+def group_rows(index, groups, stream=None):
+    """Stable grouping of the slots of ``index`` (tokens,) or (tokens, k), int32 or int64.
+
+    A slot's group is its number where that is in [0, groups); the other slots belong to no
+    group and come last.  Returns ``RowGroups``.
+    """
+    import torch
+    from . import _abi
+    if not isinstance(index, torch.Tensor) or index.dtype not in (torch.int32, torch.int64):
+        raise TypeError("index must be an int32 or int64 tensor")
+    if not index.is_cuda:
+        raise ValueError("index must be a CUDA tensor")
+    if index.dim() not in (1, 2) or not index.is_contiguous():
+        raise ValueError("index must be a contiguous tensor (tokens,) or (tokens, k)")
+    tokens = index.shape[0]
+    fan = index.shape[1] if index.dim() == 2 else 1
+    if fan < 1:
+        raise ValueError("index must have at least one column")
+    slots = tokens * fan
+    # One allocation; every array starts on a 16-byte boundary.
+    at = (slots + 3) // 4 * 4
+    buf = torch.empty(3 * at + groups + 1, dtype=torch.int32, device=index.device)
+    order, rows, position = (buf[i * at:i * at + slots] for i in range(3))
+    offsets = buf[3 * at:]
+    lib = _abi.load()
+    need = int(lib.group_rows_workspace_size(tokens, fan, groups))
+    ws, ws_bytes, keep = _workspace(None, need, index)
+    with torch.cuda.device(index.device):
+        _run("group_rows", lib.group_rows(
+            tokens, fan, groups, index.data_ptr(), 64 if index.dtype == torch.int64 else 32,
+            offsets.data_ptr(), order.data_ptr(), rows.data_ptr(), position.data_ptr(), ws,
+            ws_bytes, _on(index, stream).cuda_stream))
+    return RowGroups(offsets, order, rows, position)
+
+
+def _result(given, name, shape, like):
+    import torch
+    if given is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    if tuple(given.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(given.shape)}")
+    return given
+
+
+def gemm_grouped(x, w, offsets, rows=None, y=None, workspace=None, stream=None):
+    """y[p] = x[rows[p]] w[g] for the rows p of every group g (offsets[g] <= p < offsets[g+1]).
+
+    x: (x_rows, K); w: (groups, K, N), or a transposed view of (groups, N, K); offsets: int32
+    (groups + 1); rows: int32, the row of x that each p reads (a number outside x reads zeros),
+    or None for p itself.  y: (len(rows) or x_rows, N); its rows of no group are zero.
+    """
+    import torch
+    from . import _abi
+    code = _dtype_code(x, "x")
+    x_rows, K, ldx, _, _ = _operand(x, "x", x, 2)
+    K2, N, ldw, stride_w, trans = _operand(w, "w", x, 3, True)
+    groups = w.shape[0]
+    if K != K2:
+        raise ValueError(f"inner dimensions differ: x is {tuple(x.shape)}, w is {tuple(w.shape)}")
+    _index_tensor(offsets, "offsets", x, groups + 1)
+    if rows is not None:
+        _index_tensor(rows, "rows", x, None)
+    R = rows.numel() if rows is not None else x_rows
+    y = _result(y, "y", (R, N), x)
+    _, _, ldy, _, _ = _operand(y, "y", x, 2)
+    lib = _abi.load()
+    head = (code, trans, groups, R, N, K, x.data_ptr(), x_rows, ldx)
+    need = int(lib.gemm_grouped_workspace_size(*head, w.data_ptr(), ldw, stride_w))
+    ws, ws_bytes, keep = _workspace(workspace, need, x)
+    with torch.cuda.device(x.device):
+        _run("gemm_grouped", lib.gemm_grouped(
+            *head, offsets.data_ptr(), rows.data_ptr() if rows is not None else 0, w.data_ptr(),
+            ldw, stride_w, y.data_ptr(), ldy, ws, ws_bytes, _on(x, stream).cuda_stream))
+    return y
+
+
+def gemm_grouped_wgrad(x, dy, offsets, rows=None, dw=None, workspace=None, stream=None):
+    """dw[g] = sum over the rows p of group g of x[rows[p]]^T dy[p]: (groups, K, N).
+
+    The gradient of ``gemm_grouped`` with respect to w; x, offsets and rows as there, dy (R, N).
+    """
+    import torch
+    from . import _abi
+    code = _dtype_code(x, "x")
+    x_rows, K, ldx, _, _ = _operand(x, "x", x, 2)
+    R, N, lddy, _, _ = _operand(dy, "dy", x, 2)
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must be a 1-D tensor of groups + 1 values")
+    _index_tensor(offsets, "offsets", x, None)
+    groups = offsets.numel() - 1
+    if rows is not None:
+        _index_tensor(rows, "rows", x, R)
+    elif x_rows != R:
+        raise ValueError(f"x has {x_rows} rows, dy {R}")
+    dw = _result(dw, "dw", (groups, K, N), x)
+    _, _, lddw, stride, _ = _operand(dw, "dw", x, 3)
+    lib = _abi.load()
+    head = (code, groups, R, N, K, x.data_ptr(), x_rows, ldx)
+    need = int(lib.gemm_grouped_wgrad_workspace_size(*head, dy.data_ptr(), lddy))
+    ws, ws_bytes, keep = _workspace(workspace, need, x)
+    with torch.cuda.device(x.device):
+        _run("gemm_grouped_wgrad", lib.gemm_grouped_wgrad(
+            *head, offsets.data_ptr(), rows.data_ptr() if rows is not None else 0, dy.data_ptr(),
+            lddy, dw.data_ptr(), lddw, stride, ws, ws_bytes, _on(x, stream).cuda_stream))
+    return dw
+
+
+def gemm_lora(x, w, a, b, scale, offsets, rows=None, y=None, workspace=None, stream=None):
+    """y[t] = x[t] w + scale[g] (x[t] a[g]) b[g], g the adapter of row t.
+
+    x: (T, K); w: (K, N); a: (adapters, K, r); b: (adapters, r, N) -- w, a and b also as
+    transposed views; scale: float32 (adapters,).  offsets, rows: the rows grouped by adapter,
+    ``offsets`` and ``order`` of ``group_rows(index, adapters)``; rows past offsets[-1] have no
+    adapter.  rows=None: x is in group order already.
+    """
+    import torch
+    from . import _abi
+    code = _dtype_code(x, "x")
+    T, K, ldx, _, _ = _operand(x, "x", x, 2)
+    K2, N, ldw, _, tw = _operand(w, "w", x, 2, True)
+    K3, r, lda, stride_a, ta = _operand(a, "a", x, 3, True)
+    r2, N2, ldb, stride_b, tb = _operand(b, "b", x, 3, True)
+    groups = a.shape[0]
+    if K != K2 or K != K3 or N != N2 or r != r2 or b.shape[0] != groups:
+        raise ValueError(f"shapes do not fit: x {tuple(x.shape)}, w {tuple(w.shape)}, "
+                         f"a {tuple(a.shape)}, b {tuple(b.shape)}")
+    if not isinstance(scale, torch.Tensor) or scale.dtype != torch.float32:
+        raise TypeError("scale must be a float32 tensor")
+    if scale.shape != (groups,) or scale.device != x.device or not scale.is_contiguous():
+        raise ValueError(f"scale must be a contiguous tensor of {groups} values on {x.device}")
+    _index_tensor(offsets, "offsets", x, groups + 1)
+    if rows is not None:
+        _index_tensor(rows, "rows", x, T)
+    y = _result(y, "y", (T, N), x)
+    _, _, ldy, _, _ = _operand(y, "y", x, 2)
+    lib = _abi.load()
+    head = (code, tw, ta, tb, groups, T, N, K, r, x.data_ptr(), ldx)
+    mats = (w.data_ptr(), ldw, a.data_ptr(), lda, stride_a, b.data_ptr(), ldb, stride_b)
+    need = int(lib.gemm_lora_workspace_size(*head, *mats))
+    ws, ws_bytes, keep = _workspace(workspace, need, x)
+    with torch.cuda.device(x.device):
+        _run("gemm_lora", lib.gemm_lora(
+            *head, offsets.data_ptr(), rows.data_ptr() if rows is not None else 0, *mats,
+            scale.data_ptr(), y.data_ptr(), ldy, ws, ws_bytes, _on(x, stream).cuda_stream))
+    return y
