@@ -21,12 +21,22 @@ from __future__ import annotations
 
 from ._abi import (TMM_ERR_ALIAS, TMM_ERR_CUDA, TMM_ERR_INVALID_ARG,  # noqa: F401
                    TMM_ERR_UNSUPPORTED_DEVICE, TMM_OK, TmmError)
-from .grouped import (RowGroups, gemm_grouped, gemm_grouped_wgrad, gemm_lora,  # noqa: F401
-                      group_rows)
 
 __all__ = ["gemm_f32", "gemm_f32_naive", "gemm_f32_tc3", "tc3_workspace_bytes",
            "window_sum_f32", "sum_f32", "softmax_rows_f32", "group_rows", "RowGroups", "gemm_grouped",
            "gemm_grouped_wgrad", "gemm_lora", "check_device", "raw_call", "TmmError"]
+
+
+_GROUPED = ("group_rows", "RowGroups", "gemm_grouped", "gemm_grouped_wgrad", "gemm_lora")
+
+
+def __getattr__(name):
+    # The grouped operators' module imports torch when it is loaded; the package itself does not.
+    if name in _GROUPED:
+        from . import grouped
+        globals().update({n: getattr(grouped, n) for n in _GROUPED})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _matrix(x, name, allow_transposed=False):

@@ -79,6 +79,8 @@ def library_path() -> str:
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load libtmm_gemm.so and declare its signatures (once per process)."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib

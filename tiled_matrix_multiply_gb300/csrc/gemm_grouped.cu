@@ -40,8 +40,8 @@
 //          scratch, no atomics: results are deterministic).  For few rows per group, where
 //          reading w is the bound and more blocks read it faster.
 // Both are persistent: the tile list is made in every block from the group offsets, which only
-// the GPU knows.  Roles: warp 0 copies, one thread of warp 1 issues the products, eight warps
-// take results out.  Every wait is bounded (globaltimer); on timeout bit 1 of the status word
+// the GPU knows.  Roles: four warps copy, eight take results out, one issues the
+// products.  Every wait is bounded (globaltimer); on timeout bit 1 of the status word
 // is set and the kernel runs to its end.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -63,14 +63,18 @@ namespace {
 
 constexpr int kForward = 0, kWgrad = 1, kLora = 2;
 constexpr int kBK = 64;                  // 16-bit values per K slice: one 128-byte swizzle row
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kCopyWarps = 4, kEpiWarps = 8;
+constexpr int kEpi0 = kCopyWarps;                  // first of the result warps
+constexpr int kMmaWarp = kCopyWarps + kEpiWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kChunk = 2;                // slices per tensor-memory sum of split operands
 constexpr uint32_t kPTile = 128 * 128;   // 128 lanes x 64 values: 16 KiB
 constexpr uint32_t kMaxSmem = 232448;    // 227 KiB
 
 // How the results are written.
-constexpr int kOutF32 = 0, kOutBF16 = 1, kOutF16 = 2, kOutPlanes = 3;   // planes: split3
+constexpr int kOutF32 = 0, kOutBF16 = 1, kOutF16 = 2;
+constexpr int kOutU = 3;       // the adapters' u: three planes (split3), or a pair of values
+
 
 template <int CG, int PLANES>
 struct Shape {
@@ -83,7 +87,9 @@ struct Shape {
   static constexpr uint32_t kTmemCols =
       PLANES == 3 ? 4 * kBN : 2 * kBN;               // two accumulators (of each kind)
   static constexpr uint32_t kRed = CG == 1 ? 128 * kBN * 4 : 0;
-  static constexpr uint32_t kTable = (kMaxGroups + 1) * 4 * 3;
+  // Values of `rank` per slice of the adapters' part: 16-bit u is a pair of values (hi and lo).
+  static constexpr int kRankSlice = PLANES == 3 ? 64 : 32;
+  static constexpr uint32_t kTable = (kMaxGroups + 1) * 4 * 3 + kCopyWarps * 128 + 116;
   static constexpr uint32_t kBars = 8 * (2 * kStages + 5) + 32;
   static constexpr uint32_t kSmem = 1024 + kStages * kStage + kRed + kTable + kBars;
   static_assert(kSmem <= kMaxSmem, "one block's shared memory");
@@ -107,6 +113,7 @@ struct Params {
   void *out;
   int64_t ld_out, stride_out;   // stride: of dw's matrices, or of the result's planes
   int out_type;
+  int n_out;             // columns written (from N on: zeros)
   const float *scale;    // per group, or NULL
   int ksplit;            // blocks of a cluster that share a tile's sum (CG = 1)
   int64_t wait_limit_ns;
@@ -150,6 +157,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int64_t
   while (!mbar_try_wait(bar, parity))
     if (int64_t(timer_ns() - t0) > limit_ns) return false;
   return true;
+}
+// True in one thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -375,12 +389,12 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const Table &tab, int t
 
 // This block's K slices [s0, s1) of a tile: the slices of the base sum, then those of the
 // adapters in the tile; blocks that share a tile take equal runs of them.
-template <int MODE>
+template <int MODE, int RS>
 __device__ __forceinline__ void slices_of(const Params &p, const Tile &t, int rank, int &base,
                                           int &s0, int &s1) {
   base = (t.klen + kBK - 1) / kBK;
   int n = base;
-  if (MODE == kLora) n += t.en * ((p.rank + kBK - 1) / kBK);
+  if (MODE == kLora) n += t.en * ((p.rank + RS - 1) / RS);
   if (p.ksplit == 1) {
     s0 = 0;
     s1 = n;
@@ -415,23 +429,40 @@ __device__ __forceinline__ void split3(float x, uint16_t (&h)[3]) {
   h[2] = uint16_t(nearest_bf16(__float_as_uint(s)) >> 16);
 }
 
-// One result at element offset `o` of the output.  Split operands (PLANES = 3) give FP32 or
-// planes, 16-bit operands their own type.
+// The adapters' u in a 16-bit type T: v = hi + lo, hi the value rounded to T and lo what that
+// leaves, so that u keeps about twice T's bits and only the final result is rounded to T.
+// Column n is stored at 64 (n / 32) + n % 32, its lo 32 columns on.
+template <typename T>
+__device__ __forceinline__ void store_pair(void *row, int n, float v) {
+  T *o = static_cast<T *>(row) + (n >> 5) * 64 + (n & 31);
+  const T hi = T(v);
+  const float f = float(hi);
+  o[0] = hi;
+  o[32] = T(isfinite(f) ? v - f : 0.0f);
+}
+
+// One result at column n of the row at element offset `o` of the output.  Split operands
+// (PLANES = 3) give FP32, 16-bit operands their own type, and both the forms of u.
 template <int PLANES>
-__device__ __forceinline__ void store_out(const Params &p, int64_t o, float v) {
+__device__ __forceinline__ void store_out(const Params &p, int64_t o, int n, float v) {
   if constexpr (PLANES == 3) {
     if (p.out_type == kOutF32) {
-      static_cast<float *>(p.out)[o] = v;
+      static_cast<float *>(p.out)[o + n] = v;
     } else {
       uint16_t h[3];
       split3(v, h);
 #pragma unroll
-      for (int i = 0; i < 3; ++i) static_cast<uint16_t *>(p.out)[o + i * p.stride_out] = h[i];
+      for (int i = 0; i < 3; ++i) static_cast<uint16_t *>(p.out)[o + n + i * p.stride_out] = h[i];
     }
   } else if (p.out_type == kOutBF16) {
-    static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(v);
+    static_cast<__nv_bfloat16 *>(p.out)[o + n] = __float2bfloat16_rn(v);
+  } else if (p.out_type == kOutF16) {
+    static_cast<__half *>(p.out)[o + n] = __float2half_rn(v);
   } else {
-    static_cast<__half *>(p.out)[o] = __float2half_rn(v);
+    uint16_t *row = static_cast<uint16_t *>(p.out) + o;
+    if (n >= p.N) v = 0.0f;
+    if (p.idesc & (1u << 7)) store_pair<__nv_bfloat16>(row, n, v);
+    else store_pair<__half>(row, n, v);
   }
 }
 
@@ -460,16 +491,16 @@ __device__ __forceinline__ void store_columns(const Params &p, const Tile &t, in
     row = lane < count ? p.row_index[t.q0 + c0 + lane] : -1;
     if (row >= p.q_rows) row = -1;
   }
-  const bool in = n < p.N;
-  int64_t o = out_row<kForward>(p, t, c0) + n;
+  const bool in = n < p.n_out;
+  int64_t o = out_row<kForward>(p, t, c0);
   if (MODE == kWgrad) o += int64_t(t.g) * p.stride_out;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     if (by_row) {
       const int r = __shfl_sync(~0u, row, j);
-      if (in && r >= 0) store_out<PLANES>(p, int64_t(r) * p.ld_out + n, v[j] * scale);
+      if (in && r >= 0) store_out<PLANES>(p, int64_t(r) * p.ld_out, n, v[j] * scale);
     } else {
-      if (in && j < count) store_out<PLANES>(p, o, v[j] * scale);
+      if (in && j < count) store_out<PLANES>(p, o, n, v[j] * scale);
       o += p.ld_out;
     }
   }
@@ -499,13 +530,16 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   const uint32_t bar_drain = bar_tempty + 16;
   const uint32_t slot = bar_drain + 8;             // tensor memory address; then the counts
 
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int *const tab_gid = reinterpret_cast<int *>(smem + (table - base));
   int *const tab_row = tab_gid + (kMaxGroups + 1);
   int *const tab_tile = tab_row + (kMaxGroups + 1);
+  // Row numbers that a copy warp is about to fetch, four to a copy; 16-byte aligned.
+  int *const my_rows = reinterpret_cast<int *>(
+      (reinterpret_cast<uintptr_t>(tab_tile + (kMaxGroups + 1)) + 15) & ~uintptr_t(15)) + 32 * warp;
   volatile uint32_t *const slot_ptr = reinterpret_cast<volatile uint32_t *>(smem + (slot - base));
   float *const red_ptr = reinterpret_cast<float *>(smem + (red - base));
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int cluster_size = CG == 2 ? 2 : p.ksplit;
   const int cluster = int(blockIdx.x) / cluster_size;
@@ -529,7 +563,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     mbar_init(bar_drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     if constexpr (CG == 2) {
       asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
                    "r"(S::kTmemCols)
@@ -608,189 +642,236 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   uint32_t done = 0;   // tiles with a sum so far
 
   // Forward: rows of the result that belong to no group are zero.
-  if (MODE == kForward && warp >= 2) {
+  if (MODE == kForward && warp >= kEpi0 && warp < kMmaWarp) {
     const int lo = int(slot_ptr[3]), hi = int(slot_ptr[4]);
     for (int64_t i = blockIdx.x; i < int64_t(lo) + (p.rows - hi); i += gridDim.x) {
       const int64_t row = i < lo ? i : hi + (i - lo);
-      for (int n = int(threadIdx.x) - 64; n < p.N; n += 32 * kEpiWarps)
-        store_out<PLANES>(p, row * p.ld_out + n, 0.0f);
+      for (int n = int(threadIdx.x) - 32 * kEpi0; n < p.n_out; n += 32 * kEpiWarps)
+        store_out<PLANES>(p, row * p.ld_out, n, 0.0f);
     }
   }
 
   for (int t = cluster; t < tab.tiles; t += clusters) {
     const Tile tile = tile_at<CG, MODE, PLANES>(p, tab, t);
     int nbase, s0, s1;
-    slices_of<MODE>(p, tile, CG == 2 ? 0 : int(rank), nbase, s0, s1);
-    const int per_rank = MODE == kLora ? (p.rank + kBK - 1) / kBK : 1;
+    slices_of<MODE, S::kRankSlice>(p, tile, CG == 2 ? 0 : int(rank), nbase, s0, s1);
+    const int per_rank = MODE == kLora ? (p.rank + S::kRankSlice - 1) / S::kRankSlice : 1;
 
-    if (warp == 0) {
+    if (warp < kCopyWarps) {
       // ---- copies ----
       const int hr = tile.bn / CG;                      // columns staged by this block
       const int qf = tile.q0 + half_rank * hr;          // the first of them
       const int n0 = tile.n0 + half_rank * 128;
       const int pg = (p.p_shared ? 0 : tile.g);
       const int pcount = p.p_shared ? 1 : p.groups;
-      // Rows of x this lane fetches, four of them (forward, adapters: columns 4 lane .. + 3 of
-      // this block's; gradient: rows 4 (lane % 16) .. + 3 of the next slice); -1 is a zero row.
-      int mine[4];
-      auto fetch_rows = [&](int first, int limit) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int at = first + i;
-          int row = -1;
-          if (at < limit) {
-            row = p.row_index ? p.row_index[at] : at;
-            if (row < 0 || row >= p.q_rows) row = -1;
-          }
-          mine[i] = row;
-        }
+      // Columns of this block that hold rows (the others' sums are not stored, so whatever
+      // their part of the ring holds will do), in groups of four; of the other block of a pair.
+      const auto held = [&](int half) {
+        return max(0, min(tile.qn - half * hr, hr));
       };
       const bool by_row = p.row_index != nullptr;
-      if (MODE != kWgrad && by_row) fetch_rows(qf + 4 * lane, tile.q0 + tile.qn);
-      if (MODE == kWgrad && s0 < s1)
-        fetch_rows(tile.k0 + s0 * kBK + 4 * (lane & 15), tile.k0 + tile.klen);
+      const int quads = (held(half_rank) + 3) / 4;
+      const int boxes = (held(half_rank) + S::kBox - 1) / S::kBox;
+      // Copies by row are dealt out to the copy warps: warp w issues groups w, w + 4, ... (a copy
+      // of four rows takes a warp about 80 cycles to issue, whatever its size; from one warp 32
+      // of them took 2.7 times as long as the slice's products).  Lane l looks up row l % 4 of
+      // the warp's group l / 4; -1 is a row of zeros.
+      const int row_in_slice = 4 * (warp + kCopyWarps * (lane >> 2)) + (lane & 3);
+      auto row_of = [&](int at, int limit) {
+        if (at >= limit) return -1;
+        const int row = by_row ? p.row_index[at] : at;
+        return row >= 0 && row < p.q_rows ? row : -1;
+      };
+      int next = -1;      // gradient: this lane's row of the next slice
+      if (MODE != kWgrad && by_row) {
+        __syncwarp();
+        my_rows[lane] = row_of(qf + row_in_slice, tile.q0 + tile.qn);
+        __syncwarp();
+      }
+      if (MODE == kWgrad && s0 < s1 && lane < 16)
+        next = row_of(tile.k0 + s0 * kBK + row_in_slice, tile.k0 + tile.klen);
       for (int s = s0; s < s1 && !timed_out; ++s, ++r) {
         const uint32_t st_i = r % S::kStages;
-        bool ok = true;
-        if (lane == 0 && r >= S::kStages)
-          ok = mbar_wait(bar_empty + 8 * st_i, ((r / S::kStages) - 1) & 1u, p.wait_limit_ns);
-        if (!__all_sync(~0u, ok)) {
-          timed_out = true;
-          break;
+        if (r >= S::kStages) {
+          const bool ok =
+              mbar_wait(bar_empty + 8 * st_i, ((r / S::kStages) - 1) & 1u, p.wait_limit_ns);
+          if (!__all_sync(~0u, ok)) {
+            timed_out = true;
+            break;
+          }
         }
         const uint32_t st = base + st_i * S::kStage;
         const uint32_t sq = st + PLANES * kPTile;
         const uint32_t full_local = bar_full + 8 * st_i;
         const uint32_t full = CG == 2 ? map_rank(full_local, 0) : full_local;
-        uint32_t bytes;
-        int cnt = kBK;
         if (MODE == kWgrad) {
-          cnt = min(kBK, tile.klen - s * kBK);
-          bytes = uint32_t((cnt + 15) & ~15) * 128u * uint32_t(2 + hr / 64) * PLANES;
-        } else {
-          bytes = PLANES * (kPTile + uint32_t(hr) * 128u);
-        }
-        if (lane == 0 && leader) {
-          bytes *= CG;
-          if (int(blockIdx.x) == p.drop_block && r == 0) bytes += 16;
-          mbar_expect(full_local, bytes);
-        }
-        __syncwarp();
-        if (MODE == kWgrad) {
+          const int cnt = min(kBK, tile.klen - s * kBK);
+          const int groups4 = (cnt + 15) / 16 * 4;      // groups of four rows copied
           const int p0 = tile.k0 + s * kBK;
-          const int quads = (cnt + 15) / 16 * 4;        // groups of four rows copied
-          const int quad = lane & 15, part = lane >> 4;
           const int qblocks = hr / 64;
-          if (cnt == kBK) {
-            if (lane < 2 * PLANES)
-              tma_2d<CG>(st + lane * 8192, &map_p, n0 + (lane & 1) * 64,
-                         p0 + (lane >> 1) * p.rows, full);
-          } else if (quad < quads) {
+          if (by_row || cnt < kBK) {
+            __syncwarp();
+            if (lane < 16) my_rows[lane] = next;
+            __syncwarp();
+            if (s + 1 < s1 && lane < 16)
+              next = row_of(p0 + kBK + row_in_slice, tile.k0 + tile.klen);
+          } else if (s + 1 < s1 && lane < 16) {
+            next = row_of(p0 + kBK + row_in_slice, tile.k0 + tile.klen);
+          }
+          if (elect_one()) {
+            if (warp == 0 && leader) {
+              uint32_t bytes = uint32_t(groups4) * 512u * uint32_t(2 + qblocks) * PLANES * CG;
+              if (int(blockIdx.x) == p.drop_block && r == 0) bytes += 16;
+              mbar_expect(full_local, bytes);
+            }
+            if (cnt == kBK) {
+              if (warp == 0) {
 #pragma unroll
-            for (int pl = 0; pl < PLANES; ++pl) {
-              int y[4];
+                for (int i = 0; i < 2 * PLANES; ++i)
+                  tma_2d<CG>(st + i * 8192, &map_p, n0 + (i & 1) * 64, p0 + (i >> 1) * p.rows, full);
+              }
+            } else {
+              for (int g = warp; g < groups4; g += kCopyWarps)
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                y[i] = 4 * quad + i < cnt ? p0 + 4 * quad + i + pl * p.rows : PLANES * p.rows;
-              tma_rows4<CG>(st + pl * kPTile + part * 8192 + quad * 512, &map_e, n0 + part * 64, y,
-                            full);
+                for (int i = 0; i < 2 * PLANES; ++i) {
+                  int y[4];
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    y[j] = 4 * g + j < cnt ? p0 + 4 * g + j + (i >> 1) * p.rows : PLANES * p.rows;
+                  tma_rows4<CG>(st + i * 8192 + g * 512, &map_e, n0 + (i & 1) * 64, y, full);
+                }
+            }
+            if (cnt == kBK && !by_row) {
+              if (warp == 1)
+                for (int pl = 0; pl < PLANES; ++pl)
+                  for (int b = 0; b < qblocks; ++b)
+                    tma_2d<CG>(sq + pl * S::kQTile + b * 8192, &map_q, qf + b * 64,
+                               p0 + pl * p.q_rows, full);
+            } else {
+              for (int g = warp, k = 0; g < groups4; g += kCopyWarps, ++k) {
+                const int4 v = *reinterpret_cast<const int4 *>(my_rows + 4 * k);
+#pragma unroll
+                for (int pl = 0; pl < PLANES; ++pl) {
+                  const int out = PLANES * p.q_rows, add = pl * p.q_rows;
+                  const int y[4] = {v.x < 0 ? out : v.x + add, v.y < 0 ? out : v.y + add,
+                                    v.z < 0 ? out : v.z + add, v.w < 0 ? out : v.w + add};
+                  for (int b = 0; b < qblocks; ++b)
+                    tma_rows4<CG>(sq + pl * S::kQTile + b * 8192 + g * 512, &map_qr, qf + b * 64, y,
+                                  full);
+                }
+              }
             }
           }
-          if (cnt == kBK && !by_row) {
-            if (lane < qblocks * PLANES) {
-              const int pl = lane / qblocks, b = lane - pl * qblocks;
-              tma_2d<CG>(sq + pl * S::kQTile + b * 8192, &map_q, qf + b * 64, p0 + pl * p.q_rows,
-                         full);
-            }
-          } else if (quad < quads) {
-#pragma unroll
-            for (int pl = 0; pl < PLANES; ++pl) {
-              int y[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                y[i] = mine[i] < 0 ? PLANES * p.q_rows : mine[i] + pl * p.q_rows;
-              for (int b = part; b < qblocks; b += 2)
-                tma_rows4<CG>(sq + pl * S::kQTile + b * 8192 + quad * 512, &map_qr, qf + b * 64, y,
-                              full);
-            }
-          }
-          if (s + 1 < s1)
-            fetch_rows(tile.k0 + (s + 1) * kBK + 4 * quad, tile.k0 + tile.klen);
+          __syncwarp();
         } else {
           const bool ext = MODE == kLora && s >= nbase;
-          int k0 = s * kBK, g = pg, gcount = pcount, lo = 0, hi = 0;
+          int k0 = s * kBK, g = pg, gcount = pcount, lo = 0, hi = 0, rank0 = 0;
           if (ext) {
             const int e = (s - nbase) / per_rank;
-            k0 = (s - nbase - e * per_rank) * kBK;
+            const int j = s - nbase - e * per_rank;
+            k0 = j * kBK;                    // of u
+            rank0 = j * S::kRankSlice;       // of b
             g = p.e_shared ? 0 : tab.gid[tile.e0 + e];
             gcount = p.e_shared ? 1 : p.groups;
             lo = tab.row[tile.e0 + e];
-            hi = tab.row[tile.e0 + e + 1];
+            hi = min(tab.row[tile.e0 + e + 1], tile.q0 + tile.qn);
           }
-          const CUtensorMap *mp = ext ? &map_e : &map_p;
-          if (ext ? p.e_mn : p.p_mn) {
-            if (lane < 2 * PLANES)
-              tma_3d<CG>(st + lane * 8192, mp, n0 + (lane & 1) * 64, k0, g + (lane >> 1) * gcount,
-                         full);
-          } else if (lane < PLANES) {
-            tma_3d<CG>(st + lane * kPTile, mp, k0, n0, g + lane * gcount, full);
-          }
-          if (ext || by_row) {
-            if (lane < hr / 4) {
+          if (elect_one()) {
+            if (warp == 0) {
+              if (leader) {
+                uint32_t bytes = CG * PLANES * kPTile;
+                if (ext && p.e_mn) bytes = CG * PLANES * 2 * S::kRankSlice * 128;
 #pragma unroll
-              for (int pl = 0; pl < PLANES; ++pl) {
-                int y[4];
+                for (int h = 0; h < CG; ++h)
+                  bytes += PLANES * (ext || by_row
+                                         ? uint32_t((held(h) + 3) / 4) * 512u
+                                         : uint32_t((held(h) + S::kBox - 1) / S::kBox) *
+                                               uint32_t(S::kBox * 128));
+                if (int(blockIdx.x) == p.drop_block && r == 0) bytes += 16;
+                mbar_expect(full_local, bytes);
+              }
+              if (ext) {
+                if (p.e_mn) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  if (ext) {
-                    const int at = qf + 4 * lane + i;
-                    y[i] = at >= lo && at < hi && at < tile.q0 + tile.qn ? at + pl * p.rows
-                                                                         : PLANES * p.rows;
-                  } else {
-                    y[i] = mine[i] < 0 ? PLANES * p.q_rows : mine[i] + pl * p.q_rows;
-                  }
+                  for (int i = 0; i < 2 * PLANES; ++i)
+                    tma_3d<CG>(st + i * 8192, &map_e, n0 + (i & 1) * 64, rank0,
+                               g + (i >> 1) * gcount, full);
+                } else {
+#pragma unroll
+                  for (int i = 0; i < PLANES; ++i)
+                    tma_3d<CG>(st + i * kPTile, &map_e, rank0, n0, g + i * gcount, full);
                 }
-                tma_rows4<CG>(sq + pl * S::kQTile + lane * 512, ext ? &map_u : &map_qr, k0, y,
-                              full);
+              } else if (p.p_mn) {
+#pragma unroll
+                for (int i = 0; i < 2 * PLANES; ++i)
+                  tma_3d<CG>(st + i * 8192, &map_p, n0 + (i & 1) * 64, k0, g + (i >> 1) * gcount,
+                             full);
+              } else {
+#pragma unroll
+                for (int i = 0; i < PLANES; ++i)
+                  tma_3d<CG>(st + i * kPTile, &map_p, k0, n0, g + i * gcount, full);
               }
             }
-          } else {
-            const int boxes = hr / S::kBox;
-            if (lane < boxes * PLANES) {
-              const int pl = lane / boxes, b = lane - pl * boxes;
-              tma_2d<CG>(sq + pl * S::kQTile + b * (S::kBox * 128), &map_q, k0,
-                         qf + b * S::kBox + pl * p.q_rows, full);
+            if (ext) {
+              for (int c = warp; c < quads; c += kCopyWarps) {
+                const int at = qf + 4 * c;
+#pragma unroll
+                for (int pl = 0; pl < PLANES; ++pl) {
+                  int y[4];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    y[i] = at + i >= lo && at + i < hi ? at + i + pl * p.rows : PLANES * p.rows;
+                  tma_rows4<CG>(sq + pl * S::kQTile + c * 512, &map_u, k0, y, full);
+                }
+              }
+            } else if (by_row) {
+              for (int c = warp, k = 0; c < quads; c += kCopyWarps, ++k) {
+                const int4 v = *reinterpret_cast<const int4 *>(my_rows + 4 * k);
+#pragma unroll
+                for (int pl = 0; pl < PLANES; ++pl) {
+                  const int out = PLANES * p.q_rows, add = pl * p.q_rows;
+                  const int y[4] = {v.x < 0 ? out : v.x + add, v.y < 0 ? out : v.y + add,
+                                    v.z < 0 ? out : v.z + add, v.w < 0 ? out : v.w + add};
+                  tma_rows4<CG>(sq + pl * S::kQTile + c * 512, &map_qr, k0, y, full);
+                }
+              }
+            } else if (warp == 1) {
+              for (int pl = 0; pl < PLANES; ++pl)
+                for (int b = 0; b < boxes; ++b)
+                  tma_2d<CG>(sq + pl * S::kQTile + b * (S::kBox * 128), &map_q, k0,
+                             qf + b * S::kBox + pl * p.q_rows, full);
             }
           }
+          __syncwarp();
         }
       }
-    } else if (warp == 1) {
+    } else if (warp == kMmaWarp) {
       // ---- products ----
-      if (lane == 0 && leader) {
+      if (leader) {
         const uint32_t sizes = (uint32_t(tile.bn >> 3) << 17) | (uint32_t(128 * CG >> 4) << 24) |
                                (MODE == kWgrad ? 1u << 16 : 0u);
         const int n = s1 - s0;
         for (int i = 0; i < n && !timed_out; ++i, ++r) {
           const int s = s0 + i;
           const bool first = PLANES == 3 ? i % kChunk == 0 : i == 0;
+          bool ok = true;
           if (first) {
-            if (q >= 2 && !mbar_wait(bar_tempty + 8 * (q & 1), ((q >> 1) - 1) & 1u,
-                                     p.wait_limit_ns)) {
-              timed_out = true;
-              break;
-            }
+            if (q >= 2)
+              ok = mbar_wait(bar_tempty + 8 * (q & 1), ((q >> 1) - 1) & 1u, p.wait_limit_ns);
             ++q;
           }
           const uint32_t buf = (q - 1) & 1;
           const uint32_t st_i = r % S::kStages;
-          if (!mbar_wait(bar_full + 8 * st_i, (r / S::kStages) & 1u, p.wait_limit_ns)) {
+          ok = ok && mbar_wait(bar_full + 8 * st_i, (r / S::kStages) & 1u, p.wait_limit_ns);
+          if (!__all_sync(~0u, ok)) {
             timed_out = true;
             break;
           }
           tc_fence_after();
           const bool ext = MODE == kLora && s >= nbase;
-          const int left = ext ? p.rank - (s - nbase) % per_rank * kBK : tile.klen - s * kBK;
-          const int steps = (min(left, kBK) + 15) / 16;
+          const int left = ext ? min(S::kRankSlice, p.rank - (s - nbase) % per_rank * S::kRankSlice)
+                               : min(kBK, tile.klen - s * kBK);
+          const int steps = (left + 15) / 16;
           const bool pmn = MODE == kWgrad || (ext ? p.e_mn : p.p_mn);
           const uint32_t idesc = p.idesc | sizes | (pmn ? 1u << 15 : 0u);
           const uint32_t st = base + st_i * S::kStage;
@@ -798,28 +879,35 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           const uint64_t dq = tile_desc(st + PLANES * kPTile, MODE == kWgrad);
           const uint32_t pstep = pmn ? 128 : 2, qstep = MODE == kWgrad ? 128 : 2;   // 16 bytes
           const uint32_t d = tmem + buf * S::kBN;
-          for (int k = 0; k < steps; ++k) {
-            const uint64_t a = dp + k * pstep, b = dq + k * qstep;
-            mma<CG>(d, a, b, idesc, !(first && k == 0));
-            if constexpr (PLANES == 3) {
-              constexpr uint64_t pa = kPTile >> 4, qa = S::kQTile >> 4;
-              const uint32_t ds = tmem + (2 + (done & 1)) * S::kBN;
-              mma<CG>(ds, a + 2 * pa, b, idesc, !(i == 0 && k == 0));
-              mma<CG>(ds, a, b + 2 * qa, idesc, true);
-              mma<CG>(ds, a + pa, b + qa, idesc, true);
-              mma<CG>(ds, a + pa, b, idesc, true);
-              mma<CG>(ds, a, b + qa, idesc, true);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k >= steps) break;
+              const uint64_t a = dp + k * pstep, b = dq + k * qstep;
+              mma<CG>(d, a, b, idesc, !(first && k == 0));
+              if constexpr (PLANES == 3) {
+                constexpr uint64_t pa = kPTile >> 4, qa = S::kQTile >> 4;
+                const uint32_t ds = tmem + (2 + (done & 1)) * S::kBN;
+                mma<CG>(ds, a + 2 * pa, b, idesc, !(i == 0 && k == 0));
+                mma<CG>(ds, a, b + 2 * qa, idesc, true);
+                mma<CG>(ds, a + pa, b + qa, idesc, true);
+                mma<CG>(ds, a + pa, b, idesc, true);
+                mma<CG>(ds, a, b + qa, idesc, true);
+              } else if (ext) {
+                mma<CG>(d, a, b + 2 * qstep, idesc, true);      // b[g] times u's lo
+              }
             }
+            mma_commit<CG>(bar_empty + 8 * st_i, true);
+            if (i == n - 1 || (PLANES == 3 && i % kChunk == kChunk - 1))
+              mma_commit<CG>(bar_tfull + 8 * buf, true);
           }
-          mma_commit<CG>(bar_empty + 8 * st_i, true);
-          if (i == n - 1 || (PLANES == 3 && i % kChunk == kChunk - 1))
-            mma_commit<CG>(bar_tfull + 8 * buf, true);
+          __syncwarp();
         }
         if (n > 0) ++done;
       }
     } else {
       // ---- results ----
-      const int quarter = warp & 3, half = (warp - 2) >> 2;
+      const int quarter = warp & 3, half = (warp - kEpi0) >> 2;
       const int n = s1 - s0;
       const uint32_t lanes = tmem + (uint32_t(32 * quarter) << 16);
       const uint32_t tempty = CG == 2 ? map_rank(bar_tempty, 0) : bar_tempty;
@@ -906,16 +994,16 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       // in block order, and stores them.
       __syncwarp();
       cluster_sync();
-      if (warp >= 2) {
+      if (warp >= kEpi0 && warp < kMmaWarp) {
         const int c0 = tile.qn * int(rank) / p.ksplit, c1 = tile.qn * int(rank + 1) / p.ksplit;
         const float scale = MODE == kForward && p.scale ? p.scale[tile.g] : 1.0f;
-        for (int i = int(threadIdx.x) - 64; i < 128 * (c1 - c0); i += 32 * kEpiWarps) {
+        for (int i = int(threadIdx.x) - 32 * kEpi0; i < 128 * (c1 - c0); i += 32 * kEpiWarps) {
           const int l = i & 127, col = c0 + (i >> 7);
           const uint32_t at = red + uint32_t(col * 128 + l) * 4;
           float v = 0.0f;
           for (int b = 0; b < p.ksplit; ++b) v += ld_cluster(map_rank(at, uint32_t(b)));
           const int64_t o = out_row<MODE>(p, tile, col);
-          if (o >= 0 && tile.n0 + l < p.N) store_out<PLANES>(p, o + tile.n0 + l, v * scale);
+          if (o >= 0 && tile.n0 + l < p.n_out) store_out<PLANES>(p, o, tile.n0 + l, v * scale);
         }
       }
       __syncwarp();
@@ -929,17 +1017,18 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     for (uint32_t i = r > S::kStages ? r - S::kStages : 0; i < r; ++i)
       mbar_wait(bar_full + 8 * (i % S::kStages), (i / S::kStages) & 1u, p.wait_limit_ns);
   }
-  if (warp == 1 && lane == 0 && leader) {
-    mma_commit<CG>(bar_drain, false);
+  if (warp == kMmaWarp && leader) {
+    if (elect_one()) mma_commit<CG>(bar_drain, false);
+    __syncwarp();
     if (!mbar_wait(bar_drain, 0u, p.wait_limit_ns)) timed_out = true;
   }
   __syncwarp();
-  if (timed_out) atomicOr(&g_grouped_status, 2u);
+  if (timed_out && lane == 0) atomicOr(&g_grouped_status, 2u);
   tc_fence_before();
   __syncthreads();
   if (CG == 2) cluster_sync();   // remote arrivals have landed; neither block uses tensor memory
   tc_fence_after();
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     if constexpr (CG == 2)
       asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                    "r"(S::kTmemCols)
@@ -1178,6 +1267,7 @@ cudaError_t run_forward(const Planes &x, int64_t x_rows, const Planes &w, bool s
       prm.panels * (std::min<int64_t>(prm.groups, prm.rows) + prm.rows / bn);
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
   prm.ksplit = cg == 2 ? 1 : split_of(tiles, (prm.K + kBK - 1) / kBK, dev);
+  if (prm.n_out == 0) prm.n_out = prm.N;
   prm.q_rows = int(x_rows);
   prm.p_mn = trans_w ? 0 : 1;
   prm.p_shared = shared_w ? 1 : 0;
@@ -1248,6 +1338,7 @@ cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *wor
   prm.ld_out = p.lddw;
   prm.stride_out = p.stride_dw;
   prm.out_type = out_type(p.dtype);
+  prm.n_out = prm.N;
   prm.ksplit = 1;
   const int cg = p.N > 128 ? 2 : 1;
   const int bn = columns_of(cg, planes);
@@ -1263,9 +1354,14 @@ cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *wor
   return launch_any(cg, planes, kWgrad, m, prm, tiles, dev, stream);
 }
 
-// The workspace holds u (a row for every p, in planes) and the planes of the operands.
+// Columns of u: pairs of 16-bit values in blocks of 32 + 32, or one plane's 16-byte rows.
+static int64_t u_columns(const LoraProblem &p) {
+  return p.dtype == TMM_F32 ? round8(p.rank) : (p.rank + 31) / 32 * 64;
+}
+
+// The workspace holds u (a row for every p) and the planes of the operands.
 size_t lora_workspace_bytes(const LoraProblem &p) {
-  const __int128 u = __int128(p.dtype == TMM_F32 ? 6 : 2) * p.rows * round8(p.rank);
+  const __int128 u = __int128(p.dtype == TMM_F32 ? 6 : 2) * p.rows * u_columns(p);
   return add_sizes({u > __int128(INT64_MAX / 4) ? SIZE_MAX : round256(size_t(u)),
                     plane_bytes(p.x, p.dtype), plane_bytes(p.w, p.dtype),
                     plane_bytes(p.a, p.dtype), plane_bytes(p.b, p.dtype)});
@@ -1275,7 +1371,7 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
                         cudaStream_t stream) {
   char *ws = static_cast<char *>(workspace);
   const int planes = p.dtype == TMM_F32 ? 3 : 1;
-  const int64_t ldu = round8(p.rank);
+  const int64_t ldu = u_columns(p);
   uint16_t *u = reinterpret_cast<uint16_t *>(ws);
   ws += round256(size_t(planes) * 2 * p.rows * ldu);
   Planes x, w, a, b;
@@ -1296,7 +1392,8 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   prm.out = u;
   prm.ld_out = ldu;
   prm.stride_out = p.rows * ldu;
-  prm.out_type = p.dtype == TMM_F32 ? kOutPlanes : out_type(p.dtype);
+  prm.out_type = kOutU;
+  prm.n_out = p.dtype == TMM_F32 ? int(p.rank) : int(ldu / 2);
   prm.scale = p.scale;
   if ((e = run_forward(x, p.x.rows, a, p.groups > 1 && p.a.count == 1, p.trans_a != 0, planes, prm,
                        dev, stream)) !=
@@ -1305,7 +1402,7 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
 
   const int cg = p.rows > 64 ? 2 : 1;
   const int bn = columns_of(cg, planes);
-  prm.N = int(p.N);
+  prm.N = prm.n_out = int(p.N);
   prm.q_rows = int(p.x.rows);
   prm.rank = int(p.rank);
   prm.panels = int((p.N + 128 * cg - 1) / (128 * cg));
@@ -1321,12 +1418,12 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   prm.ld_out = p.ldy;
   prm.stride_out = 0;
   prm.out_type = out_type(p.dtype);
-  const Planes up = {u, planes, p.rows, p.rank, ldu, p.rows * ldu};
+  const Planes up = {u, planes, p.rows, planes == 3 ? p.rank : ldu, ldu, p.rows * ldu};
   Maps m;
   if ((e = tile_map(&m.p, w, p.trans_w ? 128 : 64)) != cudaSuccess ||
       (e = row_map(&m.q, x, uint32_t(box_of(cg)))) != cudaSuccess ||
       (e = row_map(&m.qr, x, 1)) != cudaSuccess ||
-      (e = tile_map(&m.e, b, p.trans_b ? 128 : 64)) != cudaSuccess ||
+      (e = tile_map(&m.e, b, p.trans_b ? 128 : planes == 3 ? 64 : 32)) != cudaSuccess ||
       (e = row_map(&m.u, up, 1)) != cudaSuccess)
     return e;
   return launch_any(cg, planes, kLora, m, prm, tiles, dev, stream);

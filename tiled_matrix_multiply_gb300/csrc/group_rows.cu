@@ -11,6 +11,7 @@
 // real batch: launches and dependent loads are the cost.  Up to kOneBlock slots one block does
 // everything in one launch; more take two (counts per block, then places), each block adding up
 // the counts of all blocks for itself.
+#include <atomic>
 #include <cstdint>
 
 #include "grouped.h"
@@ -150,10 +151,15 @@ cudaError_t launch(int64_t slots, int fan, int groups, const void *index, int32_
   const int warps = int(want < 1 ? 1 : want > kMaxWarps ? kMaxWarps : want);
   const size_t smem = size_t(groups + 1) * (warps + 2) * sizeof(int);
   // Up to 513 x 34 counts (70 KB): above the default limit, so the kernel is opted in.
-  cudaError_t e = cudaFuncSetAttribute(place_kernel<T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       int((kMaxGroups + 1) * (kMaxWarps + 2) * sizeof(int)));
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> configured{0};
+  const uint64_t bit = uint64_t(1) << (dev.id & 63);
+  if (!(configured.load(std::memory_order_acquire) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        place_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        int((kMaxGroups + 1) * (kMaxWarps + 2) * sizeof(int)));
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_release);
+  }
   place_kernel<T><<<unsigned(blocks), unsigned(32 * warps), smem, stream>>>(
       index, slots, chunk, fan, groups, counts, offsets, order, rows, position);
   return cudaGetLastError();

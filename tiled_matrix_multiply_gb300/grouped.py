@@ -20,6 +20,13 @@ from __future__ import annotations
 
 from typing import NamedTuple
 
+import torch
+
+from . import _abi
+
+_CODES = {torch.float32: _abi.TMM_F32, torch.bfloat16: _abi.TMM_BF16,
+          torch.float16: _abi.TMM_F16}
+
 
 class RowGroups(NamedTuple):
     """Slots sorted by group (see ``group_rows``), int32 CUDA tensors."""
@@ -30,15 +37,12 @@ class RowGroups(NamedTuple):
 
 
 def _dtype_code(x, name):
-    import torch
-    from . import _abi
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    codes = {torch.float32: _abi.TMM_F32, torch.bfloat16: _abi.TMM_BF16,
-             torch.float16: _abi.TMM_F16}
-    if x.dtype not in codes:
+    code = _CODES.get(x.dtype)
+    if code is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {x.dtype}")
-    return codes[x.dtype]
+    return code
 
 
 def _operand(x, name, like, dims, transposable=False):
@@ -47,64 +51,77 @@ def _operand(x, name, like, dims, transposable=False):
     stride: elements between matrices (0: one matrix, or an expanded one); trans = 1: every
     matrix is the transposed view of a row-major one, whose ld this is.
     """
-    import torch
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if x.dim() != dims:
-        raise ValueError(f"{name} must be {dims}-D, got shape {tuple(x.shape)}")
+    shape = x.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name} must be {dims}-D, got shape {tuple(shape)}")
     if x.dtype != like.dtype:
         raise TypeError(f"{name} must be {like.dtype} like the first operand, got {x.dtype}")
-    if x.device != like.device:
-        raise ValueError(f"{name} is on {x.device}, the first operand on {like.device}")
     if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    rows, cols = x.shape[-2:]
-    s0, s1 = x.stride(-2), x.stride(-1)
-    stride = x.stride(0) if dims == 3 and x.shape[0] > 1 else 0
-    if x.numel() == 0:
-        return rows, cols, max(cols, 1), max(stride, 0), 0
-    if (cols <= 1 or s1 == 1) and (rows <= 1 or s0 >= cols):
-        return rows, cols, max(s0 if rows > 1 else cols, cols, 1), stride, 0
-    if transposable and (rows <= 1 or s0 == 1) and (cols <= 1 or s1 >= rows):
-        return rows, cols, max(s1 if cols > 1 else rows, rows, 1), stride, 1
+    if x.get_device() != like.get_device():
+        raise ValueError(f"{name} is on {x.device}, the first operand on {like.device}")
+    strides = x.stride()
+    rows, cols = shape[-2], shape[-1]
+    s0, s1 = strides[-2], strides[-1]
+    stride = strides[0] if dims == 3 and shape[0] > 1 else 0
+    if rows == 0 or cols == 0 or (dims == 3 and shape[0] == 0):
+        return rows, cols, max(cols, 1), stride, 0
+    if (s1 == 1 or cols == 1) and (s0 >= cols or rows == 1):
+        return rows, cols, max(s0 if rows > 1 else cols, cols), stride, 0
+    if transposable and (s0 == 1 or rows == 1) and (s1 >= rows or cols == 1):
+        return rows, cols, max(s1 if cols > 1 else rows, rows), stride, 1
     raise ValueError(f"{name} must be row-major (unit column stride)"
                      + (" or a transposed row-major view" if transposable else ""))
 
 
 def _index_tensor(t, name, like, length):
-    import torch
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
         raise TypeError(f"{name} must be an int32 tensor")
-    if t.device != like.device:
+    if not t.is_cuda or t.get_device() != like.get_device():
         raise ValueError(f"{name} is on {t.device}, the operands on {like.device}")
-    if t.dim() != 1 or (length is not None and t.numel() != length) or not t.is_contiguous():
+    if t.dim() != 1 or (length is not None and t.shape[0] != length) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 1-D tensor"
                          + (f" of {length} values" if length is not None else ""))
-    return t
+
+
+def _result(given, name, shape, like):
+    if given is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    if tuple(given.shape) != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(given.shape)}")
+    return given
 
 
 def _workspace(given, need, like):
-    """A workspace of `need` bytes: the given tensor, or a new one (torch's start 256-byte
-    aligned at least)."""
-    import torch
+    """A workspace of `need` bytes (None: none needed): the given tensor, or a new one (torch's
+    start on 256-byte boundaries at least)."""
     if given is None:
-        if need == 0:
-            return 0, 0, None
-        given = torch.empty(need, dtype=torch.uint8, device=like.device)
-    elif given.device != like.device or not given.is_contiguous():
+        return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
+    if not given.is_cuda or given.get_device() != like.get_device() or not given.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the operands' device")
-    return given.data_ptr(), given.numel() * given.element_size(), given
+    return given
 
 
-def _run(name, rc):
-    from . import _abi
+# The handle of the current stream of a device, without making a Stream object for it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _call(name, like, stream, ws, *args):
+    """Call the entry point on the operands' device and stream; raise its error."""
+    device = like.get_device()
+    s = stream.cuda_stream if stream is not None else _raw_stream(device)
+    tail = (ws.data_ptr(), ws.numel() * ws.element_size(), s) if ws is not None else (0, 0, s)
+    fn = getattr(_abi.load(), name)
+    if torch.cuda.current_device() == device:
+        rc = fn(*args, *tail)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, *tail)
     if rc != _abi.TMM_OK:
         raise _abi.TmmError(name, rc, _abi.last_error())
-
-
-def _on(like, stream):
-    import torch
-    return stream if stream is not None else torch.cuda.current_stream(like.device)
 
 
 def group_rows(index, groups, stream=None):
@@ -113,42 +130,31 @@ def group_rows(index, groups, stream=None):
     A slot's group is its number where that is in [0, groups); the other slots belong to no
     group and come last.  Returns ``RowGroups``.
     """
-    import torch
-    from . import _abi
     if not isinstance(index, torch.Tensor) or index.dtype not in (torch.int32, torch.int64):
         raise TypeError("index must be an int32 or int64 tensor")
     if not index.is_cuda:
         raise ValueError("index must be a CUDA tensor")
-    if index.dim() not in (1, 2) or not index.is_contiguous():
+    shape = index.shape
+    if len(shape) not in (1, 2) or not index.is_contiguous():
         raise ValueError("index must be a contiguous tensor (tokens,) or (tokens, k)")
-    tokens = index.shape[0]
-    fan = index.shape[1] if index.dim() == 2 else 1
+    tokens, fan = shape[0], shape[1] if len(shape) == 2 else 1
     if fan < 1:
         raise ValueError("index must have at least one column")
+    if not 1 <= groups <= _abi.TMM_MAX_GROUPS:
+        raise ValueError(f"groups must be between 1 and {_abi.TMM_MAX_GROUPS}, got {groups}")
     slots = tokens * fan
     # One allocation; every array starts on a 16-byte boundary.
     at = (slots + 3) // 4 * 4
     buf = torch.empty(3 * at + groups + 1, dtype=torch.int32, device=index.device)
-    order, rows, position = (buf[i * at:i * at + slots] for i in range(3))
-    offsets = buf[3 * at:]
-    lib = _abi.load()
-    need = int(lib.group_rows_workspace_size(tokens, fan, groups))
-    ws, ws_bytes, keep = _workspace(None, need, index)
-    with torch.cuda.device(index.device):
-        _run("group_rows", lib.group_rows(
-            tokens, fan, groups, index.data_ptr(), 64 if index.dtype == torch.int64 else 32,
-            offsets.data_ptr(), order.data_ptr(), rows.data_ptr(), position.data_ptr(), ws,
-            ws_bytes, _on(index, stream).cuda_stream))
+    order, rows, position, offsets = buf.split_with_sizes([at, at, at, groups + 1])
+    if at != slots:
+        order, rows, position = order[:slots], rows[:slots], position[:slots]
+    need = _abi.load().group_rows_workspace_size(tokens, fan, groups)
+    base = buf.data_ptr()
+    _call("group_rows", index, stream, _workspace(None, need, index), tokens, fan, groups,
+          index.data_ptr(), 64 if index.dtype == torch.int64 else 32, base + 12 * at, base,
+          base + 4 * at, base + 8 * at)
     return RowGroups(offsets, order, rows, position)
-
-
-def _result(given, name, shape, like):
-    import torch
-    if given is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
-    if tuple(given.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(given.shape)}")
-    return given
 
 
 def gemm_grouped(x, w, offsets, rows=None, y=None, workspace=None, stream=None):
@@ -158,8 +164,6 @@ def gemm_grouped(x, w, offsets, rows=None, y=None, workspace=None, stream=None):
     (groups + 1); rows: int32, the row of x that each p reads (a number outside x reads zeros),
     or None for p itself.  y: (len(rows) or x_rows, N); its rows of no group are zero.
     """
-    import torch
-    from . import _abi
     code = _dtype_code(x, "x")
     x_rows, K, ldx, _, _ = _operand(x, "x", x, 2)
     K2, N, ldw, stride_w, trans = _operand(w, "w", x, 3, True)
@@ -167,19 +171,20 @@ def gemm_grouped(x, w, offsets, rows=None, y=None, workspace=None, stream=None):
     if K != K2:
         raise ValueError(f"inner dimensions differ: x is {tuple(x.shape)}, w is {tuple(w.shape)}")
     _index_tensor(offsets, "offsets", x, groups + 1)
+    R, rows_ptr = x_rows, 0
     if rows is not None:
         _index_tensor(rows, "rows", x, None)
-    R = rows.numel() if rows is not None else x_rows
+        R, rows_ptr = rows.shape[0], rows.data_ptr()
     y = _result(y, "y", (R, N), x)
-    _, _, ldy, _, _ = _operand(y, "y", x, 2)
-    lib = _abi.load()
-    head = (code, trans, groups, R, N, K, x.data_ptr(), x_rows, ldx)
-    need = int(lib.gemm_grouped_workspace_size(*head, w.data_ptr(), ldw, stride_w))
-    ws, ws_bytes, keep = _workspace(workspace, need, x)
-    with torch.cuda.device(x.device):
-        _run("gemm_grouped", lib.gemm_grouped(
-            *head, offsets.data_ptr(), rows.data_ptr() if rows is not None else 0, w.data_ptr(),
-            ldw, stride_w, y.data_ptr(), ldy, ws, ws_bytes, _on(x, stream).cuda_stream))
+    ldy = _operand(y, "y", x, 2)[2]
+    x_ptr, w_ptr = x.data_ptr(), w.data_ptr()
+    head = (code, trans, groups, R, N, K, x_ptr, x_rows, ldx)
+    # 16-bit operands on 16-byte boundaries are read in place and need no workspace.
+    if code == _abi.TMM_F32 or (x_ptr | w_ptr) & 15 or (ldx | ldw | stride_w) & 7:
+        need = _abi.load().gemm_grouped_workspace_size(*head, w_ptr, ldw, stride_w)
+        workspace = _workspace(workspace, need, x)
+    _call("gemm_grouped", x, stream, workspace, *head, offsets.data_ptr(), rows_ptr, w_ptr, ldw,
+          stride_w, y.data_ptr(), ldy)
     return y
 
 
@@ -188,29 +193,28 @@ def gemm_grouped_wgrad(x, dy, offsets, rows=None, dw=None, workspace=None, strea
 
     The gradient of ``gemm_grouped`` with respect to w; x, offsets and rows as there, dy (R, N).
     """
-    import torch
-    from . import _abi
     code = _dtype_code(x, "x")
     x_rows, K, ldx, _, _ = _operand(x, "x", x, 2)
     R, N, lddy, _, _ = _operand(dy, "dy", x, 2)
-    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
-        raise ValueError("offsets must be a 1-D tensor of groups + 1 values")
     _index_tensor(offsets, "offsets", x, None)
-    groups = offsets.numel() - 1
+    groups = offsets.shape[0] - 1
+    if groups < 1:
+        raise ValueError("offsets must have groups + 1 values")
+    rows_ptr = 0
     if rows is not None:
         _index_tensor(rows, "rows", x, R)
+        rows_ptr = rows.data_ptr()
     elif x_rows != R:
         raise ValueError(f"x has {x_rows} rows, dy {R}")
     dw = _result(dw, "dw", (groups, K, N), x)
     _, _, lddw, stride, _ = _operand(dw, "dw", x, 3)
-    lib = _abi.load()
-    head = (code, groups, R, N, K, x.data_ptr(), x_rows, ldx)
-    need = int(lib.gemm_grouped_wgrad_workspace_size(*head, dy.data_ptr(), lddy))
-    ws, ws_bytes, keep = _workspace(workspace, need, x)
-    with torch.cuda.device(x.device):
-        _run("gemm_grouped_wgrad", lib.gemm_grouped_wgrad(
-            *head, offsets.data_ptr(), rows.data_ptr() if rows is not None else 0, dy.data_ptr(),
-            lddy, dw.data_ptr(), lddw, stride, ws, ws_bytes, _on(x, stream).cuda_stream))
+    x_ptr, dy_ptr = x.data_ptr(), dy.data_ptr()
+    head = (code, groups, R, N, K, x_ptr, x_rows, ldx)
+    if code == _abi.TMM_F32 or (x_ptr | dy_ptr) & 15 or (ldx | lddy) & 7:
+        need = _abi.load().gemm_grouped_wgrad_workspace_size(*head, dy_ptr, lddy)
+        workspace = _workspace(workspace, need, x)
+    _call("gemm_grouped_wgrad", x, stream, workspace, *head, offsets.data_ptr(), rows_ptr, dy_ptr,
+          lddy, dw.data_ptr(), lddw, stride)
     return dw
 
 
@@ -222,8 +226,6 @@ def gemm_lora(x, w, a, b, scale, offsets, rows=None, y=None, workspace=None, str
     ``offsets`` and ``order`` of ``group_rows(index, adapters)``; rows past offsets[-1] have no
     adapter.  rows=None: x is in group order already.
     """
-    import torch
-    from . import _abi
     code = _dtype_code(x, "x")
     T, K, ldx, _, _ = _operand(x, "x", x, 2)
     K2, N, ldw, _, tw = _operand(w, "w", x, 2, True)
@@ -235,20 +237,19 @@ def gemm_lora(x, w, a, b, scale, offsets, rows=None, y=None, workspace=None, str
                          f"a {tuple(a.shape)}, b {tuple(b.shape)}")
     if not isinstance(scale, torch.Tensor) or scale.dtype != torch.float32:
         raise TypeError("scale must be a float32 tensor")
-    if scale.shape != (groups,) or scale.device != x.device or not scale.is_contiguous():
+    if scale.shape != (groups,) or not scale.is_cuda or scale.get_device() != x.get_device() \
+            or not scale.is_contiguous():
         raise ValueError(f"scale must be a contiguous tensor of {groups} values on {x.device}")
     _index_tensor(offsets, "offsets", x, groups + 1)
+    rows_ptr = 0
     if rows is not None:
         _index_tensor(rows, "rows", x, T)
+        rows_ptr = rows.data_ptr()
     y = _result(y, "y", (T, N), x)
-    _, _, ldy, _, _ = _operand(y, "y", x, 2)
-    lib = _abi.load()
+    ldy = _operand(y, "y", x, 2)[2]
     head = (code, tw, ta, tb, groups, T, N, K, r, x.data_ptr(), ldx)
     mats = (w.data_ptr(), ldw, a.data_ptr(), lda, stride_a, b.data_ptr(), ldb, stride_b)
-    need = int(lib.gemm_lora_workspace_size(*head, *mats))
-    ws, ws_bytes, keep = _workspace(workspace, need, x)
-    with torch.cuda.device(x.device):
-        _run("gemm_lora", lib.gemm_lora(
-            *head, offsets.data_ptr(), rows.data_ptr() if rows is not None else 0, *mats,
-            scale.data_ptr(), y.data_ptr(), ldy, ws, ws_bytes, _on(x, stream).cuda_stream))
+    need = _abi.load().gemm_lora_workspace_size(*head, *mats)
+    _call("gemm_lora", x, stream, _workspace(workspace, need, x), *head, offsets.data_ptr(),
+          rows_ptr, *mats, scale.data_ptr(), y.data_ptr(), ldy)
     return y
