@@ -416,7 +416,8 @@ int softmax_rows_f32(int64_t rows, int64_t cols, const float *x, int64_t ldx, fl
  *
  * Alignment: operands whose rows (and matrices) start on 16-byte boundaries
  * are read in place in the 16-bit types; others, and every FP32 operand, are
- * first restaged into the workspace (FP32: 6 bytes a value).
+ * first restaged into the workspace (FP32: 6 bytes a value), and so are, in
+ * larger products, the rows that row_index names.
  *
  * workspace: DEVICE memory, 256-byte aligned, of at least the bytes that the
  * matching *_workspace_size call gives for the same arguments (0: none needed,
@@ -468,7 +469,8 @@ int gemm_grouped(int dtype, int transw, int64_t groups, int64_t rows, int64_t N,
                  void *workspace, size_t workspace_bytes, tmm_stream_t stream);
 size_t gemm_grouped_workspace_size(int dtype, int transw, int64_t groups, int64_t rows, int64_t N,
                                    int64_t K, const void *x, int64_t x_rows, int64_t ldx,
-                                   const void *w, int64_t ldw, int64_t stride_w);
+                                   const int32_t *row_index, const void *w, int64_t ldw,
+                                   int64_t stride_w);
 
 /*
  * gemm_grouped_wgrad -- the gradient of gemm_grouped with respect to w:
@@ -485,7 +487,7 @@ int gemm_grouped_wgrad(int dtype, int64_t groups, int64_t rows, int64_t N, int64
                        void *workspace, size_t workspace_bytes, tmm_stream_t stream);
 size_t gemm_grouped_wgrad_workspace_size(int dtype, int64_t groups, int64_t rows, int64_t N,
                                          int64_t K, const void *x, int64_t x_rows, int64_t ldx,
-                                         const void *dy, int64_t lddy);
+                                         const int32_t *row_index, const void *dy, int64_t lddy);
 
 /*
  * gemm_lora -- a shared projection with a low-rank adapter per row:
@@ -512,9 +514,9 @@ int gemm_lora(int dtype, int transw, int transa, int transb, int64_t groups, int
               void *workspace, size_t workspace_bytes, tmm_stream_t stream);
 size_t gemm_lora_workspace_size(int dtype, int transw, int transa, int transb, int64_t groups,
                                 int64_t rows, int64_t N, int64_t K, int64_t rank,
-                                const void *x, int64_t ldx, const void *w, int64_t ldw,
-                                const void *a, int64_t lda, int64_t stride_a,
-                                const void *b, int64_t ldb, int64_t stride_b);
+                                const void *x, int64_t ldx, const int32_t *row_index,
+                                const void *w, int64_t ldw, const void *a, int64_t lda,
+                                int64_t stride_a, const void *b, int64_t ldb, int64_t stride_b);
 
 /* One-line description of the calling thread's last failed call ("" if none).
  * The string is owned by the library and valid until the thread's next call. */

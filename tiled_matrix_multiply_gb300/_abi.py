@@ -125,19 +125,19 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                      i64, ptr, i64, ptr, size, ptr]
         lib.gemm_grouped.restype = ci
         lib.gemm_grouped_workspace_size.argtypes = [ci, ci, i64, i64, i64, i64, ptr, i64, i64, ptr,
-                                                    i64, i64]
+                                                    ptr, i64, i64]
         lib.gemm_grouped_workspace_size.restype = size
         lib.gemm_grouped_wgrad.argtypes = [ci, i64, i64, i64, i64, ptr, i64, i64, ptr, ptr, ptr,
                                            i64, ptr, i64, i64, ptr, size, ptr]
         lib.gemm_grouped_wgrad.restype = ci
         lib.gemm_grouped_wgrad_workspace_size.argtypes = [ci, i64, i64, i64, i64, ptr, i64, i64,
-                                                          ptr, i64]
+                                                          ptr, ptr, i64]
         lib.gemm_grouped_wgrad_workspace_size.restype = size
         lib.gemm_lora.argtypes = [ci, ci, ci, ci, i64, i64, i64, i64, i64, ptr, i64, ptr, ptr, ptr,
                                   i64, ptr, i64, i64, ptr, i64, i64, ptr, ptr, i64, ptr, size, ptr]
         lib.gemm_lora.restype = ci
         lib.gemm_lora_workspace_size.argtypes = [ci, ci, ci, ci, i64, i64, i64, i64, i64, ptr, i64,
-                                                 ptr, i64, ptr, i64, i64, ptr, i64, i64]
+                                                 ptr, ptr, i64, ptr, i64, i64, ptr, i64, i64]
         lib.gemm_lora_workspace_size.restype = size
         lib.tmm_check_device.argtypes = [ptr]
         lib.tmm_check_device.restype = ctypes.c_int

@@ -634,10 +634,13 @@ int group_rows(int64_t tokens, int64_t fan, int64_t groups, const void *index, i
 
 size_t gemm_grouped_workspace_size(int dtype, int transw, int64_t groups, int64_t rows, int64_t N,
                                    int64_t K, const void *x, int64_t x_rows, int64_t ldx,
-                                   const void *w, int64_t ldw, int64_t stride_w) {
+                                   const int32_t *row_index, const void *w, int64_t ldw,
+                                   int64_t stride_w) {
   if (!sizes_ok(dtype, groups, rows, N, K) || !extent_ok(x_rows)) return 0;
-  return tmm::grouped_workspace_bytes(
-      grouped_problem(dtype, transw, groups, rows, N, K, x, x_rows, ldx, w, ldw, stride_w));
+  tmm::GroupedProblem p =
+      grouped_problem(dtype, transw, groups, rows, N, K, x, x_rows, ldx, w, ldw, stride_w);
+  p.row_index = row_index;
+  return tmm::grouped_workspace_bytes(p);
 }
 
 int gemm_grouped(int dtype, int transw, int64_t groups, int64_t rows, int64_t N, int64_t K,
@@ -652,6 +655,8 @@ int gemm_grouped(int dtype, int transw, int64_t groups, int64_t rows, int64_t N,
   if ((rc = check_x_rows(who, rows, x_rows, row_index)) != TMM_OK) return rc;
   tmm::GroupedProblem p =
       grouped_problem(dtype, transw, groups, rows, N, K, x, x_rows, ldx, w, ldw, stride_w);
+  p.offsets = offsets;
+  p.row_index = row_index;
   const int size = element_size(dtype);
   const tmm::Stack y_s = stack_of(y, 1, rows, N, ldy, 0);
   if ((rc = check_stack(who, "x", p.x, size)) != TMM_OK ||
@@ -674,8 +679,6 @@ int gemm_grouped(int dtype, int transw, int64_t groups, int64_t rows, int64_t N,
   if ((rc = current_device(&dev)) != TMM_OK) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (K == 0) return zero_output(who, y, 1, rows, N, ldy, 0, size, s);
-  p.offsets = offsets;
-  p.row_index = row_index;
   p.y = y;
   p.ldy = ldy;
   if (x_rows == 0) return zero_output(who, y, 1, rows, N, ldy, 0, size, s);   // all zero rows
@@ -686,10 +689,14 @@ int gemm_grouped(int dtype, int transw, int64_t groups, int64_t rows, int64_t N,
 
 size_t gemm_grouped_wgrad_workspace_size(int dtype, int64_t groups, int64_t rows, int64_t N,
                                          int64_t K, const void *x, int64_t x_rows, int64_t ldx,
-                                         const void *dy, int64_t lddy) {
+                                         const int32_t *row_index, const void *dy,
+                                         int64_t lddy) {
   if (!sizes_ok(dtype, groups, rows, N, K) || !extent_ok(x_rows)) return 0;
   tmm::WgradProblem p = {};
   p.dtype = dtype;
+  p.rows = rows;
+  p.N = N;
+  p.row_index = row_index;
   p.x = stack_of(x, 1, x_rows, K, ldx, 0);
   p.dy = stack_of(dy, 1, rows, N, lddy, 0);
   return tmm::wgrad_workspace_bytes(p);
@@ -711,6 +718,8 @@ int gemm_grouped_wgrad(int dtype, int64_t groups, int64_t rows, int64_t N, int64
   p.rows = rows;
   p.K = K;
   p.N = N;
+  p.offsets = offsets;
+  p.row_index = row_index;
   p.x = stack_of(x, 1, x_rows, K, ldx, 0);
   p.dy = stack_of(dy, 1, rows, N, lddy, 0);
   tmm::Stack dw_s = {dw, groups, K, N, lddw, stride_dw};
@@ -738,8 +747,6 @@ int gemm_grouped_wgrad(int dtype, int64_t groups, int64_t rows, int64_t N, int64
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (rows == 0 || x_rows == 0)
     return zero_output(who, dw, groups, K, N, lddw, stride_dw, size, s);
-  p.offsets = offsets;
-  p.row_index = row_index;
   p.dw = dw;
   p.lddw = lddw;
   p.stride_dw = stride_dw;
@@ -750,13 +757,14 @@ int gemm_grouped_wgrad(int dtype, int64_t groups, int64_t rows, int64_t N, int64
 
 size_t gemm_lora_workspace_size(int dtype, int transw, int transa, int transb, int64_t groups,
                                 int64_t rows, int64_t N, int64_t K, int64_t rank, const void *x,
-                                int64_t ldx, const void *w, int64_t ldw, const void *a,
-                                int64_t lda, int64_t stride_a, const void *b, int64_t ldb,
-                                int64_t stride_b) {
+                                int64_t ldx, const int32_t *row_index, const void *w, int64_t ldw,
+                                const void *a, int64_t lda, int64_t stride_a, const void *b,
+                                int64_t ldb, int64_t stride_b) {
   if (!sizes_ok(dtype, groups, rows, N, K) || rank < 1 || rank > tmm::kMaxAdapterRank) return 0;
-  return tmm::lora_workspace_bytes(lora_problem(dtype, transw, transa, transb, groups, rows, N, K,
-                                                rank, x, ldx, w, ldw, a, lda, stride_a, b, ldb,
-                                                stride_b));
+  tmm::LoraProblem p = lora_problem(dtype, transw, transa, transb, groups, rows, N, K, rank, x,
+                                    ldx, w, ldw, a, lda, stride_a, b, ldb, stride_b);
+  p.row_index = row_index;
+  return tmm::lora_workspace_bytes(p);
 }
 
 int gemm_lora(int dtype, int transw, int transa, int transb, int64_t groups, int64_t rows,
@@ -775,6 +783,8 @@ int gemm_lora(int dtype, int transw, int transa, int transb, int64_t groups, int
                 tmm::kMaxAdapterRank, (long long)rank);
   tmm::LoraProblem p = lora_problem(dtype, transw, transa, transb, groups, rows, N, K, rank, x,
                                     ldx, w, ldw, a, lda, stride_a, b, ldb, stride_b);
+  p.offsets = offsets;
+  p.row_index = row_index;
   const int size = element_size(dtype);
   const tmm::Stack y_s = stack_of(y, 1, rows, N, ldy, 0);
   if ((rc = check_stack(who, "x", p.x, size)) != TMM_OK ||
@@ -804,8 +814,6 @@ int gemm_lora(int dtype, int transw, int transa, int transb, int64_t groups, int
   if ((rc = current_device(&dev)) != TMM_OK) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (K == 0) return zero_output(who, y, 1, rows, N, ldy, 0, size, s);
-  p.offsets = offsets;
-  p.row_index = row_index;
   p.scale = scale;
   p.y = y;
   p.ldy = ldy;

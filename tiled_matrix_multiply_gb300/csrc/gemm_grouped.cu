@@ -90,7 +90,7 @@ struct Shape {
   // Values of `rank` per slice of the adapters' part: 16-bit u is a pair of values (hi and lo).
   static constexpr int kRankSlice = PLANES == 3 ? 64 : 32;
   static constexpr uint32_t kTable = (kMaxGroups + 1) * 4 * 3 + kCopyWarps * 128 + 116;
-  static constexpr uint32_t kBars = 8 * (2 * kStages + 5) + 32;
+  static constexpr uint32_t kBars = 8 * (3 * kStages + 5) + 32;
   static constexpr uint32_t kSmem = 1024 + kStages * kStage + kRed + kTable + kBars;
   static_assert(kSmem <= kMaxSmem, "one block's shared memory");
   static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory columns");
@@ -100,8 +100,10 @@ struct Params {
   int rows;              // p runs over [0, rows)
   int groups;
   const int *offsets;    // groups + 1
-  const int *row_index;  // r(p), or NULL
-  int q_rows;            // rows of x
+  const int *row_index;  // r(p) of the rows read (single blocks; pairs read gathered rows), or NULL
+  const int *out_index;  // r(p) of the rows written (adapters), or NULL
+  int q_rows;            // rows of the x that is read
+  int out_rows;          // rows of y, by out_index
   int K;                 // forward, adapters: length of the sum
   int N;                 // extent of the lanes' dimension
   int q_cols;            // gradient: columns of x
@@ -137,8 +139,18 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
+// Bytes to come in the barrier's present phase, without an arrival.
+__device__ __forceinline__ void mbar_expect_only(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+// The same where no access of this thread has to be ordered before it.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
@@ -219,24 +231,22 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-// Four rows y[0..3] of 64 values from column x.
-template <int CG>
+// Four rows y[0..3] of 64 values from column x (single blocks only).
 __device__ __forceinline__ void tma_rows4(uint32_t dst, const CUtensorMap *map, int x,
                                           const int (&y)[4], uint32_t bar) {
-  if constexpr (CG == 2)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        ".cta_group::2 [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
-        "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
-        "r"(bar)
-        : "memory");
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
+      "r"(bar)
+      : "memory");
+}
+// Orders ordinary accesses to shared memory before the copy engine's and the tensor core's.
+__device__ __forceinline__ void proxy_fence() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void zero16(uint32_t addr) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
 }
 
 __device__ __forceinline__ void tc_fence_before() {
@@ -471,9 +481,9 @@ template <int MODE>
 __device__ __forceinline__ int64_t out_row(const Params &p, const Tile &t, int col) {
   if (MODE == kWgrad) return int64_t(t.g) * p.stride_out + int64_t(t.q0 + col) * p.ld_out;
   int r = t.q0 + col;
-  if (MODE == kLora && p.row_index) {
-    r = p.row_index[r];
-    if (r < 0 || r >= p.q_rows) return -1;
+  if (MODE == kLora && p.out_index) {
+    r = p.out_index[r];
+    if (r < 0 || r >= p.out_rows) return -1;
   }
   return int64_t(r) * p.ld_out;
 }
@@ -485,11 +495,11 @@ __device__ __forceinline__ void store_columns(const Params &p, const Tile &t, in
                                               const float (&v)[16], float scale) {
   const int count = min(16, t.qn - c0);
   int row = 0;      // adapters: the row of column c0 + lane % 16
-  const bool by_row = MODE == kLora && p.row_index;
+  const bool by_row = MODE == kLora && p.out_index;
   if (by_row) {
     const int lane = threadIdx.x & 15;
-    row = lane < count ? p.row_index[t.q0 + c0 + lane] : -1;
-    if (row >= p.q_rows) row = -1;
+    row = lane < count ? p.out_index[t.q0 + c0 + lane] : -1;
+    if (row >= p.out_rows) row = -1;
   }
   const bool in = n < p.n_out;
   int64_t o = out_row<kForward>(p, t, c0);
@@ -512,9 +522,9 @@ template <int CG, int MODE, int PLANES>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                const __grid_constant__ CUtensorMap map_q,    // Q tiles
-               const __grid_constant__ CUtensorMap map_qr,   // rows of x
-               const __grid_constant__ CUtensorMap map_e,    // b tiles; gradient: rows of dy
-               const __grid_constant__ CUtensorMap map_u,    // rows of u
+               const __grid_constant__ CUtensorMap map_qr,   // single rows of x
+               const __grid_constant__ CUtensorMap map_e,    // b tiles
+               const __grid_constant__ CUtensorMap map_u,    // u tiles
                const Params p) {
   using S = Shape<CG, PLANES>;
   extern __shared__ uint8_t smem_raw[];
@@ -525,7 +535,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   const uint32_t table = red + S::kRed;
   const uint32_t bar_full = (table + S::kTable + 7u) & ~7u;
   const uint32_t bar_empty = bar_full + 8 * S::kStages;
-  const uint32_t bar_tfull = bar_empty + 8 * S::kStages;
+  const uint32_t bar_patch = bar_empty + 8 * S::kStages;   // slices that need rows of zeros
+  const uint32_t bar_tfull = bar_patch + 8 * S::kStages;
   const uint32_t bar_tempty = bar_tfull + 16;      // pairs: used in the leader
   const uint32_t bar_drain = bar_tempty + 16;
   const uint32_t slot = bar_drain + 8;             // tensor memory address; then the counts
@@ -553,7 +564,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     offs[g] = max(0, min(p.offsets[g], p.rows));
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_full + 8 * s, MODE == kForward ? 1 : CG);
+      mbar_init(bar_patch + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -626,8 +638,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       slot_ptr[2] = uint32_t(tiles);
       slot_ptr[4] = uint32_t(carry);                    // end of the last group
     }
-    // The ring is written by the copy engine from here on.
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    proxy_fence();      // the ring is written by the copy engine from here on
   }
   tc_fence_before();
   __syncthreads();
@@ -640,6 +651,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   uint32_t r = 0;      // ring position: slices so far
   uint32_t q = 0;      // tensor-memory sums so far
   uint32_t done = 0;   // tiles with a sum so far
+  uint32_t patched = 0;   // a bit per stage: parity of its patched slices
 
   // Forward: rows of the result that belong to no group are zero.
   if (MODE == kForward && warp >= kEpi0 && warp < kMmaWarp) {
@@ -664,22 +676,21 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       const int n0 = tile.n0 + half_rank * 128;
       const int pg = (p.p_shared ? 0 : tile.g);
       const int pcount = p.p_shared ? 1 : p.groups;
-      // Columns of this block that hold rows (the others' sums are not stored, so whatever
-      // their part of the ring holds will do), in groups of four; of the other block of a pair.
-      const auto held = [&](int half) {
-        return max(0, min(tile.qn - half * hr, hr));
-      };
-      const bool by_row = p.row_index != nullptr;
-      const int quads = (held(half_rank) + 3) / 4;
-      const int boxes = (held(half_rank) + S::kBox - 1) / S::kBox;
-      // Copies by row are dealt out to the copy warps: warp w issues groups w, w + 4, ... (a copy
-      // of four rows takes a warp about 80 cycles to issue, whatever its size; from one warp 32
-      // of them took 2.7 times as long as the slice's products).  Lane l looks up row l % 4 of
-      // the warp's group l / 4; -1 is a row of zeros.
+      // Columns of a block that hold rows: the others' sums are not stored, so whatever their
+      // part of the ring holds will do.
+      const auto held = [&](int half) { return max(0, min(tile.qn - half * hr, hr)); };
+      const int mine = held(half_rank);
+      // Rows by number, four to a copy (single blocks): warp w issues fours w, w + 4, ...; lane l
+      // looks up row l % 4 of the warp's four l / 4; -1 is a row of zeros.  (Such a copy takes
+      // the copy engine about 40 cycles.  The 16 of a slice of 64 columns keep up with the
+      // memory; the 32 of a pair's slice, whose products take 512 cycles, do not: there the rows
+      // are gathered by a kernel first.  16384 rows x 4096 x 4096: 620 us by number, 331 us + 40
+      // us gathered.  cp.async by the copy warps, announced through a barrier: 758 us.)
+      const bool by_row = CG == 1 && p.row_index != nullptr;
       const int row_in_slice = 4 * (warp + kCopyWarps * (lane >> 2)) + (lane & 3);
-      auto row_of = [&](int at, int limit) {
+      const auto row_of = [&](int at, int limit) {
         if (at >= limit) return -1;
-        const int row = by_row ? p.row_index[at] : at;
+        const int row = p.row_index[at];
         return row >= 0 && row < p.q_rows ? row : -1;
       };
       int next = -1;      // gradient: this lane's row of the next slice
@@ -688,8 +699,23 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         my_rows[lane] = row_of(qf + row_in_slice, tile.q0 + tile.qn);
         __syncwarp();
       }
-      if (MODE == kWgrad && s0 < s1 && lane < 16)
+      if (MODE == kWgrad && by_row && s0 < s1 && lane < 16)
         next = row_of(tile.k0 + s0 * kBK + row_in_slice, tile.k0 + tile.klen);
+      // Issues the copies by number of a slice's `fours`: to dst, from column x of each block.
+      const auto copy_rows = [&](uint32_t dst, int fours, int blocks, int x, uint32_t bar) {
+        for (int c = warp, k = 0; c < fours; c += kCopyWarps, ++k) {
+          const int4 v = *reinterpret_cast<const int4 *>(my_rows + 4 * k);
+#pragma unroll
+          for (int pl = 0; pl < PLANES; ++pl) {
+            const int out = PLANES * p.q_rows, add = pl * p.q_rows;
+            const int y[4] = {v.x < 0 ? out : v.x + add, v.y < 0 ? out : v.y + add,
+                              v.z < 0 ? out : v.z + add, v.w < 0 ? out : v.w + add};
+            for (int b = 0; b < blocks; ++b)
+              tma_rows4(dst + pl * S::kQTile + b * 8192 + c * 512, &map_qr, x + b * 64, y, bar);
+          }
+        }
+      };
+
       for (int s = s0; s < s1 && !timed_out; ++s, ++r) {
         const uint32_t st_i = r % S::kStages;
         if (r >= S::kStages) {
@@ -704,145 +730,137 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         const uint32_t sq = st + PLANES * kPTile;
         const uint32_t full_local = bar_full + 8 * st_i;
         const uint32_t full = CG == 2 ? map_rank(full_local, 0) : full_local;
+
+        // What this slice is: rows [z0, z1) of its tiles count, the others have to be zeros.
+        const bool ext = MODE == kLora && s >= nbase;
+        int k0 = s * kBK, g = pg, gcount = pcount, lo = 0, hi = 0, rank0 = 0;
+        int cnt = kBK;
         if (MODE == kWgrad) {
-          const int cnt = min(kBK, tile.klen - s * kBK);
-          const int groups4 = (cnt + 15) / 16 * 4;      // groups of four rows copied
-          const int p0 = tile.k0 + s * kBK;
-          const int qblocks = hr / 64;
-          if (by_row || cnt < kBK) {
+          k0 += tile.k0;
+          cnt = min(kBK, tile.klen - s * kBK);
+        } else if (ext) {
+          const int e = (s - nbase) / per_rank;
+          const int j = s - nbase - e * per_rank;
+          k0 = j * kBK;                    // of u
+          rank0 = j * S::kRankSlice;       // of b
+          g = p.e_shared ? 0 : tab.gid[tile.e0 + e];
+          gcount = p.e_shared ? 1 : p.groups;
+          lo = tab.row[tile.e0 + e];
+          hi = tab.row[tile.e0 + e + 1];
+        }
+        const int qblocks = hr / 64;
+        // Bytes that the copies of a block bring, and whether rows of zeros follow them.
+        const auto bytes_of = [&](int half) {
+          if (MODE == kWgrad)
+            return uint32_t(PLANES) * (kPTile + uint32_t(by_row ? (cnt + 15) / 16 * 2048 * qblocks
+                                                               : qblocks * 8192));
+          const uint32_t cols = by_row && !ext ? (held(half) + 3) / 4 * 512
+                                               : (held(half) + S::kBox - 1) / S::kBox * (S::kBox * 128);
+          return PLANES * ((ext && p.e_mn ? 2 * S::kRankSlice * 128 : kPTile) + cols);
+        };
+        const auto patch_of = [&](int half) {
+          if (MODE == kWgrad) return cnt < kBK;
+          const int q = tile.q0 + half * hr;
+          return ext && held(half) > 0 && (lo > q || hi < q + held(half));
+        };
+        const bool patch = MODE != kForward && patch_of(half_rank);
+        const uint32_t bar = patch ? bar_patch + 8 * st_i : full;
+        if (warp == 0 && elect_one()) {
+          uint32_t bytes = 0;
+#pragma unroll
+          for (int h = 0; h < CG; ++h)
+            if (MODE == kForward || !patch_of(h)) bytes += bytes_of(h);
+          if (int(blockIdx.x) == p.drop_block && r == 0) bytes += 16;
+          if (patch) mbar_expect(bar, bytes_of(half_rank));
+          if (leader && !patch) mbar_expect(full_local, bytes);
+          if (leader && patch && bytes) mbar_expect_only(full_local, bytes);
+          if (MODE == kWgrad) {
+#pragma unroll
+            for (int i = 0; i < 2 * PLANES; ++i)
+              tma_2d<CG>(st + i * 8192, &map_p, n0 + (i & 1) * 64, k0 + (i >> 1) * p.rows, bar);
+          } else if (ext) {
+            if (p.e_mn) {
+#pragma unroll
+              for (int i = 0; i < 2 * PLANES; ++i)
+                tma_3d<CG>(st + i * 8192, &map_e, n0 + (i & 1) * 64, rank0, g + (i >> 1) * gcount,
+                           bar);
+            } else {
+#pragma unroll
+              for (int i = 0; i < PLANES; ++i)
+                tma_3d<CG>(st + i * kPTile, &map_e, rank0, n0, g + i * gcount, bar);
+            }
+          } else if (p.p_mn) {
+#pragma unroll
+            for (int i = 0; i < 2 * PLANES; ++i)
+              tma_3d<CG>(st + i * 8192, &map_p, n0 + (i & 1) * 64, k0, g + (i >> 1) * gcount, bar);
+          } else {
+#pragma unroll
+            for (int i = 0; i < PLANES; ++i)
+              tma_3d<CG>(st + i * kPTile, &map_p, k0, n0, g + i * gcount, bar);
+          }
+          if (MODE != kForward && !leader && !patch) mbar_arrive_relaxed(full);
+        }
+        __syncwarp();
+        if (by_row && !ext) {
+          if (MODE == kWgrad) {
             __syncwarp();
             if (lane < 16) my_rows[lane] = next;
             __syncwarp();
             if (s + 1 < s1 && lane < 16)
-              next = row_of(p0 + kBK + row_in_slice, tile.k0 + tile.klen);
-          } else if (s + 1 < s1 && lane < 16) {
-            next = row_of(p0 + kBK + row_in_slice, tile.k0 + tile.klen);
+              next = row_of(k0 + kBK + row_in_slice, tile.k0 + tile.klen);
           }
-          if (elect_one()) {
-            if (warp == 0 && leader) {
-              uint32_t bytes = uint32_t(groups4) * 512u * uint32_t(2 + qblocks) * PLANES * CG;
-              if (int(blockIdx.x) == p.drop_block && r == 0) bytes += 16;
-              mbar_expect(full_local, bytes);
+          if (elect_one())
+            copy_rows(sq, MODE == kWgrad ? (cnt + 15) / 16 * 4 : (mine + 3) / 4,
+                      MODE == kWgrad ? qblocks : 1, MODE == kWgrad ? qf : k0, bar);
+        } else if (warp == 1 && elect_one()) {
+          if (MODE == kWgrad) {
+            for (int pl = 0; pl < PLANES; ++pl)
+              for (int b = 0; b < qblocks; ++b)
+                tma_2d<CG>(sq + pl * S::kQTile + b * 8192, &map_q, qf + b * 64, k0 + pl * p.q_rows,
+                           bar);
+          } else {
+            const CUtensorMap *map = ext ? &map_u : &map_q;
+            const int rows = ext ? p.rows : p.q_rows;
+            for (int pl = 0; pl < PLANES; ++pl)
+              for (int b = 0; b < (mine + S::kBox - 1) / S::kBox; ++b)
+                tma_2d<CG>(sq + pl * S::kQTile + b * (S::kBox * 128), map, k0,
+                           qf + b * S::kBox + pl * rows, bar);
+          }
+        }
+        __syncwarp();
+        if (patch) {
+          // Rows of zeros, once the copies are here, by one of the three warps that have little
+          // else to do; then this block's word to the products.
+          const uint32_t parity = (patched >> st_i) & 1u;
+          patched ^= 1u << st_i;
+          if (warp == 1 + int(r % 3)) {
+            const bool ok = mbar_wait(bar_patch + 8 * st_i, parity, p.wait_limit_ns);
+            if (!__all_sync(~0u, ok)) {
+              timed_out = true;
+              break;
             }
-            if (cnt == kBK) {
-              if (warp == 0) {
-#pragma unroll
-                for (int i = 0; i < 2 * PLANES; ++i)
-                  tma_2d<CG>(st + i * 8192, &map_p, n0 + (i & 1) * 64, p0 + (i >> 1) * p.rows, full);
-              }
-            } else {
-              for (int g = warp; g < groups4; g += kCopyWarps)
-#pragma unroll
-                for (int i = 0; i < 2 * PLANES; ++i) {
-                  int y[4];
-#pragma unroll
-                  for (int j = 0; j < 4; ++j)
-                    y[j] = 4 * g + j < cnt ? p0 + 4 * g + j + (i >> 1) * p.rows : PLANES * p.rows;
-                  tma_rows4<CG>(st + i * 8192 + g * 512, &map_e, n0 + (i & 1) * 64, y, full);
-                }
-            }
-            if (cnt == kBK && !by_row) {
-              if (warp == 1)
+            if (MODE == kWgrad) {
+              // Rows [cnt, the next multiple of 16): past the group's end.
+              const int n = 8 * (((cnt + 15) & ~15) - cnt);
+              for (int i = lane; i < n; i += 32) {
+                const uint32_t at = uint32_t(cnt * 128 + i * 16);
+                for (int b = 0; b < 2 * PLANES; ++b) zero16(st + b * 8192 + at);
                 for (int pl = 0; pl < PLANES; ++pl)
-                  for (int b = 0; b < qblocks; ++b)
-                    tma_2d<CG>(sq + pl * S::kQTile + b * 8192, &map_q, qf + b * 64,
-                               p0 + pl * p.q_rows, full);
+                  for (int b = 0; b < qblocks; ++b) zero16(sq + pl * S::kQTile + b * 8192 + at);
+              }
             } else {
-              for (int g = warp, k = 0; g < groups4; g += kCopyWarps, ++k) {
-                const int4 v = *reinterpret_cast<const int4 *>(my_rows + 4 * k);
-#pragma unroll
-                for (int pl = 0; pl < PLANES; ++pl) {
-                  const int out = PLANES * p.q_rows, add = pl * p.q_rows;
-                  const int y[4] = {v.x < 0 ? out : v.x + add, v.y < 0 ? out : v.y + add,
-                                    v.z < 0 ? out : v.z + add, v.w < 0 ? out : v.w + add};
-                  for (int b = 0; b < qblocks; ++b)
-                    tma_rows4<CG>(sq + pl * S::kQTile + b * 8192 + g * 512, &map_qr, qf + b * 64, y,
-                                  full);
-                }
+              // Rows of u of other adapters.
+              for (int i = lane; i < 8 * mine; i += 32) {
+                const int at = qf + (i >> 3);
+                if (at < lo || at >= hi)
+                  for (int pl = 0; pl < PLANES; ++pl) zero16(sq + pl * S::kQTile + i * 16);
               }
             }
+            proxy_fence();
+            __syncwarp();
+            if (elect_one()) mbar_arrive(full);
+            __syncwarp();
           }
-          __syncwarp();
-        } else {
-          const bool ext = MODE == kLora && s >= nbase;
-          int k0 = s * kBK, g = pg, gcount = pcount, lo = 0, hi = 0, rank0 = 0;
-          if (ext) {
-            const int e = (s - nbase) / per_rank;
-            const int j = s - nbase - e * per_rank;
-            k0 = j * kBK;                    // of u
-            rank0 = j * S::kRankSlice;       // of b
-            g = p.e_shared ? 0 : tab.gid[tile.e0 + e];
-            gcount = p.e_shared ? 1 : p.groups;
-            lo = tab.row[tile.e0 + e];
-            hi = min(tab.row[tile.e0 + e + 1], tile.q0 + tile.qn);
-          }
-          if (elect_one()) {
-            if (warp == 0) {
-              if (leader) {
-                uint32_t bytes = CG * PLANES * kPTile;
-                if (ext && p.e_mn) bytes = CG * PLANES * 2 * S::kRankSlice * 128;
-#pragma unroll
-                for (int h = 0; h < CG; ++h)
-                  bytes += PLANES * (ext || by_row
-                                         ? uint32_t((held(h) + 3) / 4) * 512u
-                                         : uint32_t((held(h) + S::kBox - 1) / S::kBox) *
-                                               uint32_t(S::kBox * 128));
-                if (int(blockIdx.x) == p.drop_block && r == 0) bytes += 16;
-                mbar_expect(full_local, bytes);
-              }
-              if (ext) {
-                if (p.e_mn) {
-#pragma unroll
-                  for (int i = 0; i < 2 * PLANES; ++i)
-                    tma_3d<CG>(st + i * 8192, &map_e, n0 + (i & 1) * 64, rank0,
-                               g + (i >> 1) * gcount, full);
-                } else {
-#pragma unroll
-                  for (int i = 0; i < PLANES; ++i)
-                    tma_3d<CG>(st + i * kPTile, &map_e, rank0, n0, g + i * gcount, full);
-                }
-              } else if (p.p_mn) {
-#pragma unroll
-                for (int i = 0; i < 2 * PLANES; ++i)
-                  tma_3d<CG>(st + i * 8192, &map_p, n0 + (i & 1) * 64, k0, g + (i >> 1) * gcount,
-                             full);
-              } else {
-#pragma unroll
-                for (int i = 0; i < PLANES; ++i)
-                  tma_3d<CG>(st + i * kPTile, &map_p, k0, n0, g + i * gcount, full);
-              }
-            }
-            if (ext) {
-              for (int c = warp; c < quads; c += kCopyWarps) {
-                const int at = qf + 4 * c;
-#pragma unroll
-                for (int pl = 0; pl < PLANES; ++pl) {
-                  int y[4];
-#pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    y[i] = at + i >= lo && at + i < hi ? at + i + pl * p.rows : PLANES * p.rows;
-                  tma_rows4<CG>(sq + pl * S::kQTile + c * 512, &map_u, k0, y, full);
-                }
-              }
-            } else if (by_row) {
-              for (int c = warp, k = 0; c < quads; c += kCopyWarps, ++k) {
-                const int4 v = *reinterpret_cast<const int4 *>(my_rows + 4 * k);
-#pragma unroll
-                for (int pl = 0; pl < PLANES; ++pl) {
-                  const int out = PLANES * p.q_rows, add = pl * p.q_rows;
-                  const int y[4] = {v.x < 0 ? out : v.x + add, v.y < 0 ? out : v.y + add,
-                                    v.z < 0 ? out : v.z + add, v.w < 0 ? out : v.w + add};
-                  tma_rows4<CG>(sq + pl * S::kQTile + c * 512, &map_qr, k0, y, full);
-                }
-              }
-            } else if (warp == 1) {
-              for (int pl = 0; pl < PLANES; ++pl)
-                for (int b = 0; b < boxes; ++b)
-                  tma_2d<CG>(sq + pl * S::kQTile + b * (S::kBox * 128), &map_q, k0,
-                             qf + b * S::kBox + pl * p.q_rows, full);
-            }
-          }
-          __syncwarp();
         }
       }
     } else if (warp == kMmaWarp) {
@@ -1017,6 +1035,12 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     for (uint32_t i = r > S::kStages ? r - S::kStages : 0; i < r; ++i)
       mbar_wait(bar_full + 8 * (i % S::kStages), (i / S::kStages) & 1u, p.wait_limit_ns);
   }
+  if (warp == 0 && timed_out) {
+    // And those counted by other barriers: a copy that was issued lands within microseconds.
+    const uint64_t t0 = timer_ns();
+    while (timer_ns() - t0 < 1000 * 1000) {
+    }
+  }
   if (warp == kMmaWarp && leader) {
     if (elect_one()) mma_commit<CG>(bar_drain, false);
     __syncwarp();
@@ -1044,13 +1068,14 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
 
 // Copies a stack of matrices into 16-bit planes whose rows start on 16-byte boundaries: FP32
 // values into their three bf16 parts (planes), 16-bit values as they are (one plane).  Layout:
-// [plane][matrix][row][ld8].  Matrices of groups without rows are left out.  Bound by memory:
-// each thread moves eight values.
+// [plane][matrix][row][ld8].  With `index` (one matrix only) row r is the source's row index[r],
+// zeros for a number outside [0, src_rows).  Matrices of groups without rows are left out.
+// Bound by memory: each thread moves eight values.
 template <bool F32>
 __global__ void planes_kernel(const void *__restrict__ src, int64_t count, int64_t rows,
                               int64_t cols, int64_t ld, int64_t stride, int vec,
-                              const int *__restrict__ offsets, uint16_t *__restrict__ dst,
-                              int64_t ld8) {
+                              const int *__restrict__ offsets, const int *__restrict__ index,
+                              int64_t src_rows, uint16_t *__restrict__ dst, int64_t ld8) {
   const int64_t per_row = ld8 / 8;
   const int64_t total = rows * per_row;
   const int64_t plane = count * rows * ld8;
@@ -1059,19 +1084,24 @@ __global__ void planes_kernel(const void *__restrict__ src, int64_t count, int64
     for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < total;
          i += int64_t(gridDim.x) * blockDim.x) {
       const int64_t row = i / per_row, c = (i - row * per_row) * 8;
-      const int64_t so = m * stride + row * ld + c;
+      int64_t from = row, left = cols - c;
+      if (index) {
+        from = index[row];
+        if (from < 0 || from >= src_rows) from = left = 0;
+      }
+      const int64_t so = m * stride + from * ld + c;
       const int64_t to = (m * rows + row) * ld8 + c;
       if constexpr (F32) {
         const float *s = static_cast<const float *>(src) + so;
         float x[8];
-        if (vec && c + 8 <= cols) {
+        if (vec && left >= 8) {
           const float4 a = *reinterpret_cast<const float4 *>(s);
           const float4 b = *reinterpret_cast<const float4 *>(s + 4);
           x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
           x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = c + j < cols ? s[j] : 0.0f;
+          for (int j = 0; j < 8; ++j) x[j] = j < left ? s[j] : 0.0f;
         }
         uint16_t h[8][3];
 #pragma unroll
@@ -1087,12 +1117,17 @@ __global__ void planes_kernel(const void *__restrict__ src, int64_t count, int64
         }
       } else {
         const uint16_t *s = static_cast<const uint16_t *>(src) + so;
-        uint32_t x[8];
+        uint4 v;
+        if (vec && left >= 8) {
+          v = *reinterpret_cast<const uint4 *>(s);
+        } else {
+          uint32_t x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = c + j < cols ? s[j] : 0u;
-        *reinterpret_cast<uint4 *>(dst + to) =
-            make_uint4(x[0] | (x[1] << 16), x[2] | (x[3] << 16), x[4] | (x[5] << 16),
-                       x[6] | (x[7] << 16));
+          for (int j = 0; j < 8; ++j) x[j] = j < left ? s[j] : 0u;
+          v = make_uint4(x[0] | (x[1] << 16), x[2] | (x[3] << 16), x[4] | (x[5] << 16),
+                         x[6] | (x[7] << 16));
+        }
+        *reinterpret_cast<uint4 *>(dst + to) = v;
       }
     }
   }
@@ -1114,10 +1149,12 @@ bool in_place(const Stack &s, int dtype) {
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Bytes of an operand's planes in the workspace (0: read in place), or SIZE_MAX.
-size_t plane_bytes(const Stack &s, int dtype) {
-  if (in_place(s, dtype)) return 0;
-  const __int128 n = __int128(dtype == TMM_F32 ? 6 : 2) * s.count * s.rows * round8(s.cols);
+// Bytes of an operand's planes in the workspace (0: read in place), or SIZE_MAX; `gathered`:
+// rows fetched through the row index (0: none).
+size_t plane_bytes(const Stack &s, int dtype, int64_t gathered = 0) {
+  if (in_place(s, dtype) && gathered == 0) return 0;
+  const __int128 n = __int128(dtype == TMM_F32 ? 6 : 2) * s.count *
+                     (gathered ? gathered : s.rows) * round8(s.cols);
   return n > __int128(INT64_MAX / 4) ? SIZE_MAX : round256(size_t(n));
 }
 
@@ -1137,30 +1174,34 @@ struct Planes {
 };
 
 // The operand in place, or its planes made in *ws (which advances past them); matrices of
-// groups without rows (by `offsets`, a matrix per group) are not made.
+// groups without rows (by `offsets`, a matrix per group) are not made.  With `gathered` the
+// planes hold the rows that `index` names.
 cudaError_t make_planes(const Stack &s, int dtype, const int32_t *offsets, char **ws,
-                        const DeviceInfo &dev, cudaStream_t stream, Planes *out) {
-  if (in_place(s, dtype)) {
+                        const DeviceInfo &dev, cudaStream_t stream, Planes *out,
+                        int64_t gathered = 0, const int32_t *index = nullptr) {
+  if (in_place(s, dtype) && gathered == 0) {
     *out = {s.data, s.count, s.rows, s.cols, s.ld, s.count > 1 ? s.stride : s.rows * s.ld};
     return cudaSuccess;
   }
-  const int64_t ld8 = round8(s.cols);
+  const int64_t ld8 = round8(s.cols), rows = gathered ? gathered : s.rows;
   const int planes = dtype == TMM_F32 ? 3 : 1;
+  const int size = dtype == TMM_F32 ? 4 : 2;
   uint16_t *dst = reinterpret_cast<uint16_t *>(*ws);
-  *ws += plane_bytes(s, dtype);
-  const int64_t work = (s.rows * (ld8 / 8) + 255) / 256;
+  *ws += plane_bytes(s, dtype, gathered);
+  const int64_t work = (rows * (ld8 / 8) + 255) / 256;
   const dim3 grid(unsigned(std::min<int64_t>(work, 8 * dev.sm_count)),
                   unsigned(std::min<int64_t>(s.count, 1024)));
-  const int vec = (reinterpret_cast<uintptr_t>(s.data) & 15u) == 0 && s.ld % 4 == 0 &&
-                  (s.count == 1 || s.stride % 4 == 0);
+  const int vec = (reinterpret_cast<uintptr_t>(s.data) & 15u) == 0 && s.ld * size % 16 == 0 &&
+                  (s.count == 1 || s.stride * size % 16 == 0);
   if (s.count == 1) offsets = nullptr;      // one matrix may serve every group
+  if (gathered == 0) index = nullptr;
   if (dtype == TMM_F32)
-    planes_kernel<true><<<grid, 256, 0, stream>>>(s.data, s.count, s.rows, s.cols, s.ld, s.stride,
-                                                  vec, offsets, dst, ld8);
+    planes_kernel<true><<<grid, 256, 0, stream>>>(s.data, s.count, rows, s.cols, s.ld, s.stride,
+                                                  vec, offsets, index, s.rows, dst, ld8);
   else
-    planes_kernel<false><<<grid, 256, 0, stream>>>(s.data, s.count, s.rows, s.cols, s.ld,
-                                                   s.stride, 0, offsets, dst, ld8);
-  *out = {dst, planes * s.count, s.rows, s.cols, ld8, s.rows * ld8};
+    planes_kernel<false><<<grid, 256, 0, stream>>>(s.data, s.count, rows, s.cols, s.ld, s.stride,
+                                                   vec, offsets, index, s.rows, dst, ld8);
+  *out = {dst, planes * s.count, rows, s.cols, ld8, rows * ld8};
   return cudaGetLastError();
 }
 
@@ -1255,12 +1296,16 @@ int split_of(int64_t tiles, int64_t slices, const DeviceInfo &dev) {
   return s;
 }
 
-// Forward product on prepared operands.
-cudaError_t run_forward(const Planes &x, int64_t x_rows, const Planes &w, bool shared_w,
+// Pairs from 64 rows per group on average.
+int forward_shape(int64_t rows, int64_t groups) { return rows > 64 * groups ? 2 : 1; }
+int lora_shape(int64_t rows) { return rows > 64 ? 2 : 1; }
+int wgrad_shape(int64_t N) { return N > 128 ? 2 : 1; }
+
+// Forward product on prepared operands; `index`: the rows of x by number, or NULL.
+cudaError_t run_forward(const Planes &x, const int32_t *index, const Planes &w, bool shared_w,
                         bool trans_w, int planes, Params prm, const DeviceInfo &dev,
                         cudaStream_t stream) {
-  // Pairs from 64 rows per group on average.
-  const int cg = prm.rows > 64 * int64_t(prm.groups) ? 2 : 1;
+  const int cg = forward_shape(prm.rows, prm.groups);
   const int bn = columns_of(cg, planes);
   prm.panels = int((prm.N + 128 * cg - 1) / (128 * cg));
   const int64_t tiles =
@@ -1268,33 +1313,45 @@ cudaError_t run_forward(const Planes &x, int64_t x_rows, const Planes &w, bool s
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
   prm.ksplit = cg == 2 ? 1 : split_of(tiles, (prm.K + kBK - 1) / kBK, dev);
   if (prm.n_out == 0) prm.n_out = prm.N;
-  prm.q_rows = int(x_rows);
+  prm.row_index = index;
+  prm.q_rows = int(x.rows);
   prm.p_mn = trans_w ? 0 : 1;
   prm.p_shared = shared_w ? 1 : 0;
   Maps m;
   cudaError_t e;
   if ((e = tile_map(&m.p, w, trans_w ? 128 : 64)) != cudaSuccess ||
-      (e = row_map(&m.q, x, uint32_t(box_of(cg)))) != cudaSuccess ||
-      (e = row_map(&m.qr, x, 1)) != cudaSuccess)
+      (e = index ? row_map(&m.qr, x, 1) : row_map(&m.q, x, uint32_t(box_of(cg)))) != cudaSuccess)
     return e;
+  if (index) m.q = m.qr;
+  else m.qr = m.q;
   m.e = m.p;
-  m.u = m.qr;
+  m.u = m.q;
   return launch_any(cg, planes, kForward, m, prm, tiles, dev, stream);
 }
 
 }  // namespace
 
+// Rows that are gathered before a product of pairs (0: none).
+static int64_t gathered_rows(int cg, const int32_t *row_index, int64_t rows) {
+  return cg == 2 && row_index != nullptr ? rows : 0;
+}
+
 size_t grouped_workspace_bytes(const GroupedProblem &p) {
-  return add_sizes({plane_bytes(p.x, p.dtype), plane_bytes(p.w, p.dtype)});
+  const int64_t gathered =
+      gathered_rows(forward_shape(p.rows, p.groups), p.row_index, p.rows);
+  return add_sizes({plane_bytes(p.x, p.dtype, gathered), plane_bytes(p.w, p.dtype)});
 }
 
 cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void *workspace,
                            cudaStream_t stream) {
   char *ws = static_cast<char *>(workspace);
   const bool shared = p.groups > 1 && p.w.count == 1;
+  const int64_t gathered =
+      gathered_rows(forward_shape(p.rows, p.groups), p.row_index, p.rows);
   Planes x, w;
   cudaError_t e;
-  if ((e = make_planes(p.x, p.dtype, nullptr, &ws, dev, stream, &x)) != cudaSuccess ||
+  if ((e = make_planes(p.x, p.dtype, nullptr, &ws, dev, stream, &x, gathered, p.row_index)) !=
+          cudaSuccess ||
       (e = make_planes(p.w, p.dtype, p.offsets, &ws, dev, stream, &w)) != cudaSuccess)
     return e;
   const int planes = p.dtype == TMM_F32 ? 3 : 1;
@@ -1302,18 +1359,20 @@ cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void 
   prm.rows = int(p.rows);
   prm.groups = int(p.groups);
   prm.offsets = p.offsets;
-  prm.row_index = p.row_index;
   prm.K = int(p.K);
   prm.N = int(p.N);
   prm.idesc = type_desc(p.dtype);
   prm.out = p.y;
   prm.ld_out = p.ldy;
   prm.out_type = out_type(p.dtype);
-  return run_forward(x, p.x.rows, w, shared, p.trans_w != 0, planes, prm, dev, stream);
+  return run_forward(x, gathered ? nullptr : p.row_index, w, shared, p.trans_w != 0, planes, prm,
+                     dev, stream);
 }
 
 size_t wgrad_workspace_bytes(const WgradProblem &p) {
-  return add_sizes({plane_bytes(p.x, p.dtype), plane_bytes(p.dy, p.dtype)});
+  return add_sizes(
+      {plane_bytes(p.x, p.dtype, gathered_rows(wgrad_shape(p.N), p.row_index, p.rows)),
+       plane_bytes(p.dy, p.dtype)});
 }
 
 cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *workspace,
@@ -1321,7 +1380,11 @@ cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *wor
   char *ws = static_cast<char *>(workspace);
   Planes x, dy;
   cudaError_t e;
-  if ((e = make_planes(p.x, p.dtype, nullptr, &ws, dev, stream, &x)) != cudaSuccess ||
+  const int cg = wgrad_shape(p.N);
+  const int64_t gathered = gathered_rows(cg, p.row_index, p.rows);
+  const int32_t *index = gathered ? nullptr : p.row_index;
+  if ((e = make_planes(p.x, p.dtype, nullptr, &ws, dev, stream, &x, gathered, p.row_index)) !=
+          cudaSuccess ||
       (e = make_planes(p.dy, p.dtype, nullptr, &ws, dev, stream, &dy)) != cudaSuccess)
     return e;
   const int planes = p.dtype == TMM_F32 ? 3 : 1;
@@ -1329,8 +1392,8 @@ cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *wor
   prm.rows = int(p.rows);
   prm.groups = int(p.groups);
   prm.offsets = p.offsets;
-  prm.row_index = p.row_index;
-  prm.q_rows = int(p.x.rows);
+  prm.row_index = index;
+  prm.q_rows = int(x.rows);
   prm.q_cols = int(p.K);
   prm.N = int(p.N);
   prm.idesc = type_desc(p.dtype);
@@ -1340,17 +1403,19 @@ cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *wor
   prm.out_type = out_type(p.dtype);
   prm.n_out = prm.N;
   prm.ksplit = 1;
-  const int cg = p.N > 128 ? 2 : 1;
   const int bn = columns_of(cg, planes);
   prm.panels = int((p.N + 128 * cg - 1) / (128 * cg));
   const int64_t tiles = p.groups * prm.panels * ((p.K + bn - 1) / bn);
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
   if (cg == 1) prm.ksplit = split_of(tiles, (p.rows / p.groups + kBK - 1) / kBK, dev);
   Maps m;
-  if ((e = row_map(&m.p, dy, kBK)) != cudaSuccess || (e = row_map(&m.e, dy, 1)) != cudaSuccess ||
-      (e = row_map(&m.q, x, kBK)) != cudaSuccess || (e = row_map(&m.qr, x, 1)) != cudaSuccess)
+  if ((e = row_map(&m.p, dy, kBK)) != cudaSuccess ||
+      (e = index ? row_map(&m.qr, x, 1) : row_map(&m.q, x, kBK)) != cudaSuccess)
     return e;
-  m.u = m.qr;
+  if (index) m.q = m.qr;
+  else m.qr = m.q;
+  m.e = m.p;
+  m.u = m.q;
   return launch_any(cg, planes, kWgrad, m, prm, tiles, dev, stream);
 }
 
@@ -1363,7 +1428,9 @@ static int64_t u_columns(const LoraProblem &p) {
 size_t lora_workspace_bytes(const LoraProblem &p) {
   const __int128 u = __int128(p.dtype == TMM_F32 ? 6 : 2) * p.rows * u_columns(p);
   return add_sizes({u > __int128(INT64_MAX / 4) ? SIZE_MAX : round256(size_t(u)),
-                    plane_bytes(p.x, p.dtype), plane_bytes(p.w, p.dtype),
+                    plane_bytes(p.x, p.dtype,
+                                gathered_rows(lora_shape(p.rows), p.row_index, p.rows)),
+                    plane_bytes(p.w, p.dtype),
                     plane_bytes(p.a, p.dtype), plane_bytes(p.b, p.dtype)});
 }
 
@@ -1376,7 +1443,11 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   ws += round256(size_t(planes) * 2 * p.rows * ldu);
   Planes x, w, a, b;
   cudaError_t e;
-  if ((e = make_planes(p.x, p.dtype, nullptr, &ws, dev, stream, &x)) != cudaSuccess ||
+  const int cg = lora_shape(p.rows);
+  const int64_t gathered = gathered_rows(cg, p.row_index, p.rows);
+  const int32_t *index = gathered ? nullptr : p.row_index;
+  if ((e = make_planes(p.x, p.dtype, nullptr, &ws, dev, stream, &x, gathered, p.row_index)) !=
+          cudaSuccess ||
       (e = make_planes(p.w, p.dtype, nullptr, &ws, dev, stream, &w)) != cudaSuccess ||
       (e = make_planes(p.a, p.dtype, p.offsets, &ws, dev, stream, &a)) != cudaSuccess ||
       (e = make_planes(p.b, p.dtype, p.offsets, &ws, dev, stream, &b)) != cudaSuccess)
@@ -1385,7 +1456,6 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   prm.rows = int(p.rows);
   prm.groups = int(p.groups);
   prm.offsets = p.offsets;
-  prm.row_index = p.row_index;
   prm.K = int(p.K);
   prm.N = int(p.rank);
   prm.idesc = type_desc(p.dtype);
@@ -1395,15 +1465,17 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   prm.out_type = kOutU;
   prm.n_out = p.dtype == TMM_F32 ? int(p.rank) : int(ldu / 2);
   prm.scale = p.scale;
-  if ((e = run_forward(x, p.x.rows, a, p.groups > 1 && p.a.count == 1, p.trans_a != 0, planes, prm,
+  if ((e = run_forward(x, index, a, p.groups > 1 && p.a.count == 1, p.trans_a != 0, planes, prm,
                        dev, stream)) !=
       cudaSuccess)
     return e;
 
-  const int cg = p.rows > 64 ? 2 : 1;
   const int bn = columns_of(cg, planes);
   prm.N = prm.n_out = int(p.N);
-  prm.q_rows = int(p.x.rows);
+  prm.row_index = index;
+  prm.out_index = p.row_index;
+  prm.q_rows = int(x.rows);
+  prm.out_rows = int(p.rows);
   prm.rank = int(p.rank);
   prm.panels = int((p.N + 128 * cg - 1) / (128 * cg));
   const int64_t tiles = prm.panels * ((p.rows + bn - 1) / bn);
@@ -1421,11 +1493,13 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   const Planes up = {u, planes, p.rows, planes == 3 ? p.rank : ldu, ldu, p.rows * ldu};
   Maps m;
   if ((e = tile_map(&m.p, w, p.trans_w ? 128 : 64)) != cudaSuccess ||
-      (e = row_map(&m.q, x, uint32_t(box_of(cg)))) != cudaSuccess ||
-      (e = row_map(&m.qr, x, 1)) != cudaSuccess ||
+      (e = index ? row_map(&m.qr, x, 1) : row_map(&m.q, x, uint32_t(box_of(cg)))) !=
+          cudaSuccess ||
       (e = tile_map(&m.e, b, p.trans_b ? 128 : planes == 3 ? 64 : 32)) != cudaSuccess ||
-      (e = row_map(&m.u, up, 1)) != cudaSuccess)
+      (e = row_map(&m.u, up, uint32_t(box_of(cg)))) != cudaSuccess)
     return e;
+  if (index) m.q = m.qr;
+  else m.qr = m.q;
   return launch_any(cg, planes, kLora, m, prm, tiles, dev, stream);
 }
 

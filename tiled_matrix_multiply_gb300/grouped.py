@@ -179,10 +179,8 @@ def gemm_grouped(x, w, offsets, rows=None, y=None, workspace=None, stream=None):
     ldy = _operand(y, "y", x, 2)[2]
     x_ptr, w_ptr = x.data_ptr(), w.data_ptr()
     head = (code, trans, groups, R, N, K, x_ptr, x_rows, ldx)
-    # 16-bit operands on 16-byte boundaries are read in place and need no workspace.
-    if code == _abi.TMM_F32 or (x_ptr | w_ptr) & 15 or (ldx | ldw | stride_w) & 7:
-        need = _abi.load().gemm_grouped_workspace_size(*head, w_ptr, ldw, stride_w)
-        workspace = _workspace(workspace, need, x)
+    need = _abi.load().gemm_grouped_workspace_size(*head, rows_ptr, w_ptr, ldw, stride_w)
+    workspace = _workspace(workspace, need, x)
     _call("gemm_grouped", x, stream, workspace, *head, offsets.data_ptr(), rows_ptr, w_ptr, ldw,
           stride_w, y.data_ptr(), ldy)
     return y
@@ -210,9 +208,8 @@ def gemm_grouped_wgrad(x, dy, offsets, rows=None, dw=None, workspace=None, strea
     _, _, lddw, stride, _ = _operand(dw, "dw", x, 3)
     x_ptr, dy_ptr = x.data_ptr(), dy.data_ptr()
     head = (code, groups, R, N, K, x_ptr, x_rows, ldx)
-    if code == _abi.TMM_F32 or (x_ptr | dy_ptr) & 15 or (ldx | lddy) & 7:
-        need = _abi.load().gemm_grouped_wgrad_workspace_size(*head, dy_ptr, lddy)
-        workspace = _workspace(workspace, need, x)
+    need = _abi.load().gemm_grouped_wgrad_workspace_size(*head, rows_ptr, dy_ptr, lddy)
+    workspace = _workspace(workspace, need, x)
     _call("gemm_grouped_wgrad", x, stream, workspace, *head, offsets.data_ptr(), rows_ptr, dy_ptr,
           lddy, dw.data_ptr(), lddw, stride)
     return dw
@@ -249,7 +246,7 @@ def gemm_lora(x, w, a, b, scale, offsets, rows=None, y=None, workspace=None, str
     ldy = _operand(y, "y", x, 2)[2]
     head = (code, tw, ta, tb, groups, T, N, K, r, x.data_ptr(), ldx)
     mats = (w.data_ptr(), ldw, a.data_ptr(), lda, stride_a, b.data_ptr(), ldb, stride_b)
-    need = _abi.load().gemm_lora_workspace_size(*head, *mats)
+    need = _abi.load().gemm_lora_workspace_size(*head, rows_ptr, *mats)
     _call("gemm_lora", x, stream, _workspace(workspace, need, x), *head, offsets.data_ptr(),
           rows_ptr, *mats, scale.data_ptr(), y.data_ptr(), ldy)
     return y
