@@ -86,12 +86,14 @@ struct Shape {
   static constexpr int kStages = PLANES == 3 ? (CG == 2 ? 3 : 2) : (CG == 2 ? 6 : 7);
   static constexpr uint32_t kTmemCols =
       PLANES == 3 ? 4 * kBN : 2 * kBN;               // two accumulators (of each kind)
+  // The parts of a shared sum (single blocks), and 1 KiB a result warp for 16-bit results.
   static constexpr uint32_t kRed = CG == 1 ? 128 * kBN * 4 : 0;
+  static constexpr uint32_t kOutStage = PLANES == 1 ? kEpiWarps * 1024 : 0;
   // Values of `rank` per slice of the adapters' part: 16-bit u is a pair of values (hi and lo).
   static constexpr int kRankSlice = PLANES == 3 ? 64 : 32;
   static constexpr uint32_t kTable = (kMaxGroups + 1) * 4 * 3 + kCopyWarps * 128 + 116;
   static constexpr uint32_t kBars = 8 * (3 * kStages + 5) + 32;
-  static constexpr uint32_t kSmem = 1024 + kStages * kStage + kRed + kTable + kBars;
+  static constexpr uint32_t kSmem = 1024 + kStages * kStage + kRed + kOutStage + kTable + kBars;
   static_assert(kSmem <= kMaxSmem, "one block's shared memory");
   static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory columns");
 };
@@ -116,6 +118,7 @@ struct Params {
   int64_t ld_out, stride_out;   // stride: of dw's matrices, or of the result's planes
   int out_type;
   int n_out;             // columns written (from N on: zeros)
+  int vec_out;           // 16-bit results with rows (and matrices) on 16-byte boundaries
   const float *scale;    // per group, or NULL
   int ksplit;            // blocks of a cluster that share a tile's sum (CG = 1)
   int64_t wait_limit_ns;
@@ -488,30 +491,85 @@ __device__ __forceinline__ int64_t out_row(const Params &p, const Tile &t, int c
   return int64_t(r) * p.ld_out;
 }
 
-// 16 consecutive columns of the tile from c0 on, for this lane's n: 32 lanes write 64 (128)
-// consecutive bytes of each result row.
+// 16 consecutive columns of the tile from c0 on, for the 32 n of the warp from nw on (lane l
+// holds nw + l).  16-bit results with rows on 16-byte boundaries go through 1 KiB of shared memory
+// (`stage`), from which four lanes take the 64 bytes of a result row: 2 stores of 16 bytes a lane
+// in place of 16 of two bytes.
 template <int MODE, int PLANES>
-__device__ __forceinline__ void store_columns(const Params &p, const Tile &t, int c0, int n,
-                                              const float (&v)[16], float scale) {
+__device__ __forceinline__ void store_columns(const Params &p, const Tile &t, int c0, int nw,
+                                              const float (&v)[16], float scale, uint32_t stage) {
+  const int lane = threadIdx.x & 31;
   const int count = min(16, t.qn - c0);
-  int row = 0;      // adapters: the row of column c0 + lane % 16
+  const int n = nw + lane;
   const bool by_row = MODE == kLora && p.out_index;
+  int64_t first = 0;
+  if (!by_row) {
+    first = out_row<kForward>(p, t, c0);
+    if (MODE == kWgrad) first += int64_t(t.g) * p.stride_out;
+  }
+  if constexpr (PLANES == 1) {
+    if (p.vec_out) {
+      uint16_t h[16];
+      if (p.out_type == kOutBF16) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) h[j] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j] * scale));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) h[j] = __half_as_ushort(__float2half_rn(v[j] * scale));
+      }
+      __syncwarp();      // the reads of the block before are done
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + uint32_t(j * 64 + lane * 2)), "h"(h[j])
+                     : "memory");
+      __syncwarp();
+      const int n8 = nw + (lane & 3) * 8;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = (lane >> 2) + 8 * i;
+        uint4 w;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                     : "r"(stage + uint32_t(row * 64 + (lane & 3) * 16))
+                     : "memory");
+        if (row >= count || n8 >= p.N) continue;
+        const int64_t o = by_row ? out_row<MODE>(p, t, c0 + row) : first + row * p.ld_out;
+        if (o < 0) continue;
+        uint16_t *dst = static_cast<uint16_t *>(p.out) + o + n8;
+        if (n8 + 8 <= p.N) {
+          *reinterpret_cast<uint4 *>(dst) = w;
+        } else {
+          const uint32_t part[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (n8 + j < p.N) dst[j] = uint16_t(part[j / 2] >> (16 * (j & 1)));
+        }
+      }
+      return;
+    }
+  } else if (!by_row && p.out_type == kOutF32) {
+    // 32 lanes write 128 consecutive bytes.
+    float *dst = static_cast<float *>(p.out) + first + n;
+    const bool in = n < p.N;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (in && j < count) dst[j * p.ld_out] = v[j] * scale;
+    return;
+  }
+  int row = 0;      // the row of column c0 + lane % 16
   if (by_row) {
-    const int lane = threadIdx.x & 15;
-    row = lane < count ? p.out_index[t.q0 + c0 + lane] : -1;
+    const int l = lane & 15;
+    row = l < count ? p.out_index[t.q0 + c0 + l] : -1;
     if (row >= p.out_rows) row = -1;
   }
   const bool in = n < p.n_out;
-  int64_t o = out_row<kForward>(p, t, c0);
-  if (MODE == kWgrad) o += int64_t(t.g) * p.stride_out;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     if (by_row) {
       const int r = __shfl_sync(~0u, row, j);
       if (in && r >= 0) store_out<PLANES>(p, int64_t(r) * p.ld_out, n, v[j] * scale);
-    } else {
-      if (in && j < count) store_out<PLANES>(p, o, n, v[j] * scale);
-      o += p.ld_out;
+    } else if (in && j < count) {
+      store_out<PLANES>(p, first + j * p.ld_out, n, v[j] * scale);
     }
   }
 }
@@ -522,7 +580,8 @@ template <int CG, int MODE, int PLANES>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                const __grid_constant__ CUtensorMap map_q,    // Q tiles
-               const __grid_constant__ CUtensorMap map_qr,   // single rows of x
+               const __grid_constant__ CUtensorMap map_qr,   // single rows of x; pairs: tiles of
+                                                             // all the columns of a block
                const __grid_constant__ CUtensorMap map_e,    // b tiles
                const __grid_constant__ CUtensorMap map_u,    // u tiles
                const Params p) {
@@ -532,7 +591,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   const uint32_t base = (raw + 1023u) & ~1023u;    // the same offset in every block
   uint8_t *const smem = smem_raw + (base - raw);
   const uint32_t red = base + S::kStages * S::kStage;
-  const uint32_t table = red + S::kRed;
+  const uint32_t out_stage = red + S::kRed;
+  const uint32_t table = out_stage + S::kOutStage;
   const uint32_t bar_full = (table + S::kTable + 7u) & ~7u;
   const uint32_t bar_empty = bar_full + 8 * S::kStages;
   const uint32_t bar_patch = bar_empty + 8 * S::kStages;   // slices that need rows of zeros
@@ -680,6 +740,13 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       // part of the ring holds will do.
       const auto held = [&](int half) { return max(0, min(tile.qn - half * hr, hr)); };
       const int mine = held(half_rank);
+      const int boxes = (mine + S::kBox - 1) / S::kBox;
+      uint32_t usual = 0;      // bytes of an ordinary slice, of both blocks of a pair
+#pragma unroll
+      for (int h = 0; h < CG; ++h)
+        usual += PLANES * (kPTile + uint32_t(CG == 1 && p.row_index
+                                                 ? (held(h) + 3) / 4 * 512
+                                                 : (held(h) + S::kBox - 1) / S::kBox * S::kBox * 128));
       // Rows by number, four to a copy (single blocks): warp w issues fours w, w + 4, ...; lane l
       // looks up row l % 4 of the warp's four l / 4; -1 is a row of zeros.  (Such a copy takes
       // the copy engine about 40 cycles.  The 16 of a slice of 64 columns keep up with the
@@ -749,14 +816,14 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           hi = tab.row[tile.e0 + e + 1];
         }
         const int qblocks = hr / 64;
-        // Bytes that the copies of a block bring, and whether rows of zeros follow them.
+        // Bytes that the copies of a block bring (gradient, adapters' part), and whether rows of
+        // zeros follow them.
         const auto bytes_of = [&](int half) {
           if (MODE == kWgrad)
             return uint32_t(PLANES) * (kPTile + uint32_t(by_row ? (cnt + 15) / 16 * 2048 * qblocks
                                                                : qblocks * 8192));
-          const uint32_t cols = by_row && !ext ? (held(half) + 3) / 4 * 512
-                                               : (held(half) + S::kBox - 1) / S::kBox * (S::kBox * 128);
-          return PLANES * ((ext && p.e_mn ? 2 * S::kRankSlice * 128 : kPTile) + cols);
+          return PLANES * ((p.e_mn ? 2 * S::kRankSlice * 128 : kPTile) +
+                           uint32_t((held(half) + S::kBox - 1) / S::kBox * (S::kBox * 128)));
         };
         const auto patch_of = [&](int half) {
           if (MODE == kWgrad) return cnt < kBK;
@@ -766,10 +833,13 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         const bool patch = MODE != kForward && patch_of(half_rank);
         const uint32_t bar = patch ? bar_patch + 8 * st_i : full;
         if (warp == 0 && elect_one()) {
-          uint32_t bytes = 0;
+          uint32_t bytes = usual;
+          if (MODE == kWgrad || ext) {
+            bytes = 0;
 #pragma unroll
-          for (int h = 0; h < CG; ++h)
-            if (MODE == kForward || !patch_of(h)) bytes += bytes_of(h);
+            for (int h = 0; h < CG; ++h)
+              if (!patch_of(h)) bytes += bytes_of(h);
+          }
           if (int(blockIdx.x) == p.drop_block && r == 0) bytes += 16;
           if (patch) mbar_expect(bar, bytes_of(half_rank));
           if (leader && !patch) mbar_expect(full_local, bytes);
@@ -800,6 +870,25 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           }
           if (MODE != kForward && !leader && !patch) mbar_arrive_relaxed(full);
         }
+        if (warp == 1 && (!by_row || ext) && elect_one()) {
+          if (MODE == kWgrad) {
+            for (int pl = 0; pl < PLANES; ++pl)
+              for (int b = 0; b < qblocks; ++b)
+                tma_2d<CG>(sq + pl * S::kQTile + b * 8192, &map_q, qf + b * 64, k0 + pl * p.q_rows,
+                           bar);
+          } else if (CG == 2 && mine == S::kBN / CG && !ext) {
+            // A full tile: one copy a plane.
+            for (int pl = 0; pl < PLANES; ++pl)
+              tma_2d<CG>(sq + pl * S::kQTile, &map_qr, k0, qf + pl * p.q_rows, bar);
+          } else {
+            const CUtensorMap *map = ext ? &map_u : &map_q;
+            const int rows = ext ? p.rows : p.q_rows;
+            for (int pl = 0; pl < PLANES; ++pl)
+              for (int b = 0; b < boxes; ++b)
+                tma_2d<CG>(sq + pl * S::kQTile + b * (S::kBox * 128), map, k0,
+                           qf + b * S::kBox + pl * rows, bar);
+          }
+        }
         __syncwarp();
         if (by_row && !ext) {
           if (MODE == kWgrad) {
@@ -812,28 +901,14 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           if (elect_one())
             copy_rows(sq, MODE == kWgrad ? (cnt + 15) / 16 * 4 : (mine + 3) / 4,
                       MODE == kWgrad ? qblocks : 1, MODE == kWgrad ? qf : k0, bar);
-        } else if (warp == 1 && elect_one()) {
-          if (MODE == kWgrad) {
-            for (int pl = 0; pl < PLANES; ++pl)
-              for (int b = 0; b < qblocks; ++b)
-                tma_2d<CG>(sq + pl * S::kQTile + b * 8192, &map_q, qf + b * 64, k0 + pl * p.q_rows,
-                           bar);
-          } else {
-            const CUtensorMap *map = ext ? &map_u : &map_q;
-            const int rows = ext ? p.rows : p.q_rows;
-            for (int pl = 0; pl < PLANES; ++pl)
-              for (int b = 0; b < (mine + S::kBox - 1) / S::kBox; ++b)
-                tma_2d<CG>(sq + pl * S::kQTile + b * (S::kBox * 128), map, k0,
-                           qf + b * S::kBox + pl * rows, bar);
-          }
         }
         __syncwarp();
         if (patch) {
-          // Rows of zeros, once the copies are here, by one of the three warps that have little
+          // Rows of zeros, once the copies are here, by one of the two warps that have little
           // else to do; then this block's word to the products.
           const uint32_t parity = (patched >> st_i) & 1u;
           patched ^= 1u << st_i;
-          if (warp == 1 + int(r % 3)) {
+          if (warp == 2 + int(r & 1)) {
             const bool ok = mbar_wait(bar_patch + 8 * st_i, parity, p.wait_limit_ns);
             if (!__all_sync(~0u, ok)) {
               timed_out = true;
@@ -898,21 +973,28 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           const uint32_t pstep = pmn ? 128 : 2, qstep = MODE == kWgrad ? 128 : 2;   // 16 bytes
           const uint32_t d = tmem + buf * S::kBN;
           if (elect_one()) {
+            if (PLANES == 1 && MODE == kLora && ext) {
+              // b[g] times u's hi, and times its lo, 32 columns on.
+              for (int k = 0; k < steps; ++k) {
+                const uint64_t a = dp + k * pstep, b = dq + k * qstep;
+                mma<CG>(d, a, b, idesc, !(first && k == 0));
+                mma<CG>(d, a, b + 2 * qstep, idesc, true);
+              }
+            } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (k >= steps) break;
-              const uint64_t a = dp + k * pstep, b = dq + k * qstep;
-              mma<CG>(d, a, b, idesc, !(first && k == 0));
-              if constexpr (PLANES == 3) {
-                constexpr uint64_t pa = kPTile >> 4, qa = S::kQTile >> 4;
-                const uint32_t ds = tmem + (2 + (done & 1)) * S::kBN;
-                mma<CG>(ds, a + 2 * pa, b, idesc, !(i == 0 && k == 0));
-                mma<CG>(ds, a, b + 2 * qa, idesc, true);
-                mma<CG>(ds, a + pa, b + qa, idesc, true);
-                mma<CG>(ds, a + pa, b, idesc, true);
-                mma<CG>(ds, a, b + qa, idesc, true);
-              } else if (ext) {
-                mma<CG>(d, a, b + 2 * qstep, idesc, true);      // b[g] times u's lo
+              for (int k = 0; k < 4; ++k) {
+                if (k >= steps) break;
+                const uint64_t a = dp + k * pstep, b = dq + k * qstep;
+                mma<CG>(d, a, b, idesc, !(first && k == 0));
+                if constexpr (PLANES == 3) {
+                  constexpr uint64_t pa = kPTile >> 4, qa = S::kQTile >> 4;
+                  const uint32_t ds = tmem + (2 + (done & 1)) * S::kBN;
+                  mma<CG>(ds, a + 2 * pa, b, idesc, !(i == 0 && k == 0));
+                  mma<CG>(ds, a, b + 2 * qa, idesc, true);
+                  mma<CG>(ds, a + pa, b + qa, idesc, true);
+                  mma<CG>(ds, a + pa, b, idesc, true);
+                  mma<CG>(ds, a, b + qa, idesc, true);
+                }
               }
             }
             mma_commit<CG>(bar_empty + 8 * st_i, true);
@@ -929,7 +1011,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       const int n = s1 - s0;
       const uint32_t lanes = tmem + (uint32_t(32 * quarter) << 16);
       const uint32_t tempty = CG == 2 ? map_rank(bar_tempty, 0) : bar_tempty;
-      const int nn = tile.n0 + half_rank * 128 + 32 * quarter + lane;
+      const int nw = tile.n0 + half_rank * 128 + 32 * quarter;
+      const uint32_t stage = out_stage + uint32_t(warp - kEpi0) * 1024;
       const float scale = MODE == kForward && p.scale ? p.scale[tile.g] : 1.0f;
       constexpr int kBlocks = S::kBN / 32;     // 16-column blocks of a warp, every other one
       auto put = [&](int c0, const float (&v)[16]) {
@@ -937,7 +1020,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
 #pragma unroll
           for (int j = 0; j < 16; ++j) red_ptr[(c0 + j) * 128 + 32 * quarter + lane] = v[j];
         } else {
-          store_columns<MODE, PLANES>(p, tile, c0, nn, v, scale);
+          store_columns<MODE, PLANES>(p, tile, c0, nw, v, scale, stage);
         }
       };
       if constexpr (PLANES == 1) {
@@ -1270,6 +1353,9 @@ cudaError_t launch_any(int cg, int planes, int mode, const Maps &m, Params &prm,
                        const DeviceInfo &dev, cudaStream_t stream) {
   prm.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   prm.drop_block = g_drop_block.load(std::memory_order_relaxed);
+  prm.vec_out = (prm.out_type == kOutBF16 || prm.out_type == kOutF16) &&
+                (reinterpret_cast<uintptr_t>(prm.out) & 15u) == 0 && prm.ld_out % 8 == 0 &&
+                prm.stride_out % 8 == 0;
   if (cg == 2)
     return planes == 3 ? launch_mode<2, 3>(mode, m, prm, tiles, dev, stream)
                        : launch_mode<2, 1>(mode, m, prm, tiles, dev, stream);
@@ -1301,6 +1387,20 @@ int forward_shape(int64_t rows, int64_t groups) { return rows > 64 * groups ? 2 
 int lora_shape(int64_t rows) { return rows > 64 ? 2 : 1; }
 int wgrad_shape(int64_t N) { return N > 128 ? 2 : 1; }
 
+// The maps of x: rows by number; or tiles of box_of rows, and (pairs) of a whole block's columns.
+cudaError_t q_maps(Maps *m, const Planes &x, const int32_t *index, int cg, int bn) {
+  cudaError_t e;
+  if (index) {
+    e = row_map(&m->qr, x, 1);
+    m->q = m->qr;
+    return e;
+  }
+  if ((e = row_map(&m->q, x, uint32_t(box_of(cg)))) != cudaSuccess) return e;
+  if (cg == 2) return row_map(&m->qr, x, uint32_t(bn / 2));
+  m->qr = m->q;
+  return cudaSuccess;
+}
+
 // Forward product on prepared operands; `index`: the rows of x by number, or NULL.
 cudaError_t run_forward(const Planes &x, const int32_t *index, const Planes &w, bool shared_w,
                         bool trans_w, int planes, Params prm, const DeviceInfo &dev,
@@ -1320,10 +1420,8 @@ cudaError_t run_forward(const Planes &x, const int32_t *index, const Planes &w, 
   Maps m;
   cudaError_t e;
   if ((e = tile_map(&m.p, w, trans_w ? 128 : 64)) != cudaSuccess ||
-      (e = index ? row_map(&m.qr, x, 1) : row_map(&m.q, x, uint32_t(box_of(cg)))) != cudaSuccess)
+      (e = q_maps(&m, x, index, cg, bn)) != cudaSuccess)
     return e;
-  if (index) m.q = m.qr;
-  else m.qr = m.q;
   m.e = m.p;
   m.u = m.q;
   return launch_any(cg, planes, kForward, m, prm, tiles, dev, stream);
@@ -1399,7 +1497,7 @@ cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *wor
   prm.idesc = type_desc(p.dtype);
   prm.out = p.dw;
   prm.ld_out = p.lddw;
-  prm.stride_out = p.stride_dw;
+  prm.stride_out = p.groups > 1 ? p.stride_dw : 0;
   prm.out_type = out_type(p.dtype);
   prm.n_out = prm.N;
   prm.ksplit = 1;
@@ -1493,13 +1591,10 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   const Planes up = {u, planes, p.rows, planes == 3 ? p.rank : ldu, ldu, p.rows * ldu};
   Maps m;
   if ((e = tile_map(&m.p, w, p.trans_w ? 128 : 64)) != cudaSuccess ||
-      (e = index ? row_map(&m.qr, x, 1) : row_map(&m.q, x, uint32_t(box_of(cg)))) !=
-          cudaSuccess ||
+      (e = q_maps(&m, x, index, cg, bn)) != cudaSuccess ||
       (e = tile_map(&m.e, b, p.trans_b ? 128 : planes == 3 ? 64 : 32)) != cudaSuccess ||
       (e = row_map(&m.u, up, uint32_t(box_of(cg)))) != cudaSuccess)
     return e;
-  if (index) m.q = m.qr;
-  else m.qr = m.q;
   return launch_any(cg, planes, kLora, m, prm, tiles, dev, stream);
 }
 
