@@ -111,6 +111,7 @@ struct Params {
   int q_cols;            // gradient: columns of x
   int rank;              // adapters
   int panels;            // tiles along N
+  int tile_n;            // columns of a tile, at most kBN
   int p_mn, e_mn;        // P (and b) stored with n contiguous
   int p_shared, e_shared;   // one P (one b) for all groups
   uint32_t idesc;        // types; majors and sizes are added in the kernel
@@ -120,9 +121,29 @@ struct Params {
   int n_out;             // columns written (from N on: zeros)
   int vec_out;           // 16-bit results with rows (and matrices) on 16-byte boundaries
   const float *scale;    // per group, or NULL
+  int zero_rows;         // forward: write zeros to the rows of no group
   int ksplit;            // blocks of a cluster that share a tile's sum (CG = 1)
   int64_t wait_limit_ns;
   int drop_block;        // testing hook: this block waits for bytes that never come (-1: none)
+};
+
+// A place in the ring of stages, and the parity of its round.
+struct Ring {
+  int stage;
+  uint32_t parity;
+  template <int STAGES>
+  __device__ __forceinline__ void next() {
+    if (++stage == STAGES) {
+      stage = 0;
+      parity ^= 1;
+    }
+  }
+  template <int STAGES>
+  __device__ __forceinline__ void skip(int n) {
+    const int to = stage + n;
+    parity ^= uint32_t(to / STAGES) & 1u;
+    stage = to % STAGES;
+  }
 };
 
 // ---- primitives -------------------------------------------------------------------------
@@ -252,6 +273,15 @@ __device__ __forceinline__ void zero16(uint32_t addr) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+// Programmatic dependent launch: wait for the grid before (its results are visible then), and
+// let the next one start its prologue as soon as there is room.
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ void tc_fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
@@ -341,14 +371,14 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const Table &tab, int t
   Tile r;
   r.e0 = r.en = r.k0 = 0;
   if (MODE == kWgrad) {
-    const int qt = (p.q_cols + S::kBN - 1) / S::kBN;
+    const int qt = (p.q_cols + p.tile_n - 1) / p.tile_n;
     const int per = qt * p.panels;
     r.g = t / per;
     const int i = t - r.g * per;
     const int panel = i / qt;
     r.n0 = panel * 128 * CG;
-    r.q0 = (i - panel * qt) * S::kBN;
-    r.qn = min(S::kBN, p.q_cols - r.q0);
+    r.q0 = (i - panel * qt) * p.tile_n;
+    r.qn = min(p.tile_n, p.q_cols - r.q0);
     r.bn = (r.qn + 64 * CG - 1) / (64 * CG) * (64 * CG);
     r.k0 = tab.row[r.g];
     r.klen = tab.row[r.g + 1] - r.k0;
@@ -372,11 +402,11 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const Table &tab, int t
     hi = tab.row[a + 1];
     i = t - tab.tile[a];
   }
-  const int qt = (hi - lo + S::kBN - 1) / S::kBN;
+  const int qt = (hi - lo + p.tile_n - 1) / p.tile_n;
   const int panel = i / qt;
   r.n0 = panel * 128 * CG;
-  r.q0 = lo + (i - panel * qt) * S::kBN;
-  r.qn = min(S::kBN, hi - r.q0);
+  r.q0 = lo + (i - panel * qt) * p.tile_n;
+  r.qn = min(p.tile_n, hi - r.q0);
   r.bn = (r.qn + S::kUnit - 1) / S::kUnit * S::kUnit;
   r.klen = p.K;
   if (MODE == kLora) {
@@ -618,10 +648,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   const bool leader = CG == 1 || rank == 0;
   const int half_rank = CG == 2 ? int(rank) : 0;   // which 128 lanes, which half of the columns
 
-  // Group offsets, clamped, into the (still unused) ring; barriers; tensor memory.
+  // Barriers and tensor memory; then, once the launches before are done, the group offsets,
+  // clamped, into the (still unused) ring.
   int *const offs = reinterpret_cast<int *>(smem);
-  for (int g = threadIdx.x; g <= p.groups; g += kThreads)
-    offs[g] = max(0, min(p.offsets[g], p.rows));
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(bar_full + 8 * s, MODE == kForward ? 1 : CG);
@@ -648,6 +677,14 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
   }
+  if (warp == 0 && elect_one()) {
+    prefetch_map(&map_p);
+    prefetch_map(&map_q);
+    prefetch_map(&map_qr);
+  }
+  grid_wait();
+  for (int g = threadIdx.x; g <= p.groups; g += kThreads)
+    offs[g] = max(0, min(p.offsets[g], p.rows));
   __syncthreads();
   if (warp == 0) {
     // Group bounds are the running maximum of the offsets: offsets that step back make an
@@ -674,7 +711,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         const int n = g < p.groups ? hi - lo : 0;
         const unsigned have = __ballot_sync(~0u, n > 0);
         const int at = count + __popc(have & ((1u << lane) - 1));
-        const int mine = (n + S::kBN - 1) / S::kBN * p.panels;
+        const int mine = (n + p.tile_n - 1) / p.tile_n * p.panels;
         int sum = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -692,8 +729,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     }
     if (lane == 0) {
       if (MODE != kWgrad) tab_row[count] = carry;
-      if (MODE == kWgrad) tiles = p.groups * p.panels * ((p.q_cols + S::kBN - 1) / S::kBN);
-      if (MODE == kLora) tiles = p.panels * ((p.rows + S::kBN - 1) / S::kBN);
+      if (MODE == kWgrad) tiles = p.groups * p.panels * ((p.q_cols + p.tile_n - 1) / p.tile_n);
+      if (MODE == kLora) tiles = p.panels * ((p.rows + p.tile_n - 1) / p.tile_n);
       slot_ptr[1] = uint32_t(count);
       slot_ptr[2] = uint32_t(tiles);
       slot_ptr[4] = uint32_t(carry);                    // end of the last group
@@ -708,22 +745,31 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   const Table tab = {tab_gid, tab_row, tab_tile, int(slot_ptr[1]), int(slot_ptr[2])};
 
   bool timed_out = false;
-  uint32_t r = 0;      // ring position: slices so far
+  Ring ring = {0, 0};
   uint32_t q = 0;      // tensor-memory sums so far
   uint32_t done = 0;   // tiles with a sum so far
   uint32_t patched = 0;   // a bit per stage: parity of its patched slices
+  bool dropped = int(blockIdx.x) == p.drop_block;   // testing hook: the next expectation is wrong
 
-  // Forward: rows of the result that belong to no group are zero.
-  if (MODE == kForward && warp >= kEpi0 && warp < kMmaWarp) {
+  // Forward: rows of the result that belong to no group are zero, a warp a row.
+  if (MODE == kForward && p.zero_rows && warp >= kEpi0 && warp < kMmaWarp) {
     const int lo = int(slot_ptr[3]), hi = int(slot_ptr[4]);
-    for (int64_t i = blockIdx.x; i < int64_t(lo) + (p.rows - hi); i += gridDim.x) {
-      const int64_t row = i < lo ? i : hi + (i - lo);
-      for (int n = int(threadIdx.x) - 32 * kEpi0; n < p.n_out; n += 32 * kEpiWarps)
-        store_out<PLANES>(p, row * p.ld_out, n, 0.0f);
+    const int64_t count = int64_t(lo) + (p.rows - hi);
+    for (int64_t i = int64_t(blockIdx.x) * kEpiWarps + warp - kEpi0; i < count;
+         i += int64_t(gridDim.x) * kEpiWarps) {
+      const int64_t row = (i < lo ? i : hi + (i - lo)) * p.ld_out;
+      if (p.vec_out && p.N % 8 == 0) {
+        for (int n = lane * 8; n < p.N; n += 256)
+          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + row + n) =
+              make_uint4(0, 0, 0, 0);
+      } else {
+        for (int n = lane; n < p.N; n += 32) store_out<PLANES>(p, row, n, 0.0f);
+      }
     }
   }
 
   for (int t = cluster; t < tab.tiles; t += clusters) {
+    if (timed_out && p.ksplit == 1) break;
     const Tile tile = tile_at<CG, MODE, PLANES>(p, tab, t);
     int nbase, s0, s1;
     slices_of<MODE, S::kRankSlice>(p, tile, CG == 2 ? 0 : int(rank), nbase, s0, s1);
@@ -741,270 +787,362 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       const auto held = [&](int half) { return max(0, min(tile.qn - half * hr, hr)); };
       const int mine = held(half_rank);
       const int boxes = (mine + S::kBox - 1) / S::kBox;
-      uint32_t usual = 0;      // bytes of an ordinary slice, of both blocks of a pair
-#pragma unroll
-      for (int h = 0; h < CG; ++h)
-        usual += PLANES * (kPTile + uint32_t(CG == 1 && p.row_index
-                                                 ? (held(h) + 3) / 4 * 512
-                                                 : (held(h) + S::kBox - 1) / S::kBox * S::kBox * 128));
-      // Rows by number, four to a copy (single blocks): warp w issues fours w, w + 4, ...; lane l
-      // looks up row l % 4 of the warp's four l / 4; -1 is a row of zeros.  (Such a copy takes
-      // the copy engine about 40 cycles.  The 16 of a slice of 64 columns keep up with the
-      // memory; the 32 of a pair's slice, whose products take 512 cycles, do not: there the rows
-      // are gathered by a kernel first.  16384 rows x 4096 x 4096: 620 us by number, 331 us + 40
-      // us gathered.  cp.async by the copy warps, announced through a barrier: 758 us.)
+      const int qblocks = hr / 64;
       const bool by_row = CG == 1 && p.row_index != nullptr;
-      const int row_in_slice = 4 * (warp + kCopyWarps * (lane >> 2)) + (lane & 3);
-      const auto row_of = [&](int at, int limit) {
-        if (at >= limit) return -1;
-        const int row = p.row_index[at];
-        return row >= 0 && row < p.q_rows ? row : -1;
-      };
-      int next = -1;      // gradient: this lane's row of the next slice
-      if (MODE != kWgrad && by_row) {
-        __syncwarp();
-        my_rows[lane] = row_of(qf + row_in_slice, tile.q0 + tile.qn);
-        __syncwarp();
-      }
-      if (MODE == kWgrad && by_row && s0 < s1 && lane < 16)
-        next = row_of(tile.k0 + s0 * kBK + row_in_slice, tile.k0 + tile.klen);
-      // Issues the copies by number of a slice's `fours`: to dst, from column x of each block.
-      const auto copy_rows = [&](uint32_t dst, int fours, int blocks, int x, uint32_t bar) {
-        for (int c = warp, k = 0; c < fours; c += kCopyWarps, ++k) {
-          const int4 v = *reinterpret_cast<const int4 *>(my_rows + 4 * k);
+      uint32_t usual = 0;      // bytes of an ordinary slice, of both blocks of a pair
+      if (MODE == kWgrad) {
+        usual = CG * PLANES * (kPTile + uint32_t(qblocks) * 8192u);
+      } else {
 #pragma unroll
-          for (int pl = 0; pl < PLANES; ++pl) {
-            const int out = PLANES * p.q_rows, add = pl * p.q_rows;
-            const int y[4] = {v.x < 0 ? out : v.x + add, v.y < 0 ? out : v.y + add,
-                              v.z < 0 ? out : v.z + add, v.w < 0 ? out : v.w + add};
-            for (int b = 0; b < blocks; ++b)
-              tma_rows4(dst + pl * S::kQTile + b * 8192 + c * 512, &map_qr, x + b * 64, y, bar);
+        for (int h = 0; h < CG; ++h)
+          usual += PLANES * (kPTile + uint32_t(by_row ? (held(h) + 3) / 4 * 512
+                                                      : (held(h) + S::kBox - 1) / S::kBox *
+                                                            (S::kBox * 128)));
+      }
+
+      // What a slice s is.  Slices of the adapters' part and a group's last one may need rows of
+      // zeros: their copies are counted by the block's own bar_patch, a warp zeroes the rows, and
+      // only then does the block arrive on the leader's bar_full.
+      struct Slice {
+        bool ext;
+        int k0, g, gcount, rank0, lo, hi;   // ext: rows of u in [lo, hi) belong to the adapter
+        int cnt;                            // gradient: rows of the group
+      };
+      const auto slice_at = [&](int s) {
+        Slice c = {MODE == kLora && s >= nbase, s * kBK, pg, pcount, 0, 0, 0, kBK};
+        if (MODE == kWgrad) {
+          c.k0 += tile.k0;
+          c.cnt = min(kBK, tile.klen - s * kBK);
+        } else if (MODE == kLora && c.ext) {
+          const int e = (s - nbase) / per_rank;
+          const int j = s - nbase - e * per_rank;
+          c.k0 = j * kBK;                    // of u
+          c.rank0 = j * S::kRankSlice;       // of b
+          c.g = p.e_shared ? 0 : tab.gid[tile.e0 + e];
+          c.gcount = p.e_shared ? 1 : p.groups;
+          c.lo = tab.row[tile.e0 + e];
+          c.hi = tab.row[tile.e0 + e + 1];
+        }
+        return c;
+      };
+      const auto bytes_of = [&](const Slice &c, int half) {
+        if (MODE == kWgrad)
+          return uint32_t(PLANES) * (kPTile + uint32_t(by_row ? (c.cnt + 15) / 16 * 2048 * qblocks
+                                                             : qblocks * 8192));
+        return PLANES * ((p.e_mn ? 2 * S::kRankSlice * 128 : kPTile) +
+                         uint32_t((held(half) + S::kBox - 1) / S::kBox * (S::kBox * 128)));
+      };
+      const auto patch_of = [&](const Slice &c, int half) {
+        if (MODE == kWgrad) return c.cnt < kBK;
+        const int q = tile.q0 + half * hr;
+        return MODE == kLora && c.ext && held(half) > 0 && (c.lo > q || c.hi < q + held(half));
+      };
+      // A slice that slice_at describes as ordinary in every respect.
+      const auto is_plain = [&](int s) {
+        if (MODE == kWgrad) return (s + 1) * kBK <= tile.klen;
+        return MODE == kForward || s < nbase;
+      };
+      const auto full_at = [&](int stage) {
+        const uint32_t bar = bar_full + 8 * stage;
+        return CG == 2 ? map_rank(bar, 0) : bar;
+      };
+      const auto expect = [&](int stage, uint32_t bytes) {
+        mbar_expect(bar_full + 8 * stage, bytes + (dropped ? 16 : 0));
+        dropped = false;
+      };
+      // Copies of P, and of Q as tiles, of one slice (one thread).
+      const auto copy_p = [&](const Slice &c, uint32_t st, uint32_t bar) {
+        if (MODE == kWgrad) {
+#pragma unroll
+          for (int i = 0; i < 2 * PLANES; ++i)
+            tma_2d<CG>(st + i * 8192, &map_p, n0 + (i & 1) * 64, c.k0 + (i >> 1) * p.rows, bar);
+        } else if (MODE == kLora && c.ext) {
+          if (p.e_mn) {
+#pragma unroll
+            for (int i = 0; i < 2 * PLANES; ++i)
+              tma_3d<CG>(st + i * 8192, &map_e, n0 + (i & 1) * 64, c.rank0,
+                         c.g + (i >> 1) * c.gcount, bar);
+          } else {
+#pragma unroll
+            for (int i = 0; i < PLANES; ++i)
+              tma_3d<CG>(st + i * kPTile, &map_e, c.rank0, n0, c.g + i * c.gcount, bar);
           }
+        } else if (p.p_mn) {
+#pragma unroll
+          for (int i = 0; i < 2 * PLANES; ++i)
+            tma_3d<CG>(st + i * 8192, &map_p, n0 + (i & 1) * 64, c.k0, pg + (i >> 1) * pcount, bar);
+        } else {
+#pragma unroll
+          for (int i = 0; i < PLANES; ++i)
+            tma_3d<CG>(st + i * kPTile, &map_p, c.k0, n0, pg + i * pcount, bar);
         }
       };
+      const auto copy_q = [&](const Slice &c, uint32_t sq, uint32_t bar) {
+        if (MODE == kWgrad) {
+          for (int pl = 0; pl < PLANES; ++pl)
+            for (int b = 0; b < qblocks; ++b)
+              tma_2d<CG>(sq + pl * S::kQTile + b * 8192, &map_q, qf + b * 64, c.k0 + pl * p.q_rows,
+                         bar);
+        } else if (MODE == kLora && c.ext) {
+          for (int pl = 0; pl < PLANES; ++pl)
+            for (int b = 0; b < boxes; ++b)
+              tma_2d<CG>(sq + pl * S::kQTile + b * (S::kBox * 128), &map_u, c.k0,
+                         qf + b * S::kBox + pl * p.rows, bar);
+        } else if (CG == 2 && mine * CG == p.tile_n) {
+          // A full tile: one copy a plane.
+#pragma unroll
+          for (int pl = 0; pl < PLANES; ++pl)
+            tma_2d<CG>(sq + pl * S::kQTile, &map_qr, c.k0, qf + pl * p.q_rows, bar);
+        } else {
+          for (int pl = 0; pl < PLANES; ++pl)
+            for (int b = 0; b < boxes; ++b)
+              tma_2d<CG>(sq + pl * S::kQTile + b * (S::kBox * 128), &map_q, c.k0,
+                         qf + b * S::kBox + pl * p.q_rows, bar);
+        }
+      };
+      // The expectations of one slice (one thread, before or while its copies arrive).
+      const auto announce = [&](const Slice &c, int stage) {
+        const bool patch = patch_of(c, half_rank);
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int h = 0; h < CG; ++h)
+          if (!patch_of(c, h)) bytes += bytes_of(c, h);
+        if (patch) mbar_expect(bar_patch + 8 * stage, bytes_of(c, half_rank));
+        if (leader) {
+          if (!patch) expect(stage, bytes);
+          else if (bytes) mbar_expect_only(bar_full + 8 * stage, bytes);
+        } else if (!patch) {
+          mbar_arrive_relaxed(full_at(stage));
+        }
+        if (leader && patch && dropped) {
+          mbar_expect_only(bar_full + 8 * stage, 16);
+          dropped = false;
+        }
+      };
+      // Zeroes a slice's rows that do not count, once its copies are here (a whole warp).
+      const auto patch_rows = [&](const Slice &c, int stage, uint32_t parity) {
+        const uint32_t st = base + stage * S::kStage, sq = st + PLANES * kPTile;
+        const bool ok = mbar_wait(bar_patch + 8 * stage, parity, p.wait_limit_ns);
+        if (!__all_sync(~0u, ok)) return false;
+        if (MODE == kWgrad) {
+          // Rows [cnt, the next multiple of 16): past the group's end.
+          const int n = 8 * (((c.cnt + 15) & ~15) - c.cnt);
+          for (int i = lane; i < n; i += 32) {
+            const uint32_t at = uint32_t(c.cnt * 128 + i * 16);
+            for (int b = 0; b < 2 * PLANES; ++b) zero16(st + b * 8192 + at);
+            for (int pl = 0; pl < PLANES; ++pl)
+              for (int b = 0; b < qblocks; ++b) zero16(sq + pl * S::kQTile + b * 8192 + at);
+          }
+        } else {
+          // Rows of u of other adapters.
+          for (int i = lane; i < 8 * mine; i += 32) {
+            const int at = qf + (i >> 3);
+            if (at < c.lo || at >= c.hi)
+              for (int pl = 0; pl < PLANES; ++pl) zero16(sq + pl * S::kQTile + i * 16);
+          }
+        }
+        proxy_fence();
+        __syncwarp();
+        if (elect_one()) mbar_arrive(full_at(stage));
+        __syncwarp();
+        return true;
+      };
 
-      for (int s = s0; s < s1 && !timed_out; ++s, ++r) {
-        const uint32_t st_i = r % S::kStages;
-        if (r >= S::kStages) {
-          const bool ok =
-              mbar_wait(bar_empty + 8 * st_i, ((r / S::kStages) - 1) & 1u, p.wait_limit_ns);
+      if (!by_row) {
+        // Warp 0 copies P, warp 1 copies Q, one thread each; warps 2 and 3 zero rows in turn.
+        if (warp < 2) {
+          if (elect_one()) {
+            for (int s = s0; s < s1; ++s) {
+              const uint32_t st = base + ring.stage * S::kStage;
+              if (!mbar_wait(bar_empty + 8 * ring.stage, ring.parity ^ 1u, p.wait_limit_ns)) {
+                timed_out = true;
+                break;
+              }
+              if (is_plain(s)) {
+                const Slice c = {false, MODE == kWgrad ? tile.k0 + s * kBK : s * kBK, 0, 0, 0, 0, 0,
+                                 kBK};
+                const uint32_t full = full_at(ring.stage);
+                if (warp == 0) {
+                  if (leader) expect(ring.stage, usual);
+                  copy_p(c, st, full);
+                  if (MODE != kForward && !leader) mbar_arrive_relaxed(full);
+                } else {
+                  copy_q(c, st + PLANES * kPTile, full);
+                }
+              } else {
+                const Slice c = slice_at(s);
+                const uint32_t bar =
+                    patch_of(c, half_rank) ? bar_patch + 8 * ring.stage : full_at(ring.stage);
+                if (warp == 0) {
+                  announce(c, ring.stage);
+                  copy_p(c, st, bar);
+                } else {
+                  copy_q(c, st + PLANES * kPTile, bar);
+                }
+              }
+              ring.template next<S::kStages>();
+            }
+          }
+          __syncwarp();
+          timed_out = __any_sync(~0u, timed_out);
+        } else if (MODE != kForward) {
+          Ring at = ring;
+          int s = s0;
+          if (MODE == kLora && nbase > s0) s = min(nbase, s1);
+          if (MODE == kWgrad && s1 > s0) s = is_plain(s1 - 1) ? s1 : s1 - 1;
+          at.template skip<S::kStages>(s - s0);
+          for (int turn = 0; s < s1 && !timed_out; ++s, ++turn) {
+            const Slice c = slice_at(s);
+            if (patch_of(c, half_rank)) {
+              const uint32_t parity = (patched >> at.stage) & 1u;
+              patched ^= 1u << at.stage;
+              if (warp == 2 + (turn & 1)) timed_out = !patch_rows(c, at.stage, parity);
+            }
+            at.template next<S::kStages>();
+          }
+          ring.template skip<S::kStages>(s1 - s0);
+        }
+      } else {
+        // Rows by number, four to a copy (single blocks): warp w issues fours w, w + 4, ...; lane
+        // l looks up row l % 4 of the warp's four l / 4; -1 is a row of zeros.  (Such a copy takes
+        // the copy engine about 40 cycles.  The 16 of a slice of 64 columns keep up with the
+        // memory; the 32 of a pair's slice, whose products take 512 cycles, do not: there the
+        // rows are gathered by a kernel first.  16384 rows x 4096 x 4096: 620 us by number, 331
+        // us + 40 us gathered.  cp.async by the copy warps, counted by a barrier: 758 us.)
+        const int row_in_slice = 4 * (warp + kCopyWarps * (lane >> 2)) + (lane & 3);
+        const auto row_of = [&](int at, int limit) {
+          if (at >= limit) return -1;
+          const int row = p.row_index[at];
+          return row >= 0 && row < p.q_rows ? row : -1;
+        };
+        int next = -1;      // gradient: this lane's row of the next slice
+        if (MODE != kWgrad) {
+          __syncwarp();
+          my_rows[lane] = row_of(qf + row_in_slice, tile.q0 + tile.qn);
+          __syncwarp();
+        } else if (s0 < s1 && lane < 16) {
+          next = row_of(tile.k0 + s0 * kBK + row_in_slice, tile.k0 + tile.klen);
+        }
+        for (int s = s0; s < s1 && !timed_out; ++s) {
+          const uint32_t st = base + ring.stage * S::kStage, sq = st + PLANES * kPTile;
+          const bool ok = mbar_wait(bar_empty + 8 * ring.stage, ring.parity ^ 1u, p.wait_limit_ns);
           if (!__all_sync(~0u, ok)) {
             timed_out = true;
             break;
           }
-        }
-        const uint32_t st = base + st_i * S::kStage;
-        const uint32_t sq = st + PLANES * kPTile;
-        const uint32_t full_local = bar_full + 8 * st_i;
-        const uint32_t full = CG == 2 ? map_rank(full_local, 0) : full_local;
-
-        // What this slice is: rows [z0, z1) of its tiles count, the others have to be zeros.
-        const bool ext = MODE == kLora && s >= nbase;
-        int k0 = s * kBK, g = pg, gcount = pcount, lo = 0, hi = 0, rank0 = 0;
-        int cnt = kBK;
-        if (MODE == kWgrad) {
-          k0 += tile.k0;
-          cnt = min(kBK, tile.klen - s * kBK);
-        } else if (ext) {
-          const int e = (s - nbase) / per_rank;
-          const int j = s - nbase - e * per_rank;
-          k0 = j * kBK;                    // of u
-          rank0 = j * S::kRankSlice;       // of b
-          g = p.e_shared ? 0 : tab.gid[tile.e0 + e];
-          gcount = p.e_shared ? 1 : p.groups;
-          lo = tab.row[tile.e0 + e];
-          hi = tab.row[tile.e0 + e + 1];
-        }
-        const int qblocks = hr / 64;
-        // Bytes that the copies of a block bring (gradient, adapters' part), and whether rows of
-        // zeros follow them.
-        const auto bytes_of = [&](int half) {
-          if (MODE == kWgrad)
-            return uint32_t(PLANES) * (kPTile + uint32_t(by_row ? (cnt + 15) / 16 * 2048 * qblocks
-                                                               : qblocks * 8192));
-          return PLANES * ((p.e_mn ? 2 * S::kRankSlice * 128 : kPTile) +
-                           uint32_t((held(half) + S::kBox - 1) / S::kBox * (S::kBox * 128)));
-        };
-        const auto patch_of = [&](int half) {
-          if (MODE == kWgrad) return cnt < kBK;
-          const int q = tile.q0 + half * hr;
-          return ext && held(half) > 0 && (lo > q || hi < q + held(half));
-        };
-        const bool patch = MODE != kForward && patch_of(half_rank);
-        const uint32_t bar = patch ? bar_patch + 8 * st_i : full;
-        if (warp == 0 && elect_one()) {
-          uint32_t bytes = usual;
-          if (MODE == kWgrad || ext) {
-            bytes = 0;
-#pragma unroll
-            for (int h = 0; h < CG; ++h)
-              if (!patch_of(h)) bytes += bytes_of(h);
+          const Slice c = slice_at(s);
+          const bool patch = patch_of(c, 0);
+          const uint32_t bar = patch ? bar_patch + 8 * ring.stage : bar_full + 8 * ring.stage;
+          if (warp == 0 && elect_one()) {
+            if (is_plain(s) && MODE != kWgrad) expect(ring.stage, usual);
+            else announce(c, ring.stage);
+            copy_p(c, st, bar);
           }
-          if (int(blockIdx.x) == p.drop_block && r == 0) bytes += 16;
-          if (patch) mbar_expect(bar, bytes_of(half_rank));
-          if (leader && !patch) mbar_expect(full_local, bytes);
-          if (leader && patch && bytes) mbar_expect_only(full_local, bytes);
-          if (MODE == kWgrad) {
-#pragma unroll
-            for (int i = 0; i < 2 * PLANES; ++i)
-              tma_2d<CG>(st + i * 8192, &map_p, n0 + (i & 1) * 64, k0 + (i >> 1) * p.rows, bar);
-          } else if (ext) {
-            if (p.e_mn) {
-#pragma unroll
-              for (int i = 0; i < 2 * PLANES; ++i)
-                tma_3d<CG>(st + i * 8192, &map_e, n0 + (i & 1) * 64, rank0, g + (i >> 1) * gcount,
-                           bar);
-            } else {
-#pragma unroll
-              for (int i = 0; i < PLANES; ++i)
-                tma_3d<CG>(st + i * kPTile, &map_e, rank0, n0, g + i * gcount, bar);
-            }
-          } else if (p.p_mn) {
-#pragma unroll
-            for (int i = 0; i < 2 * PLANES; ++i)
-              tma_3d<CG>(st + i * 8192, &map_p, n0 + (i & 1) * 64, k0, g + (i >> 1) * gcount, bar);
+          dropped = false;
+          __syncwarp();
+          if (c.ext) {
+            if (warp == 1 && elect_one()) copy_q(c, sq, bar);
           } else {
-#pragma unroll
-            for (int i = 0; i < PLANES; ++i)
-              tma_3d<CG>(st + i * kPTile, &map_p, k0, n0, g + i * gcount, bar);
-          }
-          if (MODE != kForward && !leader && !patch) mbar_arrive_relaxed(full);
-        }
-        if (warp == 1 && (!by_row || ext) && elect_one()) {
-          if (MODE == kWgrad) {
-            for (int pl = 0; pl < PLANES; ++pl)
-              for (int b = 0; b < qblocks; ++b)
-                tma_2d<CG>(sq + pl * S::kQTile + b * 8192, &map_q, qf + b * 64, k0 + pl * p.q_rows,
-                           bar);
-          } else if (CG == 2 && mine == S::kBN / CG && !ext) {
-            // A full tile: one copy a plane.
-            for (int pl = 0; pl < PLANES; ++pl)
-              tma_2d<CG>(sq + pl * S::kQTile, &map_qr, k0, qf + pl * p.q_rows, bar);
-          } else {
-            const CUtensorMap *map = ext ? &map_u : &map_q;
-            const int rows = ext ? p.rows : p.q_rows;
-            for (int pl = 0; pl < PLANES; ++pl)
-              for (int b = 0; b < boxes; ++b)
-                tma_2d<CG>(sq + pl * S::kQTile + b * (S::kBox * 128), map, k0,
-                           qf + b * S::kBox + pl * rows, bar);
-          }
-        }
-        __syncwarp();
-        if (by_row && !ext) {
-          if (MODE == kWgrad) {
-            __syncwarp();
-            if (lane < 16) my_rows[lane] = next;
-            __syncwarp();
-            if (s + 1 < s1 && lane < 16)
-              next = row_of(k0 + kBK + row_in_slice, tile.k0 + tile.klen);
-          }
-          if (elect_one())
-            copy_rows(sq, MODE == kWgrad ? (cnt + 15) / 16 * 4 : (mine + 3) / 4,
-                      MODE == kWgrad ? qblocks : 1, MODE == kWgrad ? qf : k0, bar);
-        }
-        __syncwarp();
-        if (patch) {
-          // Rows of zeros, once the copies are here, by one of the two warps that have little
-          // else to do; then this block's word to the products.
-          const uint32_t parity = (patched >> st_i) & 1u;
-          patched ^= 1u << st_i;
-          if (warp == 2 + int(r & 1)) {
-            const bool ok = mbar_wait(bar_patch + 8 * st_i, parity, p.wait_limit_ns);
-            if (!__all_sync(~0u, ok)) {
-              timed_out = true;
-              break;
-            }
             if (MODE == kWgrad) {
-              // Rows [cnt, the next multiple of 16): past the group's end.
-              const int n = 8 * (((cnt + 15) & ~15) - cnt);
-              for (int i = lane; i < n; i += 32) {
-                const uint32_t at = uint32_t(cnt * 128 + i * 16);
-                for (int b = 0; b < 2 * PLANES; ++b) zero16(st + b * 8192 + at);
-                for (int pl = 0; pl < PLANES; ++pl)
-                  for (int b = 0; b < qblocks; ++b) zero16(sq + pl * S::kQTile + b * 8192 + at);
-              }
-            } else {
-              // Rows of u of other adapters.
-              for (int i = lane; i < 8 * mine; i += 32) {
-                const int at = qf + (i >> 3);
-                if (at < lo || at >= hi)
-                  for (int pl = 0; pl < PLANES; ++pl) zero16(sq + pl * S::kQTile + i * 16);
+              if (lane < 16) my_rows[lane] = next;
+              __syncwarp();
+              if (s + 1 < s1 && lane < 16)
+                next = row_of(c.k0 + kBK + row_in_slice, tile.k0 + tile.klen);
+            }
+            if (elect_one()) {
+              const int fours = MODE == kWgrad ? (c.cnt + 15) / 16 * 4 : (mine + 3) / 4;
+              const int x = MODE == kWgrad ? qf : c.k0;
+              for (int f = warp, k = 0; f < fours; f += kCopyWarps, ++k) {
+                const int4 v = *reinterpret_cast<const int4 *>(my_rows + 4 * k);
+#pragma unroll
+                for (int pl = 0; pl < PLANES; ++pl) {
+                  const int out = PLANES * p.q_rows, add = pl * p.q_rows;
+                  const int y[4] = {v.x < 0 ? out : v.x + add, v.y < 0 ? out : v.y + add,
+                                    v.z < 0 ? out : v.z + add, v.w < 0 ? out : v.w + add};
+                  for (int b = 0; b < (MODE == kWgrad ? qblocks : 1); ++b)
+                    tma_rows4(sq + pl * S::kQTile + b * 8192 + f * 512, &map_qr, x + b * 64, y, bar);
+                }
               }
             }
-            proxy_fence();
-            __syncwarp();
-            if (elect_one()) mbar_arrive(full);
-            __syncwarp();
           }
+          __syncwarp();
+          if (patch) {
+            const uint32_t parity = (patched >> ring.stage) & 1u;
+            patched ^= 1u << ring.stage;
+            if (warp == 2 + (s & 1)) timed_out = !patch_rows(c, ring.stage, parity);
+          }
+          ring.template next<S::kStages>();
         }
       }
     } else if (warp == kMmaWarp) {
-      // ---- products ----
-      if (leader) {
+      // ---- products ---- (one thread)
+      if (leader && elect_one()) {
         const uint32_t sizes = (uint32_t(tile.bn >> 3) << 17) | (uint32_t(128 * CG >> 4) << 24) |
-                               (MODE == kWgrad ? 1u << 16 : 0u);
+                               (MODE == kWgrad ? 1u << 16 : 0u) | p.idesc;
+        const bool base_mn = MODE == kWgrad || p.p_mn;
+        const uint32_t qstep = MODE == kWgrad ? 128 : 2;      // 16 values of K, in 16 bytes
         const int n = s1 - s0;
-        for (int i = 0; i < n && !timed_out; ++i, ++r) {
+        for (int i = 0; i < n; ++i) {
           const int s = s0 + i;
           const bool first = PLANES == 3 ? i % kChunk == 0 : i == 0;
-          bool ok = true;
           if (first) {
-            if (q >= 2)
-              ok = mbar_wait(bar_tempty + 8 * (q & 1), ((q >> 1) - 1) & 1u, p.wait_limit_ns);
+            if (q >= 2 && !mbar_wait(bar_tempty + 8 * (q & 1), ((q >> 1) - 1) & 1u,
+                                     p.wait_limit_ns)) {
+              timed_out = true;
+              break;
+            }
             ++q;
           }
           const uint32_t buf = (q - 1) & 1;
-          const uint32_t st_i = r % S::kStages;
-          ok = ok && mbar_wait(bar_full + 8 * st_i, (r / S::kStages) & 1u, p.wait_limit_ns);
-          if (!__all_sync(~0u, ok)) {
+          if (!mbar_wait(bar_full + 8 * ring.stage, ring.parity, p.wait_limit_ns)) {
             timed_out = true;
             break;
           }
           tc_fence_after();
           const bool ext = MODE == kLora && s >= nbase;
+          const bool pmn = ext ? p.e_mn : base_mn;
+          const uint32_t idesc = sizes | (pmn ? 1u << 15 : 0u);
+          const uint32_t st = base + ring.stage * S::kStage;
+          const uint64_t dp = tile_desc(st, pmn);
+          const uint64_t dq = tile_desc(st + PLANES * kPTile, MODE == kWgrad);
+          const uint32_t pstep = pmn ? 128 : 2;
+          const uint32_t d = tmem + buf * S::kBN;
           const int left = ext ? min(S::kRankSlice, p.rank - (s - nbase) % per_rank * S::kRankSlice)
                                : min(kBK, tile.klen - s * kBK);
           const int steps = (left + 15) / 16;
-          const bool pmn = MODE == kWgrad || (ext ? p.e_mn : p.p_mn);
-          const uint32_t idesc = p.idesc | sizes | (pmn ? 1u << 15 : 0u);
-          const uint32_t st = base + st_i * S::kStage;
-          const uint64_t dp = tile_desc(st, pmn);
-          const uint64_t dq = tile_desc(st + PLANES * kPTile, MODE == kWgrad);
-          const uint32_t pstep = pmn ? 128 : 2, qstep = MODE == kWgrad ? 128 : 2;   // 16 bytes
-          const uint32_t d = tmem + buf * S::kBN;
-          if (elect_one()) {
-            if (PLANES == 1 && MODE == kLora && ext) {
-              // b[g] times u's hi, and times its lo, 32 columns on.
-              for (int k = 0; k < steps; ++k) {
-                const uint64_t a = dp + k * pstep, b = dq + k * qstep;
-                mma<CG>(d, a, b, idesc, !(first && k == 0));
-                mma<CG>(d, a, b + 2 * qstep, idesc, true);
-              }
-            } else {
+          if (PLANES == 1 && MODE == kLora && ext) {
+            // b[g] times u's hi, and times its lo, 32 columns on.
+            for (int k = 0; k < steps; ++k) {
+              const uint64_t a = dp + k * pstep, b = dq + k * qstep;
+              mma<CG>(d, a, b, idesc, !(first && k == 0));
+              mma<CG>(d, a, b + 2 * qstep, idesc, true);
+            }
+          } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if (k >= steps) break;
-                const uint64_t a = dp + k * pstep, b = dq + k * qstep;
-                mma<CG>(d, a, b, idesc, !(first && k == 0));
-                if constexpr (PLANES == 3) {
-                  constexpr uint64_t pa = kPTile >> 4, qa = S::kQTile >> 4;
-                  const uint32_t ds = tmem + (2 + (done & 1)) * S::kBN;
-                  mma<CG>(ds, a + 2 * pa, b, idesc, !(i == 0 && k == 0));
-                  mma<CG>(ds, a, b + 2 * qa, idesc, true);
-                  mma<CG>(ds, a + pa, b + qa, idesc, true);
-                  mma<CG>(ds, a + pa, b, idesc, true);
-                  mma<CG>(ds, a, b + qa, idesc, true);
-                }
+            for (int k = 0; k < 4; ++k) {
+              if (k >= steps) break;
+              const uint64_t a = dp + k * pstep, b = dq + k * qstep;
+              mma<CG>(d, a, b, idesc, !(first && k == 0));
+              if constexpr (PLANES == 3) {
+                constexpr uint64_t pa = kPTile >> 4, qa = S::kQTile >> 4;
+                const uint32_t ds = tmem + (2 + (done & 1)) * S::kBN;
+                mma<CG>(ds, a + 2 * pa, b, idesc, !(i == 0 && k == 0));
+                mma<CG>(ds, a, b + 2 * qa, idesc, true);
+                mma<CG>(ds, a + pa, b + qa, idesc, true);
+                mma<CG>(ds, a + pa, b, idesc, true);
+                mma<CG>(ds, a, b + qa, idesc, true);
               }
             }
-            mma_commit<CG>(bar_empty + 8 * st_i, true);
-            if (i == n - 1 || (PLANES == 3 && i % kChunk == kChunk - 1))
-              mma_commit<CG>(bar_tfull + 8 * buf, true);
           }
-          __syncwarp();
+          mma_commit<CG>(bar_empty + 8 * ring.stage, true);
+          if (i == n - 1 || (PLANES == 3 && i % kChunk == kChunk - 1))
+            mma_commit<CG>(bar_tfull + 8 * buf, true);
+          ring.template next<S::kStages>();
         }
         if (n > 0) ++done;
       }
+      __syncwarp();
+      timed_out = __any_sync(~0u, timed_out);
     } else {
       // ---- results ----
       const int quarter = warp & 3, half = (warp - kEpi0) >> 2;
@@ -1112,14 +1250,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     }
   }
 
-  if (warp == 0 && timed_out && leader && lane == 0) {
-    // Let the copies in flight land before the block goes away (the leader's barriers count
-    // both blocks' copies).
-    for (uint32_t i = r > S::kStages ? r - S::kStages : 0; i < r; ++i)
-      mbar_wait(bar_full + 8 * (i % S::kStages), (i / S::kStages) & 1u, p.wait_limit_ns);
-  }
-  if (warp == 0 && timed_out) {
-    // And those counted by other barriers: a copy that was issued lands within microseconds.
+  if (warp < kCopyWarps && timed_out) {
+    // Let the copies in flight land before the block goes away: one that was issued does within
+    // microseconds.
     const uint64_t t0 = timer_ns();
     while (timer_ns() - t0 < 1000 * 1000) {
     }
@@ -1159,6 +1292,7 @@ __global__ void planes_kernel(const void *__restrict__ src, int64_t count, int64
                               int64_t cols, int64_t ld, int64_t stride, int vec,
                               const int *__restrict__ offsets, const int *__restrict__ index,
                               int64_t src_rows, uint16_t *__restrict__ dst, int64_t ld8) {
+  grid_wait();
   const int64_t per_row = ld8 / 8;
   const int64_t total = rows * per_row;
   const int64_t plane = count * rows * ld8;
@@ -1221,6 +1355,14 @@ __global__ void planes_kernel(const void *__restrict__ src, int64_t count, int64
 std::atomic<int64_t> g_wait_limit_ns{int64_t(10) * 1000 * 1000 * 1000};
 std::atomic<int> g_drop_block{-1};
 
+// The launch may begin its prologue while the one before it in the stream ends (grid_wait).
+cudaLaunchAttribute overlap_attribute() {
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+
 int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
 
 // Whether the copy engine can read the matrices in place: 16-bit values, rows and matrices on
@@ -1278,14 +1420,18 @@ cudaError_t make_planes(const Stack &s, int dtype, const int32_t *offsets, char 
                   (s.count == 1 || s.stride * size % 16 == 0);
   if (s.count == 1) offsets = nullptr;      // one matrix may serve every group
   if (gathered == 0) index = nullptr;
-  if (dtype == TMM_F32)
-    planes_kernel<true><<<grid, 256, 0, stream>>>(s.data, s.count, rows, s.cols, s.ld, s.stride,
-                                                  vec, offsets, index, s.rows, dst, ld8);
-  else
-    planes_kernel<false><<<grid, 256, 0, stream>>>(s.data, s.count, rows, s.cols, s.ld, s.stride,
-                                                   vec, offsets, index, s.rows, dst, ld8);
   *out = {dst, planes * s.count, rows, s.cols, ld8, rows * ld8};
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  attr[0] = overlap_attribute();
+  return cudaLaunchKernelEx(&cfg, dtype == TMM_F32 ? planes_kernel<true> : planes_kernel<false>,
+                            s.data, s.count, rows, s.cols, s.ld, s.stride, vec, offsets, index,
+                            s.rows, dst, ld8);
 }
 
 // Maps of an operand: tiles of `box_rows` rows x 64 values in matrix z, or of the rows of all
@@ -1325,13 +1471,14 @@ cudaError_t launch_shape(const Maps &m, Params &prm, int64_t tiles, const Device
   }
   const int cluster = CG == 2 ? 2 : prm.ksplit;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1] = overlap_attribute();
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = unsigned(cluster);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = stream;
@@ -1382,8 +1529,10 @@ int split_of(int64_t tiles, int64_t slices, const DeviceInfo &dev) {
   return s;
 }
 
-// Pairs from 64 rows per group on average.
-int forward_shape(int64_t rows, int64_t groups) { return rows > 64 * groups ? 2 : 1; }
+// Pairs from 64 rows per group on average, if their 256 lanes have something to hold.
+int forward_shape(int64_t rows, int64_t groups, int64_t N) {
+  return rows > 64 * groups && N > 128 ? 2 : 1;
+}
 int lora_shape(int64_t rows) { return rows > 64 ? 2 : 1; }
 int wgrad_shape(int64_t N) { return N > 128 ? 2 : 1; }
 
@@ -1405,8 +1554,9 @@ cudaError_t q_maps(Maps *m, const Planes &x, const int32_t *index, int cg, int b
 cudaError_t run_forward(const Planes &x, const int32_t *index, const Planes &w, bool shared_w,
                         bool trans_w, int planes, Params prm, const DeviceInfo &dev,
                         cudaStream_t stream) {
-  const int cg = forward_shape(prm.rows, prm.groups);
+  const int cg = forward_shape(prm.rows, prm.groups, prm.N);
   const int bn = columns_of(cg, planes);
+  prm.tile_n = bn;
   prm.panels = int((prm.N + 128 * cg - 1) / (128 * cg));
   const int64_t tiles =
       prm.panels * (std::min<int64_t>(prm.groups, prm.rows) + prm.rows / bn);
@@ -1436,7 +1586,7 @@ static int64_t gathered_rows(int cg, const int32_t *row_index, int64_t rows) {
 
 size_t grouped_workspace_bytes(const GroupedProblem &p) {
   const int64_t gathered =
-      gathered_rows(forward_shape(p.rows, p.groups), p.row_index, p.rows);
+      gathered_rows(forward_shape(p.rows, p.groups, p.N), p.row_index, p.rows);
   return add_sizes({plane_bytes(p.x, p.dtype, gathered), plane_bytes(p.w, p.dtype)});
 }
 
@@ -1445,7 +1595,7 @@ cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void 
   char *ws = static_cast<char *>(workspace);
   const bool shared = p.groups > 1 && p.w.count == 1;
   const int64_t gathered =
-      gathered_rows(forward_shape(p.rows, p.groups), p.row_index, p.rows);
+      gathered_rows(forward_shape(p.rows, p.groups, p.N), p.row_index, p.rows);
   Planes x, w;
   cudaError_t e;
   if ((e = make_planes(p.x, p.dtype, nullptr, &ws, dev, stream, &x, gathered, p.row_index)) !=
@@ -1463,6 +1613,7 @@ cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void 
   prm.out = p.y;
   prm.ld_out = p.ldy;
   prm.out_type = out_type(p.dtype);
+  prm.zero_rows = 1;
   return run_forward(x, gathered ? nullptr : p.row_index, w, shared, p.trans_w != 0, planes, prm,
                      dev, stream);
 }
@@ -1502,6 +1653,7 @@ cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *wor
   prm.n_out = prm.N;
   prm.ksplit = 1;
   const int bn = columns_of(cg, planes);
+  prm.tile_n = bn;
   prm.panels = int((p.N + 128 * cg - 1) / (128 * cg));
   const int64_t tiles = p.groups * prm.panels * ((p.K + bn - 1) / bn);
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
@@ -1575,6 +1727,7 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   prm.q_rows = int(x.rows);
   prm.out_rows = int(p.rows);
   prm.rank = int(p.rank);
+  prm.tile_n = bn;
   prm.panels = int((p.N + 128 * cg - 1) / (128 * cg));
   const int64_t tiles = prm.panels * ((p.rows + bn - 1) / bn);
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
