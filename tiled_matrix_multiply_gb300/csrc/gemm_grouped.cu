@@ -172,7 +172,9 @@ __device__ __forceinline__ void mbar_arrive(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
-// The same where no access of this thread has to be ordered before it.
+// The same where no access to memory of this thread has to be ordered before it.  (A release
+// waits for the thread's stores: result warps handing tensor memory back, whose reads have
+// completed, would wait for their results to reach memory.)
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
@@ -949,7 +951,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       };
 
       if (!by_row) {
-        // Warp 0 copies P, warp 1 copies Q, one thread each; warps 2 and 3 zero rows in turn.
+        // Warp 0 copies P, warp 1 copies Q, one thread each; warps 2 and 3 zero rows, of even and
+        // odd stages.  They do not wait for a stage to be free, so all uses of a stage have to be
+        // the same warp's: only then is the parity it waits for never that of a round before.
         if (warp < 2) {
           if (elect_one()) {
             for (int s = s0; s < s1; ++s) {
@@ -991,12 +995,12 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           if (MODE == kLora && nbase > s0) s = min(nbase, s1);
           if (MODE == kWgrad && s1 > s0) s = is_plain(s1 - 1) ? s1 : s1 - 1;
           at.template skip<S::kStages>(s - s0);
-          for (int turn = 0; s < s1 && !timed_out; ++s, ++turn) {
+          for (; s < s1 && !timed_out; ++s) {
             const Slice c = slice_at(s);
             if (patch_of(c, half_rank)) {
               const uint32_t parity = (patched >> at.stage) & 1u;
               patched ^= 1u << at.stage;
-              if (warp == 2 + (turn & 1)) timed_out = !patch_rows(c, at.stage, parity);
+              if (warp == 2 + (at.stage & 1)) timed_out = !patch_rows(c, at.stage, parity);
             }
             at.template next<S::kStages>();
           }
@@ -1069,7 +1073,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           if (patch) {
             const uint32_t parity = (patched >> ring.stage) & 1u;
             patched ^= 1u << ring.stage;
-            if (warp == 2 + (s & 1)) timed_out = !patch_rows(c, ring.stage, parity);
+            if (warp == 2 + (ring.stage & 1)) timed_out = !patch_rows(c, ring.stage, parity);
           }
           ring.template next<S::kStages>();
         }
@@ -1181,7 +1185,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(tempty + 8 * buf);
+          if (lane == 0) mbar_arrive_relaxed(tempty + 8 * buf);
         }
       } else {
         float acc[kBlocks][16];
@@ -1215,7 +1219,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(tempty + 8 * buf);
+          if (lane == 0) mbar_arrive_relaxed(tempty + 8 * buf);
         }
         if (n > 0) ++done;
         if (!timed_out) {
