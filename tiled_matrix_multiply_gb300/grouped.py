@@ -36,15 +36,6 @@ class RowGroups(NamedTuple):
     position: object    # (slots): the place of each slot
 
 
-def _dtype_code(x, name):
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    code = _CODES.get(x.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {x.dtype}")
-    return code
-
-
 def _operand(x, name, like, dims, transposable=False):
     """(rows, cols, ld, stride, trans) of a matrix or a stack of matrices (dims = 3).
 
@@ -53,21 +44,29 @@ def _operand(x, name, like, dims, transposable=False):
     """
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    shape = x.shape
-    if len(shape) != dims:
-        raise ValueError(f"{name} must be {dims}-D, got shape {tuple(shape)}")
     if x.dtype != like.dtype:
         raise TypeError(f"{name} must be {like.dtype} like the first operand, got {x.dtype}")
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
     if x.get_device() != like.get_device():
         raise ValueError(f"{name} is on {x.device}, the first operand on {like.device}")
-    strides = x.stride()
-    rows, cols = shape[-2], shape[-1]
-    s0, s1 = strides[-2], strides[-1]
-    stride = strides[0] if dims == 3 and shape[0] > 1 else 0
-    if rows == 0 or cols == 0 or (dims == 3 and shape[0] == 0):
-        return rows, cols, max(cols, 1), stride, 0
+    stride = 0
+    if dims == 2:
+        if x.dim() != 2:
+            raise ValueError(f"{name} must be 2-D, got shape {tuple(x.shape)}")
+        rows, cols = x.shape
+        s0, s1 = x.stride()
+    else:
+        if x.dim() != 3:
+            raise ValueError(f"{name} must be 3-D, got shape {tuple(x.shape)}")
+        count, rows, cols = x.shape
+        stride, s0, s1 = x.stride()
+        if count <= 1:
+            stride = 0
+            if count == 0:
+                return rows, cols, cols or 1, 0, 0
+    if s1 == 1 and s0 >= cols:                       # the usual case
+        return rows, cols, s0 or 1, stride, 0
+    if rows == 0 or cols == 0:
+        return rows, cols, cols or 1, stride, 0
     if (s1 == 1 or cols == 1) and (s0 >= cols or rows == 1):
         return rows, cols, max(s0 if rows > 1 else cols, cols), stride, 0
     if transposable and (s0 == 1 or rows == 1) and (s1 >= rows or cols == 1):
@@ -76,14 +75,27 @@ def _operand(x, name, like, dims, transposable=False):
                      + (" or a transposed row-major view" if transposable else ""))
 
 
-def _index_tensor(t, name, like, length):
+def _first(x, name):
+    """The type code of the first operand, a matrix on a GPU."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = _CODES.get(x.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {x.dtype}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return code
+
+
+def _index_ptr(t, name, like, length):
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
         raise TypeError(f"{name} must be an int32 tensor")
-    if not t.is_cuda or t.get_device() != like.get_device():
+    if t.get_device() != like.get_device():
         raise ValueError(f"{name} is on {t.device}, the operands on {like.device}")
     if t.dim() != 1 or (length is not None and t.shape[0] != length) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 1-D tensor"
                          + (f" of {length} values" if length is not None else ""))
+    return t.data_ptr()
 
 
 def _result(given, name, shape, like):
@@ -94,12 +106,9 @@ def _result(given, name, shape, like):
     return given
 
 
-def _workspace(given, need, like):
-    """A workspace of `need` bytes (None: none needed): the given tensor, or a new one (torch's
-    start on 256-byte boundaries at least)."""
-    if given is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
-    if not given.is_cuda or given.get_device() != like.get_device() or not given.is_contiguous():
+def _given_workspace(given, like):
+    if not isinstance(given, torch.Tensor) or given.get_device() != like.get_device() \
+            or not given.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the operands' device")
     return given
 
@@ -112,16 +121,26 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 def _call(name, like, stream, ws, *args):
     """Call the entry point on the operands' device and stream; raise its error."""
     device = like.get_device()
-    s = stream.cuda_stream if stream is not None else _raw_stream(device)
-    tail = (ws.data_ptr(), ws.numel() * ws.element_size(), s) if ws is not None else (0, 0, s)
-    fn = getattr(_abi.load(), name)
+    s = _raw_stream(device) if stream is None else stream.cuda_stream
+    lib = _abi.load()
     if torch.cuda.current_device() == device:
-        rc = fn(*args, *tail)
+        rc = _try(lib, name, ws, s, args)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, *tail)
+            rc = _try(lib, name, ws, s, args)
     if rc != _abi.TMM_OK:
         raise _abi.TmmError(name, rc, _abi.last_error())
+
+
+def _try(lib, name, ws, s, args):
+    if ws is None:
+        return getattr(lib, name)(*args, None, 0, s)
+    return getattr(lib, name)(*args, ws.data_ptr(), ws.numel() * ws.element_size(), s)
+
+
+def _scratch(need, like):
+    """A workspace of `need` bytes, None for 0 (torch's blocks start on 512-byte boundaries)."""
+    return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
 
 
 def group_rows(index, groups, stream=None):
@@ -142,18 +161,16 @@ def group_rows(index, groups, stream=None):
         raise ValueError("index must have at least one column")
     if not 1 <= groups <= _abi.TMM_MAX_GROUPS:
         raise ValueError(f"groups must be between 1 and {_abi.TMM_MAX_GROUPS}, got {groups}")
-    slots = tokens * fan
-    # One allocation; every array starts on a 16-byte boundary.
-    at = (slots + 3) // 4 * 4
-    buf = torch.empty(3 * at + groups + 1, dtype=torch.int32, device=index.device)
-    order, rows, position, offsets = buf.split_with_sizes([at, at, at, groups + 1])
-    if at != slots:
-        order, rows, position = order[:slots], rows[:slots], position[:slots]
-    need = _abi.load().group_rows_workspace_size(tokens, fan, groups)
-    base = buf.data_ptr()
-    _call("group_rows", index, stream, _workspace(None, need, index), tokens, fan, groups,
-          index.data_ptr(), 64 if index.dtype == torch.int64 else 32, base + 12 * at, base,
-          base + 4 * at, base + 8 * at)
+    # (Four allocations: views of one cost three times as much to make.)
+    i32, device, slots = torch.int32, index.device, tokens * fan
+    offsets = torch.empty(groups + 1, dtype=i32, device=device)
+    order = torch.empty(slots, dtype=i32, device=device)
+    rows = torch.empty(slots, dtype=i32, device=device)
+    position = torch.empty(slots, dtype=i32, device=device)
+    ws = _scratch(_abi.load().group_rows_workspace_size(tokens, fan, groups), index)
+    _call("group_rows", index, stream, ws, tokens, fan, groups, index.data_ptr(),
+          64 if index.dtype == torch.int64 else 32, offsets.data_ptr(), order.data_ptr(),
+          rows.data_ptr(), position.data_ptr())
     return RowGroups(offsets, order, rows, position)
 
 
@@ -164,24 +181,29 @@ def gemm_grouped(x, w, offsets, rows=None, y=None, workspace=None, stream=None):
     (groups + 1); rows: int32, the row of x that each p reads (a number outside x reads zeros),
     or None for p itself.  y: (len(rows) or x_rows, N); its rows of no group are zero.
     """
-    code = _dtype_code(x, "x")
+    code = _first(x, "x")
     x_rows, K, ldx, _, _ = _operand(x, "x", x, 2)
     K2, N, ldw, stride_w, trans = _operand(w, "w", x, 3, True)
     groups = w.shape[0]
     if K != K2:
         raise ValueError(f"inner dimensions differ: x is {tuple(x.shape)}, w is {tuple(w.shape)}")
-    _index_tensor(offsets, "offsets", x, groups + 1)
+    offsets_ptr = _index_ptr(offsets, "offsets", x, groups + 1)
     R, rows_ptr = x_rows, 0
     if rows is not None:
-        _index_tensor(rows, "rows", x, None)
-        R, rows_ptr = rows.shape[0], rows.data_ptr()
-    y = _result(y, "y", (R, N), x)
-    ldy = _operand(y, "y", x, 2)[2]
-    x_ptr, w_ptr = x.data_ptr(), w.data_ptr()
-    head = (code, trans, groups, R, N, K, x_ptr, x_rows, ldx)
-    need = _abi.load().gemm_grouped_workspace_size(*head, rows_ptr, w_ptr, ldw, stride_w)
-    workspace = _workspace(workspace, need, x)
-    _call("gemm_grouped", x, stream, workspace, *head, offsets.data_ptr(), rows_ptr, w_ptr, ldw,
+        rows_ptr = _index_ptr(rows, "rows", x, None)
+        R = rows.shape[0]
+    if y is None:
+        y, ldy = torch.empty((R, N), dtype=x.dtype, device=x.device), N or 1
+    else:
+        ldy = _operand(_result(y, "y", (R, N), x), "y", x, 2)[2]
+    w_ptr = w.data_ptr()
+    head = (code, trans, groups, R, N, K, x.data_ptr(), x_rows, ldx)
+    if workspace is None:
+        workspace = _scratch(_abi.load().gemm_grouped_workspace_size(
+            *head, rows_ptr, w_ptr, ldw, stride_w), x)
+    else:
+        _given_workspace(workspace, x)
+    _call("gemm_grouped", x, stream, workspace, *head, offsets_ptr, rows_ptr, w_ptr, ldw,
           stride_w, y.data_ptr(), ldy)
     return y
 
@@ -191,27 +213,29 @@ def gemm_grouped_wgrad(x, dy, offsets, rows=None, dw=None, workspace=None, strea
 
     The gradient of ``gemm_grouped`` with respect to w; x, offsets and rows as there, dy (R, N).
     """
-    code = _dtype_code(x, "x")
+    code = _first(x, "x")
     x_rows, K, ldx, _, _ = _operand(x, "x", x, 2)
     R, N, lddy, _, _ = _operand(dy, "dy", x, 2)
-    _index_tensor(offsets, "offsets", x, None)
+    offsets_ptr = _index_ptr(offsets, "offsets", x, None)
     groups = offsets.shape[0] - 1
     if groups < 1:
         raise ValueError("offsets must have groups + 1 values")
     rows_ptr = 0
     if rows is not None:
-        _index_tensor(rows, "rows", x, R)
-        rows_ptr = rows.data_ptr()
+        rows_ptr = _index_ptr(rows, "rows", x, R)
     elif x_rows != R:
         raise ValueError(f"x has {x_rows} rows, dy {R}")
     dw = _result(dw, "dw", (groups, K, N), x)
     _, _, lddw, stride, _ = _operand(dw, "dw", x, 3)
-    x_ptr, dy_ptr = x.data_ptr(), dy.data_ptr()
-    head = (code, groups, R, N, K, x_ptr, x_rows, ldx)
-    need = _abi.load().gemm_grouped_wgrad_workspace_size(*head, rows_ptr, dy_ptr, lddy)
-    workspace = _workspace(workspace, need, x)
-    _call("gemm_grouped_wgrad", x, stream, workspace, *head, offsets.data_ptr(), rows_ptr, dy_ptr,
-          lddy, dw.data_ptr(), lddw, stride)
+    dy_ptr = dy.data_ptr()
+    head = (code, groups, R, N, K, x.data_ptr(), x_rows, ldx)
+    if workspace is None:
+        workspace = _scratch(_abi.load().gemm_grouped_wgrad_workspace_size(
+            *head, rows_ptr, dy_ptr, lddy), x)
+    else:
+        _given_workspace(workspace, x)
+    _call("gemm_grouped_wgrad", x, stream, workspace, *head, offsets_ptr, rows_ptr, dy_ptr, lddy,
+          dw.data_ptr(), lddw, stride)
     return dw
 
 
@@ -223,7 +247,7 @@ def gemm_lora(x, w, a, b, scale, offsets, rows=None, y=None, workspace=None, str
     ``offsets`` and ``order`` of ``group_rows(index, adapters)``; rows past offsets[-1] have no
     adapter.  rows=None: x is in group order already.
     """
-    code = _dtype_code(x, "x")
+    code = _first(x, "x")
     T, K, ldx, _, _ = _operand(x, "x", x, 2)
     K2, N, ldw, _, tw = _operand(w, "w", x, 2, True)
     K3, r, lda, stride_a, ta = _operand(a, "a", x, 3, True)
@@ -234,19 +258,21 @@ def gemm_lora(x, w, a, b, scale, offsets, rows=None, y=None, workspace=None, str
                          f"a {tuple(a.shape)}, b {tuple(b.shape)}")
     if not isinstance(scale, torch.Tensor) or scale.dtype != torch.float32:
         raise TypeError("scale must be a float32 tensor")
-    if scale.shape != (groups,) or not scale.is_cuda or scale.get_device() != x.get_device() \
+    if scale.dim() != 1 or scale.shape[0] != groups or scale.get_device() != x.get_device() \
             or not scale.is_contiguous():
         raise ValueError(f"scale must be a contiguous tensor of {groups} values on {x.device}")
-    _index_tensor(offsets, "offsets", x, groups + 1)
-    rows_ptr = 0
-    if rows is not None:
-        _index_tensor(rows, "rows", x, T)
-        rows_ptr = rows.data_ptr()
-    y = _result(y, "y", (T, N), x)
-    ldy = _operand(y, "y", x, 2)[2]
+    offsets_ptr = _index_ptr(offsets, "offsets", x, groups + 1)
+    rows_ptr = _index_ptr(rows, "rows", x, T) if rows is not None else 0
+    if y is None:
+        y, ldy = torch.empty((T, N), dtype=x.dtype, device=x.device), N or 1
+    else:
+        ldy = _operand(_result(y, "y", (T, N), x), "y", x, 2)[2]
     head = (code, tw, ta, tb, groups, T, N, K, r, x.data_ptr(), ldx)
     mats = (w.data_ptr(), ldw, a.data_ptr(), lda, stride_a, b.data_ptr(), ldb, stride_b)
-    need = _abi.load().gemm_lora_workspace_size(*head, rows_ptr, *mats)
-    _call("gemm_lora", x, stream, _workspace(workspace, need, x), *head, offsets.data_ptr(),
-          rows_ptr, *mats, scale.data_ptr(), y.data_ptr(), ldy)
+    if workspace is None:
+        workspace = _scratch(_abi.load().gemm_lora_workspace_size(*head, rows_ptr, *mats), x)
+    else:
+        _given_workspace(workspace, x)
+    _call("gemm_lora", x, stream, workspace, *head, offsets_ptr, rows_ptr, *mats,
+          scale.data_ptr(), y.data_ptr(), ldy)
     return y
