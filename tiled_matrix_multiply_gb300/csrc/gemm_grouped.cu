@@ -278,10 +278,15 @@ __device__ __forceinline__ void zero16(uint32_t addr) {
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
-// Programmatic dependent launch: wait for the grid before (its results are visible then), and
-// let the next one start its prologue as soon as there is room.
+// Programmatic dependent launch: wait for the grid before (its results, and those of the grids
+// before it, are visible then), and let the next one start as soon as there is room.  Every grid
+// starts the next one only after its own wait, so whatever is before the grid before is done
+// when a grid starts.
 __device__ __forceinline__ void grid_wait() {
-  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void grid_start_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 __device__ __forceinline__ void tc_fence_before() {
@@ -684,7 +689,12 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     prefetch_map(&map_q);
     prefetch_map(&map_qr);
   }
-  grid_wait();
+  // The adapters' product follows the one that makes u, and needs nothing else of it: its wait
+  // comes before the first slice of u, so that the shared projection starts beside it.
+  if (MODE != kLora) {
+    grid_wait();
+    grid_start_next();
+  }
   for (int g = threadIdx.x; g <= p.groups; g += kThreads)
     offs[g] = max(0, min(p.offsets[g], p.rows));
   __syncthreads();
@@ -974,6 +984,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                   copy_q(c, st + PLANES * kPTile, full);
                 }
               } else {
+                if (MODE == kLora) grid_wait();
                 const Slice c = slice_at(s);
                 const uint32_t bar =
                     patch_of(c, half_rank) ? bar_patch + 8 * ring.stage : full_at(ring.stage);
@@ -1045,6 +1056,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           dropped = false;
           __syncwarp();
           if (c.ext) {
+            if (MODE == kLora) grid_wait();
             if (warp == 1 && elect_one()) copy_q(c, sq, bar);
           } else {
             if (MODE == kWgrad) {
@@ -1254,6 +1266,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     }
   }
 
+  if (MODE == kLora) {
+    grid_wait();       // no grid ends before the one it follows
+    grid_start_next();
+  }
   if (warp < kCopyWarps && timed_out) {
     // Let the copies in flight land before the block goes away: one that was issued does within
     // microseconds.
@@ -1297,6 +1313,7 @@ __global__ void planes_kernel(const void *__restrict__ src, int64_t count, int64
                               const int *__restrict__ offsets, const int *__restrict__ index,
                               int64_t src_rows, uint16_t *__restrict__ dst, int64_t ld8) {
   grid_wait();
+  grid_start_next();
   const int64_t per_row = ld8 / 8;
   const int64_t total = rows * per_row;
   const int64_t plane = count * rows * ld8;
@@ -1351,6 +1368,119 @@ __global__ void planes_kernel(const void *__restrict__ src, int64_t count, int64
         *reinterpret_cast<uint4 *>(dst + to) = v;
       }
     }
+  }
+}
+
+// ---- u for few rows ------------------------------------------------------------------------
+
+constexpr int kRowThreads = 512;
+constexpr int kRowRanks = 16;            // values of u a block makes
+
+// Eight values from p, those from `left` on as zeros; vec: p is on a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, int64_t left, int vec, float (&v)[8]) {
+  if (left >= 8 && vec) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 a = *reinterpret_cast<const float4 *>(p);
+      const float4 b = *reinterpret_cast<const float4 *>(p + 4);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+      const uint4 a = *reinterpret_cast<const uint4 *>(p);
+      const T *t = reinterpret_cast<const T *>(&a);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = float(t[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < left ? float(p[j]) : 0.0f;
+  }
+}
+
+// u[p, j] = scale[g] sum_k x[r(p), k] a[g, k, j] for one row p (blockIdx.x) and 16 j (blockIdx.y).
+// For a batch of few rows with an adapter each, a is read once per row and everything else is
+// small: the bound is the latency of reading K x 16 values, so one block takes them all at once
+// (512 threads, 16 bytes each, K / 256 rounds) instead of a product kernel's ring of slices, and
+// rows that share an adapter read it from L2.  FP32 throughout; sums of 512 threads in a fixed
+// order.  64 rows of 64 adapters, K = 4096, rank 16 bf16: see the adapters' figures.
+template <typename T, bool TRANS_A>
+__global__ void __launch_bounds__(kRowThreads)
+row_ranks_kernel(const T *__restrict__ x, int64_t ldx, int64_t x_rows, int vec_x,
+                 const int *__restrict__ row_index, const int *__restrict__ offsets, int groups,
+                 const T *__restrict__ a, int64_t lda, int64_t stride_a, int vec_a,
+                 const float *__restrict__ scale, int K, const Params out) {
+  grid_wait();
+  grid_start_next();
+  __shared__ float sums[kRowThreads / 32][kRowRanks];
+  __shared__ int owner;
+  const int p = blockIdx.x, j0 = blockIdx.y * kRowRanks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The group of row p: the first whose end is past p (with ends that never step back, and the
+  // first start not past it).
+  if (threadIdx.x == 0) owner = groups;
+  __syncthreads();
+  for (int g = threadIdx.x; g < groups; g += kRowThreads)
+    if (offsets[g + 1] > p) atomicMin(&owner, g);
+  __syncthreads();
+  const int g = owner;
+  if (g == groups || offsets[0] > p) return;
+  const int64_t row = row_index ? row_index[p] : p;
+  const bool have = row >= 0 && row < x_rows;
+  const T *const xr = x + (have ? row : 0) * ldx;
+  const T *const ag = a + int64_t(g) * stride_a;
+  const int ranks = min(kRowRanks, out.N - j0);
+  if constexpr (TRANS_A) {
+    // a stored rank x K: a warp a rank, 256 k a round.
+    for (int j = warp; j < kRowRanks; j += kRowThreads / 32) {
+      float sum = 0.0f;
+      if (j < ranks && have) {
+        const T *const aj = ag + int64_t(j0 + j) * lda;
+#pragma unroll 4
+        for (int k = lane * 8; k < K; k += 256) {
+          float u[8], v[8];
+          load8(aj + k, K - k, vec_a, u);
+          load8(xr + k, K - k, vec_x, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum = fmaf(u[i], v[i], sum);
+        }
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+      if (lane == 0) sums[0][j] = sum;
+    }
+  } else {
+    // a stored K x rank: two threads a k, eight ranks each, 256 k a round.
+    const int half = threadIdx.x & 1;
+    float sum[8] = {};
+    if (have) {
+#pragma unroll 8
+      for (int k = threadIdx.x >> 1; k < K; k += kRowThreads / 2) {
+        float u[8];
+        load8(ag + int64_t(k) * lda + j0 + 8 * half, ranks - 8 * half, vec_a, u);
+        const float v = float(xr[k]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = fmaf(u[i], v, sum[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int d = 16; d > 1; d >>= 1) sum[i] += __shfl_xor_sync(~0u, sum[i], d);
+      if (lane < 2) sums[warp][8 * lane + i] = sum[i];
+    }
+  }
+  __syncthreads();
+  // Ranks up to the padded width: zeros past the rank.
+  if (threadIdx.x < kRowRanks && j0 + int(threadIdx.x) < out.n_out) {
+    float v = 0.0f;
+    if constexpr (TRANS_A) {
+      v = sums[0][threadIdx.x];
+    } else {
+#pragma unroll
+      for (int w = 0; w < kRowThreads / 32; ++w) v += sums[w][threadIdx.x];
+    }
+    v *= scale[g];
+    store_out<sizeof(T) == 4 ? 3 : 1>(out, int64_t(p) * out.ld_out, j0 + threadIdx.x, v);
   }
 }
 
@@ -1538,6 +1668,8 @@ int forward_shape(int64_t rows, int64_t groups, int64_t N) {
   return rows > 64 * groups && N > 128 ? 2 : 1;
 }
 int lora_shape(int64_t rows) { return rows > 64 ? 2 : 1; }
+// u by rows (row_ranks_kernel).
+bool few_rows(int64_t rows) { return rows <= 64; }
 int wgrad_shape(int64_t N) { return N > 128 ? 2 : 1; }
 
 // The maps of x: rows by number; or tiles of box_of rows, and (pairs) of a whole block's columns.
@@ -1673,6 +1805,42 @@ cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *wor
   return launch_any(cg, planes, kWgrad, m, prm, tiles, dev, stream);
 }
 
+template <typename T, bool TRANS_A>
+static cudaError_t launch_row_ranks_as(const LoraProblem &p, const Params &out,
+                                       cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0] = overlap_attribute();
+  cfg.gridDim = dim3(unsigned(p.rows), unsigned((out.n_out + kRowRanks - 1) / kRowRanks), 1);
+  cfg.blockDim = dim3(kRowThreads, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const auto on16 = [](const void *q, int64_t ld, int64_t stride) {
+    return int((reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld * sizeof(T) % 16 == 0 &&
+               stride * sizeof(T) % 16 == 0);
+  };
+  const int64_t stride_a = p.a.count > 1 ? p.a.stride : 0;
+  return cudaLaunchKernelEx(&cfg, row_ranks_kernel<T, TRANS_A>, static_cast<const T *>(p.x.data),
+                            p.x.ld, p.x.rows, on16(p.x.data, p.x.ld, 0),
+                            static_cast<const int *>(p.row_index),
+                            static_cast<const int *>(p.offsets), int(p.groups),
+                            static_cast<const T *>(p.a.data), p.a.ld, stride_a,
+                            on16(p.a.data, p.a.ld, stride_a), p.scale, int(p.K), out);
+}
+
+static cudaError_t launch_row_ranks(const LoraProblem &p, const Params &out,
+                                    cudaStream_t stream) {
+  if (p.dtype == TMM_F32)
+    return p.trans_a ? launch_row_ranks_as<float, true>(p, out, stream)
+                     : launch_row_ranks_as<float, false>(p, out, stream);
+  if (p.dtype == TMM_BF16)
+    return p.trans_a ? launch_row_ranks_as<__nv_bfloat16, true>(p, out, stream)
+                     : launch_row_ranks_as<__nv_bfloat16, false>(p, out, stream);
+  return p.trans_a ? launch_row_ranks_as<__half, true>(p, out, stream)
+                   : launch_row_ranks_as<__half, false>(p, out, stream);
+}
+
 // Columns of u: pairs of 16-bit values in blocks of 32 + 32, or one plane's 16-byte rows.
 static int64_t u_columns(const LoraProblem &p) {
   return p.dtype == TMM_F32 ? round8(p.rank) : (p.rank + 31) / 32 * 64;
@@ -1685,7 +1853,7 @@ size_t lora_workspace_bytes(const LoraProblem &p) {
                     plane_bytes(p.x, p.dtype,
                                 gathered_rows(lora_shape(p.rows), p.row_index, p.rows)),
                     plane_bytes(p.w, p.dtype),
-                    plane_bytes(p.a, p.dtype), plane_bytes(p.b, p.dtype)});
+                    few_rows(p.rows) ? 0 : plane_bytes(p.a, p.dtype), plane_bytes(p.b, p.dtype)});
 }
 
 cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *workspace,
@@ -1698,12 +1866,13 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   Planes x, w, a, b;
   cudaError_t e;
   const int cg = lora_shape(p.rows);
+  const bool few = few_rows(p.rows);
   const int64_t gathered = gathered_rows(cg, p.row_index, p.rows);
   const int32_t *index = gathered ? nullptr : p.row_index;
   if ((e = make_planes(p.x, p.dtype, nullptr, &ws, dev, stream, &x, gathered, p.row_index)) !=
           cudaSuccess ||
       (e = make_planes(p.w, p.dtype, nullptr, &ws, dev, stream, &w)) != cudaSuccess ||
-      (e = make_planes(p.a, p.dtype, p.offsets, &ws, dev, stream, &a)) != cudaSuccess ||
+      (!few && (e = make_planes(p.a, p.dtype, p.offsets, &ws, dev, stream, &a)) != cudaSuccess) ||
       (e = make_planes(p.b, p.dtype, p.offsets, &ws, dev, stream, &b)) != cudaSuccess)
     return e;
   Params prm = {};
@@ -1719,10 +1888,11 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   prm.out_type = kOutU;
   prm.n_out = p.dtype == TMM_F32 ? int(p.rank) : int(ldu / 2);
   prm.scale = p.scale;
-  if ((e = run_forward(x, index, a, p.groups > 1 && p.a.count == 1, p.trans_a != 0, planes, prm,
-                       dev, stream)) !=
-      cudaSuccess)
-    return e;
+  // Few rows: a block for every row and 16 ranks; more: a product.
+  e = few ? launch_row_ranks(p, prm, stream)
+          : run_forward(x, index, a, p.groups > 1 && p.a.count == 1, p.trans_a != 0, planes, prm,
+                        dev, stream);
+  if (e != cudaSuccess) return e;
 
   const int bn = columns_of(cg, planes);
   prm.N = prm.n_out = int(p.N);
