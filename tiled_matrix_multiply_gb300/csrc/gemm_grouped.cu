@@ -65,6 +65,7 @@ constexpr int kForward = 0, kWgrad = 1, kLora = 2;
 constexpr int kBK = 64;                  // 16-bit values per K slice: one 128-byte swizzle row
 constexpr int kCopyWarps = 4, kEpiWarps = 8;
 constexpr int kEpi0 = kCopyWarps;                  // first of the result warps
+constexpr int kFewRows = 256;                      // rows of an adapters' call on single blocks
 constexpr int kMmaWarp = kCopyWarps + kEpiWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kChunk = 2;                // slices per tensor-memory sum of split operands
@@ -91,7 +92,8 @@ struct Shape {
   static constexpr uint32_t kOutStage = PLANES == 1 ? kEpiWarps * 1024 : 0;
   // Values of `rank` per slice of the adapters' part: 16-bit u is a pair of values (hi and lo).
   static constexpr int kRankSlice = PLANES == 3 ? 64 : 32;
-  static constexpr uint32_t kTable = (kMaxGroups + 1) * 4 * 3 + kCopyWarps * 128 + 116;
+  static constexpr uint32_t kTable =
+      (kMaxGroups + 1) * 4 * 3 + kCopyWarps * 128 + 116 + (CG == 1 ? kFewRows * 4 : 0);
   static constexpr uint32_t kBars = 8 * (3 * kStages + 5) + 32;
   static constexpr uint32_t kSmem = 1024 + kStages * kStage + kRed + kOutStage + kTable + kBars;
   static_assert(kSmem <= kMaxSmem, "one block's shared memory");
@@ -121,6 +123,11 @@ struct Params {
   int n_out;             // columns written (from N on: zeros)
   int vec_out;           // 16-bit results with rows (and matrices) on 16-byte boundaries
   const float *scale;    // per group, or NULL
+  // Adapters on single blocks: u in FP32 by row of x, and b as it is stored.
+  const float *u;
+  const void *b;
+  int64_t ldu, ldb, stride_b;
+  int trans_b, vec_b;
   int zero_rows;         // forward: write zeros to the rows of no group
   int ksplit;            // blocks of a cluster that share a tile's sum (CG = 1)
   int64_t wait_limit_ns;
@@ -416,7 +423,7 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const Table &tab, int t
   r.qn = min(p.tile_n, hi - r.q0);
   r.bn = (r.qn + S::kUnit - 1) / S::kUnit * S::kUnit;
   r.klen = p.K;
-  if (MODE == kLora) {
+  if (MODE == kLora && CG == 2) {
     // Entries whose rows overlap [q0, q0 + qn): first with an end past q0, up to a start past it.
     int a = 0, b = tab.count;
     while (a < b) {
@@ -439,12 +446,12 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const Table &tab, int t
 
 // This block's K slices [s0, s1) of a tile: the slices of the base sum, then those of the
 // adapters in the tile; blocks that share a tile take equal runs of them.
-template <int MODE, int RS>
+template <bool EXT, int RS>
 __device__ __forceinline__ void slices_of(const Params &p, const Tile &t, int rank, int &base,
                                           int &s0, int &s1) {
   base = (t.klen + kBK - 1) / kBK;
   int n = base;
-  if (MODE == kLora) n += t.en * ((p.rank + RS - 1) / RS);
+  if (EXT) n += t.en * ((p.rank + RS - 1) / RS);
   if (p.ksplit == 1) {
     s0 = 0;
     s1 = n;
@@ -534,11 +541,13 @@ __device__ __forceinline__ int64_t out_row(const Params &p, const Tile &t, int c
 // in place of 16 of two bytes.
 template <int MODE, int PLANES>
 __device__ __forceinline__ void store_columns(const Params &p, const Tile &t, int c0, int nw,
-                                              const float (&v)[16], float scale, uint32_t stage) {
+                                              const float (&v)[16], float scale, uint32_t stage,
+                                              const int *owner) {
   const int lane = threadIdx.x & 31;
   const int count = min(16, t.qn - c0);
   const int n = nw + lane;
   const bool by_row = MODE == kLora && p.out_index;
+  const bool check = MODE == kLora && p.u;      // rows that are not written (see owner)
   int64_t first = 0;
   if (!by_row) {
     first = out_row<kForward>(p, t, c0);
@@ -571,7 +580,7 @@ __device__ __forceinline__ void store_columns(const Params &p, const Tile &t, in
                      : "memory");
         if (row >= count || n8 >= p.N) continue;
         const int64_t o = by_row ? out_row<MODE>(p, t, c0 + row) : first + row * p.ld_out;
-        if (o < 0) continue;
+        if (o < 0 || (check && owner[t.q0 + c0 + row] == -2)) continue;
         uint16_t *dst = static_cast<uint16_t *>(p.out) + o + n8;
         if (n8 + 8 <= p.N) {
           *reinterpret_cast<uint4 *>(dst) = w;
@@ -590,7 +599,8 @@ __device__ __forceinline__ void store_columns(const Params &p, const Tile &t, in
     const bool in = n < p.N;
 #pragma unroll
     for (int j = 0; j < 16; ++j)
-      if (in && j < count) dst[j * p.ld_out] = v[j] * scale;
+      if (in && j < count && !(check && owner[t.q0 + c0 + j] == -2))
+        dst[j * p.ld_out] = v[j] * scale;
     return;
   }
   int row = 0;      // the row of column c0 + lane % 16
@@ -605,8 +615,88 @@ __device__ __forceinline__ void store_columns(const Params &p, const Tile &t, in
     if (by_row) {
       const int r = __shfl_sync(~0u, row, j);
       if (in && r >= 0) store_out<PLANES>(p, int64_t(r) * p.ld_out, n, v[j] * scale);
-    } else if (in && j < count) {
+    } else if (in && j < count && !(check && owner[t.q0 + c0 + j] == -2)) {
       store_out<PLANES>(p, first + j * p.ld_out, n, v[j] * scale);
+    }
+  }
+}
+
+// Eight values from p, those from `left` on as zeros; vec: p is on a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, int64_t left, int vec, float (&v)[8]) {
+  if (left >= 8 && vec) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 a = *reinterpret_cast<const float4 *>(p);
+      const float4 b = *reinterpret_cast<const float4 *>(p + 4);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+      const uint4 a = *reinterpret_cast<const uint4 *>(p);
+      const T *t = reinterpret_cast<const T *>(&a);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = float(t[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < left ? float(p[j]) : 0.0f;
+  }
+}
+
+// All threads of the result warps.
+__device__ __forceinline__ void results_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+}
+
+// The adapters' part of columns [c0, c1) of a tile (rows of x), to sums[column][lane]:
+// sum_j u[row, j] b[g, j, n].  Few rows: b is read once per row and lane, on the CUDA cores,
+// while the weights stream: `rank` loads of 16 bytes a thread in flight for eight n of one row.
+template <typename T>
+__device__ __forceinline__ void add_adapters(const Params &p, const int *owner, const Tile &t,
+                                             int c0, int c1, float *sums) {
+  grid_wait();      // u is the launch before's
+  const int tid = int(threadIdx.x) - 32 * kEpi0;
+  const T *const b = static_cast<const T *>(p.b);
+  if (!p.trans_b) {
+    // b stored rank x N.
+    const int l = (tid & 15) * 8, n = t.n0 + l;
+    for (int col = c0 + (tid >> 4); col < c1; col += 32 * kEpiWarps / 16) {
+      float v[8] = {};
+      const int g = owner[t.q0 + col];
+      if (g >= 0 && n < p.N) {
+        const T *const bn = b + int64_t(g) * p.stride_b + n;
+        const float *const u = p.u + int64_t(t.q0 + col) * p.ldu;
+#pragma unroll 8
+        for (int j = 0; j < p.rank; ++j) {
+          float w[8];
+          load8(bn + j * p.ldb, p.N - n, p.vec_b, w);
+          const float f = u[j];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = fmaf(f, w[i], v[i]);
+        }
+      }
+      float4 *const to = reinterpret_cast<float4 *>(sums + col * 128 + l);
+      to[0] = make_float4(v[0], v[1], v[2], v[3]);
+      to[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+    // b stored N x rank.
+    const int l = tid & 127, n = t.n0 + l;
+    for (int col = c0 + (tid >> 7); col < c1; col += 32 * kEpiWarps / 128) {
+      float v = 0.0f;
+      const int g = owner[t.q0 + col];
+      if (g >= 0 && n < p.N) {
+        const T *const bn = b + int64_t(g) * p.stride_b + int64_t(n) * p.ldb;
+        const float *const u = p.u + int64_t(t.q0 + col) * p.ldu;
+#pragma unroll 4
+        for (int j = 0; j < p.rank; j += 8) {
+          float w[8], f[8];
+          load8(bn + j, p.rank - j, p.vec_b, w);
+          load8(u + j, p.rank - j, 1, f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v = fmaf(f[i], w[i], v);
+        }
+      }
+      sums[col * 128 + l] = v;
     }
   }
 }
@@ -623,6 +713,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                const __grid_constant__ CUtensorMap map_u,    // u tiles
                const Params p) {
   using S = Shape<CG, PLANES>;
+  // The adapters' part: pairs extend the sum (EXT); single blocks, whose rows are few, add it to
+  // the results on the CUDA cores while the weights stream (FEW).
+  constexpr bool EXT = MODE == kLora && CG == 2, FEW = MODE == kLora && CG == 1;
+  constexpr bool PATCH = EXT || MODE == kWgrad;      // some slices get rows of zeros
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;    // the same offset in every block
@@ -645,6 +739,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   // Row numbers that a copy warp is about to fetch, four to a copy; 16-byte aligned.
   int *const my_rows = reinterpret_cast<int *>(
       (reinterpret_cast<uintptr_t>(tab_tile + (kMaxGroups + 1)) + 15) & ~uintptr_t(15)) + 32 * warp;
+  int *const owner = tab_gid + (S::kTable / 4 - kFewRows);      // adapters on single blocks
   volatile uint32_t *const slot_ptr = reinterpret_cast<volatile uint32_t *>(smem + (slot - base));
   float *const red_ptr = reinterpret_cast<float *>(smem + (red - base));
 
@@ -660,7 +755,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   int *const offs = reinterpret_cast<int *>(smem);
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(bar_full + 8 * s, MODE == kForward ? 1 : CG);
+      mbar_init(bar_full + 8 * s, PATCH ? CG : 1);
       mbar_init(bar_patch + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
     }
@@ -749,6 +844,23 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     }
     proxy_fence();      // the ring is written by the copy engine from here on
   }
+  if constexpr (FEW) {
+    // The adapter of every row of x: its list entry's number, -1 for none, -2 for a row that the
+    // order does not name (which is not written).
+    for (int i = threadIdx.x; i < kFewRows; i += kThreads) owner[i] = -2;
+    __syncthreads();
+    const int count = int(slot_ptr[1]);
+    for (int i = threadIdx.x; i < p.rows; i += kThreads) {
+      const int row = p.row_index ? p.row_index[i] : i;
+      int a = 0, b = count;        // entries that start at or before place i
+      while (a < b) {
+        const int m = (a + b) >> 1;
+        if (tab_row[m] <= i) a = m + 1;
+        else b = m;
+      }
+      if (row >= 0 && row < p.rows) owner[row] = a > 0 && i < tab_row[a] ? tab_gid[a - 1] : -1;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if (CG == 2 || p.ksplit > 1) cluster_sync();   // barriers exist before any remote arrival
@@ -781,11 +893,11 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   }
 
   for (int t = cluster; t < tab.tiles; t += clusters) {
-    if (timed_out && p.ksplit == 1) break;
+    if (timed_out && p.ksplit == 1 && !FEW) break;     // (else warps meet at every tile)
     const Tile tile = tile_at<CG, MODE, PLANES>(p, tab, t);
     int nbase, s0, s1;
-    slices_of<MODE, S::kRankSlice>(p, tile, CG == 2 ? 0 : int(rank), nbase, s0, s1);
-    const int per_rank = MODE == kLora ? (p.rank + S::kRankSlice - 1) / S::kRankSlice : 1;
+    slices_of<EXT, S::kRankSlice>(p, tile, CG == 2 ? 0 : int(rank), nbase, s0, s1);
+    const int per_rank = EXT ? (p.rank + S::kRankSlice - 1) / S::kRankSlice : 1;
 
     if (warp < kCopyWarps) {
       // ---- copies ----
@@ -800,7 +912,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       const int mine = held(half_rank);
       const int boxes = (mine + S::kBox - 1) / S::kBox;
       const int qblocks = hr / 64;
-      const bool by_row = CG == 1 && p.row_index != nullptr;
+      const bool by_row = CG == 1 && MODE != kLora && p.row_index != nullptr;
       uint32_t usual = 0;      // bytes of an ordinary slice, of both blocks of a pair
       if (MODE == kWgrad) {
         usual = CG * PLANES * (kPTile + uint32_t(qblocks) * 8192u);
@@ -821,11 +933,11 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         int cnt;                            // gradient: rows of the group
       };
       const auto slice_at = [&](int s) {
-        Slice c = {MODE == kLora && s >= nbase, s * kBK, pg, pcount, 0, 0, 0, kBK};
+        Slice c = {EXT && s >= nbase, s * kBK, pg, pcount, 0, 0, 0, kBK};
         if (MODE == kWgrad) {
           c.k0 += tile.k0;
           c.cnt = min(kBK, tile.klen - s * kBK);
-        } else if (MODE == kLora && c.ext) {
+        } else if (EXT && c.ext) {
           const int e = (s - nbase) / per_rank;
           const int j = s - nbase - e * per_rank;
           c.k0 = j * kBK;                    // of u
@@ -847,12 +959,12 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       const auto patch_of = [&](const Slice &c, int half) {
         if (MODE == kWgrad) return c.cnt < kBK;
         const int q = tile.q0 + half * hr;
-        return MODE == kLora && c.ext && held(half) > 0 && (c.lo > q || c.hi < q + held(half));
+        return EXT && c.ext && held(half) > 0 && (c.lo > q || c.hi < q + held(half));
       };
       // A slice that slice_at describes as ordinary in every respect.
       const auto is_plain = [&](int s) {
         if (MODE == kWgrad) return (s + 1) * kBK <= tile.klen;
-        return MODE == kForward || s < nbase;
+        return !EXT || s < nbase;
       };
       const auto full_at = [&](int stage) {
         const uint32_t bar = bar_full + 8 * stage;
@@ -868,7 +980,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
 #pragma unroll
           for (int i = 0; i < 2 * PLANES; ++i)
             tma_2d<CG>(st + i * 8192, &map_p, n0 + (i & 1) * 64, c.k0 + (i >> 1) * p.rows, bar);
-        } else if (MODE == kLora && c.ext) {
+        } else if (EXT && c.ext) {
           if (p.e_mn) {
 #pragma unroll
             for (int i = 0; i < 2 * PLANES; ++i)
@@ -895,7 +1007,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
             for (int b = 0; b < qblocks; ++b)
               tma_2d<CG>(sq + pl * S::kQTile + b * 8192, &map_q, qf + b * 64, c.k0 + pl * p.q_rows,
                          bar);
-        } else if (MODE == kLora && c.ext) {
+        } else if (EXT && c.ext) {
           for (int pl = 0; pl < PLANES; ++pl)
             for (int b = 0; b < boxes; ++b)
               tma_2d<CG>(sq + pl * S::kQTile + b * (S::kBox * 128), &map_u, c.k0,
@@ -979,12 +1091,12 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                 if (warp == 0) {
                   if (leader) expect(ring.stage, usual);
                   copy_p(c, st, full);
-                  if (MODE != kForward && !leader) mbar_arrive_relaxed(full);
+                  if (PATCH && !leader) mbar_arrive_relaxed(full);
                 } else {
                   copy_q(c, st + PLANES * kPTile, full);
                 }
               } else {
-                if (MODE == kLora) grid_wait();
+                if (EXT) grid_wait();
                 const Slice c = slice_at(s);
                 const uint32_t bar =
                     patch_of(c, half_rank) ? bar_patch + 8 * ring.stage : full_at(ring.stage);
@@ -1000,10 +1112,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           }
           __syncwarp();
           timed_out = __any_sync(~0u, timed_out);
-        } else if (MODE != kForward) {
+        } else if (PATCH) {
           Ring at = ring;
           int s = s0;
-          if (MODE == kLora && nbase > s0) s = min(nbase, s1);
+          if (EXT && nbase > s0) s = min(nbase, s1);
           if (MODE == kWgrad && s1 > s0) s = is_plain(s1 - 1) ? s1 : s1 - 1;
           at.template skip<S::kStages>(s - s0);
           for (; s < s1 && !timed_out; ++s) {
@@ -1055,29 +1167,24 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           }
           dropped = false;
           __syncwarp();
-          if (c.ext) {
-            if (MODE == kLora) grid_wait();
-            if (warp == 1 && elect_one()) copy_q(c, sq, bar);
-          } else {
-            if (MODE == kWgrad) {
-              if (lane < 16) my_rows[lane] = next;
-              __syncwarp();
-              if (s + 1 < s1 && lane < 16)
-                next = row_of(c.k0 + kBK + row_in_slice, tile.k0 + tile.klen);
-            }
-            if (elect_one()) {
-              const int fours = MODE == kWgrad ? (c.cnt + 15) / 16 * 4 : (mine + 3) / 4;
-              const int x = MODE == kWgrad ? qf : c.k0;
-              for (int f = warp, k = 0; f < fours; f += kCopyWarps, ++k) {
-                const int4 v = *reinterpret_cast<const int4 *>(my_rows + 4 * k);
+          if (MODE == kWgrad) {
+            if (lane < 16) my_rows[lane] = next;
+            __syncwarp();
+            if (s + 1 < s1 && lane < 16)
+              next = row_of(c.k0 + kBK + row_in_slice, tile.k0 + tile.klen);
+          }
+          if (elect_one()) {
+            const int fours = MODE == kWgrad ? (c.cnt + 15) / 16 * 4 : (mine + 3) / 4;
+            const int x = MODE == kWgrad ? qf : c.k0;
+            for (int f = warp, k = 0; f < fours; f += kCopyWarps, ++k) {
+              const int4 v = *reinterpret_cast<const int4 *>(my_rows + 4 * k);
 #pragma unroll
-                for (int pl = 0; pl < PLANES; ++pl) {
-                  const int out = PLANES * p.q_rows, add = pl * p.q_rows;
-                  const int y[4] = {v.x < 0 ? out : v.x + add, v.y < 0 ? out : v.y + add,
-                                    v.z < 0 ? out : v.z + add, v.w < 0 ? out : v.w + add};
-                  for (int b = 0; b < (MODE == kWgrad ? qblocks : 1); ++b)
-                    tma_rows4(sq + pl * S::kQTile + b * 8192 + f * 512, &map_qr, x + b * 64, y, bar);
-                }
+              for (int pl = 0; pl < PLANES; ++pl) {
+                const int out = PLANES * p.q_rows, add = pl * p.q_rows;
+                const int y[4] = {v.x < 0 ? out : v.x + add, v.y < 0 ? out : v.y + add,
+                                  v.z < 0 ? out : v.z + add, v.w < 0 ? out : v.w + add};
+                for (int b = 0; b < (MODE == kWgrad ? qblocks : 1); ++b)
+                  tma_rows4(sq + pl * S::kQTile + b * 8192 + f * 512, &map_qr, x + b * 64, y, bar);
               }
             }
           }
@@ -1115,7 +1222,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
             break;
           }
           tc_fence_after();
-          const bool ext = MODE == kLora && s >= nbase;
+          const bool ext = EXT && s >= nbase;
           const bool pmn = ext ? p.e_mn : base_mn;
           const uint32_t idesc = sizes | (pmn ? 1u << 15 : 0u);
           const uint32_t st = base + ring.stage * S::kStage;
@@ -1126,7 +1233,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           const int left = ext ? min(S::kRankSlice, p.rank - (s - nbase) % per_rank * S::kRankSlice)
                                : min(kBK, tile.klen - s * kBK);
           const int steps = (left + 15) / 16;
-          if (PLANES == 1 && MODE == kLora && ext) {
+          if (PLANES == 1 && EXT && ext) {
             // b[g] times u's hi, and times its lo, 32 columns on.
             for (int k = 0; k < steps; ++k) {
               const uint64_t a = dp + k * pstep, b = dq + k * qstep;
@@ -1169,12 +1276,32 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       const uint32_t stage = out_stage + uint32_t(warp - kEpi0) * 1024;
       const float scale = MODE == kForward && p.scale ? p.scale[tile.g] : 1.0f;
       constexpr int kBlocks = S::kBN / 32;     // 16-column blocks of a warp, every other one
+      // The columns that this block adds up and stores: all of them, or its share.
+      const int own0 = CG == 1 ? tile.qn * int(rank) / p.ksplit : 0;
+      const int own1 = CG == 1 ? tile.qn * int(rank + 1) / p.ksplit : tile.qn;
+      if constexpr (FEW) {
+        results_sync();      // the last tile's sums have been read
+        if (PLANES == 3)
+          add_adapters<float>(p, owner, tile, own0, own1, red_ptr);
+        else if (p.idesc & (1u << 7))
+          add_adapters<__nv_bfloat16>(p, owner, tile, own0, own1, red_ptr);
+        else
+          add_adapters<__half>(p, owner, tile, own0, own1, red_ptr);
+        results_sync();
+      }
       auto put = [&](int c0, const float (&v)[16]) {
-        if (CG == 1 && p.ksplit > 1) {
+        if (CG == 1 && (FEW || p.ksplit > 1)) {
+          float w[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) red_ptr[(c0 + j) * 128 + 32 * quarter + lane] = v[j];
+          for (int j = 0; j < 16; ++j) {
+            float *const at = &red_ptr[(c0 + j) * 128 + 32 * quarter + lane];
+            w[j] = v[j];
+            if (FEW && c0 + j >= own0 && c0 + j < own1) w[j] += *at;
+            if (p.ksplit > 1) *at = w[j];
+          }
+          if (p.ksplit == 1) store_columns<MODE, PLANES>(p, tile, c0, nw, w, scale, stage, owner);
         } else {
-          store_columns<MODE, PLANES>(p, tile, c0, nw, v, scale, stage);
+          store_columns<MODE, PLANES>(p, tile, c0, nw, v, scale, stage, owner);
         }
       };
       if constexpr (PLANES == 1) {
@@ -1183,7 +1310,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           for (int c0 = 16 * half; c0 < tile.bn; c0 += 32) put(c0, v);
         } else {
           const uint32_t buf = q & 1;
-          const bool ready = mbar_wait(bar_tfull + 8 * buf, (q >> 1) & 1u, p.wait_limit_ns);
+          const bool ready =
+              !timed_out && mbar_wait(bar_tfull + 8 * buf, (q >> 1) & 1u, p.wait_limit_ns);
           ++q;
           if (!__all_sync(~0u, ready)) timed_out = true;
           tc_fence_after();
@@ -1257,7 +1385,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           const uint32_t at = red + uint32_t(col * 128 + l) * 4;
           float v = 0.0f;
           for (int b = 0; b < p.ksplit; ++b) v += ld_cluster(map_rank(at, uint32_t(b)));
-          const int64_t o = out_row<MODE>(p, tile, col);
+          int64_t o = out_row<MODE>(p, tile, col);
+          if (FEW && owner[tile.q0 + col] == -2) o = -1;
           if (o >= 0 && tile.n0 + l < p.n_out) store_out<PLANES>(p, o, tile.n0 + l, v * scale);
         }
       }
@@ -1376,28 +1505,8 @@ __global__ void planes_kernel(const void *__restrict__ src, int64_t count, int64
 constexpr int kRowThreads = 512;
 constexpr int kRowRanks = 16;            // values of u a block makes
 
-// Eight values from p, those from `left` on as zeros; vec: p is on a 16-byte boundary.
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, int64_t left, int vec, float (&v)[8]) {
-  if (left >= 8 && vec) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 a = *reinterpret_cast<const float4 *>(p);
-      const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-      const uint4 a = *reinterpret_cast<const uint4 *>(p);
-      const T *t = reinterpret_cast<const T *>(&a);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = float(t[j]);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < left ? float(p[j]) : 0.0f;
-  }
-}
-
-// u[p, j] = scale[g] sum_k x[r(p), k] a[g, k, j] for one row p (blockIdx.x) and 16 j (blockIdx.y).
+// u[r(p), j] = scale[g] sum_k x[r(p), k] a[g, k, j] for one place p (blockIdx.x) and 16 j
+// (blockIdx.y), in FP32.
 // For a batch of few rows with an adapter each, a is read once per row and everything else is
 // small: the bound is the latency of reading K x 16 values, so one block takes them all at once
 // (512 threads, 16 bytes each, K / 256 rounds) instead of a product kernel's ring of slices, and
@@ -1408,7 +1517,8 @@ __global__ void __launch_bounds__(kRowThreads)
 row_ranks_kernel(const T *__restrict__ x, int64_t ldx, int64_t x_rows, int vec_x,
                  const int *__restrict__ row_index, const int *__restrict__ offsets, int groups,
                  const T *__restrict__ a, int64_t lda, int64_t stride_a, int vec_a,
-                 const float *__restrict__ scale, int K, const Params out) {
+                 const float *__restrict__ scale, int K, int rank, float *__restrict__ u,
+                 int64_t ldu) {
   grid_wait();
   grid_start_next();
   __shared__ float sums[kRowThreads / 32][kRowRanks];
@@ -1428,7 +1538,7 @@ row_ranks_kernel(const T *__restrict__ x, int64_t ldx, int64_t x_rows, int vec_x
   const bool have = row >= 0 && row < x_rows;
   const T *const xr = x + (have ? row : 0) * ldx;
   const T *const ag = a + int64_t(g) * stride_a;
-  const int ranks = min(kRowRanks, out.N - j0);
+  const int ranks = min(kRowRanks, rank - j0);
   if constexpr (TRANS_A) {
     // a stored rank x K: a warp a rank, 256 k a round.
     for (int j = warp; j < kRowRanks; j += kRowThreads / 32) {
@@ -1437,11 +1547,11 @@ row_ranks_kernel(const T *__restrict__ x, int64_t ldx, int64_t x_rows, int vec_x
         const T *const aj = ag + int64_t(j0 + j) * lda;
 #pragma unroll 4
         for (int k = lane * 8; k < K; k += 256) {
-          float u[8], v[8];
-          load8(aj + k, K - k, vec_a, u);
+          float w[8], v[8];
+          load8(aj + k, K - k, vec_a, w);
           load8(xr + k, K - k, vec_x, v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum = fmaf(u[i], v[i], sum);
+          for (int i = 0; i < 8; ++i) sum = fmaf(w[i], v[i], sum);
         }
       }
 #pragma unroll
@@ -1455,11 +1565,11 @@ row_ranks_kernel(const T *__restrict__ x, int64_t ldx, int64_t x_rows, int vec_x
     if (have) {
 #pragma unroll 8
       for (int k = threadIdx.x >> 1; k < K; k += kRowThreads / 2) {
-        float u[8];
-        load8(ag + int64_t(k) * lda + j0 + 8 * half, ranks - 8 * half, vec_a, u);
+        float w[8];
+        load8(ag + int64_t(k) * lda + j0 + 8 * half, ranks - 8 * half, vec_a, w);
         const float v = float(xr[k]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] = fmaf(u[i], v, sum[i]);
+        for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[i], v, sum[i]);
       }
     }
 #pragma unroll
@@ -1470,8 +1580,7 @@ row_ranks_kernel(const T *__restrict__ x, int64_t ldx, int64_t x_rows, int vec_x
     }
   }
   __syncthreads();
-  // Ranks up to the padded width: zeros past the rank.
-  if (threadIdx.x < kRowRanks && j0 + int(threadIdx.x) < out.n_out) {
+  if (int(threadIdx.x) < ranks && have) {
     float v = 0.0f;
     if constexpr (TRANS_A) {
       v = sums[0][threadIdx.x];
@@ -1479,8 +1588,7 @@ row_ranks_kernel(const T *__restrict__ x, int64_t ldx, int64_t x_rows, int vec_x
 #pragma unroll
       for (int w = 0; w < kRowThreads / 32; ++w) v += sums[w][threadIdx.x];
     }
-    v *= scale[g];
-    store_out<sizeof(T) == 4 ? 3 : 1>(out, int64_t(p) * out.ld_out, j0 + threadIdx.x, v);
+    u[row * ldu + j0 + threadIdx.x] = v * scale[g];
   }
 }
 
@@ -1499,11 +1607,16 @@ cudaLaunchAttribute overlap_attribute() {
 
 int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
 
+// Rows (and matrices) of `size`-byte elements on 16-byte boundaries.
+int on16(const Stack &s, int64_t size) {
+  return (reinterpret_cast<uintptr_t>(s.data) & 15u) == 0 && s.ld * size % 16 == 0 &&
+         (s.count == 1 || s.stride * size % 16 == 0);
+}
+
 // Whether the copy engine can read the matrices in place: 16-bit values, rows and matrices on
 // 16-byte boundaries.
 bool in_place(const Stack &s, int dtype) {
-  return dtype != TMM_F32 && (reinterpret_cast<uintptr_t>(s.data) & 15u) == 0 && s.ld % 8 == 0 &&
-         (s.count == 1 || s.stride % 8 == 0);
+  return dtype != TMM_F32 && on16(s, 2);
 }
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
@@ -1550,8 +1663,7 @@ cudaError_t make_planes(const Stack &s, int dtype, const int32_t *offsets, char 
   const int64_t work = (rows * (ld8 / 8) + 255) / 256;
   const dim3 grid(unsigned(std::min<int64_t>(work, 8 * dev.sm_count)),
                   unsigned(std::min<int64_t>(s.count, 1024)));
-  const int vec = (reinterpret_cast<uintptr_t>(s.data) & 15u) == 0 && s.ld * size % 16 == 0 &&
-                  (s.count == 1 || s.stride * size % 16 == 0);
+  const int vec = on16(s, size);
   if (s.count == 1) offsets = nullptr;      // one matrix may serve every group
   if (gathered == 0) index = nullptr;
   *out = {dst, planes * s.count, rows, s.cols, ld8, rows * ld8};
@@ -1667,9 +1779,7 @@ int split_of(int64_t tiles, int64_t slices, const DeviceInfo &dev) {
 int forward_shape(int64_t rows, int64_t groups, int64_t N) {
   return rows > 64 * groups && N > 128 ? 2 : 1;
 }
-int lora_shape(int64_t rows) { return rows > 64 ? 2 : 1; }
-// u by rows (row_ranks_kernel).
-bool few_rows(int64_t rows) { return rows <= 64; }
+int lora_shape(int64_t rows) { return rows > kFewRows ? 2 : 1; }
 int wgrad_shape(int64_t N) { return N > 128 ? 2 : 1; }
 
 // The maps of x: rows by number; or tiles of box_of rows, and (pairs) of a whole block's columns.
@@ -1806,101 +1916,119 @@ cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *wor
 }
 
 template <typename T, bool TRANS_A>
-static cudaError_t launch_row_ranks_as(const LoraProblem &p, const Params &out,
+static cudaError_t launch_row_ranks_as(const LoraProblem &p, float *u, int64_t ldu,
                                        cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0] = overlap_attribute();
-  cfg.gridDim = dim3(unsigned(p.rows), unsigned((out.n_out + kRowRanks - 1) / kRowRanks), 1);
+  cfg.gridDim = dim3(unsigned(p.rows), unsigned((p.rank + kRowRanks - 1) / kRowRanks), 1);
   cfg.blockDim = dim3(kRowThreads, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const auto on16 = [](const void *q, int64_t ld, int64_t stride) {
-    return int((reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld * sizeof(T) % 16 == 0 &&
-               stride * sizeof(T) % 16 == 0);
-  };
-  const int64_t stride_a = p.a.count > 1 ? p.a.stride : 0;
   return cudaLaunchKernelEx(&cfg, row_ranks_kernel<T, TRANS_A>, static_cast<const T *>(p.x.data),
-                            p.x.ld, p.x.rows, on16(p.x.data, p.x.ld, 0),
+                            p.x.ld, p.x.rows, on16(p.x, sizeof(T)),
                             static_cast<const int *>(p.row_index),
                             static_cast<const int *>(p.offsets), int(p.groups),
-                            static_cast<const T *>(p.a.data), p.a.ld, stride_a,
-                            on16(p.a.data, p.a.ld, stride_a), p.scale, int(p.K), out);
+                            static_cast<const T *>(p.a.data), p.a.ld,
+                            p.a.count > 1 ? p.a.stride : int64_t(0), on16(p.a, sizeof(T)), p.scale,
+                            int(p.K), int(p.rank), u, ldu);
 }
 
-static cudaError_t launch_row_ranks(const LoraProblem &p, const Params &out,
+static cudaError_t launch_row_ranks(const LoraProblem &p, float *u, int64_t ldu,
                                     cudaStream_t stream) {
   if (p.dtype == TMM_F32)
-    return p.trans_a ? launch_row_ranks_as<float, true>(p, out, stream)
-                     : launch_row_ranks_as<float, false>(p, out, stream);
+    return p.trans_a ? launch_row_ranks_as<float, true>(p, u, ldu, stream)
+                     : launch_row_ranks_as<float, false>(p, u, ldu, stream);
   if (p.dtype == TMM_BF16)
-    return p.trans_a ? launch_row_ranks_as<__nv_bfloat16, true>(p, out, stream)
-                     : launch_row_ranks_as<__nv_bfloat16, false>(p, out, stream);
-  return p.trans_a ? launch_row_ranks_as<__half, true>(p, out, stream)
-                   : launch_row_ranks_as<__half, false>(p, out, stream);
+    return p.trans_a ? launch_row_ranks_as<__nv_bfloat16, true>(p, u, ldu, stream)
+                     : launch_row_ranks_as<__nv_bfloat16, false>(p, u, ldu, stream);
+  return p.trans_a ? launch_row_ranks_as<__half, true>(p, u, ldu, stream)
+                   : launch_row_ranks_as<__half, false>(p, u, ldu, stream);
 }
 
-// Columns of u: pairs of 16-bit values in blocks of 32 + 32, or one plane's 16-byte rows.
+// Columns of u: FP32 values on single blocks; for pairs a plane's 16-byte rows, or pairs of 16-bit
+// values in blocks of 32 + 32.
 static int64_t u_columns(const LoraProblem &p) {
-  return p.dtype == TMM_F32 ? round8(p.rank) : (p.rank + 31) / 32 * 64;
+  return p.dtype == TMM_F32 || lora_shape(p.rows) == 1 ? round8(p.rank) : (p.rank + 31) / 32 * 64;
+}
+static size_t u_bytes(const LoraProblem &p) {
+  const int size = lora_shape(p.rows) == 1 ? 4 : p.dtype == TMM_F32 ? 6 : 2;
+  return round256(size_t(p.rows) * size_t(u_columns(p)) * size);   // below 2^29 * 2^11 * 6
 }
 
-// The workspace holds u (a row for every p) and the planes of the operands.
+// The workspace holds u and the planes of the operands.
 size_t lora_workspace_bytes(const LoraProblem &p) {
-  const __int128 u = __int128(p.dtype == TMM_F32 ? 6 : 2) * p.rows * u_columns(p);
-  return add_sizes({u > __int128(INT64_MAX / 4) ? SIZE_MAX : round256(size_t(u)),
-                    plane_bytes(p.x, p.dtype,
-                                gathered_rows(lora_shape(p.rows), p.row_index, p.rows)),
-                    plane_bytes(p.w, p.dtype),
-                    few_rows(p.rows) ? 0 : plane_bytes(p.a, p.dtype), plane_bytes(p.b, p.dtype)});
+  if (lora_shape(p.rows) == 1)
+    return add_sizes({u_bytes(p), plane_bytes(p.x, p.dtype), plane_bytes(p.w, p.dtype)});
+  return add_sizes({u_bytes(p),
+                    plane_bytes(p.x, p.dtype, gathered_rows(2, p.row_index, p.rows)),
+                    plane_bytes(p.w, p.dtype), plane_bytes(p.a, p.dtype),
+                    plane_bytes(p.b, p.dtype)});
 }
 
 cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *workspace,
                         cudaStream_t stream) {
   char *ws = static_cast<char *>(workspace);
   const int planes = p.dtype == TMM_F32 ? 3 : 1;
-  const int64_t ldu = u_columns(p);
-  uint16_t *u = reinterpret_cast<uint16_t *>(ws);
-  ws += round256(size_t(planes) * 2 * p.rows * ldu);
-  Planes x, w, a, b;
-  cudaError_t e;
   const int cg = lora_shape(p.rows);
-  const bool few = few_rows(p.rows);
+  const int64_t ldu = u_columns(p);
+  void *u = ws;
+  ws += u_bytes(p);
   const int64_t gathered = gathered_rows(cg, p.row_index, p.rows);
-  const int32_t *index = gathered ? nullptr : p.row_index;
+  Planes x, w;
+  cudaError_t e;
   if ((e = make_planes(p.x, p.dtype, nullptr, &ws, dev, stream, &x, gathered, p.row_index)) !=
           cudaSuccess ||
-      (e = make_planes(p.w, p.dtype, nullptr, &ws, dev, stream, &w)) != cudaSuccess ||
-      (!few && (e = make_planes(p.a, p.dtype, p.offsets, &ws, dev, stream, &a)) != cudaSuccess) ||
-      (e = make_planes(p.b, p.dtype, p.offsets, &ws, dev, stream, &b)) != cudaSuccess)
+      (e = make_planes(p.w, p.dtype, nullptr, &ws, dev, stream, &w)) != cudaSuccess)
     return e;
   Params prm = {};
   prm.rows = int(p.rows);
   prm.groups = int(p.groups);
   prm.offsets = p.offsets;
   prm.K = int(p.K);
-  prm.N = int(p.rank);
+  prm.rank = int(p.rank);
   prm.idesc = type_desc(p.dtype);
-  prm.out = u;
-  prm.ld_out = ldu;
-  prm.stride_out = p.rows * ldu;
-  prm.out_type = kOutU;
-  prm.n_out = p.dtype == TMM_F32 ? int(p.rank) : int(ldu / 2);
-  prm.scale = p.scale;
-  // Few rows: a block for every row and 16 ranks; more: a product.
-  e = few ? launch_row_ranks(p, prm, stream)
-          : run_forward(x, index, a, p.groups > 1 && p.a.count == 1, p.trans_a != 0, planes, prm,
-                        dev, stream);
-  if (e != cudaSuccess) return e;
-
+  Maps m;
+  if (cg == 1) {
+    if ((e = launch_row_ranks(p, static_cast<float *>(u), ldu, stream)) != cudaSuccess) return e;
+    prm.row_index = p.row_index;
+    prm.u = static_cast<const float *>(u);
+    prm.ldu = ldu;
+    prm.b = p.b.data;
+    prm.ldb = p.b.ld;
+    prm.stride_b = p.b.count > 1 ? p.b.stride : 0;
+    prm.trans_b = p.trans_b;
+    prm.vec_b = on16(p.b, p.dtype == TMM_F32 ? 4 : 2);
+  } else {
+    Planes a, b;
+    if ((e = make_planes(p.a, p.dtype, p.offsets, &ws, dev, stream, &a)) != cudaSuccess ||
+        (e = make_planes(p.b, p.dtype, p.offsets, &ws, dev, stream, &b)) != cudaSuccess)
+      return e;
+    Params up = prm;
+    up.N = int(p.rank);
+    up.out = u;
+    up.ld_out = ldu;
+    up.stride_out = p.rows * ldu;
+    up.out_type = kOutU;
+    up.n_out = p.dtype == TMM_F32 ? int(p.rank) : int(ldu / 2);
+    up.scale = p.scale;
+    const int32_t *index = gathered ? nullptr : p.row_index;
+    if ((e = run_forward(x, index, a, p.groups > 1 && p.a.count == 1, p.trans_a != 0, planes, up,
+                         dev, stream)) != cudaSuccess)
+      return e;
+    prm.out_index = p.row_index;
+    prm.out_rows = int(p.rows);
+    prm.e_mn = p.trans_b ? 0 : 1;
+    prm.e_shared = p.groups > 1 && p.b.count == 1;
+    const Planes um = {u, planes, p.rows, planes == 3 ? p.rank : ldu, ldu, p.rows * ldu};
+    if ((e = tile_map(&m.e, b, p.trans_b ? 128 : planes == 3 ? 64 : 32)) != cudaSuccess ||
+        (e = row_map(&m.u, um, uint32_t(box_of(cg)))) != cudaSuccess)
+      return e;
+  }
   const int bn = columns_of(cg, planes);
   prm.N = prm.n_out = int(p.N);
-  prm.row_index = index;
-  prm.out_index = p.row_index;
   prm.q_rows = int(x.rows);
-  prm.out_rows = int(p.rows);
-  prm.rank = int(p.rank);
   prm.tile_n = bn;
   prm.panels = int((p.N + 128 * cg - 1) / (128 * cg));
   const int64_t tiles = prm.panels * ((p.rows + bn - 1) / bn);
@@ -1908,20 +2036,13 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   prm.ksplit = cg == 2 ? 1 : split_of(tiles, (p.K + kBK - 1) / kBK, dev);
   prm.p_mn = p.trans_w ? 0 : 1;
   prm.p_shared = 1;
-  prm.e_mn = p.trans_b ? 0 : 1;
-  prm.e_shared = p.groups > 1 && p.b.count == 1;
-  prm.scale = nullptr;
   prm.out = p.y;
   prm.ld_out = p.ldy;
-  prm.stride_out = 0;
   prm.out_type = out_type(p.dtype);
-  const Planes up = {u, planes, p.rows, planes == 3 ? p.rank : ldu, ldu, p.rows * ldu};
-  Maps m;
   if ((e = tile_map(&m.p, w, p.trans_w ? 128 : 64)) != cudaSuccess ||
-      (e = q_maps(&m, x, index, cg, bn)) != cudaSuccess ||
-      (e = tile_map(&m.e, b, p.trans_b ? 128 : planes == 3 ? 64 : 32)) != cudaSuccess ||
-      (e = row_map(&m.u, up, uint32_t(box_of(cg)))) != cudaSuccess)
+      (e = q_maps(&m, x, nullptr, cg, bn)) != cudaSuccess)
     return e;
+  if (cg == 1) m.e = m.u = m.p;
   return launch_any(cg, planes, kLora, m, prm, tiles, dev, stream);
 }
 
