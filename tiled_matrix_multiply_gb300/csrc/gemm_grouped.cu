@@ -621,25 +621,32 @@ __device__ __forceinline__ void store_columns(const Params &p, const Tile &t, in
   }
 }
 
-// Eight values from p, those from `left` on as zeros; vec: p is on a 16-byte boundary.
+// Eight values as they are stored, 16 bytes or 32.
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, int64_t left, int vec, float (&v)[8]) {
-  if (left >= 8 && vec) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 a = *reinterpret_cast<const float4 *>(p);
-      const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-      const uint4 a = *reinterpret_cast<const uint4 *>(p);
-      const T *t = reinterpret_cast<const T *>(&a);
+struct Eight {
+  uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ float get(int i) const {
+    return float(reinterpret_cast<const T *>(w)[i]);
+  }
+};
+// Eight values from p, those from `left` on (and all without `on`) as zeros.  VEC: p is on a
+// 16-byte boundary and left >= 8.
+template <bool VEC, typename T>
+__device__ __forceinline__ Eight<T> load8(const T *p, bool on, int64_t left) {
+  Eight<T> v;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = float(t[j]);
+  for (int i = 0; i < int(sizeof(T) / 2); ++i) v.w[i] = make_uint4(0, 0, 0, 0);
+  if constexpr (VEC) {
+    if (on) {
+#pragma unroll
+      for (int i = 0; i < int(sizeof(T) / 2); ++i) v.w[i] = reinterpret_cast<const uint4 *>(p)[i];
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < left ? float(p[j]) : 0.0f;
+    for (int j = 0; j < 8; ++j)
+      if (on && j < left) reinterpret_cast<T *>(v.w)[j] = p[j];
   }
+  return v;
 }
 
 // All threads of the result warps.
@@ -650,14 +657,14 @@ __device__ __forceinline__ void results_sync() {
 // The adapters' part of columns [c0, c1) of a tile (rows of x), to sums[column][lane]:
 // sum_j u[row, j] b[g, j, n].  Few rows: b is read once per row and lane, on the CUDA cores,
 // while the weights stream: `rank` loads of 16 bytes a thread in flight for eight n of one row.
-template <typename T>
-__device__ __forceinline__ void add_adapters(const Params &p, const int *owner, const Tile &t,
-                                             int c0, int c1, float *sums) {
-  grid_wait();      // u is the launch before's
+template <typename T, bool VEC>
+__device__ __forceinline__ void add_adapters_as(const Params &p, const int *owner, const Tile &t,
+                                                int c0, int c1, float *sums) {
   const int tid = int(threadIdx.x) - 32 * kEpi0;
   const T *const b = static_cast<const T *>(p.b);
+  constexpr int kAhead = VEC ? (sizeof(T) == 2 ? 16 : 8) : 2;      // loads in flight
   if (!p.trans_b) {
-    // b stored rank x N.
+    // b stored rank x N: 16 threads a row, eight n each.
     const int l = (tid & 15) * 8, n = t.n0 + l;
     for (int col = c0 + (tid >> 4); col < c1; col += 32 * kEpiWarps / 16) {
       float v[8] = {};
@@ -665,13 +672,20 @@ __device__ __forceinline__ void add_adapters(const Params &p, const int *owner, 
       if (g >= 0 && n < p.N) {
         const T *const bn = b + int64_t(g) * p.stride_b + n;
         const float *const u = p.u + int64_t(t.q0 + col) * p.ldu;
-#pragma unroll 8
-        for (int j = 0; j < p.rank; ++j) {
-          float w[8];
-          load8(bn + j * p.ldb, p.N - n, p.vec_b, w);
-          const float f = u[j];
+        for (int j0 = 0; j0 < p.rank; j0 += kAhead) {
+          Eight<T> w[kAhead];
+          float f[kAhead];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = fmaf(f, w[i], v[i]);
+          for (int j = 0; j < kAhead; ++j) {
+            const bool on = j0 + j < p.rank;
+            w[j] = load8<VEC>(bn + int64_t(j0 + j) * p.ldb, on, p.N - n);
+            f[j] = on ? u[j0 + j] : 0.0f;
+          }
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j)
+            if (VEC || j0 + j < p.rank)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = fmaf(f[j], w[j].get(i), v[i]);
         }
       }
       float4 *const to = reinterpret_cast<float4 *>(sums + col * 128 + l);
@@ -679,7 +693,7 @@ __device__ __forceinline__ void add_adapters(const Params &p, const int *owner, 
       to[1] = make_float4(v[4], v[5], v[6], v[7]);
     }
   } else {
-    // b stored N x rank.
+    // b stored N x rank: a thread an n, eight ranks at a time.
     const int l = tid & 127, n = t.n0 + l;
     for (int col = c0 + (tid >> 7); col < c1; col += 32 * kEpiWarps / 128) {
       float v = 0.0f;
@@ -687,18 +701,29 @@ __device__ __forceinline__ void add_adapters(const Params &p, const int *owner, 
       if (g >= 0 && n < p.N) {
         const T *const bn = b + int64_t(g) * p.stride_b + int64_t(n) * p.ldb;
         const float *const u = p.u + int64_t(t.q0 + col) * p.ldu;
-#pragma unroll 4
-        for (int j = 0; j < p.rank; j += 8) {
-          float w[8], f[8];
-          load8(bn + j, p.rank - j, p.vec_b, w);
-          load8(u + j, p.rank - j, 1, f);
+        constexpr int kNow = kAhead / 2;
+        for (int j0 = 0; j0 < p.rank; j0 += 8 * kNow) {
+          Eight<T> w[kNow];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v = fmaf(f[i], w[i], v);
+          for (int j = 0; j < kNow; ++j)
+            w[j] = load8<VEC>(bn + j0 + 8 * j, j0 + 8 * j < p.rank, p.rank - j0 - 8 * j);
+#pragma unroll
+          for (int j = 0; j < kNow; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (j0 + 8 * j + i < p.rank) v = fmaf(u[j0 + 8 * j + i], w[j].get(i), v);
         }
       }
       sums[col * 128 + l] = v;
     }
   }
+}
+template <typename T>
+__device__ __forceinline__ void add_adapters(const Params &p, const int *owner, const Tile &t,
+                                             int c0, int c1, float *sums) {
+  grid_wait();      // u is the launch before's
+  if (p.vec_b) add_adapters_as<T, true>(p, owner, t, c0, c1, sums);
+  else add_adapters_as<T, false>(p, owner, t, c0, c1, sums);
 }
 
 // ---- kernel -----------------------------------------------------------------------------
@@ -1512,75 +1537,86 @@ constexpr int kRowRanks = 16;            // values of u a block makes
 // (512 threads, 16 bytes each, K / 256 rounds) instead of a product kernel's ring of slices, and
 // rows that share an adapter read it from L2.  FP32 throughout; sums of 512 threads in a fixed
 // order.  64 rows of 64 adapters, K = 4096, rank 16 bf16: see the adapters' figures.
-template <typename T, bool TRANS_A>
+template <typename T, bool TRANS_A, bool VEC>
 __global__ void __launch_bounds__(kRowThreads)
-row_ranks_kernel(const T *__restrict__ x, int64_t ldx, int64_t x_rows, int vec_x,
+row_ranks_kernel(const T *__restrict__ x, int64_t ldx, int64_t x_rows,
                  const int *__restrict__ row_index, const int *__restrict__ offsets, int groups,
-                 const T *__restrict__ a, int64_t lda, int64_t stride_a, int vec_a,
+                 const T *__restrict__ a, int64_t lda, int64_t stride_a,
                  const float *__restrict__ scale, int K, int rank, float *__restrict__ u,
                  int64_t ldu) {
   grid_wait();
   grid_start_next();
   __shared__ float sums[kRowThreads / 32][kRowRanks];
-  __shared__ int owner;
   const int p = blockIdx.x, j0 = blockIdx.y * kRowRanks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // The group of row p: the first whose end is past p (with ends that never step back, and the
-  // first start not past it).
-  if (threadIdx.x == 0) owner = groups;
-  __syncthreads();
-  for (int g = threadIdx.x; g < groups; g += kRowThreads)
-    if (offsets[g + 1] > p) atomicMin(&owner, g);
-  __syncthreads();
-  const int g = owner;
-  if (g == groups || offsets[0] > p) return;
+  // The group of place p: the first whose end is past p (ends never step back, and the first
+  // start must not be past p).  Every warp looks for itself.
   const int64_t row = row_index ? row_index[p] : p;
-  const bool have = row >= 0 && row < x_rows;
-  const T *const xr = x + (have ? row : 0) * ldx;
+  const int start = offsets[0];
+  int g = groups;
+  for (int g0 = 0; g0 < groups && g == groups; g0 += 32) {
+    const bool past = g0 + lane < groups && offsets[g0 + lane + 1] > p;
+    const unsigned any = __ballot_sync(~0u, past);
+    if (any) g = g0 + __ffs(any) - 1;
+  }
+  if (g == groups || start > p || row < 0 || row >= x_rows) return;
+  const T *const xr = x + row * ldx;
   const T *const ag = a + int64_t(g) * stride_a;
   const int ranks = min(kRowRanks, rank - j0);
+  constexpr int kAhead = VEC ? 8 : 2;      // loads in flight
   if constexpr (TRANS_A) {
     // a stored rank x K: a warp a rank, 256 k a round.
-    for (int j = warp; j < kRowRanks; j += kRowThreads / 32) {
-      float sum = 0.0f;
-      if (j < ranks && have) {
-        const T *const aj = ag + int64_t(j0 + j) * lda;
-#pragma unroll 4
-        for (int k = lane * 8; k < K; k += 256) {
-          float w[8], v[8];
-          load8(aj + k, K - k, vec_a, w);
-          load8(xr + k, K - k, vec_x, v);
+    static_assert(kRowRanks == kRowThreads / 32, "a rank for every warp");
+    float sum = 0.0f;
+    if (warp < ranks) {
+      const T *const aj = ag + int64_t(j0 + warp) * lda;
+      for (int k0 = lane * 8; k0 < K; k0 += 256 * kAhead) {
+        Eight<T> w[kAhead], v[kAhead];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum = fmaf(w[i], v[i], sum);
+        for (int i = 0; i < kAhead; ++i) {
+          const int k = k0 + 256 * i;
+          w[i] = load8<VEC>(aj + k, k < K, K - k);
+          v[i] = load8<VEC>(xr + k, k < K, K - k);
         }
-      }
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-      if (lane == 0) sums[0][j] = sum;
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (k0 + 256 * i + e < K) sum = fmaf(w[i].get(e), v[i].get(e), sum);
+      }
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+    if (lane == 0) sums[0][warp] = sum;
   } else {
     // a stored K x rank: two threads a k, eight ranks each, 256 k a round.
     const int half = threadIdx.x & 1;
+    const int left = ranks - 8 * half;
     float sum[8] = {};
-    if (have) {
-#pragma unroll 8
-      for (int k = threadIdx.x >> 1; k < K; k += kRowThreads / 2) {
-        float w[8];
-        load8(ag + int64_t(k) * lda + j0 + 8 * half, ranks - 8 * half, vec_a, w);
-        const float v = float(xr[k]);
+    for (int k0 = threadIdx.x >> 1; k0 < K && left > 0; k0 += kRowThreads / 2 * kAhead) {
+      Eight<T> w[kAhead];
+      float v[kAhead];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[i], v, sum[i]);
+      for (int i = 0; i < kAhead; ++i) {
+        const int k = k0 + kRowThreads / 2 * i;
+        w[i] = load8<VEC>(ag + int64_t(k) * lda + j0 + 8 * half, k < K, left);
+        v[i] = k < K ? float(xr[k]) : 0.0f;
       }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (k0 + kRowThreads / 2 * i < K)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[e] = fmaf(w[i].get(e), v[i], sum[e]);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int e = 0; e < 8; ++e) {
 #pragma unroll
-      for (int d = 16; d > 1; d >>= 1) sum[i] += __shfl_xor_sync(~0u, sum[i], d);
-      if (lane < 2) sums[warp][8 * lane + i] = sum[i];
+      for (int d = 16; d > 1; d >>= 1) sum[e] += __shfl_xor_sync(~0u, sum[e], d);
+      if (lane < 2) sums[warp][8 * lane + e] = sum[e];
     }
   }
   __syncthreads();
-  if (int(threadIdx.x) < ranks && have) {
+  if (int(threadIdx.x) < ranks) {
     float v = 0.0f;
     if constexpr (TRANS_A) {
       v = sums[0][threadIdx.x];
@@ -1926,13 +1962,17 @@ static cudaError_t launch_row_ranks_as(const LoraProblem &p, float *u, int64_t l
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, row_ranks_kernel<T, TRANS_A>, static_cast<const T *>(p.x.data),
-                            p.x.ld, p.x.rows, on16(p.x, sizeof(T)),
+  // Whole vectors: rows on 16-byte boundaries, and eight values at a time end with the rows.
+  const bool vec = on16(p.a, sizeof(T)) && (!TRANS_A || on16(p.x, sizeof(T))) && p.a.cols % 8 == 0;
+  return cudaLaunchKernelEx(&cfg,
+                            vec ? row_ranks_kernel<T, TRANS_A, true>
+                                : row_ranks_kernel<T, TRANS_A, false>,
+                            static_cast<const T *>(p.x.data), p.x.ld, p.x.rows,
                             static_cast<const int *>(p.row_index),
                             static_cast<const int *>(p.offsets), int(p.groups),
                             static_cast<const T *>(p.a.data), p.a.ld,
-                            p.a.count > 1 ? p.a.stride : int64_t(0), on16(p.a, sizeof(T)), p.scale,
-                            int(p.K), int(p.rank), u, ldu);
+                            p.a.count > 1 ? p.a.stride : int64_t(0), p.scale, int(p.K),
+                            int(p.rank), u, ldu);
 }
 
 static cudaError_t launch_row_ranks(const LoraProblem &p, float *u, int64_t ldu,
@@ -1999,7 +2039,7 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
     prm.ldb = p.b.ld;
     prm.stride_b = p.b.count > 1 ? p.b.stride : 0;
     prm.trans_b = p.trans_b;
-    prm.vec_b = on16(p.b, p.dtype == TMM_F32 ? 4 : 2);
+    prm.vec_b = on16(p.b, p.dtype == TMM_F32 ? 4 : 2) && p.b.cols % 8 == 0;
   } else {
     Planes a, b;
     if ((e = make_planes(p.a, p.dtype, p.offsets, &ws, dev, stream, &a)) != cudaSuccess ||
