@@ -127,6 +127,10 @@ struct Params {
   const float *u;
   const void *b;
   int64_t ldu, ldb, stride_b;
+  // Adapters on pairs: u holds the rows of the list's entry e from place + e * slot_n on, so that
+  // every tile of the product finds the rows of each of its adapters at the tile's own places,
+  // with zeros for the others (slot_n: the product's tile_n; 0: plain rows).
+  int slot_n, u_rows;
   int trans_b, vec_b;
   int zero_rows;         // forward: write zeros to the rows of no group
   int ksplit;            // blocks of a cluster that share a tile's sum (CG = 1)
@@ -369,7 +373,8 @@ struct Tile {
   int q0, qn;     // columns of the tile
   int bn;         // qn rounded up for the tensor core
   int k0, klen;
-  int e0, en;     // adapters with rows in the tile: list entries [e0, e0 + en)
+  int e0, en;     // adapters: list entries with rows in the tile, [e0, e0 + en); forward: the
+                  // group's entry e0
 };
 
 // The tables in shared memory: the groups that have rows (every group in the gradient): number,
@@ -412,6 +417,7 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const Table &tab, int t
       else b = m;
     }
     r.g = tab.gid[a];
+    r.e0 = a;
     lo = tab.row[a];
     hi = tab.row[a + 1];
     i = t - tab.tile[a];
@@ -528,6 +534,7 @@ template <int MODE>
 __device__ __forceinline__ int64_t out_row(const Params &p, const Tile &t, int col) {
   if (MODE == kWgrad) return int64_t(t.g) * p.stride_out + int64_t(t.q0 + col) * p.ld_out;
   int r = t.q0 + col;
+  if (MODE == kForward) r += t.e0 * p.slot_n;
   if (MODE == kLora && p.out_index) {
     r = p.out_index[r];
     if (r < 0 || r >= p.out_rows) return -1;
@@ -549,10 +556,7 @@ __device__ __forceinline__ void store_columns(const Params &p, const Tile &t, in
   const bool by_row = MODE == kLora && p.out_index;
   const bool check = MODE == kLora && p.u;      // rows that are not written (see owner)
   int64_t first = 0;
-  if (!by_row) {
-    first = out_row<kForward>(p, t, c0);
-    if (MODE == kWgrad) first += int64_t(t.g) * p.stride_out;
-  }
+  if (!by_row) first = out_row<MODE>(p, t, c0);
   if constexpr (PLANES == 1) {
     if (p.vec_out) {
       uint16_t h[16];
@@ -741,7 +745,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   // The adapters' part: pairs extend the sum (EXT); single blocks, whose rows are few, add it to
   // the results on the CUDA cores while the weights stream (FEW).
   constexpr bool EXT = MODE == kLora && CG == 2, FEW = MODE == kLora && CG == 1;
-  constexpr bool PATCH = EXT || MODE == kWgrad;      // some slices get rows of zeros
+  constexpr bool PATCH = MODE == kWgrad;      // some slices get rows of zeros
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;    // the same offset in every block
@@ -917,6 +921,26 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     }
   }
 
+  if (MODE == kForward && p.slot_n && warp >= kEpi0 && warp < kMmaWarp) {
+    // u: zeros at the other places of the tiles in which an entry has rows, a warp a row.
+    const int bn = p.slot_n;
+    for (int i = int(blockIdx.x) * kEpiWarps + warp - kEpi0; i < tab.count * 2 * bn;
+         i += int(gridDim.x) * kEpiWarps) {
+      const int e = i / (2 * bn), k = i - e * 2 * bn;
+      const int lo = tab.row[e], hi = tab.row[e + 1];
+      // Places of the first tile before lo, then those of the last one from hi on.
+      const int at = k < bn ? lo / bn * bn + k : hi + (k - bn);
+      const bool zero = k < bn ? at < lo : at < min((hi + bn - 1) / bn * bn, p.rows);
+      if (!zero) continue;
+      for (int pl = 0; pl < PLANES; ++pl) {
+        uint16_t *const row = static_cast<uint16_t *>(p.out) + pl * p.stride_out +
+                              (int64_t(at) + int64_t(e) * bn) * p.ld_out;
+        for (int n = lane * 8; n < p.ld_out; n += 256)
+          *reinterpret_cast<uint4 *>(row + n) = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+
   for (int t = cluster; t < tab.tiles; t += clusters) {
     if (timed_out && p.ksplit == 1 && !FEW) break;     // (else warps meet at every tile)
     const Tile tile = tile_at<CG, MODE, PLANES>(p, tab, t);
@@ -949,16 +973,16 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                                                             (S::kBox * 128)));
       }
 
-      // What a slice s is.  Slices of the adapters' part and a group's last one may need rows of
-      // zeros: their copies are counted by the block's own bar_patch, a warp zeroes the rows, and
-      // only then does the block arrive on the leader's bar_full.
+      // What a slice s is.  A group's last slice in the gradient needs rows of zeros: its copies
+      // are counted by the block's own bar_patch, a warp zeroes the rows, and only then does the
+      // block arrive on the leader's bar_full.
       struct Slice {
         bool ext;
-        int k0, g, gcount, rank0, lo, hi;   // ext: rows of u in [lo, hi) belong to the adapter
+        int k0, g, gcount, rank0, row;      // ext: ranks from rank0, rows of u from row
         int cnt;                            // gradient: rows of the group
       };
       const auto slice_at = [&](int s) {
-        Slice c = {EXT && s >= nbase, s * kBK, pg, pcount, 0, 0, 0, kBK};
+        Slice c = {EXT && s >= nbase, s * kBK, pg, pcount, 0, 0, kBK};
         if (MODE == kWgrad) {
           c.k0 += tile.k0;
           c.cnt = min(kBK, tile.klen - s * kBK);
@@ -969,8 +993,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           c.rank0 = j * S::kRankSlice;       // of b
           c.g = p.e_shared ? 0 : tab.gid[tile.e0 + e];
           c.gcount = p.e_shared ? 1 : p.groups;
-          c.lo = tab.row[tile.e0 + e];
-          c.hi = tab.row[tile.e0 + e + 1];
+          c.row = qf + (tile.e0 + e) * p.tile_n;
         }
         return c;
       };
@@ -981,11 +1004,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         return PLANES * ((p.e_mn ? 2 * S::kRankSlice * 128 : kPTile) +
                          uint32_t((held(half) + S::kBox - 1) / S::kBox * (S::kBox * 128)));
       };
-      const auto patch_of = [&](const Slice &c, int half) {
-        if (MODE == kWgrad) return c.cnt < kBK;
-        const int q = tile.q0 + half * hr;
-        return EXT && c.ext && held(half) > 0 && (c.lo > q || c.hi < q + held(half));
-      };
+      const auto patch_of = [&](const Slice &c) { return MODE == kWgrad && c.cnt < kBK; };
       // A slice that slice_at describes as ordinary in every respect.
       const auto is_plain = [&](int s) {
         if (MODE == kWgrad) return (s + 1) * kBK <= tile.klen;
@@ -1036,7 +1055,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           for (int pl = 0; pl < PLANES; ++pl)
             for (int b = 0; b < boxes; ++b)
               tma_2d<CG>(sq + pl * S::kQTile + b * (S::kBox * 128), &map_u, c.k0,
-                         qf + b * S::kBox + pl * p.rows, bar);
+                         c.row + b * S::kBox + pl * p.u_rows, bar);
         } else if (CG == 2 && mine * CG == p.tile_n) {
           // A full tile: one copy a plane.
 #pragma unroll
@@ -1051,44 +1070,30 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       };
       // The expectations of one slice (one thread, before or while its copies arrive).
       const auto announce = [&](const Slice &c, int stage) {
-        const bool patch = patch_of(c, half_rank);
+        if (patch_of(c)) {
+          mbar_expect(bar_patch + 8 * stage, bytes_of(c, half_rank));
+          if (leader && dropped) mbar_expect_only(bar_full + 8 * stage, 16);
+          dropped = false;
+          return;
+        }
         uint32_t bytes = 0;
 #pragma unroll
-        for (int h = 0; h < CG; ++h)
-          if (!patch_of(c, h)) bytes += bytes_of(c, h);
-        if (patch) mbar_expect(bar_patch + 8 * stage, bytes_of(c, half_rank));
-        if (leader) {
-          if (!patch) expect(stage, bytes);
-          else if (bytes) mbar_expect_only(bar_full + 8 * stage, bytes);
-        } else if (!patch) {
-          mbar_arrive_relaxed(full_at(stage));
-        }
-        if (leader && patch && dropped) {
-          mbar_expect_only(bar_full + 8 * stage, 16);
-          dropped = false;
-        }
+        for (int h = 0; h < CG; ++h) bytes += bytes_of(c, h);
+        if (leader) expect(stage, bytes);
+        else if (PATCH) mbar_arrive_relaxed(full_at(stage));
       };
       // Zeroes a slice's rows that do not count, once its copies are here (a whole warp).
       const auto patch_rows = [&](const Slice &c, int stage, uint32_t parity) {
         const uint32_t st = base + stage * S::kStage, sq = st + PLANES * kPTile;
         const bool ok = mbar_wait(bar_patch + 8 * stage, parity, p.wait_limit_ns);
         if (!__all_sync(~0u, ok)) return false;
-        if (MODE == kWgrad) {
-          // Rows [cnt, the next multiple of 16): past the group's end.
-          const int n = 8 * (((c.cnt + 15) & ~15) - c.cnt);
-          for (int i = lane; i < n; i += 32) {
-            const uint32_t at = uint32_t(c.cnt * 128 + i * 16);
-            for (int b = 0; b < 2 * PLANES; ++b) zero16(st + b * 8192 + at);
-            for (int pl = 0; pl < PLANES; ++pl)
-              for (int b = 0; b < qblocks; ++b) zero16(sq + pl * S::kQTile + b * 8192 + at);
-          }
-        } else {
-          // Rows of u of other adapters.
-          for (int i = lane; i < 8 * mine; i += 32) {
-            const int at = qf + (i >> 3);
-            if (at < c.lo || at >= c.hi)
-              for (int pl = 0; pl < PLANES; ++pl) zero16(sq + pl * S::kQTile + i * 16);
-          }
+        // Rows [cnt, the next multiple of 16): past the group's end.
+        const int n = 8 * (((c.cnt + 15) & ~15) - c.cnt);
+        for (int i = lane; i < n; i += 32) {
+          const uint32_t at = uint32_t(c.cnt * 128 + i * 16);
+          for (int b = 0; b < 2 * PLANES; ++b) zero16(st + b * 8192 + at);
+          for (int pl = 0; pl < PLANES; ++pl)
+            for (int b = 0; b < qblocks; ++b) zero16(sq + pl * S::kQTile + b * 8192 + at);
         }
         proxy_fence();
         __syncwarp();
@@ -1110,7 +1115,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                 break;
               }
               if (is_plain(s)) {
-                const Slice c = {false, MODE == kWgrad ? tile.k0 + s * kBK : s * kBK, 0, 0, 0, 0, 0,
+                const Slice c = {false, MODE == kWgrad ? tile.k0 + s * kBK : s * kBK, 0, 0, 0, 0,
                                  kBK};
                 const uint32_t full = full_at(ring.stage);
                 if (warp == 0) {
@@ -1124,7 +1129,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                 if (EXT) grid_wait();
                 const Slice c = slice_at(s);
                 const uint32_t bar =
-                    patch_of(c, half_rank) ? bar_patch + 8 * ring.stage : full_at(ring.stage);
+                    patch_of(c) ? bar_patch + 8 * ring.stage : full_at(ring.stage);
                 if (warp == 0) {
                   announce(c, ring.stage);
                   copy_p(c, st, bar);
@@ -1140,12 +1145,11 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         } else if (PATCH) {
           Ring at = ring;
           int s = s0;
-          if (EXT && nbase > s0) s = min(nbase, s1);
-          if (MODE == kWgrad && s1 > s0) s = is_plain(s1 - 1) ? s1 : s1 - 1;
+          if (s1 > s0) s = is_plain(s1 - 1) ? s1 : s1 - 1;      // only the last can need it
           at.template skip<S::kStages>(s - s0);
           for (; s < s1 && !timed_out; ++s) {
             const Slice c = slice_at(s);
-            if (patch_of(c, half_rank)) {
+            if (patch_of(c)) {
               const uint32_t parity = (patched >> at.stage) & 1u;
               patched ^= 1u << at.stage;
               if (warp == 2 + (at.stage & 1)) timed_out = !patch_rows(c, at.stage, parity);
@@ -1183,7 +1187,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
             break;
           }
           const Slice c = slice_at(s);
-          const bool patch = patch_of(c, 0);
+          const bool patch = patch_of(c);
           const uint32_t bar = patch ? bar_patch + 8 * ring.stage : bar_full + 8 * ring.stage;
           if (warp == 0 && elect_one()) {
             if (is_plain(s) && MODE != kWgrad) expect(ring.stage, usual);
@@ -1992,9 +1996,15 @@ static cudaError_t launch_row_ranks(const LoraProblem &p, float *u, int64_t ldu,
 static int64_t u_columns(const LoraProblem &p) {
   return p.dtype == TMM_F32 || lora_shape(p.rows) == 1 ? round8(p.rank) : (p.rank + 31) / 32 * 64;
 }
+// Rows of u: on pairs, room for every adapter's part of every tile.
+static int64_t u_rows(const LoraProblem &p) {
+  if (lora_shape(p.rows) == 1) return p.rows;
+  const int64_t bn = columns_of(2, p.dtype == TMM_F32 ? 3 : 1);
+  return ((p.rows + bn - 1) / bn + p.groups) * bn;
+}
 static size_t u_bytes(const LoraProblem &p) {
   const int size = lora_shape(p.rows) == 1 ? 4 : p.dtype == TMM_F32 ? 6 : 2;
-  return round256(size_t(p.rows) * size_t(u_columns(p)) * size);   // below 2^29 * 2^11 * 6
+  return round256(size_t(u_rows(p)) * size_t(u_columns(p)) * size);   // below 2^30 * 2^11 * 6
 }
 
 // The workspace holds u and the planes of the operands.
@@ -2049,9 +2059,11 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
     up.N = int(p.rank);
     up.out = u;
     up.ld_out = ldu;
-    up.stride_out = p.rows * ldu;
+    up.stride_out = u_rows(p) * ldu;
+    up.slot_n = columns_of(2, planes);
     up.out_type = kOutU;
     up.n_out = p.dtype == TMM_F32 ? int(p.rank) : int(ldu / 2);
+    if (u_rows(p) * planes > INT32_MAX) return cudaErrorInvalidConfiguration;
     up.scale = p.scale;
     const int32_t *index = gathered ? nullptr : p.row_index;
     if ((e = run_forward(x, index, a, p.groups > 1 && p.a.count == 1, p.trans_a != 0, planes, up,
@@ -2059,9 +2071,10 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
       return e;
     prm.out_index = p.row_index;
     prm.out_rows = int(p.rows);
+    prm.u_rows = int(u_rows(p));
     prm.e_mn = p.trans_b ? 0 : 1;
     prm.e_shared = p.groups > 1 && p.b.count == 1;
-    const Planes um = {u, planes, p.rows, planes == 3 ? p.rank : ldu, ldu, p.rows * ldu};
+    const Planes um = {u, planes, u_rows(p), planes == 3 ? p.rank : ldu, ldu, u_rows(p) * ldu};
     if ((e = tile_map(&m.e, b, p.trans_b ? 128 : planes == 3 ? 64 : 32)) != cudaSuccess ||
         (e = row_map(&m.u, um, uint32_t(box_of(cg)))) != cudaSuccess)
       return e;
