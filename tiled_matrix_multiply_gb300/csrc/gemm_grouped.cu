@@ -1807,19 +1807,45 @@ int out_type(int dtype) {
 int box_of(int cg) { return cg == 2 ? 32 : 16; }
 int columns_of(int cg, int planes) { return cg == 1 ? 64 : planes == 3 ? 128 : 256; }
 
-// Blocks that share a tile's sum: the largest power of two up to eight that still leaves every
-// block four slices and the cluster's blocks resident together.
-int split_of(int64_t tiles, int64_t slices, const DeviceInfo &dev) {
+// Blocks that share a tile's sum: the largest power of two up to eight that leaves every block
+// enough slices to pay for meeting, about 3 us, and the cluster's blocks resident together.  16
+// slices of 16-bit operands take about that long (K = 512 in two groups of 32 rows, N = 320: 9.7 us
+// shared by two, 6.6 us not), four of split ones (64 rows of K = 1000, N = 2047 with adapters: 48 us
+// not shared, 27 us by four).
+int split_slices(int planes) { return planes == 3 ? 4 : 16; }
+int split_of(int64_t tiles, int64_t slices, int planes, const DeviceInfo &dev) {
   int s = 1;
-  while (s < 8 && tiles * (2 * s) <= dev.sm_count && slices >= 4 * (2 * s)) s *= 2;
+  while (s < 8 && tiles * (2 * s) <= dev.sm_count && slices >= split_slices(planes) * (2 * s))
+    s *= 2;
   return s;
 }
 
-// Pairs from 64 rows per group on average, if their 256 lanes have something to hold.
-int forward_shape(int64_t rows, int64_t groups, int64_t N) {
-  return rows > 64 * groups && N > 128 ? 2 : 1;
+// Pairs or single blocks for a forward product, by the cycles a K slice of 64 takes in a tile and
+// the rounds of tiles, for groups of equal size: products at 8192 multiply-adds a cycle and SM,
+// copies at 64 bytes.  (Counted per plane product: 16-bit operands have one, split ones six of
+// three planes.)
+int forward_shape(int64_t rows, int64_t groups, int64_t N, int64_t K, int dtype) {
+  if (N <= 128) return 1;      // 256 lanes would be half empty
+  constexpr int64_t kSms = 152;
+  const int planes = dtype == TMM_F32 ? 3 : 1, products = dtype == TMM_F32 ? 6 : 1;
+  const int64_t live = std::max<int64_t>(1, std::min(groups, rows));
+  const int64_t each = (rows + live - 1) / live;
+  const auto cost = [&](int cg, int64_t widest, int64_t unit) {
+    const int64_t across = (each + widest - 1) / widest;
+    const int64_t cols = ((each + across - 1) / across + unit - 1) / unit * unit;
+    const int64_t tiles = live * across * ((N + 128 * cg - 1) / (128 * cg));
+    const int64_t slice = std::max(products * 2 * cols, planes * (256 + 2 * cols / cg));
+    // Fewer tiles than blocks: single blocks split a long sum.
+    if (cg == 1 && 2 * tiles <= kSms && K >= 2 * split_slices(planes) * kBK)
+      return slice * tiles / kSms + slice / 8;
+    return (tiles + kSms / cg - 1) / (kSms / cg) * slice;
+  };
+  return cost(2, dtype == TMM_F32 ? 128 : 256, 64) <= cost(1, 64, 16) ? 2 : 1;
 }
-int lora_shape(int64_t rows) { return rows > kFewRows ? 2 : 1; }
+// Adapters: single blocks while the part on the CUDA cores (rows x rank) is small.
+int lora_shape(int64_t rows, int64_t rank) {
+  return rows <= 64 || (rows <= kFewRows && rows * rank <= 8192) ? 1 : 2;
+}
 int wgrad_shape(int64_t N) { return N > 128 ? 2 : 1; }
 
 // The maps of x: rows by number; or tiles of box_of rows, and (pairs) of a whole block's columns.
@@ -1840,14 +1866,15 @@ cudaError_t q_maps(Maps *m, const Planes &x, const int32_t *index, int cg, int b
 cudaError_t run_forward(const Planes &x, const int32_t *index, const Planes &w, bool shared_w,
                         bool trans_w, int planes, Params prm, const DeviceInfo &dev,
                         cudaStream_t stream) {
-  const int cg = forward_shape(prm.rows, prm.groups, prm.N);
+  const int cg = forward_shape(prm.rows, prm.groups, prm.N, prm.K,
+                               planes == 3 ? TMM_F32 : TMM_BF16);
   const int bn = columns_of(cg, planes);
   prm.tile_n = bn;
   prm.panels = int((prm.N + 128 * cg - 1) / (128 * cg));
   const int64_t tiles =
       prm.panels * (std::min<int64_t>(prm.groups, prm.rows) + prm.rows / bn);
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
-  prm.ksplit = cg == 2 ? 1 : split_of(tiles, (prm.K + kBK - 1) / kBK, dev);
+  prm.ksplit = cg == 2 ? 1 : split_of(tiles, (prm.K + kBK - 1) / kBK, planes, dev);
   if (prm.n_out == 0) prm.n_out = prm.N;
   prm.row_index = index;
   prm.q_rows = int(x.rows);
@@ -1872,7 +1899,7 @@ static int64_t gathered_rows(int cg, const int32_t *row_index, int64_t rows) {
 
 size_t grouped_workspace_bytes(const GroupedProblem &p) {
   const int64_t gathered =
-      gathered_rows(forward_shape(p.rows, p.groups, p.N), p.row_index, p.rows);
+      gathered_rows(forward_shape(p.rows, p.groups, p.N, p.K, p.dtype), p.row_index, p.rows);
   return add_sizes({plane_bytes(p.x, p.dtype, gathered), plane_bytes(p.w, p.dtype)});
 }
 
@@ -1881,7 +1908,7 @@ cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void 
   char *ws = static_cast<char *>(workspace);
   const bool shared = p.groups > 1 && p.w.count == 1;
   const int64_t gathered =
-      gathered_rows(forward_shape(p.rows, p.groups, p.N), p.row_index, p.rows);
+      gathered_rows(forward_shape(p.rows, p.groups, p.N, p.K, p.dtype), p.row_index, p.rows);
   Planes x, w;
   cudaError_t e;
   if ((e = make_planes(p.x, p.dtype, nullptr, &ws, dev, stream, &x, gathered, p.row_index)) !=
@@ -1943,7 +1970,7 @@ cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *wor
   prm.panels = int((p.N + 128 * cg - 1) / (128 * cg));
   const int64_t tiles = p.groups * prm.panels * ((p.K + bn - 1) / bn);
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
-  if (cg == 1) prm.ksplit = split_of(tiles, (p.rows / p.groups + kBK - 1) / kBK, dev);
+  if (cg == 1) prm.ksplit = split_of(tiles, (p.rows / p.groups + kBK - 1) / kBK, planes, dev);
   Maps m;
   if ((e = row_map(&m.p, dy, kBK)) != cudaSuccess ||
       (e = index ? row_map(&m.qr, x, 1) : row_map(&m.q, x, kBK)) != cudaSuccess)
@@ -1994,22 +2021,22 @@ static cudaError_t launch_row_ranks(const LoraProblem &p, float *u, int64_t ldu,
 // Columns of u: FP32 values on single blocks; for pairs a plane's 16-byte rows, or pairs of 16-bit
 // values in blocks of 32 + 32.
 static int64_t u_columns(const LoraProblem &p) {
-  return p.dtype == TMM_F32 || lora_shape(p.rows) == 1 ? round8(p.rank) : (p.rank + 31) / 32 * 64;
+  return p.dtype == TMM_F32 || lora_shape(p.rows, p.rank) == 1 ? round8(p.rank) : (p.rank + 31) / 32 * 64;
 }
 // Rows of u: on pairs, room for every adapter's part of every tile.
 static int64_t u_rows(const LoraProblem &p) {
-  if (lora_shape(p.rows) == 1) return p.rows;
+  if (lora_shape(p.rows, p.rank) == 1) return p.rows;
   const int64_t bn = columns_of(2, p.dtype == TMM_F32 ? 3 : 1);
   return ((p.rows + bn - 1) / bn + p.groups) * bn;
 }
 static size_t u_bytes(const LoraProblem &p) {
-  const int size = lora_shape(p.rows) == 1 ? 4 : p.dtype == TMM_F32 ? 6 : 2;
+  const int size = lora_shape(p.rows, p.rank) == 1 ? 4 : p.dtype == TMM_F32 ? 6 : 2;
   return round256(size_t(u_rows(p)) * size_t(u_columns(p)) * size);   // below 2^30 * 2^11 * 6
 }
 
 // The workspace holds u and the planes of the operands.
 size_t lora_workspace_bytes(const LoraProblem &p) {
-  if (lora_shape(p.rows) == 1)
+  if (lora_shape(p.rows, p.rank) == 1)
     return add_sizes({u_bytes(p), plane_bytes(p.x, p.dtype), plane_bytes(p.w, p.dtype)});
   return add_sizes({u_bytes(p),
                     plane_bytes(p.x, p.dtype, gathered_rows(2, p.row_index, p.rows)),
@@ -2021,7 +2048,7 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
                         cudaStream_t stream) {
   char *ws = static_cast<char *>(workspace);
   const int planes = p.dtype == TMM_F32 ? 3 : 1;
-  const int cg = lora_shape(p.rows);
+  const int cg = lora_shape(p.rows, p.rank);
   const int64_t ldu = u_columns(p);
   void *u = ws;
   ws += u_bytes(p);
@@ -2086,7 +2113,7 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   prm.panels = int((p.N + 128 * cg - 1) / (128 * cg));
   const int64_t tiles = prm.panels * ((p.rows + bn - 1) / bn);
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
-  prm.ksplit = cg == 2 ? 1 : split_of(tiles, (p.K + kBK - 1) / kBK, dev);
+  prm.ksplit = cg == 2 ? 1 : split_of(tiles, (p.K + kBK - 1) / kBK, planes, dev);
   prm.p_mn = p.trans_w ? 0 : 1;
   prm.p_shared = 1;
   prm.out = p.y;

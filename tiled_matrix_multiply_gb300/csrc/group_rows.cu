@@ -20,7 +20,7 @@ namespace tmm {
 namespace {
 
 constexpr int kMaxWarps = 32;
-constexpr int64_t kOneBlock = 8192;     // slots that one block handles alone
+constexpr int64_t kOneBlock = 2048;     // slots that one block handles alone
 constexpr int64_t kChunk = 1024;        // slots of a block, at least, otherwise
 
 template <typename T>
@@ -29,12 +29,18 @@ __device__ __forceinline__ int key_of(const void *index, int64_t s, int groups) 
   return v >= 0 && v < groups ? int(v) : groups;
 }
 
+// Programmatic dependent launch: wait for the launch before, then let the next one start.
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // h[b][g] for g <= groups.
 template <typename T>
 __global__ void __launch_bounds__(1024)
 count_kernel(const void *__restrict__ index, int64_t slots, int64_t chunk, int groups,
              int *__restrict__ counts) {
   __shared__ int h[kMaxGroups + 1];
+  grid_wait();
   for (int g = threadIdx.x; g <= groups; g += blockDim.x) h[g] = 0;
   __syncthreads();
   const int64_t s0 = blockIdx.x * chunk, s1 = min(s0 + chunk, slots);
@@ -60,6 +66,7 @@ place_kernel(const void *__restrict__ index, int64_t slots, int64_t chunk, int f
   const int64_t run = ((s1 - s0 + warps - 1) / warps + 31) / 32 * 32;   // slots of a warp
   const int64_t w0 = min(s0 + warp * run, s1), w1 = min(w0 + run, s1);
   for (int i = threadIdx.x; i < G * (warps + 2); i += blockDim.x) sh[i] = 0;
+  grid_wait();
   __syncthreads();
   for (int64_t s = w0 + lane; s < w1; s += 32)
     atomicAdd(&mine[warp * G + key_of<T>(index, s, groups)], 1);
@@ -69,6 +76,7 @@ place_kernel(const void *__restrict__ index, int64_t slots, int64_t chunk, int f
     for (int i = threadIdx.x; i < G * step; i += blockDim.x) {
       const int g = i % G;
       int all = 0, low = 0;
+#pragma unroll 8
       for (int b = i / G; b < int(gridDim.x); b += step) {
         const int c = counts[int64_t(b) * G + g];
         all += c;
@@ -144,8 +152,20 @@ cudaError_t launch(int64_t slots, int fan, int groups, const void *index, int32_
   int64_t chunk;
   const int64_t blocks = blocks_of(slots, dev.sm_count, &chunk);
   int *counts = blocks > 1 ? static_cast<int *>(workspace) : nullptr;
-  if (counts)
-    count_kernel<T><<<unsigned(blocks), 1024, 0, stream>>>(index, slots, chunk, groups, counts);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(unsigned(blocks), 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (counts) {
+    cfg.blockDim = dim3(1024, 1, 1);
+    const cudaError_t e =
+        cudaLaunchKernelEx(&cfg, count_kernel<T>, index, slots, chunk, groups, counts);
+    if (e != cudaSuccess) return e;
+  }
   const int64_t in_block = chunk < slots ? chunk : slots;
   const int64_t want = (in_block + 31) / 32;
   const int warps = int(want < 1 ? 1 : want > kMaxWarps ? kMaxWarps : want);
@@ -160,9 +180,10 @@ cudaError_t launch(int64_t slots, int fan, int groups, const void *index, int32_
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_release);
   }
-  place_kernel<T><<<unsigned(blocks), unsigned(32 * warps), smem, stream>>>(
-      index, slots, chunk, fan, groups, counts, offsets, order, rows, position);
-  return cudaGetLastError();
+  cfg.blockDim = dim3(unsigned(32 * warps), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  return cudaLaunchKernelEx(&cfg, place_kernel<T>, index, slots, chunk, fan, groups,
+                            static_cast<const int *>(counts), offsets, order, rows, position);
 }
 
 }  // namespace
