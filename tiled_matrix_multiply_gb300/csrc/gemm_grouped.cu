@@ -50,6 +50,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "bounds_check.cuh"
 #include "grouped.h"
@@ -1460,48 +1461,67 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
 
 // ---- operand planes -----------------------------------------------------------------------
 
-// Copies a stack of matrices into 16-bit planes whose rows start on 16-byte boundaries: FP32
+// Copies stacks of matrices into 16-bit planes whose rows start on 16-byte boundaries: FP32
 // values into their three bf16 parts (planes), 16-bit values as they are (one plane).  Layout:
 // [plane][matrix][row][ld8].  With `index` (one matrix only) row r is the source's row index[r],
 // zeros for a number outside [0, src_rows).  Matrices of groups without rows are left out.
-// Bound by memory: each thread moves eight values.
+// One launch makes the planes of all of a call's operands; bound by memory, each thread has
+// kPlaneAhead units of eight values in flight.
+struct PlaneJob {
+  const void *src;
+  int64_t rows, cols, ld, stride, src_rows, ld8, plane;   // plane: values between planes
+  int64_t count;
+  const int *offsets, *index;
+  uint16_t *dst;
+  int64_t tiles;        // tiles of kPlaneTile units of a matrix
+  int vec;              // 16-byte loads
+};
+struct PlaneJobs {
+  PlaneJob job[4];
+  int64_t first[5];     // tiles (of all matrices) before each job
+  int count;
+};
+constexpr int kPlaneThreads = 256, kPlaneAhead = 4;
+constexpr int kPlaneTile = kPlaneThreads * kPlaneAhead;
+
 template <bool F32>
-__global__ void planes_kernel(const void *__restrict__ src, int64_t count, int64_t rows,
-                              int64_t cols, int64_t ld, int64_t stride, int vec,
-                              const int *__restrict__ offsets, const int *__restrict__ index,
-                              int64_t src_rows, uint16_t *__restrict__ dst, int64_t ld8) {
+__global__ void __launch_bounds__(kPlaneThreads)
+planes_kernel(const __grid_constant__ PlaneJobs jobs) {
+  using T = std::conditional_t<F32, float, uint16_t>;
   grid_wait();
   grid_start_next();
-  const int64_t per_row = ld8 / 8;
-  const int64_t total = rows * per_row;
-  const int64_t plane = count * rows * ld8;
-  for (int64_t m = blockIdx.y; m < count; m += gridDim.y) {
-    if (offsets && offsets[m + 1] <= offsets[m]) continue;
-    for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < total;
-         i += int64_t(gridDim.x) * blockDim.x) {
-      const int64_t row = i / per_row, c = (i - row * per_row) * 8;
-      int64_t from = row, left = cols - c;
-      if (index) {
-        from = index[row];
-        if (from < 0 || from >= src_rows) from = left = 0;
-      }
-      const int64_t so = m * stride + from * ld + c;
-      const int64_t to = (m * rows + row) * ld8 + c;
-      if constexpr (F32) {
-        const float *s = static_cast<const float *>(src) + so;
-        float x[8];
-        if (vec && left >= 8) {
-          const float4 a = *reinterpret_cast<const float4 *>(s);
-          const float4 b = *reinterpret_cast<const float4 *>(s + 4);
-          x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-          x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-        } else {
+  for (int64_t t = blockIdx.x; t < jobs.first[jobs.count]; t += gridDim.x) {
+    int n = 0;
+    while (t >= jobs.first[n + 1]) ++n;
+    const PlaneJob &j = jobs.job[n];
+    const int64_t m = (t - jobs.first[n]) / j.tiles;
+    if (j.offsets && j.offsets[m + 1] <= j.offsets[m]) continue;
+    const int64_t per_row = j.ld8 / 8, total = j.rows * per_row;
+    const int64_t unit0 = (t - jobs.first[n] - m * j.tiles) * kPlaneTile + threadIdx.x;
+    Eight<T> x[kPlaneAhead];
+    int64_t to[kPlaneAhead];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = j < left ? s[j] : 0.0f;
-        }
+    for (int k = 0; k < kPlaneAhead; ++k) {
+      const int64_t i = unit0 + k * kPlaneThreads;
+      const int64_t row = total <= UINT32_MAX ? uint32_t(i) / uint32_t(per_row) : i / per_row;
+      const int64_t c = (i - row * per_row) * 8;
+      int64_t from = row, left = j.cols - c;
+      bool on = i < total;
+      if (j.index && on) {
+        from = j.index[row];
+        on = from >= 0 && from < j.src_rows;
+      }
+      to[k] = i < total ? (m * j.rows + row) * j.ld8 + c : -1;
+      const T *const s = static_cast<const T *>(j.src) + m * j.stride + from * j.ld + c;
+      x[k] = j.vec && left >= 8 ? load8<true>(s, on, left) : load8<false>(s, on, left);
+    }
+#pragma unroll
+    for (int k = 0; k < kPlaneAhead; ++k) {
+      if (to[k] < 0) continue;
+      if constexpr (F32) {
         uint16_t h[8][3];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) split3(x[j], h[j]);
+        for (int i = 0; i < 8; ++i) split3(x[k].get(i), h[i]);
 #pragma unroll
         for (int pl = 0; pl < 3; ++pl) {
           uint4 v;
@@ -1509,21 +1529,10 @@ __global__ void planes_kernel(const void *__restrict__ src, int64_t count, int64
           v.y = h[2][pl] | (uint32_t(h[3][pl]) << 16);
           v.z = h[4][pl] | (uint32_t(h[5][pl]) << 16);
           v.w = h[6][pl] | (uint32_t(h[7][pl]) << 16);
-          *reinterpret_cast<uint4 *>(dst + pl * plane + to) = v;
+          *reinterpret_cast<uint4 *>(j.dst + pl * j.plane + to[k]) = v;
         }
       } else {
-        const uint16_t *s = static_cast<const uint16_t *>(src) + so;
-        uint4 v;
-        if (vec && left >= 8) {
-          v = *reinterpret_cast<const uint4 *>(s);
-        } else {
-          uint32_t x[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = j < left ? s[j] : 0u;
-          v = make_uint4(x[0] | (x[1] << 16), x[2] | (x[3] << 16), x[4] | (x[5] << 16),
-                         x[6] | (x[7] << 16));
-        }
-        *reinterpret_cast<uint4 *>(dst + to) = v;
+        *reinterpret_cast<uint4 *>(j.dst + to[k]) = x[k].w[0];
       }
     }
   }
@@ -1685,39 +1694,49 @@ struct Planes {
   int64_t count, rows, cols, ld, stride;   // count: matrices of all planes
 };
 
-// The operand in place, or its planes made in *ws (which advances past them); matrices of
-// groups without rows (by `offsets`, a matrix per group) are not made.  With `gathered` the
-// planes hold the rows that `index` names.
-cudaError_t make_planes(const Stack &s, int dtype, const int32_t *offsets, char **ws,
-                        const DeviceInfo &dev, cudaStream_t stream, Planes *out,
-                        int64_t gathered = 0, const int32_t *index = nullptr) {
-  if (in_place(s, dtype) && gathered == 0) {
-    *out = {s.data, s.count, s.rows, s.cols, s.ld, s.count > 1 ? s.stride : s.rows * s.ld};
-    return cudaSuccess;
-  }
-  const int64_t ld8 = round8(s.cols), rows = gathered ? gathered : s.rows;
+// The operand in place, or a job that makes its planes in *ws (which advances past them);
+// matrices of groups without rows (by `offsets`, a matrix per group) are not made.  With
+// `gathered` the planes hold the rows that `index` names.
+Planes plan_planes(const Stack &s, int dtype, const int32_t *offsets, char **ws, PlaneJobs *jobs,
+                   int64_t gathered = 0, const int32_t *index = nullptr) {
+  if (in_place(s, dtype) && gathered == 0)
+    return {s.data, s.count, s.rows, s.cols, s.ld, s.count > 1 ? s.stride : s.rows * s.ld};
   const int planes = dtype == TMM_F32 ? 3 : 1;
-  const int size = dtype == TMM_F32 ? 4 : 2;
-  uint16_t *dst = reinterpret_cast<uint16_t *>(*ws);
+  PlaneJob &j = jobs->job[jobs->count];
+  j.src = s.data;
+  j.rows = gathered ? gathered : s.rows;
+  j.cols = s.cols;
+  j.ld = s.ld;
+  j.stride = s.count > 1 ? s.stride : 0;
+  j.src_rows = s.rows;
+  j.ld8 = round8(s.cols);
+  j.count = s.count;
+  j.plane = s.count * j.rows * j.ld8;
+  j.offsets = s.count > 1 ? offsets : nullptr;      // one matrix may serve every group
+  j.index = gathered ? index : nullptr;
+  j.dst = reinterpret_cast<uint16_t *>(*ws);
+  j.tiles = (j.rows * (j.ld8 / 8) + kPlaneTile - 1) / kPlaneTile;
+  j.vec = on16(s, dtype == TMM_F32 ? 4 : 2);
+  jobs->first[jobs->count + 1] = jobs->first[jobs->count] + j.tiles * j.count;
+  ++jobs->count;
   *ws += plane_bytes(s, dtype, gathered);
-  const int64_t work = (rows * (ld8 / 8) + 255) / 256;
-  const dim3 grid(unsigned(std::min<int64_t>(work, 8 * dev.sm_count)),
-                  unsigned(std::min<int64_t>(s.count, 1024)));
-  const int vec = on16(s, size);
-  if (s.count == 1) offsets = nullptr;      // one matrix may serve every group
-  if (gathered == 0) index = nullptr;
-  *out = {dst, planes * s.count, rows, s.cols, ld8, rows * ld8};
+  return {j.dst, planes * s.count, j.rows, s.cols, j.ld8, j.rows * j.ld8};
+}
+
+cudaError_t make_planes(const PlaneJobs &jobs, int dtype, const DeviceInfo &dev,
+                        cudaStream_t stream) {
+  if (jobs.count == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(256, 1, 1);
+  attr[0] = overlap_attribute();
+  cfg.gridDim =
+      dim3(unsigned(std::min<int64_t>(jobs.first[jobs.count], 4 * dev.sm_count)), 1, 1);
+  cfg.blockDim = dim3(kPlaneThreads, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  attr[0] = overlap_attribute();
   return cudaLaunchKernelEx(&cfg, dtype == TMM_F32 ? planes_kernel<true> : planes_kernel<false>,
-                            s.data, s.count, rows, s.cols, s.ld, s.stride, vec, offsets, index,
-                            s.rows, dst, ld8);
+                            jobs);
 }
 
 // Maps of an operand: tiles of `box_rows` rows x 64 values in matrix z, or of the rows of all
@@ -1909,12 +1928,11 @@ cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void 
   const bool shared = p.groups > 1 && p.w.count == 1;
   const int64_t gathered =
       gathered_rows(forward_shape(p.rows, p.groups, p.N, p.K, p.dtype), p.row_index, p.rows);
-  Planes x, w;
-  cudaError_t e;
-  if ((e = make_planes(p.x, p.dtype, nullptr, &ws, dev, stream, &x, gathered, p.row_index)) !=
-          cudaSuccess ||
-      (e = make_planes(p.w, p.dtype, p.offsets, &ws, dev, stream, &w)) != cudaSuccess)
-    return e;
+  PlaneJobs jobs = {};
+  const Planes x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs, gathered, p.row_index);
+  const Planes w = plan_planes(p.w, p.dtype, p.offsets, &ws, &jobs);
+  const cudaError_t e = make_planes(jobs, p.dtype, dev, stream);
+  if (e != cudaSuccess) return e;
   const int planes = p.dtype == TMM_F32 ? 3 : 1;
   Params prm = {};
   prm.rows = int(p.rows);
@@ -1940,15 +1958,14 @@ size_t wgrad_workspace_bytes(const WgradProblem &p) {
 cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *workspace,
                          cudaStream_t stream) {
   char *ws = static_cast<char *>(workspace);
-  Planes x, dy;
-  cudaError_t e;
   const int cg = wgrad_shape(p.N);
   const int64_t gathered = gathered_rows(cg, p.row_index, p.rows);
   const int32_t *index = gathered ? nullptr : p.row_index;
-  if ((e = make_planes(p.x, p.dtype, nullptr, &ws, dev, stream, &x, gathered, p.row_index)) !=
-          cudaSuccess ||
-      (e = make_planes(p.dy, p.dtype, nullptr, &ws, dev, stream, &dy)) != cudaSuccess)
-    return e;
+  PlaneJobs jobs = {};
+  const Planes x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs, gathered, p.row_index);
+  const Planes dy = plan_planes(p.dy, p.dtype, nullptr, &ws, &jobs);
+  cudaError_t e = make_planes(jobs, p.dtype, dev, stream);
+  if (e != cudaSuccess) return e;
   const int planes = p.dtype == TMM_F32 ? 3 : 1;
   Params prm = {};
   prm.rows = int(p.rows);
@@ -2053,12 +2070,16 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   void *u = ws;
   ws += u_bytes(p);
   const int64_t gathered = gathered_rows(cg, p.row_index, p.rows);
-  Planes x, w;
-  cudaError_t e;
-  if ((e = make_planes(p.x, p.dtype, nullptr, &ws, dev, stream, &x, gathered, p.row_index)) !=
-          cudaSuccess ||
-      (e = make_planes(p.w, p.dtype, nullptr, &ws, dev, stream, &w)) != cudaSuccess)
-    return e;
+  PlaneJobs jobs = {};
+  const Planes x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs, gathered, p.row_index);
+  const Planes w = plan_planes(p.w, p.dtype, nullptr, &ws, &jobs);
+  Planes a = {}, b = {};
+  if (cg == 2) {
+    a = plan_planes(p.a, p.dtype, p.offsets, &ws, &jobs);
+    b = plan_planes(p.b, p.dtype, p.offsets, &ws, &jobs);
+  }
+  cudaError_t e = make_planes(jobs, p.dtype, dev, stream);
+  if (e != cudaSuccess) return e;
   Params prm = {};
   prm.rows = int(p.rows);
   prm.groups = int(p.groups);
@@ -2078,10 +2099,6 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
     prm.trans_b = p.trans_b;
     prm.vec_b = on16(p.b, p.dtype == TMM_F32 ? 4 : 2) && p.b.cols % 8 == 0;
   } else {
-    Planes a, b;
-    if ((e = make_planes(p.a, p.dtype, p.offsets, &ws, dev, stream, &a)) != cudaSuccess ||
-        (e = make_planes(p.b, p.dtype, p.offsets, &ws, dev, stream, &b)) != cudaSuccess)
-      return e;
     Params up = prm;
     up.N = int(p.rank);
     up.out = u;
