@@ -1474,7 +1474,7 @@ struct PlaneJob {
   const int *offsets, *index;
   uint16_t *dst;
   int64_t tiles;        // tiles of kPlaneTile units of a matrix
-  int vec;              // 16-byte loads
+  int vec;              // whole 16-byte loads
 };
 struct PlaneJobs {
   PlaneJob job[4];
@@ -1484,10 +1484,53 @@ struct PlaneJobs {
 constexpr int kPlaneThreads = 256, kPlaneAhead = 4;
 constexpr int kPlaneTile = kPlaneThreads * kPlaneAhead;
 
+// One tile of units; VEC: whole 16-byte loads throughout.
+template <bool F32, bool VEC>
+__device__ __forceinline__ void plane_tile(const PlaneJob &j, int64_t m, int64_t unit0) {
+  using T = std::conditional_t<F32, float, uint16_t>;
+  const int64_t per_row = j.ld8 / 8, total = j.rows * per_row;
+  Eight<T> x[kPlaneAhead];
+  int64_t to[kPlaneAhead];
+#pragma unroll
+  for (int k = 0; k < kPlaneAhead; ++k) {
+    const int64_t i = unit0 + k * kPlaneThreads;
+    const int64_t row = total <= UINT32_MAX ? uint32_t(i) / uint32_t(per_row) : i / per_row;
+    const int64_t c = (i - row * per_row) * 8;
+    int64_t from = row;
+    bool on = i < total;
+    if (j.index) {
+      from = on ? j.index[row] : -1;
+      on = from >= 0 && from < j.src_rows;
+    }
+    to[k] = i < total ? (m * j.rows + row) * j.ld8 + c : -1;
+    x[k] = load8<VEC>(static_cast<const T *>(j.src) + m * j.stride + (on ? from : 0) * j.ld + c, on,
+                      j.cols - c);
+  }
+#pragma unroll
+  for (int k = 0; k < kPlaneAhead; ++k) {
+    if (to[k] < 0) continue;
+    if constexpr (F32) {
+      uint16_t h[8][3];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) split3(x[k].get(i), h[i]);
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl) {
+        uint4 v;
+        v.x = h[0][pl] | (uint32_t(h[1][pl]) << 16);
+        v.y = h[2][pl] | (uint32_t(h[3][pl]) << 16);
+        v.z = h[4][pl] | (uint32_t(h[5][pl]) << 16);
+        v.w = h[6][pl] | (uint32_t(h[7][pl]) << 16);
+        *reinterpret_cast<uint4 *>(j.dst + pl * j.plane + to[k]) = v;
+      }
+    } else {
+      *reinterpret_cast<uint4 *>(j.dst + to[k]) = x[k].w[0];
+    }
+  }
+}
+
 template <bool F32>
 __global__ void __launch_bounds__(kPlaneThreads)
 planes_kernel(const __grid_constant__ PlaneJobs jobs) {
-  using T = std::conditional_t<F32, float, uint16_t>;
   grid_wait();
   grid_start_next();
   for (int64_t t = blockIdx.x; t < jobs.first[jobs.count]; t += gridDim.x) {
@@ -1496,45 +1539,9 @@ planes_kernel(const __grid_constant__ PlaneJobs jobs) {
     const PlaneJob &j = jobs.job[n];
     const int64_t m = (t - jobs.first[n]) / j.tiles;
     if (j.offsets && j.offsets[m + 1] <= j.offsets[m]) continue;
-    const int64_t per_row = j.ld8 / 8, total = j.rows * per_row;
     const int64_t unit0 = (t - jobs.first[n] - m * j.tiles) * kPlaneTile + threadIdx.x;
-    Eight<T> x[kPlaneAhead];
-    int64_t to[kPlaneAhead];
-#pragma unroll
-    for (int k = 0; k < kPlaneAhead; ++k) {
-      const int64_t i = unit0 + k * kPlaneThreads;
-      const int64_t row = total <= UINT32_MAX ? uint32_t(i) / uint32_t(per_row) : i / per_row;
-      const int64_t c = (i - row * per_row) * 8;
-      int64_t from = row, left = j.cols - c;
-      bool on = i < total;
-      if (j.index && on) {
-        from = j.index[row];
-        on = from >= 0 && from < j.src_rows;
-      }
-      to[k] = i < total ? (m * j.rows + row) * j.ld8 + c : -1;
-      const T *const s = static_cast<const T *>(j.src) + m * j.stride + from * j.ld + c;
-      x[k] = j.vec && left >= 8 ? load8<true>(s, on, left) : load8<false>(s, on, left);
-    }
-#pragma unroll
-    for (int k = 0; k < kPlaneAhead; ++k) {
-      if (to[k] < 0) continue;
-      if constexpr (F32) {
-        uint16_t h[8][3];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) split3(x[k].get(i), h[i]);
-#pragma unroll
-        for (int pl = 0; pl < 3; ++pl) {
-          uint4 v;
-          v.x = h[0][pl] | (uint32_t(h[1][pl]) << 16);
-          v.y = h[2][pl] | (uint32_t(h[3][pl]) << 16);
-          v.z = h[4][pl] | (uint32_t(h[5][pl]) << 16);
-          v.w = h[6][pl] | (uint32_t(h[7][pl]) << 16);
-          *reinterpret_cast<uint4 *>(j.dst + pl * j.plane + to[k]) = v;
-        }
-      } else {
-        *reinterpret_cast<uint4 *>(j.dst + to[k]) = x[k].w[0];
-      }
-    }
+    if (j.vec) plane_tile<F32, true>(j, m, unit0);
+    else plane_tile<F32, false>(j, m, unit0);
   }
 }
 
@@ -1716,7 +1723,7 @@ Planes plan_planes(const Stack &s, int dtype, const int32_t *offsets, char **ws,
   j.index = gathered ? index : nullptr;
   j.dst = reinterpret_cast<uint16_t *>(*ws);
   j.tiles = (j.rows * (j.ld8 / 8) + kPlaneTile - 1) / kPlaneTile;
-  j.vec = on16(s, dtype == TMM_F32 ? 4 : 2);
+  j.vec = on16(s, dtype == TMM_F32 ? 4 : 2) && s.cols % 8 == 0;
   jobs->first[jobs->count + 1] = jobs->first[jobs->count] + j.tiles * j.count;
   ++jobs->count;
   *ws += plane_bytes(s, dtype, gathered);
@@ -1730,7 +1737,7 @@ cudaError_t make_planes(const PlaneJobs &jobs, int dtype, const DeviceInfo &dev,
   cudaLaunchAttribute attr[1];
   attr[0] = overlap_attribute();
   cfg.gridDim =
-      dim3(unsigned(std::min<int64_t>(jobs.first[jobs.count], 4 * dev.sm_count)), 1, 1);
+      dim3(unsigned(std::min<int64_t>(jobs.first[jobs.count], 8 * dev.sm_count)), 1, 1);
   cfg.blockDim = dim3(kPlaneThreads, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
