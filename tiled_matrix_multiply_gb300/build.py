@@ -9,6 +9,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +19,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libtmm_gemm.so")
+# The CPython module that marshals the grouped operators' usual calls (csrc/grouped_call.c).
+CALL_SOURCE = os.path.join(CSRC, "grouped_call.c")
+CALL_PATH = os.path.join(LIB_DIR, "grouped_call.so")
 # The bounds-checked debug build (every global address and shared-memory offset
 # of the product kernels range-checked, see csrc/bounds_check.cuh): its own
 # objects and library, beside the normal ones.
@@ -102,8 +106,28 @@ def _build(lib_path: str, build_dir: str, extra: list[str]) -> str:
     return lib_path
 
 
+def build_call(force: bool = False) -> str:
+    """Build the marshalling module with the C compiler unless an up-to-date copy exists."""
+    header = os.path.join(INCLUDE, "tmm_gemm.h")
+    if not force and os.path.exists(CALL_PATH) and all(
+            os.path.getmtime(f) <= os.path.getmtime(CALL_PATH)
+            for f in (CALL_SOURCE, header, os.path.abspath(__file__))):
+        return CALL_PATH
+    os.makedirs(LIB_DIR, exist_ok=True)
+    tmp = CALL_PATH + f".tmp{os.getpid()}"
+    cmd = ["gcc", "-O2", "-std=c11", "-Wall", "-Wextra", "-fPIC", "-shared", "-I", INCLUDE, "-I",
+           sysconfig.get_paths()["include"], CALL_SOURCE, "-o", tmp]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"gcc failed on grouped_call.c:\n{res.stderr}")
+    os.replace(tmp, CALL_PATH)
+    return CALL_PATH
+
+
 def build(force: bool = False, extra_flags: list[str] | None = None) -> str:
-    """Build libtmm_gemm.so unless an up-to-date copy exists; return its path."""
+    """Build libtmm_gemm.so (and the marshalling module) unless up-to-date copies exist; return
+    the library's path."""
+    build_call(force)
     if not force and not extra_flags and is_fresh():
         return LIB_PATH
     return _build(LIB_PATH, BUILD_DIR, list(extra_flags or []))

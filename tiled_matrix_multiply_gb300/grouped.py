@@ -18,11 +18,15 @@ no call reads a group's size on the host.
 """
 from __future__ import annotations
 
+import ctypes
+import importlib.machinery
+import importlib.util
+import os
 from typing import NamedTuple
 
 import torch
 
-from . import _abi
+from . import _abi, build as _build
 
 _CODES = {torch.float32: _abi.TMM_F32, torch.bfloat16: _abi.TMM_BF16,
           torch.float16: _abi.TMM_F16}
@@ -143,12 +147,38 @@ def _scratch(need, like):
     return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
 
 
+def _load_call():
+    """The module that takes the usual calls (csrc/grouped_call.c), handed what it needs."""
+    if not os.path.exists(_build.CALL_PATH):
+        raise RuntimeError(f"{_build.CALL_PATH} is missing: build it with "
+                           "tiled_matrix_multiply_gb300.build.build()")
+    loader = importlib.machinery.ExtensionFileLoader("grouped_call", _build.CALL_PATH)
+    module = importlib.util.module_from_spec(
+        importlib.util.spec_from_file_location("grouped_call", _build.CALL_PATH, loader=loader))
+    loader.exec_module(module)
+    lib = _abi.load()
+    names = ("group_rows", "group_rows_workspace_size", "gemm_grouped",
+             "gemm_grouped_workspace_size", "gemm_grouped_wgrad",
+             "gemm_grouped_wgrad_workspace_size", "gemm_lora", "gemm_lora_workspace_size")
+    module.start((torch.Tensor, torch.empty, _raw_stream, torch.cuda.current_device, RowGroups,
+                  torch.uint8, torch.int32, torch.int64, torch.float32, torch.float32,
+                  torch.bfloat16, torch.float16),
+                 tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
+    return module
+
+
+_usual = _load_call()
+
+
 def group_rows(index, groups, stream=None):
     """Stable grouping of the slots of ``index`` (tokens,) or (tokens, k), int32 or int64.
 
     A slot's group is its number where that is in [0, groups); the other slots belong to no
     group and come last.  Returns ``RowGroups``.
     """
+    done = _usual.group_rows(index, groups, stream)
+    if done is not None:
+        return done
     if not isinstance(index, torch.Tensor) or index.dtype not in (torch.int32, torch.int64):
         raise TypeError("index must be an int32 or int64 tensor")
     if not index.is_cuda:
@@ -181,6 +211,10 @@ def gemm_grouped(x, w, offsets, rows=None, y=None, workspace=None, stream=None):
     (groups + 1); rows: int32, the row of x that each p reads (a number outside x reads zeros),
     or None for p itself.  y: (len(rows) or x_rows, N); its rows of no group are zero.
     """
+    if y is None and workspace is None:
+        done = _usual.grouped(x, w, offsets, rows, stream)
+        if done is not None:
+            return done
     code = _first(x, "x")
     x_rows, K, ldx, _, _ = _operand(x, "x", x, 2)
     K2, N, ldw, stride_w, trans = _operand(w, "w", x, 3, True)
@@ -213,6 +247,10 @@ def gemm_grouped_wgrad(x, dy, offsets, rows=None, dw=None, workspace=None, strea
 
     The gradient of ``gemm_grouped`` with respect to w; x, offsets and rows as there, dy (R, N).
     """
+    if dw is None and workspace is None:
+        done = _usual.wgrad(x, dy, offsets, rows, stream)
+        if done is not None:
+            return done
     code = _first(x, "x")
     x_rows, K, ldx, _, _ = _operand(x, "x", x, 2)
     R, N, lddy, _, _ = _operand(dy, "dy", x, 2)
@@ -247,6 +285,10 @@ def gemm_lora(x, w, a, b, scale, offsets, rows=None, y=None, workspace=None, str
     ``offsets`` and ``order`` of ``group_rows(index, adapters)``; rows past offsets[-1] have no
     adapter.  rows=None: x is in group order already.
     """
+    if y is None and workspace is None:
+        done = _usual.lora(x, w, a, b, scale, offsets, rows, stream)
+        if done is not None:
+            return done
     code = _first(x, "x")
     T, K, ldx, _, _ = _operand(x, "x", x, 2)
     K2, N, ldw, _, tw = _operand(w, "w", x, 2, True)
