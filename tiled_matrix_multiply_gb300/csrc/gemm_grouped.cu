@@ -64,11 +64,8 @@ namespace {
 
 constexpr int kForward = 0, kWgrad = 1, kLora = 2;
 constexpr int kBK = 64;                  // 16-bit values per K slice: one 128-byte swizzle row
-constexpr int kCopyWarps = 4, kEpiWarps = 8;
-constexpr int kEpi0 = kCopyWarps;                  // first of the result warps
+constexpr int kEpiWarps = 8;
 constexpr int kFewRows = 256;                      // rows of an adapters' call on single blocks
-constexpr int kMmaWarp = kCopyWarps + kEpiWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kChunk = 2;                // slices per tensor-memory sum of split operands
 constexpr uint32_t kPTile = 128 * 128;   // 128 lanes x 64 values: 16 KiB
 constexpr uint32_t kMaxSmem = 232448;    // 227 KiB
@@ -80,6 +77,13 @@ constexpr int kOutU = 3;       // the adapters' u: three planes (split3), or a p
 
 template <int CG, int PLANES>
 struct Shape {
+  // FP32 on single blocks: the copy warps read the operands as they are stored and split them
+  // on the way (DIRECT); no planes.
+  static constexpr bool kDirect = CG == 1 && PLANES == 3;
+  static constexpr int kCopyWarps = kDirect ? 16 : 4;
+  static constexpr int kEpi0 = kCopyWarps;           // first of the result warps
+  static constexpr int kMmaWarp = kCopyWarps + kEpiWarps;
+  static constexpr int kThreads = 32 * (kMmaWarp + 1);
   static constexpr int kBN = PLANES == 3 ? (CG == 2 ? 128 : 64) : (CG == 2 ? 256 : 64);
   static constexpr int kUnit = CG == 2 ? 64 : 16;    // columns are rounded up to this
   static constexpr int kBox = kUnit / CG;            // rows of one copy of Q
@@ -118,6 +122,10 @@ struct Params {
   int p_mn, e_mn;        // P (and b) stored with n contiguous
   int p_shared, e_shared;   // one P (one b) for all groups
   uint32_t idesc;        // types; majors and sizes are added in the kernel
+  // FP32 operands as they are stored (single blocks): P and x.
+  const float *fp, *fx;
+  int64_t ldp, stride_p, ldx;
+  int vec;               // whole 16-byte loads of both
   void *out;
   int64_t ld_out, stride_out;   // stride: of dw's matrices, or of the result's planes
   int out_type;
@@ -183,6 +191,10 @@ __device__ __forceinline__ void mbar_expect_only(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
+}
+// On this block's own barrier (`bar`: its shared memory address).
+__device__ __forceinline__ void mbar_arrive_local(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // The same where no access to memory of this thread has to be ordered before it.  (A release
 // waits for the thread's stores: result warps handing tensor memory back, whose reads have
@@ -493,6 +505,42 @@ __device__ __forceinline__ void split3(float x, uint16_t (&h)[3]) {
   h[2] = uint16_t(nearest_bf16(__float_as_uint(s)) >> 16);
 }
 
+// split3 of eight values: the parts of value i in 16 bits of h[part], as they are stored.  Values
+// below 2^127 take the conversion instruction, two at a time (5.5 instructions a value against
+// split3's 20).
+__device__ __forceinline__ uint32_t pair_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void split8(const float (&x)[8], uint32_t (&h)[3][4]) {
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));      // (a NaN is not seen)
+  const float sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+  if (top < 0x1p127f && sum == sum) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a = x[2 * i], b = x[2 * i + 1];
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl) {
+        h[pl][i] = pair_bf16(a, b);
+        a -= __uint_as_float(h[pl][i] << 16);
+        b -= __uint_as_float(h[pl][i] & 0xFFFF0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint16_t a[3], b[3];
+      split3(x[2 * i], a);
+      split3(x[2 * i + 1], b);
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl) h[pl][i] = a[pl] | (uint32_t(b[pl]) << 16);
+    }
+  }
+}
+
 // The adapters' u in a 16-bit type T: v = hi + lo, hi the value rounded to T and lo what that
 // leaves, so that u keeps about twice T's bits and only the final result is rounded to T.
 // Column n is stored at 64 (n / 32) + n % 32, its lo 32 columns on.
@@ -654,7 +702,7 @@ __device__ __forceinline__ Eight<T> load8(const T *p, bool on, int64_t left) {
   return v;
 }
 
-// All threads of the result warps.
+// All threads of the result warps; `tid` numbers them.
 __device__ __forceinline__ void results_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
 }
@@ -664,10 +712,9 @@ __device__ __forceinline__ void results_sync() {
 // while the weights stream: `rank` loads of 16 bytes a thread in flight for eight n of one row.
 template <typename T, bool VEC>
 __device__ __forceinline__ void add_adapters_as(const Params &p, const int *owner, const Tile &t,
-                                                int c0, int c1, float *sums) {
-  const int tid = int(threadIdx.x) - 32 * kEpi0;
+                                                int c0, int c1, float *sums, int tid) {
   const T *const b = static_cast<const T *>(p.b);
-  constexpr int kAhead = VEC ? (sizeof(T) == 2 ? 16 : 8) : 2;      // loads in flight
+  constexpr int kAhead = VEC ? (sizeof(T) == 2 ? 16 : 4) : 2;      // loads in flight
   if (!p.trans_b) {
     // b stored rank x N: 16 threads a row, eight n each.
     const int l = (tid & 15) * 8, n = t.n0 + l;
@@ -725,16 +772,121 @@ __device__ __forceinline__ void add_adapters_as(const Params &p, const int *owne
 }
 template <typename T>
 __device__ __forceinline__ void add_adapters(const Params &p, const int *owner, const Tile &t,
-                                             int c0, int c1, float *sums) {
+                                             int c0, int c1, float *sums, int tid) {
   grid_wait();      // u is the launch before's
-  if (p.vec_b) add_adapters_as<T, true>(p, owner, t, c0, c1, sums);
-  else add_adapters_as<T, false>(p, owner, t, c0, c1, sums);
+  if (p.vec_b) add_adapters_as<T, true>(p, owner, t, c0, c1, sums, tid);
+  else add_adapters_as<T, false>(p, owner, t, c0, c1, sums, tid);
+}
+
+// FP32 on single blocks: one tile's slices [s0, s1), split into planes by the 16 copy warps.  A
+// slice is 128 x 64 values of P and up to 64 x 64 of Q, split by eight of the warps -- the other
+// eight have the next one's in flight -- in chunks of eight values that are contiguous as stored,
+// so both majors are read in rows.  Reading FP32 operands in place costs 4 bytes a
+// value, planes made by a kernel before 4 + 6 + 6.  False when a wait ran out.
+template <int MODE, bool VEC>
+__device__ __forceinline__ bool split_tile(const Params &p, const Tile &t, int s0, int s1,
+                                           uint32_t base, uint32_t bar_full, uint32_t bar_empty,
+                                           Ring &ring, bool &dropped) {
+  using S = Shape<1, 3>;
+  static_assert(S::kStages == 2 && S::kCopyWarps == 16, "eight warps for each of two stages");
+  const int warp = (threadIdx.x >> 5) & 7, team = threadIdx.x >> 8, lane = threadIdx.x & 31;
+  const bool mn = MODE == kWgrad || p.p_mn;
+  const float *const P = p.fp + (MODE == kWgrad || p.p_shared ? 0 : int64_t(t.g) * p.stride_p);
+  // Chunks of P: row r (of n, or of k where n is contiguous) and column 8 c; of Q likewise.
+  const int pc = mn ? lane & 15 : lane & 7;
+  const int pr = mn ? 8 * warp + (lane >> 4) : 16 * warp + (lane >> 3);
+  const int pstep = mn ? 2 : 4;        // to the thread's next row
+  const int qc = lane & 7, qr = 8 * warp + (lane >> 3);
+  int qrow[2] = {-1, -1};              // forward: the rows of x
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (MODE != kWgrad && qr + 4 * i < t.qn) {
+      const int at = t.q0 + qr + 4 * i;
+      qrow[i] = MODE == kForward && p.row_index ? p.row_index[at] : at;
+      if (qrow[i] >= p.q_rows) qrow[i] = -1;
+    }
+  struct Chunks {
+    Eight<float> p[4], q[2];
+  };
+  const auto load = [&](int s) {
+    Chunks v;
+    const int k0 = s * kBK;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = pr + i * pstep;
+      if (mn) {
+        const int k = k0 + r, n = t.n0 + 8 * pc;
+        v.p[i] = load8<VEC>(P + (MODE == kWgrad ? int64_t(t.k0) + k : int64_t(k)) * p.ldp + n,
+                            k < t.klen && n < p.N, p.N - n);
+      } else {
+        const int n = t.n0 + r, k = k0 + 8 * pc;
+        v.p[i] = load8<VEC>(P + int64_t(n) * p.ldp + k, n < p.N && k < t.klen, t.klen - k);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (MODE == kWgrad) {
+        const int k = k0 + qr + 4 * i, c = t.q0 + 8 * qc;
+        int row = -1;
+        if (k < t.klen) {
+          row = p.row_index ? p.row_index[t.k0 + k] : t.k0 + k;
+          if (row >= p.q_rows) row = -1;
+        }
+        v.q[i] = load8<VEC>(p.fx + int64_t(max(row, 0)) * p.ldx + c, row >= 0 && c < p.q_cols,
+                            p.q_cols - c);
+      } else {
+        const int k = k0 + 8 * qc;
+        v.q[i] = load8<VEC>(p.fx + int64_t(max(qrow[i], 0)) * p.ldx + k,
+                            qrow[i] >= 0 && k < t.klen, t.klen - k);
+      }
+    }
+    return v;
+  };
+  const auto store8 = [&](const Eight<float> &v, uint32_t to, uint32_t plane) {
+    float f[8];
+    uint32_t h[3][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = v.get(i);
+    split8(f, h);
+#pragma unroll
+    for (int pl = 0; pl < 3; ++pl)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + pl * plane),
+                   "r"(h[pl][0]), "r"(h[pl][1]), "r"(h[pl][2]), "r"(h[pl][3])
+                   : "memory");
+  };
+  const auto put = [&](const Chunks &v) {
+    const bool ok = mbar_wait(bar_empty + 8 * ring.stage, ring.parity ^ 1u, p.wait_limit_ns);
+    if (!__all_sync(~0u, ok)) return false;
+    const uint32_t st = base + ring.stage * S::kStage, sq = st + 3 * kPTile;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = pr + i * pstep;
+      const uint32_t at = mn ? uint32_t((pc >> 3) * 8192 + r * 128 + (((pc & 7) ^ (r & 7)) << 4))
+                             : uint32_t(r * 128 + ((pc ^ (r & 7)) << 4));
+      store8(v.p[i], st + at, kPTile);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = qr + 4 * i;
+      store8(v.q[i], sq + uint32_t(r * 128 + ((qc ^ (r & 7)) << 4)), S::kQTile);
+    }
+    proxy_fence();
+    __syncwarp();
+    if (lane == 0 && !(dropped && warp == 0)) mbar_arrive_local(bar_full + 8 * ring.stage);
+    return true;
+  };
+  for (int s = s0; s < s1; ++s) {
+    if (ring.stage == team && !put(load(s))) return false;
+    dropped = false;
+    ring.template next<S::kStages>();
+  }
+  return true;
 }
 
 // ---- kernel -----------------------------------------------------------------------------
 
 template <int CG, int MODE, int PLANES>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<CG, PLANES>::kThreads, 1)
 grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                const __grid_constant__ CUtensorMap map_q,    // Q tiles
                const __grid_constant__ CUtensorMap map_qr,   // single rows of x; pairs: tiles of
@@ -785,7 +937,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   int *const offs = reinterpret_cast<int *>(smem);
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(bar_full + 8 * s, PATCH ? CG : 1);
+      mbar_init(bar_full + 8 * s, S::kDirect ? S::kCopyWarps / 2 : PATCH ? CG : 1);
       mbar_init(bar_patch + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
     }
@@ -796,7 +948,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     mbar_init(bar_drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kMmaWarp) {
+  if (warp == S::kMmaWarp) {
     if constexpr (CG == 2) {
       asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
                    "r"(S::kTmemCols)
@@ -809,7 +961,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
   }
-  if (warp == 0 && elect_one()) {
+  if (!S::kDirect && warp == 0 && elect_one()) {
     prefetch_map(&map_p);
     prefetch_map(&map_q);
     prefetch_map(&map_qr);
@@ -820,7 +972,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     grid_wait();
     grid_start_next();
   }
-  for (int g = threadIdx.x; g <= p.groups; g += kThreads)
+  for (int g = threadIdx.x; g <= p.groups; g += S::kThreads)
     offs[g] = max(0, min(p.offsets[g], p.rows));
   __syncthreads();
   if (warp == 0) {
@@ -877,10 +1029,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   if constexpr (FEW) {
     // The adapter of every row of x: its list entry's number, -1 for none, -2 for a row that the
     // order does not name (which is not written).
-    for (int i = threadIdx.x; i < kFewRows; i += kThreads) owner[i] = -2;
+    for (int i = threadIdx.x; i < kFewRows; i += S::kThreads) owner[i] = -2;
     __syncthreads();
     const int count = int(slot_ptr[1]);
-    for (int i = threadIdx.x; i < p.rows; i += kThreads) {
+    for (int i = threadIdx.x; i < p.rows; i += S::kThreads) {
       const int row = p.row_index ? p.row_index[i] : i;
       int a = 0, b = count;        // entries that start at or before place i
       while (a < b) {
@@ -906,10 +1058,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   bool dropped = int(blockIdx.x) == p.drop_block;   // testing hook: the next expectation is wrong
 
   // Forward: rows of the result that belong to no group are zero, a warp a row.
-  if (MODE == kForward && p.zero_rows && warp >= kEpi0 && warp < kMmaWarp) {
+  if (MODE == kForward && p.zero_rows && warp >= S::kEpi0 && warp < S::kMmaWarp) {
     const int lo = int(slot_ptr[3]), hi = int(slot_ptr[4]);
     const int64_t count = int64_t(lo) + (p.rows - hi);
-    for (int64_t i = int64_t(blockIdx.x) * kEpiWarps + warp - kEpi0; i < count;
+    for (int64_t i = int64_t(blockIdx.x) * kEpiWarps + warp - S::kEpi0; i < count;
          i += int64_t(gridDim.x) * kEpiWarps) {
       const int64_t row = (i < lo ? i : hi + (i - lo)) * p.ld_out;
       if (p.vec_out && p.N % 8 == 0) {
@@ -922,10 +1074,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     }
   }
 
-  if (MODE == kForward && p.slot_n && warp >= kEpi0 && warp < kMmaWarp) {
+  if (MODE == kForward && p.slot_n && warp >= S::kEpi0 && warp < S::kMmaWarp) {
     // u: zeros at the other places of the tiles in which an entry has rows, a warp a row.
     const int bn = p.slot_n;
-    for (int i = int(blockIdx.x) * kEpiWarps + warp - kEpi0; i < tab.count * 2 * bn;
+    for (int i = int(blockIdx.x) * kEpiWarps + warp - S::kEpi0; i < tab.count * 2 * bn;
          i += int(gridDim.x) * kEpiWarps) {
       const int e = i / (2 * bn), k = i - e * 2 * bn;
       const int lo = tab.row[e], hi = tab.row[e + 1];
@@ -949,7 +1101,15 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     slices_of<EXT, S::kRankSlice>(p, tile, CG == 2 ? 0 : int(rank), nbase, s0, s1);
     const int per_rank = EXT ? (p.rank + S::kRankSlice - 1) / S::kRankSlice : 1;
 
-    if (warp < kCopyWarps) {
+    if (S::kDirect && warp < S::kCopyWarps) {
+      if constexpr (S::kDirect) {
+        const bool ok = p.vec ? split_tile<MODE, true>(p, tile, s0, s1, base, bar_full, bar_empty,
+                                                       ring, dropped)
+                              : split_tile<MODE, false>(p, tile, s0, s1, base, bar_full, bar_empty,
+                                                        ring, dropped);
+        if (!ok) timed_out = true;
+      }
+    } else if (!S::kDirect && warp < S::kCopyWarps) {
       // ---- copies ----
       const int hr = tile.bn / CG;                      // columns staged by this block
       const int qf = tile.q0 + half_rank * hr;          // the first of them
@@ -1166,7 +1326,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         // memory; the 32 of a pair's slice, whose products take 512 cycles, do not: there the
         // rows are gathered by a kernel first.  16384 rows x 4096 x 4096: 620 us by number, 331
         // us + 40 us gathered.  cp.async by the copy warps, counted by a barrier: 758 us.)
-        const int row_in_slice = 4 * (warp + kCopyWarps * (lane >> 2)) + (lane & 3);
+        const int row_in_slice = 4 * (warp + S::kCopyWarps * (lane >> 2)) + (lane & 3);
         const auto row_of = [&](int at, int limit) {
           if (at >= limit) return -1;
           const int row = p.row_index[at];
@@ -1206,7 +1366,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           if (elect_one()) {
             const int fours = MODE == kWgrad ? (c.cnt + 15) / 16 * 4 : (mine + 3) / 4;
             const int x = MODE == kWgrad ? qf : c.k0;
-            for (int f = warp, k = 0; f < fours; f += kCopyWarps, ++k) {
+            for (int f = warp, k = 0; f < fours; f += S::kCopyWarps, ++k) {
               const int4 v = *reinterpret_cast<const int4 *>(my_rows + 4 * k);
 #pragma unroll
               for (int pl = 0; pl < PLANES; ++pl) {
@@ -1227,7 +1387,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           ring.template next<S::kStages>();
         }
       }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == S::kMmaWarp) {
       // ---- products ---- (one thread)
       if (leader && elect_one()) {
         const uint32_t sizes = (uint32_t(tile.bn >> 3) << 17) | (uint32_t(128 * CG >> 4) << 24) |
@@ -1298,12 +1458,12 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       timed_out = __any_sync(~0u, timed_out);
     } else {
       // ---- results ----
-      const int quarter = warp & 3, half = (warp - kEpi0) >> 2;
+      const int quarter = warp & 3, half = (warp - S::kEpi0) >> 2;
       const int n = s1 - s0;
       const uint32_t lanes = tmem + (uint32_t(32 * quarter) << 16);
       const uint32_t tempty = CG == 2 ? map_rank(bar_tempty, 0) : bar_tempty;
       const int nw = tile.n0 + half_rank * 128 + 32 * quarter;
-      const uint32_t stage = out_stage + uint32_t(warp - kEpi0) * 1024;
+      const uint32_t stage = out_stage + uint32_t(warp - S::kEpi0) * 1024;
       const float scale = MODE == kForward && p.scale ? p.scale[tile.g] : 1.0f;
       constexpr int kBlocks = S::kBN / 32;     // 16-column blocks of a warp, every other one
       // The columns that this block adds up and stores: all of them, or its share.
@@ -1311,12 +1471,13 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       const int own1 = CG == 1 ? tile.qn * int(rank + 1) / p.ksplit : tile.qn;
       if constexpr (FEW) {
         results_sync();      // the last tile's sums have been read
-        if (PLANES == 3)
-          add_adapters<float>(p, owner, tile, own0, own1, red_ptr);
+        const int tid = int(threadIdx.x) - 32 * S::kEpi0;
+        if constexpr (PLANES == 3)
+          add_adapters<float>(p, owner, tile, own0, own1, red_ptr, tid);
         else if (p.idesc & (1u << 7))
-          add_adapters<__nv_bfloat16>(p, owner, tile, own0, own1, red_ptr);
+          add_adapters<__nv_bfloat16>(p, owner, tile, own0, own1, red_ptr, tid);
         else
-          add_adapters<__half>(p, owner, tile, own0, own1, red_ptr);
+          add_adapters<__half>(p, owner, tile, own0, own1, red_ptr, tid);
         results_sync();
       }
       auto put = [&](int c0, const float (&v)[16]) {
@@ -1407,10 +1568,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       // in block order, and stores them.
       __syncwarp();
       cluster_sync();
-      if (warp >= kEpi0 && warp < kMmaWarp) {
+      if (warp >= S::kEpi0 && warp < S::kMmaWarp) {
         const int c0 = tile.qn * int(rank) / p.ksplit, c1 = tile.qn * int(rank + 1) / p.ksplit;
         const float scale = MODE == kForward && p.scale ? p.scale[tile.g] : 1.0f;
-        for (int i = int(threadIdx.x) - 32 * kEpi0; i < 128 * (c1 - c0); i += 32 * kEpiWarps) {
+        for (int i = int(threadIdx.x) - 32 * S::kEpi0; i < 128 * (c1 - c0); i += 32 * kEpiWarps) {
           const int l = i & 127, col = c0 + (i >> 7);
           const uint32_t at = red + uint32_t(col * 128 + l) * 4;
           float v = 0.0f;
@@ -1429,14 +1590,14 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     grid_wait();       // no grid ends before the one it follows
     grid_start_next();
   }
-  if (warp < kCopyWarps && timed_out) {
+  if (warp < S::kCopyWarps && timed_out) {
     // Let the copies in flight land before the block goes away: one that was issued does within
     // microseconds.
     const uint64_t t0 = timer_ns();
     while (timer_ns() - t0 < 1000 * 1000) {
     }
   }
-  if (warp == kMmaWarp && leader) {
+  if (warp == S::kMmaWarp && leader) {
     if (elect_one()) mma_commit<CG>(bar_drain, false);
     __syncwarp();
     if (!mbar_wait(bar_drain, 0u, p.wait_limit_ns)) timed_out = true;
@@ -1447,7 +1608,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   __syncthreads();
   if (CG == 2) cluster_sync();   // remote arrivals have landed; neither block uses tensor memory
   tc_fence_after();
-  if (warp == kMmaWarp) {
+  if (warp == S::kMmaWarp) {
     if constexpr (CG == 2)
       asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                    "r"(S::kTmemCols)
@@ -1510,18 +1671,15 @@ __device__ __forceinline__ void plane_tile(const PlaneJob &j, int64_t m, int64_t
   for (int k = 0; k < kPlaneAhead; ++k) {
     if (to[k] < 0) continue;
     if constexpr (F32) {
-      uint16_t h[8][3];
+      float f[8];
+      uint32_t h[3][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) split3(x[k].get(i), h[i]);
+      for (int i = 0; i < 8; ++i) f[i] = x[k].get(i);
+      split8(f, h);
 #pragma unroll
-      for (int pl = 0; pl < 3; ++pl) {
-        uint4 v;
-        v.x = h[0][pl] | (uint32_t(h[1][pl]) << 16);
-        v.y = h[2][pl] | (uint32_t(h[3][pl]) << 16);
-        v.z = h[4][pl] | (uint32_t(h[5][pl]) << 16);
-        v.w = h[6][pl] | (uint32_t(h[7][pl]) << 16);
-        *reinterpret_cast<uint4 *>(j.dst + pl * j.plane + to[k]) = v;
-      }
+      for (int pl = 0; pl < 3; ++pl)
+        *reinterpret_cast<uint4 *>(j.dst + pl * j.plane + to[k]) =
+            make_uint4(h[pl][0], h[pl][1], h[pl][2], h[pl][3]);
     } else {
       *reinterpret_cast<uint4 *>(j.dst + to[k]) = x[k].w[0];
     }
@@ -1791,7 +1949,7 @@ cudaError_t launch_shape(const Maps &m, Params &prm, int64_t tiles, const Device
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(S::kThreads, 1, 1);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = stream;
   // Persistent: a cluster for every tile there can be, at most one per resident slot.
@@ -1846,27 +2004,31 @@ int split_of(int64_t tiles, int64_t slices, int planes, const DeviceInfo &dev) {
   return s;
 }
 
-// Pairs or single blocks for a forward product, by the cycles a K slice of 64 takes in a tile and
-// the rounds of tiles, for groups of equal size: products at 8192 multiply-adds a cycle and SM,
-// copies at 64 bytes.  (Counted per plane product: 16-bit operands have one, split ones six of
-// three planes.)
+// Pairs or single blocks for a forward product, by an estimate of its cycles for groups of equal
+// size: rounds of tiles times what a K slice of 64 takes in one (products at 8192 multiply-adds a
+// cycle and SM, copies at 64 bytes; FP32 has six products of three planes, and on single blocks
+// splits 128 lanes and the columns on the way), and for FP32 pairs the planes' 10 bytes a value
+// at 23 bytes a cycle and SM.  FP32, K = 2048, N = 4096: 16 rows in 8 groups 132 us by planes.
 int forward_shape(int64_t rows, int64_t groups, int64_t N, int64_t K, int dtype) {
   if (N <= 128) return 1;      // 256 lanes would be half empty
   constexpr int64_t kSms = 152;
-  const int planes = dtype == TMM_F32 ? 3 : 1, products = dtype == TMM_F32 ? 6 : 1;
+  const bool f32 = dtype == TMM_F32;
   const int64_t live = std::max<int64_t>(1, std::min(groups, rows));
-  const int64_t each = (rows + live - 1) / live;
+  const int64_t each = (rows + live - 1) / live, slices = (K + kBK - 1) / kBK;
   const auto cost = [&](int cg, int64_t widest, int64_t unit) {
     const int64_t across = (each + widest - 1) / widest;
     const int64_t cols = ((each + across - 1) / across + unit - 1) / unit * unit;
     const int64_t tiles = live * across * ((N + 128 * cg - 1) / (128 * cg));
-    const int64_t slice = std::max(products * 2 * cols, planes * (256 + 2 * cols / cg));
+    const int64_t slice = cg == 1 ? (f32 ? std::max(12 * cols, 900 + 7 * cols) : 256 + 2 * cols)
+                                  : (f32 ? std::max(12 * cols, 768 + 3 * cols)
+                                         : std::max(2 * cols, 256 + cols));
+    const int64_t before = f32 && cg == 2 ? 10 * (live * N + rows) * K / (23 * kSms) : 0;
     // Fewer tiles than blocks: single blocks split a long sum.
-    if (cg == 1 && 2 * tiles <= kSms && K >= 2 * split_slices(planes) * kBK)
-      return slice * tiles / kSms + slice / 8;
-    return (tiles + kSms / cg - 1) / (kSms / cg) * slice;
+    if (cg == 1 && 2 * tiles <= kSms && slices >= 2 * split_slices(f32 ? 3 : 1))
+      return slices * slice * tiles / kSms + slices * slice / 8;
+    return before + slices * slice * ((tiles + kSms / cg - 1) / (kSms / cg));
   };
-  return cost(2, dtype == TMM_F32 ? 128 : 256, 64) <= cost(1, 64, 16) ? 2 : 1;
+  return cost(2, f32 ? 128 : 256, 64) <= cost(1, 64, 16) ? 2 : 1;
 }
 // Adapters: single blocks while the part on the CUDA cores (rows x rank) is small.
 int lora_shape(int64_t rows, int64_t rank) {
@@ -1888,12 +2050,24 @@ cudaError_t q_maps(Maps *m, const Planes &x, const int32_t *index, int cg, int b
   return cudaSuccess;
 }
 
-// Forward product on prepared operands; `index`: the rows of x by number, or NULL.
-cudaError_t run_forward(const Planes &x, const int32_t *index, const Planes &w, bool shared_w,
-                        bool trans_w, int planes, Params prm, const DeviceInfo &dev,
-                        cudaStream_t stream) {
-  const int cg = forward_shape(prm.rows, prm.groups, prm.N, prm.K,
-                               planes == 3 ? TMM_F32 : TMM_BF16);
+// FP32 operands read as they are stored (single blocks; see split_tile).
+bool direct(int cg, int dtype) { return cg == 1 && dtype == TMM_F32; }
+void set_direct(Params *prm, const Stack &P, const Stack &x) {
+  prm->fp = static_cast<const float *>(P.data);
+  prm->ldp = P.ld;
+  prm->stride_p = P.stride;
+  prm->fx = static_cast<const float *>(x.data);
+  prm->ldx = x.ld;
+  prm->vec = on16(P, 4) && on16(x, 4) && P.cols % 8 == 0 && x.cols % 8 == 0;
+}
+
+// Forward product: on the planes (x, w) of the stacks (xs, ws), or on FP32 stacks directly;
+// `index`: the rows of x by number, or NULL.
+cudaError_t run_forward(int dtype, const Planes &x, const Stack &xs, const int32_t *index,
+                        const Planes &w, const Stack &ws, bool trans_w, Params prm,
+                        const DeviceInfo &dev, cudaStream_t stream) {
+  const int planes = dtype == TMM_F32 ? 3 : 1;
+  const int cg = forward_shape(prm.rows, prm.groups, prm.N, prm.K, dtype);
   const int bn = columns_of(cg, planes);
   prm.tile_n = bn;
   prm.panels = int((prm.N + 128 * cg - 1) / (128 * cg));
@@ -1903,16 +2077,21 @@ cudaError_t run_forward(const Planes &x, const int32_t *index, const Planes &w, 
   prm.ksplit = cg == 2 ? 1 : split_of(tiles, (prm.K + kBK - 1) / kBK, planes, dev);
   if (prm.n_out == 0) prm.n_out = prm.N;
   prm.row_index = index;
-  prm.q_rows = int(x.rows);
   prm.p_mn = trans_w ? 0 : 1;
-  prm.p_shared = shared_w ? 1 : 0;
-  Maps m;
-  cudaError_t e;
-  if ((e = tile_map(&m.p, w, trans_w ? 128 : 64)) != cudaSuccess ||
-      (e = q_maps(&m, x, index, cg, bn)) != cudaSuccess)
-    return e;
-  m.e = m.p;
-  m.u = m.q;
+  prm.p_shared = prm.groups > 1 && ws.count == 1;
+  Maps m = {};
+  if (direct(cg, dtype)) {
+    prm.q_rows = int(xs.rows);
+    set_direct(&prm, ws, xs);
+  } else {
+    prm.q_rows = int(x.rows);
+    cudaError_t e;
+    if ((e = tile_map(&m.p, w, trans_w ? 128 : 64)) != cudaSuccess ||
+        (e = q_maps(&m, x, index, cg, bn)) != cudaSuccess)
+      return e;
+    m.e = m.p;
+    m.u = m.q;
+  }
   return launch_any(cg, planes, kForward, m, prm, tiles, dev, stream);
 }
 
@@ -1923,24 +2102,30 @@ static int64_t gathered_rows(int cg, const int32_t *row_index, int64_t rows) {
   return cg == 2 && row_index != nullptr ? rows : 0;
 }
 
+static int shape_of(const GroupedProblem &p) {
+  return forward_shape(p.rows, p.groups, p.N, p.K, p.dtype);
+}
+
 size_t grouped_workspace_bytes(const GroupedProblem &p) {
-  const int64_t gathered =
-      gathered_rows(forward_shape(p.rows, p.groups, p.N, p.K, p.dtype), p.row_index, p.rows);
-  return add_sizes({plane_bytes(p.x, p.dtype, gathered), plane_bytes(p.w, p.dtype)});
+  const int cg = shape_of(p);
+  if (direct(cg, p.dtype)) return 0;
+  return add_sizes({plane_bytes(p.x, p.dtype, gathered_rows(cg, p.row_index, p.rows)),
+                    plane_bytes(p.w, p.dtype)});
 }
 
 cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void *workspace,
                            cudaStream_t stream) {
   char *ws = static_cast<char *>(workspace);
-  const bool shared = p.groups > 1 && p.w.count == 1;
-  const int64_t gathered =
-      gathered_rows(forward_shape(p.rows, p.groups, p.N, p.K, p.dtype), p.row_index, p.rows);
-  PlaneJobs jobs = {};
-  const Planes x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs, gathered, p.row_index);
-  const Planes w = plan_planes(p.w, p.dtype, p.offsets, &ws, &jobs);
-  const cudaError_t e = make_planes(jobs, p.dtype, dev, stream);
-  if (e != cudaSuccess) return e;
-  const int planes = p.dtype == TMM_F32 ? 3 : 1;
+  const int cg = shape_of(p);
+  const int64_t gathered = gathered_rows(cg, p.row_index, p.rows);
+  Planes x = {}, w = {};
+  if (!direct(cg, p.dtype)) {
+    PlaneJobs jobs = {};
+    x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs, gathered, p.row_index);
+    w = plan_planes(p.w, p.dtype, p.offsets, &ws, &jobs);
+    const cudaError_t e = make_planes(jobs, p.dtype, dev, stream);
+    if (e != cudaSuccess) return e;
+  }
   Params prm = {};
   prm.rows = int(p.rows);
   prm.groups = int(p.groups);
@@ -1952,11 +2137,12 @@ cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void 
   prm.ld_out = p.ldy;
   prm.out_type = out_type(p.dtype);
   prm.zero_rows = 1;
-  return run_forward(x, gathered ? nullptr : p.row_index, w, shared, p.trans_w != 0, planes, prm,
-                     dev, stream);
+  return run_forward(p.dtype, x, p.x, gathered ? nullptr : p.row_index, w, p.w, p.trans_w != 0,
+                     prm, dev, stream);
 }
 
 size_t wgrad_workspace_bytes(const WgradProblem &p) {
+  if (direct(wgrad_shape(p.N), p.dtype)) return 0;
   return add_sizes(
       {plane_bytes(p.x, p.dtype, gathered_rows(wgrad_shape(p.N), p.row_index, p.rows)),
        plane_bytes(p.dy, p.dtype)});
@@ -1968,18 +2154,21 @@ cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *wor
   const int cg = wgrad_shape(p.N);
   const int64_t gathered = gathered_rows(cg, p.row_index, p.rows);
   const int32_t *index = gathered ? nullptr : p.row_index;
-  PlaneJobs jobs = {};
-  const Planes x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs, gathered, p.row_index);
-  const Planes dy = plan_planes(p.dy, p.dtype, nullptr, &ws, &jobs);
-  cudaError_t e = make_planes(jobs, p.dtype, dev, stream);
-  if (e != cudaSuccess) return e;
+  Planes x = {}, dy = {};
+  cudaError_t e;
+  if (!direct(cg, p.dtype)) {
+    PlaneJobs jobs = {};
+    x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs, gathered, p.row_index);
+    dy = plan_planes(p.dy, p.dtype, nullptr, &ws, &jobs);
+    if ((e = make_planes(jobs, p.dtype, dev, stream)) != cudaSuccess) return e;
+  }
   const int planes = p.dtype == TMM_F32 ? 3 : 1;
   Params prm = {};
   prm.rows = int(p.rows);
   prm.groups = int(p.groups);
   prm.offsets = p.offsets;
   prm.row_index = index;
-  prm.q_rows = int(x.rows);
+  prm.q_rows = int(gathered ? p.rows : p.x.rows);
   prm.q_cols = int(p.K);
   prm.N = int(p.N);
   prm.idesc = type_desc(p.dtype);
@@ -1995,14 +2184,18 @@ cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *wor
   const int64_t tiles = p.groups * prm.panels * ((p.K + bn - 1) / bn);
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
   if (cg == 1) prm.ksplit = split_of(tiles, (p.rows / p.groups + kBK - 1) / kBK, planes, dev);
-  Maps m;
-  if ((e = row_map(&m.p, dy, kBK)) != cudaSuccess ||
-      (e = index ? row_map(&m.qr, x, 1) : row_map(&m.q, x, kBK)) != cudaSuccess)
-    return e;
-  if (index) m.q = m.qr;
-  else m.qr = m.q;
-  m.e = m.p;
-  m.u = m.q;
+  Maps m = {};
+  if (direct(cg, p.dtype)) {
+    set_direct(&prm, p.dy, p.x);
+  } else {
+    if ((e = row_map(&m.p, dy, kBK)) != cudaSuccess ||
+        (e = index ? row_map(&m.qr, x, 1) : row_map(&m.q, x, kBK)) != cudaSuccess)
+      return e;
+    if (index) m.q = m.qr;
+    else m.qr = m.q;
+    m.e = m.p;
+    m.u = m.q;
+  }
   return launch_any(cg, planes, kWgrad, m, prm, tiles, dev, stream);
 }
 
@@ -2058,13 +2251,21 @@ static size_t u_bytes(const LoraProblem &p) {
   return round256(size_t(u_rows(p)) * size_t(u_columns(p)) * size);   // below 2^30 * 2^11 * 6
 }
 
+// How the product with a is computed on pairs: a forward product of its own.
+static int low_shape(const LoraProblem &p) {
+  return forward_shape(p.rows, p.groups, p.rank, p.K, p.dtype);
+}
+
 // The workspace holds u and the planes of the operands.
 size_t lora_workspace_bytes(const LoraProblem &p) {
   if (lora_shape(p.rows, p.rank) == 1)
-    return add_sizes({u_bytes(p), plane_bytes(p.x, p.dtype), plane_bytes(p.w, p.dtype)});
+    return p.dtype == TMM_F32 ? u_bytes(p)
+                              : add_sizes({u_bytes(p), plane_bytes(p.x, p.dtype),
+                                           plane_bytes(p.w, p.dtype)});
   return add_sizes({u_bytes(p),
                     plane_bytes(p.x, p.dtype, gathered_rows(2, p.row_index, p.rows)),
-                    plane_bytes(p.w, p.dtype), plane_bytes(p.a, p.dtype),
+                    plane_bytes(p.w, p.dtype),
+                    direct(low_shape(p), p.dtype) ? 0 : plane_bytes(p.a, p.dtype),
                     plane_bytes(p.b, p.dtype)});
 }
 
@@ -2077,16 +2278,19 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   void *u = ws;
   ws += u_bytes(p);
   const int64_t gathered = gathered_rows(cg, p.row_index, p.rows);
-  PlaneJobs jobs = {};
-  const Planes x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs, gathered, p.row_index);
-  const Planes w = plan_planes(p.w, p.dtype, nullptr, &ws, &jobs);
-  Planes a = {}, b = {};
-  if (cg == 2) {
-    a = plan_planes(p.a, p.dtype, p.offsets, &ws, &jobs);
-    b = plan_planes(p.b, p.dtype, p.offsets, &ws, &jobs);
+  const bool low_direct = direct(low_shape(p), p.dtype);
+  Planes x = {}, w = {}, a = {}, b = {};
+  cudaError_t e;
+  if (!direct(cg, p.dtype)) {
+    PlaneJobs jobs = {};
+    x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs, gathered, p.row_index);
+    w = plan_planes(p.w, p.dtype, nullptr, &ws, &jobs);
+    if (cg == 2) {
+      if (!low_direct) a = plan_planes(p.a, p.dtype, p.offsets, &ws, &jobs);
+      b = plan_planes(p.b, p.dtype, p.offsets, &ws, &jobs);
+    }
+    if ((e = make_planes(jobs, p.dtype, dev, stream)) != cudaSuccess) return e;
   }
-  cudaError_t e = make_planes(jobs, p.dtype, dev, stream);
-  if (e != cudaSuccess) return e;
   Params prm = {};
   prm.rows = int(p.rows);
   prm.groups = int(p.groups);
@@ -2094,7 +2298,7 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   prm.K = int(p.K);
   prm.rank = int(p.rank);
   prm.idesc = type_desc(p.dtype);
-  Maps m;
+  Maps m = {};
   if (cg == 1) {
     if ((e = launch_row_ranks(p, static_cast<float *>(u), ldu, stream)) != cudaSuccess) return e;
     prm.row_index = p.row_index;
@@ -2116,9 +2320,9 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
     up.n_out = p.dtype == TMM_F32 ? int(p.rank) : int(ldu / 2);
     if (u_rows(p) * planes > INT32_MAX) return cudaErrorInvalidConfiguration;
     up.scale = p.scale;
-    const int32_t *index = gathered ? nullptr : p.row_index;
-    if ((e = run_forward(x, index, a, p.groups > 1 && p.a.count == 1, p.trans_a != 0, planes, up,
-                         dev, stream)) != cudaSuccess)
+    const int32_t *index = gathered && !low_direct ? nullptr : p.row_index;
+    if ((e = run_forward(p.dtype, x, p.x, index, a, p.a, p.trans_a != 0, up, dev, stream)) !=
+        cudaSuccess)
       return e;
     prm.out_index = p.row_index;
     prm.out_rows = int(p.rows);
@@ -2132,7 +2336,7 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   }
   const int bn = columns_of(cg, planes);
   prm.N = prm.n_out = int(p.N);
-  prm.q_rows = int(x.rows);
+  prm.q_rows = int(p.rows);
   prm.tile_n = bn;
   prm.panels = int((p.N + 128 * cg - 1) / (128 * cg));
   const int64_t tiles = prm.panels * ((p.rows + bn - 1) / bn);
@@ -2143,10 +2347,14 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   prm.out = p.y;
   prm.ld_out = p.ldy;
   prm.out_type = out_type(p.dtype);
-  if ((e = tile_map(&m.p, w, p.trans_w ? 128 : 64)) != cudaSuccess ||
-      (e = q_maps(&m, x, nullptr, cg, bn)) != cudaSuccess)
-    return e;
-  if (cg == 1) m.e = m.u = m.p;
+  if (direct(cg, p.dtype)) {
+    set_direct(&prm, p.w, p.x);
+  } else {
+    if ((e = tile_map(&m.p, w, p.trans_w ? 128 : 64)) != cudaSuccess ||
+        (e = q_maps(&m, x, nullptr, cg, bn)) != cudaSuccess)
+      return e;
+    if (cg == 1) m.e = m.u = m.p;
+  }
   return launch_any(cg, planes, kLora, m, prm, tiles, dev, stream);
 }
 
