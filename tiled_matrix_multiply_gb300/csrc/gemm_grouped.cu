@@ -2005,10 +2005,12 @@ int split_of(int64_t tiles, int64_t slices, int planes, const DeviceInfo &dev) {
 }
 
 // Pairs or single blocks for a forward product, by an estimate of its cycles for groups of equal
-// size: rounds of tiles times what a K slice of 64 takes in one (products at 8192 multiply-adds a
-// cycle and SM, copies at 64 bytes; FP32 has six products of three planes, and on single blocks
-// splits 128 lanes and the columns on the way), and for FP32 pairs the planes' 10 bytes a value
-// at 23 bytes a cycle and SM.  FP32, K = 2048, N = 4096: 16 rows in 8 groups 132 us by planes.
+// size: rounds of tiles times what a K slice of 64 takes in one.  16-bit: products at 8192
+// multiply-adds a cycle and SM, copies at 64 bytes.  FP32: six products of three planes on pairs,
+// after making the planes (10 bytes a value at 23 bytes a cycle and SM, and a launch); on single
+// blocks, the measured 2600 + 8 cycles a column of splitting on the way.  (FP32, K = 2048,
+// N = 4096: 1024 rows in 64 groups 706 us on single blocks, 1177 us by planes; 2048 rows in 8
+// groups 406 us and 275 us.)
 int forward_shape(int64_t rows, int64_t groups, int64_t N, int64_t K, int dtype) {
   if (N <= 128) return 1;      // 256 lanes would be half empty
   constexpr int64_t kSms = 152;
@@ -2019,10 +2021,10 @@ int forward_shape(int64_t rows, int64_t groups, int64_t N, int64_t K, int dtype)
     const int64_t across = (each + widest - 1) / widest;
     const int64_t cols = ((each + across - 1) / across + unit - 1) / unit * unit;
     const int64_t tiles = live * across * ((N + 128 * cg - 1) / (128 * cg));
-    const int64_t slice = cg == 1 ? (f32 ? std::max(12 * cols, 900 + 7 * cols) : 256 + 2 * cols)
+    const int64_t slice = cg == 1 ? (f32 ? 2600 + 8 * cols : 256 + 2 * cols)
                                   : (f32 ? std::max(12 * cols, 768 + 3 * cols)
                                          : std::max(2 * cols, 256 + cols));
-    const int64_t before = f32 && cg == 2 ? 10 * (live * N + rows) * K / (23 * kSms) : 0;
+    const int64_t before = f32 && cg == 2 ? 4000 + 10 * (live * N + rows) * K / (23 * kSms) : 0;
     // Fewer tiles than blocks: single blocks split a long sum.
     if (cg == 1 && 2 * tiles <= kSms && slices >= 2 * split_slices(f32 ? 3 : 1))
       return slices * slice * tiles / kSms + slices * slice / 8;
