@@ -56,6 +56,7 @@ FORWARD = [
     ([1], 1, 1), ([3], 16, 8), ([1, 0, 2], 64, 64), ([0, 0, 5, 0], 65, 129),
     ([17, 64, 65, 1], 128, 130), ([200, 30], 72, 257), ([63, 0, 129, 256, 257], 192, 256),
     ([300, 513], 130, 520), ([0, 0], 40, 24), ([1] * 40, 200, 136), ([5, 700, 0, 3], 333, 131),
+    ([2, 1], 2100, 136), ([1500, 0, 900, 7], 96, 392),
 ]
 
 
@@ -241,7 +242,9 @@ def test_single_precision_keeps_all_bits():
 
 LORA = [([1], 1, 64, 64, 8), ([0, 1, 0], 1, 200, 130, 16), ([1, 1, 0, 1], 5, 128, 257, 4),
         ([3, 0, 40, 21], 70, 72, 136, 20), ([90, 0, 100], 200, 130, 300, 64),
-        ([0, 0], 9, 64, 48, 8), ([200, 157], 357, 256, 520, 100), ([1] * 30, 33, 96, 140, 130)]
+        ([0, 0], 9, 64, 48, 8), ([200, 157], 357, 256, 520, 100), ([1] * 30, 33, 96, 140, 130),
+        ([100, 0, 56, 300], 500, 128, 260, 33), ([9] * 40, 400, 64, 136, 8),
+        ([2, 5], 8, 2200, 136, 24)]
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
@@ -352,22 +355,89 @@ def test_repeats_streams_and_graphs_give_the_same_bits(dtype):
     tmm.check_device()
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_outputs_workspaces_and_streams_of_the_caller(dtype):
+    # The same bits whether the call allocates (and is marshalled in one piece) or is given its
+    # output, its workspace or a stream.
+    gen = torch.Generator().manual_seed(23)
+    sizes, K, N, r = [30, 0, 400], 200, 300, 12
+    R = sum(sizes)
+    x = normals(gen, 50, K).to(dtype).cuda()
+    w, a, b = (normals(gen, 3, *s).to(dtype).cuda() for s in ((K, N), (K, r), (r, N)))
+    rows = torch.randint(0, 50, (R,), generator=gen, dtype=torch.int32).cuda()
+    off, dy = offsets_of(sizes).cuda(), normals(gen, R, N).to(dtype).cuda()
+    scale, side = torch.ones(3).cuda(), torch.cuda.Stream()
+    xs = x[rows.long()].contiguous()
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    calls = [(tmm.gemm_grouped, (x, w, off), dict(rows=rows), "y"),
+             (tmm.gemm_grouped_wgrad, (x, dy, off), dict(rows=rows), "dw"),
+             (tmm.gemm_lora, (xs, w[0], a, b, scale, off), {}, "y")]
+    for fn, args, more, name in calls:
+        want = checked(fn, *args, **more)
+        out = torch.zeros_like(want)
+        got = checked(fn, *args, **more, **{name: out}, workspace=ws)
+        assert got is out and torch.equal(out, want)
+        side.wait_stream(torch.cuda.current_stream())
+        got = fn(*args, **more, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    index = torch.randint(0, 3, (300, 2), generator=gen, dtype=torch.int32).cuda()
+    want = checked(tmm.group_rows, index, 3)
+    for g, h in zip(want, tmm.group_rows(index, 3, stream=side)):
+        torch.cuda.synchronize()
+        assert torch.equal(g, h)
+
+
+def test_refusals_with_tensors_on_the_gpu():
+    bf, i = torch.bfloat16, torch.int32
+    x, w = torch.zeros(4, 8, dtype=bf, device="cuda"), torch.zeros(2, 8, 8, dtype=bf, device="cuda")
+    off = torch.zeros(3, dtype=i, device="cuda")
+    for bad in (dict(x=x.float()), dict(w=w[:, :4]), dict(w=w.half()), dict(w=w[0]),
+                dict(offsets=off[:2]), dict(offsets=off.long()), dict(offsets=off.cpu()),
+                dict(rows=off.long()), dict(x=x[:, ::2]), dict(x=x.t())):
+        args = dict(x=x, w=w, offsets=off)
+        args.update(bad)
+        with pytest.raises((TypeError, ValueError)):
+            tmm.gemm_grouped(**args)
+    with pytest.raises(_abi.TmmError) as e:
+        tmm.gemm_grouped(x, w, off, y=x)
+    assert e.value.status == _abi.TMM_ERR_ALIAS
+    with pytest.raises(ValueError):
+        tmm.gemm_grouped_wgrad(x, x[:3], off)
+    with pytest.raises(ValueError):
+        tmm.group_rows(torch.zeros(4, 2, dtype=i, device="cuda"), 513)
+    with pytest.raises(TypeError):
+        tmm.gemm_lora(x, w[0], w, w, torch.ones(2, dtype=bf, device="cuda"), off)
+
+
 def test_a_wait_that_runs_out_is_reported():
-    x = torch.ones(300, 256, dtype=torch.bfloat16, device="cuda")
-    w = torch.ones(2, 256, 256, dtype=torch.bfloat16, device="cuda")
-    few, many = offsets_of([2, 3]).cuda(), offsets_of([140, 160]).cuda()
+    # One block or pair, clusters that share a sum, splitting blocks; adapters, and the gradient.
     lib = _abi.load()
-    for off, rows in ((few, 5), (many, 300)):     # clusters that share a sum; pairs
-        lib.tmm_testing_set_wait_hooks(0, 2_000_000)
-        try:
-            tmm.gemm_grouped(x[:rows], w, off)
-            with pytest.raises(tmm.TmmError) as e:
-                tmm.check_device()
-            assert e.value.status == _abi.TMM_ERR_DEVICE_TIMEOUT
-        finally:
-            lib.tmm_testing_set_wait_hooks(-1, 0)
-        y = checked(tmm.gemm_grouped, x[:rows], w, off)
-        assert torch.equal(y, torch.full_like(y, 256.0))
+    K = 2048
+    few, many = offsets_of([2, 3]).cuda(), offsets_of([1400, 1600]).cuda()
+    for dtype, off, rows in itertools.product(TYPES, (few, many), (5, 3000)):
+        if rows != int(off[-1]):
+            continue
+        x = torch.ones(rows, K, dtype=dtype, device="cuda")
+        w = torch.ones(2, K, 256, dtype=dtype, device="cuda")
+        dy = torch.ones(rows, 256, dtype=dtype, device="cuda")
+        a, b = torch.zeros_like(w[:, :, :8]), torch.zeros_like(w[:, :8])
+        one = torch.ones(2, device="cuda")
+        calls = [lambda: tmm.gemm_grouped(x, w, off), lambda: tmm.gemm_grouped_wgrad(x, dy, off),
+                 lambda: tmm.gemm_lora(x, w[0], a.contiguous(), b.contiguous(), one, off)]
+        wants = [call() for call in calls]
+        tmm.check_device()
+        for call, want in zip(calls, wants):
+            lib.tmm_testing_set_wait_hooks(0, 2_000_000)
+            try:
+                call()
+                with pytest.raises(tmm.TmmError) as e:
+                    tmm.check_device()
+                assert e.value.status == _abi.TMM_ERR_DEVICE_TIMEOUT
+            finally:
+                lib.tmm_testing_set_wait_hooks(-1, 0)
+            assert torch.equal(checked(call), want)
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
@@ -433,3 +503,39 @@ def test_gradients_of_the_adapters(dtype):
     db = checked(tmm.gemm_grouped_wgrad, u, dys_d, offd)
     u_ref = ref.grouped(xs, a, off).to(dtype).double()
     assert torch.equal(db.cpu(), ref.wgrad(u_ref, dys, off).to(dtype))
+
+
+def test_the_expert_layer_of_the_example():
+    # The layer's outputs and gradients in single precision against the same formulas in 64 bits.
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                                    "examples"))
+    import experts_and_adapters as ex
+    gen = torch.Generator().manual_seed(41)
+    T, D, H, E = 70, 96, 130, 5
+    x, dy = normals(gen, T, D).float(), normals(gen, T, D).float()
+    w1, w2 = normals(gen, E, D, H, std=D ** -0.5).float(), normals(gen, E, H, D, std=H ** -0.5).float()
+    logits = normals(gen, T, E).float()
+    y, saved = ex.experts_forward(x.cuda(), w1.cuda(), w2.cuda(), logits.cuda())
+    grads = ex.experts_backward(dy.cuda(), saved)
+    tmm.check_device()
+    leaves = [t.double().requires_grad_() for t in (x, w1, w2, logits)]
+    xd, w1d, w2d, ld = leaves
+    top, experts = ld.topk(2, dim=1)
+    p = torch.softmax(top, dim=1)
+    h = torch.einsum("td,tkdh->tkh", xd, w1d[experts])
+    z = torch.einsum("tkh,tkhd->tkd", torch.relu(h).square(), w2d[experts])
+    want = (z * p[..., None]).sum(1)
+    want.backward(dy.double())
+    dlog = ld.grad.gather(1, experts)
+    # Each step is within 1e-6 of its own norm (two products and a sum in a row, and the square's
+    # factor of two): 1e-5 holds them all.
+    for got, ref64 in zip((y, *grads), (want.detach(), xd.grad, w1d.grad, w2d.grad, dlog)):
+        assert (got.double().cpu() - ref64).norm() <= 1e-5 * ref64.norm()
+
+
+def test_the_example_runs():
+    import experts_and_adapters as ex
+    out = ex.main(tokens=200, model=128, inner=256, experts=4)
+    assert all(bool(torch.isfinite(t.float()).all()) for t in out.values())

@@ -341,13 +341,12 @@ int tmm_check_device(tmm_stream_t stream) {
   if (e == cudaSuccess) e = tmm::grouped_device_status(&grouped, true);
   if (e != cudaSuccess)
     return fail(TMM_ERR_CUDA, "tmm_check_device: status read: %s", cudaGetErrorString(e));
-  if ((simt | tc3 | naive | stage | grouped) & tmm::kStatusBounds)
+  if ((simt | tc3 | naive | stage) & tmm::kStatusBounds)
     return fail(TMM_ERR_BOUNDS,
                 "tmm_check_device: a range check of the bounds-checked build failed inside %s",
                 (simt & tmm::kStatusBounds)    ? "gemm_f32"
                 : (stage & tmm::kStatusBounds) ? "gemm_f32 (operand restaging)"
                 : (tc3 & tmm::kStatusBounds)   ? "gemm_f32_tc3"
-                : (grouped & tmm::kStatusBounds) ? "a grouped product"
                                                : "gemm_f32_naive");
   if (simt | tc3 | win | sm | grouped)
     return fail(TMM_ERR_DEVICE_TIMEOUT,

@@ -52,7 +52,6 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "bounds_check.cuh"
 #include "grouped.h"
 #include "tmm_gemm.h"
 
@@ -2017,18 +2016,19 @@ int forward_shape(int64_t rows, int64_t groups, int64_t N, int64_t K, int dtype)
   const bool f32 = dtype == TMM_F32;
   const int64_t live = std::max<int64_t>(1, std::min(groups, rows));
   const int64_t each = (rows + live - 1) / live, slices = (K + kBK - 1) / kBK;
-  const auto cost = [&](int cg, int64_t widest, int64_t unit) {
+  const auto cost = [&](int cg, int64_t widest, int64_t unit) {      // double: no size overflows it
     const int64_t across = (each + widest - 1) / widest;
     const int64_t cols = ((each + across - 1) / across + unit - 1) / unit * unit;
     const int64_t tiles = live * across * ((N + 128 * cg - 1) / (128 * cg));
-    const int64_t slice = cg == 1 ? (f32 ? 2600 + 8 * cols : 256 + 2 * cols)
-                                  : (f32 ? std::max(12 * cols, 768 + 3 * cols)
-                                         : std::max(2 * cols, 256 + cols));
-    const int64_t before = f32 && cg == 2 ? 4000 + 10 * (live * N + rows) * K / (23 * kSms) : 0;
+    const double slice = cg == 1 ? (f32 ? 2600 + 8 * cols : 256 + 2 * cols)
+                                 : (f32 ? std::max(12 * cols, 768 + 3 * cols)
+                                        : std::max(2 * cols, 256 + cols));
+    const double before =
+        f32 && cg == 2 ? 4000 + 10 * (double(live) * N + rows) * K / (23 * kSms) : 0;
     // Fewer tiles than blocks: single blocks split a long sum.
     if (cg == 1 && 2 * tiles <= kSms && slices >= 2 * split_slices(f32 ? 3 : 1))
-      return slices * slice * tiles / kSms + slices * slice / 8;
-    return before + slices * slice * ((tiles + kSms / cg - 1) / (kSms / cg));
+      return slices * slice * (double(tiles) / kSms + 0.125);
+    return before + slices * slice * double((tiles + kSms / cg - 1) / (kSms / cg));
   };
   return cost(2, f32 ? 128 : 256, 64) <= cost(1, 64, 16) ? 2 : 1;
 }

@@ -65,8 +65,7 @@ cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *wor
                          cudaStream_t stream);
 cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *workspace,
                         cudaStream_t stream);
-// Status word of the grouped kernels: bit 1 a bounded wait ran out of time, bit 2 a range
-// check of the bounds-checked build failed.
+// Status word of the grouped kernels: bit 1 a bounded wait ran out of time.
 cudaError_t grouped_device_status(unsigned int *status, bool clear);
 void grouped_set_test_hooks(int drop_block, int64_t wait_limit_ns);
 

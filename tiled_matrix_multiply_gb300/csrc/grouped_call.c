@@ -12,8 +12,7 @@
 
 #include "tmm_gemm.h"
 
-static PyObject *s_dtype, *s_device, *s_is_cuda, *s_shape, *s_stride, *s_data_ptr, *s_get_device,
-    *s_cuda_stream;
+static PyObject *s_dtype, *s_device, *s_is_cuda, *s_shape, *s_stride, *s_data_ptr, *s_get_device;
 static PyObject *t_tensor, *t_empty, *t_raw_stream, *t_current_device, *t_row_groups, *t_uint8,
     *t_int32, *t_int64, *t_float32, *t_types[3], *t_kwnames;
 
@@ -106,19 +105,15 @@ static int index_of(PyObject *x, const Operand *like, int64_t length, Operand *o
          (length < 0 || o->cols == length);
 }
 
-/* The device is the current one; its current stream (or the given one's handle). */
-static int stream_of(long device, PyObject *given, tmm_stream_t *out) {
+/* The current stream of the device, which has to be the current one. */
+static int stream_of(long device, tmm_stream_t *out) {
   PyObject *v = PyObject_CallNoArgs(t_current_device);
   const long now = v ? PyLong_AsLong(v) : -1;
   Py_XDECREF(v);
   if (now != device) return 0;
-  if (given != Py_None) {
-    v = PyObject_GetAttr(given, s_cuda_stream);
-  } else {
-    PyObject *d = PyLong_FromLong(device);
-    v = d ? PyObject_CallOneArg(t_raw_stream, d) : NULL;
-    Py_XDECREF(d);
-  }
+  PyObject *d = PyLong_FromLong(device);
+  v = d ? PyObject_CallOneArg(t_raw_stream, d) : NULL;
+  Py_XDECREF(d);
   if (v == NULL) return 0;
   *out = (tmm_stream_t)PyLong_AsVoidPtr(v);
   Py_DECREF(v);
@@ -165,7 +160,7 @@ static PyObject *other(PyObject *a, PyObject *b, PyObject *c) {
 static PyObject *grouped(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
   Operand x, w, off, rows;
-  if (n != 5 || !describe(a[0], 2, 0, &x) || x.code < 0 || !describe(a[1], 3, 1, &w) ||
+  if (n != 4 || !describe(a[0], 2, 0, &x) || x.code < 0 || !describe(a[1], 3, 1, &w) ||
       w.type != x.type || w.device != x.device || w.rows != x.cols ||
       !index_of(a[2], &x, w.count + 1, &off))
     return other(NULL, NULL, NULL);
@@ -177,7 +172,7 @@ static PyObject *grouped(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     index = rows.ptr;
   }
   tmm_stream_t s;
-  if (!stream_of(x.device, a[4], &s)) return other(NULL, NULL, NULL);
+  if (!stream_of(x.device, &s)) return other(NULL, NULL, NULL);
   PyObject *device = PyObject_GetAttr(a[0], s_device), *ws = NULL, *y = NULL;
   void *wp, *yp;
   const size_t need = f_grouped_size(x.code, w.trans, w.count, R, w.cols, x.cols, x.ptr, x.rows,
@@ -196,7 +191,7 @@ static PyObject *grouped(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 static PyObject *wgrad(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
   Operand x, dy, off, rows;
-  if (n != 5 || !describe(a[0], 2, 0, &x) || x.code < 0 || !describe(a[1], 2, 0, &dy) ||
+  if (n != 4 || !describe(a[0], 2, 0, &x) || x.code < 0 || !describe(a[1], 2, 0, &dy) ||
       dy.type != x.type || dy.device != x.device || !index_of(a[2], &x, -1, &off) || off.cols < 2)
     return other(NULL, NULL, NULL);
   const int32_t *index = NULL;
@@ -208,7 +203,7 @@ static PyObject *wgrad(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   }
   const int64_t groups = off.cols - 1, K = x.cols, N = dy.cols;
   tmm_stream_t s;
-  if (!stream_of(x.device, a[4], &s)) return other(NULL, NULL, NULL);
+  if (!stream_of(x.device, &s)) return other(NULL, NULL, NULL);
   PyObject *device = PyObject_GetAttr(a[0], s_device), *ws = NULL, *dw = NULL;
   void *wp, *dwp;
   const size_t need =
@@ -227,7 +222,7 @@ static PyObject *wgrad(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 static PyObject *lora(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
   Operand x, w, la, lb, scale, off, rows;
-  if (n != 8 || !describe(a[0], 2, 0, &x) || x.code < 0 || !describe(a[1], 2, 1, &w) ||
+  if (n != 7 || !describe(a[0], 2, 0, &x) || x.code < 0 || !describe(a[1], 2, 1, &w) ||
       !describe(a[2], 3, 1, &la) || !describe(a[3], 3, 1, &lb) || w.type != x.type ||
       la.type != x.type || lb.type != x.type || w.device != x.device || la.device != x.device ||
       lb.device != x.device || w.rows != x.cols || la.rows != x.cols || lb.cols != w.cols ||
@@ -242,7 +237,7 @@ static PyObject *lora(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   }
   const int64_t T = x.rows, K = x.cols, N = w.cols, r = la.cols;
   tmm_stream_t s;
-  if (!stream_of(x.device, a[7], &s)) return other(NULL, NULL, NULL);
+  if (!stream_of(x.device, &s)) return other(NULL, NULL, NULL);
   PyObject *device = PyObject_GetAttr(a[0], s_device), *ws = NULL, *y = NULL;
   void *wp, *yp;
   const size_t need =
@@ -263,7 +258,7 @@ static PyObject *lora(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 static PyObject *group_rows_(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
   Operand x;
-  if (n != 3 || !PyLong_Check(a[1])) return other(NULL, NULL, NULL);
+  if (n != 2 || !PyLong_Check(a[1])) return other(NULL, NULL, NULL);
   const long groups = PyLong_AsLong(a[1]);
   int two = describe(a[0], 2, 0, &x);
   if (!two) {
@@ -275,7 +270,7 @@ static PyObject *group_rows_(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     return other(NULL, NULL, NULL);
   const int64_t tokens = two ? x.rows : x.cols, fan = two ? x.cols : 1, slots = tokens * fan;
   tmm_stream_t s;
-  if (!stream_of(x.device, a[2], &s)) return other(NULL, NULL, NULL);
+  if (!stream_of(x.device, &s)) return other(NULL, NULL, NULL);
   PyObject *device = PyObject_GetAttr(a[0], s_device), *ws = NULL, *r = NULL;
   if (device == NULL) return other(NULL, NULL, NULL);
   PyObject *out[4] = {NULL, NULL, NULL, NULL};
@@ -331,11 +326,11 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "grouped_call", NULL,
                                     NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit_grouped_call(void) {
-  PyObject **const names[8] = {&s_dtype, &s_device, &s_is_cuda, &s_shape, &s_stride, &s_data_ptr,
-                               &s_get_device, &s_cuda_stream};
-  static const char *const text[8] = {"dtype", "device", "is_cuda", "shape", "stride", "data_ptr",
-                                      "get_device", "cuda_stream"};
-  for (int i = 0; i < 8; ++i)
+  PyObject **const names[7] = {&s_dtype, &s_device,   &s_is_cuda,   &s_shape,
+                               &s_stride, &s_data_ptr, &s_get_device};
+  static const char *const text[7] = {"dtype",  "device",   "is_cuda",   "shape",
+                                      "stride", "data_ptr", "get_device"};
+  for (int i = 0; i < 7; ++i)
     if ((*names[i] = PyUnicode_InternFromString(text[i])) == NULL) return NULL;
   t_kwnames = Py_BuildValue("(OO)", s_dtype, s_device);
   if (t_kwnames == NULL) return NULL;

@@ -13,8 +13,9 @@ are bfloat16, float16 and float32, the same for all matrices of a call.
     dx_rows = tmm.gemm_grouped(dh, w.transpose(1, 2), plan.offsets)
     out = h[plan.position.view(tokens, k)]          # back in token order
 
-Everything is asynchronous on the current torch stream of the operands' device;
-no call reads a group's size on the host.
+Everything is asynchronous on the current torch stream of the operands' device (or, with
+``stream``, on that stream, to which outputs and workspace then belong); no call reads a
+group's size on the host.
 """
 from __future__ import annotations
 
@@ -122,10 +123,18 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _call(name, like, stream, ws, *args):
-    """Call the entry point on the operands' device and stream; raise its error."""
+def _on_stream(stream, like, fn, *args, **kwargs):
+    """The call with `stream` as the current one, so that what it allocates belongs there."""
+    if stream.device != like.device:
+        raise ValueError(f"stream is on {stream.device}, the operands on {like.device}")
+    with torch.cuda.stream(stream):
+        return fn(*args, **kwargs)
+
+
+def _call(name, like, ws, *args):
+    """Call the entry point on the operands' device and its current stream; raise its error."""
     device = like.get_device()
-    s = _raw_stream(device) if stream is None else stream.cuda_stream
+    s = _raw_stream(device)
     lib = _abi.load()
     if torch.cuda.current_device() == device:
         rc = _try(lib, name, ws, s, args)
@@ -176,13 +185,16 @@ def group_rows(index, groups, stream=None):
     A slot's group is its number where that is in [0, groups); the other slots belong to no
     group and come last.  Returns ``RowGroups``.
     """
-    done = _usual.group_rows(index, groups, stream)
-    if done is not None:
-        return done
+    if stream is None:
+        done = _usual.group_rows(index, groups)
+        if done is not None:
+            return done
     if not isinstance(index, torch.Tensor) or index.dtype not in (torch.int32, torch.int64):
         raise TypeError("index must be an int32 or int64 tensor")
     if not index.is_cuda:
         raise ValueError("index must be a CUDA tensor")
+    if stream is not None:
+        return _on_stream(stream, index, group_rows, index, groups)
     shape = index.shape
     if len(shape) not in (1, 2) or not index.is_contiguous():
         raise ValueError("index must be a contiguous tensor (tokens,) or (tokens, k)")
@@ -198,7 +210,7 @@ def group_rows(index, groups, stream=None):
     rows = torch.empty(slots, dtype=i32, device=device)
     position = torch.empty(slots, dtype=i32, device=device)
     ws = _scratch(_abi.load().group_rows_workspace_size(tokens, fan, groups), index)
-    _call("group_rows", index, stream, ws, tokens, fan, groups, index.data_ptr(),
+    _call("group_rows", index, ws, tokens, fan, groups, index.data_ptr(),
           64 if index.dtype == torch.int64 else 32, offsets.data_ptr(), order.data_ptr(),
           rows.data_ptr(), position.data_ptr())
     return RowGroups(offsets, order, rows, position)
@@ -211,11 +223,13 @@ def gemm_grouped(x, w, offsets, rows=None, y=None, workspace=None, stream=None):
     (groups + 1); rows: int32, the row of x that each p reads (a number outside x reads zeros),
     or None for p itself.  y: (len(rows) or x_rows, N); its rows of no group are zero.
     """
-    if y is None and workspace is None:
-        done = _usual.grouped(x, w, offsets, rows, stream)
+    if y is None and workspace is None and stream is None:
+        done = _usual.grouped(x, w, offsets, rows)
         if done is not None:
             return done
     code = _first(x, "x")
+    if stream is not None:
+        return _on_stream(stream, x, gemm_grouped, x, w, offsets, rows, y, workspace)
     x_rows, K, ldx, _, _ = _operand(x, "x", x, 2)
     K2, N, ldw, stride_w, trans = _operand(w, "w", x, 3, True)
     groups = w.shape[0]
@@ -237,7 +251,7 @@ def gemm_grouped(x, w, offsets, rows=None, y=None, workspace=None, stream=None):
             *head, rows_ptr, w_ptr, ldw, stride_w), x)
     else:
         _given_workspace(workspace, x)
-    _call("gemm_grouped", x, stream, workspace, *head, offsets_ptr, rows_ptr, w_ptr, ldw,
+    _call("gemm_grouped", x, workspace, *head, offsets_ptr, rows_ptr, w_ptr, ldw,
           stride_w, y.data_ptr(), ldy)
     return y
 
@@ -247,11 +261,13 @@ def gemm_grouped_wgrad(x, dy, offsets, rows=None, dw=None, workspace=None, strea
 
     The gradient of ``gemm_grouped`` with respect to w; x, offsets and rows as there, dy (R, N).
     """
-    if dw is None and workspace is None:
-        done = _usual.wgrad(x, dy, offsets, rows, stream)
+    if dw is None and workspace is None and stream is None:
+        done = _usual.wgrad(x, dy, offsets, rows)
         if done is not None:
             return done
     code = _first(x, "x")
+    if stream is not None:
+        return _on_stream(stream, x, gemm_grouped_wgrad, x, dy, offsets, rows, dw, workspace)
     x_rows, K, ldx, _, _ = _operand(x, "x", x, 2)
     R, N, lddy, _, _ = _operand(dy, "dy", x, 2)
     offsets_ptr = _index_ptr(offsets, "offsets", x, None)
@@ -272,7 +288,7 @@ def gemm_grouped_wgrad(x, dy, offsets, rows=None, dw=None, workspace=None, strea
             *head, rows_ptr, dy_ptr, lddy), x)
     else:
         _given_workspace(workspace, x)
-    _call("gemm_grouped_wgrad", x, stream, workspace, *head, offsets_ptr, rows_ptr, dy_ptr, lddy,
+    _call("gemm_grouped_wgrad", x, workspace, *head, offsets_ptr, rows_ptr, dy_ptr, lddy,
           dw.data_ptr(), lddw, stride)
     return dw
 
@@ -285,11 +301,13 @@ def gemm_lora(x, w, a, b, scale, offsets, rows=None, y=None, workspace=None, str
     ``offsets`` and ``order`` of ``group_rows(index, adapters)``; rows past offsets[-1] have no
     adapter.  rows=None: x is in group order already.
     """
-    if y is None and workspace is None:
-        done = _usual.lora(x, w, a, b, scale, offsets, rows, stream)
+    if y is None and workspace is None and stream is None:
+        done = _usual.lora(x, w, a, b, scale, offsets, rows)
         if done is not None:
             return done
     code = _first(x, "x")
+    if stream is not None:
+        return _on_stream(stream, x, gemm_lora, x, w, a, b, scale, offsets, rows, y, workspace)
     T, K, ldx, _, _ = _operand(x, "x", x, 2)
     K2, N, ldw, _, tw = _operand(w, "w", x, 2, True)
     K3, r, lda, stride_a, ta = _operand(a, "a", x, 3, True)
@@ -315,6 +333,6 @@ def gemm_lora(x, w, a, b, scale, offsets, rows=None, y=None, workspace=None, str
         workspace = _scratch(_abi.load().gemm_lora_workspace_size(*head, rows_ptr, *mats), x)
     else:
         _given_workspace(workspace, x)
-    _call("gemm_lora", x, stream, workspace, *head, offsets_ptr, rows_ptr, *mats,
+    _call("gemm_lora", x, workspace, *head, offsets_ptr, rows_ptr, *mats,
           scale.data_ptr(), y.data_ptr(), ldy)
     return y
