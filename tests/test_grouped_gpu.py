@@ -273,6 +273,22 @@ def test_lora_integers_are_exact(dtype, trans, sizes, T, K, N, r):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("T,N", [(4096, 4096), (4031, 4096), (3000, 4090), (2300, 4096),
+                                 (1000, 8192)])
+def test_lora_many_tiles(dtype, T, N):
+    # Many tiles of rows, whole ones and ends of every kind.
+    gen = torch.Generator().manual_seed(T)
+    K, r, sizes = 40, 8, [T // 3, 0, T // 2 + 5]
+    x, w = ints(gen, T, K, top=1), ints(gen, K, N, top=1)
+    a, b = ints(gen, 3, K, r, top=1), ints(gen, 3, r, N, top=1)
+    scale, off = torch.ones(3), offsets_of(sizes)
+    order = torch.randperm(T, generator=gen).to(torch.int32)
+    y = checked(tmm.gemm_lora, cuda(x, dtype), cuda(w, dtype), cuda(a, dtype), cuda(b, dtype),
+                scale.cuda(), cuda(off), rows=cuda(order))
+    assert torch.equal(y.cpu(), ref.lora(x, w, a, b, scale, off, order).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
 @pytest.mark.parametrize("sizes,T,K,N,r", [([1] * 12, 14, 1024, 300, 16),
                                            ([150, 0, 260], 430, 600, 515, 48)])
 def test_lora_random(dtype, sizes, T, K, N, r):

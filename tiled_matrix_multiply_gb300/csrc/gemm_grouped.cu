@@ -84,8 +84,9 @@ struct Shape {
   static constexpr int kMmaWarp = kCopyWarps + kEpiWarps;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
   static constexpr int kBN = PLANES == 3 ? (CG == 2 ? 128 : 64) : (CG == 2 ? 256 : 64);
-  static constexpr int kUnit = CG == 2 ? 64 : 16;    // columns are rounded up to this
-  static constexpr int kBox = kUnit / CG;            // rows of one copy of Q
+  static constexpr int kUnit = CG == 2 ? 32 : 16;    // columns are rounded up to this
+  static constexpr int kBox = CG == 2 ? 32 : 16;     // rows of one copy of Q (the last one may
+                                                     // bring more rows than the tile needs)
   static constexpr uint32_t kQTile = uint32_t(kBN / CG) * 128;
   static constexpr uint32_t kStage = PLANES * (kPTile + kQTile);
   static constexpr int kStages = PLANES == 3 ? (CG == 2 ? 3 : 2) : (CG == 2 ? 6 : 7);
@@ -389,8 +390,9 @@ struct Tile {
                   // group's entry e0
 };
 
-// The tables in shared memory: the groups that have rows (every group in the gradient): number,
-// first row (one more entry: the end of the last), first tile.
+// The tables in shared memory: the groups that have rows: number, first row (one more entry: the
+// end of the last), first tile.  In the gradient: every group's first row, by its number, and the
+// numbers in the order of the tiles.
 struct Table {
   const int *gid, *row, *tile;
   int count, tiles;
@@ -406,6 +408,7 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const Table &tab, int t
     const int per = qt * p.panels;
     r.g = t / per;
     const int i = t - r.g * per;
+    r.g = tab.gid[r.g];
     const int panel = i / qt;
     r.n0 = panel * 128 * CG;
     r.q0 = (i - panel * qt) * p.tile_n;
@@ -1025,6 +1028,20 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     }
     proxy_fence();      // the ring is written by the copy engine from here on
   }
+  if constexpr (MODE == kWgrad) {
+    // The order of the groups: most rows first, so that the rounds of tiles, handed out in turn,
+    // end with the short ones (8 groups of a router's sizes, 4096 x 4096: 8 % less).
+    __syncthreads();
+    for (int g = threadIdx.x; g < p.groups; g += S::kThreads) {
+      const int n = tab_row[g + 1] - tab_row[g];
+      int before = 0;
+      for (int h = 0; h < p.groups; ++h) {
+        const int m = tab_row[h + 1] - tab_row[h];
+        before += m > n || (m == n && h < g);
+      }
+      tab_gid[before] = g;
+    }
+  }
   if constexpr (FEW) {
     // The adapter of every row of x: its list entry's number, -1 for none, -2 for a row that the
     // order does not name (which is not written).
@@ -1044,7 +1061,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   }
   tc_fence_before();
   __syncthreads();
-  if (CG == 2 || p.ksplit > 1) cluster_sync();   // barriers exist before any remote arrival
+  if (CG == 2) cluster_sync();   // barriers exist before any remote arrival
   tc_fence_after();
   const uint32_t tmem = slot_ptr[0];
   const Table tab = {tab_gid, tab_row, tab_tile, int(slot_ptr[1]), int(slot_ptr[2])};
@@ -1119,7 +1136,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       // part of the ring holds will do.
       const auto held = [&](int half) { return max(0, min(tile.qn - half * hr, hr)); };
       const int mine = held(half_rank);
-      const int boxes = (mine + S::kBox - 1) / S::kBox;
+      const auto boxes_of = [&](int half) { return (held(half) + S::kBox - 1) / S::kBox; };
+      const auto whole = [&](int half) { return CG == 2 && held(half) * CG == p.tile_n; };
+      const int boxes = boxes_of(half_rank);
       const int qblocks = hr / 64;
       const bool by_row = CG == 1 && MODE != kLora && p.row_index != nullptr;
       uint32_t usual = 0;      // bytes of an ordinary slice, of both blocks of a pair
@@ -1128,9 +1147,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       } else {
 #pragma unroll
         for (int h = 0; h < CG; ++h)
-          usual += PLANES * (kPTile + uint32_t(by_row ? (held(h) + 3) / 4 * 512
-                                                      : (held(h) + S::kBox - 1) / S::kBox *
-                                                            (S::kBox * 128)));
+          usual += PLANES * (kPTile + uint32_t(by_row         ? (held(h) + 3) / 4 * 512
+                                               : whole(h) ? hr * 128
+                                                          : boxes_of(h) * (S::kBox * 128)));
       }
 
       // What a slice s is.  A group's last slice in the gradient needs rows of zeros: its copies
@@ -1162,7 +1181,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           return uint32_t(PLANES) * (kPTile + uint32_t(by_row ? (c.cnt + 15) / 16 * 2048 * qblocks
                                                              : qblocks * 8192));
         return PLANES * ((p.e_mn ? 2 * S::kRankSlice * 128 : kPTile) +
-                         uint32_t((held(half) + S::kBox - 1) / S::kBox * (S::kBox * 128)));
+                         uint32_t(boxes_of(half) * (S::kBox * 128)));
       };
       const auto patch_of = [&](const Slice &c) { return MODE == kWgrad && c.cnt < kBK; };
       // A slice that slice_at describes as ordinary in every respect.
@@ -1216,7 +1235,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
             for (int b = 0; b < boxes; ++b)
               tma_2d<CG>(sq + pl * S::kQTile + b * (S::kBox * 128), &map_u, c.k0,
                          c.row + b * S::kBox + pl * p.u_rows, bar);
-        } else if (CG == 2 && mine * CG == p.tile_n) {
+        } else if (whole(half_rank)) {
           // A full tile: one copy a plane.
 #pragma unroll
           for (int pl = 0; pl < PLANES; ++pl)
@@ -1319,24 +1338,26 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           ring.template skip<S::kStages>(s1 - s0);
         }
       } else {
-        // Rows by number, four to a copy (single blocks): warp w issues fours w, w + 4, ...; lane
-        // l looks up row l % 4 of the warp's four l / 4; -1 is a row of zeros.  (Such a copy takes
+        // Rows by number, four to a copy (single blocks), by warps 1 to 3, while warp 0 copies P:
+        // warp w issues fours w - 1, w + 2, ...; lane l looks up row l % 4 of the warp's four l / 4;
+        // -1 is a row of zeros.  (Such a copy takes
         // the copy engine about 40 cycles.  The 16 of a slice of 64 columns keep up with the
         // memory; the 32 of a pair's slice, whose products take 512 cycles, do not: there the
         // rows are gathered by a kernel first.  16384 rows x 4096 x 4096: 620 us by number, 331
         // us + 40 us gathered.  cp.async by the copy warps, counted by a barrier: 758 us.)
-        const int row_in_slice = 4 * (warp + S::kCopyWarps * (lane >> 2)) + (lane & 3);
+        const int row_in_slice = 4 * (warp - 1 + 3 * (lane >> 2)) + (lane & 3);
         const auto row_of = [&](int at, int limit) {
           if (at >= limit) return -1;
           const int row = p.row_index[at];
           return row >= 0 && row < p.q_rows ? row : -1;
         };
         int next = -1;      // gradient: this lane's row of the next slice
-        if (MODE != kWgrad) {
+        if (warp == 0) {
+        } else if (MODE != kWgrad) {
           __syncwarp();
           my_rows[lane] = row_of(qf + row_in_slice, tile.q0 + tile.qn);
           __syncwarp();
-        } else if (s0 < s1 && lane < 16) {
+        } else if (s0 < s1 && lane < 24) {
           next = row_of(tile.k0 + s0 * kBK + row_in_slice, tile.k0 + tile.klen);
         }
         for (int s = s0; s < s1 && !timed_out; ++s) {
@@ -1356,16 +1377,16 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           }
           dropped = false;
           __syncwarp();
-          if (MODE == kWgrad) {
-            if (lane < 16) my_rows[lane] = next;
+          if (MODE == kWgrad && warp > 0) {
+            if (lane < 24) my_rows[lane] = next;
             __syncwarp();
-            if (s + 1 < s1 && lane < 16)
+            if (s + 1 < s1 && lane < 24)
               next = row_of(c.k0 + kBK + row_in_slice, tile.k0 + tile.klen);
           }
-          if (elect_one()) {
+          if (warp > 0 && elect_one()) {
             const int fours = MODE == kWgrad ? (c.cnt + 15) / 16 * 4 : (mine + 3) / 4;
             const int x = MODE == kWgrad ? qf : c.k0;
-            for (int f = warp, k = 0; f < fours; f += S::kCopyWarps, ++k) {
+            for (int f = warp - 1, k = 0; f < fours; f += 3, ++k) {
               const int4 v = *reinterpret_cast<const int4 *>(my_rows + 4 * k);
 #pragma unroll
               for (int pl = 0; pl < PLANES; ++pl) {
@@ -2276,6 +2297,7 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   char *ws = static_cast<char *>(workspace);
   const int planes = p.dtype == TMM_F32 ? 3 : 1;
   const int cg = lora_shape(p.rows, p.rank);
+  const int bn = columns_of(cg, planes);
   const int64_t ldu = u_columns(p);
   void *u = ws;
   ws += u_bytes(p);
@@ -2317,7 +2339,7 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
     up.out = u;
     up.ld_out = ldu;
     up.stride_out = u_rows(p) * ldu;
-    up.slot_n = columns_of(2, planes);
+    up.slot_n = bn;
     up.out_type = kOutU;
     up.n_out = p.dtype == TMM_F32 ? int(p.rank) : int(ldu / 2);
     if (u_rows(p) * planes > INT32_MAX) return cudaErrorInvalidConfiguration;
@@ -2336,7 +2358,6 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
         (e = row_map(&m.u, um, uint32_t(box_of(cg)))) != cudaSuccess)
       return e;
   }
-  const int bn = columns_of(cg, planes);
   prm.N = prm.n_out = int(p.N);
   prm.q_rows = int(p.rows);
   prm.tile_n = bn;
