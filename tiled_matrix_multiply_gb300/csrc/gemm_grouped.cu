@@ -241,9 +241,12 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -1591,14 +1594,42 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       if (warp >= S::kEpi0 && warp < S::kMmaWarp) {
         const int c0 = tile.qn * int(rank) / p.ksplit, c1 = tile.qn * int(rank + 1) / p.ksplit;
         const float scale = MODE == kForward && p.scale ? p.scale[tile.g] : 1.0f;
-        for (int i = int(threadIdx.x) - 32 * S::kEpi0; i < 128 * (c1 - c0); i += 32 * kEpiWarps) {
-          const int l = i & 127, col = c0 + (i >> 7);
-          const uint32_t at = red + uint32_t(col * 128 + l) * 4;
-          float v = 0.0f;
-          for (int b = 0; b < p.ksplit; ++b) v += ld_cluster(map_rank(at, uint32_t(b)));
-          int64_t o = out_row<MODE>(p, tile, col);
-          if (FEW && owner[tile.q0 + col] == -2) o = -1;
-          if (o >= 0 && tile.n0 + l < p.n_out) store_out<PLANES>(p, o, tile.n0 + l, v * scale);
+        // Four lanes' values a load and kBatch loads of every block in flight: read one by one
+        // they took longer than the slices (4096 x 4096 x 64 shared by two: 17.5 us).
+        constexpr int kBatch = 4, kStep = 32 * kEpiWarps;
+        const int total = 32 * (c1 - c0);
+        for (int i0 = int(threadIdx.x) - 32 * S::kEpi0; i0 < total; i0 += kStep * kBatch) {
+          float4 v[kBatch] = {};
+#pragma unroll 2
+          for (int b = 0; b < p.ksplit; ++b) {
+            const uint32_t from = map_rank(red, uint32_t(b)) + uint32_t(c0 * 512);
+            float4 w[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+              w[u] = make_float4(0, 0, 0, 0);
+              if (i0 + u * kStep < total) w[u] = ld_cluster4(from + uint32_t(i0 + u * kStep) * 16);
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+              v[u].x += w[u].x;
+              v[u].y += w[u].y;
+              v[u].z += w[u].z;
+              v[u].w += w[u].w;
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) {
+            const int i = i0 + u * kStep;
+            if (i >= total) break;
+            const int col = c0 + (i >> 5), n = tile.n0 + (i & 31) * 4;
+            int64_t o = out_row<MODE>(p, tile, col);
+            if (FEW && owner[tile.q0 + col] == -2) o = -1;
+            if (o < 0) continue;
+            const float f[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (n + j < p.n_out) store_out<PLANES>(p, o, n + j, f[j] * scale);
+          }
         }
       }
       __syncwarp();
