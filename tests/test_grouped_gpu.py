@@ -555,3 +555,64 @@ def test_the_example_runs():
     import experts_and_adapters as ex
     out = ex.main(tokens=200, model=128, inner=256, experts=4)
     assert all(bool(torch.isfinite(t.float()).all()) for t in out.values())
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_empty_sizes(dtype):
+    def z(*shape):
+        return torch.zeros(*shape, dtype=dtype, device="cuda")
+    off, none = offsets_of([2, 1]).cuda(), offsets_of([0, 0]).cuda()
+    ones = torch.ones(2, device="cuda")
+    # Sums of nothing are zeros, results of no rows or columns are empty.
+    y = torch.ones(3, 8, dtype=dtype, device="cuda")
+    assert not checked(tmm.gemm_grouped, z(3, 0), z(2, 0, 8), off, y=y).any()
+    assert checked(tmm.gemm_grouped, z(0, 16), z(2, 16, 8), none).shape == (0, 8)
+    assert checked(tmm.gemm_grouped, z(3, 16), z(2, 16, 0), off).shape == (3, 0)
+    dw = torch.ones(2, 16, 8, dtype=dtype, device="cuda")
+    assert not checked(tmm.gemm_grouped_wgrad, z(0, 16), z(0, 8), none, dw=dw).any()
+    assert checked(tmm.gemm_grouped_wgrad, z(3, 16), z(3, 0), off).shape == (2, 16, 0)
+    rows = torch.tensor([0, 5, -1], dtype=torch.int32, device="cuda")
+    y = torch.ones(3, 8, dtype=dtype, device="cuda")
+    assert not checked(tmm.gemm_grouped, z(0, 16), z(2, 16, 8) + 1, off, rows=rows, y=y).any()
+    assert checked(tmm.gemm_lora, z(0, 16), z(16, 8), z(2, 16, 4), z(2, 4, 8), ones,
+                   none).shape == (0, 8)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("T", [20, 500])
+def test_lora_shared_adapter_and_unaligned_operands(dtype, T):
+    gen = torch.Generator().manual_seed(T)
+    K, N, r, sizes = 72, 136, 8, [T // 3, 0, T // 3]
+    x, w = ints(gen, T, K, top=1), ints(gen, K, N, top=1)
+    a, b = ints(gen, 1, K, r, top=1), ints(gen, 1, r, N, top=1)
+    scale, off = torch.tensor([1.0, 2.0, -1.0]), offsets_of(sizes, first=1)
+    a3, b3 = a.expand(3, K, r), b.expand(3, r, N)
+    want = ref.lora(x, w, a3, b3, scale, off).to(dtype)
+    y = checked(tmm.gemm_lora, cuda(x, dtype), cuda(w, dtype), cuda(a, dtype).expand(3, K, r),
+                cuda(b, dtype).expand(3, r, N), scale.cuda(), cuda(off))
+    assert torch.equal(y.cpu(), want)
+    put = [window(t, dtype, 3, 1)[0] for t in (x, w, a3.contiguous(), b3.contiguous())]
+    out, buf = window(torch.zeros(T, N), dtype, 5, 1)
+    checked(tmm.gemm_lora, *put, scale.cuda(), cuda(off), y=out)
+    assert torch.equal(out.cpu(), want)
+    assert int(torch.isnan(buf).sum()) == buf.numel() - T * N
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("sizes", [[10, 0, 20], [200, 0, 260]])
+def test_lora_rows_do_not_meet_other_adapters(dtype, bad, sizes):
+    # One adapter's matrices, and the rows of it, hold NaN or infinities.
+    gen = torch.Generator().manual_seed(9)
+    T, K, N, r = sum(sizes) + 7, 64, 264, 8
+    x, w = ints(gen, T, K, top=1), ints(gen, K, N, top=1)
+    a, b = ints(gen, 3, K, r, top=1), ints(gen, 3, r, N, top=1)
+    off, scale = offsets_of(sizes), torch.ones(3)
+    want = ref.lora(x, w, a, b, scale, off).to(dtype)
+    x[:sizes[0]] = bad
+    a[0], b[0] = bad, bad
+    a[1], b[1] = bad, bad                 # an adapter without rows
+    y = checked(tmm.gemm_lora, cuda(x, dtype), cuda(w, dtype), cuda(a, dtype), cuda(b, dtype),
+                scale.cuda(), cuda(off)).cpu()
+    assert torch.equal(y[sizes[0]:], want[sizes[0]:])
+    assert not torch.isfinite(y[:sizes[0]]).any()

@@ -13,13 +13,12 @@
 // whole tile, and the weights -- the larger operand when rows are few -- fill the lanes.
 //   forward:  P = w[g] (stored K x N or N x K: both majors are read in place),  Q = rows of x
 //   gradient: P = dy^T,  Q = x^T, the sum running over the group's rows
-//   adapters: the forward product with one group, its sum extended by `rank` values for every
-//             adapter that has rows in the tile: P = b[g], Q = u with the other adapters' rows
-//             read as zeros
-// Rows are fetched through the row index by the copy engine itself (four rows a copy); a row
-// number outside the matrix makes it deliver zeros, which also masks the rows past a group's
-// end in the gradient and the other adapters' rows: no operand value of another group, not even
-// a NaN, meets this group's sums.
+//   adapters: the forward product with one P = w for all; an adapter's columns start at a
+//             multiple of 32 of the tile's, and its part, P = b[g] and Q = u, is added to those
+//             columns alone
+// No operand value of another group, not even a NaN, meets a group's sums: columns are summed
+// apart, those past a group's end are not stored, and the gradient, whose sum runs over the rows,
+// has them zeroed in shared memory.  A row number outside the matrix reads as zeros.
 //
 // Single precision: every operand x is split into three bf16 parts, x = x0 + x1 + x2 exactly
 // (split3), by a pre-pass (planes).  Of the nine part products the three smallest (2^-24 of the
@@ -64,6 +63,7 @@ namespace {
 constexpr int kForward = 0, kWgrad = 1, kLora = 2;
 constexpr int kBK = 64;                  // 16-bit values per K slice: one 128-byte swizzle row
 constexpr int kEpiWarps = 8;
+constexpr int kListed = kMaxGroups + 3;            // entries of a list of groups, see Table
 constexpr int kFewRows = 256;                      // rows of an adapters' call on single blocks
 constexpr int kChunk = 2;                // slices per tensor-memory sum of split operands
 constexpr uint32_t kPTile = 128 * 128;   // 128 lanes x 64 values: 16 KiB
@@ -98,7 +98,7 @@ struct Shape {
   // Values of `rank` per slice of the adapters' part: 16-bit u is a pair of values (hi and lo).
   static constexpr int kRankSlice = PLANES == 3 ? 64 : 32;
   static constexpr uint32_t kTable =
-      (kMaxGroups + 1) * 4 * 3 + kCopyWarps * 128 + 116 + (CG == 1 ? kFewRows * 4 : 0);
+      kListed * 4 * 3 + kCopyWarps * 128 + 116 + (CG == 1 ? kFewRows * 4 : 0);
   static constexpr uint32_t kBars = 8 * (3 * kStages + 5) + 32;
   static constexpr uint32_t kSmem = 1024 + kStages * kStage + kRed + kOutStage + kTable + kBars;
   static_assert(kSmem <= kMaxSmem, "one block's shared memory");
@@ -136,10 +136,6 @@ struct Params {
   const float *u;
   const void *b;
   int64_t ldu, ldb, stride_b;
-  // Adapters on pairs: u holds the rows of the list's entry e from place + e * slot_n on, so that
-  // every tile of the product finds the rows of each of its adapters at the tile's own places,
-  // with zeros for the others (slot_n: the product's tile_n; 0: plain rows).
-  int slot_n, u_rows;
   int trans_b, vec_b;
   int zero_rows;         // forward: write zeros to the rows of no group
   int ksplit;            // blocks of a cluster that share a tile's sum (CG = 1)
@@ -382,24 +378,36 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr, bool mn) {
 // ---- tiles ------------------------------------------------------------------------------
 
 // What a tile covers.  Forward, adapters: columns are rows p in [q0, q0 + qn); gradient: they
-// are columns of x, and the sum runs over the rows [k0, k0 + klen).
+// are columns of x, and the sum runs over the rows [k0, k0 + klen).  Adapters on pairs: columns
+// count places in which every entry of the list starts at a multiple of 32.
 struct Tile {
-  int g;          // group (adapters: 0)
+  int g;          // group (adapters on pairs: the entry of the first column)
   int n0;         // first n
   int q0, qn;     // columns of the tile
   int bn;         // qn rounded up for the tensor core
   int k0, klen;
-  int e0, en;     // adapters: list entries with rows in the tile, [e0, e0 + en); forward: the
-                  // group's entry e0
+  int e0, en;     // adapters on pairs: entries [e0, e0 + en) are those of adapters
 };
 
 // The tables in shared memory: the groups that have rows: number, first row (one more entry: the
-// end of the last), first tile.  In the gradient: every group's first row, by its number, and the
-// numbers in the order of the tiles.
+// end of the last), first tile.  Adapters on pairs: the rows of no adapter, before and after the
+// others, are entries too, of number -1, and `tile` counts 32 columns (one more entry: the end).
+// In the gradient: every group's first row, by its number, and the numbers in the order of the
+// tiles.
 struct Table {
   const int *gid, *row, *tile;
   int count, tiles;
 };
+
+// An entry's part of a tile: columns from c0 on, 32 n32 of them, and the row of the first.
+struct Part {
+  int c0, n32, row;
+};
+__device__ __forceinline__ Part part_of(const Params &p, const Table &tab, const Tile &t, int e) {
+  const int u0 = t.q0 >> 5, u1 = u0 + (p.tile_n >> 5);
+  const int a = max(tab.tile[e], u0), b = min(tab.tile[e + 1], u1);
+  return {(a - u0) * 32, b - a, tab.row[e] + (a - tab.tile[e]) * 32};
+}
 
 template <int CG, int MODE, int PLANES>
 __device__ __forceinline__ Tile tile_at(const Params &p, const Table &tab, int t) {
@@ -425,7 +433,7 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const Table &tab, int t
   if (MODE == kLora) {
     r.g = 0;
     lo = 0;
-    hi = p.rows;
+    hi = CG == 2 ? tab.tile[tab.count] * 32 : p.rows;
     i = t;
   } else {
     int a = 0, b = tab.count;      // the last entry whose first tile is <= t
@@ -435,7 +443,6 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const Table &tab, int t
       else b = m;
     }
     r.g = tab.gid[a];
-    r.e0 = a;
     lo = tab.row[a];
     hi = tab.row[a + 1];
     i = t - tab.tile[a];
@@ -448,22 +455,22 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const Table &tab, int t
   r.bn = (r.qn + S::kUnit - 1) / S::kUnit * S::kUnit;
   r.klen = p.K;
   if (MODE == kLora && CG == 2) {
-    // Entries whose rows overlap [q0, q0 + qn): first with an end past q0, up to a start past it.
-    int a = 0, b = tab.count;
-    while (a < b) {
-      const int m = (a + b) >> 1;
-      if (tab.row[m + 1] > r.q0) b = m;
-      else a = m + 1;
-    }
-    r.e0 = a;
-    b = tab.count;
-    int c = a;
-    while (c < b) {
-      const int m = (c + b) >> 1;
-      if (tab.row[m] >= r.q0 + r.qn) b = m;
-      else c = m + 1;
-    }
-    r.en = c - a;
+    // Halves of the tile are whole 32 columns.  The entries in it: the last that starts at or
+    // before its first column, to the last that starts before its end.
+    r.bn = (r.qn + 63) / 64 * 64;
+    const auto last = [&](int unit) {
+      int a = 0, b = tab.count;
+      while (b - a > 1) {
+        const int m = (a + b) >> 1;
+        if (tab.tile[m] <= unit) a = m;
+        else b = m;
+      }
+      return a;
+    };
+    r.g = last(r.q0 >> 5);
+    const int end = last((r.q0 + r.qn - 1) >> 5);
+    r.e0 = r.g + (tab.gid[r.g] < 0);
+    r.en = max(0, end + (tab.gid[end] >= 0) - r.e0);
   }
   return r;
 }
@@ -588,7 +595,6 @@ template <int MODE>
 __device__ __forceinline__ int64_t out_row(const Params &p, const Tile &t, int col) {
   if (MODE == kWgrad) return int64_t(t.g) * p.stride_out + int64_t(t.q0 + col) * p.ld_out;
   int r = t.q0 + col;
-  if (MODE == kForward) r += t.e0 * p.slot_n;
   if (MODE == kLora && p.out_index) {
     r = p.out_index[r];
     if (r < 0 || r >= p.out_rows) return -1;
@@ -921,11 +927,11 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int *const tab_gid = reinterpret_cast<int *>(smem + (table - base));
-  int *const tab_row = tab_gid + (kMaxGroups + 1);
-  int *const tab_tile = tab_row + (kMaxGroups + 1);
+  int *const tab_row = tab_gid + kListed;
+  int *const tab_tile = tab_row + kListed;
   // Row numbers that a copy warp is about to fetch, four to a copy; 16-byte aligned.
   int *const my_rows = reinterpret_cast<int *>(
-      (reinterpret_cast<uintptr_t>(tab_tile + (kMaxGroups + 1)) + 15) & ~uintptr_t(15)) + 32 * warp;
+      (reinterpret_cast<uintptr_t>(tab_tile + kListed) + 15) & ~uintptr_t(15)) + 32 * warp;
   int *const owner = tab_gid + (S::kTable / 4 - kFewRows);      // adapters on single blocks
   volatile uint32_t *const slot_ptr = reinterpret_cast<volatile uint32_t *>(smem + (slot - base));
   float *const red_ptr = reinterpret_cast<float *>(smem + (red - base));
@@ -986,6 +992,14 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     // the gradient, whose result has a matrix for each).
     int carry = offs[0], count = 0, tiles = 0;
     if (lane == 0) slot_ptr[3] = uint32_t(carry);       // first row of any group
+    if (EXT && carry > 0) {
+      if (lane == 0) {
+        tab_gid[0] = -1;
+        tab_row[0] = tab_tile[0] = 0;
+      }
+      count = 1;
+      tiles = (carry + 31) / 32;
+    }
     if (MODE == kWgrad && lane == 0) tab_row[0] = carry;
     for (int g0 = 0; g0 < p.groups; g0 += 32) {
       const int g = g0 + lane;
@@ -1005,7 +1019,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         const int n = g < p.groups ? hi - lo : 0;
         const unsigned have = __ballot_sync(~0u, n > 0);
         const int at = count + __popc(have & ((1u << lane) - 1));
-        const int mine = (n + p.tile_n - 1) / p.tile_n * p.panels;
+        const int mine = EXT ? (n + 31) / 32 : (n + p.tile_n - 1) / p.tile_n * p.panels;
         int sum = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -1022,9 +1036,21 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       }
     }
     if (lane == 0) {
-      if (MODE != kWgrad) tab_row[count] = carry;
+      if (EXT && carry < p.rows) {
+        tab_gid[count] = -1;
+        tab_row[count] = carry;
+        tab_tile[count++] = tiles;
+        tiles += (p.rows - carry + 31) / 32;
+      }
+      if (EXT) {
+        tab_row[count] = p.rows;
+        tab_tile[count] = tiles;
+        tiles = p.panels * ((32 * tiles + p.tile_n - 1) / p.tile_n);
+      } else if (MODE != kWgrad) {
+        tab_row[count] = carry;
+      }
       if (MODE == kWgrad) tiles = p.groups * p.panels * ((p.q_cols + p.tile_n - 1) / p.tile_n);
-      if (MODE == kLora) tiles = p.panels * ((p.rows + p.tile_n - 1) / p.tile_n);
+      if (FEW) tiles = p.panels * ((p.rows + p.tile_n - 1) / p.tile_n);
       slot_ptr[1] = uint32_t(count);
       slot_ptr[2] = uint32_t(tiles);
       slot_ptr[4] = uint32_t(carry);                    // end of the last group
@@ -1093,26 +1119,6 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     }
   }
 
-  if (MODE == kForward && p.slot_n && warp >= S::kEpi0 && warp < S::kMmaWarp) {
-    // u: zeros at the other places of the tiles in which an entry has rows, a warp a row.
-    const int bn = p.slot_n;
-    for (int i = int(blockIdx.x) * kEpiWarps + warp - S::kEpi0; i < tab.count * 2 * bn;
-         i += int(gridDim.x) * kEpiWarps) {
-      const int e = i / (2 * bn), k = i - e * 2 * bn;
-      const int lo = tab.row[e], hi = tab.row[e + 1];
-      // Places of the first tile before lo, then those of the last one from hi on.
-      const int at = k < bn ? lo / bn * bn + k : hi + (k - bn);
-      const bool zero = k < bn ? at < lo : at < min((hi + bn - 1) / bn * bn, p.rows);
-      if (!zero) continue;
-      for (int pl = 0; pl < PLANES; ++pl) {
-        uint16_t *const row = static_cast<uint16_t *>(p.out) + pl * p.stride_out +
-                              (int64_t(at) + int64_t(e) * bn) * p.ld_out;
-        for (int n = lane * 8; n < p.ld_out; n += 256)
-          *reinterpret_cast<uint4 *>(row + n) = make_uint4(0, 0, 0, 0);
-      }
-    }
-  }
-
   for (int t = cluster; t < tab.tiles; t += clusters) {
     if (timed_out && p.ksplit == 1 && !FEW) break;     // (else warps meet at every tile)
     const Tile tile = tile_at<CG, MODE, PLANES>(p, tab, t);
@@ -1143,6 +1149,20 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       const auto whole = [&](int half) { return CG == 2 && held(half) * CG == p.tile_n; };
       const int boxes = boxes_of(half_rank);
       const int qblocks = hr / 64;
+      // The first row of every copy of Q, and whether they follow one another in a full tile.
+      constexpr int kBoxes = S::kBN / CG / S::kBox;
+      int box_row[kBoxes];
+      bool in_one = whole(half_rank);
+      int e = tile.g;
+#pragma unroll
+      for (int b = 0; b < kBoxes; ++b) {
+        box_row[b] = qf + b * S::kBox;
+        if (EXT && b < boxes) {
+          while (tab.tile[e + 1] * 32 <= qf + b * 32) ++e;
+          box_row[b] = tab.row[e] + qf + b * 32 - tab.tile[e] * 32;
+          in_one &= box_row[b] == box_row[0] + b * 32;
+        }
+      }
       const bool by_row = CG == 1 && MODE != kLora && p.row_index != nullptr;
       uint32_t usual = 0;      // bytes of an ordinary slice, of both blocks of a pair
       if (MODE == kWgrad) {
@@ -1161,7 +1181,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       struct Slice {
         bool ext;
         int k0, g, gcount, rank0, row;      // ext: ranks from rank0, rows of u from row
-        int cnt;                            // gradient: rows of the group
+        int cnt;                            // gradient: rows of the group; ext: copies of u
       };
       const auto slice_at = [&](int s) {
         Slice c = {EXT && s >= nbase, s * kBK, pg, pcount, 0, 0, kBK};
@@ -1175,16 +1195,19 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           c.rank0 = j * S::kRankSlice;       // of b
           c.g = p.e_shared ? 0 : tab.gid[tile.e0 + e];
           c.gcount = p.e_shared ? 1 : p.groups;
-          c.row = qf + (tile.e0 + e) * p.tile_n;
+          // This block's half of the entry's columns, 16 n32 rows.
+          const Part part = part_of(p, tab, tile, tile.e0 + e);
+          c.row = part.row + half_rank * 16 * part.n32;
+          c.cnt = (part.n32 + 1) / 2;
         }
         return c;
       };
-      const auto bytes_of = [&](const Slice &c, int half) {
+      const auto bytes_of = [&](const Slice &c) {
         if (MODE == kWgrad)
           return uint32_t(PLANES) * (kPTile + uint32_t(by_row ? (c.cnt + 15) / 16 * 2048 * qblocks
                                                              : qblocks * 8192));
         return PLANES * ((p.e_mn ? 2 * S::kRankSlice * 128 : kPTile) +
-                         uint32_t(boxes_of(half) * (S::kBox * 128)));
+                         uint32_t(c.cnt * (S::kBox * 128)));
       };
       const auto patch_of = [&](const Slice &c) { return MODE == kWgrad && c.cnt < kBK; };
       // A slice that slice_at describes as ordinary in every respect.
@@ -1235,33 +1258,33 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                          bar);
         } else if (EXT && c.ext) {
           for (int pl = 0; pl < PLANES; ++pl)
-            for (int b = 0; b < boxes; ++b)
+            for (int b = 0; b < c.cnt; ++b)
               tma_2d<CG>(sq + pl * S::kQTile + b * (S::kBox * 128), &map_u, c.k0,
-                         c.row + b * S::kBox + pl * p.u_rows, bar);
-        } else if (whole(half_rank)) {
+                         c.row + b * S::kBox + pl * p.rows, bar);
+        } else if (in_one) {
           // A full tile: one copy a plane.
 #pragma unroll
           for (int pl = 0; pl < PLANES; ++pl)
-            tma_2d<CG>(sq + pl * S::kQTile, &map_qr, c.k0, qf + pl * p.q_rows, bar);
+            tma_2d<CG>(sq + pl * S::kQTile, &map_qr, c.k0, box_row[0] + pl * p.q_rows, bar);
         } else {
+#pragma unroll
           for (int pl = 0; pl < PLANES; ++pl)
-            for (int b = 0; b < boxes; ++b)
-              tma_2d<CG>(sq + pl * S::kQTile + b * (S::kBox * 128), &map_q, c.k0,
-                         qf + b * S::kBox + pl * p.q_rows, bar);
+#pragma unroll
+            for (int b = 0; b < kBoxes; ++b)
+              if (b < boxes)
+                tma_2d<CG>(sq + pl * S::kQTile + b * (S::kBox * 128), &map_q, c.k0,
+                           box_row[b] + pl * p.q_rows, bar);
         }
       };
       // The expectations of one slice (one thread, before or while its copies arrive).
       const auto announce = [&](const Slice &c, int stage) {
         if (patch_of(c)) {
-          mbar_expect(bar_patch + 8 * stage, bytes_of(c, half_rank));
+          mbar_expect(bar_patch + 8 * stage, bytes_of(c));
           if (leader && dropped) mbar_expect_only(bar_full + 8 * stage, 16);
           dropped = false;
           return;
         }
-        uint32_t bytes = 0;
-#pragma unroll
-        for (int h = 0; h < CG; ++h) bytes += bytes_of(c, h);
-        if (leader) expect(stage, bytes);
+        if (leader) expect(stage, CG * bytes_of(c));      // of both blocks of a pair
         else if (PATCH) mbar_arrive_relaxed(full_at(stage));
       };
       // Zeroes a slice's rows that do not count, once its copies are here (a whole warp).
@@ -1413,8 +1436,11 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     } else if (warp == S::kMmaWarp) {
       // ---- products ---- (one thread)
       if (leader && elect_one()) {
-        const uint32_t sizes = (uint32_t(tile.bn >> 3) << 17) | (uint32_t(128 * CG >> 4) << 24) |
-                               (MODE == kWgrad ? 1u << 16 : 0u) | p.idesc;
+        const auto size_of = [&](int columns) {
+          return (uint32_t(columns >> 3) << 17) | (uint32_t(128 * CG >> 4) << 24) |
+                 (MODE == kWgrad ? 1u << 16 : 0u) | p.idesc;
+        };
+        const uint32_t all = size_of(tile.bn);
         const bool base_mn = MODE == kWgrad || p.p_mn;
         const uint32_t qstep = MODE == kWgrad ? 128 : 2;      // 16 values of K, in 16 bytes
         const int n = s1 - s0;
@@ -1437,12 +1463,25 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           tc_fence_after();
           const bool ext = EXT && s >= nbase;
           const bool pmn = ext ? p.e_mn : base_mn;
+          uint32_t d = tmem + buf * S::kBN;
+          uint32_t sizes = all;
+          bool fresh = first;
+          Part part = {};
+          if (EXT && ext) {
+            // An adapter's part: on its columns alone.  PLANES = 3: it is the first of them in
+            // this tensor-memory sum if that holds adapters' slices only, and none of it yet.
+            const int e = tile.e0 + (s - nbase) / per_rank;
+            part = part_of(p, tab, tile, e);
+            d += part.c0;
+            sizes = size_of(32 * part.n32);
+            const int from = s - i % kChunk;
+            fresh = from >= nbase && (s == from || (s - nbase) % per_rank == 0);
+          }
           const uint32_t idesc = sizes | (pmn ? 1u << 15 : 0u);
           const uint32_t st = base + ring.stage * S::kStage;
           const uint64_t dp = tile_desc(st, pmn);
           const uint64_t dq = tile_desc(st + PLANES * kPTile, MODE == kWgrad);
           const uint32_t pstep = pmn ? 128 : 2;
-          const uint32_t d = tmem + buf * S::kBN;
           const int left = ext ? min(S::kRankSlice, p.rank - (s - nbase) % per_rank * S::kRankSlice)
                                : min(kBK, tile.klen - s * kBK);
           const int steps = (left + 15) / 16;
@@ -1450,7 +1489,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
             // b[g] times u's hi, and times its lo, 32 columns on.
             for (int k = 0; k < steps; ++k) {
               const uint64_t a = dp + k * pstep, b = dq + k * qstep;
-              mma<CG>(d, a, b, idesc, !(first && k == 0));
+              mma<CG>(d, a, b, idesc, true);
               mma<CG>(d, a, b + 2 * qstep, idesc, true);
             }
           } else {
@@ -1458,10 +1497,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
             for (int k = 0; k < 4; ++k) {
               if (k >= steps) break;
               const uint64_t a = dp + k * pstep, b = dq + k * qstep;
-              mma<CG>(d, a, b, idesc, !(first && k == 0));
+              mma<CG>(d, a, b, idesc, !(fresh && k == 0));
               if constexpr (PLANES == 3) {
                 constexpr uint64_t pa = kPTile >> 4, qa = S::kQTile >> 4;
-                const uint32_t ds = tmem + (2 + (done & 1)) * S::kBN;
+                const uint32_t ds = tmem + (2 + (done & 1)) * S::kBN + part.c0;
                 mma<CG>(ds, a + 2 * pa, b, idesc, !(i == 0 && k == 0));
                 mma<CG>(ds, a, b + 2 * qa, idesc, true);
                 mma<CG>(ds, a + pa, b + qa, idesc, true);
@@ -1503,8 +1542,18 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           add_adapters<__half>(p, owner, tile, own0, own1, red_ptr, tid);
         results_sync();
       }
+      int entry = tile.g;      // EXT: the entry of the last columns stored
       auto put = [&](int c0, const float (&v)[16]) {
-        if (CG == 1 && (FEW || p.ksplit > 1)) {
+        if (EXT) {
+          // The rows of these columns, which are one entry's.
+          const int at = tile.q0 + c0;
+          if (c0 >= tile.qn) return;
+          while (tab.tile[entry + 1] * 32 <= at) ++entry;
+          Tile t = tile;
+          t.q0 = tab.row[entry] + at - tab.tile[entry] * 32 - c0;
+          t.qn = tab.row[entry + 1] - t.q0;
+          if (t.qn > c0) store_columns<MODE, PLANES>(p, t, c0, nw, v, scale, stage, owner);
+        } else if (CG == 1 && (FEW || p.ksplit > 1)) {
           float w[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -1556,15 +1605,25 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
             break;
           }
           tc_fence_after();
+          int from = 0, to = tile.bn;      // the columns of this part of the sum
+          if (EXT && c * kChunk >= nbase) {
+            const int e = tile.e0 + (c * kChunk - nbase) / per_rank;
+            const int e1 = tile.e0 + (min(c * kChunk + kChunk, n) - 1 - nbase) / per_rank;
+            from = part_of(p, tab, tile, e).c0;
+            const Part end = part_of(p, tab, tile, e1);
+            to = end.c0 + 32 * end.n32;
+          }
 #pragma unroll
           for (int b = 0; b < kBlocks; ++b) {
             const int c0 = 32 * b + 16 * half;
             if (c0 >= tile.bn) break;
             float v[16];
             __syncwarp();
-            tmem_load_16(lanes + buf * S::kBN + c0, v);
+            if (!EXT || (c0 >= from && c0 < to)) {
+              tmem_load_16(lanes + buf * S::kBN + c0, v);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[b][j] += v[j];
+              for (int j = 0; j < 16; ++j) acc[b][j] += v[j];
+            }
             if (c == chunks - 1) {
               tmem_load_16(lanes + (2 + (done & 1)) * S::kBN + c0, v);
 #pragma unroll
@@ -2294,15 +2353,9 @@ static cudaError_t launch_row_ranks(const LoraProblem &p, float *u, int64_t ldu,
 static int64_t u_columns(const LoraProblem &p) {
   return p.dtype == TMM_F32 || lora_shape(p.rows, p.rank) == 1 ? round8(p.rank) : (p.rank + 31) / 32 * 64;
 }
-// Rows of u: on pairs, room for every adapter's part of every tile.
-static int64_t u_rows(const LoraProblem &p) {
-  if (lora_shape(p.rows, p.rank) == 1) return p.rows;
-  const int64_t bn = columns_of(2, p.dtype == TMM_F32 ? 3 : 1);
-  return ((p.rows + bn - 1) / bn + p.groups) * bn;
-}
 static size_t u_bytes(const LoraProblem &p) {
   const int size = lora_shape(p.rows, p.rank) == 1 ? 4 : p.dtype == TMM_F32 ? 6 : 2;
-  return round256(size_t(u_rows(p)) * size_t(u_columns(p)) * size);   // below 2^30 * 2^11 * 6
+  return round256(size_t(p.rows) * size_t(u_columns(p)) * size);   // below 2^31 * 2^11 * 6
 }
 
 // How the product with a is computed on pairs: a forward product of its own.
@@ -2369,11 +2422,9 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
     up.N = int(p.rank);
     up.out = u;
     up.ld_out = ldu;
-    up.stride_out = u_rows(p) * ldu;
-    up.slot_n = bn;
+    up.stride_out = p.rows * ldu;
     up.out_type = kOutU;
     up.n_out = p.dtype == TMM_F32 ? int(p.rank) : int(ldu / 2);
-    if (u_rows(p) * planes > INT32_MAX) return cudaErrorInvalidConfiguration;
     up.scale = p.scale;
     const int32_t *index = gathered && !low_direct ? nullptr : p.row_index;
     if ((e = run_forward(p.dtype, x, p.x, index, a, p.a, p.trans_a != 0, up, dev, stream)) !=
@@ -2381,10 +2432,9 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
       return e;
     prm.out_index = p.row_index;
     prm.out_rows = int(p.rows);
-    prm.u_rows = int(u_rows(p));
     prm.e_mn = p.trans_b ? 0 : 1;
     prm.e_shared = p.groups > 1 && p.b.count == 1;
-    const Planes um = {u, planes, u_rows(p), planes == 3 ? p.rank : ldu, ldu, u_rows(p) * ldu};
+    const Planes um = {u, planes, p.rows, planes == 3 ? p.rank : ldu, ldu, p.rows * ldu};
     if ((e = tile_map(&m.e, b, p.trans_b ? 128 : planes == 3 ? 64 : 32)) != cudaSuccess ||
         (e = row_map(&m.u, um, uint32_t(box_of(cg)))) != cudaSuccess)
       return e;
@@ -2393,8 +2443,11 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   prm.q_rows = int(p.rows);
   prm.tile_n = bn;
   prm.panels = int((p.N + 128 * cg - 1) / (128 * cg));
-  const int64_t tiles = prm.panels * ((p.rows + bn - 1) / bn);
-  if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
+  // Pairs: columns at most, every adapter's rounded up to 32.
+  const int64_t columns = cg == 1 ? p.rows : p.rows + 31 * (std::min(p.groups, p.rows) + 2);
+  const int64_t tiles = prm.panels * ((columns + bn - 1) / bn);
+  if (tiles > INT32_MAX / 2 || columns > INT32_MAX - bn || (cg == 2 && p.rows * planes > INT32_MAX))
+    return cudaErrorInvalidConfiguration;
   prm.ksplit = cg == 2 ? 1 : split_of(tiles, (p.K + kBK - 1) / kBK, planes, dev);
   prm.p_mn = p.trans_w ? 0 : 1;
   prm.p_shared = 1;
