@@ -579,7 +579,7 @@ def test_empty_sizes(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
-@pytest.mark.parametrize("T", [20, 500])
+@pytest.mark.parametrize("T", [20, 500, 700])
 def test_lora_shared_adapter_and_unaligned_operands(dtype, T):
     gen = torch.Generator().manual_seed(T)
     K, N, r, sizes = 72, 136, 8, [T // 3, 0, T // 3]
@@ -600,7 +600,7 @@ def test_lora_shared_adapter_and_unaligned_operands(dtype, T):
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-@pytest.mark.parametrize("sizes", [[10, 0, 20], [200, 0, 260]])
+@pytest.mark.parametrize("sizes", [[10, 0, 20], [200, 0, 260], [300, 0, 260]])
 def test_lora_rows_do_not_meet_other_adapters(dtype, bad, sizes):
     # One adapter's matrices, and the rows of it, hold NaN or infinities.
     gen = torch.Generator().manual_seed(9)
@@ -616,3 +616,26 @@ def test_lora_rows_do_not_meet_other_adapters(dtype, bad, sizes):
                 scale.cuda(), cuda(off)).cpu()
     assert torch.equal(y[sizes[0]:], want[sizes[0]:])
     assert not torch.isfinite(y[:sizes[0]]).any()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("r", [8, 40, 130])
+@pytest.mark.parametrize("K", [24, 200])
+@pytest.mark.parametrize("sizes,first,T", [([9] * 60, 0, 600), ([1] * 200, 7, 530),
+                                           ([1, 31, 32, 33, 64, 0, 95, 300], 5, 620),
+                                           ([0, 0, 700], 0, 700), ([255, 257, 128], 33, 673)])
+def test_lora_parts_of_tiles(dtype, sizes, first, T, K, r):
+    # Adapters of any size beside one another in a tile, between rows of none.
+    gen = torch.Generator().manual_seed(T + K + r)
+    L, N = len(sizes), 300
+    x, w = ints(gen, T, K, top=1), ints(gen, K, N, top=1)
+    a, b = ints(gen, L, K, r, top=1), ints(gen, L, r, N, top=1)
+    a *= torch.rand(L, K, 1, generator=gen) < 0.2
+    scale = torch.tensor([2.0 ** (i % 3 - 1) for i in range(L)])
+    off = offsets_of(sizes, first=first)
+    order = torch.randperm(T, generator=gen).to(torch.int32)
+    y = checked(tmm.gemm_lora, cuda(x, dtype), cuda(w, dtype), cuda(a, dtype), cuda(b, dtype),
+                scale.cuda(), cuda(off), rows=cuda(order))
+    low = None if dtype == torch.float32 else dtype
+    want = ref.lora(x, w, a, b, scale, off, order, low=low)
+    assert torch.equal(y.cpu(), want.to(dtype))

@@ -64,7 +64,7 @@ constexpr int kForward = 0, kWgrad = 1, kLora = 2;
 constexpr int kBK = 64;                  // 16-bit values per K slice: one 128-byte swizzle row
 constexpr int kEpiWarps = 8;
 constexpr int kListed = kMaxGroups + 3;            // entries of a list of groups, see Table
-constexpr int kFewRows = 256;                      // rows of an adapters' call on single blocks
+constexpr int kFewRows = 512;                      // rows of an adapters' call on single blocks
 constexpr int kChunk = 2;                // slices per tensor-memory sum of split operands
 constexpr uint32_t kPTile = 128 * 128;   // 128 lanes x 64 values: 16 KiB
 constexpr uint32_t kMaxSmem = 232448;    // 227 KiB
@@ -2143,9 +2143,24 @@ int forward_shape(int64_t rows, int64_t groups, int64_t N, int64_t K, int dtype)
   };
   return cost(2, f32 ? 128 : 256, 64) <= cost(1, 64, 16) ? 2 : 1;
 }
-// Adapters: single blocks while the part on the CUDA cores (rows x rank) is small.
-int lora_shape(int64_t rows, int64_t rank) {
-  return rows <= 64 || (rows <= kFewRows && rows * rank <= 8192) ? 1 : 2;
+// Adapters: single blocks while the part on the CUDA cores (rows x rank) is small and their tiles
+// are few, or pairs would need more than one round of tiles, an adapter's rows taking about 24
+// columns more than they are.  (K = 4096, BF16, rank 16, on single blocks and on pairs: 257 rows of
+// 4 adapters 22 us and 34 us at N = 1024, 45 us and 35 us at N = 4096; of 32 adapters 46 us and 59
+// us at N = 4096; 512 rows of 32 adapters 55 us and 61 us.  FP32, K = 2048: 128 rows of 7 adapters
+// 43 us and 55 us, 256 rows of 4 75 us and 56 us, of 32 73 us and 109 us, all at N = 4096; sizes
+// that do not allow vector loads, K = 1000 and N = 2047: 128 rows 29 us and 32 us, 200 rows 48 us
+// and 34 us.)
+int lora_shape(const LoraProblem &p) {
+  if (p.rows <= 64) return 1;
+  if (p.rows > kFewRows || p.rows * p.rank > 8192) return 2;
+  constexpr int64_t kSms = 152;
+  const bool f32 = p.dtype == TMM_F32;
+  const int64_t tiles = (p.rows + 63) / 64 * ((p.N + 127) / 128);
+  if (tiles <= (!f32 ? kSms : p.K % 8 == 0 && p.N % 8 == 0 ? kSms / 2 : kSms / 4)) return 1;
+  if (f32 && p.rows > 256) return 2;
+  const int64_t width = f32 ? 128 : 256, columns = p.rows + 24 * std::min(p.groups, p.rows);
+  return (columns + width - 1) / width * ((p.N + 255) / 256) > kSms / 2 ? 1 : 2;
 }
 int wgrad_shape(int64_t N) { return N > 128 ? 2 : 1; }
 
@@ -2351,10 +2366,10 @@ static cudaError_t launch_row_ranks(const LoraProblem &p, float *u, int64_t ldu,
 // Columns of u: FP32 values on single blocks; for pairs a plane's 16-byte rows, or pairs of 16-bit
 // values in blocks of 32 + 32.
 static int64_t u_columns(const LoraProblem &p) {
-  return p.dtype == TMM_F32 || lora_shape(p.rows, p.rank) == 1 ? round8(p.rank) : (p.rank + 31) / 32 * 64;
+  return p.dtype == TMM_F32 || lora_shape(p) == 1 ? round8(p.rank) : (p.rank + 31) / 32 * 64;
 }
 static size_t u_bytes(const LoraProblem &p) {
-  const int size = lora_shape(p.rows, p.rank) == 1 ? 4 : p.dtype == TMM_F32 ? 6 : 2;
+  const int size = lora_shape(p) == 1 ? 4 : p.dtype == TMM_F32 ? 6 : 2;
   return round256(size_t(p.rows) * size_t(u_columns(p)) * size);   // below 2^31 * 2^11 * 6
 }
 
@@ -2365,7 +2380,7 @@ static int low_shape(const LoraProblem &p) {
 
 // The workspace holds u and the planes of the operands.
 size_t lora_workspace_bytes(const LoraProblem &p) {
-  if (lora_shape(p.rows, p.rank) == 1)
+  if (lora_shape(p) == 1)
     return p.dtype == TMM_F32 ? u_bytes(p)
                               : add_sizes({u_bytes(p), plane_bytes(p.x, p.dtype),
                                            plane_bytes(p.w, p.dtype)});
@@ -2380,7 +2395,7 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
                         cudaStream_t stream) {
   char *ws = static_cast<char *>(workspace);
   const int planes = p.dtype == TMM_F32 ? 3 : 1;
-  const int cg = lora_shape(p.rows, p.rank);
+  const int cg = lora_shape(p);
   const int bn = columns_of(cg, planes);
   const int64_t ldu = u_columns(p);
   void *u = ws;
