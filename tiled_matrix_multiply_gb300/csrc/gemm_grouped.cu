@@ -18,7 +18,7 @@
 //             columns alone
 // No operand value of another group, not even a NaN, meets a group's sums: columns are summed
 // apart, those past a group's end are not stored, and the gradient, whose sum runs over the rows,
-// has them zeroed in shared memory.  A row number outside the matrix reads as zeros.
+// reads zeros in their place.  A row number outside the matrix reads as zeros.
 //
 // Single precision: every operand x is split into three bf16 parts, x = x0 + x1 + x2 exactly
 // (split3), by a pre-pass (planes).  Of the nine part products the three smallest (2^-24 of the
@@ -99,7 +99,7 @@ struct Shape {
   static constexpr int kRankSlice = PLANES == 3 ? 64 : 32;
   static constexpr uint32_t kTable =
       kListed * 4 * 3 + kCopyWarps * 128 + 116 + (CG == 1 ? kFewRows * 4 : 0);
-  static constexpr uint32_t kBars = 8 * (3 * kStages + 5) + 32;
+  static constexpr uint32_t kBars = 8 * (2 * kStages + 5) + 32;
   static constexpr uint32_t kSmem = 1024 + kStages * kStage + kRed + kOutStage + kTable + kBars;
   static_assert(kSmem <= kMaxSmem, "one block's shared memory");
   static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory columns");
@@ -179,22 +179,14 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
-// Bytes to come in the barrier's present phase, without an arrival.
-__device__ __forceinline__ void mbar_expect_only(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
 // On this block's own barrier (`bar`: its shared memory address).
 __device__ __forceinline__ void mbar_arrive_local(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The same where no access to memory of this thread has to be ordered before it.  (A release
-// waits for the thread's stores: result warps handing tensor memory back, whose reads have
-// completed, would wait for their results to reach memory.)
+// Of any block of the cluster, where no access to memory of this thread has to be ordered before
+// it.  (A cluster-wide release takes about 1500 cycles and waits for the thread's stores: result
+// warps handing tensor memory back, whose reads have completed, would wait for their results to
+// reach memory.)
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
@@ -280,22 +272,30 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-// Four rows y[0..3] of 64 values from column x (single blocks only).
+// Four rows y[0..3] of 64 values from column x.
+template <int CG>
 __device__ __forceinline__ void tma_rows4(uint32_t dst, const CUtensorMap *map, int x,
                                           const int (&y)[4], uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
-      "r"(bar)
-      : "memory");
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4"
+        ".mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
+        "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4"
+        ".mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
+        "r"(bar)
+        : "memory");
 }
 // Orders ordinary accesses to shared memory before the copy engine's and the tensor core's.
 __device__ __forceinline__ void proxy_fence() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-__device__ __forceinline__ void zero16(uint32_t addr) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
 }
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
@@ -902,14 +902,14 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                const __grid_constant__ CUtensorMap map_q,    // Q tiles
                const __grid_constant__ CUtensorMap map_qr,   // single rows of x; pairs: tiles of
                                                              // all the columns of a block
-               const __grid_constant__ CUtensorMap map_e,    // b tiles
-               const __grid_constant__ CUtensorMap map_u,    // u tiles
+               const __grid_constant__ CUtensorMap map_e,    // b tiles; gradient: 16 rows of dy
+               const __grid_constant__ CUtensorMap map_u,    // u tiles; gradient: 16 rows of x
+               const __grid_constant__ CUtensorMap map_pr,   // gradient: single rows of dy
                const Params p) {
   using S = Shape<CG, PLANES>;
   // The adapters' part: pairs extend the sum (EXT); single blocks, whose rows are few, add it to
   // the results on the CUDA cores while the weights stream (FEW).
   constexpr bool EXT = MODE == kLora && CG == 2, FEW = MODE == kLora && CG == 1;
-  constexpr bool PATCH = MODE == kWgrad;      // some slices get rows of zeros
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;    // the same offset in every block
@@ -919,8 +919,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   const uint32_t table = out_stage + S::kOutStage;
   const uint32_t bar_full = (table + S::kTable + 7u) & ~7u;
   const uint32_t bar_empty = bar_full + 8 * S::kStages;
-  const uint32_t bar_patch = bar_empty + 8 * S::kStages;   // slices that need rows of zeros
-  const uint32_t bar_tfull = bar_patch + 8 * S::kStages;
+  const uint32_t bar_tfull = bar_empty + 8 * S::kStages;
   const uint32_t bar_tempty = bar_tfull + 16;      // pairs: used in the leader
   const uint32_t bar_drain = bar_tempty + 16;
   const uint32_t slot = bar_drain + 8;             // tensor memory address; then the counts
@@ -948,8 +947,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   int *const offs = reinterpret_cast<int *>(smem);
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(bar_full + 8 * s, S::kDirect ? S::kCopyWarps / 2 : PATCH ? CG : 1);
-      mbar_init(bar_patch + 8 * s, 1);
+      mbar_init(bar_full + 8 * s, S::kDirect ? S::kCopyWarps / 2 : 1);
       mbar_init(bar_empty + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -1099,7 +1097,6 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   Ring ring = {0, 0};
   uint32_t q = 0;      // tensor-memory sums so far
   uint32_t done = 0;   // tiles with a sum so far
-  uint32_t patched = 0;   // a bit per stage: parity of its patched slices
   bool dropped = int(blockIdx.x) == p.drop_block;   // testing hook: the next expectation is wrong
 
   // Forward: rows of the result that belong to no group are zero, a warp a row.
@@ -1175,9 +1172,12 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                                                           : boxes_of(h) * (S::kBox * 128)));
       }
 
-      // What a slice s is.  A group's last slice in the gradient needs rows of zeros: its copies
-      // are counted by the block's own bar_patch, a warp zeroes the rows, and only then does the
-      // block arrive on the leader's bar_full.
+      // What a slice s is.  A group's last slice in the gradient has to end in rows of zeros: it
+      // comes in copies of 16 rows and, for the rows that are not 16, of four by number, where one
+      // outside the matrix reads as zeros.  (The copy of a whole slice, and its last rows zeroed in
+      // shared memory afterwards, held the products up by 1250 cycles a tile, most of it the
+      // cluster-wide release of the zeros: 1000 rows in each of 8 groups, 4096 x 4096,
+      // 182 us in place of 167.)
       struct Slice {
         bool ext;
         int k0, g, gcount, rank0, row;      // ext: ranks from rank0, rows of u from row
@@ -1204,12 +1204,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       };
       const auto bytes_of = [&](const Slice &c) {
         if (MODE == kWgrad)
-          return uint32_t(PLANES) * (kPTile + uint32_t(by_row ? (c.cnt + 15) / 16 * 2048 * qblocks
-                                                             : qblocks * 8192));
+          return uint32_t(PLANES) * ((c.cnt + 15) / 16 * 2048 * (2 + qblocks));
         return PLANES * ((p.e_mn ? 2 * S::kRankSlice * 128 : kPTile) +
                          uint32_t(c.cnt * (S::kBox * 128)));
       };
-      const auto patch_of = [&](const Slice &c) { return MODE == kWgrad && c.cnt < kBK; };
       // A slice that slice_at describes as ordinary in every respect.
       const auto is_plain = [&](int s) {
         if (MODE == kWgrad) return (s + 1) * kBK <= tile.klen;
@@ -1223,9 +1221,37 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         mbar_expect(bar_full + 8 * stage, bytes + (dropped ? 16 : 0));
         dropped = false;
       };
+      // A group's last rows, rounded up to 16 (one thread): `blocks` of 64 columns from column x,
+      // planes `plane` bytes and `rows` rows apart.
+      const auto copy_end = [&](const Slice &c, uint32_t to, const CUtensorMap *map16,
+                                const CUtensorMap *map1, int x, int blocks, uint32_t plane,
+                                int rows, uint32_t bar) {
+        for (int pl = 0; pl < PLANES; ++pl, to += plane) {
+          for (int r = 0; r < c.cnt; r += 16) {
+            const bool all = r + 16 <= c.cnt;
+            for (int b = 0; b < blocks; ++b) {
+              const uint32_t at = to + uint32_t(b * 8192 + r * 128);
+              if (all) {
+                tma_2d<CG>(at, map16, x + b * 64, c.k0 + r + pl * rows, bar);
+              } else {
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                  const int out = PLANES * rows, first = c.k0 + r + 4 * f + pl * rows;
+                  const int in = c.cnt - r - 4 * f;      // of the four rows
+                  const int y[4] = {in > 0 ? first : out, in > 1 ? first + 1 : out,
+                                    in > 2 ? first + 2 : out, in > 3 ? first + 3 : out};
+                  tma_rows4<CG>(at + f * 512, map1, x + b * 64, y, bar);
+                }
+              }
+            }
+          }
+        }
+      };
       // Copies of P, and of Q as tiles, of one slice (one thread).
       const auto copy_p = [&](const Slice &c, uint32_t st, uint32_t bar) {
-        if (MODE == kWgrad) {
+        if (MODE == kWgrad && c.cnt < kBK) {
+          copy_end(c, st, &map_e, &map_pr, n0, 2, 2 * 8192, p.rows, bar);
+        } else if (MODE == kWgrad) {
 #pragma unroll
           for (int i = 0; i < 2 * PLANES; ++i)
             tma_2d<CG>(st + i * 8192, &map_p, n0 + (i & 1) * 64, c.k0 + (i >> 1) * p.rows, bar);
@@ -1251,7 +1277,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         }
       };
       const auto copy_q = [&](const Slice &c, uint32_t sq, uint32_t bar) {
-        if (MODE == kWgrad) {
+        if (MODE == kWgrad && c.cnt < kBK) {
+          copy_end(c, sq, &map_u, &map_qr, qf, qblocks, S::kQTile, p.q_rows, bar);
+        } else if (MODE == kWgrad) {
           for (int pl = 0; pl < PLANES; ++pl)
             for (int b = 0; b < qblocks; ++b)
               tma_2d<CG>(sq + pl * S::kQTile + b * 8192, &map_q, qf + b * 64, c.k0 + pl * p.q_rows,
@@ -1278,39 +1306,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       };
       // The expectations of one slice (one thread, before or while its copies arrive).
       const auto announce = [&](const Slice &c, int stage) {
-        if (patch_of(c)) {
-          mbar_expect(bar_patch + 8 * stage, bytes_of(c));
-          if (leader && dropped) mbar_expect_only(bar_full + 8 * stage, 16);
-          dropped = false;
-          return;
-        }
         if (leader) expect(stage, CG * bytes_of(c));      // of both blocks of a pair
-        else if (PATCH) mbar_arrive_relaxed(full_at(stage));
       };
-      // Zeroes a slice's rows that do not count, once its copies are here (a whole warp).
-      const auto patch_rows = [&](const Slice &c, int stage, uint32_t parity) {
-        const uint32_t st = base + stage * S::kStage, sq = st + PLANES * kPTile;
-        const bool ok = mbar_wait(bar_patch + 8 * stage, parity, p.wait_limit_ns);
-        if (!__all_sync(~0u, ok)) return false;
-        // Rows [cnt, the next multiple of 16): past the group's end.
-        const int n = 8 * (((c.cnt + 15) & ~15) - c.cnt);
-        for (int i = lane; i < n; i += 32) {
-          const uint32_t at = uint32_t(c.cnt * 128 + i * 16);
-          for (int b = 0; b < 2 * PLANES; ++b) zero16(st + b * 8192 + at);
-          for (int pl = 0; pl < PLANES; ++pl)
-            for (int b = 0; b < qblocks; ++b) zero16(sq + pl * S::kQTile + b * 8192 + at);
-        }
-        proxy_fence();
-        __syncwarp();
-        if (elect_one()) mbar_arrive(full_at(stage));
-        __syncwarp();
-        return true;
-      };
-
       if (!by_row) {
-        // Warp 0 copies P, warp 1 copies Q, one thread each; warps 2 and 3 zero rows, of even and
-        // odd stages.  They do not wait for a stage to be free, so all uses of a stage have to be
-        // the same warp's: only then is the parity it waits for never that of a round before.
+        // Warp 0 copies P, warp 1 copies Q, one thread each.
         if (warp < 2) {
           if (elect_one()) {
             for (int s = s0; s < s1; ++s) {
@@ -1326,15 +1325,13 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                 if (warp == 0) {
                   if (leader) expect(ring.stage, usual);
                   copy_p(c, st, full);
-                  if (PATCH && !leader) mbar_arrive_relaxed(full);
                 } else {
                   copy_q(c, st + PLANES * kPTile, full);
                 }
               } else {
                 if (EXT) grid_wait();
                 const Slice c = slice_at(s);
-                const uint32_t bar =
-                    patch_of(c) ? bar_patch + 8 * ring.stage : full_at(ring.stage);
+                const uint32_t bar = full_at(ring.stage);
                 if (warp == 0) {
                   announce(c, ring.stage);
                   copy_p(c, st, bar);
@@ -1347,21 +1344,6 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           }
           __syncwarp();
           timed_out = __any_sync(~0u, timed_out);
-        } else if (PATCH) {
-          Ring at = ring;
-          int s = s0;
-          if (s1 > s0) s = is_plain(s1 - 1) ? s1 : s1 - 1;      // only the last can need it
-          at.template skip<S::kStages>(s - s0);
-          for (; s < s1 && !timed_out; ++s) {
-            const Slice c = slice_at(s);
-            if (patch_of(c)) {
-              const uint32_t parity = (patched >> at.stage) & 1u;
-              patched ^= 1u << at.stage;
-              if (warp == 2 + (at.stage & 1)) timed_out = !patch_rows(c, at.stage, parity);
-            }
-            at.template next<S::kStages>();
-          }
-          ring.template skip<S::kStages>(s1 - s0);
         }
       } else {
         // Rows by number, four to a copy (single blocks), by warps 1 to 3, while warp 0 copies P:
@@ -1394,8 +1376,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
             break;
           }
           const Slice c = slice_at(s);
-          const bool patch = patch_of(c);
-          const uint32_t bar = patch ? bar_patch + 8 * ring.stage : bar_full + 8 * ring.stage;
+          const uint32_t bar = bar_full + 8 * ring.stage;
           if (warp == 0 && elect_one()) {
             if (is_plain(s) && MODE != kWgrad) expect(ring.stage, usual);
             else announce(c, ring.stage);
@@ -1420,16 +1401,12 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                 const int y[4] = {v.x < 0 ? out : v.x + add, v.y < 0 ? out : v.y + add,
                                   v.z < 0 ? out : v.z + add, v.w < 0 ? out : v.w + add};
                 for (int b = 0; b < (MODE == kWgrad ? qblocks : 1); ++b)
-                  tma_rows4(sq + pl * S::kQTile + b * 8192 + f * 512, &map_qr, x + b * 64, y, bar);
+                  tma_rows4<CG>(sq + pl * S::kQTile + b * 8192 + f * 512, &map_qr, x + b * 64, y,
+                                bar);
               }
             }
           }
           __syncwarp();
-          if (patch) {
-            const uint32_t parity = (patched >> ring.stage) & 1u;
-            patched ^= 1u << ring.stage;
-            if (warp == 2 + (ring.stage & 1)) timed_out = !patch_rows(c, ring.stage, parity);
-          }
           ring.template next<S::kStages>();
         }
       }
@@ -2030,7 +2007,7 @@ cudaError_t row_map(CUtensorMap *map, const Planes &o, uint32_t box_rows) {
 }
 
 struct Maps {
-  CUtensorMap p, q, qr, e, u;
+  CUtensorMap p, q, qr, e, u, pr;
 };
 
 template <int CG, int MODE, int PLANES>
@@ -2065,7 +2042,7 @@ cudaError_t launch_shape(const Maps &m, Params &prm, int64_t tiles, const Device
   // Persistent: a cluster for every tile there can be, at most one per resident slot.
   const int64_t slots = std::max(1, dev.sm_count / cluster);
   cfg.gridDim = dim3(unsigned(cluster * std::max<int64_t>(1, std::min(tiles, slots))), 1, 1);
-  return cudaLaunchKernelEx(&cfg, kernel, m.p, m.q, m.qr, m.e, m.u, prm);
+  return cudaLaunchKernelEx(&cfg, kernel, m.p, m.q, m.qr, m.e, m.u, m.pr, prm);
 }
 
 template <int CG, int PLANES>
@@ -2317,12 +2294,13 @@ cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *wor
     set_direct(&prm, p.dy, p.x);
   } else {
     if ((e = row_map(&m.p, dy, kBK)) != cudaSuccess ||
-        (e = index ? row_map(&m.qr, x, 1) : row_map(&m.q, x, kBK)) != cudaSuccess)
+        (e = row_map(&m.e, dy, 16)) != cudaSuccess || (e = row_map(&m.pr, dy, 1)) != cudaSuccess ||
+        (e = row_map(&m.qr, x, 1)) != cudaSuccess)
       return e;
-    if (index) m.q = m.qr;
-    else m.qr = m.q;
-    m.e = m.p;
-    m.u = m.q;
+    m.q = m.u = m.qr;
+    if (!index && ((e = row_map(&m.q, x, kBK)) != cudaSuccess ||
+                   (e = row_map(&m.u, x, 16)) != cudaSuccess))
+      return e;
   }
   return launch_any(cg, planes, kWgrad, m, prm, tiles, dev, stream);
 }
