@@ -364,6 +364,20 @@ __device__ __forceinline__ void tmem_load_16(uint32_t addr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 16 lanes x 16 consecutive FP32 columns, in the order of an 8 x 8 matrix instruction: r[4 c + 2 h]
+// and the one after it are columns 8 c + 2 (l % 4) and + 1 of lane 8 h + l / 4 (l: this thread).
+// The values are there after tmem_wait.
+__device__ __forceinline__ void tmem_load_matrices(uint32_t addr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
 // Shared-memory matrix descriptor, 128-byte swizzle: start address >> 4 (bits 0-13), leading
 // byte offset >> 4 (16-29), stride byte offset >> 4 (32-45), version 1 (46-47), swizzle 2
 // (61-63).  A tile stored with K contiguous has rows of 64 values (128 bytes), eight of them
@@ -602,10 +616,77 @@ __device__ __forceinline__ int64_t out_row(const Params &p, const Tile &t, int c
   return int64_t(r) * p.ld_out;
 }
 
+// 16-bit results with rows on 16-byte boundaries go through 1 KiB of shared memory a warp, 16 result
+// rows of 32 n, from which four lanes take the 64 bytes of a row: 2 stores of 16 bytes a lane in
+// place of 16 of two bytes.  Piece `c` of 8 n of row `row` is at:
+__device__ __forceinline__ uint32_t staged(uint32_t stage, int row, int c) {
+  return stage + uint32_t(row * 64 + ((c ^ (row >> 1 & 3)) << 4));      // free of bank conflicts
+}
+template <int MODE>
+__device__ __forceinline__ void store_staged(const Params &p, const Tile &t, int c0, int nw,
+                                             uint32_t stage, const int *owner) {
+  const int lane = threadIdx.x & 31;
+  const int count = min(16, t.qn - c0);
+  const bool by_row = MODE == kLora && p.out_index;
+  const bool check = MODE == kLora && p.u;      // rows that are not written (see owner)
+  const int64_t first = by_row ? 0 : out_row<MODE>(p, t, c0);
+  const int n8 = nw + (lane & 3) * 8;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = (lane >> 2) + 8 * i;
+    uint4 w;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                 : "r"(staged(stage, row, lane & 3))
+                 : "memory");
+    if (row >= count || n8 >= p.N) continue;
+    const int64_t o = by_row ? out_row<MODE>(p, t, c0 + row) : first + row * p.ld_out;
+    if (o < 0 || (check && owner[t.q0 + c0 + row] == -2)) continue;
+    uint16_t *dst = static_cast<uint16_t *>(p.out) + o + n8;
+    if (n8 + 8 <= p.N) {
+      *reinterpret_cast<uint4 *>(dst) = w;
+    } else {
+      const uint32_t part[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (n8 + j < p.N) dst[j] = uint16_t(part[j / 2] >> (16 * (j & 1)));
+    }
+  }
+}
+// 16 columns of the tile from c0 on, for the 32 n of the warp, as tmem_load_matrices leaves lanes
+// 16 i to 16 i + 15 in f[i]: the matrices are transposed on their way to shared memory, two
+// instructions in place of the 16 of store_columns (gradient of 32 groups of 64 rows, 4096 x 4096:
+// 349 us -> 322 us; with two blocks' values loaded at a time 363 us).
+template <int MODE>
+__device__ __forceinline__ void store_matrices(const Params &p, const Tile &t, int c0, int nw,
+                                               const uint32_t (&f)[2][8], float scale,
+                                               uint32_t stage, const int *owner) {
+  const int lane = threadIdx.x & 31;
+  uint32_t h[2][4];      // [8 columns][8 n]: two neighbouring columns of one n
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const float lo = __uint_as_float(f[m >> 1][4 * c + 2 * (m & 1)]) * scale;
+      const float hi = __uint_as_float(f[m >> 1][4 * c + 2 * (m & 1) + 1]) * scale;
+      if (p.out_type == kOutBF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[c][m]) : "f"(hi), "f"(lo));
+      else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[c][m]) : "f"(hi), "f"(lo));
+    }
+  __syncwarp();      // the reads of the block before are done
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                     staged(stage, 8 * c + (lane & 7), lane >> 3)),
+                 "r"(h[c][0]), "r"(h[c][1]), "r"(h[c][2]), "r"(h[c][3])
+                 : "memory");
+  __syncwarp();
+  store_staged<MODE>(p, t, c0, nw, stage, owner);
+}
+
 // 16 consecutive columns of the tile from c0 on, for the 32 n of the warp from nw on (lane l
-// holds nw + l).  16-bit results with rows on 16-byte boundaries go through 1 KiB of shared memory
-// (`stage`), from which four lanes take the 64 bytes of a result row: 2 stores of 16 bytes a lane
-// in place of 16 of two bytes.
+// holds nw + l).
 template <int MODE, int PLANES>
 __device__ __forceinline__ void store_columns(const Params &p, const Tile &t, int c0, int nw,
                                               const float (&v)[16], float scale, uint32_t stage,
@@ -630,31 +711,11 @@ __device__ __forceinline__ void store_columns(const Params &p, const Tile &t, in
       __syncwarp();      // the reads of the block before are done
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + uint32_t(j * 64 + lane * 2)), "h"(h[j])
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(staged(stage, j, lane >> 3) + (lane & 7) * 2),
+                     "h"(h[j])
                      : "memory");
       __syncwarp();
-      const int n8 = nw + (lane & 3) * 8;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = (lane >> 2) + 8 * i;
-        uint4 w;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                     : "r"(stage + uint32_t(row * 64 + (lane & 3) * 16))
-                     : "memory");
-        if (row >= count || n8 >= p.N) continue;
-        const int64_t o = by_row ? out_row<MODE>(p, t, c0 + row) : first + row * p.ld_out;
-        if (o < 0 || (check && owner[t.q0 + c0 + row] == -2)) continue;
-        uint16_t *dst = static_cast<uint16_t *>(p.out) + o + n8;
-        if (n8 + 8 <= p.N) {
-          *reinterpret_cast<uint4 *>(dst) = w;
-        } else {
-          const uint32_t part[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (n8 + j < p.N) dst[j] = uint16_t(part[j / 2] >> (16 * (j & 1)));
-        }
-      }
+      store_staged<MODE>(p, t, c0, nw, stage, owner);
       return;
     }
   } else if (!by_row && p.out_type == kOutF32) {
@@ -1226,25 +1287,34 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       const auto copy_end = [&](const Slice &c, uint32_t to, const CUtensorMap *map16,
                                 const CUtensorMap *map1, int x, int blocks, uint32_t plane,
                                 int rows, uint32_t bar) {
-        for (int pl = 0; pl < PLANES; ++pl, to += plane) {
-          for (int r = 0; r < c.cnt; r += 16) {
-            const bool all = r + 16 <= c.cnt;
-            for (int b = 0; b < blocks; ++b) {
-              const uint32_t at = to + uint32_t(b * 8192 + r * 128);
-              if (all) {
-                tma_2d<CG>(at, map16, x + b * 64, c.k0 + r + pl * rows, bar);
-              } else {
+        const int whole16 = c.cnt >> 4, left = c.cnt & 15;
 #pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                  const int out = PLANES * rows, first = c.k0 + r + 4 * f + pl * rows;
-                  const int in = c.cnt - r - 4 * f;      // of the four rows
-                  const int y[4] = {in > 0 ? first : out, in > 1 ? first + 1 : out,
-                                    in > 2 ? first + 2 : out, in > 3 ? first + 3 : out};
-                  tma_rows4<CG>(at + f * 512, map1, x + b * 64, y, bar);
-                }
-              }
+        for (int pl = 0; pl < PLANES; ++pl) {
+          const int row = c.k0 + pl * rows;
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            if (i < whole16) {
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                if (b < blocks)
+                  tma_2d<CG>(to + uint32_t(b * 8192 + i * 2048), map16, x + b * 64, row + 16 * i,
+                             bar);
+            }
+          if (left > 0) {
+            const int out = PLANES * rows, first = row + 16 * whole16;
+            const uint32_t at = to + uint32_t(whole16 * 2048);
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              int y[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) y[k] = 4 * f + k < left ? first + 4 * f + k : out;
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                if (b < blocks)
+                  tma_rows4<CG>(at + uint32_t(b * 8192 + f * 512), map1, x + b * 64, y, bar);
             }
           }
+          to += plane;
         }
       };
       // Copies of P, and of Q as tiles, of one slice (one thread).
@@ -1520,15 +1590,20 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         results_sync();
       }
       int entry = tile.g;      // EXT: the entry of the last columns stored
-      auto put = [&](int c0, const float (&v)[16]) {
-        if (EXT) {
-          // The rows of these columns, which are one entry's.
+      // EXT: the tile with the rows of the columns from c0 on, which are one entry's.
+      auto rows_at = [&](int c0) {
+        Tile t = tile;
+        if (EXT && c0 < tile.qn) {
           const int at = tile.q0 + c0;
-          if (c0 >= tile.qn) return;
           while (tab.tile[entry + 1] * 32 <= at) ++entry;
-          Tile t = tile;
           t.q0 = tab.row[entry] + at - tab.tile[entry] * 32 - c0;
           t.qn = tab.row[entry + 1] - t.q0;
+        }
+        return t;
+      };
+      auto put = [&](int c0, const float (&v)[16]) {
+        if (EXT) {
+          const Tile t = rows_at(c0);
           if (t.qn > c0) store_columns<MODE, PLANES>(p, t, c0, nw, v, scale, stage, owner);
         } else if (CG == 1 && (FEW || p.ksplit > 1)) {
           float w[16];
@@ -1555,7 +1630,18 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           ++q;
           if (!__all_sync(~0u, ready)) timed_out = true;
           tc_fence_after();
-          if (!timed_out) {
+          if (!timed_out && p.vec_out && !FEW && p.ksplit == 1) {
+            const uint32_t at = lanes + buf * S::kBN;
+            for (int c0 = 16 * half; c0 < tile.bn; c0 += 32) {
+              uint32_t f[2][8];
+              __syncwarp();
+              tmem_load_matrices(at + c0, f[0]);
+              tmem_load_matrices(at + c0 + (16u << 16), f[1]);
+              tmem_wait();
+              const Tile t = rows_at(c0);
+              if (t.qn > c0) store_matrices<MODE>(p, t, c0, nw, f, scale, stage, owner);
+            }
+          } else if (!timed_out) {
             for (int c0 = 16 * half; c0 < tile.bn; c0 += 32) {
               float v[16];
               __syncwarp();
