@@ -271,9 +271,11 @@ int gemm_f32_tc3_noalloc(int64_t M, int64_t N, int64_t K,
  * bounded wait inside gemm_f32 (between the blocks sharing a split tile, or
  * for a K-slice's TMA copy),
  * gemm_f32_tc3 (between the copy, tensor-core and epilogue roles of a block
- * or block pair), window_sum_f32 (for a tile's bulk copy) or softmax_rows_f32
- * (between the blocks sharing a row of more than 65536 columns) ran out of time
- * since the last check; results written since then are not valid.  The pages have no counterpart: this is the library's failure
+ * or block pair), window_sum_f32 (for a tile's bulk copy), softmax_rows_f32
+ * (between the blocks sharing a row of more than 65536 columns) or of the
+ * grouped products (between the copy, tensor-core and result roles) ran out of
+ * time since the last check; results written since then are not valid.  The
+ * pages have no counterpart: this is the library's failure
  * detection ("CMU DLSys Lecture 12" section 2 only asks that API and launch
  * errors be checked).  TMM_ERR_CUDA if the synchronisation itself failed.
  * In the bounds-checked build, TMM_ERR_BOUNDS (which takes precedence) when a
@@ -291,7 +293,9 @@ int tmm_check_device(tmm_stream_t stream);
  * for 16 bytes more than the first copy of each tile brings; makes that block of later window_sum_f32
  * launches (16-byte-aligned x) wait for 16 bytes more than its first tile
  * copy brings, and that block of later softmax_rows_f32 launches on rows of
- * more than 65536 columns skip counting itself in;
+ * more than 65536 columns skip counting itself in; makes that block of later
+ * grouped products wait for 16 bytes more than the copies of its first slice
+ * bring (of a pair, the first block);
  * wait_limit_ns > 0 sets the limit of every bounded wait of these kernels
  * (default, and for values <= 0, 10 s).
  * Process-wide; pass (-1, 0) to restore the defaults.  Always TMM_OK.
@@ -415,9 +419,9 @@ int softmax_rows_f32(int64_t rows, int64_t cols, const float *x, int64_t ldx, fl
  * rows, x_rows, N and K are below 2^29.
  *
  * Alignment: operands whose rows (and matrices) start on 16-byte boundaries
- * are read in place in the 16-bit types; others, and every FP32 operand, are
- * first restaged into the workspace (FP32: 6 bytes a value), and so are, in
- * larger products, the rows that row_index names.
+ * are read in place in the 16-bit types; others are first restaged into the
+ * workspace, and so are, in larger products, FP32 operands (6 bytes a value)
+ * and the rows that row_index names.
  *
  * workspace: DEVICE memory, 256-byte aligned, of at least the bytes that the
  * matching *_workspace_size call gives for the same arguments (0: none needed,
@@ -499,8 +503,9 @@ size_t gemm_grouped_wgrad_workspace_size(int dtype, int64_t groups, int64_t rows
  * that place p holds, all `rows` of them once (order of group_rows), or NULL:
  * the rows are in group order as they are.  Rows of no group get the shared
  * projection alone, and a row that row_index does not name is not written.
- * The product with a is rounded to dtype (FP32: kept to 24 bits) before the one
- * with b; everything else is summed in FP32 and rounded once.  With
+ * The product with a is kept in FP32, or, in larger products of the 16-bit
+ * types, as the sum of two values of dtype (16 bits of bf16, 22 of fp16; fp16:
+ * infinite above 65504); everything is summed in FP32 and rounded once.  With
  * a = w = b transposed and a and b exchanged it is the gradient with respect
  * to x.  1 <= rank <= 1024.
  */
