@@ -639,3 +639,33 @@ def test_lora_parts_of_tiles(dtype, sizes, first, T, K, r):
     low = None if dtype == torch.float32 else dtype
     want = ref.lora(x, w, a, b, scale, off, order, low=low)
     assert torch.equal(y.cpu(), want.to(dtype))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("T", [20, 600])
+def test_offsets_past_32_bits(dtype, T):
+    # Rows, matrices and results that lie more than 2^31 elements apart.
+    gen = torch.Generator().manual_seed(T)
+    K, N, r, sizes = 72, 136, 8, [T // 4, 0, T // 2]
+    ld, far = (2 ** 31 + 2 ** 29) // T // 8 * 8, 2 ** 30 + 2 ** 28
+
+    def rows(n):
+        return torch.empty(T * ld, dtype=dtype, device="cuda").as_strided((T, n), (ld, 1))
+
+    def stack(m, n):
+        return torch.empty(2 * far + m * n, dtype=dtype, device="cuda").as_strided(
+            (3, m, n), (far, n, 1))
+    x, dy = ints(gen, T, K, top=1), ints(gen, T, N, top=1)
+    w, a, b = ints(gen, 3, K, N, top=1), ints(gen, 3, K, r, top=1), ints(gen, 3, r, N, top=1)
+    off, scale = offsets_of(sizes), torch.ones(3)
+    offd = off.cuda()
+    xd, wd, yd = rows(K), stack(K, N), rows(N)
+    xd.copy_(x.to(dtype))
+    wd.copy_(w.to(dtype))
+    checked(tmm.gemm_grouped, xd, wd, offd, y=yd)
+    assert torch.equal(yd.cpu(), ref.grouped(x, w, off).to(dtype))
+    checked(tmm.gemm_lora, xd, wd[2], cuda(a, dtype), cuda(b, dtype), scale.cuda(), offd, y=yd)
+    assert torch.equal(yd.cpu(), ref.lora(x, w[2], a, b, scale, off).to(dtype))
+    yd.copy_(dy.to(dtype))
+    checked(tmm.gemm_grouped_wgrad, xd, yd, offd, dw=wd)
+    assert torch.equal(wd.cpu(), ref.wgrad(x, dy, off).to(dtype))

@@ -167,12 +167,6 @@ struct Ring {
       parity ^= 1;
     }
   }
-  template <int STAGES>
-  __device__ __forceinline__ void skip(int n) {
-    const int to = stage + n;
-    parity ^= uint32_t(to / STAGES) & 1u;
-    stage = to % STAGES;
-  }
 };
 
 // ---- primitives -------------------------------------------------------------------------
