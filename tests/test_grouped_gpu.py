@@ -669,3 +669,32 @@ def test_offsets_past_32_bits(dtype, T):
     yd.copy_(dy.to(dtype))
     checked(tmm.gemm_grouped_wgrad, xd, yd, offd, dw=wd)
     assert torch.equal(wd.cpu(), ref.wgrad(x, dy, off).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("sizes,K,N", [([70], 1100, 136), ([40, 0, 90], 2048, 264),
+                                       ([300, 1, 300], 1032, 520), ([31, 33], 1200, 130)])
+def test_rows_by_number_of_long_sums(dtype, sizes, K, N):
+    # Rows fetched by number and rows gathered first, tiles of every width.
+    gen = torch.Generator().manual_seed(K)
+    R, X = sum(sizes), 50
+    x, w = ints(gen, X, K, top=1), ints(gen, len(sizes), K, N, top=1)
+    x *= torch.rand(X, K, generator=gen) < 0.1
+    rows = torch.randint(-1, X + 2, (R,), generator=gen).to(torch.int32)
+    off = offsets_of(sizes)
+    y = checked(tmm.gemm_grouped, cuda(x, dtype), cuda(w, dtype), cuda(off), rows=cuda(rows))
+    assert torch.equal(y.cpu(), ref.grouped(x, w, off, rows).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("sizes", [[100], [300], [0, 500, 77], [129, 130]])
+def test_wgrad_of_rows_by_number_with_few_columns(dtype, sizes):
+    gen = torch.Generator().manual_seed(sum(sizes))
+    R, X, K, N = sum(sizes), 60, 200, 72
+    x, dy = ints(gen, X, K, top=1), ints(gen, R, N, top=1)
+    x *= torch.rand(X, K, generator=gen) < 0.2
+    rows = torch.randint(-1, X + 2, (R,), generator=gen).to(torch.int32)
+    off = offsets_of(sizes)
+    dw = checked(tmm.gemm_grouped_wgrad, cuda(x, dtype), cuda(dy, dtype), cuda(off),
+                 rows=cuda(rows))
+    assert torch.equal(dw.cpu(), ref.wgrad(x, dy, off, rows).to(dtype))

@@ -693,6 +693,7 @@ size_t gemm_grouped_wgrad_workspace_size(int dtype, int64_t groups, int64_t rows
   if (!sizes_ok(dtype, groups, rows, N, K) || !extent_ok(x_rows)) return 0;
   tmm::WgradProblem p = {};
   p.dtype = dtype;
+  p.groups = groups;
   p.rows = rows;
   p.N = N;
   p.row_index = row_index;

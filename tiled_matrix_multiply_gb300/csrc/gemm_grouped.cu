@@ -1425,11 +1425,11 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       } else {
         // Rows by number, four to a copy (single blocks), by warps 1 to 3, while warp 0 copies P:
         // warp w issues fours w - 1, w + 2, ...; lane l looks up row l % 4 of the warp's four l / 4;
-        // -1 is a row of zeros.  (Such a copy takes
-        // the copy engine about 40 cycles.  The 16 of a slice of 64 columns keep up with the
-        // memory; the 32 of a pair's slice, whose products take 512 cycles, do not: there the
-        // rows are gathered by a kernel first.  16384 rows x 4096 x 4096: 620 us by number, 331
-        // us + 40 us gathered.  cp.async by the copy warps, counted by a barrier: 758 us.)
+        // -1 is a row of zeros.  (Such a copy takes the copy engine about 40 cycles.  The 12 of a
+        // slice of 48 columns keep up with the memory; more do not, and there, as on pairs, the
+        // rows are gathered by a kernel first.  16384 rows x 4096 x 4096 on pairs: 620 us by
+        // number, 331 us + 40 us gathered.  cp.async by the copy warps, counted by a barrier: 758
+        // us.)
         const int row_in_slice = 4 * (warp - 1 + 3 * (lane >> 2)) + (lane & 3);
         const auto row_of = [&](int at, int limit) {
           if (at >= limit) return -1;
@@ -2186,6 +2186,21 @@ int split_of(int64_t tiles, int64_t slices, int planes, const DeviceInfo &dev) {
   return s;
 }
 
+// Columns of a pair's tile: the fewest of which one round of tiles is enough, so that few tiles
+// spread over more pairs and every slice is copied sooner; else the widest.  `most` bounds the tiles
+// of a width.  (4096 x 4096, 257 rows of 4 adapters, rank 16: 128 columns 31.7 us, 256 34.2 us; one
+// group of 300 rows 24.3 us and 27.8 us; FP32, 2 groups of 300 rows, 2048 x 1024: 64 columns 32 us,
+// 128 42 us.  Two rounds of narrow tiles are slower: 2048 rows of 16 adapters at N = 1024, 128
+// columns 51 us, 256 40 us.)
+template <typename Tiles>
+int pair_columns(int planes, Tiles most) {
+  constexpr int64_t kPairs = 76;
+  const int widest = columns_of(2, planes);
+  for (int n = 64; n < widest; n *= 2)
+    if (most(n) <= kPairs) return n;
+  return widest;
+}
+
 // Pairs or single blocks for a forward product, by an estimate of its cycles for groups of equal
 // size: rounds of tiles times what a K slice of 64 takes in one.  16-bit: products at 8192
 // multiply-adds a cycle and SM, copies at 64 bytes.  FP32: six products of three planes on pairs,
@@ -2268,11 +2283,13 @@ cudaError_t run_forward(int dtype, const Planes &x, const Stack &xs, const int32
                         const DeviceInfo &dev, cudaStream_t stream) {
   const int planes = dtype == TMM_F32 ? 3 : 1;
   const int cg = forward_shape(prm.rows, prm.groups, prm.N, prm.K, dtype);
-  const int bn = columns_of(cg, planes);
-  prm.tile_n = bn;
   prm.panels = int((prm.N + 128 * cg - 1) / (128 * cg));
-  const int64_t tiles =
-      prm.panels * (std::min<int64_t>(prm.groups, prm.rows) + prm.rows / bn);
+  const auto most = [&](int n) {
+    return prm.panels * (std::min<int64_t>(prm.groups, prm.rows) + prm.rows / n);
+  };
+  const int bn = cg == 1 ? columns_of(cg, planes) : pair_columns(planes, most);
+  prm.tile_n = bn;
+  const int64_t tiles = most(bn);
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
   prm.ksplit = cg == 2 ? 1 : split_of(tiles, (prm.K + kBK - 1) / kBK, planes, dev);
   if (prm.n_out == 0) prm.n_out = prm.N;
@@ -2297,9 +2314,17 @@ cudaError_t run_forward(int dtype, const Planes &x, const Stack &xs, const int32
 
 }  // namespace
 
-// Rows that are gathered before a product of pairs (0: none).
-static int64_t gathered_rows(int cg, const int32_t *row_index, int64_t rows) {
-  return cg == 2 && row_index != nullptr ? rows : 0;
+// Rows that are gathered by a kernel before a product (0: none): for pairs all, for single blocks
+// `many`, where the copies by number of a slice would take longer.  FP32 on single blocks reads rows
+// by number as cheaply as others.
+static int64_t gathered_rows(int cg, int dtype, const int32_t *row_index, int64_t rows, bool many) {
+  return row_index && !direct(cg, dtype) && (cg == 2 || many) ? rows : 0;
+}
+// Groups of more than 32 rows (of equal size), long sums.  (Single blocks, 4096 x 4096, bf16, one
+// group, by number and gathered: 33 rows 12.4 us and 12.8 us, 64 rows 21.4 us and 16.5 us, 200 rows
+// 34 us and 24 us; 64 rows of K = 1024 10.8 us both.)
+static int64_t grouped_gathered(const GroupedProblem &p, int cg) {
+  return gathered_rows(cg, p.dtype, p.row_index, p.rows, p.rows > 32 * p.groups && p.K > 1024);
 }
 
 static int shape_of(const GroupedProblem &p) {
@@ -2309,7 +2334,7 @@ static int shape_of(const GroupedProblem &p) {
 size_t grouped_workspace_bytes(const GroupedProblem &p) {
   const int cg = shape_of(p);
   if (direct(cg, p.dtype)) return 0;
-  return add_sizes({plane_bytes(p.x, p.dtype, gathered_rows(cg, p.row_index, p.rows)),
+  return add_sizes({plane_bytes(p.x, p.dtype, grouped_gathered(p, cg)),
                     plane_bytes(p.w, p.dtype)});
 }
 
@@ -2317,7 +2342,7 @@ cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void 
                            cudaStream_t stream) {
   char *ws = static_cast<char *>(workspace);
   const int cg = shape_of(p);
-  const int64_t gathered = gathered_rows(cg, p.row_index, p.rows);
+  const int64_t gathered = grouped_gathered(p, cg);
   Planes x = {}, w = {};
   if (!direct(cg, p.dtype)) {
     PlaneJobs jobs = {};
@@ -2341,10 +2366,16 @@ cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void 
                      prm, dev, stream);
 }
 
+// Every 64 columns of x read the group's rows again.  (Single blocks, 4096 x 128, bf16, by number and
+// gathered: 128 rows of a group 6.6 us and 7.7 us, 512 of each of 8 44 us and 30 us.)
+static int64_t wgrad_gathered(const WgradProblem &p) {
+  return gathered_rows(wgrad_shape(p.N), p.dtype, p.row_index, p.rows, p.rows > 128 * p.groups);
+}
+
 size_t wgrad_workspace_bytes(const WgradProblem &p) {
   if (direct(wgrad_shape(p.N), p.dtype)) return 0;
   return add_sizes(
-      {plane_bytes(p.x, p.dtype, gathered_rows(wgrad_shape(p.N), p.row_index, p.rows)),
+      {plane_bytes(p.x, p.dtype, wgrad_gathered(p)),
        plane_bytes(p.dy, p.dtype)});
 }
 
@@ -2352,7 +2383,7 @@ cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *wor
                          cudaStream_t stream) {
   char *ws = static_cast<char *>(workspace);
   const int cg = wgrad_shape(p.N);
-  const int64_t gathered = gathered_rows(cg, p.row_index, p.rows);
+  const int64_t gathered = wgrad_gathered(p);
   const int32_t *index = gathered ? nullptr : p.row_index;
   Planes x = {}, dy = {};
   cudaError_t e;
@@ -2458,7 +2489,7 @@ size_t lora_workspace_bytes(const LoraProblem &p) {
                               : add_sizes({u_bytes(p), plane_bytes(p.x, p.dtype),
                                            plane_bytes(p.w, p.dtype)});
   return add_sizes({u_bytes(p),
-                    plane_bytes(p.x, p.dtype, gathered_rows(2, p.row_index, p.rows)),
+                    plane_bytes(p.x, p.dtype, p.row_index ? p.rows : 0),
                     plane_bytes(p.w, p.dtype),
                     direct(low_shape(p), p.dtype) ? 0 : plane_bytes(p.a, p.dtype),
                     plane_bytes(p.b, p.dtype)});
@@ -2469,11 +2500,10 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   char *ws = static_cast<char *>(workspace);
   const int planes = p.dtype == TMM_F32 ? 3 : 1;
   const int cg = lora_shape(p);
-  const int bn = columns_of(cg, planes);
   const int64_t ldu = u_columns(p);
   void *u = ws;
   ws += u_bytes(p);
-  const int64_t gathered = gathered_rows(cg, p.row_index, p.rows);
+  const int64_t gathered = cg == 2 && p.row_index ? p.rows : 0;
   const bool low_direct = direct(low_shape(p), p.dtype);
   Planes x = {}, w = {}, a = {}, b = {};
   cudaError_t e;
@@ -2529,11 +2559,13 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
   }
   prm.N = prm.n_out = int(p.N);
   prm.q_rows = int(p.rows);
-  prm.tile_n = bn;
   prm.panels = int((p.N + 128 * cg - 1) / (128 * cg));
   // Pairs: columns at most, every adapter's rounded up to 32.
   const int64_t columns = cg == 1 ? p.rows : p.rows + 31 * (std::min(p.groups, p.rows) + 2);
-  const int64_t tiles = prm.panels * ((columns + bn - 1) / bn);
+  const auto most = [&](int n) { return prm.panels * ((columns + n - 1) / n); };
+  const int bn = cg == 1 ? columns_of(cg, planes) : pair_columns(planes, most);
+  prm.tile_n = bn;
+  const int64_t tiles = most(bn);
   if (tiles > INT32_MAX / 2 || columns > INT32_MAX - bn || (cg == 2 && p.rows * planes > INT32_MAX))
     return cudaErrorInvalidConfiguration;
   prm.ksplit = cg == 2 ? 1 : split_of(tiles, (p.K + kBK - 1) / kBK, planes, dev);
