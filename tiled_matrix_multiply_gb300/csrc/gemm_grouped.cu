@@ -2487,7 +2487,8 @@ size_t lora_workspace_bytes(const LoraProblem &p) {
   if (lora_shape(p) == 1)
     return p.dtype == TMM_F32 ? u_bytes(p)
                               : add_sizes({u_bytes(p), plane_bytes(p.x, p.dtype),
-                                           plane_bytes(p.w, p.dtype)});
+                                           plane_bytes(p.w, p.dtype),
+                                           plane_bytes(p.b, p.dtype)});
   return add_sizes({u_bytes(p),
                     plane_bytes(p.x, p.dtype, p.row_index ? p.rows : 0),
                     plane_bytes(p.w, p.dtype),
@@ -2511,10 +2512,8 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
     PlaneJobs jobs = {};
     x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs, gathered, p.row_index);
     w = plan_planes(p.w, p.dtype, nullptr, &ws, &jobs);
-    if (cg == 2) {
-      if (!low_direct) a = plan_planes(p.a, p.dtype, p.offsets, &ws, &jobs);
-      b = plan_planes(p.b, p.dtype, p.offsets, &ws, &jobs);
-    }
+    if (!low_direct && cg == 2) a = plan_planes(p.a, p.dtype, p.offsets, &ws, &jobs);
+    b = plan_planes(p.b, p.dtype, p.offsets, &ws, &jobs);
     if ((e = make_planes(jobs, p.dtype, dev, stream)) != cudaSuccess) return e;
   }
   Params prm = {};
@@ -2530,11 +2529,14 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
     prm.row_index = p.row_index;
     prm.u = static_cast<const float *>(u);
     prm.ldu = ldu;
-    prm.b = p.b.data;
-    prm.ldb = p.b.ld;
-    prm.stride_b = p.b.count > 1 ? p.b.stride : 0;
+    // b off 16-byte boundaries is copied beside w, 16-bit types (3 rows, K = 896, N = 205, rank 100:
+    // 52 us read as it is, 18 us copied); the copies' rows are whole vectors.
+    const bool as_is = direct(cg, p.dtype) || b.data == p.b.data;
+    prm.b = as_is ? p.b.data : b.data;
+    prm.ldb = as_is ? p.b.ld : b.ld;
+    prm.stride_b = p.b.count == 1 ? 0 : as_is ? p.b.stride : b.stride;
     prm.trans_b = p.trans_b;
-    prm.vec_b = on16(p.b, p.dtype == TMM_F32 ? 4 : 2) && p.b.cols % 8 == 0;
+    prm.vec_b = !as_is || (on16(p.b, p.dtype == TMM_F32 ? 4 : 2) && p.b.cols % 8 == 0);
   } else {
     Params up = prm;
     up.N = int(p.rank);
