@@ -407,7 +407,7 @@ int softmax_rows_f32(int64_t rows, int64_t cols, const float *x, int64_t ldx, fl
  * leading ones in FP32 registers every 128 values of the sum: normwise error
  * below 1e-6 at any K.  An infinite FP32 entry gives NaN or an infinity in the
  * results it enters (its lower parts are zero, and infinity times zero is NaN);
- * 16-bit types follow IEEE.
+ * 16-bit types follow IEEE (but see b of gemm_lora).
  *
  * Groups: `offsets` is a DEVICE array of groups + 1 int32; group g owns the
  * rows p with offsets[g] <= p < offsets[g+1].  Values are clamped to
@@ -503,11 +503,14 @@ size_t gemm_grouped_wgrad_workspace_size(int dtype, int64_t groups, int64_t rows
  * that place p holds, all `rows` of them once (order of group_rows), or NULL:
  * the rows are in group order as they are.  Rows of no group get the shared
  * projection alone, and a row that row_index does not name is not written.
- * The product with a is kept in FP32, or, in larger products of the 16-bit
- * types, as the sum of two values of dtype (16 bits of bf16, 22 of fp16; fp16:
- * infinite above 65504); everything is summed in FP32 and rounded once.  With
- * a = w = b transposed and a and b exchanged it is the gradient with respect
- * to x.  1 <= rank <= 1024.
+ * The product with a is an FP32 value.  In larger products it is multiplied as
+ * bf16 parts: bf16 operands as two (17 bits, FP32's range), fp16 and fp32 as all
+ * three (an fp16 b as two, exact); there an infinite entry of a 16-bit b gives
+ * NaN or an infinity in the results it enters, the lower parts of the product
+ * with a being zero as a rule.  Everything is
+ * summed in FP32 and rounded once.  With a = w = b transposed and a and b
+ * exchanged it is the gradient with respect to x.  1 <= rank <= 1024.  K == 0
+ * writes zeros to every row.
  */
 int gemm_lora(int dtype, int transw, int transa, int transb, int64_t groups, int64_t rows,
               int64_t N, int64_t K, int64_t rank,

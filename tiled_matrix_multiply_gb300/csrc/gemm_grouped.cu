@@ -15,8 +15,8 @@
 //   gradient: P = dy^T,  Q = x^T, the sum running over the group's rows
 //   adapters: the forward product with one P = w for all.  On pairs an adapter's columns start
 //             at a multiple of 32 of the tile's, and its part, P = b[g] and Q = u, is added to
-//             those columns alone (u keeps twice the type's bits, see store_pair); on single
-//             blocks, whose rows are few, it is added on the CUDA cores while w streams
+//             those columns alone; on single blocks, whose rows are few, it is added on the CUDA
+//             cores while w streams.  (On pairs u is read as parts: see store_u4.)
 // No operand value of another group, not even a NaN, meets a group's sums: columns are summed
 // apart, those past a group's end are not stored, and the gradient, whose sum runs over the rows,
 // reads zeros in their place.  A row number outside the matrix reads as zeros.
@@ -84,8 +84,14 @@ constexpr uint32_t kMaxSmem = 232448;    // 227 KiB
 
 // How the results are written.
 constexpr int kOutF32 = 0, kOutBF16 = 1, kOutF16 = 2;
-constexpr int kOutU = 3;       // the adapters' u: three planes (split3), or a pair of values
+constexpr int kOutU = 3;       // the adapters' u: its parts, in three planes or side by side
 
+
+// Values of `rank` per slice of the adapters' part: as many as the parts of u leave of the 64 columns
+// of a slice (store_u4), or FP32's planes.
+__host__ __device__ constexpr int rank_slice(int planes, int b_parts) {
+  return planes == 3 ? 64 : b_parts == 2 ? 16 : 32;
+}
 
 template <int CG, int PLANES>
 struct Shape {
@@ -108,8 +114,6 @@ struct Shape {
   // The parts of a shared sum (single blocks), and 1 KiB a result warp for 16-bit results.
   static constexpr uint32_t kRed = CG == 1 ? 128 * kBN * 4 : 0;
   static constexpr uint32_t kOutStage = PLANES == 1 ? kEpiWarps * 1024 : 0;
-  // Values of `rank` per slice of the adapters' part: 16-bit u is a pair of values (hi and lo).
-  static constexpr int kRankSlice = PLANES == 3 ? 64 : 32;
   static constexpr uint32_t kTable =
       kListed * 4 * 3 + kCopyWarps * 128 + 116 + (CG == 1 ? kFewRows * 4 : 0);
   static constexpr uint32_t kBars = 8 * (2 * kStages + 5) + 32;
@@ -135,6 +139,7 @@ struct Params {
   int p_mn, e_mn;        // P (and b) stored with n contiguous
   int p_shared, e_shared;   // one P (one b) for all groups
   uint32_t idesc;        // types; majors and sizes are added in the kernel
+  uint32_t idesc_e;      // types of the adapters' part
   // FP32 operands as they are stored (single blocks): P and x.
   const float *fp, *fx;
   int64_t ldp, stride_p, ldx;
@@ -574,24 +579,77 @@ __device__ __forceinline__ void split8(const float (&x)[8], uint32_t (&h)[3][4])
   }
 }
 
-// The adapters' u in a 16-bit type T: v = hi + lo, hi the value rounded to T and lo what that
-// leaves, so that u keeps about twice T's bits and only the final result is rounded to T.
-// Column n is stored at 64 (n / 32) + n % 32, its lo 32 columns on.
-template <typename T>
-__device__ __forceinline__ void store_pair(void *row, int n, float v) {
-  T *o = static_cast<T *>(row) + (n >> 5) * 64 + (n & 31);
-  const T hi = T(v);
-  const float f = float(hi);
-  o[0] = hi;
-  o[32] = T(isfinite(f) ? v - f : 0.0f);
+// The adapters' u beside 16-bit operands: BF16 parts of the FP32 value (split3) side by side in a
+// row, in blocks of 64 columns.  BF16 operands: two parts of 32 values, 17 bits of u, far below the
+// result's rounding (all three parts took 2 to 13 % longer).  FP16 operands: all three parts of 16
+// values, u's 24 bits and FP32's range (a pair of FP16 values is infinite above 65504 and has fewer
+// than 17 bits below 2^-8; the number of rows, which decides how u is made, would decide that).  The
+// fourth part is the first with zero in place of an infinity, for the products with b's second
+// part, which is zero as a rule.  Measured, 4096 x 4096, FP16, rank 64: 4096 rows of 6 adapters 141
+// us (with a pair of FP16 values 134), of 64 adapters 197 us (170).
+//
+// Parts of columns n to n + 3 (n % 4 = 0) of a row from one thread.
+__device__ __forceinline__ uint2 pack4(const uint16_t (&h)[4][4], int i) {
+  return make_uint2(h[0][i] | (uint32_t(h[1][i]) << 16), h[2][i] | (uint32_t(h[3][i]) << 16));
+}
+__device__ __forceinline__ void store_u4(uint16_t *row, int n, const float (&v)[4], bool bf16) {
+  uint16_t h[4][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint16_t s[3];
+    split3(v[j], s);
+    h[j][0] = s[0];
+    h[j][1] = s[1];
+    h[j][2] = s[2];
+    h[j][3] = (s[0] & 0x7FFFu) == 0x7F80u ? uint16_t(0) : s[0];
+  }
+  if (bf16) {
+    uint16_t *const o = row + (n >> 5) * 64 + (n & 31);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<uint2 *>(o + 32 * i) = pack4(h, i);
+  } else {
+    uint16_t *const o = row + (n >> 4) * 64 + (n & 15);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint2 *>(o + 16 * i) = pack4(h, i);
+  }
+}
+// Four rows' column n from every lane (n: its lane in the warp, on from a multiple of 32), `in` the
+// same in four lanes: they exchange values, so that each stores four columns of one row.  (Stores of
+// two bytes took the whole kernel 3 us longer.)
+__device__ __forceinline__ void store_u(uint16_t *row, int64_t ld, int n, const float (&v)[4],
+                                        bool in, int count, bool bf16) {
+  const int q = n & 3;
+  float f[4];      // columns n - q + 0..3 of row q
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // In turn i, lane q has its value of row q ^ i taken by lane q ^ i.
+    const float mine = q == 0 ? v[i] : q == 1 ? v[i ^ 1] : q == 2 ? v[i ^ 2] : v[i ^ 3];
+    const float got = __shfl_xor_sync(~0u, mine, i);
+    // Column q ^ i of row q.
+    if (q == 0) f[i] = got;
+    else if (q == 1) f[i ^ 1] = got;
+    else if (q == 2) f[i ^ 2] = got;
+    else f[i ^ 3] = got;
+  }
+  if (in && q < count) store_u4(row + q * ld, n - q, f, bf16);
+}
+
+// Two FP16 values (low and high half) as two BF16 parts each, exactly: 8 of the 11 bits and what they
+// leave (none of an infinity or a NaN).
+__device__ __forceinline__ void half_parts(uint32_t two, uint32_t (&h)[2]) {
+  const float a = __half2float(__ushort_as_half(uint16_t(two)));
+  const float b = __half2float(__ushort_as_half(uint16_t(two >> 16)));
+  h[0] = pair_bf16(a, b);
+  const float ra = a - __uint_as_float(h[0] << 16), rb = b - __uint_as_float(h[0] & 0xFFFF0000u);
+  h[1] = pair_bf16(ra == ra ? ra : 0.0f, rb == rb ? rb : 0.0f);
 }
 
 // One result at column n of the row at element offset `o` of the output.  Split operands
-// (PLANES = 3) give FP32, 16-bit operands their own type, and both the forms of u.
-template <int PLANES>
+// (PLANES = 3) give FP32, or u's planes; 16-bit operands their own type (u: store_u).
+template <int MODE, int PLANES>
 __device__ __forceinline__ void store_out(const Params &p, int64_t o, int n, float v) {
   if constexpr (PLANES == 3) {
-    if (p.out_type == kOutF32) {
+    if (MODE != kForward || p.out_type == kOutF32) {
       static_cast<float *>(p.out)[o + n] = v;
     } else {
       uint16_t h[3];
@@ -601,13 +659,8 @@ __device__ __forceinline__ void store_out(const Params &p, int64_t o, int n, flo
     }
   } else if (p.out_type == kOutBF16) {
     static_cast<__nv_bfloat16 *>(p.out)[o + n] = __float2bfloat16_rn(v);
-  } else if (p.out_type == kOutF16) {
-    static_cast<__half *>(p.out)[o + n] = __float2half_rn(v);
   } else {
-    uint16_t *row = static_cast<uint16_t *>(p.out) + o;
-    if (n >= p.N) v = 0.0f;
-    if (p.idesc & (1u << 7)) store_pair<__nv_bfloat16>(row, n, v);
-    else store_pair<__half>(row, n, v);
+    static_cast<__half *>(p.out)[o + n] = __float2half_rn(v);
   }
 }
 
@@ -742,13 +795,26 @@ __device__ __forceinline__ void store_columns(const Params &p, const Tile &t, in
     if (row >= p.out_rows) row = -1;
   }
   const bool in = n < p.n_out;
+  if constexpr (MODE == kForward && PLANES == 1) {
+    if (p.out_type == kOutU) {
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = n < p.N ? v[j + i] * scale : 0.0f;
+        store_u(static_cast<uint16_t *>(p.out) + first + j * p.ld_out, p.ld_out, n, f, in,
+                count - j, p.idesc & (1u << 7));
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     if (by_row) {
       const int r = __shfl_sync(~0u, row, j);
-      if (in && r >= 0) store_out<PLANES>(p, int64_t(r) * p.ld_out, n, v[j] * scale);
+      if (in && r >= 0) store_out<MODE, PLANES>(p, int64_t(r) * p.ld_out, n, v[j] * scale);
     } else if (in && j < count && !(check && owner[t.q0 + c0 + j] == -2)) {
-      store_out<PLANES>(p, first + j * p.ld_out, n, v[j] * scale);
+      store_out<MODE, PLANES>(p, first + j * p.ld_out, n, v[j] * scale);
     }
   }
 }
@@ -964,7 +1030,8 @@ __device__ __forceinline__ bool split_tile(const Params &p, const Tile &t, int s
 
 // ---- kernel -----------------------------------------------------------------------------
 
-template <int CG, int MODE, int PLANES>
+// BP: parts of b in the adapters' part on pairs, 2 where it is FP16 (half_parts).
+template <int CG, int MODE, int PLANES, int BP = 1>
 __global__ void __launch_bounds__(Shape<CG, PLANES>::kThreads, 1)
 grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                const __grid_constant__ CUtensorMap map_q,    // Q tiles
@@ -978,6 +1045,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   // The adapters' part: pairs extend the sum (EXT); single blocks, whose rows are few, add it to
   // the results on the CUDA cores while the weights stream (FEW).
   constexpr bool EXT = MODE == kLora && CG == 2, FEW = MODE == kLora && CG == 1;
+  constexpr int RS = rank_slice(PLANES, BP);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;    // the same offset in every block
@@ -1179,7 +1247,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + row + n) =
               make_uint4(0, 0, 0, 0);
       } else {
-        for (int n = lane; n < p.N; n += 32) store_out<PLANES>(p, row, n, 0.0f);
+        for (int n = lane; n < p.N; n += 32) store_out<MODE, PLANES>(p, row, n, 0.0f);
       }
     }
   }
@@ -1188,8 +1256,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     if (timed_out && p.ksplit == 1 && !FEW) break;     // (else warps meet at every tile)
     const Tile tile = tile_at<CG, MODE, PLANES>(p, tab, t);
     int nbase, s0, s1;
-    slices_of<EXT, S::kRankSlice>(p, tile, CG == 2 ? 0 : int(rank), nbase, s0, s1);
-    const int per_rank = EXT ? (p.rank + S::kRankSlice - 1) / S::kRankSlice : 1;
+    slices_of<EXT, RS>(p, tile, CG == 2 ? 0 : int(rank), nbase, s0, s1);
+    const int per_rank = EXT ? (p.rank + RS - 1) / RS : 1;
 
     if (S::kDirect && warp < S::kCopyWarps) {
       if constexpr (S::kDirect) {
@@ -1260,7 +1328,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           const int e = (s - nbase) / per_rank;
           const int j = s - nbase - e * per_rank;
           c.k0 = j * kBK;                    // of u
-          c.rank0 = j * S::kRankSlice;       // of b
+          c.rank0 = j * (p.e_mn ? RS : BP * RS);      // of b (N x rank, two parts: plan_parts)
           c.g = p.e_shared ? 0 : tab.gid[tile.e0 + e];
           c.gcount = p.e_shared ? 1 : p.groups;
           // This block's half of the entry's columns, 16 n32 rows.
@@ -1273,7 +1341,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       const auto bytes_of = [&](const Slice &c) {
         if (MODE == kWgrad)
           return uint32_t(PLANES) * ((c.cnt + 15) / 16 * 2048 * (2 + qblocks));
-        return PLANES * ((p.e_mn ? 2 * S::kRankSlice * 128 : kPTile) +
+        return PLANES * ((p.e_mn ? BP * 2 * RS * 128 : kPTile) +
                          uint32_t(c.cnt * (S::kBox * 128)));
       };
       // A slice that slice_at describes as ordinary in every respect.
@@ -1338,6 +1406,12 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
             for (int i = 0; i < 2 * PLANES; ++i)
               tma_3d<CG>(st + i * 8192, &map_e, n0 + (i & 1) * 64, c.rank0,
                          c.g + (i >> 1) * c.gcount, bar);
+            // The second part of b, 16 more values of the sum.
+            if (BP == 2) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                tma_3d<CG>(st + i * 8192 + 2048, &map_e, n0 + i * 64, c.rank0, c.g + c.gcount, bar);
+            }
           } else {
 #pragma unroll
             for (int i = 0; i < PLANES; ++i)
@@ -1492,9 +1566,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       if (leader && elect_one()) {
         const auto size_of = [&](int columns) {
           return (uint32_t(columns >> 3) << 17) | (uint32_t(128 * CG >> 4) << 24) |
-                 (MODE == kWgrad ? 1u << 16 : 0u) | p.idesc;
+                 (MODE == kWgrad ? 1u << 16 : 0u);
         };
-        const uint32_t all = size_of(tile.bn);
+        const uint32_t all = size_of(tile.bn) | p.idesc;
         const bool base_mn = MODE == kWgrad || p.p_mn;
         const uint32_t qstep = MODE == kWgrad ? 128 : 2;      // 16 values of K, in 16 bytes
         const int n = s1 - s0;
@@ -1527,7 +1601,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
             const int e = tile.e0 + (s - nbase) / per_rank;
             part = part_of(p, tab, tile, e);
             d += part.c0;
-            sizes = size_of(32 * part.n32);
+            sizes = size_of(32 * part.n32) | p.idesc_e;
             const int from = s - i % kChunk;
             fresh = from >= nbase && (s == from || (s - nbase) % per_rank == 0);
           }
@@ -1536,15 +1610,24 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           const uint64_t dp = tile_desc(st, pmn);
           const uint64_t dq = tile_desc(st + PLANES * kPTile, MODE == kWgrad);
           const uint32_t pstep = pmn ? 128 : 2;
-          const int left = ext ? min(S::kRankSlice, p.rank - (s - nbase) % per_rank * S::kRankSlice)
+          const int left = ext ? min(RS, p.rank - (s - nbase) % per_rank * RS)
                                : min(kBK, tile.klen - s * kBK);
           const int steps = (left + 15) / 16;
           if (PLANES == 1 && EXT && ext) {
-            // b[g] times u's hi, and times its lo, 32 columns on.
-            for (int k = 0; k < steps; ++k) {
-              const uint64_t a = dp + k * pstep, b = dq + k * qstep;
-              mma<CG>(d, a, b, idesc, true);
-              mma<CG>(d, a, b + 2 * qstep, idesc, true);
+            if constexpr (BP == 1) {
+              // b[g] times u's first part, and times its second, 32 columns on.
+              for (int k = 0; k < steps; ++k) {
+                const uint64_t a = dp + k * pstep, b = dq + k * qstep;
+                mma<CG>(d, a, b, idesc, true);
+                mma<CG>(d, a, b + 2 * qstep, idesc, true);
+              }
+            } else {
+              // The first part of b times u's three, 16 columns apart, and the second times the
+              // second and, in the fourth place, the first (with the third: 2^-24 of the product).
+#pragma unroll
+              for (int k = 0; k < 3; ++k) mma<CG>(d, dp, dq + k * qstep, idesc, true);
+              mma<CG>(d, dp + pstep, dq + 1 * qstep, idesc, true);
+              mma<CG>(d, dp + pstep, dq + 3 * qstep, idesc, true);
             }
           } else {
 #pragma unroll
@@ -1755,9 +1838,19 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
             if (FEW && owner[tile.q0 + col] == -2) o = -1;
             if (o < 0) continue;
             const float f[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+            if constexpr (MODE == kForward && PLANES == 1) {
+              if (p.out_type == kOutU) {
+                float g[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) g[j] = n + j < p.N ? f[j] * scale : 0.0f;
+                if (n < p.n_out)
+                  store_u4(static_cast<uint16_t *>(p.out) + o, n, g, p.idesc & (1u << 7));
+                continue;
+              }
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              if (n + j < p.n_out) store_out<PLANES>(p, o, n + j, f[j] * scale);
+              if (n + j < p.n_out) store_out<MODE, PLANES>(p, o, n + j, f[j] * scale);
           }
         }
       }
@@ -1803,7 +1896,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
 // ---- operand planes -----------------------------------------------------------------------
 
 // Copies stacks of matrices into 16-bit planes whose rows start on 16-byte boundaries: FP32
-// values into their three bf16 parts (planes), 16-bit values as they are (one plane).  Layout:
+// values into their three bf16 parts (planes), 16-bit values as they are (one plane), the FP16 b of
+// adapters on pairs into its two bf16 parts: two planes, or (`side`) side by side in a row, 16
+// columns each by turns.  Layout:
 // [plane][matrix][row][ld8].  With `index` (one matrix only) row r is the source's row index[r],
 // zeros for a number outside [0, src_rows).  Matrices of groups without rows are left out.
 // One launch makes the planes of all of a call's operands; bound by memory, each thread has
@@ -1815,8 +1910,10 @@ struct PlaneJob {
   int64_t count;
   const int *offsets, *index;
   uint16_t *dst;
+  int64_t units;        // units of eight values of a row
   int64_t tiles;        // tiles of kPlaneTile units of a matrix
   int vec;              // whole 16-byte loads
+  int parts, side;      // 16-bit values: parts of each, and whether they lie side by side
 };
 struct PlaneJobs {
   PlaneJob job[4];
@@ -1827,10 +1924,10 @@ constexpr int kPlaneThreads = 256, kPlaneAhead = 4;
 constexpr int kPlaneTile = kPlaneThreads * kPlaneAhead;
 
 // One tile of units; VEC: whole 16-byte loads throughout.
-template <bool F32, bool VEC>
+template <bool F32, bool PARTS, bool VEC>
 __device__ __forceinline__ void plane_tile(const PlaneJob &j, int64_t m, int64_t unit0) {
   using T = std::conditional_t<F32, float, uint16_t>;
-  const int64_t per_row = j.ld8 / 8, total = j.rows * per_row;
+  const int64_t per_row = j.units, total = j.rows * per_row;
   Eight<T> x[kPlaneAhead];
   int64_t to[kPlaneAhead];
 #pragma unroll
@@ -1839,12 +1936,14 @@ __device__ __forceinline__ void plane_tile(const PlaneJob &j, int64_t m, int64_t
     const int64_t row = total <= UINT32_MAX ? uint32_t(i) / uint32_t(per_row) : i / per_row;
     const int64_t c = (i - row * per_row) * 8;
     int64_t from = row;
-    bool on = i < total;
+    bool on = i < total && (!PARTS || c < j.cols);
     if (j.index) {
       from = on ? j.index[row] : -1;
       on = from >= 0 && from < j.src_rows;
     }
-    to[k] = i < total ? (m * j.rows + row) * j.ld8 + c : -1;
+    to[k] = i < total ? (m * j.rows + row) * j.ld8 +
+                          (PARTS && j.side ? (c >> 4) * 32 + (c & 15) : c)
+                    : -1;
     x[k] = load8<VEC>(static_cast<const T *>(j.src) + m * j.stride + (on ? from : 0) * j.ld + c, on,
                       j.cols - c);
   }
@@ -1861,13 +1960,29 @@ __device__ __forceinline__ void plane_tile(const PlaneJob &j, int64_t m, int64_t
       for (int pl = 0; pl < 3; ++pl)
         *reinterpret_cast<uint4 *>(j.dst + pl * j.plane + to[k]) =
             make_uint4(h[pl][0], h[pl][1], h[pl][2], h[pl][3]);
+    } else if (PARTS && j.parts == 2) {
+      const uint4 v = x[k].w[0];
+      const uint32_t two[4] = {v.x, v.y, v.z, v.w};
+      uint32_t h[2][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t parts[2];
+        half_parts(two[i], parts);
+        h[0][i] = parts[0];
+        h[1][i] = parts[1];
+      }
+      uint16_t *const dst = j.dst + to[k];
+      *reinterpret_cast<uint4 *>(dst) = make_uint4(h[0][0], h[0][1], h[0][2], h[0][3]);
+      *reinterpret_cast<uint4 *>(dst + (j.side ? 16 : j.plane)) =
+          make_uint4(h[1][0], h[1][1], h[1][2], h[1][3]);
     } else {
       *reinterpret_cast<uint4 *>(j.dst + to[k]) = x[k].w[0];
     }
   }
 }
 
-template <bool F32>
+// PARTS: a job makes parts of 16-bit values.
+template <bool F32, bool PARTS>
 __global__ void __launch_bounds__(kPlaneThreads)
 planes_kernel(const __grid_constant__ PlaneJobs jobs) {
   grid_wait();
@@ -1879,8 +1994,8 @@ planes_kernel(const __grid_constant__ PlaneJobs jobs) {
     const int64_t m = (t - jobs.first[n]) / j.tiles;
     if (j.offsets && j.offsets[m + 1] <= j.offsets[m]) continue;
     const int64_t unit0 = (t - jobs.first[n] - m * j.tiles) * kPlaneTile + threadIdx.x;
-    if (j.vec) plane_tile<F32, true>(j, m, unit0);
-    else plane_tile<F32, false>(j, m, unit0);
+    if (j.vec) plane_tile<F32, PARTS, true>(j, m, unit0);
+    else plane_tile<F32, PARTS, false>(j, m, unit0);
   }
 }
 
@@ -2057,17 +2172,53 @@ Planes plan_planes(const Stack &s, int dtype, const int32_t *offsets, char **ws,
   j.stride = s.count > 1 ? s.stride : 0;
   j.src_rows = s.rows;
   j.ld8 = round8(s.cols);
+  j.units = j.ld8 / 8;
+  j.parts = 1;
   j.count = s.count;
   j.plane = s.count * j.rows * j.ld8;
   j.offsets = s.count > 1 ? offsets : nullptr;      // one matrix may serve every group
   j.index = gathered ? index : nullptr;
   j.dst = reinterpret_cast<uint16_t *>(*ws);
-  j.tiles = (j.rows * (j.ld8 / 8) + kPlaneTile - 1) / kPlaneTile;
+  j.tiles = (j.rows * j.units + kPlaneTile - 1) / kPlaneTile;
   j.vec = on16(s, dtype == TMM_F32 ? 4 : 2) && s.cols % 8 == 0;
   jobs->first[jobs->count + 1] = jobs->first[jobs->count] + j.tiles * j.count;
   ++jobs->count;
   *ws += plane_bytes(s, dtype, gathered);
   return {j.dst, planes * s.count, j.rows, s.cols, j.ld8, j.rows * j.ld8};
+}
+
+// The FP16 b of adapters on pairs as two BF16 parts: its product with the BF16 parts of u is one of
+// equal types.  Stored rank x N, two planes; stored N x rank, the parts of 16 ranks side by side, so
+// that one box of the copy engine brings both.
+int64_t side_columns(const Stack &s) { return (s.cols + 15) / 16 * 32; }
+size_t part_bytes(const Stack &s, bool side) {
+  const __int128 n =
+      __int128(2) * s.count * s.rows * (side ? side_columns(s) : 2 * round8(s.cols));
+  return n > __int128(INT64_MAX / 4) ? SIZE_MAX : round256(size_t(n));
+}
+Planes plan_parts(const Stack &s, bool side, const int32_t *offsets, char **ws, PlaneJobs *jobs) {
+  PlaneJob &j = jobs->job[jobs->count];
+  j.src = s.data;
+  j.rows = s.rows;
+  j.cols = s.cols;
+  j.ld = s.ld;
+  j.stride = s.count > 1 ? s.stride : 0;
+  j.src_rows = s.rows;
+  j.ld8 = side ? side_columns(s) : round8(s.cols);
+  j.units = side ? j.ld8 / 16 : j.ld8 / 8;
+  j.parts = 2;
+  j.side = side;
+  j.count = s.count;
+  j.plane = s.count * j.rows * j.ld8;
+  j.offsets = s.count > 1 ? offsets : nullptr;
+  j.index = nullptr;
+  j.dst = reinterpret_cast<uint16_t *>(*ws);
+  j.tiles = (j.rows * j.units + kPlaneTile - 1) / kPlaneTile;
+  j.vec = on16(s, 2) && s.cols % 8 == 0;
+  jobs->first[jobs->count + 1] = jobs->first[jobs->count] + j.tiles * j.count;
+  ++jobs->count;
+  *ws += part_bytes(s, side);
+  return {j.dst, side ? s.count : 2 * s.count, j.rows, side ? j.ld8 : s.cols, j.ld8, j.rows * j.ld8};
 }
 
 cudaError_t make_planes(const PlaneJobs &jobs, int dtype, const DeviceInfo &dev,
@@ -2082,7 +2233,12 @@ cudaError_t make_planes(const PlaneJobs &jobs, int dtype, const DeviceInfo &dev,
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dtype == TMM_F32 ? planes_kernel<true> : planes_kernel<false>,
+  bool parts = false;
+  for (int i = 0; i < jobs.count; ++i) parts |= jobs.job[i].parts == 2;
+  return cudaLaunchKernelEx(&cfg,
+                            dtype == TMM_F32 ? planes_kernel<true, false>
+                            : parts          ? planes_kernel<false, true>
+                                             : planes_kernel<false, false>,
                             jobs);
 }
 
@@ -2105,12 +2261,12 @@ struct Maps {
   CUtensorMap p, q, qr, e, u, pr;
 };
 
-template <int CG, int MODE, int PLANES>
+template <int CG, int MODE, int PLANES, int BP = 1>
 cudaError_t launch_shape(const Maps &m, Params &prm, int64_t tiles, const DeviceInfo &dev,
                          cudaStream_t stream) {
   using S = Shape<CG, PLANES>;
   static std::atomic<uint64_t> configured{0};
-  auto kernel = grouped_kernel<CG, MODE, PLANES>;
+  auto kernel = grouped_kernel<CG, MODE, PLANES, BP>;
   const uint64_t bit = uint64_t(1) << (dev.id & 63);
   if (!(configured.load(std::memory_order_acquire) & bit)) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -2145,6 +2301,8 @@ cudaError_t launch_mode(int mode, const Maps &m, Params &prm, int64_t tiles,
                         const DeviceInfo &dev, cudaStream_t stream) {
   if (mode == kForward) return launch_shape<CG, kForward, PLANES>(m, prm, tiles, dev, stream);
   if (mode == kWgrad) return launch_shape<CG, kWgrad, PLANES>(m, prm, tiles, dev, stream);
+  if constexpr (CG == 2 && PLANES == 1)
+    if (prm.out_type == kOutF16) return launch_shape<2, kLora, 1, 2>(m, prm, tiles, dev, stream);
   return launch_shape<CG, kLora, PLANES>(m, prm, tiles, dev, stream);
 }
 
@@ -2467,14 +2625,18 @@ static cudaError_t launch_row_ranks(const LoraProblem &p, float *u, int64_t ldu,
                    : launch_row_ranks_as<__half, false>(p, u, ldu, stream);
 }
 
-// Columns of u: FP32 values on single blocks; for pairs a plane's 16-byte rows, or pairs of 16-bit
-// values in blocks of 32 + 32.
+// Columns of u: FP32 values on single blocks; for pairs a plane's 16-byte rows, or the parts of 32
+// values (BF16) or 16 (FP16) in blocks of 64.
+static int rank_slice_of(int dtype) {
+  return rank_slice(dtype == TMM_F32 ? 3 : 1, dtype == TMM_F16 ? 2 : 1);
+}
 static int64_t u_columns(const LoraProblem &p) {
-  return p.dtype == TMM_F32 || lora_shape(p) == 1 ? round8(p.rank) : (p.rank + 31) / 32 * 64;
+  if (p.dtype == TMM_F32 || lora_shape(p) == 1) return round8(p.rank);
+  return (p.rank + rank_slice_of(p.dtype) - 1) / rank_slice_of(p.dtype) * 64;
 }
 static size_t u_bytes(const LoraProblem &p) {
   const int size = lora_shape(p) == 1 ? 4 : p.dtype == TMM_F32 ? 6 : 2;
-  return round256(size_t(p.rows) * size_t(u_columns(p)) * size);   // below 2^31 * 2^11 * 6
+  return round256(size_t(p.rows) * size_t(u_columns(p)) * size);   // below 2^29 * 2^12 * 6
 }
 
 // How the product with a is computed on pairs: a forward product of its own.
@@ -2493,7 +2655,8 @@ size_t lora_workspace_bytes(const LoraProblem &p) {
                     plane_bytes(p.x, p.dtype, p.row_index ? p.rows : 0),
                     plane_bytes(p.w, p.dtype),
                     direct(low_shape(p), p.dtype) ? 0 : plane_bytes(p.a, p.dtype),
-                    plane_bytes(p.b, p.dtype)});
+                    p.dtype == TMM_F16 ? part_bytes(p.b, p.trans_b != 0)
+                                       : plane_bytes(p.b, p.dtype)});
 }
 
 cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *workspace,
@@ -2513,7 +2676,9 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
     x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs, gathered, p.row_index);
     w = plan_planes(p.w, p.dtype, nullptr, &ws, &jobs);
     if (!low_direct && cg == 2) a = plan_planes(p.a, p.dtype, p.offsets, &ws, &jobs);
-    b = plan_planes(p.b, p.dtype, p.offsets, &ws, &jobs);
+    b = cg == 2 && p.dtype == TMM_F16
+            ? plan_parts(p.b, p.trans_b != 0, p.offsets, &ws, &jobs)
+            : plan_planes(p.b, p.dtype, p.offsets, &ws, &jobs);
     if ((e = make_planes(jobs, p.dtype, dev, stream)) != cudaSuccess) return e;
   }
   Params prm = {};
@@ -2544,7 +2709,7 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
     up.ld_out = ldu;
     up.stride_out = p.rows * ldu;
     up.out_type = kOutU;
-    up.n_out = p.dtype == TMM_F32 ? int(p.rank) : int(ldu / 2);
+    up.n_out = int(p.dtype == TMM_F32 ? p.rank : ldu / 64 * rank_slice_of(p.dtype));
     up.scale = p.scale;
     const int32_t *index = gathered && !low_direct ? nullptr : p.row_index;
     if ((e = run_forward(p.dtype, x, p.x, index, a, p.a, p.trans_a != 0, up, dev, stream)) !=
@@ -2554,8 +2719,9 @@ cudaError_t launch_lora(const LoraProblem &p, const DeviceInfo &dev, void *works
     prm.out_rows = int(p.rows);
     prm.e_mn = p.trans_b ? 0 : 1;
     prm.e_shared = p.groups > 1 && p.b.count == 1;
+    prm.idesc_e = type_desc(TMM_BF16);
     const Planes um = {u, planes, p.rows, planes == 3 ? p.rank : ldu, ldu, p.rows * ldu};
-    if ((e = tile_map(&m.e, b, p.trans_b ? 128 : planes == 3 ? 64 : 32)) != cudaSuccess ||
+    if ((e = tile_map(&m.e, b, p.trans_b ? 128 : uint32_t(rank_slice_of(p.dtype)))) != cudaSuccess ||
         (e = row_map(&m.u, um, uint32_t(box_of(cg)))) != cudaSuccess)
       return e;
   }

@@ -299,7 +299,8 @@ def gemm_lora(x, w, a, b, scale, offsets, rows=None, y=None, workspace=None, str
     x: (T, K); w: (K, N); a: (adapters, K, r); b: (adapters, r, N) -- w, a and b also as
     transposed views; scale: float32 (adapters,).  offsets, rows: the rows grouped by adapter,
     ``offsets`` and ``order`` of ``group_rows(index, adapters)``; rows past offsets[-1] have no
-    adapter.  rows=None: x is in group order already.
+    adapter.  rows=None: x is in group order already.  The product x[t] a[g] has FP32's range for
+    every type; an infinite entry of b may give NaN where the formula gives an infinity.
     """
     if y is None and workspace is None and stream is None:
         done = _usual.lora(x, w, a, b, scale, offsets, rows)
