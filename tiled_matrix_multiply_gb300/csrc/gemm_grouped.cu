@@ -1082,8 +1082,12 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   // clamped, into the (still unused) ring.
   int *const offs = reinterpret_cast<int *>(smem);
   if (threadIdx.x == 0) {
+    // A slice is there once every warp that waits for its stage to be free has arrived, whether or not
+    // it had something to copy: one that nothing waits for could fall two rounds behind, and wait for
+    // a phase that has passed.
+    const int rows_by_number = CG == 1 && MODE != kLora && p.row_index ? S::kCopyWarps : 1;
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(bar_full + 8 * s, S::kDirect ? S::kCopyWarps / 2 : 1);
+      mbar_init(bar_full + 8 * s, S::kDirect ? S::kCopyWarps / 2 : rows_by_number);
       mbar_init(bar_empty + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -1278,7 +1282,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       // part of the ring holds will do.
       const auto held = [&](int half) { return max(0, min(tile.qn - half * hr, hr)); };
       const int mine = held(half_rank);
-      const auto boxes_of = [&](int half) { return (held(half) + S::kBox - 1) / S::kBox; };
+      // (One at least: the slice waits for the warp that copies it, see the barriers' counts.)
+      const auto boxes_of = [&](int half) { return max(1, (held(half) + S::kBox - 1) / S::kBox); };
       const auto whole = [&](int half) { return CG == 2 && held(half) * CG == p.tile_n; };
       const int boxes = boxes_of(half_rank);
       const int qblocks = hr / 64;
@@ -1290,7 +1295,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
 #pragma unroll
       for (int b = 0; b < kBoxes; ++b) {
         box_row[b] = qf + b * S::kBox;
-        if (EXT && b < boxes) {
+        if (EXT && b < boxes && mine > 0) {
           while (tab.tile[e + 1] * 32 <= qf + b * 32) ++e;
           box_row[b] = tab.row[e] + qf + b * 32 - tab.tile[e] * 32;
           in_one &= box_row[b] == box_row[0] + b * 32;
@@ -1556,6 +1561,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                                 bar);
               }
             }
+            mbar_arrive_local(bar);
           }
           __syncwarp();
           ring.template next<S::kStages>();
