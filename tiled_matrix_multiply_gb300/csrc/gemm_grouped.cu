@@ -28,8 +28,9 @@
 // (2^-8 of it and less) to another; the tensor core's additions do not round to nearest, and
 // the error of a sum grows with the number of additions made in tensor memory (16 values of K
 // each), so the first accumulator is taken out every kChunk slices and added in FP32 registers.
-// For 16-bit operands the whole sum stays in tensor memory: its error (2^-24 of the partial sum
-// per addition) is far below the result's rounding.
+// For 16-bit operands a sum stays in tensor memory for kLong slices, 512 additions whose errors
+// (2^-24 of the partial sum on the mean, of one sign where the terms are) come to 2^-15, a
+// sixteenth of FP16's rounding; longer sums are made of several, added in FP32.
 //
 // Two shapes:
 //   pairs  (CG = 2): two blocks on two SMs share 256 lanes x up to 256 columns
@@ -79,6 +80,15 @@ constexpr int kEpiWarps = 8;
 constexpr int kListed = kMaxGroups + 3;            // entries of a list of groups, see Table
 constexpr int kFewRows = 512;                      // rows of an adapters' call on single blocks
 constexpr int kChunk = 2;                // slices per tensor-memory sum of split operands
+// Slices per tensor-memory sum of 16-bit operands at most, 8192 values.  (A gradient over 524365 rows
+// of positive values was 0.7 % too small in one sum.  Taking sums out costs up to 8 %, see below.)
+constexpr int kLong = 128;
+// Slices of each of the tensor-memory sums of `n` slices, but for the last: equal ones, so that the
+// next has time to run while one is taken out.
+__device__ __forceinline__ int long_sum(int n) {
+  const int sums = (n + kLong - 1) / kLong;
+  return sums <= 1 ? n : (n + sums - 1) / sums;
+}
 constexpr uint32_t kPTile = 128 * 128;   // 128 lanes x 64 values: 16 KiB
 constexpr uint32_t kMaxSmem = 232448;    // 227 KiB
 
@@ -1574,89 +1584,112 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           return (uint32_t(columns >> 3) << 17) | (uint32_t(128 * CG >> 4) << 24) |
                  (MODE == kWgrad ? 1u << 16 : 0u);
         };
-        const uint32_t all = size_of(tile.bn) | p.idesc;
         const bool base_mn = MODE == kWgrad || p.p_mn;
         const uint32_t qstep = MODE == kWgrad ? 128 : 2;      // 16 values of K, in 16 bytes
         const int n = s1 - s0;
-        for (int i = 0; i < n; ++i) {
-          const int s = s0 + i;
-          const bool first = PLANES == 3 ? i % kChunk == 0 : i == 0;
+        // Slices [begin, last] of 16-bit operands make one tensor-memory sum; those of adapters
+        // belong to the last one of the base sum.
+        const int nb = EXT ? nbase : n;
+        const int each = PLANES == 3 ? 0 : long_sum(nb);
+        const auto last_of = [&](int from) { return nb - from <= each ? n - 1 : from + each - 1; };
+        int begin = 0, last = last_of(0);
+        // Waits for a slice's operands and, with the first of a tensor-memory sum, for its buffer.
+        const auto ready = [&](bool first) {
           if (first) {
             if (q >= 2 && !mbar_wait(bar_tempty + 8 * (q & 1), ((q >> 1) - 1) & 1u,
-                                     p.wait_limit_ns)) {
-              timed_out = true;
-              break;
-            }
+                                     p.wait_limit_ns))
+              return false;
             ++q;
           }
-          const uint32_t buf = (q - 1) & 1;
-          if (!mbar_wait(bar_full + 8 * ring.stage, ring.parity, p.wait_limit_ns)) {
-            timed_out = true;
-            break;
-          }
+          if (!mbar_wait(bar_full + 8 * ring.stage, ring.parity, p.wait_limit_ns)) return false;
           tc_fence_after();
-          const bool ext = EXT && s >= nbase;
-          const bool pmn = ext ? p.e_mn : base_mn;
-          uint32_t d = tmem + buf * S::kBN;
-          uint32_t sizes = all;
-          bool fresh = first;
-          Part part = {};
-          if (EXT && ext) {
-            // An adapter's part: on its columns alone.  PLANES = 3: it is the first of them in
-            // this tensor-memory sum if that holds adapters' slices only, and none of it yet.
-            const int e = tile.e0 + (s - nbase) / per_rank;
-            part = part_of(p, tab, tile, e);
-            d += part.c0;
-            sizes = size_of(32 * part.n32) | p.idesc_e;
-            const int from = s - i % kChunk;
-            fresh = from >= nbase && (s == from || (s - nbase) % per_rank == 0);
-          }
-          const uint32_t idesc = sizes | (pmn ? 1u << 15 : 0u);
+          return true;
+        };
+        // `steps` times 16 values of the sum to column c0 of the tile, `fresh`: its first ones
+        // (`low`: of the lower parts' sum).
+        const auto products = [&](uint32_t idesc, bool mn, int c0, int steps, bool fresh, bool low) {
           const uint32_t st = base + ring.stage * S::kStage;
-          const uint64_t dp = tile_desc(st, pmn);
+          const uint64_t dp = tile_desc(st, mn);
           const uint64_t dq = tile_desc(st + PLANES * kPTile, MODE == kWgrad);
-          const uint32_t pstep = pmn ? 128 : 2;
-          const int left = ext ? min(RS, p.rank - (s - nbase) % per_rank * RS)
-                               : min(kBK, tile.klen - s * kBK);
-          const int steps = (left + 15) / 16;
-          if (PLANES == 1 && EXT && ext) {
-            if constexpr (BP == 1) {
-              // b[g] times u's first part, and times its second, 32 columns on.
-              for (int k = 0; k < steps; ++k) {
-                const uint64_t a = dp + k * pstep, b = dq + k * qstep;
-                mma<CG>(d, a, b, idesc, true);
-                mma<CG>(d, a, b + 2 * qstep, idesc, true);
-              }
-            } else {
-              // The first part of b times u's three, 16 columns apart, and the second times the
-              // second and, in the fourth place, the first (with the third: 2^-24 of the product).
+          const uint32_t pstep = mn ? 128 : 2;
+          const uint32_t d = tmem + ((q - 1) & 1) * S::kBN + c0;
+          idesc |= mn ? 1u << 15 : 0u;
 #pragma unroll
-              for (int k = 0; k < 3; ++k) mma<CG>(d, dp, dq + k * qstep, idesc, true);
-              mma<CG>(d, dp + pstep, dq + 1 * qstep, idesc, true);
-              mma<CG>(d, dp + pstep, dq + 3 * qstep, idesc, true);
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (k >= steps) break;
-              const uint64_t a = dp + k * pstep, b = dq + k * qstep;
-              mma<CG>(d, a, b, idesc, !(fresh && k == 0));
-              if constexpr (PLANES == 3) {
-                constexpr uint64_t pa = kPTile >> 4, qa = S::kQTile >> 4;
-                const uint32_t ds = tmem + (2 + (done & 1)) * S::kBN + part.c0;
-                mma<CG>(ds, a + 2 * pa, b, idesc, !(i == 0 && k == 0));
-                mma<CG>(ds, a, b + 2 * qa, idesc, true);
-                mma<CG>(ds, a + pa, b + qa, idesc, true);
-                mma<CG>(ds, a + pa, b, idesc, true);
-                mma<CG>(ds, a, b + qa, idesc, true);
-              }
+          for (int k = 0; k < 4; ++k) {
+            if (k >= steps) break;
+            const uint64_t a = dp + k * pstep, b = dq + k * qstep;
+            mma<CG>(d, a, b, idesc, !(fresh && k == 0));
+            if constexpr (PLANES == 3) {
+              constexpr uint64_t pa = kPTile >> 4, qa = S::kQTile >> 4;
+              const uint32_t ds = tmem + (2 + (done & 1)) * S::kBN + c0;
+              mma<CG>(ds, a + 2 * pa, b, idesc, !(low && k == 0));
+              mma<CG>(ds, a, b + 2 * qa, idesc, true);
+              mma<CG>(ds, a + pa, b + qa, idesc, true);
+              mma<CG>(ds, a + pa, b, idesc, true);
+              mma<CG>(ds, a, b + qa, idesc, true);
             }
           }
+        };
+        // Slice i's products have been issued.
+        const auto finish = [&](int i) {
           mma_commit<CG>(bar_empty + 8 * ring.stage, true);
-          if (i == n - 1 || (PLANES == 3 && i % kChunk == kChunk - 1))
-            mma_commit<CG>(bar_tfull + 8 * buf, true);
+          if (PLANES == 3 ? i == n - 1 || i % kChunk == kChunk - 1 : i == last) {
+            mma_commit<CG>(bar_tfull + 8 * ((q - 1) & 1), true);
+            begin = i + 1;
+            last = last_of(begin);
+          }
           ring.template next<S::kStages>();
+        };
+        const uint32_t all = size_of(tile.bn) | p.idesc;
+        bool ok = true;
+        for (int i = 0; i < nb; ++i) {
+          const bool first = PLANES == 3 ? i % kChunk == 0 : i == begin;
+          if (!(ok = ready(first))) break;
+          products(all, base_mn, 0, (min(kBK, tile.klen - (s0 + i) * kBK) + 15) / 16, first, i == 0);
+          finish(i);
         }
+        if constexpr (EXT) {
+          // The adapters' parts, each on its columns alone.
+          int i = nb;
+          for (int e = 0; ok && e < tile.en; ++e) {
+            const Part part = part_of(p, tab, tile, tile.e0 + e);
+            const uint32_t types = size_of(32 * part.n32) | p.idesc_e;
+            for (int j = 0; j < per_rank; ++j, ++i) {
+              if (!(ok = ready(PLANES == 3 && i % kChunk == 0))) break;
+              const int steps = (min(RS, p.rank - j * RS) + 15) / 16;
+              if constexpr (PLANES == 3) {
+                // The first on these columns in this tensor-memory sum, if it holds adapters' slices
+                // only.
+                const bool fresh = i - i % kChunk >= nb && (i % kChunk == 0 || j == 0);
+                products(types, p.e_mn, part.c0, steps, fresh, false);
+              } else {
+                const uint32_t st = base + ring.stage * S::kStage;
+                const uint64_t dp = tile_desc(st, p.e_mn), dq = tile_desc(st + kPTile, false);
+                const uint32_t pstep = p.e_mn ? 128 : 2;
+                const uint32_t idesc = types | (p.e_mn ? 1u << 15 : 0u);
+                const uint32_t d = tmem + ((q - 1) & 1) * S::kBN + part.c0;
+                if constexpr (BP == 1) {
+                  // b[g] times u's first part, and times its second, 32 columns on.
+                  for (int k = 0; k < steps; ++k) {
+                    const uint64_t a = dp + k * pstep, b = dq + k * 2;
+                    mma<CG>(d, a, b, idesc, true);
+                    mma<CG>(d, a, b + 4, idesc, true);
+                  }
+                } else {
+                  // The first part of b times u's three, 16 columns apart, and the second times the
+                  // second and, in the fourth place, the first (with the third: 2^-24 of the
+                  // product).
+#pragma unroll
+                  for (int k = 0; k < 3; ++k) mma<CG>(d, dp, dq + 2 * k, idesc, true);
+                  mma<CG>(d, dp + pstep, dq + 2, idesc, true);
+                  mma<CG>(d, dp + pstep, dq + 6, idesc, true);
+                }
+              }
+              finish(i);
+            }
+          }
+        }
+        if (!ok) timed_out = true;
         if (n > 0) ++done;
       }
       __syncwarp();
@@ -1719,7 +1752,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         if (n == 0) {
           const float v[16] = {};
           for (int c0 = 16 * half; c0 < tile.bn; c0 += 32) put(c0, v);
-        } else {
+        } else if (const int nb = EXT ? nbase : n; nb <= kLong) {
           const uint32_t buf = q & 1;
           const bool ready =
               !timed_out && mbar_wait(bar_tfull + 8 * buf, (q >> 1) & 1u, p.wait_limit_ns);
@@ -1748,6 +1781,58 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_relaxed(tempty + 8 * buf);
+        } else {
+          // Several tensor-memory sums.  Their sum is kept in local memory (the loops over blocks
+          // are not unrolled), as the registers of 128 values a thread are not there: 128 KB a block
+          // and sum, on the way that the operands take (8 groups of 8320 rows, 2048 x 2048: 330 us
+          // -> 350 us; K = 8320, 4096 rows of 8 groups, N = 2048: 89 us -> 101 us; up to 8192
+          // unchanged).
+          const bool matrices = p.vec_out && !FEW && p.ksplit == 1;
+          const int each = long_sum(nb);
+          float acc[kBlocks][16];
+          for (int left = nb; left > 0; left -= each, ++q) {
+            const uint32_t buf = q & 1;
+            const bool ready =
+                !timed_out && mbar_wait(bar_tfull + 8 * buf, (q >> 1) & 1u, p.wait_limit_ns);
+            if (!__all_sync(~0u, ready)) timed_out = true;
+            if (timed_out) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 16 * half; c0 < tile.bn; c0 += 32) {
+              const uint32_t at = lanes + buf * S::kBN + c0;
+              float a[16];
+              uint32_t f[2][8];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) a[j] = left == nb ? 0.0f : acc[c0 >> 5][j];
+              __syncwarp();
+              if (matrices) {
+                tmem_load_matrices(at, f[0]);
+                tmem_load_matrices(at + (16u << 16), f[1]);
+                tmem_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) a[j] += __uint_as_float(f[j >> 3][j & 7]);
+              } else {
+                float v[16];
+                tmem_load_16(at, v);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) a[j] += v[j];
+              }
+              if (left > each) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[c0 >> 5][j] = a[j];
+              } else if (matrices) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) f[j >> 3][j & 7] = __float_as_uint(a[j]);
+                const Tile t = rows_at(c0);
+                if (t.qn > c0) store_matrices<MODE>(p, t, c0, nw, f, scale, stage, owner);
+              } else {
+                put(c0, a);
+              }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_relaxed(tempty + 8 * buf);
+          }
         }
       } else {
         float acc[kBlocks][16];
