@@ -371,19 +371,33 @@ __device__ __forceinline__ void mma_commit(uint32_t bar, bool both) {
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
         : "memory");
 }
-// 16 consecutive FP32 columns of this thread's lane.
-__device__ __forceinline__ void tmem_load_16(uint32_t addr, float (&v)[16]) {
-  uint32_t r[16];
+// Waits for this thread's tensor-memory loads.  The registers that they fill are operands, so that no
+// use of them, which depends on nothing else, is moved before the wait.
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[8], uint32_t (&s)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(s[0]), "+r"(s[1]), "+r"(s[2]), "+r"(s[3]),
+                 "+r"(s[4]), "+r"(s[5]), "+r"(s[6]), "+r"(s[7])
+               :
+               : "memory");
+}
+// 8 consecutive FP32 columns of this thread's lane, there after tmem_wait.
+__device__ __forceinline__ void tmem_load_8(uint32_t addr, uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11,"
-      " %12, %13, %14, %15}, [%16];"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(addr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        "=r"(r[7])
+      : "r"(addr)
+      : "memory");
+}
+// 16 of them, waited for.
+__device__ __forceinline__ void tmem_load_16(uint32_t addr, float (&v)[16]) {
+  uint32_t r[2][8];
+  tmem_load_8(addr, r[0]);
+  tmem_load_8(addr + 8, r[1]);
+  tmem_wait(r[0], r[1]);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i >> 3][i & 7]);
 }
 
 // 16 lanes x 16 consecutive FP32 columns, in the order of an 8 x 8 matrix instruction: r[4 c + 2 h]
@@ -394,10 +408,8 @@ __device__ __forceinline__ void tmem_load_matrices(uint32_t addr, uint32_t (&r)[
       "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7])
-      : "r"(addr));
-}
-__device__ __forceinline__ void tmem_wait() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+      : "r"(addr)
+      : "memory");
 }
 
 // Shared-memory matrix descriptor, 128-byte swizzle: start address >> 4 (bits 0-13), leading
@@ -1766,7 +1778,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
               __syncwarp();
               tmem_load_matrices(at + c0, f[0]);
               tmem_load_matrices(at + c0 + (16u << 16), f[1]);
-              tmem_wait();
+              tmem_wait(f[0], f[1]);
               const Tile t = rows_at(c0);
               if (t.qn > c0) store_matrices<MODE>(p, t, c0, nw, f, scale, stage, owner);
             }
@@ -1808,7 +1820,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
               if (matrices) {
                 tmem_load_matrices(at, f[0]);
                 tmem_load_matrices(at + (16u << 16), f[1]);
-                tmem_wait();
+                tmem_wait(f[0], f[1]);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) a[j] += __uint_as_float(f[j >> 3][j & 7]);
               } else {
