@@ -402,12 +402,15 @@ int softmax_rows_f32(int64_t rows, int64_t cols, const float *x, int64_t ldx, fl
  * counterpart; the tiling is that of gemm_f32_tc3, on the same tensor cores.
  *
  * Element types (dtype): every matrix of a call has the same one.  FP32 sums
- * throughout; results are rounded once.  FP32 operands are split into three
- * bf16 parts each (exact) and six of the nine part products are added, the
- * leading ones in FP32 registers every 128 values of the sum: normwise error
- * below 1e-6 at any K.  An infinite FP32 entry gives NaN or an infinity in the
- * results it enters (its lower parts are zero, and infinity times zero is NaN);
- * 16-bit types follow IEEE (but see b of gemm_lora).
+ * throughout; results are rounded once.  Sums of 16-bit operands are made of
+ * parts of at most 8192 values, each with an error of 2^-15 of its magnitude on
+ * the mean.  FP32 operands are split into three bf16 parts each (exact from
+ * 2^-102 up) and six of the nine part products are added, in sums of 128 values
+ * that FP32 registers add up: normwise error below 1e-6 for sums of up to 65536
+ * values, and 2^-24 at most for every 128 values beyond.  An infinite FP32 entry
+ * gives NaN or an infinity in the results it enters (its lower parts are zero,
+ * and infinity times zero is NaN); 16-bit types follow IEEE (but see b of
+ * gemm_lora).
  *
  * Groups: `offsets` is a DEVICE array of groups + 1 int32; group g owns the
  * rows p with offsets[g] <= p < offsets[g+1].  Values are clamped to

@@ -23,11 +23,11 @@
 //
 // Single precision: every operand x is split into three bf16 parts, x = x0 + x1 + x2 exactly
 // (split3): for pairs by a pre-pass (planes), on single blocks by the copy warps (split_tile).
-// Of the nine part products the three smallest (2^-24 of the
-// term and less) are dropped.  x0 y0 goes to one accumulator, the five smaller ones
-// (2^-8 of it and less) to another; the tensor core's additions do not round to nearest, and
-// the error of a sum grows with the number of additions made in tensor memory (16 values of K
-// each), so the first accumulator is taken out every kChunk slices and added in FP32 registers.
+// Of the nine part products the three smallest (2^-24 of the term and less) are dropped.  x0 y0
+// goes to one accumulator, the five smaller ones (2^-8 of it and less) to another; the tensor core's
+// additions do not round to nearest, and the error of a sum grows with the number of additions made
+// in tensor memory (16 values of K each), so both are taken out every kChunk slices and added in
+// FP32 registers.
 // For 16-bit operands a sum stays in tensor memory for kLong slices, 512 additions whose errors
 // (2^-24 of the partial sum on the mean, of one sign where the terms are) come to 2^-15, a
 // sixteenth of FP16's rounding; longer sums are made of several, added in FP32.
@@ -1258,7 +1258,6 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   bool timed_out = false;
   Ring ring = {0, 0};
   uint32_t q = 0;      // tensor-memory sums so far
-  uint32_t done = 0;   // tiles with a sum so far
   bool dropped = int(blockIdx.x) == p.drop_block;   // testing hook: the next expectation is wrong
 
   // Forward: rows of the result that belong to no group are zero, a warp a row.
@@ -1617,9 +1616,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           tc_fence_after();
           return true;
         };
-        // `steps` times 16 values of the sum to column c0 of the tile, `fresh`: its first ones
-        // (`low`: of the lower parts' sum).
-        const auto products = [&](uint32_t idesc, bool mn, int c0, int steps, bool fresh, bool low) {
+        // `steps` times 16 values of the sum to column c0 of the tile, `fresh`: its first ones.
+        const auto products = [&](uint32_t idesc, bool mn, int c0, int steps, bool fresh) {
           const uint32_t st = base + ring.stage * S::kStage;
           const uint64_t dp = tile_desc(st, mn);
           const uint64_t dq = tile_desc(st + PLANES * kPTile, MODE == kWgrad);
@@ -1633,8 +1631,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
             mma<CG>(d, a, b, idesc, !(fresh && k == 0));
             if constexpr (PLANES == 3) {
               constexpr uint64_t pa = kPTile >> 4, qa = S::kQTile >> 4;
-              const uint32_t ds = tmem + (2 + (done & 1)) * S::kBN + c0;
-              mma<CG>(ds, a + 2 * pa, b, idesc, !(low && k == 0));
+              const uint32_t ds = d + 2 * S::kBN;      // the lower parts' products
+              mma<CG>(ds, a + 2 * pa, b, idesc, !(fresh && k == 0));
               mma<CG>(ds, a, b + 2 * qa, idesc, true);
               mma<CG>(ds, a + pa, b + qa, idesc, true);
               mma<CG>(ds, a + pa, b, idesc, true);
@@ -1657,7 +1655,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         for (int i = 0; i < nb; ++i) {
           const bool first = PLANES == 3 ? i % kChunk == 0 : i == begin;
           if (!(ok = ready(first))) break;
-          products(all, base_mn, 0, (min(kBK, tile.klen - (s0 + i) * kBK) + 15) / 16, first, i == 0);
+          products(all, base_mn, 0, (min(kBK, tile.klen - (s0 + i) * kBK) + 15) / 16, first);
           finish(i);
         }
         if constexpr (EXT) {
@@ -1673,7 +1671,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                 // The first on these columns in this tensor-memory sum, if it holds adapters' slices
                 // only.
                 const bool fresh = i - i % kChunk >= nb && (i % kChunk == 0 || j == 0);
-                products(types, p.e_mn, part.c0, steps, fresh, false);
+                products(types, p.e_mn, part.c0, steps, fresh);
               } else {
                 const uint32_t st = base + ring.stage * S::kStage;
                 const uint64_t dp = tile_desc(st, p.e_mn), dq = tile_desc(st + kPTile, false);
@@ -1702,7 +1700,6 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           }
         }
         if (!ok) timed_out = true;
-        if (n > 0) ++done;
       }
       __syncwarp();
       timed_out = __any_sync(~0u, timed_out);
@@ -1873,24 +1870,25 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           for (int b = 0; b < kBlocks; ++b) {
             const int c0 = 32 * b + 16 * half;
             if (c0 >= tile.bn) break;
-            float v[16];
             __syncwarp();
-            if (!EXT || (c0 >= from && c0 < to)) {
-              tmem_load_16(lanes + buf * S::kBN + c0, v);
+            if (EXT && (c0 < from || c0 >= to)) continue;
+            // The two are added to each other first: the lower parts' sum is small, and rounded alone
+            // to steps of the whole sum its errors need not be of either sign.
 #pragma unroll
-              for (int j = 0; j < 16; ++j) acc[b][j] += v[j];
-            }
-            if (c == chunks - 1) {
-              tmem_load_16(lanes + (2 + (done & 1)) * S::kBN + c0, v);
+            for (int j0 = 0; j0 < 16; j0 += 8) {
+              uint32_t v[8], low[8];
+              tmem_load_8(lanes + buf * S::kBN + c0 + j0, v);
+              tmem_load_8(lanes + (2 + buf) * S::kBN + c0 + j0, low);
+              tmem_wait(v, low);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) acc[b][j] += v[j];
+              for (int j = 0; j < 8; ++j)
+                acc[b][j0 + j] += __uint_as_float(v[j]) + __uint_as_float(low[j]);
             }
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_relaxed(tempty + 8 * buf);
         }
-        if (n > 0) ++done;
         if (!timed_out) {
 #pragma unroll
           for (int b = 0; b < kBlocks; ++b) {
