@@ -407,10 +407,9 @@ int softmax_rows_f32(int64_t rows, int64_t cols, const float *x, int64_t ldx, fl
  * the mean.  FP32 operands are split into three bf16 parts each (exact from
  * 2^-102 up) and six of the nine part products are added, in sums of 128 values
  * that FP32 registers add up: normwise error below 1e-6 for sums of up to 65536
- * values, and 2^-24 at most for every 128 values beyond.  An infinite FP32 entry
- * gives NaN or an infinity in the results it enters (its lower parts are zero,
- * and infinity times zero is NaN); 16-bit types follow IEEE (but see b of
- * gemm_lora).
+ * values, and 2^-24 at most for every 128 values beyond.  Infinities and NaN
+ * follow IEEE in every type (but see b of gemm_lora; and an infinity times an
+ * FP32 value below 2^-126 may be NaN).
  *
  * Groups: `offsets` is a DEVICE array of groups + 1 int32; group g owns the
  * rows p with offsets[g] <= p < offsets[g+1].  Values are clamped to

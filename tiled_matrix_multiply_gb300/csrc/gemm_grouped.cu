@@ -1873,7 +1873,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
             __syncwarp();
             if (EXT && (c0 < from || c0 >= to)) continue;
             // The two are added to each other first: the lower parts' sum is small, and rounded alone
-            // to steps of the whole sum its errors need not be of either sign.
+            // to steps of the whole sum its errors need not be of either sign.  A leading sum that is
+            // not finite stands alone: an infinity's lower parts are zeros, whose products with
+            // another are NaN.
 #pragma unroll
             for (int j0 = 0; j0 < 16; j0 += 8) {
               uint32_t v[8], low[8];
@@ -1881,8 +1883,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
               tmem_load_8(lanes + (2 + buf) * S::kBN + c0 + j0, low);
               tmem_wait(v, low);
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                acc[b][j0 + j] += __uint_as_float(v[j]) + __uint_as_float(low[j]);
+              for (int j = 0; j < 8; ++j) {
+                const float top = __uint_as_float(v[j]);
+                acc[b][j0 + j] += isfinite(top) ? top + __uint_as_float(low[j]) : top;
+              }
             }
           }
           tc_fence_before();
