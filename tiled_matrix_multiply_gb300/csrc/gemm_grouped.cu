@@ -953,7 +953,7 @@ __device__ __forceinline__ void add_adapters(const Params &p, const int *owner, 
 template <int MODE, bool VEC>
 __device__ __forceinline__ bool split_tile(const Params &p, const Tile &t, int s0, int s1,
                                            uint32_t base, uint32_t bar_full, uint32_t bar_empty,
-                                           Ring &ring, bool &dropped) {
+                                           Ring &ring, bool &dropped, int64_t limit_ns) {
   using S = Shape<1, 3>;
   static_assert(S::kStages == 2 && S::kCopyWarps == 16, "eight warps for each of two stages");
   const int warp = (threadIdx.x >> 5) & 7, team = threadIdx.x >> 8, lane = threadIdx.x & 31;
@@ -1022,7 +1022,7 @@ __device__ __forceinline__ bool split_tile(const Params &p, const Tile &t, int s
                    : "memory");
   };
   const auto put = [&](const Chunks &v) {
-    const bool ok = mbar_wait(bar_empty + 8 * ring.stage, ring.parity ^ 1u, p.wait_limit_ns);
+    const bool ok = mbar_wait(bar_empty + 8 * ring.stage, ring.parity ^ 1u, limit_ns);
     if (!__all_sync(~0u, ok)) return false;
     const uint32_t st = base + ring.stage * S::kStage, sq = st + 3 * kPTile;
 #pragma unroll
@@ -1279,6 +1279,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
 
   for (int t = cluster; t < tab.tiles; t += clusters) {
     if (timed_out && p.ksplit == 1 && !FEW) break;     // (else warps meet at every tile)
+    const int64_t limit_ns = timed_out ? 0 : p.wait_limit_ns;      // a warp waits in vain only once
     const Tile tile = tile_at<CG, MODE, PLANES>(p, tab, t);
     int nbase, s0, s1;
     slices_of<EXT, RS>(p, tile, CG == 2 ? 0 : int(rank), nbase, s0, s1);
@@ -1287,9 +1288,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     if (S::kDirect && warp < S::kCopyWarps) {
       if constexpr (S::kDirect) {
         const bool ok = p.vec ? split_tile<MODE, true>(p, tile, s0, s1, base, bar_full, bar_empty,
-                                                       ring, dropped)
+                                                       ring, dropped, limit_ns)
                               : split_tile<MODE, false>(p, tile, s0, s1, base, bar_full, bar_empty,
-                                                        ring, dropped);
+                                                        ring, dropped, limit_ns);
         if (!ok) timed_out = true;
       }
     } else if (!S::kDirect && warp < S::kCopyWarps) {
@@ -1491,7 +1492,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           if (elect_one()) {
             for (int s = s0; s < s1; ++s) {
               const uint32_t st = base + ring.stage * S::kStage;
-              if (!mbar_wait(bar_empty + 8 * ring.stage, ring.parity ^ 1u, p.wait_limit_ns)) {
+              if (!mbar_wait(bar_empty + 8 * ring.stage, ring.parity ^ 1u, limit_ns)) {
                 timed_out = true;
                 break;
               }
@@ -1547,7 +1548,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         }
         for (int s = s0; s < s1 && !timed_out; ++s) {
           const uint32_t st = base + ring.stage * S::kStage, sq = st + PLANES * kPTile;
-          const bool ok = mbar_wait(bar_empty + 8 * ring.stage, ring.parity ^ 1u, p.wait_limit_ns);
+          const bool ok = mbar_wait(bar_empty + 8 * ring.stage, ring.parity ^ 1u, limit_ns);
           if (!__all_sync(~0u, ok)) {
             timed_out = true;
             break;
@@ -1608,11 +1609,11 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         const auto ready = [&](bool first) {
           if (first) {
             if (q >= 2 && !mbar_wait(bar_tempty + 8 * (q & 1), ((q >> 1) - 1) & 1u,
-                                     p.wait_limit_ns))
+                                     limit_ns))
               return false;
             ++q;
           }
-          if (!mbar_wait(bar_full + 8 * ring.stage, ring.parity, p.wait_limit_ns)) return false;
+          if (!mbar_wait(bar_full + 8 * ring.stage, ring.parity, limit_ns)) return false;
           tc_fence_after();
           return true;
         };
@@ -1764,7 +1765,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         } else if (const int nb = EXT ? nbase : n; nb <= kLong) {
           const uint32_t buf = q & 1;
           const bool ready =
-              !timed_out && mbar_wait(bar_tfull + 8 * buf, (q >> 1) & 1u, p.wait_limit_ns);
+              !timed_out && mbar_wait(bar_tfull + 8 * buf, (q >> 1) & 1u, limit_ns);
           ++q;
           if (!__all_sync(~0u, ready)) timed_out = true;
           tc_fence_after();
@@ -1802,7 +1803,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           for (int left = nb; left > 0; left -= each, ++q) {
             const uint32_t buf = q & 1;
             const bool ready =
-                !timed_out && mbar_wait(bar_tfull + 8 * buf, (q >> 1) & 1u, p.wait_limit_ns);
+                !timed_out && mbar_wait(bar_tfull + 8 * buf, (q >> 1) & 1u, limit_ns);
             if (!__all_sync(~0u, ready)) timed_out = true;
             if (timed_out) break;
             tc_fence_after();
@@ -1852,7 +1853,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
         const int chunks = (n + kChunk - 1) / kChunk;
         for (int c = 0; c < chunks && !timed_out; ++c, ++q) {
           const uint32_t buf = q & 1;
-          const bool ready = mbar_wait(bar_tfull + 8 * buf, (q >> 1) & 1u, p.wait_limit_ns);
+          const bool ready = mbar_wait(bar_tfull + 8 * buf, (q >> 1) & 1u, limit_ns);
           if (!__all_sync(~0u, ready)) {
             timed_out = true;
             break;
@@ -1968,13 +1969,6 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     grid_wait();       // no grid ends before the one it follows
     grid_start_next();
   }
-  if (warp < S::kCopyWarps && timed_out) {
-    // Let the copies in flight land before the block goes away: one that was issued does within
-    // microseconds.
-    const uint64_t t0 = timer_ns();
-    while (timer_ns() - t0 < 1000 * 1000) {
-    }
-  }
   if (warp == S::kMmaWarp && leader) {
     if (elect_one()) mma_commit<CG>(bar_drain, false);
     __syncwarp();
@@ -1983,7 +1977,13 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
   __syncwarp();
   if (timed_out && lane == 0) atomicOr(&g_grouped_status, 2u);
   tc_fence_before();
-  __syncthreads();
+  if (__syncthreads_or(timed_out)) {
+    // Let the copies in flight land before the block goes away: one that was issued does within
+    // microseconds.
+    const uint64_t t0 = timer_ns();
+    while (timer_ns() - t0 < 1000 * 1000) {
+    }
+  }
   if (CG == 2) cluster_sync();   // remote arrivals have landed; neither block uses tensor memory
   tc_fence_after();
   if (warp == S::kMmaWarp) {
