@@ -22,9 +22,11 @@ from __future__ import annotations
 from ._abi import (TMM_ERR_ALIAS, TMM_ERR_CUDA, TMM_ERR_INVALID_ARG,  # noqa: F401
                    TMM_ERR_UNSUPPORTED_DEVICE, TMM_OK, TmmError)
 
+# What `from ... import *` takes: names that are there without torch or a built library.  The grouped
+# operators are attributes of the package beside them (see __getattr__).
 __all__ = ["gemm_f32", "gemm_f32_naive", "gemm_f32_tc3", "tc3_workspace_bytes",
-           "window_sum_f32", "sum_f32", "softmax_rows_f32", "group_rows", "RowGroups", "gemm_grouped",
-           "gemm_grouped_wgrad", "gemm_lora", "check_device", "raw_call", "TmmError"]
+           "window_sum_f32", "sum_f32", "softmax_rows_f32", "check_device", "raw_call",
+           "TmmError"]
 
 
 _GROUPED = ("group_rows", "RowGroups", "gemm_grouped", "gemm_grouped_wgrad", "gemm_lora")
@@ -37,6 +39,10 @@ def __getattr__(name):
         globals().update({n: getattr(grouped, n) for n in _GROUPED})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted({*globals(), *_GROUPED})
 
 
 def _matrix(x, name, allow_transposed=False):
