@@ -27,3 +27,29 @@ def test_star_import_loads_neither_torch_nor_a_library(tmp_path):
                  "assert {'gemm_grouped', 'group_rows', 'gemm_lora'} <= set(dir(tmm))\n"
                  "assert tmm.__file__.startswith(%r)" % str(tmp_path), tmp_path)
     assert run.returncode == 0, run.stderr
+
+
+def test_the_library_is_built_without_the_headers_of_python(tmp_path, monkeypatch):
+    from tiled_matrix_multiply_gb300 import build
+    built = []
+    monkeypatch.setattr(build, "_build", lambda path, *_: built.append(path) or path)
+    monkeypatch.setattr(build.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    assert build.build(force=True) == build.LIB_PATH
+    assert built == [build.LIB_PATH]
+
+
+def test_calls_go_through_ctypes_where_the_module_cannot_be_built(tmp_path):
+    code = ("import sys; sys.path.insert(0, %r)\n"
+            "from tiled_matrix_multiply_gb300 import build\n"
+            "build.build()\n"
+            "build.CALL_PATH += '.absent'\n"
+            "build.sysconfig.get_paths = lambda: {'include': '/nowhere'}\n"
+            "import torch, tiled_matrix_multiply_gb300 as tmm\n"
+            "i = torch.zeros(3, dtype=torch.int32)\n"
+            "for fn, args in ((tmm.group_rows, (i, 2)), (tmm.gemm_grouped, (i, i, i)),\n"
+            "                 (tmm.gemm_grouped_wgrad, (i, i, i)), (tmm.gemm_lora, (i,) * 6)):\n"
+            "    try: fn(*args)\n"
+            "    except (TypeError, ValueError): pass\n"
+            "    else: raise AssertionError(fn)\n" % ROOT)
+    run = python(code, tmp_path)
+    assert run.returncode == 0, run.stderr

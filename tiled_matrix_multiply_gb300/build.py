@@ -106,6 +106,12 @@ def _build(lib_path: str, build_dir: str, extra: list[str]) -> str:
     return lib_path
 
 
+def call_buildable() -> bool:
+    """Whether Python's headers are here: without them the grouped operators are called through
+    ctypes, and the C library is built all the same."""
+    return os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))
+
+
 def build_call(force: bool = False) -> str:
     """Build the marshalling module with the C compiler unless an up-to-date copy exists."""
     header = os.path.join(INCLUDE, "tmm_gemm.h")
@@ -125,12 +131,13 @@ def build_call(force: bool = False) -> str:
 
 
 def build(force: bool = False, extra_flags: list[str] | None = None) -> str:
-    """Build libtmm_gemm.so (and the marshalling module) unless up-to-date copies exist; return
-    the library's path."""
-    build_call(force)
-    if not force and not extra_flags and is_fresh():
-        return LIB_PATH
-    return _build(LIB_PATH, BUILD_DIR, list(extra_flags or []))
+    """Build libtmm_gemm.so (and the marshalling module, where Python's headers are) unless
+    up-to-date copies exist; return the library's path."""
+    if force or extra_flags or not is_fresh():
+        _build(LIB_PATH, BUILD_DIR, list(extra_flags or []))
+    if call_buildable():
+        build_call(force)
+    return LIB_PATH
 
 
 def build_checked(force: bool = False) -> str:

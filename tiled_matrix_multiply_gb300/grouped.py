@@ -156,9 +156,21 @@ def _scratch(need, like):
     return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
 
 
+class _NoCall:
+    """In the marshalling module's place where it cannot be built: every call is an unusual one."""
+
+    @staticmethod
+    def group_rows(*_):
+        return None
+
+    grouped = wgrad = lora = group_rows
+
+
 def _load_call():
     """The module that takes the usual calls (csrc/grouped_call.c), handed what it needs."""
     if not os.path.exists(_build.CALL_PATH):
+        if not _build.call_buildable():
+            return _NoCall
         raise RuntimeError(f"{_build.CALL_PATH} is missing: build it with "
                            "tiled_matrix_multiply_gb300.build.build()")
     loader = importlib.machinery.ExtensionFileLoader("grouped_call", _build.CALL_PATH)
