@@ -53,3 +53,12 @@ def test_calls_go_through_ctypes_where_the_module_cannot_be_built(tmp_path):
             "    else: raise AssertionError(fn)\n" % ROOT)
     run = python(code, tmp_path)
     assert run.returncode == 0, run.stderr
+
+
+def test_the_module_is_named_for_its_interpreter():
+    import importlib.machinery
+    from tiled_matrix_multiply_gb300 import build
+    name = os.path.basename(build.CALL_PATH)
+    suffix = name[len("grouped_call"):]
+    assert name.startswith("grouped_call.") and suffix in importlib.machinery.EXTENSION_SUFFIXES
+    assert sys.implementation.cache_tag.replace("-", "") in suffix.replace("-", "")

@@ -19,9 +19,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libtmm_gemm.so")
-# The CPython module that marshals the grouped operators' usual calls (csrc/grouped_call.c).
+# The CPython module that marshals the grouped operators' usual calls (csrc/grouped_call.c), named for
+# the interpreter that it is built for: another one builds its own.
 CALL_SOURCE = os.path.join(CSRC, "grouped_call.c")
-CALL_PATH = os.path.join(LIB_DIR, "grouped_call.so")
+CALL_PATH = os.path.join(LIB_DIR, "grouped_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 # The bounds-checked debug build (every global address and shared-memory offset
 # of the product kernels range-checked, see csrc/bounds_check.cuh): its own
 # objects and library, beside the normal ones.
