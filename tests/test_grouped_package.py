@@ -62,3 +62,83 @@ def test_the_module_is_named_for_its_interpreter():
     suffix = name[len("grouped_call"):]
     assert name.startswith("grouped_call.") and suffix in importlib.machinery.EXTENSION_SUFFIXES
     assert sys.implementation.cache_tag.replace("-", "") in suffix.replace("-", "")
+
+
+BLOCKING = """
+#include <stddef.h>
+#include <time.h>
+/* Stands for every entry point (the callers of both kinds pass integers and pointers only). */
+int blocking(void) {
+  struct timespec t = {0, 400 * 1000 * 1000};
+  nanosleep(&t, NULL);
+  return 0;
+}
+size_t no_workspace(void) { return 0; }
+"""
+
+
+class FakeTensor:
+    """What the marshalling module asks of a CUDA tensor; its memory is never touched."""
+    is_cuda, device = True, "cuda:0"
+
+    def __init__(self, *shape, dtype):
+        self.shape, self.dtype = shape, dtype
+
+    def stride(self):
+        out, step = [], 1
+        for n in reversed(self.shape):
+            out.insert(0, step)
+            step *= n
+        return tuple(out)
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return 0x7F0000001000
+
+
+def test_other_threads_run_while_a_call_blocks(tmp_path):
+    # The module handed an entry point that sleeps: a thread that counts goes on meanwhile.
+    import ctypes
+    import importlib.util
+    import shutil
+    import threading
+    import time
+    from tiled_matrix_multiply_gb300 import build
+    source, lib = tmp_path / "blocking.c", tmp_path / "blocking.so"
+    source.write_text(BLOCKING)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(lib), str(source)], check=True)
+    # A copy: the module's functions are its own, not those of the package's.
+    copy = shutil.copy(build.build_call(), tmp_path / "copied.so")
+    spec = importlib.util.spec_from_file_location("grouped_call", copy)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    fake = ctypes.CDLL(str(lib))
+    entry = ctypes.cast(fake.blocking, ctypes.c_void_p).value
+    size = ctypes.cast(fake.no_workspace, ctypes.c_void_p).value
+    module.start((FakeTensor, lambda shape, dtype, device: FakeTensor(*shape, dtype=dtype),
+                  lambda device: 0, lambda: 0, lambda *a: a, "u8", "i32", "i64", "f32", "f32",
+                  "bf16", "f16"), (entry, size) * 4)
+
+    def t(*shape, dtype="f32"):
+        return FakeTensor(*shape, dtype=dtype)
+    off, i = t(3, dtype="i32"), t(4, 1, dtype="i32")
+    calls = [lambda: module.group_rows(i, 2), lambda: module.grouped(t(4, 8), t(2, 8, 8), off, None),
+             lambda: module.wgrad(t(4, 8), t(4, 8), off, None),
+             lambda: module.lora(t(4, 8), t(8, 8), t(2, 8, 2), t(2, 2, 8), t(2), off, None)]
+    for call in calls:
+        stop, ticks = threading.Event(), []
+
+        def count():
+            while not stop.wait(0.02):
+                ticks.append(time.perf_counter())
+        thread = threading.Thread(target=count)
+        thread.start()
+        began = time.perf_counter()
+        assert call() is not None
+        ended = time.perf_counter()
+        stop.set()
+        thread.join()
+        assert ended - began >= 0.4
+        assert sum(began < at < ended for at in ticks) >= 3

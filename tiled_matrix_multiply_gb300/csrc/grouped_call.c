@@ -148,6 +148,13 @@ static int scratch(size_t need, PyObject *device, PyObject **ws, void **p) {
   return *p != NULL;
 }
 
+/* rc = call, with the interpreter's lock released: a launch may block, on a full queue or while its
+ * kernel is loaded, and holds only this call's own values. */
+#define WITHOUT_LOCK(call)                  \
+  int rc;                                   \
+  Py_BEGIN_ALLOW_THREADS rc = (call);       \
+  Py_END_ALLOW_THREADS
+
 /* None, with no error set: the caller's Python path takes over (and meets the error itself). */
 static PyObject *other(PyObject *a, PyObject *b, PyObject *c) {
   Py_XDECREF(a);
@@ -180,9 +187,9 @@ static PyObject *grouped(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   if (device == NULL || !scratch(need, device, &ws, &wp)) return other(device, ws, NULL);
   y = empty(Py_BuildValue("(LL)", (long long)R, (long long)w.cols), x.type, device);
   if (y == NULL || (yp = pointer(y)) == NULL) return other(device, ws, y);
-  if (f_grouped(x.code, w.trans, w.count, R, w.cols, x.cols, x.ptr, x.rows, x.ld, off.ptr, index,
-                w.ptr, w.ld, w.stride, yp, w.cols, wp, need, s) != TMM_OK)
-    return other(device, ws, y);
+  WITHOUT_LOCK(f_grouped(x.code, w.trans, w.count, R, w.cols, x.cols, x.ptr, x.rows, x.ld, off.ptr,
+                         index, w.ptr, w.ld, w.stride, yp, w.cols, wp, need, s))
+  if (rc != TMM_OK) return other(device, ws, y);
   Py_DECREF(device);
   Py_XDECREF(ws);
   return y;
@@ -211,9 +218,9 @@ static PyObject *wgrad(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   if (device == NULL || !scratch(need, device, &ws, &wp)) return other(device, ws, NULL);
   dw = empty(Py_BuildValue("(LLL)", (long long)groups, (long long)K, (long long)N), x.type, device);
   if (dw == NULL || (dwp = pointer(dw)) == NULL) return other(device, ws, dw);
-  if (f_wgrad(x.code, groups, dy.rows, N, K, x.ptr, x.rows, x.ld, off.ptr, index, dy.ptr, dy.ld,
-              dwp, N, K * N, wp, need, s) != TMM_OK)
-    return other(device, ws, dw);
+  WITHOUT_LOCK(f_wgrad(x.code, groups, dy.rows, N, K, x.ptr, x.rows, x.ld, off.ptr, index, dy.ptr,
+                       dy.ld, dwp, N, K * N, wp, need, s))
+  if (rc != TMM_OK) return other(device, ws, dw);
   Py_DECREF(device);
   Py_XDECREF(ws);
   return dw;
@@ -246,10 +253,10 @@ static PyObject *lora(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   if (device == NULL || !scratch(need, device, &ws, &wp)) return other(device, ws, NULL);
   y = empty(Py_BuildValue("(LL)", (long long)T, (long long)N), x.type, device);
   if (y == NULL || (yp = pointer(y)) == NULL) return other(device, ws, y);
-  if (f_lora(x.code, w.trans, la.trans, lb.trans, la.count, T, N, K, r, x.ptr, x.ld, off.ptr, index,
-             w.ptr, w.ld, la.ptr, la.ld, la.stride, lb.ptr, lb.ld, lb.stride, scale.ptr, yp, N, wp,
-             need, s) != TMM_OK)
-    return other(device, ws, y);
+  WITHOUT_LOCK(f_lora(x.code, w.trans, la.trans, lb.trans, la.count, T, N, K, r, x.ptr, x.ld, off.ptr,
+                      index, w.ptr, w.ld, la.ptr, la.ld, la.stride, lb.ptr, lb.ld, lb.stride,
+                      scale.ptr, yp, N, wp, need, s))
+  if (rc != TMM_OK) return other(device, ws, y);
   Py_DECREF(device);
   Py_XDECREF(ws);
   return y;
@@ -281,9 +288,11 @@ static PyObject *group_rows_(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     out[i] = empty(Py_BuildValue("(L)", (long long)(i == 0 ? groups + 1 : slots)), t_int32, device);
     ok = out[i] != NULL && (p[i] = pointer(out[i])) != NULL;
   }
-  if (ok && f_group_rows(tokens, fan, groups, x.ptr, x.type == t_int64 ? 64 : 32, p[0], p[1], p[2],
-                         p[3], wp, need, s) == TMM_OK)
-    r = PyObject_Vectorcall(t_row_groups, out, 4, NULL);
+  if (ok) {
+    WITHOUT_LOCK(f_group_rows(tokens, fan, groups, x.ptr, x.type == t_int64 ? 64 : 32, p[0], p[1],
+                              p[2], p[3], wp, need, s))
+    if (rc == TMM_OK) r = PyObject_Vectorcall(t_row_groups, out, 4, NULL);
+  }
   for (int i = 0; i < 4; ++i) Py_XDECREF(out[i]);
   if (r == NULL) return other(device, ws, NULL);
   Py_DECREF(device);
