@@ -7,6 +7,10 @@ if ROOT not in sys.path:
 HERE = os.path.dirname(os.path.abspath(__file__))
 if HERE not in sys.path:
     sys.path.insert(0, HERE)
+# The examples, which tests import: whichever runs first, or alone.
+EXAMPLES = os.path.join(ROOT, "examples")
+if EXAMPLES not in sys.path:
+    sys.path.append(EXAMPLES)
 
 
 def pytest_configure(config):

@@ -1,4 +1,4 @@
-"""Infinite entries in single precision: results are infinite, or NaN, where the definition's are."""
+"""Infinite entries: results are infinite, or NaN, where the definition's are."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -36,17 +36,18 @@ def same(got, want):
 SIZES = [([3, 0, 2], 700, 72), ([3, 2], 200, 136), ([60, 200], 300, 264), ([600, 513], 200, 264)]
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=str)
 @pytest.mark.parametrize("sizes,K,N", SIZES)
 @pytest.mark.parametrize("share", [0.0005, 0.02])
-def test_infinite_entries(sizes, K, N, share):
+def test_infinite_entries(sizes, K, N, share, dtype):
     gen = torch.Generator().manual_seed(K + N)
     R = sum(sizes)
     off = torch.tensor([0] + sizes).cumsum(0).to(torch.int32)
     x, w, dy = (plant(gen, ints(gen, *s), share) for s in ((R, K), (len(sizes), K, N), (R, N)))
-    y = tmm.gemm_grouped(x.float().cuda(), w.float().cuda(), off.cuda()).cpu()
-    same(y, ref.grouped(x, w, off).float())
-    dw = tmm.gemm_grouped_wgrad(x.float().cuda(), dy.float().cuda(), off.cuda()).cpu()
-    same(dw, ref.wgrad(x, dy, off).float())
+    y = tmm.gemm_grouped(x.to(dtype).cuda(), w.to(dtype).cuda(), off.cuda()).cpu()
+    same(y, ref.grouped(x, w, off).to(dtype))
+    dw = tmm.gemm_grouped_wgrad(x.to(dtype).cuda(), dy.to(dtype).cuda(), off.cuda()).cpu()
+    same(dw, ref.wgrad(x, dy, off).to(dtype))
     tmm.check_device()
 
 
