@@ -46,16 +46,17 @@
 // one issues the products.  Every wait is bounded (globaltimer); on timeout bit 1 of the status word
 // is set and the kernel runs to its end.
 //
-// Measured (times with every launch of the call, rates of the measured 6780 GB/s and 1936 TFLOP/s):
-//   16384 rows in 8 groups, 4096 x 4096, bf16: 357 us, 1.54 PFLOP/s (80 %); the product alone 314,
-//     the rest gathers the rows.  Bound by the tensor cores (active 81 % of the product's cycles).
-//   its gradient with 8192 rows: 198 us, 1.39 PFLOP/s (72 %), product 178: the tensor cores, and
+// Measured (a call's kernels, three sets of inputs by turns; rates of the measured 6780 GB/s and 1936
+// TFLOP/s; "product": that kernel alone, nothing in the caches):
+//   16384 rows in 8 groups, 4096 x 4096, bf16: 381 us, 1.44 PFLOP/s (75 %); the product 312, a gather
+//     of the rows before it 44.  Bound by the tensor cores (active 82 % of the product's cycles).
+//   its gradient with 8192 rows: 210 us, 1.31 PFLOP/s (68 %), product 182: the tensor cores (67 %), and
 //     268 MB of results, which no products cover where a group has few rows.
-//   two rows of two groups, 4096 x 4096: 15.2 us, 65 % of the 9.9 us that 67 MB take: the first
+//   two rows of two groups, 4096 x 4096: 15.8 us, 63 % of the 9.9 us that 67 MB take: the first
 //     bytes come 4 us after the start, and the blocks meet to add their parts.
-//   one row with its adapter, 4096 x 4096: 11.4 us against 5.0 for 34 MB: as above.
-//   4096 rows with 6 adapters of rank 16, 4096 x 4096, fp16: 129 us; the product 95, of which 84 are
-//     four rounds of tiles on 76 pairs where 3.6 would do.
+//   one row with its adapter, 4096 x 4096: 12.0 us against 5.0 for 34 MB: as above.
+//   4096 rows with 6 adapters of rank 64, 4096 x 4096, fp16: 128 us; the product 100 (tensor cores 65
+//     %): four rounds of tiles on 76 pairs where 3.6 would do.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -607,8 +608,8 @@ __device__ __forceinline__ void split8(const float (&x)[8], uint32_t (&h)[3][4])
 // values, u's 24 bits and FP32's range (a pair of FP16 values is infinite above 65504 and has fewer
 // than 17 bits below 2^-8; the number of rows, which decides how u is made, would decide that).  The
 // fourth part is the first with zero in place of an infinity, for the products with b's second
-// part, which is zero as a rule.  Measured, 4096 x 4096, FP16, rank 64: 4096 rows of 6 adapters 141
-// us (with a pair of FP16 values 134), of 64 adapters 197 us (170).
+// part, which is zero as a rule.  Measured, 4096 x 4096, rank 64, FP16 and BF16: 4096 rows of 6
+// adapters 130 us and 122 us, of 64 adapters 178 us and 154 us.
 //
 // Parts of columns n to n + 3 (n % 4 = 0) of a row from one thread.
 __device__ __forceinline__ uint2 pack4(const uint16_t (&h)[4][4], int i) {
@@ -2436,8 +2437,12 @@ int out_type(int dtype) {
 int box_of(int cg) { return cg == 2 ? 32 : 16; }
 int columns_of(int cg, int planes) { return cg == 1 ? 64 : planes == 3 ? 128 : 256; }
 
+// A GB300's SMs and pairs of them: the rules that give workspace sizes are asked without a device.
+constexpr int64_t kSms = 152, kPairs = kSms / 2;
+
 // Blocks that share a tile's sum: the largest power of two up to eight that leaves every block
-// enough slices to pay for meeting, about 3 us, and the cluster's blocks resident together.  16
+// enough slices to pay for meeting, about 3 us, and needs no more blocks than there are SMs (where a
+// GPC's SMs are not a multiple of the cluster some of them wait, which is slower, not wrong).  16
 // slices of 16-bit operands take about that long (K = 512 in two groups of 32 rows, N = 320: 9.7 us
 // shared by two, 6.6 us not), four of split ones (64 rows of K = 1000, N = 2047 with adapters: 48 us
 // not shared, 27 us by four).
@@ -2457,7 +2462,6 @@ int split_of(int64_t tiles, int64_t slices, int planes, const DeviceInfo &dev) {
 // columns 51 us, 256 40 us.)
 template <typename Tiles>
 int pair_columns(int planes, Tiles most) {
-  constexpr int64_t kPairs = 76;
   const int widest = columns_of(2, planes);
   for (int n = 64; n < widest; n *= 2)
     if (most(n) <= kPairs) return n;
@@ -2473,7 +2477,6 @@ int pair_columns(int planes, Tiles most) {
 // groups 406 us and 275 us.)
 int forward_shape(int64_t rows, int64_t groups, int64_t N, int64_t K, int dtype) {
   if (N <= 128) return 1;      // 256 lanes would be half empty
-  constexpr int64_t kSms = 152;
   const bool f32 = dtype == TMM_F32;
   const int64_t live = std::max<int64_t>(1, std::min(groups, rows));
   const int64_t each = (rows + live - 1) / live, slices = (K + kBK - 1) / kBK;
@@ -2504,14 +2507,20 @@ int forward_shape(int64_t rows, int64_t groups, int64_t N, int64_t K, int dtype)
 int lora_shape(const LoraProblem &p) {
   if (p.rows <= 64) return 1;
   if (p.rows > kFewRows || p.rows * p.rank > 8192) return 2;
-  constexpr int64_t kSms = 152;
   const bool f32 = p.dtype == TMM_F32;
   const int64_t tiles = (p.rows + 63) / 64 * ((p.N + 127) / 128);
   if (tiles <= (!f32 ? kSms : p.K % 8 == 0 && p.N % 8 == 0 ? kSms / 2 : kSms / 4)) return 1;
   if (f32 && p.rows > 256) return 2;
   const int64_t width = f32 ? 128 : 256, columns = p.rows + 24 * std::min(p.groups, p.rows);
-  return (columns + width - 1) / width * ((p.N + 255) / 256) > kSms / 2 ? 1 : 2;
+  return (columns + width - 1) / width * ((p.N + 255) / 256) > kPairs ? 1 : 2;
 }
+// Gradient: pairs where results fill more than 128 lanes, whatever the rows.  (Single blocks and pairs,
+// groups x rows and K x N: BF16 8 x 1024, 4096 x 136 41 us and 19 us, 4096 x 320 53 us and 28 us; 32 x
+// 64, 2048 x 192 20 us and 15 us, 2048 x 515 83 us and 52 us; 64 x 16, 1024 x 256 21 us and 15 us; FP32
+// the same 212 us and 128 us, 313 us and 164 us, 49 us and 40 us, 134 us and 88 us, 49 us and 33 us.  At
+// N = 128, where half of a pair's lanes are empty, few rows a group are faster on single blocks: 32 x
+// 64, 2048 12.0 us and 14.7 us, FP32 27 us and 35 us; and many are not: 8 x 1024, 4096 22 us and 17
+// us, FP32 131 us and 122 us.)
 int wgrad_shape(int64_t N) { return N > 128 ? 2 : 1; }
 
 // The maps of x: rows by number; or tiles of box_of rows, and (pairs) of a whole block's columns.
