@@ -528,6 +528,92 @@ size_t gemm_lora_workspace_size(int dtype, int transw, int transa, int transb, i
                                 const void *w, int64_t ldw, const void *a, int64_t lda,
                                 int64_t stride_a, const void *b, int64_t ldb, int64_t stride_b);
 
+/*
+ * Routing to experts: which experts a token's row goes to, and with what weight.  Element types of
+ * the logits as above; weights and the bias are FP32.
+ */
+#define TMM_SOFTMAX 0
+#define TMM_SIGMOID 1
+#define TMM_MAX_EXPERTS 512
+#define TMM_MAX_FAN 16
+#define TMM_MAX_ROUTE_GROUPS 32
+
+/*
+ * route_rows -- the k best experts of every token.  With s = softmax or sigmoid (score) of the row's
+ * `experts` logits and c = s + bias (bias NULL: c = s),
+ *   - the experts are `groups` groups of equal size after one another; a group's value is the sum of
+ *     its group_best (1 or 2) largest c, and the top_groups best groups stay (ties: the lower
+ *     number; top_groups == groups: all);
+ *   - chosen[t, j] is the expert with the j-th largest c among them (ties: the lower number);
+ *   - weights[t, j] = scale s_j / (the sum of the chosen s), or (renormalise = 0) scale s_j.
+ * The choice is that of the scores in 64 bits; without a bias it is the logits' own order.  The
+ * renormalised weights do not underflow: they are right where every score is below FP32's range.  An
+ * expert whose logit or bias is -inf is never chosen; where fewer than k are left (none, in a row of
+ * padding), the last chosen are -1 with weight 0, slots of no group for group_rows.  A row with NaN,
+ * or under the softmax with +inf, has NaN weights and chooses some k experts, each once.
+ * logits: DEVICE, tokens x experts, row stride ld >= experts; chosen, weights: tokens x k, contiguous.
+ * 1 <= experts <= 512, groups <= 32 dividing experts, k <= 16 and <= the experts of top_groups
+ * groups, tokens below 2^29.  tokens == 0 is a no-op.  Outputs must not overlap inputs or each
+ * other.  Asynchronous on `stream`, one launch, no allocation, no workspace, deterministic, any number
+ * of calls at once.
+ */
+int route_rows(int dtype, int64_t tokens, int64_t experts, const void *logits, int64_t ld,
+               const float *bias, int score, int64_t groups, int64_t top_groups, int group_best,
+               int64_t k, int renormalise, float scale, int32_t *chosen, float *weights,
+               tmm_stream_t stream);
+
+/*
+ * route_rows_grad -- the gradient of route_rows' weights with respect to the logits, the choice held
+ * fixed: dlogits[t, e] = sum_j dweights[t, j] d weights[t, j] / d logits[t, e], in FP32, rounded once.
+ * chosen as route_rows gave it; a number outside [0, experts) has no part, and one that comes twice
+ * adds twice.  dlogits: tokens x experts of the logits' type, every entry written; it may be logits
+ * itself (with ldd == ld).  Otherwise as route_rows.
+ */
+int route_rows_grad(int dtype, int64_t tokens, int64_t experts, int64_t k, const float *dweights,
+                    const void *logits, int64_t ld, const int32_t *chosen, int score,
+                    int renormalise, float scale, void *dlogits, int64_t ldd,
+                    tmm_stream_t stream);
+
+#define TMM_MAX_TOP 32
+
+/*
+ * logprob_rows -- log probabilities under the softmax of every row of x = scale * logits:
+ *   lse[r]      log sum_v e^x[r, v];
+ *   logprob[r]  x[r, tokens[r]] - lse[r]; 0 for a token outside [0, cols) (padding);
+ *   entropy[r]  - sum_v p_v log p_v;
+ *   top_ids[r, j], top_logprobs[r, j]  the j-th most probable v and its log probability, j < top
+ *               (ties: the lower number).
+ * The logits are read once; sums are FP32.  Entries of -inf have probability 0 and are no
+ * alternatives; where fewer than `top` others are left the last ids are -1, with -inf.  A row of
+ * nothing else has lse and logprob -inf and entropy 0.  A row with NaN or +inf has NaN everywhere, and
+ * ids of -1.  Masks of the type's lowest finite value count as that value.
+ * logits: DEVICE, rows x cols, row stride ld >= cols, no alignment beyond the type's (any cols).
+ * tokens: DEVICE, integers of token_bits (32 or 64) bits, or NULL (logprob NULL too).  scale > 0;
+ * 0 <= top <= 32 (0: top_ids and top_logprobs may be NULL); rows and cols below 2^29.  Outputs must
+ * not overlap inputs or each other.  Asynchronous on `stream`, one launch, no allocation, no
+ * workspace, deterministic, any number of calls at once.
+ */
+int logprob_rows(int dtype, int64_t rows, int64_t cols, const void *logits, int64_t ld,
+                 float scale, const void *tokens, int token_bits, int top, float *logprob,
+                 float *entropy, float *lse, int32_t *top_ids, float *top_logprobs,
+                 tmm_stream_t stream);
+
+/*
+ * logprob_rows_grad -- the gradient with respect to the logits:
+ *   dlogits[r, v] = scale (g ([v = t] - p_v) - h p_v (log p_v + H) + sum_j e_j ([v = id_j] - p_v)),
+ * t = tokens[r] (outside [0, cols): no such term), g = dlogprob[r], h = dentropy[r], H = entropy[r],
+ * e_j = dtop[r, j], id_j = top_ids[r, j] (outside [0, cols): no such term), p_v = e^(x - lse[r]).
+ * lse, entropy and top_ids as logprob_rows gave them.  dlogprob (with tokens), dentropy (with
+ * entropy) and, by top = 0, dtop may be left out (NULL).  A row without gradients, or with nothing
+ * visible (lse = -inf), gets zeros, whatever its logits.  dlogits: of the logits' type, every entry
+ * written, rounded once; it may be logits itself (with ldd == ld).  Otherwise as logprob_rows.
+ */
+int logprob_rows_grad(int dtype, int64_t rows, int64_t cols, const void *logits, int64_t ld,
+                      float scale, const float *lse, const void *tokens, int token_bits,
+                      const float *dlogprob, const float *entropy, const float *dentropy, int top,
+                      const int32_t *top_ids, const float *dtop, void *dlogits, int64_t ldd,
+                      tmm_stream_t stream);
+
 /* One-line description of the calling thread's last failed call ("" if none).
  * The string is owned by the library and valid until the thread's next call. */
 const char *tmm_last_error_string(void);

@@ -14,35 +14,43 @@ through torch unless one is passed).  ``window_sum_f32``, ``sum_f32`` and
 ``softmax_rows_f32`` are the other tiled workloads of the same pages (sliding
 window sums, the array reduction, the two-pass row softmax).  ``group_rows``,
 ``gemm_grouped``, ``gemm_grouped_wgrad`` and ``gemm_lora`` (``grouped.py``) are
-products whose right-hand matrix is chosen row by row.  All are
-asynchronous on the current torch stream of the operands' device.
+products whose right-hand matrix is chosen row by row; ``route_rows``
+(``scores.py``) chooses the experts that they are grouped by, ``gemm_bias_act``
+(``linear.py``) is the product with one matrix for all rows, bias, activation
+and residual in its epilogue, and ``logprob_rows`` (``scores.py``) reads the
+last one's logits; each has its gradient beside it.  All are asynchronous on the current torch stream of the operands' device.
 """
 from __future__ import annotations
 
 from ._abi import (TMM_ERR_ALIAS, TMM_ERR_CUDA, TMM_ERR_INVALID_ARG,  # noqa: F401
                    TMM_ERR_UNSUPPORTED_DEVICE, TMM_OK, TmmError)
 
-# What `from ... import *` takes: names that are there without torch or a built library.  The grouped
-# operators are attributes of the package beside them (see __getattr__).
+# What `from ... import *` takes: names that are there without torch or a built library.  The
+# operators on torch tensors of several types are attributes beside them (see __getattr__).
 __all__ = ["gemm_f32", "gemm_f32_naive", "gemm_f32_tc3", "tc3_workspace_bytes",
            "window_sum_f32", "sum_f32", "softmax_rows_f32", "check_device", "raw_call",
            "TmmError"]
 
 
 _GROUPED = ("group_rows", "RowGroups", "gemm_grouped", "gemm_grouped_wgrad", "gemm_lora")
+_SCORES = ("route_rows", "RowRoutes", "route_rows_grad", "logprob_rows", "RowLogprobs",
+           "logprob_rows_grad")
+_MODULES = {"grouped": _GROUPED, "scores": _SCORES}
 
 
 def __getattr__(name):
-    # The grouped operators' module imports torch when it is loaded; the package itself does not.
-    if name in _GROUPED:
-        from . import grouped
-        globals().update({n: getattr(grouped, n) for n in _GROUPED})
-        return globals()[name]
+    # These operators' modules import torch when they are loaded; the package itself does not.
+    for module, names in _MODULES.items():
+        if name in names:
+            import importlib
+            loaded = importlib.import_module(f".{module}", __name__)
+            globals().update({n: getattr(loaded, n) for n in names})
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def __dir__():
-    return sorted({*globals(), *_GROUPED})
+    return sorted({*globals(), *(n for names in _MODULES.values() for n in names)})
 
 
 def _matrix(x, name, allow_transposed=False):

@@ -42,6 +42,9 @@ STATUS_NAMES = {
 TMM_F32, TMM_BF16, TMM_F16 = 0, 1, 2
 TMM_MAX_GROUPS = 512
 TMM_MAX_RANK = 1024
+# Scores and limits of the routing and of the log probabilities.
+TMM_SOFTMAX, TMM_SIGMOID = 0, 1
+TMM_MAX_EXPERTS, TMM_MAX_FAN, TMM_MAX_ROUTE_GROUPS, TMM_MAX_TOP = 512, 16, 32, 32
 
 # Entry points with the common product signature
 # (M, N, K, A, lda, B, ldb, C, ldc, stream) -> int.
@@ -55,6 +58,8 @@ EXPORTED = GEMM_ENTRY_POINTS + ("gemm_f32_ex", "gemm_f32_tc3", "gemm_f32_tc3_ex"
                                  "gemm_grouped", "gemm_grouped_workspace_size",
                                  "gemm_grouped_wgrad", "gemm_grouped_wgrad_workspace_size",
                                  "gemm_lora", "gemm_lora_workspace_size",
+                                 "route_rows", "route_rows_grad", "logprob_rows",
+                                 "logprob_rows_grad",
                                  "tmm_check_device", "tmm_testing_set_wait_hooks",
                                  "tmm_testing_simt_plan", "tmm_testing_tc3_plan",
                                  "tmm_last_error_string", "tmm_version",
@@ -139,6 +144,19 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.gemm_lora_workspace_size.argtypes = [ci, ci, ci, ci, i64, i64, i64, i64, i64, ptr, i64,
                                                  ptr, ptr, i64, ptr, i64, i64, ptr, i64, i64]
         lib.gemm_lora_workspace_size.restype = size
+        f32 = ctypes.c_float
+        lib.route_rows.argtypes = [ci, i64, i64, ptr, i64, ptr, ci, i64, i64, ci, i64, ci, f32, ptr,
+                                   ptr, ptr]
+        lib.route_rows.restype = ci
+        lib.route_rows_grad.argtypes = [ci, i64, i64, i64, ptr, ptr, i64, ptr, ci, ci, f32, ptr,
+                                        i64, ptr]
+        lib.route_rows_grad.restype = ci
+        lib.logprob_rows.argtypes = [ci, i64, i64, ptr, i64, f32, ptr, ci, ci, ptr, ptr, ptr, ptr,
+                                     ptr, ptr]
+        lib.logprob_rows.restype = ci
+        lib.logprob_rows_grad.argtypes = [ci, i64, i64, ptr, i64, f32, ptr, ptr, ci, ptr, ptr, ptr,
+                                          ci, ptr, ptr, ptr, i64, ptr]
+        lib.logprob_rows_grad.restype = ci
         lib.tmm_check_device.argtypes = [ptr]
         lib.tmm_check_device.restype = ctypes.c_int
         lib.tmm_testing_set_wait_hooks.argtypes = [ctypes.c_int, i64]

@@ -10,6 +10,7 @@
 
 #include "bounds_check.cuh"
 #include "grouped.h"
+#include "rows.h"
 #include "tmm_gemm.h"
 #include "tmm_internal.h"
 
@@ -818,6 +819,263 @@ int gemm_lora(int dtype, int transw, int transa, int transb, int64_t groups, int
   p.y = y;
   p.ldy = ldy;
   const cudaError_t e = tmm::launch_lora(p, dev, workspace, s);
+  if (e != cudaSuccess) return fail(TMM_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+  return TMM_OK;
+}
+
+// ---- rows of scores -----------------------------------------------------------------------
+
+namespace {
+
+// A row-major matrix of scores: rows below 2^29, as the grids and 32-bit columns need.
+int check_scores(const char *who, const char *name, int dtype, int64_t rows, int64_t cols,
+                 const void *data, int64_t ld) {
+  if (dtype != TMM_F32 && dtype != TMM_BF16 && dtype != TMM_F16)
+    return fail(TMM_ERR_INVALID_ARG, "%s: unknown dtype %d", who, dtype);
+  if (!extent_ok(rows) || !extent_ok(cols))
+    return fail(TMM_ERR_INVALID_ARG, "%s: sizes must be >= 0 and below 2^29 (%lld x %lld)", who,
+                (long long)rows, (long long)cols);
+  return check_stack(who, name, stack_of(data, 1, rows, cols, ld, 0), element_size(dtype));
+}
+
+int64_t scores_bytes(int dtype, int64_t rows, int64_t cols, int64_t ld) {
+  return stack_span(stack_of(nullptr, 1, rows, cols, ld, 0)) * element_size(dtype);
+}
+
+// Arrays of 4-byte values (or, with `size`, others): there and naturally aligned.
+int check_array(const char *who, const char *name, const void *p, int64_t n, int size = 4) {
+  if (n > 0 && p == nullptr) return fail(TMM_ERR_INVALID_ARG, "%s: %s is NULL", who, name);
+  if (reinterpret_cast<uintptr_t>(p) % unsigned(size))
+    return fail(TMM_ERR_INVALID_ARG, "%s: %s must be %d-byte aligned", who, name, size);
+  return TMM_OK;
+}
+
+int check_scale(const char *who, float scale, bool positive) {
+  if (!(scale - scale == 0.0f) || (positive && !(scale > 0.0f)))
+    return fail(TMM_ERR_INVALID_ARG, "%s: scale must be finite%s", who,
+                positive ? " and positive" : "");
+  return TMM_OK;
+}
+
+// The `outs` arrays first in `r` are written: each against all after it.
+int check_outputs(const char *who, const Bytes *r, int outs, int count) {
+  for (int i = 0; i < outs; ++i) {
+    if (r[i].p == nullptr) continue;
+    const int rc = check_alias(who, r + i, count - i);
+    if (rc != TMM_OK) return rc;
+  }
+  return TMM_OK;
+}
+
+int check_route(const char *who, int64_t tokens, int64_t experts, int64_t k, int score,
+                int renormalise) {
+  if (experts < 1 || experts > tmm::kMaxExperts)
+    return fail(TMM_ERR_INVALID_ARG, "%s: need 1 <= experts <= %d (experts=%lld)", who,
+                tmm::kMaxExperts, (long long)experts);
+  if (k < 1 || k > tmm::kMaxFan || k > experts)
+    return fail(TMM_ERR_INVALID_ARG, "%s: need 1 <= k <= min(%d, experts) (k=%lld)", who,
+                tmm::kMaxFan, (long long)k);
+  if (score != TMM_SOFTMAX && score != TMM_SIGMOID)
+    return fail(TMM_ERR_INVALID_ARG, "%s: unknown score %d", who, score);
+  if (renormalise != 0 && renormalise != 1)
+    return fail(TMM_ERR_INVALID_ARG, "%s: renormalise must be 0 or 1", who);
+  (void)tokens;
+  return TMM_OK;
+}
+
+int check_logprob(const char *who, int top, int token_bits, const void *tokens, float scale) {
+  if (top < 0 || top > tmm::kMaxTop)
+    return fail(TMM_ERR_INVALID_ARG, "%s: need 0 <= top <= %d (top=%d)", who, tmm::kMaxTop, top);
+  if (token_bits != 32 && token_bits != 64)
+    return fail(TMM_ERR_INVALID_ARG, "%s: token_bits must be 32 or 64", who);
+  if (reinterpret_cast<uintptr_t>(tokens) % unsigned(token_bits / 8))
+    return fail(TMM_ERR_INVALID_ARG, "%s: tokens must be naturally aligned", who);
+  return check_scale(who, scale, true);
+}
+
+}  // namespace
+
+int route_rows(int dtype, int64_t tokens, int64_t experts, const void *logits, int64_t ld,
+               const float *bias, int score, int64_t groups, int64_t top_groups, int group_best,
+               int64_t k, int renormalise, float scale, int32_t *chosen, float *weights,
+               tmm_stream_t stream) {
+  const char *who = "route_rows";
+  int rc;
+  if ((rc = check_scores(who, "logits", dtype, tokens, experts, logits, ld)) != TMM_OK ||
+      (rc = check_route(who, tokens, experts, k, score, renormalise)) != TMM_OK ||
+      (rc = check_scale(who, scale, false)) != TMM_OK)
+    return rc;
+  if (groups < 1 || groups > tmm::kMaxRouteGroups || experts % groups != 0 || top_groups < 1 ||
+      top_groups > groups)
+    return fail(TMM_ERR_INVALID_ARG, "%s: need groups <= %d that divide the experts, and 1 <= "
+                "top_groups <= groups (groups=%lld top_groups=%lld)", who, tmm::kMaxRouteGroups,
+                (long long)groups, (long long)top_groups);
+  if (group_best != 1 && group_best != 2)
+    return fail(TMM_ERR_INVALID_ARG, "%s: group_best must be 1 or 2", who);
+  if (k > experts / groups * top_groups)
+    return fail(TMM_ERR_INVALID_ARG, "%s: k=%lld experts of %lld in the chosen groups", who,
+                (long long)k, (long long)(experts / groups * top_groups));
+  if ((rc = check_array(who, "bias", bias, 0)) != TMM_OK ||
+      (rc = check_array(who, "chosen", chosen, tokens)) != TMM_OK ||
+      (rc = check_array(who, "weights", weights, tokens)) != TMM_OK)
+    return rc;
+  if (tokens == 0) return TMM_OK;
+  const Bytes all[4] = {{"chosen", chosen, tokens * k * 4},
+                        {"weights", weights, tokens * k * 4},
+                        {"logits", logits, scores_bytes(dtype, tokens, experts, ld)},
+                        {"bias", bias, experts * 4}};
+  if ((rc = check_outputs(who, all, 2, 4)) != TMM_OK) return rc;
+  tmm::DeviceInfo dev;
+  if ((rc = current_device(&dev)) != TMM_OK) return rc;
+  tmm::RouteProblem p = {};
+  p.dtype = dtype;
+  p.tokens = tokens;
+  p.experts = int(experts);
+  p.k = int(k);
+  p.logits = logits;
+  p.ld = ld;
+  p.bias = bias;
+  p.sigmoid = score == TMM_SIGMOID;
+  p.renormalise = renormalise;
+  p.groups = int(groups);
+  p.top_groups = int(top_groups);
+  p.best = group_best;
+  p.scale = scale;
+  p.chosen = chosen;
+  p.weights = weights;
+  const cudaError_t e = tmm::launch_route(p, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(TMM_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+  return TMM_OK;
+}
+
+int route_rows_grad(int dtype, int64_t tokens, int64_t experts, int64_t k, const float *dweights,
+                    const void *logits, int64_t ld, const int32_t *chosen, int score,
+                    int renormalise, float scale, void *dlogits, int64_t ldd,
+                    tmm_stream_t stream) {
+  const char *who = "route_rows_grad";
+  int rc;
+  if ((rc = check_scores(who, "logits", dtype, tokens, experts, logits, ld)) != TMM_OK ||
+      (rc = check_scores(who, "dlogits", dtype, tokens, experts, dlogits, ldd)) != TMM_OK ||
+      (rc = check_route(who, tokens, experts, k, score, renormalise)) != TMM_OK ||
+      (rc = check_scale(who, scale, false)) != TMM_OK ||
+      (rc = check_array(who, "dweights", dweights, tokens)) != TMM_OK ||
+      (rc = check_array(who, "chosen", chosen, tokens)) != TMM_OK)
+    return rc;
+  if (tokens == 0) return TMM_OK;
+  const bool in_place = dlogits == logits && ldd == ld;
+  const Bytes all[4] = {{"dlogits", dlogits, scores_bytes(dtype, tokens, experts, ldd)},
+                        {"dweights", dweights, tokens * k * 4},
+                        {"chosen", chosen, tokens * k * 4},
+                        {"logits", in_place ? nullptr : logits,
+                         scores_bytes(dtype, tokens, experts, ld)}};
+  if ((rc = check_outputs(who, all, 1, 4)) != TMM_OK) return rc;
+  tmm::DeviceInfo dev;
+  if ((rc = current_device(&dev)) != TMM_OK) return rc;
+  tmm::RouteGradProblem p = {};
+  p.dtype = dtype;
+  p.tokens = tokens;
+  p.experts = int(experts);
+  p.k = int(k);
+  p.dweights = dweights;
+  p.logits = logits;
+  p.ld = ld;
+  p.chosen = chosen;
+  p.sigmoid = score == TMM_SIGMOID;
+  p.renormalise = renormalise;
+  p.scale = scale;
+  p.dlogits = dlogits;
+  p.ldd = ldd;
+  const cudaError_t e = tmm::launch_route_grad(p, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(TMM_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+  return TMM_OK;
+}
+
+int logprob_rows(int dtype, int64_t rows, int64_t cols, const void *logits, int64_t ld,
+                 float scale, const void *tokens, int token_bits, int top, float *logprob,
+                 float *entropy, float *lse, int32_t *top_ids, float *top_logprobs,
+                 tmm_stream_t stream) {
+  const char *who = "logprob_rows";
+  int rc;
+  if ((rc = check_scores(who, "logits", dtype, rows, cols, logits, ld)) != TMM_OK ||
+      (rc = check_logprob(who, top, token_bits, tokens, scale)) != TMM_OK ||
+      (rc = check_array(who, "logprob", logprob, tokens ? rows : 0)) != TMM_OK ||
+      (rc = check_array(who, "entropy", entropy, rows)) != TMM_OK ||
+      (rc = check_array(who, "lse", lse, rows)) != TMM_OK ||
+      (rc = check_array(who, "top_ids", top_ids, rows * top)) != TMM_OK ||
+      (rc = check_array(who, "top_logprobs", top_logprobs, rows * top)) != TMM_OK)
+    return rc;
+  if (logprob != nullptr && tokens == nullptr && rows > 0)
+    return fail(TMM_ERR_INVALID_ARG, "%s: logprob without tokens", who);
+  if (rows == 0) return TMM_OK;
+  const Bytes all[7] = {{"logprob", logprob, rows * 4},
+                        {"entropy", entropy, rows * 4},
+                        {"lse", lse, rows * 4},
+                        {"top_ids", top_ids, rows * top * 4},
+                        {"top_logprobs", top_logprobs, rows * top * 4},
+                        {"logits", logits, scores_bytes(dtype, rows, cols, ld)},
+                        {"tokens", tokens, rows * (token_bits / 8)}};
+  if ((rc = check_outputs(who, all, 5, 7)) != TMM_OK) return rc;
+  tmm::DeviceInfo dev;
+  if ((rc = current_device(&dev)) != TMM_OK) return rc;
+  const tmm::LogprobProblem p = {dtype, rows,  cols,    logits,  ld,  tokens,  token_bits,
+                                 top,   scale, logprob, entropy, lse, top_ids, top_logprobs};
+  const cudaError_t e = tmm::launch_logprob(p, dev, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(TMM_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+  return TMM_OK;
+}
+
+int logprob_rows_grad(int dtype, int64_t rows, int64_t cols, const void *logits, int64_t ld,
+                      float scale, const float *lse, const void *tokens, int token_bits,
+                      const float *dlogprob, const float *entropy, const float *dentropy, int top,
+                      const int32_t *top_ids, const float *dtop, void *dlogits, int64_t ldd,
+                      tmm_stream_t stream) {
+  const char *who = "logprob_rows_grad";
+  int rc;
+  if ((rc = check_scores(who, "logits", dtype, rows, cols, logits, ld)) != TMM_OK ||
+      (rc = check_scores(who, "dlogits", dtype, rows, cols, dlogits, ldd)) != TMM_OK ||
+      (rc = check_logprob(who, top, token_bits, tokens, scale)) != TMM_OK ||
+      (rc = check_array(who, "lse", lse, rows)) != TMM_OK ||
+      (rc = check_array(who, "dlogprob", dlogprob, 0)) != TMM_OK ||
+      (rc = check_array(who, "tokens", tokens, dlogprob ? rows : 0)) != TMM_OK ||
+      (rc = check_array(who, "dentropy", dentropy, 0)) != TMM_OK ||
+      (rc = check_array(who, "entropy", entropy, dentropy ? rows : 0)) != TMM_OK ||
+      (rc = check_array(who, "top_ids", top_ids, rows * top)) != TMM_OK ||
+      (rc = check_array(who, "dtop", dtop, rows * top)) != TMM_OK)
+    return rc;
+  if (rows == 0 || cols == 0) return TMM_OK;
+  const bool in_place = dlogits == logits && ldd == ld;
+  const Bytes all[9] = {{"dlogits", dlogits, scores_bytes(dtype, rows, cols, ldd)},
+                        {"logits", in_place ? nullptr : logits,
+                         scores_bytes(dtype, rows, cols, ld)},
+                        {"lse", lse, rows * 4},
+                        {"tokens", tokens, rows * (token_bits / 8)},
+                        {"dlogprob", dlogprob, rows * 4},
+                        {"entropy", entropy, rows * 4},
+                        {"dentropy", dentropy, rows * 4},
+                        {"top_ids", top_ids, rows * top * 4},
+                        {"dtop", dtop, rows * top * 4}};
+  if ((rc = check_outputs(who, all, 1, 9)) != TMM_OK) return rc;
+  tmm::DeviceInfo dev;
+  if ((rc = current_device(&dev)) != TMM_OK) return rc;
+  tmm::LogprobGradProblem p = {};
+  p.dtype = dtype;
+  p.rows = rows;
+  p.cols = cols;
+  p.logits = logits;
+  p.ld = ld;
+  p.tokens = tokens;
+  p.token_bits = token_bits;
+  p.top = top;
+  p.scale = scale;
+  p.lse = lse;
+  p.entropy = entropy;
+  p.dlogprob = dlogprob;
+  p.dentropy = dentropy;
+  p.top_ids = top_ids;
+  p.dtop = top > 0 ? dtop : nullptr;
+  p.dlogits = dlogits;
+  p.ldd = ldd;
+  const cudaError_t e = tmm::launch_logprob_grad(p, dev, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(TMM_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
   return TMM_OK;
 }

@@ -151,6 +151,20 @@ def _try(lib, name, ws, s, args):
     return getattr(lib, name)(*args, ws.data_ptr(), ws.numel() * ws.element_size(), s)
 
 
+def _call_plain(name, like, *args):
+    """The same for an entry point without a workspace."""
+    device = like.get_device()
+    s = _raw_stream(device)
+    fn = getattr(_abi.load(), name)
+    if torch.cuda.current_device() == device:
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, s)
+    if rc != _abi.TMM_OK:
+        raise _abi.TmmError(name, rc, _abi.last_error())
+
+
 def _scratch(need, like):
     """A workspace of `need` bytes, None for 0 (torch's blocks start on 512-byte boundaries)."""
     return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
