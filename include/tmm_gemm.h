@@ -529,6 +529,51 @@ size_t gemm_lora_workspace_size(int dtype, int transw, int transa, int transb, i
                                 int64_t stride_a, const void *b, int64_t ldb, int64_t stride_b);
 
 /*
+ * A linear layer: the product with one matrix for all rows and what follows it, in one kernel's
+ * epilogue.  Element types, sums, rounding, alignment, workspaces and waits as for the grouped
+ * operators; sizes below 2^29.
+ */
+#define TMM_ACT_NONE 0
+#define TMM_ACT_RELU 1
+#define TMM_ACT_SILU 2          /* z / (1 + e^-z) */
+#define TMM_ACT_GELU 3          /* z/2 erfc(-z / sqrt 2) */
+#define TMM_ACT_GELU_TANH 4     /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+
+/*
+ * gemm_bias_act -- z = x w + bias,  y = act(z) + residual.
+ * x: M x K, ldx.  w: K x N, ldw >= N (transw = 0), or stored N x K, ldw >= K (transw = 1).  bias: N
+ * values of the operands' type or (bias_f32 = 1) of FP32, or NULL.  residual: M x N, ldr, or NULL.
+ * y: M x N, ldy; it may be residual itself (ldy == ldr).  pre: where z is kept (rounded to the
+ * type) for the gradients, M x N, ldpre, or NULL.  z is FP32 until then: y is rounded once.  K == 0
+ * gives z = bias; M == 0 or N == 0 is a no-op.
+ */
+int gemm_bias_act(int dtype, int transw, int act, int64_t M, int64_t N, int64_t K, const void *x,
+                  int64_t ldx, const void *w, int64_t ldw, const void *bias, int bias_f32,
+                  const void *residual, int64_t ldr, void *y, int64_t ldy, void *pre,
+                  int64_t ldpre, void *workspace, size_t workspace_bytes, tmm_stream_t stream);
+size_t gemm_bias_act_workspace_size(int dtype, int transw, int64_t M, int64_t N, int64_t K,
+                                    const void *x, int64_t ldx, const void *w, int64_t ldw);
+
+/*
+ * gemm_bias_act_grad -- with dz = dy act'(pre):
+ *     dx = dz w^T,  dw = x^T dz,  dbias[n] = sum_t dz[t, n];
+ * the gradient of the residual is dy itself.  Any of dx (M x K), dw (K x N, or with transdw = 1
+ * stored N x K) and dbias (N FP32) may be NULL.  pre as gemm_bias_act kept it (act none: may be
+ * NULL).  dz is FP32 in dbias; in the products it is rounded to the operands' type first, as a
+ * layer of its own would hand it on: for sums of many terms that adds about as much to a result's
+ * error as the result's own rounding.  relu'(0) = 0.  x is read for dw alone, w for dx alone.
+ */
+int gemm_bias_act_grad(int dtype, int transw, int act, int64_t M, int64_t N, int64_t K,
+                       const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *w,
+                       int64_t ldw, const void *pre, int64_t ldpre, void *dx, int64_t lddx,
+                       void *dw, int64_t lddw, int transdw, float *dbias, void *workspace,
+                       size_t workspace_bytes, tmm_stream_t stream);
+size_t gemm_bias_act_grad_workspace_size(int dtype, int transw, int act, int64_t M, int64_t N,
+                                         int64_t K, const void *dy, int64_t lddy, const void *x,
+                                         int64_t ldx, const void *w, int64_t ldw, const void *dx,
+                                         const void *dw, int transdw, const void *dbias);
+
+/*
  * Routing to experts: which experts a token's row goes to, and with what weight.  Element types of
  * the logits as above; weights and the bias are FP32.
  */

@@ -1,0 +1,321 @@
+"""Linear layers on the GPU, against their definitions in 64 bits.
+
+Integer inputs are exact in every type up to the one rounding of the result, so they are compared
+bit for bit; random inputs are held to the error bounds of linear_ref.
+"""
+import itertools
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import linear_ref as ref  # noqa: E402
+import tiled_matrix_multiply_gb300 as tmm  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from tiled_matrix_multiply_gb300 import build
+    build.build()
+
+
+def ints(seed, *shape, top=2):
+    gen = torch.Generator().manual_seed(seed)
+    return torch.randint(-top, top + 1, shape, generator=gen).double()
+
+
+def normals(seed, *shape, std=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    return torch.randn(*shape, generator=gen, dtype=torch.float64) * std
+
+
+def checked(fn, *a, **k):
+    out = fn(*a, **k)
+    tmm.check_device()
+    return out
+
+
+def on_gpu(t, dtype, trans=False):
+    if t is None:
+        return None
+    t = t.to(dtype)
+    return t.t().contiguous().cuda().t() if trans else t.cuda()
+
+
+def strided(t, ld, offset=0):
+    """The same matrix on the GPU with another row stride, off the start of its allocation."""
+    store = torch.full((offset + t.shape[0] * ld + 8,), float("nan"), dtype=t.dtype, device="cuda")
+    view = store[offset:offset + t.shape[0] * ld].view(t.shape[0], ld)[:, :t.shape[1]]
+    view.copy_(t)
+    return view
+
+
+SIZES = [(1, 1, 1), (1, 64, 64), (3, 130, 72), (2, 8, 1000), (17, 257, 65), (5, 1024, 2100),
+         (64, 520, 128), (65, 129, 333), (130, 256, 192), (257, 513, 96), (300, 1000, 40),
+         (700, 136, 200), (1000, 768, 72)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_integers_are_exact(dtype, trans, M, N, K):
+    x, w = ints(1, M, K), ints(2, K, N)
+    bias, res = ints(3, N, top=9), ints(4, M, N, top=9)
+    xd, wd = on_gpu(x, dtype), on_gpu(w, dtype, trans)
+    z = x @ w
+    y = checked(tmm.gemm_bias_act, xd, wd)
+    assert torch.equal(y.cpu(), z.to(dtype))
+    for kind, b32 in (("relu", True), ("none", False)):
+        b = bias.float().cuda() if b32 else on_gpu(bias, dtype)
+        y, pre = checked(tmm.gemm_bias_act, xd, wd, b, kind, on_gpu(res, dtype), pre=True)
+        assert torch.equal(pre.cpu(), (z + bias).to(dtype))
+        assert torch.equal(y.cpu(), (ref.act(z + bias, kind) + res).to(dtype))
+    y = checked(tmm.gemm_bias_act, xd, wd, residual=on_gpu(res, dtype))
+    assert torch.equal(y.cpu(), (z + res).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("kind", ref.ACTS)
+@pytest.mark.parametrize("M,N,K,trans", [(1, 512, 1024, True), (70, 515, 300, False),
+                                         (600, 384, 512, True), (9, 72, 8400, False)])
+def test_activations(dtype, kind, M, N, K, trans):
+    x = normals(1, M, K).to(dtype)
+    w = normals(2, K, N, std=2 * K ** -0.5).to(dtype)
+    bias, res = normals(3, N).float(), normals(4, M, N).to(dtype)
+    y, z = checked(tmm.gemm_bias_act, x.cuda(), on_gpu(w, dtype, trans), bias.cuda(), kind,
+                   res.cuda(), pre=True)
+    want_y, want_z, y_err, z_err = ref.forward(x, w, bias, kind, res)
+    ref.assert_close(z, want_z, z_err, "z")
+    ref.assert_close(y, want_y, y_err, "y")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("kind", ref.ACTS)
+def test_activations_over_their_range(dtype, kind):
+    """One term a sum: z takes every size, infinities and NaN among them."""
+    z = torch.cat([torch.linspace(-40, 40, 4001), torch.logspace(-30, 30, 121),
+                   -torch.logspace(-30, 30, 121), torch.tensor([0.0, -0.0])]).to(dtype)
+    z = z[torch.isfinite(z)]
+    x = z[:, None]
+    one = torch.ones(1, 24, dtype=dtype)
+    y = checked(tmm.gemm_bias_act, x.cuda(), one.cuda(), act=kind)
+    want, _, err, _ = ref.forward(x, one, None, kind, None)
+    ref.assert_close(y, want, err)
+    odd = torch.tensor([math.inf, -math.inf, math.nan], dtype=dtype)[:, None]
+    y = tmm.gemm_bias_act(odd.cuda(), one.cuda(), act=kind).cpu()
+    assert bool((y[0] == math.inf).all()) and bool(y[2].isnan().all())
+    dy = torch.ones(z.numel(), 24, dtype=dtype)
+    g = checked(tmm.gemm_bias_act_grad, dy.cuda(), None, one.cuda(),
+                pre=x.expand(-1, 24).contiguous().cuda(), act=kind, dw=False, dbias=True)
+    want, err = ref.backward(dy, torch.zeros(z.numel(), 1), one, x.expand(-1, 24), kind)
+    ref.assert_close(g.dx, want["dx"], err["dx"])
+    ref.assert_close(g.dbias, want["dbias"], err["dbias"])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_gradients_of_integers_are_exact(dtype, trans, M, N, K):
+    x, w, dy = ints(1, M, K), ints(2, K, N), ints(3, M, N)
+    z = ints(4, M, N, top=1)
+    for kind in ("none", "relu"):
+        g = checked(tmm.gemm_bias_act_grad, on_gpu(dy, dtype), on_gpu(x, dtype),
+                    on_gpu(w, dtype, trans), pre=on_gpu(z, dtype), act=kind, dbias=True)
+        dz = dy * ref.slope(z, kind)
+        assert torch.equal(g.dx.cpu(), (dz @ w.T).to(dtype))
+        assert torch.equal(g.dw.cpu(), (x.T @ dz).to(dtype))
+        assert torch.equal(g.dbias.cpu(), dz.sum(0).float())
+        assert (g.dw.stride(0) == 1) == trans or 1 in (N, K)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("kind", ref.ACTS)
+@pytest.mark.parametrize("M,N,K,trans", [(1, 512, 1024, True), (70, 515, 300, False),
+                                         (600, 384, 512, True), (8500, 72, 200, False)])
+def test_gradients(dtype, kind, M, N, K, trans):
+    x = normals(1, M, K).to(dtype)
+    w = normals(2, K, N, std=K ** -0.5).to(dtype)
+    dy, z = normals(3, M, N).to(dtype), normals(4, M, N, std=1.5).to(dtype)
+    g = checked(tmm.gemm_bias_act_grad, dy.cuda(), x.cuda(), on_gpu(w, dtype, trans), pre=z.cuda(),
+                act=kind, dbias=True)
+    want, err = ref.backward(dy, x, w, z, kind)
+    for name in ("dx", "dw", "dbias"):
+        ref.assert_close(getattr(g, name), want[name], err[name], name)
+
+
+@pytest.mark.parametrize("kind", ref.ACTS)
+def test_gradients_against_differences(kind):
+    M, N, K = 4, 6, 5
+    x, w, b = normals(1, M, K), normals(2, K, N, std=0.6), normals(3, N)
+    dy = normals(4, M, N)
+    x, w, b, dy = (t.float().double() for t in (x, w, b, dy))
+    y, z = tmm.gemm_bias_act(x.float().cuda(), w.float().cuda(), b.float().cuda(), kind, pre=True)
+    g = tmm.gemm_bias_act_grad(dy.float().cuda(), x.float().cuda(), w.float().cuda(), pre=z, act=kind,
+                               dbias=True)
+
+    def loss(x, w, b):
+        return float((ref.act(x @ w + b, kind) * dy).sum())
+
+    for got, at in ((g.dx, 0), (g.dw, 1), (g.dbias, 2)):
+        args = [x, w, b]
+        for i in range(args[at].numel()):
+            step = torch.zeros(args[at].numel(), dtype=torch.float64)
+            step[i] = 1e-5
+            up, down = list(args), list(args)
+            up[at] = args[at] + step.view_as(args[at])
+            down[at] = args[at] - step.view_as(args[at])
+            want = (loss(*up) - loss(*down)) / 2e-5
+            assert abs(want - float(got.reshape(-1)[i])) < 1e-4 * (1 + abs(want)), (kind, at, i)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("M", [3, 70, 300])
+@pytest.mark.parametrize("extra,offset", [(0, 1), (1, 0), (8, 8), (3, 5)])
+def test_strides(dtype, M, extra, offset):
+    N, K = 264, 136
+    x, w, dy = ints(1, M, K).to(dtype), ints(2, K, N).to(dtype), ints(3, M, N).to(dtype)
+    bias, res = ints(4, N).to(dtype), ints(5, M, N).to(dtype)
+    xs, ws, rs = (strided(t, t.shape[1] + extra, offset) for t in (x, w, res))
+    y, pre = (strided(torch.zeros_like(res), N + extra, offset) for _ in range(2))
+    b = torch.zeros(N + 8, dtype=dtype, device="cuda")[offset:offset + N].copy_(bias) \
+        if offset + N <= N + 8 else bias.cuda()
+    checked(tmm.gemm_bias_act, xs, ws, b, "relu", rs, y=y, pre=pre)
+    z = x.double() @ w.double() + bias.double()
+    assert torch.equal(pre.cpu(), z.to(dtype))
+    assert torch.equal(y.cpu(), (z.relu() + res.double()).to(dtype))
+    if extra:      # the gaps between rows are left alone
+        flat = y.as_strided((M - 1, extra), (N + extra, 1), y.storage_offset() + N)
+        assert bool(flat.isnan().all())
+    ds = strided(dy, N + extra, offset)
+    dx = strided(torch.zeros(M, K, dtype=dtype), K + extra, offset)
+    dw = strided(torch.zeros(K, N, dtype=dtype), N + extra, offset)
+    g = checked(tmm.gemm_bias_act_grad, ds, xs, ws, pre=pre, act="relu", dx=dx, dw=dw, dbias=True)
+    dz = dy.double() * (z.to(dtype).double() > 0)
+    assert torch.equal(dx.cpu(), (dz @ w.double().T).to(dtype))
+    assert torch.equal(dw.cpu(), (x.double().T @ dz).to(dtype))
+    assert torch.equal(g.dbias.cpu(), dz.sum(0).float())
+    dwt = torch.full((N, K), math.nan, dtype=dtype, device="cuda")
+    tmm.gemm_bias_act_grad(ds, xs, None, pre=pre, act="relu", dx=False, dw=dwt.t())
+    assert torch.equal(dwt.t(), dw)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("M", [2, 200])
+def test_residual_in_place(dtype, M):
+    x, w, res = ints(1, M, 96).to(dtype), ints(2, 96, 320).to(dtype), ints(3, M, 320).to(dtype)
+    y = res.cuda()
+    assert checked(tmm.gemm_bias_act, x.cuda(), w.cuda(), residual=y, y=y) is y
+    assert torch.equal(y.cpu(), (x.double() @ w.double() + res.double()).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("M", [1, 5, 150, 400])
+def test_values_that_are_not_finite_stay_in_their_row(dtype, M):
+    x, w = normals(1, M, 200).to(dtype), normals(2, 200, 300, std=0.1).to(dtype)
+    x[M // 2, 7] = math.nan
+    y = checked(tmm.gemm_bias_act, x.cuda(), w.cuda(), act="silu")
+    bad = y.isnan().any(1).cpu()
+    assert bool(bad[M // 2]) and int(bad.sum()) == 1
+    w[3, 11] = math.inf
+    y = tmm.gemm_bias_act(x.cuda(), w.cuda())
+    bad = (~y.isfinite()).cpu()
+    bad[M // 2] = False
+    assert not bool(bad[:, :11].any() | bad[:, 12:].any()) and (M == 1 or bool(bad[:, 11].any()))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_empty_sums_and_no_rows(dtype):
+    x = torch.empty(70, 0, dtype=dtype, device="cuda")
+    w = torch.empty(0, 40, dtype=dtype, device="cuda")
+    bias, res = ints(1, 40).to(dtype), ints(2, 70, 40).to(dtype)
+    y = checked(tmm.gemm_bias_act, x, w, bias.cuda(), "relu", res.cuda())
+    assert torch.equal(y.cpu(), (bias.double().relu() + res.double()).to(dtype))
+    assert torch.equal(tmm.gemm_bias_act(x, w), torch.zeros(70, 40, dtype=dtype, device="cuda"))
+    dy = ints(3, 70, 40).to(dtype)
+    g = checked(tmm.gemm_bias_act_grad, dy.cuda(), x, w, dbias=True)
+    assert g.dx.shape == (70, 0) and g.dw.shape == (0, 40)
+    assert torch.equal(g.dbias.cpu(), dy.double().sum(0).float())
+    x0, w0 = torch.empty(0, 8, dtype=dtype, device="cuda"), ints(4, 8, 40).to(dtype).cuda()
+    assert tmm.gemm_bias_act(x0, w0, bias.cuda()).shape == (0, 40)
+    g = tmm.gemm_bias_act_grad(torch.empty(0, 40, dtype=dtype, device="cuda"), x0, w0, dbias=True)
+    assert g.dx.shape == (0, 8) and not bool(g.dw.any()) and not bool(g.dbias.any())
+    n0 = torch.empty(8, 0, dtype=dtype, device="cuda")
+    x8 = torch.ones(5, 8, dtype=dtype, device="cuda")
+    assert tmm.gemm_bias_act(x8, n0).shape == (5, 0)
+    g = tmm.gemm_bias_act_grad(torch.empty(5, 0, dtype=dtype, device="cuda"), x8, n0)
+    assert not bool(g.dx.any()) and g.dw.shape == (8, 0)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_only_the_gradients_asked_for(dtype):
+    x, w, dy = ints(1, 90, 48), ints(2, 48, 264), ints(3, 90, 264)
+    z = ints(4, 90, 264, top=1)
+    xd, wd, dyd, zd = (on_gpu(t, dtype) for t in (x, w, dy, z))
+    full = tmm.gemm_bias_act_grad(dyd, xd, wd, pre=zd, act="silu", dbias=True)
+    for dx, dw, db in itertools.product((True, False), repeat=3):
+        g = checked(tmm.gemm_bias_act_grad, dyd, xd if dw else None, wd if dx else None, pre=zd,
+                    act="silu", dx=dx, dw=dw, dbias=db)
+        for name, on in (("dx", dx), ("dw", dw), ("dbias", db)):
+            got = getattr(g, name)
+            assert (got is not None) == on
+            assert not on or torch.equal(got, getattr(full, name))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_streams_graphs_and_workspaces(dtype):
+    M, N, K = 130, 261, 83              # odd: every operand is restaged into the workspace
+    x, w, dy = (on_gpu(t, dtype) for t in (ints(1, M, K), ints(2, K, N), ints(3, M, N)))
+    bias = on_gpu(ints(4, N), dtype)
+
+    def work():
+        y, z = tmm.gemm_bias_act(x, w, bias, "relu", pre=True)
+        return (y, z, *tmm.gemm_bias_act_grad(dy, x, w, pre=z, act="relu", dbias=True))
+
+    want = work()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y = tmm.gemm_bias_act(x, w, bias, "relu", stream=s)
+    g = tmm.gemm_bias_act_grad(dy, x, w, pre=want[1], act="relu", stream=s)
+    s.synchronize()
+    assert torch.equal(y, want[0]) and torch.equal(g.dw, want[3])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = work()
+    for t, seed in ((x, 11), (w, 12), (dy, 13)):
+        t.copy_(ints(seed, *t.shape))
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, work()):
+        assert torch.equal(a, b)
+    tmm.check_device()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("M", [1, 40, 200])
+def test_results_are_the_same_every_time(dtype, M):
+    x, w = normals(1, M, 2048).to(dtype).cuda(), normals(2, 2048, 520).to(dtype).cuda()
+    dy = normals(3, M, 520).to(dtype).cuda()
+    first = None
+    for _ in range(5):
+        y = tmm.gemm_bias_act(x, w, act="gelu")
+        g = tmm.gemm_bias_act_grad(dy, x, w, pre=y, act="gelu", dbias=True)
+        out = (y, *g)
+        first = first or out
+        assert all(torch.equal(a, b) for a, b in zip(out, first))
+
+
+def test_results_past_two_billion_values():
+    M, N = 40000, 65536
+    x = torch.zeros(M, 8, dtype=torch.bfloat16, device="cuda")
+    x[-1] = 1.0
+    w = torch.ones(8, N, dtype=torch.bfloat16, device="cuda")
+    y = torch.ones(M, N, dtype=torch.bfloat16, device="cuda")
+    tmm.gemm_bias_act(x, w, residual=y, y=y)
+    assert bool((y[-1] == 9).all()) and bool((y[-2] == 1).all()) and bool((y[0] == 1).all())
+    tmm.check_device()

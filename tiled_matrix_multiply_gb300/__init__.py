@@ -35,7 +35,8 @@ __all__ = ["gemm_f32", "gemm_f32_naive", "gemm_f32_tc3", "tc3_workspace_bytes",
 _GROUPED = ("group_rows", "RowGroups", "gemm_grouped", "gemm_grouped_wgrad", "gemm_lora")
 _SCORES = ("route_rows", "RowRoutes", "route_rows_grad", "logprob_rows", "RowLogprobs",
            "logprob_rows_grad")
-_MODULES = {"grouped": _GROUPED, "scores": _SCORES}
+_LINEAR = ("gemm_bias_act", "gemm_bias_act_grad", "LinearGrads")
+_MODULES = {"grouped": _GROUPED, "scores": _SCORES, "linear": _LINEAR}
 
 
 def __getattr__(name):

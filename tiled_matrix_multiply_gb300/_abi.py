@@ -42,6 +42,8 @@ STATUS_NAMES = {
 TMM_F32, TMM_BF16, TMM_F16 = 0, 1, 2
 TMM_MAX_GROUPS = 512
 TMM_MAX_RANK = 1024
+# Activations of a linear layer.
+TMM_ACT_NONE, TMM_ACT_RELU, TMM_ACT_SILU, TMM_ACT_GELU, TMM_ACT_GELU_TANH = range(5)
 # Scores and limits of the routing and of the log probabilities.
 TMM_SOFTMAX, TMM_SIGMOID = 0, 1
 TMM_MAX_EXPERTS, TMM_MAX_FAN, TMM_MAX_ROUTE_GROUPS, TMM_MAX_TOP = 512, 16, 32, 32
@@ -58,6 +60,8 @@ EXPORTED = GEMM_ENTRY_POINTS + ("gemm_f32_ex", "gemm_f32_tc3", "gemm_f32_tc3_ex"
                                  "gemm_grouped", "gemm_grouped_workspace_size",
                                  "gemm_grouped_wgrad", "gemm_grouped_wgrad_workspace_size",
                                  "gemm_lora", "gemm_lora_workspace_size",
+                                 "gemm_bias_act", "gemm_bias_act_workspace_size",
+                                 "gemm_bias_act_grad", "gemm_bias_act_grad_workspace_size",
                                  "route_rows", "route_rows_grad", "logprob_rows",
                                  "logprob_rows_grad",
                                  "tmm_check_device", "tmm_testing_set_wait_hooks",
@@ -145,6 +149,17 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                                  ptr, ptr, i64, ptr, i64, i64, ptr, i64, i64]
         lib.gemm_lora_workspace_size.restype = size
         f32 = ctypes.c_float
+        lib.gemm_bias_act.argtypes = [ci, ci, ci, i64, i64, i64, ptr, i64, ptr, i64, ptr, ci, ptr,
+                                      i64, ptr, i64, ptr, i64, ptr, size, ptr]
+        lib.gemm_bias_act.restype = ci
+        lib.gemm_bias_act_workspace_size.argtypes = [ci, ci, i64, i64, i64, ptr, i64, ptr, i64]
+        lib.gemm_bias_act_workspace_size.restype = size
+        lib.gemm_bias_act_grad.argtypes = [ci, ci, ci, i64, i64, i64, ptr, i64, ptr, i64, ptr, i64,
+                                           ptr, i64, ptr, i64, ptr, i64, ci, ptr, ptr, size, ptr]
+        lib.gemm_bias_act_grad.restype = ci
+        lib.gemm_bias_act_grad_workspace_size.argtypes = [ci, ci, ci, i64, i64, i64, ptr, i64, ptr,
+                                                          i64, ptr, i64, ptr, ptr, ci, ptr]
+        lib.gemm_bias_act_grad_workspace_size.restype = size
         lib.route_rows.argtypes = [ci, i64, i64, ptr, i64, ptr, ci, i64, i64, ci, i64, ci, f32, ptr,
                                    ptr, ptr]
         lib.route_rows.restype = ci

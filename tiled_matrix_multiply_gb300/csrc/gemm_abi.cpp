@@ -1080,6 +1080,200 @@ int logprob_rows_grad(int dtype, int64_t rows, int64_t cols, const void *logits,
   return TMM_OK;
 }
 
+// ---- linear layers --------------------------------------------------------------------------
+
+namespace {
+
+int check_linear(const char *who, int dtype, int trans, int act, int64_t M, int64_t N, int64_t K) {
+  if (dtype != TMM_F32 && dtype != TMM_BF16 && dtype != TMM_F16)
+    return fail(TMM_ERR_INVALID_ARG, "%s: unknown dtype %d", who, dtype);
+  if (trans != 0 && trans != 1)
+    return fail(TMM_ERR_INVALID_ARG, "%s: transw must be 0 or 1", who);
+  if (act < TMM_ACT_NONE || act > TMM_ACT_GELU_TANH)
+    return fail(TMM_ERR_INVALID_ARG, "%s: unknown activation %d", who, act);
+  if (!extent_ok(M) || !extent_ok(N) || !extent_ok(K))
+    return fail(TMM_ERR_INVALID_ARG, "%s: sizes must be >= 0 and below 2^29 (M=%lld N=%lld K=%lld)",
+                who, (long long)M, (long long)N, (long long)K);
+  return TMM_OK;
+}
+
+tmm::LinearProblem linear_problem(int dtype, int transw, int64_t M, int64_t N, int64_t K,
+                                  const void *x, int64_t ldx, const void *w, int64_t ldw) {
+  tmm::LinearProblem p = {};
+  p.dtype = dtype;
+  p.rows = M;
+  p.K = K;
+  p.N = N;
+  p.x = stack_of(x, 1, M, K, ldx, 0);
+  p.w = stack_of(w, 1, transw ? N : K, transw ? K : N, ldw, 0);
+  p.trans_w = transw;
+  return p;
+}
+
+// An optional matrix: nothing to check where it is NULL.
+int check_optional(const char *who, const char *name, const void *m, int64_t rows, int64_t cols,
+                   int64_t ld, int size) {
+  if (m == nullptr) return TMM_OK;
+  return check_stack(who, name, stack_of(m, 1, rows, cols, ld, 0), size);
+}
+
+int64_t matrix_bytes(const void *m, int64_t rows, int64_t cols, int64_t ld, int size) {
+  return m == nullptr ? 0 : stack_span(stack_of(m, 1, rows, cols, ld, 0)) * size;
+}
+
+}  // namespace
+
+size_t gemm_bias_act_workspace_size(int dtype, int transw, int64_t M, int64_t N, int64_t K,
+                                    const void *x, int64_t ldx, const void *w, int64_t ldw) {
+  if (!extent_ok(M) || !extent_ok(N) || !extent_ok(K) || M == 0 || N == 0 || K == 0) return 0;
+  return tmm::linear_workspace_bytes(linear_problem(dtype, transw, M, N, K, x, ldx, w, ldw));
+}
+
+int gemm_bias_act(int dtype, int transw, int act, int64_t M, int64_t N, int64_t K, const void *x,
+                  int64_t ldx, const void *w, int64_t ldw, const void *bias, int bias_f32,
+                  const void *residual, int64_t ldr, void *y, int64_t ldy, void *pre,
+                  int64_t ldpre, void *workspace, size_t workspace_bytes, tmm_stream_t stream) {
+  const char *who = "gemm_bias_act";
+  int rc = check_linear(who, dtype, transw, act, M, N, K);
+  if (rc != TMM_OK) return rc;
+  tmm::LinearProblem p = linear_problem(dtype, transw, M, N, K, x, ldx, w, ldw);
+  const int size = element_size(dtype), bias_size = bias_f32 ? 4 : size;
+  if (bias_f32 != 0 && bias_f32 != 1)
+    return fail(TMM_ERR_INVALID_ARG, "%s: bias_f32 must be 0 or 1", who);
+  if ((rc = check_stack(who, "x", p.x, size)) != TMM_OK ||
+      (rc = check_stack(who, "w", p.w, size)) != TMM_OK ||
+      (rc = check_stack(who, "y", stack_of(y, 1, M, N, ldy, 0), size)) != TMM_OK ||
+      (rc = check_optional(who, "residual", residual, M, N, ldr, size)) != TMM_OK ||
+      (rc = check_optional(who, "pre", pre, M, N, ldpre, size)) != TMM_OK ||
+      (rc = check_array(who, "bias", bias, 0, bias_size)) != TMM_OK)
+    return rc;
+  if (M == 0 || N == 0) return TMM_OK;
+  const size_t need = tmm::linear_workspace_bytes(p);
+  if ((rc = check_workspace(who, need, workspace, workspace_bytes)) != TMM_OK) return rc;
+  const bool in_place = y == residual && ldy == ldr;
+  const Bytes all[7] = {{"y", y, matrix_bytes(y, M, N, ldy, size)},
+                        {"pre", pre, matrix_bytes(pre, M, N, ldpre, size)},
+                        {"the workspace", need ? workspace : nullptr, int64_t(need)},
+                        {"x", x, stack_span(p.x) * size},
+                        {"w", w, stack_span(p.w) * size},
+                        {"bias", bias, bias ? N * bias_size : 0},
+                        {"residual", residual, matrix_bytes(residual, M, N, ldr, size)}};
+  if ((rc = check_alias(who, all, in_place ? 6 : 7)) != TMM_OK ||
+      (rc = check_outputs(who, all + 1, 2, 6)) != TMM_OK)
+    return rc;
+  tmm::DeviceInfo dev;
+  if ((rc = current_device(&dev)) != TMM_OK) return rc;
+  p.act = act;
+  p.bias = bias;
+  p.bias_f32 = bias_f32;
+  p.residual = residual;
+  p.ld_residual = ldr;
+  p.y = y;
+  p.ldy = ldy;
+  p.pre = pre;
+  p.ld_pre = ldpre;
+  const cudaError_t e =
+      tmm::launch_linear(p, dev, workspace, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(TMM_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+  return TMM_OK;
+}
+
+namespace {
+
+tmm::LinearGradProblem linear_grad_problem(int dtype, int transw, int act, int64_t M, int64_t N,
+                                           int64_t K, const void *dy, int64_t lddy, const void *x,
+                                           int64_t ldx, const void *w, int64_t ldw,
+                                           const void *pre, int64_t ldpre, void *dx, int64_t lddx,
+                                           void *dw, int64_t lddw, int transdw, float *dbias) {
+  tmm::LinearGradProblem p = {};
+  p.dtype = dtype;
+  p.act = act;
+  p.rows = M;
+  p.K = K;
+  p.N = N;
+  p.dy = stack_of(dy, 1, M, N, lddy, 0);
+  p.x = stack_of(x, 1, M, K, ldx, 0);
+  p.w = stack_of(w, 1, transw ? N : K, transw ? K : N, ldw, 0);
+  p.trans_w = transw;
+  p.pre = pre;
+  p.ld_pre = ldpre;
+  p.dx = K > 0 ? dx : nullptr;
+  p.lddx = lddx;
+  p.dw = K > 0 ? dw : nullptr;
+  p.lddw = lddw;
+  p.trans_dw = transdw;
+  p.dbias = dbias;
+  return p;
+}
+
+}  // namespace
+
+size_t gemm_bias_act_grad_workspace_size(int dtype, int transw, int act, int64_t M, int64_t N,
+                                         int64_t K, const void *dy, int64_t lddy, const void *x,
+                                         int64_t ldx, const void *w, int64_t ldw, const void *dx,
+                                         const void *dw, int transdw, const void *dbias) {
+  if (!extent_ok(M) || !extent_ok(N) || !extent_ok(K) || M == 0 || N == 0) return 0;
+  return tmm::linear_grad_workspace_bytes(linear_grad_problem(
+      dtype, transw, act, M, N, K, dy, lddy, x, ldx, w, ldw, nullptr, 1, const_cast<void *>(dx), 1,
+      const_cast<void *>(dw), 1, transdw, static_cast<float *>(const_cast<void *>(dbias))));
+}
+
+int gemm_bias_act_grad(int dtype, int transw, int act, int64_t M, int64_t N, int64_t K,
+                       const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *w,
+                       int64_t ldw, const void *pre, int64_t ldpre, void *dx, int64_t lddx,
+                       void *dw, int64_t lddw, int transdw, float *dbias, void *workspace,
+                       size_t workspace_bytes, tmm_stream_t stream) {
+  const char *who = "gemm_bias_act_grad";
+  int rc = check_linear(who, dtype, transw, act, M, N, K);
+  if (rc != TMM_OK) return rc;
+  if (transdw != 0 && transdw != 1)
+    return fail(TMM_ERR_INVALID_ARG, "%s: transdw must be 0 or 1", who);
+  if (act != TMM_ACT_NONE && pre == nullptr && M > 0 && N > 0)
+    return fail(TMM_ERR_INVALID_ARG, "%s: pre is NULL", who);
+  const tmm::LinearGradProblem p =
+      linear_grad_problem(dtype, transw, act, M, N, K, dy, lddy, x, ldx, w, ldw, pre, ldpre, dx,
+                          lddx, dw, lddw, transdw, dbias);
+  const int size = element_size(dtype);
+  const int64_t wr = transdw ? N : K, wc = transdw ? K : N;      // of dw
+  if ((rc = check_stack(who, "dy", p.dy, size)) != TMM_OK ||
+      (rc = check_optional(who, "pre", pre, M, N, ldpre, size)) != TMM_OK ||
+      (rc = check_optional(who, "dx", dx, M, K, lddx, size)) != TMM_OK ||
+      (rc = check_optional(who, "dw", dw, wr, wc, lddw, size)) != TMM_OK ||
+      (rc = check_array(who, "dbias", dbias, 0)) != TMM_OK ||
+      (dw && (rc = check_stack(who, "x", p.x, size)) != TMM_OK) ||
+      (dx && (rc = check_stack(who, "w", p.w, size)) != TMM_OK))
+    return rc;
+  const size_t need = M == 0 || N == 0 ? 0 : tmm::linear_grad_workspace_bytes(p);
+  if ((rc = check_workspace(who, need, workspace, workspace_bytes)) != TMM_OK) return rc;
+  const Bytes all[8] = {{"dx", dx, matrix_bytes(dx, M, K, lddx, size)},
+                        {"dw", dw, matrix_bytes(dw, wr, wc, lddw, size)},
+                        {"dbias", dbias, dbias ? N * 4 : 0},
+                        {"the workspace", need ? workspace : nullptr, int64_t(need)},
+                        {"dy", dy, stack_span(p.dy) * size},
+                        {"x", dw ? x : nullptr, stack_span(p.x) * size},
+                        {"w", dx ? w : nullptr, stack_span(p.w) * size},
+                        {"pre", pre, matrix_bytes(pre, M, N, ldpre, size)}};
+  if ((rc = check_outputs(who, all, 4, 8)) != TMM_OK) return rc;
+  if ((M == 0 || K == 0 || dx == nullptr) && (N == 0 || K == 0 || dw == nullptr) &&
+      (N == 0 || dbias == nullptr))
+    return TMM_OK;
+  tmm::DeviceInfo dev;
+  if ((rc = current_device(&dev)) != TMM_OK) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (M == 0 || N == 0) {      // empty sums
+    if (dx && M > 0 && K > 0 &&
+        (rc = zero_output(who, dx, 1, M, K, lddx, 0, size, s)) != TMM_OK)
+      return rc;
+    if (dw && N > 0 && K > 0 &&
+        (rc = zero_output(who, dw, 1, wr, wc, lddw, 0, size, s)) != TMM_OK)
+      return rc;
+    return dbias && N > 0 ? zero_output(who, dbias, 1, 1, N, N, 0, 4, s) : TMM_OK;
+  }
+  const cudaError_t e = tmm::launch_linear_grad(p, dev, workspace, s);
+  if (e != cudaSuccess) return fail(TMM_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+  return TMM_OK;
+}
+
 const char *tmm_last_error_string(void) { return g_last_error; }
 
 const char *gemm_last_error_string(void) { return g_last_error; }

@@ -66,6 +66,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "activation.cuh"
 #include "grouped.h"
 #include "tmm_gemm.h"
 
@@ -75,7 +76,7 @@ __device__ unsigned int g_grouped_status;
 
 namespace {
 
-constexpr int kForward = 0, kWgrad = 1, kLora = 2;
+constexpr int kForward = 0, kWgrad = 1, kLora = 2, kLinear = 3;
 constexpr int kBK = 64;                  // 16-bit values per K slice: one 128-byte swizzle row
 constexpr int kEpiWarps = 8;
 constexpr int kListed = kMaxGroups + 3;            // entries of a list of groups, see Table
@@ -104,7 +105,8 @@ __host__ __device__ constexpr int rank_slice(int planes, int b_parts) {
   return planes == 3 ? 64 : b_parts == 2 ? 16 : 32;
 }
 
-template <int CG, int PLANES>
+// STAGE: bytes of a result warp for 16-bit results.
+template <int CG, int PLANES, int STAGE = 1024>
 struct Shape {
   // FP32 on single blocks: the copy warps read the operands as they are stored and split them
   // on the way (DIRECT); no planes.
@@ -122,9 +124,9 @@ struct Shape {
   static constexpr int kStages = PLANES == 3 ? (CG == 2 ? 3 : 2) : (CG == 2 ? 6 : 7);
   static constexpr uint32_t kTmemCols =
       PLANES == 3 ? 4 * kBN : 2 * kBN;               // two accumulators (of each kind)
-  // The parts of a shared sum (single blocks), and 1 KiB a result warp for 16-bit results.
+  // The parts of a shared sum (single blocks), and where 16-bit results are transposed.
   static constexpr uint32_t kRed = CG == 1 ? 128 * kBN * 4 : 0;
-  static constexpr uint32_t kOutStage = PLANES == 1 ? kEpiWarps * 1024 : 0;
+  static constexpr uint32_t kOutStage = PLANES == 1 ? kEpiWarps * STAGE : 0;
   static constexpr uint32_t kTable =
       kListed * 4 * 3 + kCopyWarps * 128 + 116 + (CG == 1 ? kFewRows * 4 : 0);
   static constexpr uint32_t kBars = 8 * (2 * kStages + 5) + 32;
@@ -133,10 +135,13 @@ struct Shape {
   static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory columns");
 };
 
+template <int CG, int MODE, int PLANES>
+using ModeShape = Shape<CG, PLANES, MODE == kLinear ? 2048 : 1024>;
+
 struct Params {
   int rows;              // p runs over [0, rows)
   int groups;
-  const int *offsets;    // groups + 1
+  const int *offsets;    // groups + 1, or NULL: one group of all rows
   const int *row_index;  // r(p) of the rows read (single blocks; pairs read gathered rows), or NULL
   const int *out_index;  // r(p) of the rows written (adapters), or NULL
   int q_rows;            // rows of the x that is read
@@ -167,6 +172,14 @@ struct Params {
   int64_t ldu, ldb, stride_b;
   int trans_b, vec_b;
   int zero_rows;         // forward: write zeros to the rows of no group
+  // Linear: y = act(x w + bias) + residual, and z = x w + bias beside it.
+  const void *bias;      // of N values, or NULL
+  int bias_f32;          // else of the operands' type
+  int act;               // TMM_ACT_*
+  const void *residual;  // rows x N, or NULL
+  void *pre;             // rows x N, or NULL
+  int64_t ld_residual, ld_pre;
+  int epilogue;          // any of them
   int ksplit;            // blocks of a cluster that share a tile's sum (CG = 1)
   int64_t wait_limit_ns;
   int drop_block;        // testing hook: this block waits for bytes that never come (-1: none)
@@ -842,6 +855,125 @@ __device__ __forceinline__ void store_columns(const Params &p, const Tile &t, in
   }
 }
 
+// ---- the epilogue of a linear layer ------------------------------------------------------
+
+// Element `at` of a matrix of the operands' type, in FP32.
+template <int PLANES>
+__device__ __forceinline__ float linear_value(const Params &p, const void *m, int64_t at) {
+  if constexpr (PLANES == 3) return static_cast<const float *>(m)[at];
+  if (p.out_type == kOutBF16) return float(static_cast<const __nv_bfloat16 *>(m)[at]);
+  return float(static_cast<const __half *>(m)[at]);
+}
+template <int PLANES>
+__device__ __forceinline__ float linear_bias(const Params &p, int n) {
+  if (p.bias == nullptr || n >= p.N) return 0.0f;
+  if (p.bias_f32) return static_cast<const float *>(p.bias)[n];
+  return linear_value<PLANES>(p, p.bias, n);
+}
+template <int PLANES>
+__device__ __forceinline__ void linear_store(const Params &p, void *m, int64_t at, float v) {
+  if constexpr (PLANES == 3)
+    static_cast<float *>(m)[at] = v;
+  else if (p.out_type == kOutBF16)
+    static_cast<__nv_bfloat16 *>(m)[at] = __float2bfloat16_rn(v);
+  else
+    static_cast<__half *>(m)[at] = __float2half_rn(v);
+}
+// One result: z = the sum and the bias.
+template <int PLANES>
+__device__ __forceinline__ void linear_one(const Params &p, int64_t row, int n, float z) {
+  if (p.pre) linear_store<PLANES>(p, p.pre, row * p.ld_pre + n, z);
+  float y = activate<PLANES == 1>(p.act, z);
+  if (p.residual) y += linear_value<PLANES>(p, p.residual, row * p.ld_residual + n);
+  linear_store<PLANES>(p, p.out, row * p.ld_out + n, y);
+}
+__device__ __forceinline__ uint32_t pack_results(const Params &p, float lo, float hi) {
+  uint32_t w;
+  if (p.out_type == kOutBF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
+__device__ __forceinline__ float2 unpack_values(const Params &p, uint32_t w) {
+  if (p.out_type == kOutBF16)
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// 16 columns (rows of the result) from c0 on of the warp's 32 n.  In FP32 a lane has its n in all of
+// them, 128 bytes of a row a warp.  16-bit results go through 2 KiB of shared memory a warp as FP32,
+// 16 rows of 32 n, of which a lane then has two pieces of 8 n: everything read and written is 16
+// bytes a lane.  The bias of those 8 n (or of the lane's one) is in `bias`.
+template <int PLANES>
+__device__ __forceinline__ void linear_columns(const Params &p, const Tile &t, int c0, int nw,
+                                               const float (&v)[16], const float (&bias)[8],
+                                               uint32_t stage) {
+  const int lane = threadIdx.x & 31;
+  const int count = min(16, t.qn - c0);
+  const int64_t first = t.q0 + c0;
+  if (PLANES == 3 || !p.vec_out) {
+    const int n = nw + lane;
+    if (n < p.N)
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (j < count) linear_one<PLANES>(p, first + j, n, v[j] + bias[0]);
+    return;
+  }
+  // Chunk c of four n of row r is at r * 128 + 16 (c ^ r % 8): free of bank conflicts both ways.
+  __syncwarp();      // the reads of the block before are done
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage + j * 128 + (((lane >> 2) ^ (j & 7)) << 4) +
+                                                 (lane & 3) * 4),
+                 "f"(v[j])
+                 : "memory");
+  __syncwarp();
+  const int piece = lane & 3, n8 = nw + piece * 8;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = (lane >> 2) + 8 * i;
+    float z[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(z[4 * h]), "=f"(z[4 * h + 1]), "=f"(z[4 * h + 2]), "=f"(z[4 * h + 3])
+                   : "r"(stage + row * 128 + (((2 * piece + h) ^ (row & 7)) << 4))
+                   : "memory");
+    if (row >= count || n8 >= p.N) continue;
+    const int64_t r = first + row;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) z[k] += bias[k];
+    if (n8 + 8 > p.N) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (n8 + k < p.N) linear_one<PLANES>(p, r, n8 + k, z[k]);
+      continue;
+    }
+    uint4 res = make_uint4(0, 0, 0, 0);
+    if (p.residual)
+      res = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.residual) +
+                                             r * p.ld_residual + n8);
+    if (p.pre)
+      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.pre) + r * p.ld_pre + n8) =
+          make_uint4(pack_results(p, z[0], z[1]), pack_results(p, z[2], z[3]),
+                     pack_results(p, z[4], z[5]), pack_results(p, z[6], z[7]));
+    activate_all<8>(p.act, z);
+    if (p.residual) {
+      const uint32_t w[4] = {res.x, res.y, res.z, res.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 a = unpack_values(p, w[k]);
+        z[2 * k] += a.x;
+        z[2 * k + 1] += a.y;
+      }
+    }
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + r * p.ld_out + n8) =
+        make_uint4(pack_results(p, z[0], z[1]), pack_results(p, z[2], z[3]),
+                   pack_results(p, z[4], z[5]), pack_results(p, z[6], z[7]));
+  }
+}
+
 // Eight values as they are stored, 16 bytes or 32.
 template <typename T>
 struct Eight {
@@ -1055,7 +1187,7 @@ __device__ __forceinline__ bool split_tile(const Params &p, const Tile &t, int s
 
 // BP: parts of b in the adapters' part on pairs, 2 where it is FP16 (half_parts).
 template <int CG, int MODE, int PLANES, int BP = 1>
-__global__ void __launch_bounds__(Shape<CG, PLANES>::kThreads, 1)
+__global__ void __launch_bounds__(ModeShape<CG, MODE, PLANES>::kThreads, 1)
 grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                const __grid_constant__ CUtensorMap map_q,    // Q tiles
                const __grid_constant__ CUtensorMap map_qr,   // single rows of x; pairs: tiles of
@@ -1064,7 +1196,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                const __grid_constant__ CUtensorMap map_u,    // u tiles; gradient: 16 rows of x
                const __grid_constant__ CUtensorMap map_pr,   // gradient: single rows of dy
                const Params p) {
-  using S = Shape<CG, PLANES>;
+  using S = ModeShape<CG, MODE, PLANES>;
   // The adapters' part: pairs extend the sum (EXT); single blocks, whose rows are few, add it to
   // the results on the CUDA cores while the weights stream (FEW).
   constexpr bool EXT = MODE == kLora && CG == 2, FEW = MODE == kLora && CG == 1;
@@ -1134,9 +1266,11 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     }
   }
   if (!S::kDirect && warp == 0 && elect_one()) {
-    prefetch_map(&map_p);
-    prefetch_map(&map_q);
-    prefetch_map(&map_qr);
+    if (MODE != kLinear || p.K > 0) {      // (no maps without a sum)
+      prefetch_map(&map_p);
+      prefetch_map(&map_q);
+      prefetch_map(&map_qr);
+    }
   }
   // The adapters' product follows the one that makes u, and needs nothing else of it: its wait
   // comes before the first slice of u, so that the shared projection starts beside it.
@@ -1145,7 +1279,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     grid_start_next();
   }
   for (int g = threadIdx.x; g <= p.groups; g += S::kThreads)
-    offs[g] = max(0, min(p.offsets[g], p.rows));
+    offs[g] = p.offsets ? max(0, min(p.offsets[g], p.rows)) : g * p.rows;
   __syncthreads();
   if (warp == 0) {
     // Group bounds are the running maximum of the offsets: offsets that step back make an
@@ -1712,9 +1846,21 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       const uint32_t lanes = tmem + (uint32_t(32 * quarter) << 16);
       const uint32_t tempty = CG == 2 ? map_rank(bar_tempty, 0) : bar_tempty;
       const int nw = tile.n0 + half_rank * 128 + 32 * quarter;
-      const uint32_t stage = out_stage + uint32_t(warp - S::kEpi0) * 1024;
+      const uint32_t stage = out_stage + uint32_t(warp - S::kEpi0) * (S::kOutStage / kEpiWarps);
       const float scale = MODE == kForward && p.scale ? p.scale[tile.g] : 1.0f;
       constexpr int kBlocks = S::kBN / 32;     // 16-column blocks of a warp, every other one
+      // Linear: the bias of the n that this lane finishes, and whether anything is to be done to a
+      // sum but to store it.
+      float bias[8] = {};
+      const bool linear = MODE == kLinear && p.epilogue;
+      if constexpr (MODE == kLinear) {
+        if (p.bias && PLANES == 1 && p.vec_out) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) bias[k] = linear_bias<PLANES>(p, nw + (lane & 3) * 8 + k);
+        } else if (p.bias) {
+          bias[0] = linear_bias<PLANES>(p, nw + lane);
+        }
+      }
       // The columns that this block adds up and stores: all of them, or its share.
       const int own0 = CG == 1 ? tile.qn * int(rank) / p.ksplit : 0;
       const int own1 = CG == 1 ? tile.qn * int(rank + 1) / p.ksplit : tile.qn;
@@ -1755,6 +1901,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
             if (p.ksplit > 1) *at = w[j];
           }
           if (p.ksplit == 1) store_columns<MODE, PLANES>(p, tile, c0, nw, w, scale, stage, owner);
+        } else if (linear) {
+          linear_columns<PLANES>(p, tile, c0, nw, v, bias, stage);
         } else {
           store_columns<MODE, PLANES>(p, tile, c0, nw, v, scale, stage, owner);
         }
@@ -1770,7 +1918,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           ++q;
           if (!__all_sync(~0u, ready)) timed_out = true;
           tc_fence_after();
-          if (!timed_out && p.vec_out && !FEW && p.ksplit == 1) {
+          if (!timed_out && p.vec_out && !FEW && p.ksplit == 1 && !linear) {
             const uint32_t at = lanes + buf * S::kBN;
             for (int c0 = 16 * half; c0 < tile.bn; c0 += 32) {
               uint32_t f[2][8];
@@ -1798,7 +1946,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           // and sum, on the way that the operands take (8 groups of 8320 rows, 2048 x 2048: 330 us
           // -> 350 us; K = 8320, 4096 rows of 8 groups, N = 2048: 89 us -> 101 us; up to 8192
           // unchanged).
-          const bool matrices = p.vec_out && !FEW && p.ksplit == 1;
+          const bool matrices = p.vec_out && !FEW && p.ksplit == 1 && !linear;
           const int each = long_sum(nb);
           float acc[kBlocks][16];
           for (int left = nb; left > 0; left -= each, ++q) {
@@ -1954,6 +2102,13 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                   store_u4(static_cast<uint16_t *>(p.out) + o, n, g, p.idesc & (1u << 7));
                 continue;
               }
+            }
+            if constexpr (MODE == kLinear) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (n + j < p.N)
+                  linear_one<PLANES>(p, tile.q0 + col, n + j, f[j] + linear_bias<PLANES>(p, n + j));
+              continue;
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -2370,7 +2525,7 @@ struct Maps {
 template <int CG, int MODE, int PLANES, int BP = 1>
 cudaError_t launch_shape(const Maps &m, Params &prm, int64_t tiles, const DeviceInfo &dev,
                          cudaStream_t stream) {
-  using S = Shape<CG, PLANES>;
+  using S = ModeShape<CG, MODE, PLANES>;
   static std::atomic<uint64_t> configured{0};
   auto kernel = grouped_kernel<CG, MODE, PLANES, BP>;
   const uint64_t bit = uint64_t(1) << (dev.id & 63);
@@ -2407,6 +2562,7 @@ cudaError_t launch_mode(int mode, const Maps &m, Params &prm, int64_t tiles,
                         const DeviceInfo &dev, cudaStream_t stream) {
   if (mode == kForward) return launch_shape<CG, kForward, PLANES>(m, prm, tiles, dev, stream);
   if (mode == kWgrad) return launch_shape<CG, kWgrad, PLANES>(m, prm, tiles, dev, stream);
+  if (mode == kLinear) return launch_shape<CG, kLinear, PLANES>(m, prm, tiles, dev, stream);
   if constexpr (CG == 2 && PLANES == 1)
     if (prm.out_type == kOutF16) return launch_shape<2, kLora, 1, 2>(m, prm, tiles, dev, stream);
   return launch_shape<CG, kLora, PLANES>(m, prm, tiles, dev, stream);
@@ -2418,7 +2574,9 @@ cudaError_t launch_any(int cg, int planes, int mode, const Maps &m, Params &prm,
   prm.drop_block = g_drop_block.load(std::memory_order_relaxed);
   prm.vec_out = (prm.out_type == kOutBF16 || prm.out_type == kOutF16) &&
                 (reinterpret_cast<uintptr_t>(prm.out) & 15u) == 0 && prm.ld_out % 8 == 0 &&
-                prm.stride_out % 8 == 0;
+                prm.stride_out % 8 == 0 &&
+                (reinterpret_cast<uintptr_t>(prm.residual) & 15u) == 0 && prm.ld_residual % 8 == 0 &&
+                (reinterpret_cast<uintptr_t>(prm.pre) & 15u) == 0 && prm.ld_pre % 8 == 0;
   if (cg == 2)
     return planes == 3 ? launch_mode<2, 3>(mode, m, prm, tiles, dev, stream)
                        : launch_mode<2, 1>(mode, m, prm, tiles, dev, stream);
@@ -2552,7 +2710,7 @@ void set_direct(Params *prm, const Stack &P, const Stack &x) {
 // `index`: the rows of x by number, or NULL.
 cudaError_t run_forward(int dtype, const Planes &x, const Stack &xs, const int32_t *index,
                         const Planes &w, const Stack &ws, bool trans_w, Params prm,
-                        const DeviceInfo &dev, cudaStream_t stream) {
+                        const DeviceInfo &dev, cudaStream_t stream, int mode = kForward) {
   const int planes = dtype == TMM_F32 ? 3 : 1;
   const int cg = forward_shape(prm.rows, prm.groups, prm.N, prm.K, dtype);
   prm.panels = int((prm.N + 128 * cg - 1) / (128 * cg));
@@ -2569,7 +2727,9 @@ cudaError_t run_forward(int dtype, const Planes &x, const Stack &xs, const int32
   prm.p_mn = trans_w ? 0 : 1;
   prm.p_shared = prm.groups > 1 && ws.count == 1;
   Maps m = {};
-  if (direct(cg, dtype)) {
+  if (prm.K == 0) {
+    // Linear: nothing is read.
+  } else if (direct(cg, dtype)) {
     prm.q_rows = int(xs.rows);
     set_direct(&prm, ws, xs);
   } else {
@@ -2581,7 +2741,7 @@ cudaError_t run_forward(int dtype, const Planes &x, const Stack &xs, const int32
     m.e = m.p;
     m.u = m.q;
   }
-  return launch_any(cg, planes, kForward, m, prm, tiles, dev, stream);
+  return launch_any(cg, planes, mode, m, prm, tiles, dev, stream);
 }
 
 }  // namespace
@@ -2638,6 +2798,44 @@ cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void 
                      prm, dev, stream);
 }
 
+// A linear layer: the forward product of one group, with its epilogue.
+size_t linear_workspace_bytes(const LinearProblem &p) {
+  const int cg = forward_shape(p.rows, 1, p.N, p.K, p.dtype);
+  if (direct(cg, p.dtype) || p.K == 0) return 0;
+  return add_sizes({plane_bytes(p.x, p.dtype), plane_bytes(p.w, p.dtype)});
+}
+
+cudaError_t launch_linear(const LinearProblem &p, const DeviceInfo &dev, void *workspace,
+                          cudaStream_t stream) {
+  char *ws = static_cast<char *>(workspace);
+  Planes x = {}, w = {};
+  if (!direct(forward_shape(p.rows, 1, p.N, p.K, p.dtype), p.dtype) && p.K > 0) {
+    PlaneJobs jobs = {};
+    x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs);
+    w = plan_planes(p.w, p.dtype, nullptr, &ws, &jobs);
+    const cudaError_t e = make_planes(jobs, p.dtype, dev, stream);
+    if (e != cudaSuccess) return e;
+  }
+  Params prm = {};
+  prm.rows = int(p.rows);
+  prm.groups = 1;
+  prm.K = int(p.K);
+  prm.N = int(p.N);
+  prm.idesc = type_desc(p.dtype);
+  prm.out = p.y;
+  prm.ld_out = p.ldy;
+  prm.out_type = out_type(p.dtype);
+  prm.bias = p.bias;
+  prm.bias_f32 = p.bias_f32;
+  prm.act = p.act;
+  prm.residual = p.residual;
+  prm.ld_residual = p.residual ? p.ld_residual : 0;
+  prm.pre = p.pre;
+  prm.ld_pre = p.pre ? p.ld_pre : 0;
+  prm.epilogue = p.bias || p.residual || p.pre || p.act != TMM_ACT_NONE;
+  return run_forward(p.dtype, x, p.x, nullptr, w, p.w, p.trans_w != 0, prm, dev, stream, kLinear);
+}
+
 // Every 64 columns of x read the group's rows again.  (Single blocks, 4096 x 128, bf16, by number and
 // gathered: 128 rows of a group 6.6 us and 7.7 us, 512 of each of 8 44 us and 30 us.)
 static int64_t wgrad_gathered(const WgradProblem &p) {
@@ -2651,45 +2849,24 @@ size_t wgrad_workspace_bytes(const WgradProblem &p) {
        plane_bytes(p.dy, p.dtype)});
 }
 
-cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *workspace,
-                         cudaStream_t stream) {
-  char *ws = static_cast<char *>(workspace);
-  const int cg = wgrad_shape(p.N);
-  const int64_t gathered = wgrad_gathered(p);
-  const int32_t *index = gathered ? nullptr : p.row_index;
-  Planes x = {}, dy = {};
-  cudaError_t e;
-  if (!direct(cg, p.dtype)) {
-    PlaneJobs jobs = {};
-    x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs, gathered, p.row_index);
-    dy = plan_planes(p.dy, p.dtype, nullptr, &ws, &jobs);
-    if ((e = make_planes(jobs, p.dtype, dev, stream)) != cudaSuccess) return e;
-  }
-  const int planes = p.dtype == TMM_F32 ? 3 : 1;
-  Params prm = {};
-  prm.rows = int(p.rows);
-  prm.groups = int(p.groups);
-  prm.offsets = p.offsets;
+// The gradient's product on planes (or FP32 stacks directly); `cg` as the caller chose.
+static cudaError_t run_wgrad(int dtype, int cg, const Planes &x, const Stack &xs,
+                             const int32_t *index, const Planes &dy, const Stack &dys, Params prm,
+                             const DeviceInfo &dev, cudaStream_t stream) {
+  const int planes = dtype == TMM_F32 ? 3 : 1;
   prm.row_index = index;
-  prm.q_rows = int(gathered ? p.rows : p.x.rows);
-  prm.q_cols = int(p.K);
-  prm.N = int(p.N);
-  prm.idesc = type_desc(p.dtype);
-  prm.out = p.dw;
-  prm.ld_out = p.lddw;
-  prm.stride_out = p.groups > 1 ? p.stride_dw : 0;
-  prm.out_type = out_type(p.dtype);
   prm.n_out = prm.N;
   prm.ksplit = 1;
   const int bn = columns_of(cg, planes);
   prm.tile_n = bn;
-  prm.panels = int((p.N + 128 * cg - 1) / (128 * cg));
-  const int64_t tiles = p.groups * prm.panels * ((p.K + bn - 1) / bn);
+  prm.panels = int((prm.N + 128 * cg - 1) / (128 * cg));
+  const int64_t tiles = int64_t(prm.groups) * prm.panels * ((prm.q_cols + bn - 1) / bn);
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
-  if (cg == 1) prm.ksplit = split_of(tiles, (p.rows / p.groups + kBK - 1) / kBK, planes, dev);
+  if (cg == 1) prm.ksplit = split_of(tiles, (prm.rows / prm.groups + kBK - 1) / kBK, planes, dev);
   Maps m = {};
-  if (direct(cg, p.dtype)) {
-    set_direct(&prm, p.dy, p.x);
+  cudaError_t e;
+  if (direct(cg, dtype)) {
+    set_direct(&prm, dys, xs);
   } else {
     if ((e = row_map(&m.p, dy, kBK)) != cudaSuccess ||
         (e = row_map(&m.e, dy, 16)) != cudaSuccess || (e = row_map(&m.pr, dy, 1)) != cudaSuccess ||
@@ -2701,6 +2878,132 @@ cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *wor
       return e;
   }
   return launch_any(cg, planes, kWgrad, m, prm, tiles, dev, stream);
+}
+
+cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *workspace,
+                         cudaStream_t stream) {
+  char *ws = static_cast<char *>(workspace);
+  const int cg = wgrad_shape(p.N);
+  const int64_t gathered = wgrad_gathered(p);
+  Planes x = {}, dy = {};
+  if (!direct(cg, p.dtype)) {
+    PlaneJobs jobs = {};
+    x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs, gathered, p.row_index);
+    dy = plan_planes(p.dy, p.dtype, nullptr, &ws, &jobs);
+    const cudaError_t e = make_planes(jobs, p.dtype, dev, stream);
+    if (e != cudaSuccess) return e;
+  }
+  Params prm = {};
+  prm.rows = int(p.rows);
+  prm.groups = int(p.groups);
+  prm.offsets = p.offsets;
+  prm.q_rows = int(gathered ? p.rows : p.x.rows);
+  prm.q_cols = int(p.K);
+  prm.N = int(p.N);
+  prm.idesc = type_desc(p.dtype);
+  prm.out = p.dw;
+  prm.ld_out = p.lddw;
+  prm.stride_out = p.groups > 1 ? p.stride_dw : 0;
+  prm.out_type = out_type(p.dtype);
+  return run_wgrad(p.dtype, cg, x, p.x, gathered ? nullptr : p.row_index, dy, p.dy, prm, dev,
+                   stream);
+}
+
+// ---- a linear layer's gradients ------------------------------------------------------------
+
+namespace {
+
+// What the gradients' products run on: dz = dy act'(z) (dy itself without an activation), and the
+// operands of the two products in planes where they need them; the workspace holds them in order.
+struct LinearGradPlan {
+  Stack dz;
+  bool make_dz;
+  int cg_x, cg_w;                  // shapes of the products for dx and dw
+  bool planes_x, planes_w;         // whether they read planes (or operands in place)
+  Stack wx, wy;                    // dw's operands: its rows' and its columns' dimension
+  size_t dz_bytes, partial_bytes, bytes;
+};
+
+LinearGradPlan plan_linear_grad(const LinearGradProblem &p) {
+  LinearGradPlan g = {};
+  const int size = p.dtype == TMM_F32 ? 4 : 2;
+  g.make_dz = p.act != TMM_ACT_NONE && (p.dx || p.dw);
+  g.dz = p.dy;
+  if (g.make_dz) {
+    g.dz.ld = (p.N * size + 15) / 16 * 16 / size;
+    g.dz.stride = 0;
+    const __int128 n = __int128(p.rows) * g.dz.ld * size;
+    g.dz_bytes = n > __int128(INT64_MAX / 4) ? SIZE_MAX : round256(size_t(n));
+    g.dz.data = nullptr;           // the workspace's start, on 256 bytes
+  }
+  g.partial_bytes = p.dbias ? round256(linear_bias_bytes(p.rows, p.N, p.dtype)) : 0;
+  g.wx = p.trans_dw ? g.dz : p.x;
+  g.wy = p.trans_dw ? p.x : g.dz;
+  g.cg_x = forward_shape(p.rows, 1, p.K, p.N, p.dtype);
+  g.cg_w = wgrad_shape(g.wy.cols);
+  g.planes_x = p.dx && !direct(g.cg_x, p.dtype);
+  g.planes_w = p.dw && !direct(g.cg_w, p.dtype);
+  g.bytes = add_sizes({g.dz_bytes, g.partial_bytes,
+                       g.planes_x || g.planes_w ? plane_bytes(g.dz, p.dtype) : 0,
+                       g.planes_x ? plane_bytes(p.w, p.dtype) : 0,
+                       g.planes_w ? plane_bytes(p.x, p.dtype) : 0});
+  return g;
+}
+
+}  // namespace
+
+size_t linear_grad_workspace_bytes(const LinearGradProblem &p) {
+  return plan_linear_grad(p).bytes;
+}
+
+cudaError_t launch_linear_grad(const LinearGradProblem &p, const DeviceInfo &dev, void *workspace,
+                               cudaStream_t stream) {
+  LinearGradPlan g = plan_linear_grad(p);
+  char *ws = static_cast<char *>(workspace);
+  if (g.make_dz) {
+    g.dz.data = ws;
+    (p.trans_dw ? g.wx : g.wy).data = ws;
+    ws += g.dz_bytes;
+  }
+  cudaError_t e;
+  if (g.make_dz || p.dbias) {
+    e = launch_linear_slopes(p, g.make_dz ? const_cast<void *>(g.dz.data) : nullptr, g.dz.ld,
+                             reinterpret_cast<float *>(ws), dev, stream);
+    if (e != cudaSuccess) return e;
+  }
+  ws += g.partial_bytes;
+  PlaneJobs jobs = {};
+  Planes dz = {}, w = {}, x = {};
+  if (g.planes_x || g.planes_w) dz = plan_planes(g.dz, p.dtype, nullptr, &ws, &jobs);
+  if (g.planes_x) w = plan_planes(p.w, p.dtype, nullptr, &ws, &jobs);
+  if (g.planes_w) x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs);
+  if ((e = make_planes(jobs, p.dtype, dev, stream)) != cudaSuccess) return e;
+  Params prm = {};
+  prm.rows = int(p.rows);
+  prm.groups = 1;
+  prm.idesc = type_desc(p.dtype);
+  prm.out_type = out_type(p.dtype);
+  if (p.dx) {
+    Params q = prm;
+    q.K = int(p.N);
+    q.N = int(p.K);
+    q.out = p.dx;
+    q.ld_out = p.lddx;
+    e = run_forward(p.dtype, dz, g.dz, nullptr, w, p.w, !p.trans_w, q, dev, stream, kLinear);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.dw) {
+    Params q = prm;
+    q.q_rows = int(p.rows);
+    q.q_cols = int(g.wx.cols);
+    q.N = int(g.wy.cols);
+    q.out = p.dw;
+    q.ld_out = p.lddw;
+    e = run_wgrad(p.dtype, g.cg_w, p.trans_dw ? dz : x, g.wx, nullptr, p.trans_dw ? x : dz, g.wy, q,
+                  dev, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 template <typename T, bool TRANS_A>

@@ -53,12 +53,54 @@ struct LoraProblem {
   int64_t ldy;
 };
 
+// y = act(x w + bias) + residual, z = x w + bias.  trans_w: w is stored N x K.
+struct LinearProblem {
+  int dtype, act;
+  int64_t rows, K, N;
+  Stack x, w;
+  int trans_w;
+  const void *bias;             // N, or NULL
+  int bias_f32;                 // FP32, else of the operands' type
+  const void *residual;         // rows x N, or NULL
+  int64_t ld_residual;
+  void *y;
+  int64_t ldy;
+  void *pre;                    // z: rows x N, or NULL
+  int64_t ld_pre;
+};
+// dz = dy act'(z), dx = dz w^T, dw = x^T dz, dbias = the sum of dz's rows; any of the last three
+// NULL.
+struct LinearGradProblem {
+  int dtype, act;
+  int64_t rows, K, N;
+  Stack dy, x, w;
+  int trans_w;
+  const void *pre;              // z: rows x N (act other than none)
+  int64_t ld_pre;
+  void *dx;
+  int64_t lddx;
+  void *dw;                     // K x N, or N x K with trans_dw
+  int64_t lddw;
+  int trans_dw;
+  float *dbias;
+};
+
 // Workspace bytes (0: none needed; SIZE_MAX: the count does not fit in size_t).
 size_t grouped_workspace_bytes(const GroupedProblem &p);
 size_t wgrad_workspace_bytes(const WgradProblem &p);
 size_t lora_workspace_bytes(const LoraProblem &p);
+size_t linear_workspace_bytes(const LinearProblem &p);
+size_t linear_grad_workspace_bytes(const LinearGradProblem &p);
 
-// Sizes reaching a launcher are > 0.
+// Sizes reaching a launcher are > 0 (K of launch_linear may be 0).
+cudaError_t launch_linear(const LinearProblem &p, const DeviceInfo &dev, void *workspace,
+                          cudaStream_t stream);
+cudaError_t launch_linear_grad(const LinearGradProblem &p, const DeviceInfo &dev, void *workspace,
+                               cudaStream_t stream);
+// dz (rows x N, ldz; NULL: not written) and dbias; `partial`: linear_bias_bytes of scratch.
+size_t linear_bias_bytes(int64_t rows, int64_t N, int dtype);
+cudaError_t launch_linear_slopes(const LinearGradProblem &p, void *dz, int64_t ldz, float *partial,
+                                 const DeviceInfo &dev, cudaStream_t stream);
 cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void *workspace,
                            cudaStream_t stream);
 cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *workspace,
