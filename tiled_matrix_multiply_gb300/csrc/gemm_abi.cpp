@@ -332,7 +332,7 @@ int tmm_check_device(tmm_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess)
     return fail(TMM_ERR_CUDA, "tmm_check_device: cudaStreamSynchronize: %s", cudaGetErrorString(e));
-  unsigned int simt = 0, tc3 = 0, win = 0, sm = 0, naive = 0, stage = 0, grouped = 0;
+  unsigned int simt = 0, tc3 = 0, win = 0, sm = 0, naive = 0, stage = 0, grouped = 0, linear = 0;
   e = tmm::simt_device_status(&simt, true);
   if (e == cudaSuccess) e = tmm::tc3_device_status(&tc3, true);
   if (e == cudaSuccess) e = tmm::window_device_status(&win, true);
@@ -340,6 +340,7 @@ int tmm_check_device(tmm_stream_t stream) {
   if (e == cudaSuccess) e = tmm::naive_device_status(&naive, true);
   if (e == cudaSuccess) e = tmm::stage_device_status(&stage, true);
   if (e == cudaSuccess) e = tmm::grouped_device_status(&grouped, true);
+  if (e == cudaSuccess) e = tmm::linear_device_status(&linear, true);
   if (e != cudaSuccess)
     return fail(TMM_ERR_CUDA, "tmm_check_device: status read: %s", cudaGetErrorString(e));
   if ((simt | tc3 | naive | stage) & tmm::kStatusBounds)
@@ -349,7 +350,7 @@ int tmm_check_device(tmm_stream_t stream) {
                 : (stage & tmm::kStatusBounds) ? "gemm_f32 (operand restaging)"
                 : (tc3 & tmm::kStatusBounds)   ? "gemm_f32_tc3"
                                                : "gemm_f32_naive");
-  if (simt | tc3 | win | sm | grouped)
+  if (simt | tc3 | win | sm | grouped | linear)
     return fail(TMM_ERR_DEVICE_TIMEOUT,
                 "tmm_check_device: a bounded wait inside %s ran out of time; the affected "
                 "results are not valid",
@@ -357,6 +358,7 @@ int tmm_check_device(tmm_stream_t stream) {
                 : tc3     ? "gemm_f32_tc3"
                 : win     ? "window_sum_f32"
                 : grouped ? "a grouped product"
+                : linear  ? "a linear layer's product"
                           : "softmax_rows_f32");
   return TMM_OK;
 }
@@ -385,6 +387,7 @@ int tmm_testing_set_wait_hooks(int drop_signal_block, int64_t wait_limit_ns) {
   tmm::window_set_test_hooks(drop_signal_block, wait_limit_ns);
   tmm::softmax_set_test_hooks(drop_signal_block, wait_limit_ns);
   tmm::grouped_set_test_hooks(drop_signal_block, wait_limit_ns);
+  tmm::linear_set_test_hooks(drop_signal_block, wait_limit_ns);
   return TMM_OK;
 }
 

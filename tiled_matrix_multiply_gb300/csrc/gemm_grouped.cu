@@ -66,8 +66,9 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "activation.cuh"
 #include "grouped.h"
+#include "linear_epilogue.cuh"
+#include "tensor_core.cuh"
 #include "tmm_gemm.h"
 
 namespace tmm {
@@ -94,10 +95,8 @@ __device__ __forceinline__ int long_sum(int n) {
 constexpr uint32_t kPTile = 128 * 128;   // 128 lanes x 64 values: 16 KiB
 constexpr uint32_t kMaxSmem = 232448;    // 227 KiB
 
-// How the results are written.
-constexpr int kOutF32 = 0, kOutBF16 = 1, kOutF16 = 2;
+// How the results are written, beside kOutF32, kOutBF16 and kOutF16.
 constexpr int kOutU = 3;       // the adapters' u: its parts, in three planes or side by side
-
 
 // Values of `rank` per slice of the adapters' part: as many as the parts of u leave of the 64 columns
 // of a slice (store_u4), or FP32's planes.
@@ -197,245 +196,6 @@ struct Ring {
     }
   }
 };
-
-// ---- primitives -------------------------------------------------------------------------
-
-__device__ __forceinline__ uint32_t smem_u32(const void *p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ uint64_t timer_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-// On this block's own barrier (`bar`: its shared memory address).
-__device__ __forceinline__ void mbar_arrive_local(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// Of any block of the cluster, where no access to memory of this thread has to be ordered before
-// it.  (A cluster-wide release takes about 1500 cycles and waits for the thread's stores: result
-// warps handing tensor memory back, whose reads have completed, would wait for their results to
-// reach memory.)
-__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int64_t limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = timer_ns();
-  while (!mbar_try_wait(bar, parity))
-    if (int64_t(timer_ns() - t0) > limit_ns) return false;
-  return true;
-}
-// True in one thread of the (converged) warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
-               : "=r"(p));
-  return p != 0;
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-// Every thread of every block of the cluster.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
-// Tensor copies into this block's shared memory; `bar` counts their bytes (a shared::cluster
-// address, in pairs the leader's).
-template <int CG>
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y,
-                                       uint32_t bar) {
-  if constexpr (CG == 2)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
-                                       uint32_t bar) {
-  if constexpr (CG == 2)
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
-// Four rows y[0..3] of 64 values from column x.
-template <int CG>
-__device__ __forceinline__ void tma_rows4(uint32_t dst, const CUtensorMap *map, int x,
-                                          const int (&y)[4], uint32_t bar) {
-  if constexpr (CG == 2)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4"
-        ".mbarrier::complete_tx::bytes.cta_group::2"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
-        "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4"
-        ".mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
-        "r"(bar)
-        : "memory");
-}
-// Orders ordinary accesses to shared memory before the copy engine's and the tensor core's.
-__device__ __forceinline__ void proxy_fence() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
-// Programmatic dependent launch: wait for the grid before (its results, and those of the grids
-// before it, are visible then), and let the next one start as soon as there is room.  Every grid
-// starts the next one only after its own wait, so whatever is before the grid before is done
-// when a grid starts.
-__device__ __forceinline__ void grid_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void grid_start_next() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-template <int CG>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                    bool accumulate) {
-  if constexpr (CG == 2)
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %4, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(uint32_t(accumulate)), "r"(idesc)
-        : "memory");
-  else
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(uint32_t(accumulate)), "r"(idesc)
-        : "memory");
-}
-// Arrive on `bar` (of both blocks of a pair, with `both`) once the products issued so far by
-// this thread have completed.
-template <int CG>
-__device__ __forceinline__ void mma_commit(uint32_t bar, bool both) {
-  if constexpr (CG == 2)
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;" ::"r"(bar),
-        "h"(uint16_t(both ? 3 : 1))
-        : "memory");
-  else
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-        : "memory");
-}
-// Waits for this thread's tensor-memory loads.  The registers that they fill are operands, so that no
-// use of them, which depends on nothing else, is moved before the wait.
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[8], uint32_t (&s)[8]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(s[0]), "+r"(s[1]), "+r"(s[2]), "+r"(s[3]),
-                 "+r"(s[4]), "+r"(s[5]), "+r"(s[6]), "+r"(s[7])
-               :
-               : "memory");
-}
-// 8 consecutive FP32 columns of this thread's lane, there after tmem_wait.
-__device__ __forceinline__ void tmem_load_8(uint32_t addr, uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(addr)
-      : "memory");
-}
-// 16 of them, waited for.
-__device__ __forceinline__ void tmem_load_16(uint32_t addr, float (&v)[16]) {
-  uint32_t r[2][8];
-  tmem_load_8(addr, r[0]);
-  tmem_load_8(addr + 8, r[1]);
-  tmem_wait(r[0], r[1]);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i >> 3][i & 7]);
-}
-
-// 16 lanes x 16 consecutive FP32 columns, in the order of an 8 x 8 matrix instruction: r[4 c + 2 h]
-// and the one after it are columns 8 c + 2 (l % 4) and + 1 of lane 8 h + l / 4 (l: this thread).
-// The values are there after tmem_wait.
-__device__ __forceinline__ void tmem_load_matrices(uint32_t addr, uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(addr)
-      : "memory");
-}
-
-// Shared-memory matrix descriptor, 128-byte swizzle: start address >> 4 (bits 0-13), leading
-// byte offset >> 4 (16-29), stride byte offset >> 4 (32-45), version 1 (46-47), swizzle 2
-// (61-63).  A tile stored with K contiguous has rows of 64 values (128 bytes), eight of them
-// 1024 bytes apart (stride); 16 values of K are 32 bytes on.  A tile stored with n contiguous
-// is made of blocks of 64 n (128 bytes) x 64 k, 8 KiB apart (leading), eight k 1024 bytes
-// apart (stride); 16 values of K are 2048 bytes on.
-__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, bool mn) {
-  return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t(mn ? 512 : 1) << 16) | (uint64_t(64) << 32) |
-         (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
 
 // ---- tiles ------------------------------------------------------------------------------
 
@@ -852,125 +612,6 @@ __device__ __forceinline__ void store_columns(const Params &p, const Tile &t, in
     } else if (in && j < count && !(check && owner[t.q0 + c0 + j] == -2)) {
       store_out<MODE, PLANES>(p, first + j * p.ld_out, n, v[j] * scale);
     }
-  }
-}
-
-// ---- the epilogue of a linear layer ------------------------------------------------------
-
-// Element `at` of a matrix of the operands' type, in FP32.
-template <int PLANES>
-__device__ __forceinline__ float linear_value(const Params &p, const void *m, int64_t at) {
-  if constexpr (PLANES == 3) return static_cast<const float *>(m)[at];
-  if (p.out_type == kOutBF16) return float(static_cast<const __nv_bfloat16 *>(m)[at]);
-  return float(static_cast<const __half *>(m)[at]);
-}
-template <int PLANES>
-__device__ __forceinline__ float linear_bias(const Params &p, int n) {
-  if (p.bias == nullptr || n >= p.N) return 0.0f;
-  if (p.bias_f32) return static_cast<const float *>(p.bias)[n];
-  return linear_value<PLANES>(p, p.bias, n);
-}
-template <int PLANES>
-__device__ __forceinline__ void linear_store(const Params &p, void *m, int64_t at, float v) {
-  if constexpr (PLANES == 3)
-    static_cast<float *>(m)[at] = v;
-  else if (p.out_type == kOutBF16)
-    static_cast<__nv_bfloat16 *>(m)[at] = __float2bfloat16_rn(v);
-  else
-    static_cast<__half *>(m)[at] = __float2half_rn(v);
-}
-// One result: z = the sum and the bias.
-template <int PLANES>
-__device__ __forceinline__ void linear_one(const Params &p, int64_t row, int n, float z) {
-  if (p.pre) linear_store<PLANES>(p, p.pre, row * p.ld_pre + n, z);
-  float y = activate<PLANES == 1>(p.act, z);
-  if (p.residual) y += linear_value<PLANES>(p, p.residual, row * p.ld_residual + n);
-  linear_store<PLANES>(p, p.out, row * p.ld_out + n, y);
-}
-__device__ __forceinline__ uint32_t pack_results(const Params &p, float lo, float hi) {
-  uint32_t w;
-  if (p.out_type == kOutBF16)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
-  return w;
-}
-__device__ __forceinline__ float2 unpack_values(const Params &p, uint32_t w) {
-  if (p.out_type == kOutBF16)
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-}
-
-// 16 columns (rows of the result) from c0 on of the warp's 32 n.  In FP32 a lane has its n in all of
-// them, 128 bytes of a row a warp.  16-bit results go through 2 KiB of shared memory a warp as FP32,
-// 16 rows of 32 n, of which a lane then has two pieces of 8 n: everything read and written is 16
-// bytes a lane.  The bias of those 8 n (or of the lane's one) is in `bias`.
-template <int PLANES>
-__device__ __forceinline__ void linear_columns(const Params &p, const Tile &t, int c0, int nw,
-                                               const float (&v)[16], const float (&bias)[8],
-                                               uint32_t stage) {
-  const int lane = threadIdx.x & 31;
-  const int count = min(16, t.qn - c0);
-  const int64_t first = t.q0 + c0;
-  if (PLANES == 3 || !p.vec_out) {
-    const int n = nw + lane;
-    if (n < p.N)
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (j < count) linear_one<PLANES>(p, first + j, n, v[j] + bias[0]);
-    return;
-  }
-  // Chunk c of four n of row r is at r * 128 + 16 (c ^ r % 8): free of bank conflicts both ways.
-  __syncwarp();      // the reads of the block before are done
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage + j * 128 + (((lane >> 2) ^ (j & 7)) << 4) +
-                                                 (lane & 3) * 4),
-                 "f"(v[j])
-                 : "memory");
-  __syncwarp();
-  const int piece = lane & 3, n8 = nw + piece * 8;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = (lane >> 2) + 8 * i;
-    float z[8];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(z[4 * h]), "=f"(z[4 * h + 1]), "=f"(z[4 * h + 2]), "=f"(z[4 * h + 3])
-                   : "r"(stage + row * 128 + (((2 * piece + h) ^ (row & 7)) << 4))
-                   : "memory");
-    if (row >= count || n8 >= p.N) continue;
-    const int64_t r = first + row;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) z[k] += bias[k];
-    if (n8 + 8 > p.N) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (n8 + k < p.N) linear_one<PLANES>(p, r, n8 + k, z[k]);
-      continue;
-    }
-    uint4 res = make_uint4(0, 0, 0, 0);
-    if (p.residual)
-      res = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.residual) +
-                                             r * p.ld_residual + n8);
-    if (p.pre)
-      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.pre) + r * p.ld_pre + n8) =
-          make_uint4(pack_results(p, z[0], z[1]), pack_results(p, z[2], z[3]),
-                     pack_results(p, z[4], z[5]), pack_results(p, z[6], z[7]));
-    activate_all<8>(p.act, z);
-    if (p.residual) {
-      const uint32_t w[4] = {res.x, res.y, res.z, res.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 a = unpack_values(p, w[k]);
-        z[2 * k] += a.x;
-        z[2 * k + 1] += a.y;
-      }
-    }
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + r * p.ld_out + n8) =
-        make_uint4(pack_results(p, z[0], z[1]), pack_results(p, z[2], z[3]),
-                   pack_results(p, z[4], z[5]), pack_results(p, z[6], z[7]));
   }
 }
 
@@ -1902,7 +1543,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           }
           if (p.ksplit == 1) store_columns<MODE, PLANES>(p, tile, c0, nw, w, scale, stage, owner);
         } else if (linear) {
-          linear_columns<PLANES>(p, tile, c0, nw, v, bias, stage);
+          linear_columns<PLANES>(p, tile.q0 + c0, tile.qn - c0, nw, v, bias, stage);
         } else {
           store_columns<MODE, PLANES>(p, tile, c0, nw, v, scale, stage, owner);
         }
@@ -2798,7 +2439,12 @@ cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void 
                      prm, dev, stream);
 }
 
-// A linear layer: the forward product of one group, with its epilogue.
+// A linear layer: in 16 bits a product of its own (gemm_linear.cu) on operands in place or restaged;
+// in FP32, and for sums longer than that kernel's, the forward product of one group with the epilogue.
+static DenseOperand dense_operand(const Planes &o, bool mn) {
+  return {o.data, o.rows, o.cols, o.ld, mn ? 1 : 0};
+}
+
 size_t linear_workspace_bytes(const LinearProblem &p) {
   const int cg = forward_shape(p.rows, 1, p.N, p.K, p.dtype);
   if (direct(cg, p.dtype) || p.K == 0) return 0;
@@ -2815,6 +2461,13 @@ cudaError_t launch_linear(const LinearProblem &p, const DeviceInfo &dev, void *w
     w = plan_planes(p.w, p.dtype, nullptr, &ws, &jobs);
     const cudaError_t e = make_planes(jobs, p.dtype, dev, stream);
     if (e != cudaSuccess) return e;
+  }
+  if (p.dtype != TMM_F32 && p.K > 0) {
+    const DenseProblem d = {p.dtype, p.rows, p.N, p.K, dense_operand(w, !p.trans_w),
+                            dense_operand(x, false), p.y, p.ldy, p.bias, p.bias_f32, p.act,
+                            p.residual, p.ld_residual, p.pre, p.ld_pre};
+    const cudaError_t e = launch_dense(d, dev, stream);
+    if (e != cudaErrorNotSupported) return e;
   }
   Params prm = {};
   prm.rows = int(p.rows);
@@ -2983,7 +2636,26 @@ cudaError_t launch_linear_grad(const LinearGradProblem &p, const DeviceInfo &dev
   prm.groups = 1;
   prm.idesc = type_desc(p.dtype);
   prm.out_type = out_type(p.dtype);
+  // In 16 bits every operand is in place or has been restaged.
+  const auto dense = [&](int64_t M, int64_t N, int64_t K, const DenseOperand &a,
+                         const DenseOperand &b, void *out, int64_t ld) {
+    if (p.dtype == TMM_F32) return cudaErrorNotSupported;
+    DenseProblem d = {};
+    d.dtype = p.dtype;
+    d.M = M;
+    d.N = N;
+    d.K = K;
+    d.p = a;
+    d.q = b;
+    d.out = out;
+    d.ld_out = ld;
+    return launch_dense(d, dev, stream);
+  };
   if (p.dx) {
+    e = dense(p.rows, p.K, p.N, dense_operand(w, p.trans_w), dense_operand(dz, false), p.dx, p.lddx);
+    if (e != cudaErrorNotSupported && e != cudaSuccess) return e;
+  }
+  if (p.dx && e == cudaErrorNotSupported) {
     Params q = prm;
     q.K = int(p.N);
     q.N = int(p.K);
@@ -2993,6 +2665,11 @@ cudaError_t launch_linear_grad(const LinearGradProblem &p, const DeviceInfo &dev
     if (e != cudaSuccess) return e;
   }
   if (p.dw) {
+    e = dense(g.wx.cols, g.wy.cols, p.rows, dense_operand(p.trans_dw ? x : dz, true),
+              dense_operand(p.trans_dw ? dz : x, true), p.dw, p.lddw);
+    if (e != cudaErrorNotSupported && e != cudaSuccess) return e;
+  }
+  if (p.dw && e == cudaErrorNotSupported) {
     Params q = prm;
     q.q_rows = int(p.rows);
     q.q_cols = int(g.wx.cols);

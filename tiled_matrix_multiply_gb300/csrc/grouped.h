@@ -85,6 +85,32 @@ struct LinearGradProblem {
   float *dbias;
 };
 
+// One dense product of 16-bit operands that the copy engine can read: out[q, n] = sum_k P[n, k]
+// Q[q, k] for n < N, q < M, with a linear layer's epilogue.
+struct DenseOperand {
+  const void *data;             // rows x cols as stored, 16-byte rows
+  int64_t rows, cols, ld;
+  int mn;                       // stored k x own dimension (else own dimension x k)
+};
+struct DenseProblem {
+  int dtype;                    // TMM_BF16, TMM_F16
+  int64_t M, N, K;
+  DenseOperand p, q;
+  void *out;
+  int64_t ld_out;
+  const void *bias;             // as in LinearProblem
+  int bias_f32, act;
+  const void *residual;
+  int64_t ld_residual;
+  void *pre;
+  int64_t ld_pre;
+};
+// cudaErrorNotSupported: a product that its shapes do not fit (sums of more than 8192 values that
+// cannot be shared); nothing has been launched.
+cudaError_t launch_dense(const DenseProblem &p, const DeviceInfo &dev, cudaStream_t stream);
+cudaError_t linear_device_status(unsigned int *status, bool clear);
+void linear_set_test_hooks(int drop_block, int64_t wait_limit_ns);
+
 // Workspace bytes (0: none needed; SIZE_MAX: the count does not fit in size_t).
 size_t grouped_workspace_bytes(const GroupedProblem &p);
 size_t wgrad_workspace_bytes(const WgradProblem &p);
