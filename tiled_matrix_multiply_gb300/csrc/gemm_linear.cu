@@ -9,14 +9,15 @@
 //
 // Two shapes, chosen by an estimate of their cycles (dense_shape):
 //   pairs  (CG = 2): 256 lanes x up to 256 columns on two SMs (cta_group::2), each staging half of
-//          the columns.  Tensor memory holds two tiles, so that one's results leave it while the next
-//          is summed.  For large products.
-//   single (CG = 1): 128 lanes x up to 256 columns; where tiles are few, up to eight blocks of a
-//          cluster share a tile's sum, leave their parts in their shared memory (where the ring was)
-//          and each finish a share of the columns.  Reading the weights is the bound then, and more
-//          blocks read faster.
+//          the columns;
+//   single (CG = 1): 128 lanes x up to 256 columns.
+// Persistent where tiles are many: tensor memory holds two, so that one's results leave it while the
+// next is summed.  Where they are few, the blocks of a cluster of up to eight share a tile's sum: each
+// leaves its part in its shared memory (where the ring was) and finishes a share of the columns.
+// Reading the weights is the bound then, and more blocks read faster.
 // A warp copies (one thread: tensor copies into a ring of stages), one issues the products (one
-// thread), eight take results out.  Every wait is bounded (globaltimer); on timeout bit 1 of the
+// thread), sixteen take results out (with eight the results of a tile of one slice took 3.9 us, with
+// sixteen 2.9).  Every wait is bounded (globaltimer); on timeout bit 1 of the
 // status word is set and the kernel runs to its end.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -25,6 +26,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <mutex>
 
 #include "grouped.h"
 #include "linear_epilogue.cuh"
@@ -38,11 +40,12 @@ __device__ unsigned int g_linear_status;
 namespace {
 
 constexpr int kBK = 64;                  // values of a K slice: one 128-byte swizzle row
-constexpr int kEpiWarps = 8, kEpi0 = 2;  // result warps, the first of them
+constexpr int kEpiWarps = 16, kEpi0 = 2;  // result warps, the first of them
 constexpr int kThreads = 32 * (kEpi0 + kEpiWarps);
 constexpr uint32_t kPTile = 128 * 128;   // 128 lanes x 64 values: 16 KiB
 constexpr int kWidest = 256;             // columns of a tile, and of one of the two sums
 constexpr int kMaxStages = 10;
+constexpr int kShare = kWidest / 2 / kEpiWarps;      // columns of a thread in a shared sum, at most
 constexpr int kOutStage = 2048;          // bytes of a result warp
 constexpr uint32_t kMaxSmem = 232448;    // 227 KiB
 constexpr uint32_t kFixed = 1024 + kEpiWarps * kOutStage + 8 * (2 * kMaxStages + 5) + 16;
@@ -110,6 +113,178 @@ __device__ __forceinline__ void finish_four(const Params &p, int64_t row, int n,
       make_uint2(pack_results(p, z[0], z[1]), pack_results(p, z[2], z[3]));
 }
 
+// ---- one thread's instructions, issued by a whole warp ------------------------------------
+//
+// The copying and the multiplying warp run their loops as warps, and the one thread that acts is a
+// predicate of the instruction: descriptors, addresses and counters then stay in the uniform registers
+// that these instructions take.  (With the loops in a branch of one thread a product took 50 cycles to
+// issue, 310 cycles a slice with its waits.)
+
+template <int CG>
+__device__ __forceinline__ void copy_if(uint32_t on, uint32_t dst, const CUtensorMap *map, int x,
+                                        int y, uint32_t bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n"
+        " @p cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(on)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n"
+        " @p cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void expect_if(uint32_t on, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n"
+      " @p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(bar),
+      "r"(bytes), "r"(on)
+      : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void mma_if(uint32_t on, uint32_t d, uint64_t a, uint64_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %3, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %4, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(accumulate), "r"(idesc), "r"(on)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %3, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(accumulate), "r"(idesc), "r"(on)
+        : "memory");
+}
+// Arrive on `bar` of this block (of both blocks of the pair whose first has rank `head`) once the
+// products issued so far by the thread have completed.
+template <int CG>
+__device__ __forceinline__ void commit_if(uint32_t on, uint32_t bar, uint32_t head) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n"
+        " @p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+        ".multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(bar),
+        "h"(uint16_t(3u << head)), "r"(on)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %1, 0;\n"
+        " @p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+            bar),
+        "r"(on)
+        : "memory");
+}
+// Whether the phase has passed already, for a look ahead.
+__device__ __forceinline__ bool mbar_passed(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// A wait of a whole warp; the same answer in all lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int64_t limit_ns) {
+  if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = timer_ns();
+  while (!__all_sync(~0u, mbar_try_wait(bar, parity)))
+    if (__any_sync(~0u, int64_t(timer_ns() - t0) > limit_ns)) return false;
+  return true;
+}
+
+// ---- results in 16 bits --------------------------------------------------------------------
+
+// 16 columns of a tile (rows of the result) for the 32 n of a warp, all of them inside the result, as
+// tmem_load_matrices leaves lanes 16 i to 16 i + 15 in f[i]: pairs of neighbouring columns of one n,
+// which the bias, the activation and the residual are added to as they are.  Matrix instructions
+// transpose 16-bit values on their way to shared memory (results) and from it (the residual), so that
+// memory is read and written 16 bytes a lane: about 45 instructions and the activation's, where
+// values staged in FP32 took 260.
+template <typename Params>
+__device__ __forceinline__ void finish_block(const Params &p, int64_t row0, int nw,
+                                             const uint32_t (&f)[2][8], const float (&bias)[4],
+                                             const uint4 (&residual)[2], uint32_t stage) {
+  const int lane = threadIdx.x & 31;
+  const auto piece = [&](uint32_t at, int row, int c) {      // free of bank conflicts
+    return at + uint32_t(row * 64 + ((c ^ (row >> 1 & 3)) << 4));
+  };
+  uint64_t z[2][4];      // [8 columns][8 n]
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      z[c][m] = add2(pair_of(__uint_as_float(f[m >> 1][4 * c + 2 * (m & 1)]),
+                             __uint_as_float(f[m >> 1][4 * c + 2 * (m & 1) + 1])),
+                     both(bias[m]));
+  __syncwarp();      // the reads of the block before are done
+  if (p.residual) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                       piece(stage + 1024, (lane >> 2) + 8 * i, lane & 3)),
+                   "r"(residual[i].x), "r"(residual[i].y), "r"(residual[i].z), "r"(residual[i].w)
+                   : "memory");
+    __syncwarp();
+  }
+  // The matrices' rows: 8 c + lane % 8, n from 8 (lane / 8) on.
+  const auto put = [&](uint16_t *to, int64_t ld) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t h[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const float2 v = of_pair(z[c][m]);
+        h[m] = pack_results(p, v.x, v.y);
+      }
+      asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                       piece(stage, 8 * c + (lane & 7), lane >> 3)),
+                   "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                   : "memory");
+    }
+    __syncwarp();
+    uint16_t *const dst = to + (row0 + (lane >> 2)) * ld + nw + (lane & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint4 w;
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                   : "r"(piece(stage, (lane >> 2) + 8 * i, lane & 3))
+                   : "memory");
+      *reinterpret_cast<uint4 *>(dst + i * 8 * ld) = w;
+    }
+  };
+  if (p.pre) {
+    put(static_cast<uint16_t *>(p.pre), p.ld_pre);
+    __syncwarp();
+  }
+  activate_pairs(p.act, z[0]);
+  activate_pairs(p.act, z[1]);
+  if (p.residual) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t r[4];
+      asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                   : "r"(piece(stage + 1024, 8 * c + (lane & 7), lane >> 3))
+                   : "memory");
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const float2 v = unpack_values(p, r[m]);
+        z[c][m] = add2(z[c][m], pair_of(v.x, v.y));
+      }
+    }
+  }
+  put(static_cast<uint16_t *>(p.out), p.ld_out);
+}
+
 template <int CG, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
 dense_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
@@ -126,10 +301,19 @@ dense_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
   const uint32_t bar_tempty = bar_tfull + 16;      // pairs: used in the leader
   const uint32_t bar_drain = bar_tempty + 16;
   const uint32_t slot = bar_drain + 8;             // tensor memory address
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
+  // Of a cluster's blocks, CG make a tile's part, ksplit parts its sum.
   const uint32_t rank = cluster_rank();
-  const bool leader = CG == 1 || rank == 0;
-  const int half = CG == 2 ? int(rank) : 0;        // which 128 lanes, which half of the columns
+  const int half = CG == 2 ? int(rank & 1) : 0;    // which 128 lanes, which half of the columns
+  const int part = int(rank) / CG;                 // of the sum
+  const uint32_t head = rank - half;               // the pair's leader
+  const bool leader = half == 0;
+  const int share = CG * p.ksplit;                 // blocks of a tile
+  const int first = int(blockIdx.x) / share, step = int(gridDim.x) / share;
+  const int tiles = p.panels * p.q_tiles;
+  const int all = (p.K + kBK - 1) / kBK;           // slices, [s0, s1) of them this block's
+  const int s0 = all * part / p.ksplit, s1 = all * (part + 1) / p.ksplit;
+  DenseTile tile = tile_at(p, first, 128 * CG);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -165,170 +349,209 @@ dense_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
   grid_wait();
   grid_start_next();
 
-  const int share = CG == 2 ? 2 : p.ksplit;        // blocks of a tile
-  const int first = int(blockIdx.x) / share, step = int(gridDim.x) / share;
-  const int tiles = p.panels * p.q_tiles;
-  const int all = (p.K + kBK - 1) / kBK;           // slices, [s0, s1) of them this block's
-  const int s0 = CG == 2 ? 0 : int(int64_t(all) * rank / p.ksplit);
-  const int s1 = CG == 2 ? all : int(int64_t(all) * (rank + 1) / p.ksplit);
   bool timed_out = false;
   uint32_t q = 0;                                  // tiles so far
 
   if (warp == 0) {
     // ---- copies ----
-    if (elect_one()) {
-      bool dropped = int(blockIdx.x) == p.drop_block;
-      int stage = 0;
-      uint32_t parity = 1;
-      for (int t = first; t < tiles && !timed_out; t += step) {
-        const DenseTile tile = tile_at(p, t, 128 * CG);
-        const int n0 = tile.n0 + 128 * half, q0 = tile.q0 + mine * half;
-        for (int s = s0; s < s1; ++s) {
-          if (!mbar_wait(bar_empty + 8 * stage, parity, p.wait_limit_ns)) {
-            timed_out = true;
-            break;
-          }
-          const uint32_t to = base + stage * stage_bytes, k0 = s * kBK;
-          uint32_t bar = bar_full + 8 * stage;
-          if (leader) {
-            mbar_expect(bar, CG * stage_bytes + (dropped ? 16 : 0));
-            dropped = false;
-          }
-          if (CG == 2) bar = map_rank(bar, 0);
-          if (p.p_mn) {
-            tma_2d<CG>(to, &map_p, n0, k0, bar);
-            tma_2d<CG>(to + 8192, &map_p, n0 + 64, k0, bar);
-          } else {
-            tma_2d<CG>(to, &map_p, k0, n0, bar);
-          }
-          if (p.q_mn) {
-            for (int c = 0; c < mine; c += 64)
-              tma_2d<CG>(to + kPTile + c * 128, &map_q, q0 + c, k0, bar);
-          } else {
-            tma_2d<CG>(to + kPTile, &map_q, k0, q0, bar);
-          }
-          if (++stage == p.stages) {
-            stage = 0;
-            parity ^= 1;
-          }
+    const uint32_t on = elect_one(), lead = on && leader;
+    const uint32_t bytes = CG * stage_bytes;
+    uint32_t extra = int(blockIdx.x) == p.drop_block ? 16 : 0;
+    int stage = 0;
+    uint32_t parity = 1;
+    bool ahead = false;      // the next stage is known to be free
+    for (int t = first; t < tiles && !timed_out;) {
+      const int n0 = tile.n0 + 128 * half, q0 = tile.q0 + mine * half;
+      for (int s = s0; s < s1; ++s) {
+        if (!ahead && !warp_wait(bar_empty + 8 * stage, parity, p.wait_limit_ns)) {
+          timed_out = true;
+          break;
         }
+        const uint32_t to = base + stage * stage_bytes;
+        const int k0 = s * kBK;
+        uint32_t bar = bar_full + 8 * stage;
+        expect_if(lead, bar, bytes + extra);
+        extra = 0;
+        if (CG == 2) bar = map_rank(bar, head);
+        if (++stage == p.stages) {
+          stage = 0;
+          parity ^= 1;
+        }
+        const bool next = mbar_passed(bar_empty + 8 * stage, parity);
+        if (p.p_mn) {
+          copy_if<CG>(on, to, &map_p, n0, k0, bar);
+          copy_if<CG>(on, to + 8192, &map_p, n0 + 64, k0, bar);
+        } else {
+          copy_if<CG>(on, to, &map_p, k0, n0, bar);
+        }
+        if (p.q_mn) {
+          for (int c = 0; c < mine; c += 64)
+            copy_if<CG>(on, to + kPTile + c * 128, &map_q, q0 + c, k0, bar);
+        } else {
+          copy_if<CG>(on, to + kPTile, &map_q, k0, q0, bar);
+        }
+        ahead = __all_sync(~0u, next);
       }
+      if ((t += step) < tiles) tile = tile_at(p, t, 128 * CG);
     }
-    __syncwarp();
   } else if (warp == 1) {
     // ---- products ----
-    if (leader && elect_one()) {
+    if (leader) {
+      const uint32_t on = elect_one();
       const uint32_t idesc = p.idesc | (uint32_t(p.bn >> 3) << 17) |
                              (uint32_t(128 * CG >> 4) << 24) | (p.p_mn ? 1u << 15 : 0u) |
                              (p.q_mn ? 1u << 16 : 0u);
       const uint32_t pstep = p.p_mn ? 128 : 2, qstep = p.q_mn ? 128 : 2;   // 16 k, in 16 bytes
       int stage = 0;
       uint32_t parity = 0;
+      bool ahead = false;    // the next stage is known to be full
       for (int t = first; t < tiles && !timed_out; t += step, ++q) {
         const uint32_t d = tmem + (q & 1) * kWidest;
         if (q >= 2 &&
-            !mbar_wait(bar_tempty + 8 * (q & 1), ((q >> 1) - 1) & 1u, p.wait_limit_ns)) {
+            !warp_wait(bar_tempty + 8 * (q & 1), ((q >> 1) - 1) & 1u, p.wait_limit_ns)) {
           timed_out = true;
           break;
         }
         tc_fence_after();
         for (int s = s0; s < s1; ++s) {
-          if (!mbar_wait(bar_full + 8 * stage, parity, p.wait_limit_ns)) {
+          if (!ahead && !warp_wait(bar_full + 8 * stage, parity, p.wait_limit_ns)) {
             timed_out = true;
             break;
           }
           tc_fence_after();
-          const uint32_t at = base + stage * stage_bytes;
+          const uint32_t at = base + stage * stage_bytes, empty = bar_empty + 8 * stage;
           const uint64_t a = tile_desc(at, p.p_mn), b = tile_desc(at + kPTile, p.q_mn);
           const int steps = min(4, (p.K - s * kBK + 15) / 16);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < steps) mma<CG>(d, a + k * pstep, b + k * qstep, idesc, s > s0 || k > 0);
-          mma_commit<CG>(bar_empty + 8 * stage, true);
           if (++stage == p.stages) {
             stage = 0;
             parity ^= 1;
           }
+          const bool next = mbar_passed(bar_full + 8 * stage, parity);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < steps) mma_if<CG>(on, d, a + k * pstep, b + k * qstep, idesc, s > s0 || k > 0);
+          commit_if<CG>(on, empty, head);
+          ahead = __all_sync(~0u, next);
         }
-        if (!timed_out) mma_commit<CG>(bar_tfull + 8 * (q & 1), true);
+        if (!timed_out) commit_if<CG>(on, bar_tfull + 8 * (q & 1), head);
       }
-      mma_commit<CG>(bar_drain, false);
-      if (!mbar_wait(bar_drain, 0u, p.wait_limit_ns)) timed_out = true;
+      commit_if<CG>(on, bar_drain, head);
     }
-    __syncwarp();
+    if (!warp_wait(bar_drain, 0u, p.wait_limit_ns)) timed_out = true;
   } else {
     // ---- results ----
-    const int quarter = warp & 3, odd = (warp - kEpi0) >> 2;
+    const int quarter = warp & 3, turn = (warp - kEpi0) >> 2;
     const uint32_t lanes = tmem + (uint32_t(32 * quarter) << 16);
-    const uint32_t tempty = CG == 2 ? map_rank(bar_tempty, 0) : bar_tempty;
+    const uint32_t tempty = CG == 2 ? map_rank(bar_tempty, head) : bar_tempty;
     const uint32_t stage = out_stage + uint32_t(warp - kEpi0) * kOutStage;
     float *const parts = reinterpret_cast<float *>(smem_raw + (base - raw));
-    for (int t = first; t < tiles; t += step, ++q) {
-      const DenseTile tile = tile_at(p, t, 128 * CG);
+    for (int t = first; t < tiles; ++q) {
       const int nw = tile.n0 + 128 * half + 32 * quarter, left = p.M - tile.q0;
-      const bool split = CG == 1 && p.ksplit > 1;
-      float bias[8] = {};
+      const bool split = p.ksplit > 1;
+      // Whole blocks of 16 columns and 32 n, all of it on 16-byte rows; else one value at a time.
+      const bool whole = p.vec_out && nw + 32 <= p.N;
+      float bias[4] = {};
       if (p.bias && !split) {
-        if (p.vec_out) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) bias[k] = linear_bias<1>(p, nw + (lane & 3) * 8 + k);
-        } else {
-          bias[0] = linear_bias<1>(p, nw + lane);
-        }
+        for (int k = 0; k < 4; ++k)
+          bias[k] = linear_bias<1>(p, whole ? nw + 8 * k + (lane >> 2) : nw + lane);
       }
+      const auto load_residual = [&](int c0, uint4 (&r)[2]) {
+        if (p.residual == nullptr || split || !whole || c0 >= p.bn || left - c0 < 16) return;
+        const uint16_t *const from = static_cast<const uint16_t *>(p.residual) +
+                                     (tile.q0 + c0 + (lane >> 2)) * p.ld_residual + nw +
+                                     (lane & 3) * 8;
+        r[0] = *reinterpret_cast<const uint4 *>(from);
+        r[1] = *reinterpret_cast<const uint4 *>(from + 8 * p.ld_residual);
+      };
+      uint4 residual[2];
+      load_residual(16 * turn, residual);
       const bool ready = mbar_wait(bar_tfull + 8 * (q & 1), (q >> 1) & 1u, p.wait_limit_ns);
       if (!__all_sync(~0u, ready)) {
         timed_out = true;
         break;
       }
       tc_fence_after();
-      for (int c0 = 16 * odd; c0 < p.bn && c0 < left; c0 += 32) {
-        float v[16];
+      const uint32_t sums = lanes + (q & 1) * kWidest;
+      for (int c0 = 16 * turn; c0 < p.bn && c0 < left; c0 += 4 * kEpiWarps) {
         __syncwarp();
-        tmem_load_16(lanes + (q & 1) * kWidest + c0, v);
+        if (!split && whole && left - c0 >= 16) {
+          uint32_t f[2][8];
+          tmem_load_matrices(sums + c0, f[0]);
+          tmem_load_matrices(sums + c0 + (16u << 16), f[1]);
+          uint4 next[2];
+          load_residual(c0 + 4 * kEpiWarps, next);
+          tmem_wait(f[0], f[1]);
+          finish_block(p, tile.q0 + c0, nw, f, bias, residual, stage);
+          residual[0] = next[0];
+          residual[1] = next[1];
+          continue;
+        }
+        float v[16];
+        tmem_load_16(sums + c0, v);
         if (split) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) parts[(c0 + j) * 128 + 32 * quarter + lane] = v[j];
-        } else {
-          linear_columns<1>(p, tile.q0 + c0, left - c0, nw, v, bias, stage);
+        } else if (nw + lane < p.N) {
+          const float b = whole ? linear_bias<1>(p, nw + lane) : bias[0];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (j < left - c0) linear_one<1>(p, tile.q0 + c0 + j, nw + lane, v[j] + b);
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_relaxed(tempty + 8 * (q & 1));
+      // (Only where it is waited for: no arrival is under way when the pair's blocks end.)
+      if (lane == 0 && t + 2 * step < tiles) mbar_arrive_relaxed(tempty + 8 * (q & 1));
+      if ((t += step) < tiles) tile = tile_at(p, t, 128 * CG);
     }
   }
 
-  if (CG == 1 && p.ksplit > 1) {
-    // One tile, in parts of the sum: each block adds a share of its columns, in block order.
+  if (p.ksplit > 1) {
+    // One tile, in parts of the sum: each block adds up a share of its columns, in the parts' order,
+    // from the memory of the blocks that have the same lanes.
     __syncwarp();
     cluster_sync();
+    const int qn = min(p.bn, p.M - tile.q0);
+    const int c0 = qn * part / p.ksplit, c1 = qn * (part + 1) / p.ksplit;
+    const int tid = int(threadIdx.x) - 32 * kEpi0, n = tile.n0 + 128 * half + (tid & 31) * 4;
+    float z[kShare][4];
     if (warp >= kEpi0) {
-      const DenseTile tile = tile_at(p, first, 128);
-      const int qn = min(p.bn, p.M - tile.q0);
-      const int c0 = qn * int(rank) / p.ksplit, c1 = qn * int(rank + 1) / p.ksplit;
-      const int tid = int(threadIdx.x) - 32 * kEpi0, n = tile.n0 + (tid & 31) * 4;
+#pragma unroll
+      for (int i = 0; i < kShare; ++i) z[i][0] = z[i][1] = z[i][2] = z[i][3] = 0.0f;
+      const uint32_t mine = base + uint32_t((c0 + (tid >> 5)) * 512 + (tid & 31) * 16);
+      for (int r = 0; r < p.ksplit; ++r) {
+        const uint32_t from = map_rank(mine, uint32_t(CG * r + half));
+#pragma unroll
+        for (int i = 0; i < kShare; ++i)
+          if (c0 + (tid >> 5) + i * kEpiWarps < c1) {
+            const float4 v = ld_cluster4(from + i * kEpiWarps * 512);
+            z[i][0] += v.x;
+            z[i][1] += v.y;
+            z[i][2] += v.z;
+            z[i][3] += v.w;
+          }
+      }
+    }
+    // The others may leave once their parts have been read; what is left needs none of them (and a
+    // barrier after the results would wait for them to reach memory, 1500 cycles).
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    if (warp >= kEpi0) {
       float bias[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) bias[k] = linear_bias<1>(p, n + k);
-      for (int c = c0 + (tid >> 5); c < c1; c += kEpiWarps) {
-        float z[4] = {};
-#pragma unroll 4
-        for (int r = 0; r < p.ksplit; ++r) {
-          const float4 v =
-              ld_cluster4(map_rank(base, uint32_t(r)) + uint32_t(c * 512 + (tid & 31) * 16));
-          z[0] += v.x;
-          z[1] += v.y;
-          z[2] += v.z;
-          z[3] += v.w;
-        }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) z[k] += bias[k];
-        finish_four(p, tile.q0 + c, n, z);
+      for (int i = 0; i < kShare; ++i) {
+        const int c = c0 + (tid >> 5) + i * kEpiWarps;
+        if (c >= c1) break;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[i][k] += bias[k];
+        finish_four(p, tile.q0 + c, n, z[i]);
       }
     }
     __syncwarp();
-    cluster_sync();
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
   }
   if (timed_out && lane == 0) atomicOr(&g_linear_status, 2u);
   tc_fence_before();
@@ -339,7 +562,12 @@ dense_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
     while (timer_ns() - t0 < 1000 * 1000) {
     }
   }
-  if (CG == 2) cluster_sync();   // remote arrivals have landed; neither block uses tensor memory
+  // Neither block uses tensor memory or the other's barriers.  (Every remote arrival has been waited
+  // for, so that the order of execution is enough; a release would wait for the results to reach memory.)
+  if (CG == 2) {
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+    asm volatile("barrier.cluster.wait;" ::: "memory");
+  }
   tc_fence_after();
   if (warp == 1) {
     if constexpr (CG == 2)
@@ -359,50 +587,100 @@ struct DenseShape {
   int bn = 0, split = 1;
 };
 
-// The shape of the fewest cycles, by an estimate: rounds of tiles times what a slice of 64 takes in
-// one -- products at 4096 multiply-adds a cycle and SM, copies at 64 bytes -- and what comes before
-// and after.
-DenseShape dense_shape(const DenseProblem &p, int sms) {
+// The shape of the least time, by an estimate in ns fitted to measured products (M, N, K from 1 x 1024
+// x 1024 to 8192 x 4096 x 4096, all widths and splits; the shapes it takes are within 5 % of the best
+// measured one, as a rule):
+//   a slice of 64 takes a single block 120 + 0.9 a column (256 columns 350) and a pair 140 + 0.55 a
+//   column (256 columns 281, the products' own rate), either 180 at least;
+//   a tile takes 700 + 6 a column, however few its slices: its results have to leave;
+//   memory gives a block 70 bytes at most, all of them 6500, partly beside the above;
+//   a launch has 3400 before and after its slices, and sharing a sum costs 1000 + 18 a column (512 x
+//   4096 x 4096: pairs of 128 columns 17.2 us, of 256 columns shared by two 20.0 us; 128 x 4096 x
+//   4096: 64 columns shared by two 12.3 us, not shared 15.6 us).
+// `clusters` gives how many clusters of a size fit.
+template <typename Clusters>
+DenseShape dense_shape(const DenseProblem &p, Clusters clusters) {
   const int64_t slices = (p.K + kBK - 1) / kBK;
+  const double bytes = 2.0 * (double(p.N) * p.K + double(p.M) * p.K + double(p.M) * p.N);
   DenseShape best;
   double least = 0;
-  const auto consider = [&](int cg, int64_t bn, int split) {
-    if ((slices + split - 1) / split > kLong || (split > 1 && slices < 2 * split)) return;
-    const int64_t tiles = (p.N + 128 * cg - 1) / (128 * cg) * ((p.M + bn - 1) / bn);
-    const int64_t slots = cg == 2 ? sms / 2 : sms / split;
-    if (split > 1 && tiles > slots) return;
-    const int64_t rounds = (tiles + slots - 1) / slots;
-    const double slice = cg == 2 ? std::max(2 * bn, 256 + bn) : 256 + 2 * bn;
-    const double cycles = double(rounds) * double((slices + split - 1) / split) * slice +
-                          8.0 * double(bn) + (split > 1 ? 2500 + 6.0 * double(bn) : 0);
-    if (best.cg == 0 || cycles < least) {
-      best = {cg, int(bn), split};
-      least = cycles;
-    }
-  };
   for (int cg = 1; cg <= 2; ++cg) {
-    const int64_t unit = (p.q.mn ? 64 : 16) * cg;
-    for (int64_t bn = unit; bn <= kWidest && bn < p.M + unit; bn += unit)
-      for (int split = 1; split <= (cg == 1 ? 8 : 1); split *= 2) consider(cg, bn, split);
+    const int64_t unit = (p.q.mn ? 64 : 16) * cg, panels = (p.N + 128 * cg - 1) / (128 * cg);
+    for (int64_t bn = unit; bn <= kWidest && bn < p.M + unit; bn += unit) {
+      const int64_t tiles = panels * ((p.M + bn - 1) / bn);
+      const double wide = double(bn);
+      const double slice = cg == 2 ? std::max(180.0, 140.0 + 0.55 * wide)
+                                   : std::max(180.0, 120.0 + 0.9 * wide);
+      for (int split = 1; cg * split <= 8; split *= 2) {
+        const int64_t each = (slices + split - 1) / split, slots = clusters(cg * split);
+        if (split > 1 && (slices < 2 * split || tiles > slots)) break;
+        if (each > kLong) continue;
+        const int64_t rounds = (tiles + slots - 1) / slots;
+        const double work = double(rounds) * std::max(double(each) * slice, 700 + 6.0 * wide);
+        const double blocks = double(std::min(tiles, slots) * cg * split);
+        const double memory = bytes / std::min(6500.0, 70.0 * blocks);
+        const double ns = std::max(work, memory) + 0.25 * std::min(work, memory) + 4.0 * cg * wide +
+                          (split > 1 ? 1000 + 18.0 * wide : 0);
+        if (best.cg == 0 || ns < least) {
+          best = {cg, int(bn), split};
+          least = ns;
+        }
+      }
+    }
   }
   return best;
+}
+
+// Opts the kernels in to their shared memory, and finds how many clusters of 1, 2, 4 and 8 blocks the
+// device holds at once, a block an SM (the same for all of them): once per device.
+std::mutex g_ready_mutex;
+bool g_ready[64] = {};
+int g_clusters[64][4];
+
+template <typename Kernel>
+cudaError_t opt_in(Kernel kernel) {
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxSmem));
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                              cudaSharedmemCarveoutMaxShared);
+}
+
+cudaError_t make_ready(const DeviceInfo &dev) {
+  std::lock_guard<std::mutex> lock(g_ready_mutex);
+  if (g_ready[dev.id & 63]) return cudaSuccess;
+  cudaError_t e;
+  if ((e = opt_in(dense_kernel<1, false>)) != cudaSuccess ||
+      (e = opt_in(dense_kernel<1, true>)) != cudaSuccess ||
+      (e = opt_in(dense_kernel<2, false>)) != cudaSuccess ||
+      (e = opt_in(dense_kernel<2, true>)) != cudaSuccess)
+    return e;
+  for (int i = 0; i < 4; ++i) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << i;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(8, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kMaxSmem;
+    int count = 0;
+    if (i > 0 && (e = cudaOccupancyMaxActiveClusters(&count, dense_kernel<1, true>, &cfg)) !=
+                     cudaSuccess)
+      return e;
+    g_clusters[dev.id & 63][i] = std::max(1, i > 0 ? count : dev.sm_count);
+  }
+  g_ready[dev.id & 63] = true;
+  return cudaSuccess;
 }
 
 template <int CG, bool BF16>
 cudaError_t launch_as(const DenseProblem &g, const DenseShape &s, const DeviceInfo &dev,
                       cudaStream_t stream) {
   auto kernel = dense_kernel<CG, BF16>;
-  static std::atomic<uint64_t> configured{0};
-  const uint64_t bit = uint64_t(1) << (dev.id & 63);
   cudaError_t e;
-  if (!(configured.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxSmem));
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared);
-    if (e != cudaSuccess) return e;
-    configured.fetch_or(bit, std::memory_order_release);
-  }
   DenseParams<BF16> p = {};
   p.M = int(g.M);
   p.N = int(g.N);
@@ -445,7 +723,7 @@ cudaError_t launch_as(const DenseProblem &g, const DenseShape &s, const DeviceIn
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(CG == 2 ? 2 : s.split);
+  attr[0].val.clusterDim.x = unsigned(CG * s.split);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -455,7 +733,7 @@ cudaError_t launch_as(const DenseProblem &g, const DenseShape &s, const DeviceIn
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kFixed + p.stages * stage;
   cfg.stream = stream;
-  const int64_t tiles = int64_t(p.panels) * p.q_tiles, share = CG == 2 ? 2 : s.split;
+  const int64_t tiles = int64_t(p.panels) * p.q_tiles, share = CG * s.split;
   const int64_t slots = s.split > 1 ? tiles : dev.sm_count / share;
   cfg.gridDim = dim3(unsigned(share * std::max<int64_t>(1, std::min(tiles, slots))), 1, 1);
   return cudaLaunchKernelEx(&cfg, kernel, map_p, map_q, p);
@@ -467,7 +745,11 @@ cudaError_t launch_dense(const DenseProblem &p, const DeviceInfo &dev, cudaStrea
   if (p.dtype == TMM_F32 || p.K == 0 ||
       (p.N + 127) / 128 * ((p.M + 15) / 16) >= INT32_MAX / 16)
     return cudaErrorNotSupported;
-  const DenseShape s = dense_shape(p, dev.sm_count);
+  const cudaError_t e = make_ready(dev);
+  if (e != cudaSuccess) return e;
+  const int *const fit = g_clusters[dev.id & 63];
+  const DenseShape s = dense_shape(
+      p, [&](int size) { return fit[size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : 3]; });
   if (s.cg == 0) return cudaErrorNotSupported;
   if (p.dtype == TMM_BF16)
     return s.cg == 2 ? launch_as<2, true>(p, s, dev, stream) : launch_as<1, true>(p, s, dev, stream);
