@@ -16,8 +16,10 @@
 // The most probable: every warp keeps a sorted list of 32 keys, a lane each (a key: the value's
 // bits in the order of unsigned numbers, then the number's complement, so that the larger key is
 // the larger value or the lower number).  Its n-th is a threshold that a vector's maximum, which is
-// needed anyway, is compared with; the block's warps share the highest.  The first threshold is the
-// n-th largest of the lanes' first maxima, so that few values of a row are ever inserted.  Lists are
+// needed anyway, is compared with, and so is, for all of the block's warps, what the lanes' running
+// maxima imply: of each of w warps ceil(n / w) lanes have reached the least of the warps' ceil(n / w)-th
+// largest.  Few values of a row are then ever inserted (131072 columns, 20 listed: about 20 a warp;
+// with thresholds of the warps' own lists alone, 32 rows took 21 us in place of TOP_US).  Lists are
 // merged pair by pair (half-cleaner and five exchange steps).
 //
 // Gradient: dl_v = scale (g ([v = t] - p_v) - h p_v (log p_v + entropy) + sum_j e_j ([v = id_j] - p_v))
@@ -125,7 +127,7 @@ struct Best {
     }
   }
   // One lane's value, every lane's in turn.
-  __device__ __forceinline__ void offer(float v, uint32_t at, volatile uint32_t *shared_low) {
+  __device__ __forceinline__ void offer(float v, uint32_t at) {
     const int lane = threadIdx.x & 31;
     const uint64_t mine = v >= low_value ? key_of(v, at) : kNoKey;      // (NaN: no key)
     unsigned want = __ballot_sync(kAll, mine > low);
@@ -140,22 +142,16 @@ struct Best {
       key = lane < place ? key : lane == place ? k : above;
       raise_low(__shfl_sync(kAll, key, n - 1));
     } while (want);
-    if (lane == n - 1 && key != kNoKey)
-      atomicMax(const_cast<uint32_t *>(shared_low), uint32_t(key >> 32));
   }
-  // The n-th largest of the lanes' values is a first threshold.
-  __device__ __forceinline__ void start(float v) {
-    const int lane = threadIdx.x & 31;
-    uint32_t o = v > -INFINITY ? order_of(v) : 0;
-#pragma unroll
-    for (int size = 2; size <= 32; size *= 2)
-#pragma unroll
-      for (int d = size / 2; d > 0; d >>= 1) {
-        const uint32_t other = __shfl_xor_sync(kAll, o, d);
-        const bool up = (lane & size) == 0, first = (lane & d) == 0;      // descending where `up`
-        o = (first == up) ? max(o, other) : min(o, other);
-      }
-    raise_low(uint64_t(__shfl_sync(kAll, o, n - 1)) << 32);
+  // The each-th largest of the lanes' values (in their order's numbers, 0: none), each the warps' equal
+  // share of n: the least of the warps' is one that at least n values of the row reach.
+  __device__ __forceinline__ uint32_t share(float v, int each) const {
+    uint32_t mine = v > -INFINITY ? order_of(v) : 0, top = 0;
+    for (int j = 0; j < each; ++j) {
+      top = __reduce_max_sync(kAll, mine);
+      if ((threadIdx.x & 31) == unsigned(__ffs(int(__ballot_sync(kAll, mine == top))) - 1)) mine = 0;
+    }
+    return top;
   }
   // With another sorted list, given as its key 31 - lane.
   __device__ __forceinline__ void merge(uint64_t reversed) {
@@ -210,15 +206,11 @@ logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
   constexpr int kWarps = kMaxThreads / 32;
   __shared__ float part[3][kWarps];
   __shared__ uint64_t lists[TOP ? kWarps : 1][32];
-  __shared__ uint32_t shared_low;
+  __shared__ uint32_t reached[kWarps];      // by the lanes of each warp, see Best::share
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int threads = blockDim.x, warps = threads >> 5;
   const int64_t row = blockIdx.x / cluster;
   const int rank = int(blockIdx.x - row * cluster);
-  if (TOP) {
-    if (tid == 0) shared_low = 0;
-    __syncthreads();
-  }
   wait_then_start_next();
 
   const T *const from = static_cast<const T *>(p.logits) + row * p.ld;
@@ -255,6 +247,7 @@ logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
     }
   };
   const int step = kAhead * threads;
+  const int each = TOP ? (p.top + warps - 1) / warps : 0;
   bool first_batch = true;
   Vec<T> next[kAhead];
   fetch(v0, next);
@@ -271,9 +264,14 @@ logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
       most = fmaxf(most, top[u]);
     }
     if (TOP) {
-      if (first_batch) best.start(most);
+      const uint32_t mine = best.share(fmaxf(st.m, most), each);
+      if (lane == 0) *const_cast<volatile uint32_t *>(&reached[warp]) = mine;
+      if (first_batch) __syncthreads();
       first_batch = false;
-      best.raise_low(uint64_t(*const_cast<volatile uint32_t *>(&shared_low)) << 32);
+      // (What another warp has reached by now is reached for good: an older value will do.)
+      const uint32_t all = __reduce_min_sync(
+          kAll, lane < warps ? *const_cast<volatile uint32_t *>(&reached[lane]) : ~0u);
+      best.raise_low(uint64_t(all) << 32);
       if (__any_sync(kAll, most >= best.low_value)) {
 #pragma unroll 1
         for (int u = 0; u < kAhead; ++u) {
@@ -288,7 +286,7 @@ logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
           if (!__any_sync(kAll, t >= best.low_value)) continue;
           const uint32_t at = uint32_t(head + (i0 + u * threads + tid) * W);
 #pragma unroll
-          for (int k = 0; k < W; ++k) best.offer(x.get(k), at + k, &shared_low);
+          for (int k = 0; k < W; ++k) best.offer(x.get(k), at + k);
         }
       }
     }
@@ -310,7 +308,7 @@ logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
     const int tail = head + vectors * W, ends = head + cols - tail;
     const int i = lane < head ? lane : tail + lane - head;
     const float x = lane < ends ? as_float(from[i]) : -INFINITY;
-    if (TOP) best.offer(x, uint32_t(i), &shared_low);
+    if (TOP) best.offer(x, uint32_t(i));
     st.raise(fmaxf(st.m, x), c);
     add_term(x, st.base(), c, st.s, st.w);
   }

@@ -4,20 +4,18 @@
 //   the groups' values: the sum of a group's one or two best c,
 //   the k best c among the experts of the best groups (ties: the lower number),
 //   w_j = scale s_j / sum of the chosen s, or scale s_j.
-// The choice is that of the scores in 64 bits.  Without a bias the logits stand for the scores
-// (both functions are increasing), which is exact.  Otherwise c is computed in 32 bits with an
-// error below `tol`, and a row in which two values that decide something are closer than that is
-// done again in 64 bits: one row in a hundred at 256 experts, where 64 bits for all rows would take
-// the FP64 units about 100 times the reading of the logits.
+// The choice is that of the scores to 43 bits (without a bias the logits stand for the scores, as both
+// functions are increasing).  It is made in 32 bits, whose errors are bounded, and a row in which two
+// values that decide something are closer than that is done again in pairs of FP32 values: one row in
+// a thousand at 256 experts.
 //
 // A warp does a row, all of whose values stay in registers: with G groups rounded up to a power of
 // two every group has 32 / G lanes, so that a group's best are a butterfly within its lanes.  The
-// choice is k rounds of two warp reductions of the redux unit (the best value's bits in an order
-// that unsigned numbers have, then the lowest number that has it).
+// choice is k + 1 rounds of one warp reduction over keys that hold a value and its number.
 // Gradient: w depends on the chosen logits alone, but for the softmax without renormalisation;
-// rows are written whole, 16 bytes a lane.
-#include <atomic>
+// rows are written whole, 16 bytes a lane, and the chosen few again.
 #include <cstdint>
+#include <type_traits>
 
 #include "rows.h"
 #include "row_ops.cuh"
@@ -34,159 +32,446 @@ __device__ __forceinline__ uint32_t key_of(float c) {
   const uint32_t b = __float_as_uint(c + 0.0f);
   return c != c ? ~0u : b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ uint64_t key_of(double c) {
-  const uint64_t b = uint64_t(__double_as_longlong(c + 0.0));
-  return c != c ? ~uint64_t(0) : b >> 63 ? ~b : b | uint64_t(1) << 63;
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
-__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kAll, v); }
-__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    const uint64_t o = __shfl_xor_sync(kAll, v, d);
-    v = o > v ? o : v;
-  }
-  return v;
-}
-template <typename C>
-__device__ __forceinline__ C warp_sum(C v) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
   return v;
 }
+// (NaN left out, unless all are.)
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
-  return v;
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
 }
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
-__device__ __forceinline__ double sigmoid(double l) { return 1.0 / (1.0 + exp(-l)); }
-__device__ __forceinline__ float exp_of(float t) { return expf(t); }
-__device__ __forceinline__ double exp_of(double t) { return exp(t); }
+// For the choice, which allows for errors of 2^-20: the hardware's exponential and quotient.
+__device__ __forceinline__ float near_sigmoid(float l) {
+  return __fdividef(1.0f, 1.0f + __expf(-l));
+}
+__device__ __forceinline__ float near_exp(float t) { return __expf(t); }
 
-// A lane's experts: numbers first + v * step for v < V, where v * step + sub < size.
+// A lane's keys, the largest first (a network of exchanges: Batcher's odd-even merge sort).
+template <int V>
+__device__ __forceinline__ void sort_down(uint32_t (&k)[V]) {
+#pragma unroll
+  for (int run = 1; run < V; run *= 2)
+#pragma unroll
+    for (int d = run; d > 0; d /= 2)
+#pragma unroll
+      for (int j = d % run; j + d < V; j += 2 * d)
+#pragma unroll
+        for (int i = 0; i < d; ++i)
+          if (i + j + d < V && (i + j) / (2 * run) == (i + j + d) / (2 * run)) {
+            const uint32_t x = k[i + j], y = k[i + j + d];
+            k[i + j] = max(x, y);
+            k[i + j + d] = min(x, y);
+          }
+}
+
+// A lane's experts: numbers first + v * step for v < V, where v * step + sub < size.  VEC: every lane of
+// a group has V of them, one after another.
+template <bool VEC>
 struct Lane {
-  int first, step, sub, size, group;
-  __device__ __forceinline__ bool has(int v) const { return v * step + sub < size; }
-  __device__ __forceinline__ int expert(int v) const { return first + v * step; }
+  int first, stride, sub, size, group;
+  __device__ __forceinline__ bool has(int v) const {
+    return VEC ? size > 0 : v * stride + sub < size;
+  }
+  __device__ __forceinline__ int expert(int v) const { return first + (VEC ? v : v * stride); }
 };
-__device__ __forceinline__ Lane lane_of(const RouteProblem &p, int lane, bool vec) {
-  Lane a;
+template <bool VEC, int V>
+__device__ __forceinline__ Lane<VEC> lane_of(const RouteProblem &p, int lane) {
+  Lane<VEC> a;
   a.group = lane / p.lanes;
   const int sub = lane - a.group * p.lanes;
-  if (vec) {       // every lane has V of them, one after another
-    const int each = p.group_size / p.lanes;
-    a.step = 1;
-    a.sub = sub * each;
-  } else {
-    a.step = p.lanes;
-    a.sub = sub;
-  }
+  a.stride = p.lanes;
+  a.sub = VEC ? sub * V : sub;
   a.first = a.group * p.group_size + a.sub;
   a.size = a.group < p.groups ? p.group_size : 0;
   return a;
 }
 
-// The choice of a row: lane j < k leaves with expert j, or -1.  `close`: two values that decide
-// something are too close to tell (never in 64 bits).  l: this lane's logits, -inf where it has none.
-template <typename T, typename C, int V>
-__device__ __forceinline__ int choose(const RouteProblem &p, int64_t row, const Lane &a,
-                                      const float (&l)[V], bool &close) {
-  constexpr bool exact = sizeof(C) == 8;
-  const int lane = threadIdx.x & 31;
+// The biases of this lane's experts, 0 where it has none.
+template <bool VEC, int V>
+__device__ __forceinline__ void load_bias(const RouteProblem &p, const Lane<VEC> &a, float (&b)[V]) {
+  if constexpr (VEC && V >= 4) {
+    if (p.vec_bias) {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (a.size > 0) w = *reinterpret_cast<const float4 *>(p.bias + a.first + 4 * i);
+        b[4 * i] = w.x;
+        b[4 * i + 1] = w.y;
+        b[4 * i + 2] = w.z;
+        b[4 * i + 3] = w.w;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) b[v] = a.has(v) ? p.bias[a.expert(v)] : 0.0f;
+}
+
+// In 32 bits, the scores c of this lane's experts (the logits without a bias) and which of them may be
+// chosen; m: the row's maximum, where the scores are the softmax's.  Returns what two
+// scores may be off by together: of the sigmoids, e^-l by 2^-21 of itself (times s (1 - s)) and the
+// quotient by 2^-22; of the softmax, every term by 2^-21, their sum by as many half steps as it has
+// additions (at most 37), in all 2^-18 of the two scores, which are 1 / sum at most each.
+template <bool VEC, int V>
+__device__ __forceinline__ float make_scores(const RouteProblem &p, const Lane<VEC> &a,
+                                             const float (&l)[V], float (&c)[V], bool (&on)[V],
+                                             float &m) {
   const float *const bias = p.bias;
-  C c[V], m = 0;
-  bool on[V];
+  float error = 0x1p-20f;
+  m = 0;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    c[v] = C(l[v]);
+    c[v] = l[v];
     on[v] = l[v] != -INFINITY;
   }
   if (!p.sigmoid && (bias || p.best == 2)) {
     float top = -INFINITY;
 #pragma unroll
     for (int v = 0; v < V; ++v) top = fmaxf(top, l[v]);
-    m = C(warp_max(top));
+    m = warp_max(top);
   }
-  if (bias) {
-    if (p.sigmoid) {
+  if (bias == nullptr) return 0.0f;
+  if (p.sigmoid) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) c[v] = sigmoid(c[v]);
-    } else {
-      C sum = 0;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        c[v] = on[v] ? exp_of(c[v] - m) : C(0);
-        sum += c[v];
-      }
-      sum = warp_sum(sum);
-#pragma unroll
-      for (int v = 0; v < V; ++v) c[v] /= sum;
-    }
+    for (int v = 0; v < V; ++v) c[v] = near_sigmoid(c[v]);
+  } else {
+    float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float b = a.has(v) ? bias[a.expert(v)] : 0.0f;
-      on[v] &= b != -INFINITY;
-      c[v] += C(b);
+      c[v] = on[v] ? near_exp(c[v] - m) : 0.0f;
+      sum += c[v];
     }
+    sum = 1.0f / warp_sum(sum);
+    error = 0x1p-17f * sum;
+#pragma unroll
+    for (int v = 0; v < V; ++v) c[v] *= sum;
   }
-  bool open = true;
+  float b[V];
+  load_bias(p, a, b);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    on[v] &= b[v] != -INFINITY;
+    c[v] += b[v];
+  }
+  return error;
+}
+
+// Whether this lane's group is one of the best.  `close`: the last one taken and the first that is not
+// are too close to tell.
+// one, two: this lane's two largest values.
+template <bool VEC>
+__device__ __forceinline__ bool group_open(const RouteProblem &p, const Lane<VEC> &a, float one,
+                                           float two, float m, float error, bool &close) {
+  const bool bias = p.bias != nullptr;
+#pragma unroll 1
+  for (int d = 1; d < p.lanes; d <<= 1) {
+    const float o = __shfl_xor_sync(kAll, one, d), t = __shfl_xor_sync(kAll, two, d);
+    two = fmaxf(fmaxf(two, t), fminf(one, o));
+    one = fmaxf(one, o);
+  }
+  const bool any = one != -INFINITY && a.size > 0;
+  float value = one;
+  if (p.best == 2 && any) {
+    if (!bias && p.sigmoid)
+      value = near_sigmoid(one) + near_sigmoid(two);
+    else if (!bias)
+      value = near_exp(one - m) + near_exp(two - m);
+    else if (two != -INFINITY)
+      value = one + two;
+  }
+  const uint32_t key = any ? key_of(value) : 0u;
+  int rank = 0;
+  for (int h = 0; h < p.groups; ++h) {
+    const uint32_t other = __shfl_sync(kAll, key, h * p.lanes);
+    rank += other > key || (other == key && h < a.group);
+  }
+  const bool open = key != 0 && rank < p.top_groups;
+  if (bias || p.best == 2) {
+    // (Values are in the order of their keys.)
+    const uint32_t lo = __reduce_min_sync(kAll, open ? key : ~0u);
+    const uint32_t hi = __reduce_max_sync(kAll, open ? 0u : key);
+    const float x = value_of(lo), y = value_of(hi);
+    const float tol = bias ? 2.0f * error + 0x1p-21f * fabsf(y) : 0x1p-16f * y + 1e-37f;
+    close |= hi != 0 && x - y <= tol;
+  }
+  return open;
+}
+
+// The choice of a row in 32 bits: lane j < k leaves with expert j, or -1.  A key is 23 bits of where a
+// value lies between the lowest and the highest that may be chosen, and 9 bits of the expert's number's
+// complement, so that one reduction finds the best and, of equal ones, the lower number; every lane's
+// keys are sorted first, and the lane that had the best shows its next.  `close`: two values that
+// decide something are within the error of the scores and of a key, and not made from equal inputs.
+// l: this lane's logits, -inf where it has none.
+template <typename T, bool VEC, int V>
+__device__ __forceinline__ int choose(const RouteProblem &p, int64_t row, const Lane<VEC> &a,
+                                      const float (&l)[V], bool &close) {
+  const int lane = threadIdx.x & 31;
+  float c[V], m;
+  bool on[V], open = true;
+  const float error = make_scores(p, a, l, c, on, m);
   close = false;
   if (p.groups > 1) {
-    C one = -INFINITY, two = -INFINITY;
+    float one = -INFINITY, two = -INFINITY;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (on[v]) {
-        const C low = c[v] < one ? c[v] : one;
-        one = c[v] > one ? c[v] : one;
-        two = low > two ? low : two;
-      }
-    for (int d = 1; d < p.lanes; d <<= 1) {
-      const C o = __shfl_xor_sync(kAll, one, d), t = __shfl_xor_sync(kAll, two, d);
-      const C low = o < one ? o : one;
-      one = o > one ? o : one;
-      two = t > two ? t : two;
-      two = low > two ? low : two;
+    for (int v = 0; v < V; ++v) {
+      const float x = on[v] ? c[v] : -INFINITY;
+      two = fmaxf(two, fminf(one, x));
+      one = fmaxf(one, x);
     }
-    const bool any = one != C(-INFINITY);
-    C value = one;
-    if (p.best == 2 && any) {
-      if (!bias && p.sigmoid)
-        value = sigmoid(one) + sigmoid(two);
-      else if (!bias)
-        value = exp_of(one - m) + exp_of(two - m);
-      else if (two != C(-INFINITY))
-        value = one + two;
-    }
-    const auto key = any && a.size > 0 ? key_of(value) : key_of(C(0)) * 0;
-    int rank = 0;
-    for (int h = 0; h < p.groups; ++h) {
-      const auto other = __shfl_sync(kAll, key, h * p.lanes);
-      rank += other > key || (other == key && h < a.group);
-    }
-    open = key != 0 && rank < p.top_groups;
-    if (!exact && (bias || p.best == 2)) {
-      // The last group taken against the first that is not.
-      float lo = open ? float(value) : INFINITY, hi = key != 0 && !open ? float(value) : -INFINITY;
+    open = group_open(p, a, one, two, m, error, close);
+  }
+  float hi = -INFINITY, below = -INFINITY, odd = 0.0f;      // below: the lowest, negated
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(kAll, lo, d));
-        hi = fmaxf(hi, __shfl_xor_sync(kAll, hi, d));
-      }
-      const float tol = bias ? 0x1p-17f + 0x1p-21f * fabsf(hi) : 0x1p-16f * hi + 1e-37f;
-      close = hi != -INFINITY && lo - hi <= tol;
+  for (int v = 0; v < V; ++v) {
+    on[v] &= open;
+    if (on[v]) {
+      hi = fmaxf(hi, c[v]);
+      below = fmaxf(below, -c[v]);
+      odd += c[v] * 0.0f;      // NaN of an infinity or NaN
     }
   }
-  decltype(key_of(C(0))) key[V];
+  hi = warp_max(hi);
+  const float lo = fmaxf(-warp_max(below), hi - 32.0f);      // (values further down share a key)
+  if (__any_sync(kAll, odd != 0.0f)) close = true;
+  const float range = hi - lo, step = range > 1e-30f ? 8388600.0f / range : 0.0f;
+  const bool some = hi > -INFINITY;
+  uint32_t key[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) key[v] = on[v] && open ? key_of(c[v]) : 0;
-  // With a bias one round more, to see what the last one chosen was taken before.
-  const bool check = !exact && bias;
-  const int rounds = p.k + (check ? 1 : 0);
+  for (int v = 0; v < V; ++v) {
+    // 2^23 + 1 to 2^24 - 7, whose lower 23 bits the key takes.
+    const float at = fmaf(fmaxf(c[v], lo) - lo, step, 8388609.0f);
+    key[v] = on[v] && some ? __float_as_uint(at) * 512u + uint32_t(511 - a.expert(v)) : 0u;
+  }
+  sort_down(key);
+  // One round more than are chosen, to see what the last one was taken before.
+  uint32_t mine = 0;
+  for (int j = 0; j <= p.k; ++j) {
+    const uint32_t top = __reduce_max_sync(kAll, key[0]);
+    if (lane == j) mine = top;
+    const bool pop = key[0] == top;
+#pragma unroll
+    for (int v = 0; v + 1 < V; ++v) key[v] = pop ? key[v + 1] : key[v];
+    key[V - 1] = pop ? 0u : key[V - 1];
+  }
+  const uint32_t next = __shfl_down_sync(kAll, mine, 1);
+  // (Keys are made of steps that do not decrease: without a bias only equal ones are in doubt.)
+  const float tol =
+      p.bias ? (error + 0x1p-22f * fmaxf(fabsf(hi), fabsf(lo))) * step + 1.5f : 0.5f;
+  bool near = lane < p.k && next != 0 && float((mine >> 9) - (next >> 9)) <= tol;
+  if (__any_sync(kAll, near)) {
+    if (near) {
+      // Equal logits with equal biases are equal, and their numbers decide.
+      const T *const at = static_cast<const T *>(p.logits) + row * p.ld;
+      const int x = 511 - int(mine & 511), y = 511 - int(next & 511);
+      near = float(at[x]) != float(at[y]) || (p.bias && p.bias[x] != p.bias[y]);
+    }
+    close |= __any_sync(kAll, near);
+  }
+  return lane < p.k && mine != 0 ? 511 - int(mine & 511) : -1;
+}
+
+template <typename T, bool VEC, int V>
+__device__ __forceinline__ void load_logits(const RouteProblem &p, int64_t row, const Lane<VEC> &a,
+                                            float (&l)[V]) {
+  const T *const from = static_cast<const T *>(p.logits) + row * p.ld;
+  constexpr int kVec = Vec<T>::kCount;
+  if constexpr (VEC) {
+    Vec<T> w[V / kVec];
+    if (a.size > 0) {
+#pragma unroll
+      for (int i = 0; i < V / kVec; ++i)
+        w[i].w = *reinterpret_cast<const uint4 *>(from + a.first + i * kVec);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = a.size > 0 ? w[v / kVec].get(v % kVec) : -INFINITY;
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = a.has(v) ? as_float(from[a.expert(v)]) : -INFINITY;
+  }
+}
+
+// ---- the choice again, in pairs of FP32 values ---------------------------------------------
+//
+// A value is the sum of two FP32 values that do not overlap, 47 bits (Dekker's and Knuth's exact sums and
+// products).  The FP64 units of this GPU are few and far: a row of 256 sigmoids took them 16 us, with
+// nothing else to do.
+
+struct Two {
+  float h, l;
+};
+__device__ __forceinline__ Two sum_of(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two renewed(float h, float l) {      // |h| >= |l|
+  const float s = __fadd_rn(h, l);
+  return {s, __fsub_rn(l, __fsub_rn(s, h))};
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+  const Two s = sum_of(a.h, b.h), t = sum_of(a.l, b.l);
+  const Two u = renewed(s.h, __fadd_rn(s.l, t.h));
+  return renewed(u.h, __fadd_rn(u.l, t.l));
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+  const float p = __fmul_rn(a.h, b.h);
+  return renewed(p, __fmaf_rn(a.h, b.l, __fmaf_rn(a.l, b.h, __fmaf_rn(a.h, b.h, -p))));
+}
+__device__ __forceinline__ Two one_over(Two b) {
+  const float q = __frcp_rn(b.h);
+  // 1 - q b, exactly but for its last bits.
+  const float r = __fmaf_rn(-q, b.l, __fmaf_rn(-q, b.h, 1.0f));
+  return renewed(q, __fmul_rn(q, r));
+}
+// e^y for y.h from -87 to 88.  y = n ln 2 + r, the first part of ln 2 of nine bits, so that n times it is
+// exact; Taylor's series, whose terms from the seventh on are below 2^-22 of the sum and made in FP32.
+__device__ __forceinline__ Two exp_of(Two y) {
+  const float n = rintf(y.h * 1.44269504f);
+  const float c = -0.00021219444f, p = __fmul_rn(n, c);      // the rest of ln 2
+  const Two tail = {p, __fmaf_rn(n, 1.6465949697480609e-12f, __fmaf_rn(n, c, -p))};
+  const Two r = Two{__fmaf_rn(-n, 0.693359375f, y.h), y.l} + Two{-tail.h, -tail.l};
+  const float x = r.h;
+  float t = 1.0f / 6227020800.0f;
+  t = fmaf(t, x, 1.0f / 479001600.0f);
+  t = fmaf(t, x, 1.0f / 39916800.0f);
+  t = fmaf(t, x, 1.0f / 3628800.0f);
+  t = fmaf(t, x, 1.0f / 362880.0f);
+  t = fmaf(t, x, 1.0f / 40320.0f);
+  t = fmaf(t, x, 1.0f / 5040.0f);
+  Two q = {t, 0.0f};      // 1/6!, 1/5!, ...: their nearest FP32 values, and what these leave
+  q = q * r + Two{1.0f / 720.0f, -3.3631094437103215e-11f};
+  q = q * r + Two{1.0f / 120.0f, -4.34617203337595e-10f};
+  q = q * r + Two{1.0f / 24.0f, -1.2417634698280722e-09f};
+  q = q * r + Two{1.0f / 6.0f, -4.967053879312289e-09f};
+  q = q * r + Two{0.5f, 0.0f};
+  q = q * r + Two{1.0f, 0.0f};
+  q = q * r + Two{1.0f, 0.0f};
+  const float scale = __int_as_float((int(n) + 127) << 23);
+  return {q.h * scale, q.l * scale};
+}
+__device__ __forceinline__ uint64_t key_of(Two v) {
+  return uint64_t(key_of(v.h)) << 32 | key_of(v.l);
+}
+__device__ __forceinline__ Two value_of(uint64_t key) {
+  return {value_of(uint32_t(key >> 32)), value_of(uint32_t(key))};
+}
+__device__ __forceinline__ uint64_t more(uint64_t a, uint64_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint64_t less(uint64_t a, uint64_t b) { return a > b ? b : a; }
+
+// The scores of up to four logits, a call: seldom run, and has to be fetched when it is.
+struct Four {
+  Two v[4];
+};
+__device__ __noinline__ Four scores_of(float l0, float l1, float l2, float l3, float m,
+                                       bool is_sigmoid) {
+  const float l[4] = {l0, l1, l2, l3};
+  Four f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // 1 / (1 + e^-l) of the smaller of e^-l and e^l; e^(l - m).  0 below -87, where FP32 ends.
+    Two y = is_sigmoid ? Two{-fabsf(l[i]), 0.0f} : sum_of(l[i], -m);
+    const bool tiny = y.h < -87.0f;      // (NaN stays)
+    if (tiny) y = {0.0f, 0.0f};
+    Two e = exp_of(y);
+    if (is_sigmoid) {
+      const Two s = one_over(e + Two{1.0f, 0.0f});
+      e = l[i] < 0.0f ? e * s : s;
+    }
+    const float end = is_sigmoid && l[i] > 0.0f ? 1.0f : 0.0f;
+    f.v[i] = tiny ? Two{end, 0.0f} : e;
+  }
+  return f;
+}
+
+// `choose` in pairs of values.
+template <typename T, bool VEC, int V>
+__device__ __noinline__ int choose_again(const RouteProblem &p, int64_t row) {
+  const int lane = threadIdx.x & 31;
+  const Lane<VEC> a = lane_of<VEC, V>(p, lane);
+  float l[V], b[V], m = -INFINITY;      // -inf for an expert that may not be chosen
+  load_logits<T>(p, row, a, l);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    b[v] = 0.0f;
+    m = fmaxf(m, l[v]);
+  }
+  m = warp_max(m);
+  Two c[V], sum = {0.0f, 0.0f};
+#pragma unroll
+  for (int v = 0; v < V; ++v) c[v] = {l[v], 0.0f};
+  if (p.bias) {
+    load_bias(p, a, b);
+#pragma unroll
+    for (int v = 0; v < V; v += 4) {
+      const Four f = scores_of(l[v], v + 1 < V ? l[v + 1] : 0.0f, v + 2 < V ? l[v + 2] : 0.0f,
+                               v + 3 < V ? l[v + 3] : 0.0f, m, p.sigmoid);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (v + i < V) c[v + i] = f.v[i];
+    }
+    Two scale = {1.0f, 0.0f};
+    if (!p.sigmoid) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) sum = sum + c[v];
+#pragma unroll 1
+      for (int d = 16; d > 0; d >>= 1)
+        sum = sum + Two{__shfl_xor_sync(kAll, sum.h, d), __shfl_xor_sync(kAll, sum.l, d)};
+      scale = one_over(sum);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      c[v] = fabsf(b[v]) < INFINITY ? c[v] * scale + Two{b[v], 0.0f} : Two{b[v], 0.0f};
+  }
+  uint64_t key[V], best = 0, second = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    key[v] = l[v] == -INFINITY || b[v] == -INFINITY ? 0 : key_of(c[v]);
+    second = more(second, less(best, key[v]));
+    best = more(best, key[v]);
+  }
+  if (p.groups > 1) {
+    uint64_t one = best, two = second;
+#pragma unroll 1
+    for (int d = 1; d < p.lanes; d <<= 1) {
+      const uint64_t o = __shfl_xor_sync(kAll, one, d), t = __shfl_xor_sync(kAll, two, d);
+      two = more(more(two, t), less(one, o));
+      one = more(one, o);
+    }
+    uint64_t value = one;
+    if (p.best == 2 && two != 0) {
+      Two x = value_of(one), y = value_of(two);
+      if (!p.bias) {
+        const Four f = scores_of(x.h, y.h, 0.0f, 0.0f, m, p.sigmoid);
+        x = f.v[0];
+        y = f.v[1];
+      }
+      const Two s = x + y;
+      value = key_of(fabsf(x.h + y.h) < INFINITY ? s : Two{x.h + y.h, 0.0f});
+    } else if (p.best == 2 && one != 0 && !p.bias) {
+      value = key_of(scores_of(value_of(one).h, 0.0f, 0.0f, 0.0f, m, p.sigmoid).v[0]);
+    }
+    int rank = 0;
+#pragma unroll 1
+    for (int h = 0; h < p.groups; ++h) {
+      const uint64_t other = __shfl_sync(kAll, value, h * p.lanes);
+      rank += other > value || (other == value && h < a.group);
+    }
+    if (value == 0 || rank >= p.top_groups)
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = 0;
+  }
   int mine = -1;
-  decltype(key_of(C(0))) mine_key = 0;
-  for (int j = 0; j < rounds; ++j) {
-    auto best = key[0];
+#pragma unroll 1
+  for (int j = 0; j < p.k; ++j) {
+    best = key[0];
     int at = 0;
 #pragma unroll
     for (int v = 1; v < V; ++v)
@@ -194,74 +479,19 @@ __device__ __forceinline__ int choose(const RouteProblem &p, int64_t row, const 
         best = key[v];
         at = v;
       }
-    const auto top = warp_max(best);
-    if (top == 0) break;
+    const uint32_t high = __reduce_max_sync(kAll, uint32_t(best >> 32));
+    const uint32_t low =
+        __reduce_max_sync(kAll, uint32_t(best >> 32) == high ? uint32_t(best) : 0u);
+    const uint64_t most = uint64_t(high) << 32 | low;
+    if (most == 0) break;
     const int e = int(__reduce_min_sync(
-        kAll, best == top ? unsigned(a.first + at * a.step) : unsigned(INT32_MAX)));
+        kAll, best == most ? unsigned(a.expert(at)) : unsigned(INT32_MAX)));
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (a.first + v * a.step == e && a.has(v)) key[v] = 0;
-    if (lane == j) {
-      mine = e;
-      mine_key = top;
-    }
+      if (a.has(v) && a.expert(v) == e) key[v] = 0;
+    if (lane == j) mine = e;
   }
-  if constexpr (!exact) {
-    if (check) {
-      const auto value = [](uint32_t k) {
-        return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
-      };
-      const uint32_t next_key = __shfl_down_sync(kAll, mine_key, 1);
-      const int next = __shfl_down_sync(kAll, mine, 1);
-      const bool pair = lane < p.k && next >= 0 && lane < 31;
-      const float x = value(mine_key), gap = x - value(next_key);
-      bool near = pair && gap <= 0x1p-18f + 0x1p-22f * fabsf(x);
-      if (__any_sync(kAll, near)) {
-        if (near) {
-          // Equal logits with equal biases are equal, and their numbers decide.
-          const T *const at = static_cast<const T *>(p.logits) + row * p.ld;
-          near = float(at[mine]) != float(at[next]) || bias[mine] != bias[next];
-        }
-        close |= __any_sync(kAll, near);
-      }
-    }
-  }
-  return lane < p.k ? mine : -1;
-}
-
-template <typename T, int V>
-__device__ __forceinline__ void load_logits(const RouteProblem &p, int64_t row, const Lane &a,
-                                            bool vec, float (&l)[V]) {
-  const T *const from = static_cast<const T *>(p.logits) + row * p.ld;
-  constexpr int kVec = Vec<T>::kCount;
-  if constexpr (V >= kVec) {
-    if (vec) {
-      if (a.size == 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) l[v] = -INFINITY;
-        return;
-      }
-      Vec<T> w[V / kVec];
-#pragma unroll
-      for (int i = 0; i < V / kVec; ++i)
-        w[i].w = *reinterpret_cast<const uint4 *>(from + a.first + i * kVec);
-#pragma unroll
-      for (int v = 0; v < V; ++v) l[v] = w[v / kVec].get(v % kVec);
-      return;
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) l[v] = a.has(v) ? as_float(from[a.expert(v)]) : -INFINITY;
-}
-
-// In 64 bits; apart from the kernel's usual way, whose registers it would take.
-template <typename T, int V>
-__device__ __noinline__ int choose_again(const RouteProblem &p, int64_t row, bool vec) {
-  const Lane a = lane_of(p, threadIdx.x & 31, vec);
-  float l[V];
-  load_logits<T, V>(p, row, a, vec, l);
-  bool close;
-  return choose<T, double, V>(p, row, a, l, close);
+  return mine;
 }
 
 // The chosen scores of a row over their sum, as lane j has logit x of slot j (-inf: none), 0 where
@@ -282,20 +512,20 @@ __device__ __forceinline__ float score_of(bool is_sigmoid, bool renormalise, flo
   return none ? 0.0f : s / total;
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(32 * kWarps)
+// (64 registers a thread: the 64-bit choice would take 96 and leave fewer rows in flight.)
+template <typename T, bool VEC, int V>
+__global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 8 : V <= 16 ? 5 : 3)
 route_kernel(const __grid_constant__ RouteProblem p) {
   wait_then_start_next();
   const int lane = threadIdx.x & 31;
   const int64_t row = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (row >= p.tokens) return;
-  const bool vec = p.vec;
-  const Lane a = lane_of(p, lane, vec);
+  const Lane<VEC> a = lane_of<VEC, V>(p, lane);
   float l[V];
-  load_logits<T, V>(p, row, a, vec, l);
+  load_logits<T>(p, row, a, l);
   bool close;
-  int e = choose<T, float, V>(p, row, a, l, close);
-  if (close) e = choose_again<T, V>(p, row, vec);
+  int e = choose<T>(p, row, a, l, close);
+  if (close) e = choose_again<T, VEC, V>(p, row);
   float m = 0.0f, sum = 1.0f;
   if (!p.sigmoid && !p.renormalise) {
     float top = -INFINITY;
@@ -373,19 +603,16 @@ route_grad_kernel(const __grid_constant__ RouteGradProblem p) {
   else
     d = s * (g - dot) * (p.sigmoid ? sigmoid(-x) : 1.0f);
   const float r = dense ? -dot / sum : 0.0f;
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-    for (int c = 0; c < W; ++c) l[i][c] = dense && l[i][c] != 0.0f ? l[i][c] * r : 0.0f;
-  for (int j = 0; j < p.k; ++j) {
-    const int at = __shfl_sync(kAll, e, j);
-    const float add = __shfl_sync(kAll, d, j);
-    if (at < 0) continue;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-      for (int c = 0; c < W; ++c)
-        if ((32 * i + lane) * W + c == at) l[i][c] += add;
+  // The same expert in several slots: the first of them adds them up.
+  const unsigned same = __match_any_sync(kAll, e);
+  const bool writes = e >= 0 && (same & ((1u << lane) - 1)) == 0;
+  if (__any_sync(kAll, e >= 0 && !writes)) {
+    float all = 0.0f;
+    for (int j = 0; j < p.k; ++j) {
+      const float add = __shfl_sync(kAll, d, j);
+      if (same >> j & 1) all += add;
+    }
+    d = all;
   }
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
@@ -393,12 +620,20 @@ route_grad_kernel(const __grid_constant__ RouteGradProblem p) {
     if (first >= p.experts) continue;
     if constexpr (VEC) {
       Vec<T> w;
+      w.w = make_uint4(0, 0, 0, 0);
+      if (dense)
 #pragma unroll
-      for (int c = 0; c < W; ++c) w.set(c, l[i][c]);
+        for (int c = 0; c < W; ++c) w.set(c, l[i][c] != 0.0f ? l[i][c] * r : 0.0f);
       *reinterpret_cast<uint4 *>(to + first) = w.w;
     } else {
-      to[first] = rounded<T>(l[i][0]);
+      to[first] = rounded<T>(dense && l[i][0] != 0.0f ? l[i][0] * r : 0.0f);
     }
+  }
+  __syncwarp();      // orders the row's stores before those of the slots
+  if (writes) {
+    // (What the row has there, once more: e^(x - m), and the slots' part.)
+    const float part = dense && x != -INFINITY ? expf(x - m) : 0.0f;
+    to[e] = rounded<T>((part != 0.0f ? part * r : 0.0f) + d);
   }
 }
 
@@ -427,15 +662,22 @@ cudaError_t launch_route_as(RouteProblem p, cudaStream_t stream) {
   const int need = (p.group_size + p.lanes - 1) / p.lanes;      // at most 32
   int V = 1;
   while (V < need) V *= 2;
-  p.vec = p.group_size == V * p.lanes && V * sizeof(T) % 16 == 0 &&
-          (reinterpret_cast<uintptr_t>(p.logits) & 15u) == 0 && p.ld * sizeof(T) % 16 == 0;
+  const bool vec = p.group_size == V * p.lanes && V * sizeof(T) % 16 == 0 &&
+                   (reinterpret_cast<uintptr_t>(p.logits) & 15u) == 0 && p.ld * sizeof(T) % 16 == 0;
+  p.vec_bias = (reinterpret_cast<uintptr_t>(p.bias) & 15u) == 0;
+  const auto launch = [&](auto few) {
+    constexpr int N = decltype(few)::value;
+    if constexpr (N * sizeof(T) % 16 == 0)
+      if (vec) return launch_rows(route_kernel<T, true, N>, p, p.tokens, stream);
+    return launch_rows(route_kernel<T, false, N>, p, p.tokens, stream);
+  };
   switch (V) {
-    case 1: return launch_rows(route_kernel<T, 1>, p, p.tokens, stream);
-    case 2: return launch_rows(route_kernel<T, 2>, p, p.tokens, stream);
-    case 4: return launch_rows(route_kernel<T, 4>, p, p.tokens, stream);
-    case 8: return launch_rows(route_kernel<T, 8>, p, p.tokens, stream);
-    case 16: return launch_rows(route_kernel<T, 16>, p, p.tokens, stream);
-    default: return launch_rows(route_kernel<T, 32>, p, p.tokens, stream);
+    case 1: return launch(std::integral_constant<int, 1>());
+    case 2: return launch(std::integral_constant<int, 2>());
+    case 4: return launch(std::integral_constant<int, 4>());
+    case 8: return launch(std::integral_constant<int, 8>());
+    case 16: return launch(std::integral_constant<int, 16>());
+    default: return launch(std::integral_constant<int, 32>());
   }
 }
 
