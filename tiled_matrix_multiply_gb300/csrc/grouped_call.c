@@ -1,11 +1,12 @@
-/* grouped_call.c -- the usual calls of the grouped operators, from torch tensors to the C ABI.
+/* grouped_call.c -- the usual calls of the grouped operators, of the operators over rows of scores and of
+ * linear layers, from torch tensors to the C ABI.
  *
  * The operators of a decode step take a few microseconds on the GPU; describing their tensors in
  * Python takes longer than that.  This CPython module does it for the usual case -- torch CUDA
  * tensors of the right types on the current device, outputs and workspace allocated here -- and
  * returns None for every other, which grouped.py then handles (and reports) in full.  It holds no
  * arithmetic and no torch headers: tensors are read through their Python attributes, and the
- * entry points' addresses are handed in.
+ * entry points' addresses are handed in (grouped.py, scores.py, linear.py).
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -323,7 +324,343 @@ static PyObject *start(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+/* ---- rows of scores ---------------------------------------------------------------------- */
+
+static PyObject *t_row_routes, *t_row_logprobs;
+static int (*f_route)(int, int64_t, int64_t, const void *, int64_t, const float *, int, int64_t,
+                      int64_t, int, int64_t, int, float, int32_t *, float *, tmm_stream_t);
+static int (*f_route_grad)(int, int64_t, int64_t, int64_t, const float *, const void *, int64_t,
+                           const int32_t *, int, int, float, void *, int64_t, tmm_stream_t);
+static int (*f_logprob)(int, int64_t, int64_t, const void *, int64_t, float, const void *, int, int,
+                        float *, float *, float *, int32_t *, float *, tmm_stream_t);
+static int (*f_logprob_grad)(int, int64_t, int64_t, const void *, int64_t, float, const float *,
+                             const void *, int, const float *, const float *, const float *, int,
+                             const int32_t *, const float *, void *, int64_t, tmm_stream_t);
+
+/* A whole number that fits an int, a truth value, a float: 0 for anything else. */
+static int int_of(PyObject *x, int *out) {
+  if (!PyLong_CheckExact(x)) return 0;
+  int over = 0;
+  const long v = PyLong_AsLongAndOverflow(x, &over);
+  *out = (int)v;
+  return !over && v == (long)*out;
+}
+static int truth_of(PyObject *x, int *out) {
+  *out = x == Py_True;
+  return x == Py_True || x == Py_False;
+}
+static int float_of(PyObject *x, float *out) {
+  if (!PyFloat_CheckExact(x)) return 0;
+  *out = (float)PyFloat_AS_DOUBLE(x);
+  return 1;
+}
+
+/* The address of a contiguous tensor of `rows` x `cols` (rows 0: `cols` values) of a type, on the
+ * operands' device; NULL for None where that is allowed. */
+static int array_of(PyObject *x, const Operand *like, PyObject *type, int64_t rows, int64_t cols,
+                    int none, void **out) {
+  Operand o;
+  *out = NULL;
+  if (x == Py_None) return none;
+  if (!describe(x, rows ? 2 : 1, 0, &o) || o.type != type || o.device != like->device ||
+      o.cols != cols || (rows && (o.rows != rows || o.ld != cols)))
+    return 0;
+  *out = o.ptr;
+  return 1;
+}
+
+/* New outputs: r[i] of shape (a) or, with b[i] >= 0, (a, b[i]). */
+static int new_outputs(int n, PyObject **r, void **p, int64_t a, const int64_t *b,
+                       PyObject *const *types, PyObject *device) {
+  for (int i = 0; i < n; ++i) {
+    r[i] = empty(b[i] < 0 ? Py_BuildValue("(L)", (long long)a)
+                          : Py_BuildValue("(LL)", (long long)a, (long long)b[i]),
+                 types[i], device);
+    if (r[i] == NULL || (p[i] = pointer(r[i])) == NULL) return 0;
+  }
+  return 1;
+}
+static PyObject *drop_all(int n, PyObject **r, PyObject *device) {
+  for (int i = 0; i < n; ++i) Py_XDECREF(r[i]);
+  return other(device, NULL, NULL);
+}
+
+static PyObject *route(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  Operand x;
+  int k, score, groups, top, best, renormalise;
+  float scale;
+  void *bias, *p[2];
+  tmm_stream_t s;
+  if (n != 9 || !describe(a[0], 2, 0, &x) || x.code < 0 || !int_of(a[1], &k) ||
+      !array_of(a[2], &x, t_float32, 0, x.cols, 1, &bias) || !int_of(a[3], &score) ||
+      !int_of(a[4], &groups) || !int_of(a[5], &top) || !int_of(a[6], &best) ||
+      !truth_of(a[7], &renormalise) || !float_of(a[8], &scale) || k < 1 || k > TMM_MAX_FAN ||
+      !stream_of(x.device, &s))
+    return other(NULL, NULL, NULL);
+  PyObject *device = PyObject_GetAttr(a[0], s_device), *r[2] = {NULL, NULL};
+  PyObject *const types[2] = {t_int32, t_float32};
+  const int64_t cols[2] = {k, k};
+  if (device == NULL || !new_outputs(2, r, p, x.rows, cols, types, device))
+    return drop_all(2, r, device);
+  WITHOUT_LOCK(f_route(x.code, x.rows, x.cols, x.ptr, x.ld, bias, score, groups, top, best, k,
+                       renormalise, scale, p[0], p[1], s))
+  if (rc != TMM_OK) return drop_all(2, r, device);
+  PyObject *out = PyObject_Vectorcall(t_row_routes, r, 2, NULL);
+  for (int i = 0; i < 2; ++i) Py_DECREF(r[i]);
+  Py_DECREF(device);
+  return out;
+}
+
+static PyObject *route_grad(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  Operand dw, x;
+  int score, renormalise;
+  float scale;
+  void *chosen, *p;
+  tmm_stream_t s;
+  if (n != 6 || !describe(a[0], 2, 0, &dw) || !describe(a[1], 2, 0, &x) || x.code < 0 ||
+      dw.type != t_float32 || dw.device != x.device || dw.rows != x.rows || dw.ld != dw.cols ||
+      !array_of(a[2], &x, t_int32, x.rows, dw.cols, 0, &chosen) || !int_of(a[3], &score) ||
+      !truth_of(a[4], &renormalise) || !float_of(a[5], &scale) || !stream_of(x.device, &s))
+    return other(NULL, NULL, NULL);
+  PyObject *device = PyObject_GetAttr(a[1], s_device), *r = NULL;
+  if (device == NULL || !new_outputs(1, &r, &p, x.rows, &x.cols, &x.type, device))
+    return drop_all(1, &r, device);
+  WITHOUT_LOCK(f_route_grad(x.code, x.rows, x.cols, dw.cols, dw.ptr, x.ptr, x.ld, chosen, score,
+                            renormalise, scale, p, x.cols, s))
+  if (rc != TMM_OK) return drop_all(1, &r, device);
+  Py_DECREF(device);
+  return r;
+}
+
+/* Tokens of int32 or int64, or None. */
+static int tokens_of(PyObject *x, const Operand *like, void **p, int *bits) {
+  *bits = 32;
+  if (array_of(x, like, t_int32, 0, like->rows, 1, p)) return 1;
+  *bits = 64;
+  return !PyErr_Occurred() && array_of(x, like, t_int64, 0, like->rows, 0, p);
+}
+
+static PyObject *logprob(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  Operand x;
+  int top, bits;
+  float scale;
+  void *tokens, *p[5] = {NULL, NULL, NULL, NULL, NULL};
+  tmm_stream_t s;
+  if (n != 4 || !describe(a[0], 2, 0, &x) || x.code < 0 || !tokens_of(a[1], &x, &tokens, &bits) ||
+      !int_of(a[2], &top) || top < 0 || top > TMM_MAX_TOP || !float_of(a[3], &scale) ||
+      !stream_of(x.device, &s))
+    return other(NULL, NULL, NULL);
+  PyObject *device = PyObject_GetAttr(a[0], s_device), *r[5] = {NULL, NULL, NULL, NULL, NULL};
+  PyObject *const types[5] = {t_float32, t_float32, t_float32, t_int32, t_float32};
+  const int64_t cols[5] = {-1, -1, -1, top, top};
+  const int skip = tokens == NULL;
+  if (device == NULL ||
+      !new_outputs((top ? 5 : 3) - skip, r + skip, p + skip, x.rows, cols + skip, types + skip,
+                   device))
+    return drop_all(5, r, device);
+  WITHOUT_LOCK(f_logprob(x.code, x.rows, x.cols, x.ptr, x.ld, scale, tokens, bits, top, p[0], p[1],
+                         p[2], p[3], p[4], s))
+  if (rc != TMM_OK) return drop_all(5, r, device);
+  for (int i = 0; i < 5; ++i)
+    if (r[i] == NULL) {
+      r[i] = Py_None;
+      Py_INCREF(Py_None);
+    }
+  PyObject *out = PyObject_Vectorcall(t_row_logprobs, r, 5, NULL);
+  for (int i = 0; i < 5; ++i) Py_DECREF(r[i]);
+  Py_DECREF(device);
+  return out;
+}
+
+static PyObject *logprob_grad(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  Operand x, e;
+  int bits, top = 0;
+  float scale;
+  void *tokens, *lse, *g, *entropy, *h, *ids = NULL, *dtop = NULL, *p;
+  tmm_stream_t s;
+  if (n != 9 || !describe(a[0], 2, 0, &x) || x.code < 0 || !tokens_of(a[1], &x, &tokens, &bits) ||
+      !array_of(a[2], &x, t_float32, 0, x.rows, 0, &lse) ||
+      !array_of(a[3], &x, t_float32, 0, x.rows, 1, &g) ||
+      !array_of(a[4], &x, t_float32, 0, x.rows, 1, &entropy) ||
+      !array_of(a[5], &x, t_float32, 0, x.rows, 1, &h) || (g && !tokens) || (h && !entropy) ||
+      !float_of(a[8], &scale) || !stream_of(x.device, &s))
+    return other(NULL, NULL, NULL);
+  if (a[7] != Py_None) {
+    if (!describe(a[7], 2, 0, &e) || e.cols > TMM_MAX_TOP ||
+        !array_of(a[7], &x, t_float32, x.rows, e.cols, 0, &dtop) ||
+        !array_of(a[6], &x, t_int32, x.rows, e.cols, 0, &ids))
+      return other(NULL, NULL, NULL);
+    top = (int)e.cols;
+  }
+  PyObject *device = PyObject_GetAttr(a[0], s_device), *r = NULL;
+  if (device == NULL || !new_outputs(1, &r, &p, x.rows, &x.cols, &x.type, device))
+    return drop_all(1, &r, device);
+  WITHOUT_LOCK(f_logprob_grad(x.code, x.rows, x.cols, x.ptr, x.ld, scale, lse, tokens, bits, g,
+                              entropy, h, top, ids, dtop, p, x.cols, s))
+  if (rc != TMM_OK) return drop_all(1, &r, device);
+  Py_DECREF(device);
+  return r;
+}
+
+/* ---- linear layers ------------------------------------------------------------------------ */
+
+static PyObject *t_linear_grads, *s_t;
+static int (*f_linear)(int, int, int, int64_t, int64_t, int64_t, const void *, int64_t, const void *,
+                       int64_t, const void *, int, const void *, int64_t, void *, int64_t, void *,
+                       int64_t, void *, size_t, tmm_stream_t);
+static size_t (*f_linear_size)(int, int, int64_t, int64_t, int64_t, const void *, int64_t,
+                               const void *, int64_t);
+static int (*f_linear_grad)(int, int, int, int64_t, int64_t, int64_t, const void *, int64_t,
+                            const void *, int64_t, const void *, int64_t, const void *, int64_t,
+                            void *, int64_t, void *, int64_t, int, float *, void *, size_t,
+                            tmm_stream_t);
+static size_t (*f_linear_grad_size)(int, int, int, int64_t, int64_t, int64_t, const void *, int64_t,
+                                    const void *, int64_t, const void *, int64_t, const void *,
+                                    const void *, int, const void *);
+
+static PyObject *linear(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  Operand x, w, res;
+  int act, pre, bias_f32 = 0;
+  void *bias = NULL, *p[2] = {NULL, NULL}, *wp;
+  tmm_stream_t s;
+  if (n != 6 || !describe(a[0], 2, 0, &x) || x.code < 0 || !describe(a[1], 2, 1, &w) ||
+      w.type != x.type || w.device != x.device || w.rows != x.cols || !int_of(a[3], &act))
+    return other(NULL, NULL, NULL);
+  if (a[2] != Py_None && !array_of(a[2], &x, x.type, 0, w.cols, 0, &bias)) {
+    bias_f32 = 1;
+    if (PyErr_Occurred() || !array_of(a[2], &x, t_float32, 0, w.cols, 0, &bias))
+      return other(NULL, NULL, NULL);
+  }
+  res.ptr = NULL;
+  res.ld = 1;
+  if (a[4] != Py_None && (!describe(a[4], 2, 0, &res) || res.type != x.type ||
+                          res.device != x.device || res.rows != x.rows || res.cols != w.cols))
+    return other(NULL, NULL, NULL);
+  pre = a[5] == Py_True;
+  if ((!pre && a[5] != Py_False && a[5] != Py_None) || !stream_of(x.device, &s))
+    return other(NULL, NULL, NULL);
+  const int64_t M = x.rows, N = w.cols, K = x.cols, cols[2] = {N, N};
+  PyObject *device = PyObject_GetAttr(a[0], s_device), *ws = NULL, *r[2] = {NULL, NULL};
+  PyObject *const types[2] = {x.type, x.type};
+  const size_t need = f_linear_size(x.code, w.trans, M, N, K, x.ptr, x.ld, w.ptr, w.ld);
+  if (device == NULL || !scratch(need, device, &ws, &wp) ||
+      !new_outputs(1 + pre, r, p, M, cols, types, device)) {
+    Py_XDECREF(ws);
+    return drop_all(2, r, device);
+  }
+  WITHOUT_LOCK(f_linear(x.code, w.trans, act, M, N, K, x.ptr, x.ld, w.ptr, w.ld, bias, bias_f32,
+                        res.ptr, res.ld, p[0], N, p[1], N, wp, need, s))
+  Py_XDECREF(ws);
+  if (rc != TMM_OK) return drop_all(2, r, device);
+  Py_DECREF(device);
+  if (!pre) return r[0];
+  PyObject *out = PyTuple_Pack(2, r[0], r[1]);
+  for (int i = 0; i < 2; ++i) Py_DECREF(r[i]);
+  return out;
+}
+
+static PyObject *linear_grad(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  Operand dy, x, w, z;
+  int act, want_bias;
+  void *p[3] = {NULL, NULL, NULL}, *wp;
+  tmm_stream_t s;
+  if (n != 6 || !describe(a[0], 2, 0, &dy) || dy.code < 0 || !describe(a[1], 2, 0, &x) ||
+      !describe(a[2], 2, 1, &w) || x.type != dy.type || w.type != dy.type ||
+      x.device != dy.device || w.device != dy.device || x.rows != dy.rows || w.rows != x.cols ||
+      w.cols != dy.cols || !int_of(a[4], &act) || act < 0 || !truth_of(a[5], &want_bias))
+    return other(NULL, NULL, NULL);
+  z.ptr = NULL;
+  z.ld = 1;
+  if (act != TMM_ACT_NONE &&
+      (!describe(a[3], 2, 0, &z) || z.type != dy.type || z.device != dy.device ||
+       z.rows != dy.rows || z.cols != dy.cols))
+    return other(NULL, NULL, NULL);
+  if (!stream_of(dy.device, &s)) return other(NULL, NULL, NULL);
+  const int64_t M = dy.rows, N = dy.cols, K = x.cols;
+  const int64_t lddw = w.trans ? K : N;
+  PyObject *device = PyObject_GetAttr(a[0], s_device), *ws = NULL, *r[3] = {NULL, NULL, NULL};
+  const int64_t none = -1;
+  int ok = device != NULL && new_outputs(1, r, p, M, &K, &dy.type, device) &&
+           new_outputs(1, r + 1, p + 1, w.trans ? N : K, &lddw, &dy.type, device) &&
+           (!want_bias || new_outputs(1, r + 2, p + 2, N, &none, &t_float32, device));
+  size_t need = 0;
+  if (ok) {
+    need = f_linear_grad_size(dy.code, w.trans, act, M, N, K, dy.ptr, dy.ld, x.ptr, x.ld, w.ptr,
+                              w.ld, p[0], p[1], w.trans, p[2]);
+    ok = scratch(need, device, &ws, &wp);
+  }
+  if (ok && w.trans) {      // laid out as w is
+    PyObject *v = PyObject_CallMethodNoArgs(r[1], s_t);
+    ok = v != NULL;
+    if (ok) {
+      Py_DECREF(r[1]);
+      r[1] = v;
+    }
+  }
+  if (!ok) {
+    Py_XDECREF(ws);
+    return drop_all(3, r, device);
+  }
+  WITHOUT_LOCK(f_linear_grad(dy.code, w.trans, act, M, N, K, dy.ptr, dy.ld, x.ptr, x.ld, w.ptr, w.ld,
+                             z.ptr, z.ld, p[0], K, p[1], lddw, w.trans, p[2], wp, need, s))
+  Py_XDECREF(ws);
+  if (rc != TMM_OK) return drop_all(3, r, device);
+  if (!want_bias) {
+    r[2] = Py_None;
+    Py_INCREF(Py_None);
+  }
+  PyObject *out = PyObject_Vectorcall(t_linear_grads, r, 3, NULL);
+  for (int i = 0; i < 3; ++i) Py_DECREF(r[i]);
+  Py_DECREF(device);
+  return out;
+}
+
+/* What the modules hand in, once each: result types, and entry points. */
+static PyObject *take(PyObject *const *a, Py_ssize_t n, int objects, PyObject **const *to,
+                      int functions, void **const *fn) {
+  if (n != 2 || !PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) != objects || !PyTuple_Check(a[1]) ||
+      PyTuple_GET_SIZE(a[1]) != functions) {
+    PyErr_SetString(PyExc_TypeError, "two tuples: objects, addresses");
+    return NULL;
+  }
+  for (int i = 0; i < objects; ++i) {
+    *to[i] = PyTuple_GET_ITEM(a[0], i);
+    Py_INCREF(*to[i]);
+  }
+  for (int i = 0; i < functions; ++i) *fn[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[1], i));
+  if (PyErr_Occurred()) return NULL;
+  Py_RETURN_NONE;
+}
+static PyObject *start_scores(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  PyObject **const to[2] = {&t_row_routes, &t_row_logprobs};
+  void **const fn[4] = {(void **)&f_route, (void **)&f_route_grad, (void **)&f_logprob,
+                        (void **)&f_logprob_grad};
+  return take(a, n, 2, to, 4, fn);
+}
+static PyObject *start_linear(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  PyObject **const to[1] = {&t_linear_grads};
+  void **const fn[4] = {(void **)&f_linear, (void **)&f_linear_size, (void **)&f_linear_grad,
+                        (void **)&f_linear_grad_size};
+  return take(a, n, 1, to, 4, fn);
+}
+
 static PyMethodDef methods[] = {
+    {"start_scores", (PyCFunction)(void (*)(void))start_scores, METH_FASTCALL, NULL},
+    {"start_linear", (PyCFunction)(void (*)(void))start_linear, METH_FASTCALL, NULL},
+    {"route", (PyCFunction)(void (*)(void))route, METH_FASTCALL, NULL},
+    {"route_grad", (PyCFunction)(void (*)(void))route_grad, METH_FASTCALL, NULL},
+    {"logprob", (PyCFunction)(void (*)(void))logprob, METH_FASTCALL, NULL},
+    {"logprob_grad", (PyCFunction)(void (*)(void))logprob_grad, METH_FASTCALL, NULL},
+    {"linear", (PyCFunction)(void (*)(void))linear, METH_FASTCALL, NULL},
+    {"linear_grad", (PyCFunction)(void (*)(void))linear_grad, METH_FASTCALL, NULL},
     {"start", (PyCFunction)(void (*)(void))start, METH_FASTCALL, NULL},
     {"grouped", (PyCFunction)(void (*)(void))grouped, METH_FASTCALL, NULL},
     {"wgrad", (PyCFunction)(void (*)(void))wgrad, METH_FASTCALL, NULL},
@@ -341,6 +678,7 @@ PyMODINIT_FUNC PyInit_grouped_call(void) {
                                       "stride", "data_ptr", "get_device"};
   for (int i = 0; i < 7; ++i)
     if ((*names[i] = PyUnicode_InternFromString(text[i])) == NULL) return NULL;
+  if ((s_t = PyUnicode_InternFromString("t")) == NULL) return NULL;
   t_kwnames = Py_BuildValue("(OO)", s_dtype, s_device);
   if (t_kwnames == NULL) return NULL;
   return PyModule_Create(&module);

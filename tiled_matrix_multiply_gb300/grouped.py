@@ -178,6 +178,8 @@ class _NoCall:
         return None
 
     grouped = wgrad = lora = group_rows
+    route = route_grad = logprob = logprob_grad = linear = linear_grad = group_rows
+    start_scores = start_linear = group_rows
 
 
 def _load_call():
@@ -200,6 +202,12 @@ def _load_call():
                   torch.bfloat16, torch.float16),
                  tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
     return module
+
+
+def _addresses(*names):
+    """The entry points' addresses, as the marshalling module takes them."""
+    lib = _abi.load()
+    return tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names)
 
 
 _usual = _load_call()

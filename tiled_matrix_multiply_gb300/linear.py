@@ -19,7 +19,8 @@ from typing import NamedTuple
 import torch
 
 from . import _abi
-from .grouped import _call, _first, _given_workspace, _on_stream, _operand, _result, _scratch
+from .grouped import (_addresses, _call, _first, _given_workspace, _on_stream, _operand, _result,
+                      _scratch, _usual)
 
 _ACTS = {"none": _abi.TMM_ACT_NONE, "relu": _abi.TMM_ACT_RELU, "silu": _abi.TMM_ACT_SILU,
          "gelu": _abi.TMM_ACT_GELU, "gelu_tanh": _abi.TMM_ACT_GELU_TANH}
@@ -30,6 +31,11 @@ class LinearGrads(NamedTuple):
     dx: object
     dw: object
     dbias: object       # float32
+
+
+_usual.start_linear((LinearGrads,), _addresses(
+    "gemm_bias_act", "gemm_bias_act_workspace_size", "gemm_bias_act_grad",
+    "gemm_bias_act_grad_workspace_size"))
 
 
 def _act(act):
@@ -55,6 +61,10 @@ def gemm_bias_act(x, w, bias=None, act="none", residual=None, y=None, pre=None, 
     (M, N), which y may be itself.  pre: True, or a matrix (M, N), to keep z = x w + bias for the
     gradients; then (y, z) is returned.
     """
+    if y is None and workspace is None and stream is None:
+        done = _usual.linear(x, w, bias, _ACTS.get(act, -1), residual, pre)
+        if done is not None:
+            return done
     code = _first(x, "x")
     if stream is not None:
         return _on_stream(stream, x, gemm_bias_act, x, w, bias, act, residual, y, pre, workspace)
@@ -110,6 +120,10 @@ def gemm_bias_act_grad(dy, x, w, pre=None, act="none", dx=True, dw=True, dbias=F
     and dbias: True, False, or a tensor for the result; a new dw is laid out as w is.  w may be None
     without dx, and x without dw.
     """
+    if dx is True and dw is True and workspace is None and stream is None:
+        done = _usual.linear_grad(dy, x, w, pre, _ACTS.get(act, -1), dbias)
+        if done is not None:
+            return done
     code = _first(dy, "dy")
     if stream is not None:
         return _on_stream(stream, dy, gemm_bias_act_grad, dy, x, w, pre, act, dx, dw, dbias,

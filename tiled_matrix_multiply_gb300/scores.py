@@ -26,7 +26,7 @@ from typing import NamedTuple
 import torch
 
 from . import _abi
-from .grouped import _call_plain, _first, _on_stream, _operand
+from .grouped import _addresses, _call_plain, _first, _on_stream, _operand, _usual
 
 _SCORES = {"softmax": _abi.TMM_SOFTMAX, "sigmoid": _abi.TMM_SIGMOID}
 
@@ -44,6 +44,11 @@ class RowLogprobs(NamedTuple):
     lse: object            # (rows): log of the sum of exponentials
     top_ids: object        # int32 (rows, top), or None
     top_logprobs: object   # (rows, top), or None
+
+
+_usual.start_scores((RowRoutes, RowLogprobs),
+                    _addresses("route_rows", "route_rows_grad", "logprob_rows",
+                               "logprob_rows_grad"))
 
 
 def _score(score):
@@ -92,6 +97,11 @@ def route_rows(logits, k, bias=None, score="softmax", groups=1, top_groups=1, gr
     ``renormalise`` scale * s.  An expert whose logit or bias is -inf is never chosen; where none is
     left the expert is -1 and its weight 0.
     """
+    if stream is None:
+        done = _usual.route(logits, k, bias, _SCORES.get(score, -1), groups, top_groups, group_best,
+                            renormalise, scale)
+        if done is not None:
+            return done
     code = _first(logits, "logits")
     if stream is not None:
         return _on_stream(stream, logits, route_rows, logits, k, bias, score, groups, top_groups,
@@ -115,6 +125,11 @@ def route_rows_grad(dweights, logits, experts, score="softmax", renormalise=True
     dweights: float32 (tokens, k); logits, score, renormalise and scale as there; experts: int32
     (tokens, k), what it chose (numbers outside the experts have no part).  dlogits may be logits.
     """
+    if dlogits is None and stream is None:
+        done = _usual.route_grad(dweights, logits, experts, _SCORES.get(score, -1), renormalise,
+                                 scale)
+        if done is not None:
+            return done
     code = _first(logits, "logits")
     if stream is not None:
         return _on_stream(stream, logits, route_rows_grad, dweights, logits, experts, score,
@@ -146,6 +161,10 @@ def logprob_rows(logits, tokens=None, top=0, scale=1.0, stream=None):
     probability is 0), or None.  top: how many of the most probable tokens to list, at most 32.
     Returns ``RowLogprobs``.
     """
+    if stream is None:
+        done = _usual.logprob(logits, tokens, top, scale)
+        if done is not None:
+            return done
     code = _first(logits, "logits")
     if stream is not None:
         return _on_stream(stream, logits, logprob_rows, logits, tokens, top, scale)
@@ -175,6 +194,11 @@ def logprob_rows_grad(logits, tokens, lse, dlogprob=None, entropy=None, dentropy
     tokens), dentropy: float32 (rows); dtop: float32 (rows, top), the gradient of the listed log
     probabilities.  dlogits may be logits (in place).
     """
+    if dlogits is None and stream is None:
+        done = _usual.logprob_grad(logits, tokens, lse, dlogprob, entropy, dentropy, top_ids, dtop,
+                                   scale)
+        if done is not None:
+            return done
     code = _first(logits, "logits")
     if stream is not None:
         return _on_stream(stream, logits, logprob_rows_grad, logits, tokens, lse, dlogprob, entropy,
