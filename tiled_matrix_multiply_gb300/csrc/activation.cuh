@@ -1,16 +1,19 @@
-// activation.cuh -- the activations of a linear layer's epilogue and their derivatives.
+// activation.cuh -- the activations of a linear layer's epilogue and their derivatives, on pairs of FP32
+// values (fma.rn.f32x2 and the like: two results an instruction).
 //
 //   relu       max(z, 0)                        (derivative at 0: 0)
 //   silu       z s(z),                          s(z) = 1 / (1 + e^-z)
-//   gelu       z Phi(z) = z/2 erfc(-z / sqrt 2)
+//   gelu       z Phi(z) = max(z, 0) - |z| Phi(-|z|)
 //   gelu_tanh  z/2 (1 + tanh u) = z s(2 u),     u = sqrt(2/pi) (z + 0.044715 z^3)
-// FAST, for results of 16 bits: the exponential and the quotient are the hardware's approximations
-// (relative errors of a few 2^-22, far below 2^-12), and e^-z may overflow, which gives s = 0.
-// There erfc(x) = e^(-x^2) t q(t), t = 1 / (1 + 0.45 x), x >= 0: x e^(x^2) erfc(x) tends to a constant,
-// so that t q(t) stands for e^(x^2) erfc(x) with a relative error below 2^-21 everywhere.  q is the
-// polynomial of degree 7 whose largest relative error on [0, 10] is the smallest (a linear program
-// over 4001 points).  CUDA's erfcf, right to a few 2^-24 and three times as many instructions, held
-// the result warps up beyond the products: 8192 x 4096 x 4096 in bf16 190 us, without activation 154.
+//   Phi(-a) = erfc(a / sqrt 2) / 2,  erfc(x) = e^(-x^2) t q(t),  t = 1 / (1 + c x):  x e^(x^2) erfc(x) tends
+//   to a constant, so that t q(t) stands for e^(x^2) erfc(x) with a bounded relative error everywhere.
+//   q is the polynomial whose largest relative error on [0, 10] is the smallest (a linear program over
+//   4001 points): of degree 7 and c = 0.45, 2^-21.7; of degree 8 and c = 0.5, 2^-24.6.  CUDA's erfcf has
+//   three times as many instructions and held the result warps up beyond the products: 8192 x 4096 x
+//   4096 in bf16 190 us, without activation 154.
+// FAST, for results of 16 bits: exponentials by the hardware's power of two with a rounded argument
+// (relative error 2^-22 and |z| 2^-24, far below 2^-12).  Else the argument's rounding is made up for.
+// Infinities and NaN are the formulas'.
 #pragma once
 
 #include <cstdint>
@@ -20,75 +23,6 @@
 #include "tmm_gemm.h"
 
 namespace tmm {
-
-template <bool FAST>
-__device__ __forceinline__ float logistic(float z) {
-  if (FAST) return __fdividef(1.0f, 1.0f + __expf(-z));
-  return 1.0f / (1.0f + expf(-z));
-}
-__device__ __forceinline__ float tanh_argument(float z) {      // 2 u
-  return 1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.0f);
-}
-
-// Phi(-|z|), and e^(-z^2 / 2).
-__device__ __forceinline__ float normal_tail(float z, float &e) {
-  const float t = __fdividef(1.0f, fmaf(0.31819805f, fabsf(z), 1.0f));
-  float q = 0.0668829f;
-  q = fmaf(q, t, -0.24035851f);
-  q = fmaf(q, t, 0.2090319f);
-  q = fmaf(q, t, 0.04007119f);
-  q = fmaf(q, t, 0.18879604f);
-  q = fmaf(q, t, 0.22802131f);
-  q = fmaf(q, t, 0.25364735f);
-  q = fmaf(q, t, 0.25390811f);
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-0.72134752f * z * z));
-  return 0.5f * t * q * e;
-}
-
-template <bool FAST>
-__device__ __forceinline__ float activate(int act, float z) {
-  switch (act) {
-    case TMM_ACT_RELU: return z < 0.0f ? 0.0f : z;
-    case TMM_ACT_SILU: return z * logistic<FAST>(z);
-    case TMM_ACT_GELU: {
-      if (!FAST) return 0.5f * z * erfcf(-0.70710678118654752f * z);
-      // z Phi(-|z|), less z where z > 0; (a tail of 0 times an infinity is 0).
-      float e;
-      const float r = copysignf(fminf(fabsf(z), 64.0f), z) * normal_tail(z, e);
-      return z > 0.0f ? z - r : r;
-    }
-    case TMM_ACT_GELU_TANH: return z * logistic<FAST>(tanh_argument(z));
-    default: return z;
-  }
-}
-
-// The derivative at z.
-template <bool FAST>
-__device__ __forceinline__ float activation_slope(int act, float z) {
-  switch (act) {
-    case TMM_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-    case TMM_ACT_SILU: {
-      const float s = logistic<FAST>(z), r = logistic<FAST>(-z);
-      return s * fmaf(z, r, 1.0f);
-    }
-    case TMM_ACT_GELU: {
-      if (!FAST)
-        return fmaf(0.5f, erfcf(-0.70710678118654752f * z),
-                    0.39894228040143268f * z * expf(-0.5f * z * z));
-      float e;
-      const float tail = normal_tail(z, e);
-      return fmaf(0.39894228040143268f * z, e, z > 0.0f ? 1.0f - tail : tail);
-    }
-    case TMM_ACT_GELU_TANH: {
-      z = z > 1e4f ? 1e4f : z < -1e4f ? -1e4f : z;      // constant beyond, and z^3 finite
-      const float v = tanh_argument(z), s = logistic<FAST>(v), r = logistic<FAST>(-v);
-      return s * fmaf(z * r, 1.5957691216057308f * fmaf(0.134145f * z, z, 1.0f), 1.0f);
-    }
-    default: return 1.0f;
-  }
-}
-
-// ---- pairs, for results of 16 bits ---------------------------------------------------------
 
 __device__ __forceinline__ uint64_t pair_of(float x, float y) {
   uint64_t v;
@@ -122,78 +56,132 @@ __device__ __forceinline__ uint64_t reciprocal2(uint64_t v) {
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(f.y));
   return pair_of(f.x, f.y);
 }
-__device__ __forceinline__ uint64_t exp2_pair(uint64_t v) {
+__device__ __forceinline__ uint64_t power2(uint64_t v) {
   float2 f = of_pair(v);
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(f.x));
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(f.y));
   return pair_of(f.x, f.y);
 }
-__device__ __forceinline__ float positive_part(float z) {      // (NaN stays)
+// Between lo and hi; NaN stays.
+__device__ __forceinline__ float within(float v, float lo, float hi) {
+  float y;
+  asm("{\n .reg .f32 t;\n max.NaN.f32 t, %1, %2;\n min.NaN.f32 %0, t, %3;\n}\n"
+      : "=f"(y)
+      : "f"(v), "f"(lo), "f"(hi));
+  return y;
+}
+__device__ __forceinline__ float positive_part(float z) {
   float y;
   asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(z));
   return y;
 }
-// z / (1 + 2^u)
-__device__ __forceinline__ uint64_t times_logistic2(uint64_t z, uint64_t u) {
-  return mul2(z, reciprocal2(add2(exp2_pair(u), both(1.0f))));
-}
 
-// Two values at once, half the instructions; the same formulas as `activate`.
+// e^v
+template <bool FAST>
+__device__ __forceinline__ uint64_t exp_pair(uint64_t v) {
+  if (FAST) return power2(mul2(v, both(1.44269504f)));
+  const float2 f = of_pair(v);
+  v = pair_of(within(f.x, -88.0f, 88.0f), within(f.y, -88.0f, 88.0f));      // (finite, 0 in 1 / e)
+  // v log2(e) = h + l, and e^v = 2^h (1 + l ln 2).
+  const uint64_t h = mul2(v, both(1.44269504f));
+  const uint64_t l = fma2(v, both(1.9259630e-8f), fma2(v, both(1.44269504f), mul2(h, both(-1.0f))));
+  const uint64_t e = power2(h);
+  return fma2(mul2(e, l), both(0.69314718f), e);
+}
+// 1 / (1 + e^v)
+template <bool FAST>
+__device__ __forceinline__ uint64_t logistic(uint64_t v) {
+  return reciprocal2(add2(exp_pair<FAST>(v), both(1.0f)));
+}
+// Phi(-a), and e = e^(-a^2 / 2); a >= 0.
+template <bool FAST>
+__device__ __forceinline__ uint64_t normal_tail(uint64_t a, uint64_t &e) {
+  // The coefficients of q / 2, the highest first.
+  constexpr float few[8] = {0.03344145f, -0.120179255f, 0.10451595f, 0.020035585f,
+                            0.09439802f, 0.114010655f,  0.126823675f, 0.126954055f};
+  constexpr float more[9] = {-0.0291917f, 0.14065922f, -0.240339115f, 0.135458545f, -0.010982505f,
+                             0.100426475f, 0.121762545f, 0.14116206f, 0.141044465f};
+  const uint64_t t = reciprocal2(fma2(a, both(FAST ? 0.31819805f : 0.35355339f), both(1.0f)));
+  uint64_t q = both(FAST ? few[0] : more[0]);
+#pragma unroll
+  for (int i = 1; i < (FAST ? 8 : 9); ++i) q = fma2(q, t, both(FAST ? few[i] : more[i]));
+  e = FAST ? power2(mul2(mul2(a, both(-0.72134752f)), a))
+           : exp_pair<false>(mul2(mul2(a, both(-0.5f)), a));
+  return mul2(mul2(t, q), e);
+}
+constexpr float kTanhSlope = 1.5957691216057308f, kTanhCube = 0.044715f;      // 2 sqrt(2/pi)
+
+template <bool FAST>
 __device__ __forceinline__ uint64_t activate2(int act, uint64_t z) {
   const float2 f = of_pair(z);
   switch (act) {
     case TMM_ACT_RELU: return pair_of(positive_part(f.x), positive_part(f.y));
-    case TMM_ACT_SILU: return times_logistic2(z, mul2(z, both(-1.44269504f)));
+    case TMM_ACT_SILU: return mul2(z, logistic<FAST>(mul2(z, both(-1.0f))));
     case TMM_ACT_GELU: {
-      // max(z, 0) - a Phi(-a), a = |z| (no more than 64, whose tail is 0).
+      // (|z| no more than 64, whose tail is 0.)
       const uint64_t a = pair_of(fminf(fabsf(f.x), 64.0f), fminf(fabsf(f.y), 64.0f));
-      const uint64_t t = reciprocal2(fma2(a, both(0.31819805f), both(1.0f)));
-      uint64_t q = both(0.5f * 0.0668829f);
-      q = fma2(q, t, both(0.5f * -0.24035851f));
-      q = fma2(q, t, both(0.5f * 0.2090319f));
-      q = fma2(q, t, both(0.5f * 0.04007119f));
-      q = fma2(q, t, both(0.5f * 0.18879604f));
-      q = fma2(q, t, both(0.5f * 0.22802131f));
-      q = fma2(q, t, both(0.5f * 0.25364735f));
-      q = fma2(q, t, both(0.5f * 0.25390811f));
-      const uint64_t e = exp2_pair(mul2(mul2(a, both(-0.72134752f)), a));
-      const uint64_t tail = mul2(mul2(t, q), mul2(e, both(-1.0f)));
-      return fma2(a, tail, pair_of(positive_part(f.x), positive_part(f.y)));
+      uint64_t e;
+      return fma2(mul2(a, both(-1.0f)), normal_tail<FAST>(a, e),
+                  pair_of(positive_part(f.x), positive_part(f.y)));
     }
     case TMM_ACT_GELU_TANH: {
-      // z s(2 u): the exponent -2 u log2(e) = z (c0 + c1 z^2).
-      const uint64_t square = mul2(z, z);
-      return times_logistic2(
-          z, mul2(z, fma2(square, both(-2.3022082f * 0.044715f), both(-2.3022082f))));
+      const uint64_t w = fma2(mul2(z, z), both(-kTanhSlope * kTanhCube), both(-kTanhSlope));
+      return mul2(z, logistic<FAST>(mul2(z, w)));
     }
     default: return z;
   }
 }
-template <int N>
-__device__ __forceinline__ void activate_pairs(int act, uint64_t (&z)[N]) {
-  if (act == TMM_ACT_NONE) return;
+// The derivatives at z.
+template <bool FAST>
+__device__ __forceinline__ uint64_t slope2(int act, uint64_t z) {
+  float2 f = of_pair(z);
+  const uint64_t one = both(1.0f), minus = both(-1.0f);
+  switch (act) {
+    case TMM_ACT_RELU: return pair_of(f.x > 0.0f ? 1.0f : 0.0f, f.y > 0.0f ? 1.0f : 0.0f);
+    case TMM_ACT_SILU: {
+      const uint64_t s = logistic<FAST>(mul2(z, minus));
+      return mul2(s, fma2(z, fma2(s, minus, one), one));
+    }
+    case TMM_ACT_GELU: {
+      uint64_t e;
+      const float2 tail = of_pair(normal_tail<FAST>(pair_of(fabsf(f.x), fabsf(f.y)), e));
+      return fma2(mul2(z, both(0.39894228f)), e,
+                  pair_of(f.x > 0.0f ? 1.0f - tail.x : tail.x,
+                          f.y > 0.0f ? 1.0f - tail.y : tail.y));
+    }
+    case TMM_ACT_GELU_TANH: {
+      // (Constant beyond 10^4, and z^3 finite.)
+      z = pair_of(within(f.x, -1e4f, 1e4f), within(f.y, -1e4f, 1e4f));
+      const uint64_t square = mul2(z, z);
+      const uint64_t w = fma2(square, both(-kTanhSlope * kTanhCube), both(-kTanhSlope));
+      const uint64_t s = logistic<FAST>(mul2(z, w));
+      const uint64_t d = fma2(square, both(3.0f * kTanhSlope * kTanhCube), both(kTanhSlope));
+      return mul2(s, fma2(mul2(z, fma2(s, minus, one)), d, one));
+    }
+    default: return one;
+  }
+}
+
+// f of every pair, with one choice for all.  (A chain of comparisons: a jump table's first use in a block
+// costs more than a thousand cycles.)
+template <int N, typename F>
+__device__ __forceinline__ void for_activation(int act, uint64_t (&z)[N], F f) {
 #pragma unroll
   for (int code = TMM_ACT_RELU; code <= TMM_ACT_GELU_TANH; ++code)
     if (act == code) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) z[k] = activate2(code, z[k]);
+      for (int k = 0; k < N; ++k) z[k] = f(code, z[k]);
       return;
     }
 }
-// N values, with one choice for all.
-template <int N>
-__device__ __forceinline__ void activate_all(int act, float (&z)[N]) {
+template <bool FAST, int N>
+__device__ __forceinline__ void activate_pairs(int act, uint64_t (&z)[N]) {
   if (act == TMM_ACT_NONE) return;
-  uint64_t v[N / 2];
-#pragma unroll
-  for (int k = 0; k < N / 2; ++k) v[k] = pair_of(z[2 * k], z[2 * k + 1]);
-  activate_pairs(act, v);
-#pragma unroll
-  for (int k = 0; k < N / 2; ++k) {
-    const float2 f = of_pair(v[k]);
-    z[2 * k] = f.x;
-    z[2 * k + 1] = f.y;
-  }
+  for_activation(act, z, [](int code, uint64_t v) { return activate2<FAST>(code, v); });
+}
+template <bool FAST, int N>
+__device__ __forceinline__ void slope_pairs(int act, uint64_t (&z)[N]) {
+  for_activation(act, z, [](int code, uint64_t v) { return slope2<FAST>(code, v); });
 }
 
 }  // namespace tmm

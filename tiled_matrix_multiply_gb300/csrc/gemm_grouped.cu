@@ -67,7 +67,7 @@
 #include <type_traits>
 
 #include "grouped.h"
-#include "linear_epilogue.cuh"
+#include "split_bf16.cuh"
 #include "tensor_core.cuh"
 #include "tmm_gemm.h"
 
@@ -77,7 +77,7 @@ __device__ unsigned int g_grouped_status;
 
 namespace {
 
-constexpr int kForward = 0, kWgrad = 1, kLora = 2, kLinear = 3;
+constexpr int kForward = 0, kWgrad = 1, kLora = 2;
 constexpr int kBK = 64;                  // 16-bit values per K slice: one 128-byte swizzle row
 constexpr int kEpiWarps = 8;
 constexpr int kListed = kMaxGroups + 3;            // entries of a list of groups, see Table
@@ -95,8 +95,10 @@ __device__ __forceinline__ int long_sum(int n) {
 constexpr uint32_t kPTile = 128 * 128;   // 128 lanes x 64 values: 16 KiB
 constexpr uint32_t kMaxSmem = 232448;    // 227 KiB
 
-// How the results are written, beside kOutF32, kOutBF16 and kOutF16.
+// How the results are written.
+constexpr int kOutF32 = 0, kOutBF16 = 1, kOutF16 = 2;
 constexpr int kOutU = 3;       // the adapters' u: its parts, in three planes or side by side
+
 
 // Values of `rank` per slice of the adapters' part: as many as the parts of u leave of the 64 columns
 // of a slice (store_u4), or FP32's planes.
@@ -104,8 +106,7 @@ __host__ __device__ constexpr int rank_slice(int planes, int b_parts) {
   return planes == 3 ? 64 : b_parts == 2 ? 16 : 32;
 }
 
-// STAGE: bytes of a result warp for 16-bit results.
-template <int CG, int PLANES, int STAGE = 1024>
+template <int CG, int PLANES>
 struct Shape {
   // FP32 on single blocks: the copy warps read the operands as they are stored and split them
   // on the way (DIRECT); no planes.
@@ -123,9 +124,9 @@ struct Shape {
   static constexpr int kStages = PLANES == 3 ? (CG == 2 ? 3 : 2) : (CG == 2 ? 6 : 7);
   static constexpr uint32_t kTmemCols =
       PLANES == 3 ? 4 * kBN : 2 * kBN;               // two accumulators (of each kind)
-  // The parts of a shared sum (single blocks), and where 16-bit results are transposed.
+  // The parts of a shared sum (single blocks), and 1 KiB a result warp for 16-bit results.
   static constexpr uint32_t kRed = CG == 1 ? 128 * kBN * 4 : 0;
-  static constexpr uint32_t kOutStage = PLANES == 1 ? kEpiWarps * STAGE : 0;
+  static constexpr uint32_t kOutStage = PLANES == 1 ? kEpiWarps * 1024 : 0;
   static constexpr uint32_t kTable =
       kListed * 4 * 3 + kCopyWarps * 128 + 116 + (CG == 1 ? kFewRows * 4 : 0);
   static constexpr uint32_t kBars = 8 * (2 * kStages + 5) + 32;
@@ -134,13 +135,10 @@ struct Shape {
   static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory columns");
 };
 
-template <int CG, int MODE, int PLANES>
-using ModeShape = Shape<CG, PLANES, MODE == kLinear ? 2048 : 1024>;
-
 struct Params {
   int rows;              // p runs over [0, rows)
   int groups;
-  const int *offsets;    // groups + 1, or NULL: one group of all rows
+  const int *offsets;    // groups + 1
   const int *row_index;  // r(p) of the rows read (single blocks; pairs read gathered rows), or NULL
   const int *out_index;  // r(p) of the rows written (adapters), or NULL
   int q_rows;            // rows of the x that is read
@@ -171,14 +169,6 @@ struct Params {
   int64_t ldu, ldb, stride_b;
   int trans_b, vec_b;
   int zero_rows;         // forward: write zeros to the rows of no group
-  // Linear: y = act(x w + bias) + residual, and z = x w + bias beside it.
-  const void *bias;      // of N values, or NULL
-  int bias_f32;          // else of the operands' type
-  int act;               // TMM_ACT_*
-  const void *residual;  // rows x N, or NULL
-  void *pre;             // rows x N, or NULL
-  int64_t ld_residual, ld_pre;
-  int epilogue;          // any of them
   int ksplit;            // blocks of a cluster that share a tile's sum (CG = 1)
   int64_t wait_limit_ns;
   int drop_block;        // testing hook: this block waits for bytes that never come (-1: none)
@@ -311,67 +301,6 @@ __device__ __forceinline__ void slices_of(const Params &p, const Tile &t, int ra
   } else {
     s0 = int(int64_t(n) * rank / p.ksplit);
     s1 = int(int64_t(n) * (rank + 1) / p.ksplit);
-  }
-}
-
-// The bf16 nearest an FP32 value (ties away from zero), as its bits; in the top binade, where
-// rounding could reach infinity, the value truncated.
-__device__ __forceinline__ uint32_t nearest_bf16(uint32_t b) {
-  return (b & 0x7F800000u) == 0x7F000000u ? b & 0xFFFF0000u : (b + 0x8000u) & 0xFFFF0000u;
-}
-// The three bf16 parts of an FP32 value: each the nearest to what the ones before leave, so
-// |x1| <= 2^-8 |x| and |x2| <= 2^-16 |x|, and x = x0 + x1 + x2 exactly (for |x| >= 2^-102;
-// below, what falls under the smallest subnormal is dropped).  An infinity or a NaN is its own
-// first part.
-__device__ __forceinline__ void split3(float x, uint16_t (&h)[3]) {
-  const uint32_t b = __float_as_uint(x);
-  if ((b & 0x7F800000u) == 0x7F800000u) {
-    h[0] = uint16_t((b >> 16) | ((b & 0x007FFFFFu) ? 0x0040u : 0u));
-    h[1] = h[2] = 0;
-    return;
-  }
-  const uint32_t b0 = nearest_bf16(b);
-  const float r = x - __uint_as_float(b0);
-  const uint32_t b1 = nearest_bf16(__float_as_uint(r));
-  const float s = r - __uint_as_float(b1);
-  h[0] = uint16_t(b0 >> 16);
-  h[1] = uint16_t(b1 >> 16);
-  h[2] = uint16_t(nearest_bf16(__float_as_uint(s)) >> 16);
-}
-
-// split3 of eight values: the parts of value i in 16 bits of h[part], as they are stored.  Values
-// below 2^127 take the conversion instruction, two at a time (5.5 instructions a value against
-// split3's 20).
-__device__ __forceinline__ uint32_t pair_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ void split8(const float (&x)[8], uint32_t (&h)[3][4]) {
-  float top = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));      // (a NaN is not seen)
-  const float sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-  if (top < 0x1p127f && sum == sum) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float a = x[2 * i], b = x[2 * i + 1];
-#pragma unroll
-      for (int pl = 0; pl < 3; ++pl) {
-        h[pl][i] = pair_bf16(a, b);
-        a -= __uint_as_float(h[pl][i] << 16);
-        b -= __uint_as_float(h[pl][i] & 0xFFFF0000u);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint16_t a[3], b[3];
-      split3(x[2 * i], a);
-      split3(x[2 * i + 1], b);
-#pragma unroll
-      for (int pl = 0; pl < 3; ++pl) h[pl][i] = a[pl] | (uint32_t(b[pl]) << 16);
-    }
   }
 }
 
@@ -828,7 +757,7 @@ __device__ __forceinline__ bool split_tile(const Params &p, const Tile &t, int s
 
 // BP: parts of b in the adapters' part on pairs, 2 where it is FP16 (half_parts).
 template <int CG, int MODE, int PLANES, int BP = 1>
-__global__ void __launch_bounds__(ModeShape<CG, MODE, PLANES>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<CG, PLANES>::kThreads, 1)
 grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                const __grid_constant__ CUtensorMap map_q,    // Q tiles
                const __grid_constant__ CUtensorMap map_qr,   // single rows of x; pairs: tiles of
@@ -837,7 +766,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                const __grid_constant__ CUtensorMap map_u,    // u tiles; gradient: 16 rows of x
                const __grid_constant__ CUtensorMap map_pr,   // gradient: single rows of dy
                const Params p) {
-  using S = ModeShape<CG, MODE, PLANES>;
+  using S = Shape<CG, PLANES>;
   // The adapters' part: pairs extend the sum (EXT); single blocks, whose rows are few, add it to
   // the results on the CUDA cores while the weights stream (FEW).
   constexpr bool EXT = MODE == kLora && CG == 2, FEW = MODE == kLora && CG == 1;
@@ -907,11 +836,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     }
   }
   if (!S::kDirect && warp == 0 && elect_one()) {
-    if (MODE != kLinear || p.K > 0) {      // (no maps without a sum)
-      prefetch_map(&map_p);
-      prefetch_map(&map_q);
-      prefetch_map(&map_qr);
-    }
+    prefetch_map(&map_p);
+    prefetch_map(&map_q);
+    prefetch_map(&map_qr);
   }
   // The adapters' product follows the one that makes u, and needs nothing else of it: its wait
   // comes before the first slice of u, so that the shared projection starts beside it.
@@ -920,7 +847,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
     grid_start_next();
   }
   for (int g = threadIdx.x; g <= p.groups; g += S::kThreads)
-    offs[g] = p.offsets ? max(0, min(p.offsets[g], p.rows)) : g * p.rows;
+    offs[g] = max(0, min(p.offsets[g], p.rows));
   __syncthreads();
   if (warp == 0) {
     // Group bounds are the running maximum of the offsets: offsets that step back make an
@@ -1487,21 +1414,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
       const uint32_t lanes = tmem + (uint32_t(32 * quarter) << 16);
       const uint32_t tempty = CG == 2 ? map_rank(bar_tempty, 0) : bar_tempty;
       const int nw = tile.n0 + half_rank * 128 + 32 * quarter;
-      const uint32_t stage = out_stage + uint32_t(warp - S::kEpi0) * (S::kOutStage / kEpiWarps);
+      const uint32_t stage = out_stage + uint32_t(warp - S::kEpi0) * 1024;
       const float scale = MODE == kForward && p.scale ? p.scale[tile.g] : 1.0f;
       constexpr int kBlocks = S::kBN / 32;     // 16-column blocks of a warp, every other one
-      // Linear: the bias of the n that this lane finishes, and whether anything is to be done to a
-      // sum but to store it.
-      float bias[8] = {};
-      const bool linear = MODE == kLinear && p.epilogue;
-      if constexpr (MODE == kLinear) {
-        if (p.bias && PLANES == 1 && p.vec_out) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) bias[k] = linear_bias<PLANES>(p, nw + (lane & 3) * 8 + k);
-        } else if (p.bias) {
-          bias[0] = linear_bias<PLANES>(p, nw + lane);
-        }
-      }
       // The columns that this block adds up and stores: all of them, or its share.
       const int own0 = CG == 1 ? tile.qn * int(rank) / p.ksplit : 0;
       const int own1 = CG == 1 ? tile.qn * int(rank + 1) / p.ksplit : tile.qn;
@@ -1542,8 +1457,6 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
             if (p.ksplit > 1) *at = w[j];
           }
           if (p.ksplit == 1) store_columns<MODE, PLANES>(p, tile, c0, nw, w, scale, stage, owner);
-        } else if (linear) {
-          linear_columns<PLANES>(p, tile.q0 + c0, tile.qn - c0, nw, v, bias, stage);
         } else {
           store_columns<MODE, PLANES>(p, tile, c0, nw, v, scale, stage, owner);
         }
@@ -1559,7 +1472,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           ++q;
           if (!__all_sync(~0u, ready)) timed_out = true;
           tc_fence_after();
-          if (!timed_out && p.vec_out && !FEW && p.ksplit == 1 && !linear) {
+          if (!timed_out && p.vec_out && !FEW && p.ksplit == 1) {
             const uint32_t at = lanes + buf * S::kBN;
             for (int c0 = 16 * half; c0 < tile.bn; c0 += 32) {
               uint32_t f[2][8];
@@ -1587,7 +1500,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
           // and sum, on the way that the operands take (8 groups of 8320 rows, 2048 x 2048: 330 us
           // -> 350 us; K = 8320, 4096 rows of 8 groups, N = 2048: 89 us -> 101 us; up to 8192
           // unchanged).
-          const bool matrices = p.vec_out && !FEW && p.ksplit == 1 && !linear;
+          const bool matrices = p.vec_out && !FEW && p.ksplit == 1;
           const int each = long_sum(nb);
           float acc[kBlocks][16];
           for (int left = nb; left > 0; left -= each, ++q) {
@@ -1743,13 +1656,6 @@ grouped_kernel(const __grid_constant__ CUtensorMap map_p,    // P tiles
                   store_u4(static_cast<uint16_t *>(p.out) + o, n, g, p.idesc & (1u << 7));
                 continue;
               }
-            }
-            if constexpr (MODE == kLinear) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (n + j < p.N)
-                  linear_one<PLANES>(p, tile.q0 + col, n + j, f[j] + linear_bias<PLANES>(p, n + j));
-              continue;
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -2052,12 +1958,6 @@ size_t add_sizes(std::initializer_list<size_t> sizes) {
   return t;
 }
 
-// An operand as the copy engine reads it: `planes` stacks of 16-bit matrices after each other.
-struct Planes {
-  const void *data;
-  int64_t count, rows, cols, ld, stride;   // count: matrices of all planes
-};
-
 // The operand in place, or a job that makes its planes in *ws (which advances past them);
 // matrices of groups without rows (by `offsets`, a matrix per group) are not made.  With
 // `gathered` the planes hold the rows that `index` names.
@@ -2166,7 +2066,7 @@ struct Maps {
 template <int CG, int MODE, int PLANES, int BP = 1>
 cudaError_t launch_shape(const Maps &m, Params &prm, int64_t tiles, const DeviceInfo &dev,
                          cudaStream_t stream) {
-  using S = ModeShape<CG, MODE, PLANES>;
+  using S = Shape<CG, PLANES>;
   static std::atomic<uint64_t> configured{0};
   auto kernel = grouped_kernel<CG, MODE, PLANES, BP>;
   const uint64_t bit = uint64_t(1) << (dev.id & 63);
@@ -2203,7 +2103,6 @@ cudaError_t launch_mode(int mode, const Maps &m, Params &prm, int64_t tiles,
                         const DeviceInfo &dev, cudaStream_t stream) {
   if (mode == kForward) return launch_shape<CG, kForward, PLANES>(m, prm, tiles, dev, stream);
   if (mode == kWgrad) return launch_shape<CG, kWgrad, PLANES>(m, prm, tiles, dev, stream);
-  if (mode == kLinear) return launch_shape<CG, kLinear, PLANES>(m, prm, tiles, dev, stream);
   if constexpr (CG == 2 && PLANES == 1)
     if (prm.out_type == kOutF16) return launch_shape<2, kLora, 1, 2>(m, prm, tiles, dev, stream);
   return launch_shape<CG, kLora, PLANES>(m, prm, tiles, dev, stream);
@@ -2215,9 +2114,7 @@ cudaError_t launch_any(int cg, int planes, int mode, const Maps &m, Params &prm,
   prm.drop_block = g_drop_block.load(std::memory_order_relaxed);
   prm.vec_out = (prm.out_type == kOutBF16 || prm.out_type == kOutF16) &&
                 (reinterpret_cast<uintptr_t>(prm.out) & 15u) == 0 && prm.ld_out % 8 == 0 &&
-                prm.stride_out % 8 == 0 &&
-                (reinterpret_cast<uintptr_t>(prm.residual) & 15u) == 0 && prm.ld_residual % 8 == 0 &&
-                (reinterpret_cast<uintptr_t>(prm.pre) & 15u) == 0 && prm.ld_pre % 8 == 0;
+                prm.stride_out % 8 == 0;
   if (cg == 2)
     return planes == 3 ? launch_mode<2, 3>(mode, m, prm, tiles, dev, stream)
                        : launch_mode<2, 1>(mode, m, prm, tiles, dev, stream);
@@ -2351,7 +2248,7 @@ void set_direct(Params *prm, const Stack &P, const Stack &x) {
 // `index`: the rows of x by number, or NULL.
 cudaError_t run_forward(int dtype, const Planes &x, const Stack &xs, const int32_t *index,
                         const Planes &w, const Stack &ws, bool trans_w, Params prm,
-                        const DeviceInfo &dev, cudaStream_t stream, int mode = kForward) {
+                        const DeviceInfo &dev, cudaStream_t stream) {
   const int planes = dtype == TMM_F32 ? 3 : 1;
   const int cg = forward_shape(prm.rows, prm.groups, prm.N, prm.K, dtype);
   prm.panels = int((prm.N + 128 * cg - 1) / (128 * cg));
@@ -2368,9 +2265,7 @@ cudaError_t run_forward(int dtype, const Planes &x, const Stack &xs, const int32
   prm.p_mn = trans_w ? 0 : 1;
   prm.p_shared = prm.groups > 1 && ws.count == 1;
   Maps m = {};
-  if (prm.K == 0) {
-    // Linear: nothing is read.
-  } else if (direct(cg, dtype)) {
+  if (direct(cg, dtype)) {
     prm.q_rows = int(xs.rows);
     set_direct(&prm, ws, xs);
   } else {
@@ -2382,7 +2277,7 @@ cudaError_t run_forward(int dtype, const Planes &x, const Stack &xs, const int32
     m.e = m.p;
     m.u = m.q;
   }
-  return launch_any(cg, planes, mode, m, prm, tiles, dev, stream);
+  return launch_any(cg, planes, kForward, m, prm, tiles, dev, stream);
 }
 
 }  // namespace
@@ -2402,6 +2297,15 @@ static int64_t grouped_gathered(const GroupedProblem &p, int cg) {
 
 static int shape_of(const GroupedProblem &p) {
   return forward_shape(p.rows, p.groups, p.N, p.K, p.dtype);
+}
+
+size_t planes_bytes(const Stack &s, int dtype) { return plane_bytes(s, dtype); }
+
+cudaError_t make_operand_planes(const Stack *const *operands, Planes *planes, int count, int dtype,
+                                char **ws, const DeviceInfo &dev, cudaStream_t stream) {
+  PlaneJobs jobs = {};
+  for (int i = 0; i < count; ++i) planes[i] = plan_planes(*operands[i], dtype, nullptr, ws, &jobs);
+  return make_planes(jobs, dtype, dev, stream);
 }
 
 size_t grouped_workspace_bytes(const GroupedProblem &p) {
@@ -2439,56 +2343,6 @@ cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void 
                      prm, dev, stream);
 }
 
-// A linear layer: in 16 bits a product of its own (gemm_linear.cu) on operands in place or restaged;
-// in FP32, and for sums longer than that kernel's, the forward product of one group with the epilogue.
-static DenseOperand dense_operand(const Planes &o, bool mn) {
-  return {o.data, o.rows, o.cols, o.ld, mn ? 1 : 0};
-}
-
-size_t linear_workspace_bytes(const LinearProblem &p) {
-  const int cg = forward_shape(p.rows, 1, p.N, p.K, p.dtype);
-  if (direct(cg, p.dtype) || p.K == 0) return 0;
-  return add_sizes({plane_bytes(p.x, p.dtype), plane_bytes(p.w, p.dtype)});
-}
-
-cudaError_t launch_linear(const LinearProblem &p, const DeviceInfo &dev, void *workspace,
-                          cudaStream_t stream) {
-  char *ws = static_cast<char *>(workspace);
-  Planes x = {}, w = {};
-  if (!direct(forward_shape(p.rows, 1, p.N, p.K, p.dtype), p.dtype) && p.K > 0) {
-    PlaneJobs jobs = {};
-    x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs);
-    w = plan_planes(p.w, p.dtype, nullptr, &ws, &jobs);
-    const cudaError_t e = make_planes(jobs, p.dtype, dev, stream);
-    if (e != cudaSuccess) return e;
-  }
-  if (p.dtype != TMM_F32 && p.K > 0) {
-    const DenseProblem d = {p.dtype, p.rows, p.N, p.K, dense_operand(w, !p.trans_w),
-                            dense_operand(x, false), p.y, p.ldy, p.bias, p.bias_f32, p.act,
-                            p.residual, p.ld_residual, p.pre, p.ld_pre};
-    const cudaError_t e = launch_dense(d, dev, stream);
-    if (e != cudaErrorNotSupported) return e;
-  }
-  Params prm = {};
-  prm.rows = int(p.rows);
-  prm.groups = 1;
-  prm.K = int(p.K);
-  prm.N = int(p.N);
-  prm.idesc = type_desc(p.dtype);
-  prm.out = p.y;
-  prm.ld_out = p.ldy;
-  prm.out_type = out_type(p.dtype);
-  prm.bias = p.bias;
-  prm.bias_f32 = p.bias_f32;
-  prm.act = p.act;
-  prm.residual = p.residual;
-  prm.ld_residual = p.residual ? p.ld_residual : 0;
-  prm.pre = p.pre;
-  prm.ld_pre = p.pre ? p.ld_pre : 0;
-  prm.epilogue = p.bias || p.residual || p.pre || p.act != TMM_ACT_NONE;
-  return run_forward(p.dtype, x, p.x, nullptr, w, p.w, p.trans_w != 0, prm, dev, stream, kLinear);
-}
-
 // Every 64 columns of x read the group's rows again.  (Single blocks, 4096 x 128, bf16, by number and
 // gathered: 128 rows of a group 6.6 us and 7.7 us, 512 of each of 8 44 us and 30 us.)
 static int64_t wgrad_gathered(const WgradProblem &p) {
@@ -2502,24 +2356,45 @@ size_t wgrad_workspace_bytes(const WgradProblem &p) {
        plane_bytes(p.dy, p.dtype)});
 }
 
-// The gradient's product on planes (or FP32 stacks directly); `cg` as the caller chose.
-static cudaError_t run_wgrad(int dtype, int cg, const Planes &x, const Stack &xs,
-                             const int32_t *index, const Planes &dy, const Stack &dys, Params prm,
-                             const DeviceInfo &dev, cudaStream_t stream) {
-  const int planes = dtype == TMM_F32 ? 3 : 1;
+cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *workspace,
+                         cudaStream_t stream) {
+  char *ws = static_cast<char *>(workspace);
+  const int cg = wgrad_shape(p.N);
+  const int64_t gathered = wgrad_gathered(p);
+  const int32_t *index = gathered ? nullptr : p.row_index;
+  Planes x = {}, dy = {};
+  cudaError_t e;
+  if (!direct(cg, p.dtype)) {
+    PlaneJobs jobs = {};
+    x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs, gathered, p.row_index);
+    dy = plan_planes(p.dy, p.dtype, nullptr, &ws, &jobs);
+    if ((e = make_planes(jobs, p.dtype, dev, stream)) != cudaSuccess) return e;
+  }
+  const int planes = p.dtype == TMM_F32 ? 3 : 1;
+  Params prm = {};
+  prm.rows = int(p.rows);
+  prm.groups = int(p.groups);
+  prm.offsets = p.offsets;
   prm.row_index = index;
+  prm.q_rows = int(gathered ? p.rows : p.x.rows);
+  prm.q_cols = int(p.K);
+  prm.N = int(p.N);
+  prm.idesc = type_desc(p.dtype);
+  prm.out = p.dw;
+  prm.ld_out = p.lddw;
+  prm.stride_out = p.groups > 1 ? p.stride_dw : 0;
+  prm.out_type = out_type(p.dtype);
   prm.n_out = prm.N;
   prm.ksplit = 1;
   const int bn = columns_of(cg, planes);
   prm.tile_n = bn;
-  prm.panels = int((prm.N + 128 * cg - 1) / (128 * cg));
-  const int64_t tiles = int64_t(prm.groups) * prm.panels * ((prm.q_cols + bn - 1) / bn);
+  prm.panels = int((p.N + 128 * cg - 1) / (128 * cg));
+  const int64_t tiles = p.groups * prm.panels * ((p.K + bn - 1) / bn);
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
-  if (cg == 1) prm.ksplit = split_of(tiles, (prm.rows / prm.groups + kBK - 1) / kBK, planes, dev);
+  if (cg == 1) prm.ksplit = split_of(tiles, (p.rows / p.groups + kBK - 1) / kBK, planes, dev);
   Maps m = {};
-  cudaError_t e;
-  if (direct(cg, dtype)) {
-    set_direct(&prm, dys, xs);
+  if (direct(cg, p.dtype)) {
+    set_direct(&prm, p.dy, p.x);
   } else {
     if ((e = row_map(&m.p, dy, kBK)) != cudaSuccess ||
         (e = row_map(&m.e, dy, 16)) != cudaSuccess || (e = row_map(&m.pr, dy, 1)) != cudaSuccess ||
@@ -2531,156 +2406,6 @@ static cudaError_t run_wgrad(int dtype, int cg, const Planes &x, const Stack &xs
       return e;
   }
   return launch_any(cg, planes, kWgrad, m, prm, tiles, dev, stream);
-}
-
-cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *workspace,
-                         cudaStream_t stream) {
-  char *ws = static_cast<char *>(workspace);
-  const int cg = wgrad_shape(p.N);
-  const int64_t gathered = wgrad_gathered(p);
-  Planes x = {}, dy = {};
-  if (!direct(cg, p.dtype)) {
-    PlaneJobs jobs = {};
-    x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs, gathered, p.row_index);
-    dy = plan_planes(p.dy, p.dtype, nullptr, &ws, &jobs);
-    const cudaError_t e = make_planes(jobs, p.dtype, dev, stream);
-    if (e != cudaSuccess) return e;
-  }
-  Params prm = {};
-  prm.rows = int(p.rows);
-  prm.groups = int(p.groups);
-  prm.offsets = p.offsets;
-  prm.q_rows = int(gathered ? p.rows : p.x.rows);
-  prm.q_cols = int(p.K);
-  prm.N = int(p.N);
-  prm.idesc = type_desc(p.dtype);
-  prm.out = p.dw;
-  prm.ld_out = p.lddw;
-  prm.stride_out = p.groups > 1 ? p.stride_dw : 0;
-  prm.out_type = out_type(p.dtype);
-  return run_wgrad(p.dtype, cg, x, p.x, gathered ? nullptr : p.row_index, dy, p.dy, prm, dev,
-                   stream);
-}
-
-// ---- a linear layer's gradients ------------------------------------------------------------
-
-namespace {
-
-// What the gradients' products run on: dz = dy act'(z) (dy itself without an activation), and the
-// operands of the two products in planes where they need them; the workspace holds them in order.
-struct LinearGradPlan {
-  Stack dz;
-  bool make_dz;
-  int cg_x, cg_w;                  // shapes of the products for dx and dw
-  bool planes_x, planes_w;         // whether they read planes (or operands in place)
-  Stack wx, wy;                    // dw's operands: its rows' and its columns' dimension
-  size_t dz_bytes, partial_bytes, bytes;
-};
-
-LinearGradPlan plan_linear_grad(const LinearGradProblem &p) {
-  LinearGradPlan g = {};
-  const int size = p.dtype == TMM_F32 ? 4 : 2;
-  g.make_dz = p.act != TMM_ACT_NONE && (p.dx || p.dw);
-  g.dz = p.dy;
-  if (g.make_dz) {
-    g.dz.ld = (p.N * size + 15) / 16 * 16 / size;
-    g.dz.stride = 0;
-    const __int128 n = __int128(p.rows) * g.dz.ld * size;
-    g.dz_bytes = n > __int128(INT64_MAX / 4) ? SIZE_MAX : round256(size_t(n));
-    g.dz.data = nullptr;           // the workspace's start, on 256 bytes
-  }
-  g.partial_bytes = p.dbias ? round256(linear_bias_bytes(p.rows, p.N, p.dtype)) : 0;
-  g.wx = p.trans_dw ? g.dz : p.x;
-  g.wy = p.trans_dw ? p.x : g.dz;
-  g.cg_x = forward_shape(p.rows, 1, p.K, p.N, p.dtype);
-  g.cg_w = wgrad_shape(g.wy.cols);
-  g.planes_x = p.dx && !direct(g.cg_x, p.dtype);
-  g.planes_w = p.dw && !direct(g.cg_w, p.dtype);
-  g.bytes = add_sizes({g.dz_bytes, g.partial_bytes,
-                       g.planes_x || g.planes_w ? plane_bytes(g.dz, p.dtype) : 0,
-                       g.planes_x ? plane_bytes(p.w, p.dtype) : 0,
-                       g.planes_w ? plane_bytes(p.x, p.dtype) : 0});
-  return g;
-}
-
-}  // namespace
-
-size_t linear_grad_workspace_bytes(const LinearGradProblem &p) {
-  return plan_linear_grad(p).bytes;
-}
-
-cudaError_t launch_linear_grad(const LinearGradProblem &p, const DeviceInfo &dev, void *workspace,
-                               cudaStream_t stream) {
-  LinearGradPlan g = plan_linear_grad(p);
-  char *ws = static_cast<char *>(workspace);
-  if (g.make_dz) {
-    g.dz.data = ws;
-    (p.trans_dw ? g.wx : g.wy).data = ws;
-    ws += g.dz_bytes;
-  }
-  cudaError_t e;
-  if (g.make_dz || p.dbias) {
-    e = launch_linear_slopes(p, g.make_dz ? const_cast<void *>(g.dz.data) : nullptr, g.dz.ld,
-                             reinterpret_cast<float *>(ws), dev, stream);
-    if (e != cudaSuccess) return e;
-  }
-  ws += g.partial_bytes;
-  PlaneJobs jobs = {};
-  Planes dz = {}, w = {}, x = {};
-  if (g.planes_x || g.planes_w) dz = plan_planes(g.dz, p.dtype, nullptr, &ws, &jobs);
-  if (g.planes_x) w = plan_planes(p.w, p.dtype, nullptr, &ws, &jobs);
-  if (g.planes_w) x = plan_planes(p.x, p.dtype, nullptr, &ws, &jobs);
-  if ((e = make_planes(jobs, p.dtype, dev, stream)) != cudaSuccess) return e;
-  Params prm = {};
-  prm.rows = int(p.rows);
-  prm.groups = 1;
-  prm.idesc = type_desc(p.dtype);
-  prm.out_type = out_type(p.dtype);
-  // In 16 bits every operand is in place or has been restaged.
-  const auto dense = [&](int64_t M, int64_t N, int64_t K, const DenseOperand &a,
-                         const DenseOperand &b, void *out, int64_t ld) {
-    if (p.dtype == TMM_F32) return cudaErrorNotSupported;
-    DenseProblem d = {};
-    d.dtype = p.dtype;
-    d.M = M;
-    d.N = N;
-    d.K = K;
-    d.p = a;
-    d.q = b;
-    d.out = out;
-    d.ld_out = ld;
-    return launch_dense(d, dev, stream);
-  };
-  if (p.dx) {
-    e = dense(p.rows, p.K, p.N, dense_operand(w, p.trans_w), dense_operand(dz, false), p.dx, p.lddx);
-    if (e != cudaErrorNotSupported && e != cudaSuccess) return e;
-  }
-  if (p.dx && e == cudaErrorNotSupported) {
-    Params q = prm;
-    q.K = int(p.N);
-    q.N = int(p.K);
-    q.out = p.dx;
-    q.ld_out = p.lddx;
-    e = run_forward(p.dtype, dz, g.dz, nullptr, w, p.w, !p.trans_w, q, dev, stream, kLinear);
-    if (e != cudaSuccess) return e;
-  }
-  if (p.dw) {
-    e = dense(g.wx.cols, g.wy.cols, p.rows, dense_operand(p.trans_dw ? x : dz, true),
-              dense_operand(p.trans_dw ? dz : x, true), p.dw, p.lddw);
-    if (e != cudaErrorNotSupported && e != cudaSuccess) return e;
-  }
-  if (p.dw && e == cudaErrorNotSupported) {
-    Params q = prm;
-    q.q_rows = int(p.rows);
-    q.q_cols = int(g.wx.cols);
-    q.N = int(g.wy.cols);
-    q.out = p.dw;
-    q.ld_out = p.lddw;
-    e = run_wgrad(p.dtype, g.cg_w, p.trans_dw ? dz : x, g.wx, nullptr, p.trans_dw ? x : dz, g.wy, q,
-                  dev, stream);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
 }
 
 template <typename T, bool TRANS_A>

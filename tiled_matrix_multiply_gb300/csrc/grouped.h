@@ -85,29 +85,16 @@ struct LinearGradProblem {
   float *dbias;
 };
 
-// One dense product of 16-bit operands that the copy engine can read: out[q, n] = sum_k P[n, k]
-// Q[q, k] for n < N, q < M, with a linear layer's epilogue.
-struct DenseOperand {
-  const void *data;             // rows x cols as stored, 16-byte rows
-  int64_t rows, cols, ld;
-  int mn;                       // stored k x own dimension (else own dimension x k)
+// An operand as the copy engine reads it: `planes` stacks of 16-bit matrices after each other.
+struct Planes {
+  const void *data;
+  int64_t count, rows, cols, ld, stride;   // count: matrices of all planes
 };
-struct DenseProblem {
-  int dtype;                    // TMM_BF16, TMM_F16
-  int64_t M, N, K;
-  DenseOperand p, q;
-  void *out;
-  int64_t ld_out;
-  const void *bias;             // as in LinearProblem
-  int bias_f32, act;
-  const void *residual;
-  int64_t ld_residual;
-  void *pre;
-  int64_t ld_pre;
-};
-// cudaErrorNotSupported: a product that its shapes do not fit (sums of more than 8192 values that
-// cannot be shared); nothing has been launched.
-cudaError_t launch_dense(const DenseProblem &p, const DeviceInfo &dev, cudaStream_t stream);
+// Planes of up to four plain operands, in place where the copy engine can read them, else in *ws
+// (which advances past planes_bytes of each), made by one launch.
+size_t planes_bytes(const Stack &s, int dtype);
+cudaError_t make_operand_planes(const Stack *const *operands, Planes *planes, int count, int dtype,
+                                char **ws, const DeviceInfo &dev, cudaStream_t stream);
 cudaError_t linear_device_status(unsigned int *status, bool clear);
 void linear_set_test_hooks(int drop_block, int64_t wait_limit_ns);
 
@@ -118,15 +105,16 @@ size_t lora_workspace_bytes(const LoraProblem &p);
 size_t linear_workspace_bytes(const LinearProblem &p);
 size_t linear_grad_workspace_bytes(const LinearGradProblem &p);
 
-// Sizes reaching a launcher are > 0 (K of launch_linear may be 0).
+// Sizes reaching a launcher are > 0 (but K of launch_linear may be 0).
 cudaError_t launch_linear(const LinearProblem &p, const DeviceInfo &dev, void *workspace,
                           cudaStream_t stream);
 cudaError_t launch_linear_grad(const LinearGradProblem &p, const DeviceInfo &dev, void *workspace,
                                cudaStream_t stream);
-// dz (rows x N, ldz; NULL: not written) and dbias; `partial`: linear_bias_bytes of scratch.
+// dz (rows x N, ldz, of the type, or with `planes` an FP32 value's three bf16 parts; NULL: not written)
+// and dbias; `partial`: linear_bias_bytes of scratch.
 size_t linear_bias_bytes(int64_t rows, int64_t N, int dtype);
-cudaError_t launch_linear_slopes(const LinearGradProblem &p, void *dz, int64_t ldz, float *partial,
-                                 const DeviceInfo &dev, cudaStream_t stream);
+cudaError_t launch_linear_slopes(const LinearGradProblem &p, void *dz, int64_t ldz, bool planes,
+                                 float *partial, const DeviceInfo &dev, cudaStream_t stream);
 cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void *workspace,
                            cudaStream_t stream);
 cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *workspace,

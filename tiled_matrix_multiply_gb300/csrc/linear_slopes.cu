@@ -11,6 +11,7 @@
 #include "activation.cuh"
 #include "grouped.h"
 #include "row_ops.cuh"
+#include "split_bf16.cuh"
 #include "tmm_gemm.h"
 
 namespace tmm {
@@ -25,6 +26,7 @@ struct SlopeParams {
   float *sums;          // runs x N, or NULL
   int64_t rows, N, lddy, ld_pre, ldz, run;
   int act;
+  int planes;           // FP32: dz as its three bf16 parts, planes rows * ldz apart
 };
 
 // Lane l has columns first + l W .. + W (VEC), or first + l, + 32, ...: 16 bytes' worth.
@@ -48,7 +50,7 @@ slopes_kernel(const __grid_constant__ SlopeParams p) {
         if (column(k) < p.N) reinterpret_cast<T *>(&v.w)[k] = from[column(k)];
     }
   };
-  float sum[W] = {};
+  uint64_t sum[W / 2] = {};      // pairs of zeros
   for (int64_t r = r0 + warp; r < r1; r += kWarps * kAhead) {
     Vec<T> dy[kAhead], z[kAhead];
 #pragma unroll
@@ -64,15 +66,43 @@ slopes_kernel(const __grid_constant__ SlopeParams p) {
     for (int u = 0; u < kAhead; ++u) {
       const int64_t row = r + u * kWarps;
       if (row >= r1) break;
-      Vec<T> out;
+      uint64_t d[W / 2];
 #pragma unroll
-      for (int k = 0; k < W; ++k) {
-        float d = dy[u].get(k);
-        if (p.pre) d *= activation_slope<sizeof(T) == 2>(p.act, z[u].get(k));
-        sum[k] += d;
-        out.set(k, d);
+      for (int k = 0; k < W / 2; ++k) d[k] = pair_of(z[u].get(2 * k), z[u].get(2 * k + 1));
+      if (p.pre) slope_pairs<sizeof(T) == 2>(p.act, d);
+#pragma unroll
+      for (int k = 0; k < W / 2; ++k) {
+        const uint64_t g = pair_of(dy[u].get(2 * k), dy[u].get(2 * k + 1));
+        d[k] = p.pre ? mul2(g, d[k]) : g;
+        sum[k] = add2(sum[k], d[k]);
       }
       if (p.dz == nullptr) continue;
+      if constexpr (sizeof(T) == 4)
+        if (p.planes) {
+          uint16_t *const to = static_cast<uint16_t *>(p.dz) + row * p.ldz;
+          uint32_t h[W / 2][3];
+#pragma unroll
+          for (int k = 0; k < W / 2; ++k) split2(of_pair(d[k]).x, of_pair(d[k]).y, h[k]);
+#pragma unroll
+          for (int pl = 0; pl < 3; ++pl) {
+            uint16_t *const plane = to + pl * p.rows * p.ldz;
+            if (VEC) {
+              if (column(0) < p.N)
+                *reinterpret_cast<uint2 *>(plane + column(0)) = make_uint2(h[0][pl], h[1][pl]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < W; ++k)
+                if (column(k) < p.N) plane[column(k)] = uint16_t(h[k >> 1][pl] >> (16 * (k & 1)));
+            }
+          }
+          continue;
+        }
+      Vec<T> out;
+#pragma unroll
+      for (int k = 0; k < W / 2; ++k) {
+        out.set(2 * k, of_pair(d[k]).x);
+        out.set(2 * k + 1, of_pair(d[k]).y);
+      }
       T *const to = static_cast<T *>(p.dz) + row * p.ldz;
       if (VEC) {
         if (column(0) < p.N) *reinterpret_cast<uint4 *>(to + column(0)) = out.w;
@@ -85,7 +115,10 @@ slopes_kernel(const __grid_constant__ SlopeParams p) {
   }
   if (p.sums == nullptr) return;
 #pragma unroll
-  for (int k = 0; k < W; ++k) part[warp][VEC ? lane * W + k : lane + 32 * k] = sum[k];
+  for (int k = 0; k < W; ++k) {
+    const float2 f = of_pair(sum[k >> 1]);
+    part[warp][VEC ? lane * W + k : lane + 32 * k] = k & 1 ? f.y : f.x;
+  }
   __syncthreads();
   for (int c = threadIdx.x; c < 32 * W; c += 32 * kWarps) {
     float s = 0.0f;
@@ -125,8 +158,8 @@ bool aligned(const void *p, int64_t ld, int64_t size) {
 }
 
 template <typename T>
-cudaError_t launch_as(const LinearGradProblem &g, void *dz, int64_t ldz, float *partial,
-                      cudaStream_t stream) {
+cudaError_t launch_as(const LinearGradProblem &g, void *dz, int64_t ldz, bool planes,
+                      float *partial, cudaStream_t stream) {
   const int64_t size = sizeof(T), runs = runs_of(g.rows, g.N, g.dtype);
   SlopeParams p = {};
   p.dy = g.dy.data;
@@ -135,6 +168,7 @@ cudaError_t launch_as(const LinearGradProblem &g, void *dz, int64_t ldz, float *
   p.ld_pre = g.ld_pre;
   p.dz = dz;
   p.ldz = ldz;
+  p.planes = planes;
   p.rows = g.rows;
   p.N = g.N;
   p.act = g.act;
@@ -142,7 +176,7 @@ cudaError_t launch_as(const LinearGradProblem &g, void *dz, int64_t ldz, float *
   p.sums = g.dbias == nullptr ? nullptr : runs > 1 ? partial : g.dbias;
   const bool vec = g.N * size % 16 == 0 && aligned(p.dy, p.lddy, size) &&
                    (p.pre == nullptr || aligned(p.pre, p.ld_pre, size)) &&
-                   (dz == nullptr || aligned(dz, ldz, size));
+                   (dz == nullptr || aligned(dz, ldz, planes ? 2 : size));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -169,11 +203,11 @@ size_t linear_bias_bytes(int64_t rows, int64_t N, int dtype) {
   return runs > 1 ? size_t(runs) * size_t(N) * sizeof(float) : 0;
 }
 
-cudaError_t launch_linear_slopes(const LinearGradProblem &p, void *dz, int64_t ldz, float *partial,
-                                 const DeviceInfo &, cudaStream_t stream) {
-  if (p.dtype == TMM_BF16) return launch_as<__nv_bfloat16>(p, dz, ldz, partial, stream);
-  if (p.dtype == TMM_F16) return launch_as<__half>(p, dz, ldz, partial, stream);
-  return launch_as<float>(p, dz, ldz, partial, stream);
+cudaError_t launch_linear_slopes(const LinearGradProblem &p, void *dz, int64_t ldz, bool planes,
+                                 float *partial, const DeviceInfo &, cudaStream_t stream) {
+  if (p.dtype == TMM_BF16) return launch_as<__nv_bfloat16>(p, dz, ldz, planes, partial, stream);
+  if (p.dtype == TMM_F16) return launch_as<__half>(p, dz, ldz, planes, partial, stream);
+  return launch_as<float>(p, dz, ldz, planes, partial, stream);
 }
 
 }  // namespace tmm
