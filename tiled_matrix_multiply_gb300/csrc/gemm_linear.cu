@@ -792,17 +792,6 @@ struct DenseShape {
   int bn = 0, split = 1;
 };
 
-// The shape of the least time, by an estimate in ns fitted to measured products (M, N, K from 1 x 1024
-// x 1024 to 8192 x 4096 x 4096, all widths and splits; the shapes it takes are within 5 % of the best
-// measured one, as a rule):
-//   a slice of 64 takes a single block 120 + 0.9 a column (256 columns 350) and a pair 140 + 0.55 a
-//   column (256 columns 281, the products' own rate), either 180 at least;
-//   a tile takes 700 + 6 a column, however few its slices: its results have to leave;
-//   memory gives a block 70 bytes at most, all of them 6500, partly beside the above;
-//   a launch has 3400 before and after its slices, and sharing a sum costs 1000 + 18 a column (512 x
-//   4096 x 4096: pairs of 128 columns 17.2 us, of 256 columns shared by two 20.0 us; 128 x 4096 x
-//   4096: 64 columns shared by two 12.3 us, not shared 15.6 us).
-// `clusters` gives how many clusters of a size fit.
 // One product: out[q, n] = sum_k P[n, k] Q[q, k] for n < N, q < M.
 struct DenseOperand {
   Planes planes;
@@ -822,6 +811,18 @@ struct DenseProblem {
   int64_t ld_pre;
 };
 
+// The shape of the least time, by an estimate in ns fitted to measured products (M, N, K from 1 x 1024
+// x 1024 to 8192 x 4096 x 4096, all widths and splits; the shapes it takes are within 5 % of the best
+// measured one, as a rule):
+//   a slice of 64 takes a single block 120 + 0.9 a column (256 columns 350) and a pair 140 + 0.55 a
+//   column (256 columns 281, the products' own rate), either 180 at least;
+//   in FP32 490 + 5.3 and 430 + 3.7 a column (4096^3: pairs of 128 columns 470 us, blocks 558 us);
+//   a tile takes 700 + 6 a column, however few its slices: its results have to leave;
+//   memory gives a block 70 bytes at most, all of them 6500, partly beside the above;
+//   a launch has 3400 before and after its slices, and sharing a sum costs 1000 + 18 a column (512 x
+//   4096 x 4096: pairs of 128 columns 17.2 us, of 256 columns shared by two 20.0 us; 128 x 4096 x
+//   4096: 64 columns shared by two 12.3 us, not shared 15.6 us).
+// `clusters` gives how many clusters of a size fit.
 template <typename Clusters>
 DenseShape dense_shape(const DenseProblem &p, Clusters clusters) {
   const int planes = p.dtype == TMM_F32 ? 3 : 1;
@@ -837,7 +838,7 @@ DenseShape dense_shape(const DenseProblem &p, Clusters clusters) {
       const double wide = double(bn);
       double slice = cg == 2 ? std::max(180.0, 140.0 + 0.55 * wide)
                              : std::max(180.0, 120.0 + 0.9 * wide);
-      if (planes == 3) slice = std::max(3 * slice, 6.2 * wide);
+      if (planes == 3) slice = cg == 2 ? 430 + 3.7 * wide : 490 + 5.3 * wide;
       for (int split = 1; cg * split <= 8; split *= 2) {
         const int64_t each = (slices + split - 1) / split, slots = clusters(cg * split);
         if (split > 1 && (slices < 2 * split || tiles > slots)) break;
