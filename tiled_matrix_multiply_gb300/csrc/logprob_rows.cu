@@ -13,14 +13,15 @@
 // a cluster of up to eight does, and its first block adds up what the others have in their shared
 // memory.  Sums are added in a fixed order.
 //
-// The most probable: every warp keeps a sorted list of 32 keys, a lane each (a key: the value's
-// bits in the order of unsigned numbers, then the number's complement, so that the larger key is
-// the larger value or the lower number).  Its n-th is a threshold that a vector's maximum, which is
-// needed anyway, is compared with, and so is, for all of the block's warps, what the lanes' running
-// maxima imply: of each of w warps ceil(n / w) lanes have reached the least of the warps' ceil(n / w)-th
-// largest.  Few values of a row are then ever inserted (131072 columns, 20 listed: about 20 a warp;
-// with thresholds of the warps' own lists alone, 32 rows took 21 us in place of TOP_US).  Lists are
-// merged pair by pair (half-cleaner and five exchange steps).
+// The most probable: the pass keeps the largest value of every thread, and of each of up to 16 pieces of
+// what it reads.  Of w warps, ceil(n / w) threads each reach the least of the warps' ceil(n / w)-th
+// largest; not many more values do than are listed, and only the pieces that do are read again.  What
+// reaches that bound there (as keys: the value's bits in the order of unsigned numbers, then the number's
+// complement, so that the larger key is the larger value or the lower number) is put in order by counting
+// for each how many are larger.  So the pass is the one without alternatives, and the selection comes
+// after it.  Rows of which too many values reach the bound (thousands of equal ones) are read again
+// whole, by lists that are kept sorted.  (With such lists in the pass itself, under thresholds of various
+// kinds, 4096 rows of 131072 with 20 listed took 320 to 520 us, 248 now.)
 //
 // Gradient: dl_v = scale (g ([v = t] - p_v) - h p_v (log p_v + entropy) + sum_j e_j ([v = id_j] - p_v))
 // for the gradients g, h and e_j of the row's log probability, entropy and alternatives: one read and
@@ -37,6 +38,8 @@ namespace {
 
 constexpr int kMaxThreads = 256, kMaxCluster = 8;
 constexpr int kAhead = 4;          // vectors of a thread in flight
+constexpr int kPieces = 16;        // of what a thread reads, see the most probable
+constexpr int kFound = 1024;       // keys that may be listed, of a block's rows
 constexpr unsigned kAll = ~0u;
 constexpr uint64_t kNoKey = 0;
 
@@ -114,57 +117,74 @@ __device__ __forceinline__ void add_term(float x, float base, float c, float &s,
   w = fmaf(e, fmaxf(t, -1000.0f), w);
 }
 
-// A warp's n best keys so far, sorted, a lane each.
+// A warp's best keys, sorted, a lane each.
 struct Best {
-  uint64_t key;        // of this lane
-  uint64_t low;        // keys up to it need not be looked at
-  float low_value;
-  int n;
-  __device__ __forceinline__ void raise_low(uint64_t to) {
-    if (to > low) {
-      low = to;
-      low_value = value_of(uint32_t(low >> 32));
-    }
-  }
-  // One lane's value, every lane's in turn.
-  __device__ __forceinline__ void offer(float v, uint32_t at) {
-    const int lane = threadIdx.x & 31;
-    const uint64_t mine = v >= low_value ? key_of(v, at) : kNoKey;      // (NaN: no key)
-    unsigned want = __ballot_sync(kAll, mine > low);
-    if (want == 0) return;
-    do {
-      const int from = __ffs(int(want)) - 1;
-      want &= want - 1;
-      const uint64_t k = __shfl_sync(kAll, mine, from);
-      if (k <= low) continue;
-      const int place = __popc(__ballot_sync(kAll, key > k));
-      const uint64_t above = __shfl_up_sync(kAll, key, 1);
-      key = lane < place ? key : lane == place ? k : above;
-      raise_low(__shfl_sync(kAll, key, n - 1));
-    } while (want);
-  }
-  // The each-th largest of the lanes' values (in their order's numbers, 0: none), each the warps' equal
-  // share of n: the least of the warps' is one that at least n values of the row reach.
-  __device__ __forceinline__ uint32_t share(float v, int each) const {
-    uint32_t mine = v > -INFINITY ? order_of(v) : 0, top = 0;
-    for (int j = 0; j < each; ++j) {
-      top = __reduce_max_sync(kAll, mine);
-      if ((threadIdx.x & 31) == unsigned(__ffs(int(__ballot_sync(kAll, mine == top))) - 1)) mine = 0;
-    }
-    return top;
+  uint64_t key;
+  // Exchanges with the lane `d` away: the larger key to the first of the two, or (not `down`) the other.
+  __device__ __forceinline__ static uint64_t exchanged(uint64_t k, int d, bool down) {
+    const uint64_t other = __shfl_xor_sync(kAll, k, d);
+    const bool first = ((threadIdx.x & d) == 0) == down;
+    return first == (k > other) ? k : other;
   }
   // With another sorted list, given as its key 31 - lane.
   __device__ __forceinline__ void merge(uint64_t reversed) {
-    const int lane = threadIdx.x & 31;
     key = larger(key, reversed);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      const uint64_t other = __shfl_xor_sync(kAll, key, d);
-      const bool first = (lane & d) == 0;
-      key = first == (key > other) ? key : other;
-    }
+    for (int d = 16; d > 0; d >>= 1) key = exchanged(key, d, true);
+  }
+  // With a key of every lane (bitonic, upwards: a list's key 31 - lane).
+  __device__ __forceinline__ void add(uint64_t k) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+      for (int d = size / 2; d > 0; d >>= 1) k = exchanged(k, d, (lane & size) != 0 && size < 32);
+    merge(k);
   }
 };
+
+// The values, the largest in lane 0.
+__device__ __forceinline__ float sorted_down(float v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+    for (int d = size / 2; d > 0; d >>= 1) {
+      const float o = __shfl_xor_sync(kAll, v, d);
+      v = ((lane & d) == 0) == ((lane & size) == 0) ? fmaxf(v, o) : fminf(v, o);
+    }
+  return v;
+}
+
+// Puts the 32 largest of `count` keys (none twice, but kNoKey) where their order says; thread `tid` of
+// `threads`.
+__device__ __forceinline__ void place(const uint64_t *keys, int count, uint64_t *list, int tid,
+                                      int threads) {
+  for (int i = tid; i < count; i += threads) {
+    const uint64_t k = keys[i];
+    int before = 0;
+#pragma unroll 4
+    for (int j = 0; j < count; ++j) before += keys[j] > k;
+    if (k != kNoKey && before < 32) list[before] = k;
+  }
+}
+
+// The n best keys of elements [begin, end) of a row, those of `stride` warps' turn: any values.
+template <typename T>
+__device__ __noinline__ uint64_t scan_whole(const T *row, int64_t begin, int64_t end, int stride,
+                                            int n) {
+  const int lane = threadIdx.x & 31;
+  Best best = {kNoKey};
+  uint64_t low = kNoKey;
+  for (int64_t i = begin; i < end; i += 32 * stride) {
+    const float x = i + lane < end ? as_float(row[i + lane]) : -INFINITY;
+    const uint64_t k = x > -INFINITY ? key_of(x, uint32_t(i + lane)) : kNoKey;
+    if (!__any_sync(kAll, k > low)) continue;
+    best.add(k);
+    low = __shfl_sync(kAll, best.key, n - 1);
+  }
+  return best.key;
+}
 
 __device__ __forceinline__ uint32_t shared_address(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -199,19 +219,28 @@ __device__ __forceinline__ int head_of(const T *row, int64_t cols) {
   return int(min(int64_t(n), cols));
 }
 
-template <typename T, bool TOP>
+// ONE: a warp does a row, eight a block.
+template <typename T, bool TOP, bool ONE>
 __global__ void __launch_bounds__(kMaxThreads)
 logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
   constexpr int W = Vec<T>::kCount;
   constexpr int kWarps = kMaxThreads / 32;
   __shared__ float part[3][kWarps];
   __shared__ uint64_t lists[TOP ? kWarps : 1][32];
-  __shared__ uint32_t reached[kWarps];      // by the lanes of each warp, see Best::share
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int threads = blockDim.x, warps = threads >> 5;
-  const int64_t row = blockIdx.x / cluster;
-  const int rank = int(blockIdx.x - row * cluster);
+  // What every warp has reached, the largest value of each of a thread's pieces, and what may be listed.
+  __shared__ float most_of[kWarps];
+  __shared__ float piece_of[TOP ? kPieces : 1][kMaxThreads];
+  __shared__ uint64_t found[TOP ? kFound : 1];
+  __shared__ int founds[kWarps];
+  // ONE: of the row's only warp, from here on.
+  const int lane = threadIdx.x & 31, warp = ONE ? 0 : threadIdx.x >> 5;
+  const int tid = ONE ? lane : threadIdx.x;
+  const int threads = ONE ? 32 : blockDim.x, warps = ONE ? 1 : threads >> 5;
+  const int64_t row = ONE ? int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)
+                          : int64_t(blockIdx.x / cluster);
+  const int rank = ONE ? 0 : int(blockIdx.x - row * cluster);
   wait_then_start_next();
+  if (ONE && row >= p.rows) return;
 
   const T *const from = static_cast<const T *>(p.logits) + row * p.ld;
   const int cols = int(p.cols);
@@ -230,13 +259,6 @@ logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
   const uint4 *const body = reinterpret_cast<const uint4 *>(from + head);
 
   Stats st = {-INFINITY, 0.0f, 0.0f};
-  Best best;
-  if (TOP) {
-    best.key = kNoKey;
-    best.low = uint64_t(order_of(-3.402823466e38f)) << 32;      // values of -inf are not listed
-    best.low_value = -3.402823466e38f;
-    best.n = p.top;
-  }
   const auto fetch = [&](int first, Vec<T> (&v)[kAhead]) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -247,8 +269,11 @@ logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
     }
   };
   const int step = kAhead * threads;
-  const int each = TOP ? (p.top + warps - 1) / warps : 0;
-  bool first_batch = true;
+  // Rounds of loads in a piece, and the piece so far.
+  const int rounds = TOP ? (v1 - v0 + step - 1) / step : 0;
+  const int in_piece = TOP ? max(1, (rounds + kPieces - 1) / kPieces) : 1;
+  int piece = 0, left = in_piece;
+  float piece_most = -INFINITY;
   Vec<T> next[kAhead];
   fetch(v0, next);
   // Every warp makes the same number of rounds, so that its lanes stay together.
@@ -257,37 +282,16 @@ logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) v[u] = next[u];
     fetch(i0 + step, next);
-    float top[kAhead], most = -INFINITY;
+    float most = -INFINITY;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      top[u] = max_of(v[u]);
-      most = fmaxf(most, top[u]);
-    }
+    for (int u = 0; u < kAhead; ++u) most = fmaxf(most, max_of(v[u]));
     if (TOP) {
-      const uint32_t mine = best.share(fmaxf(st.m, most), each);
-      if (lane == 0) *const_cast<volatile uint32_t *>(&reached[warp]) = mine;
-      if (first_batch) __syncthreads();
-      first_batch = false;
-      // (What another warp has reached by now is reached for good: an older value will do.)
-      const uint32_t all = __reduce_min_sync(
-          kAll, lane < warps ? *const_cast<volatile uint32_t *>(&reached[lane]) : ~0u);
-      best.raise_low(uint64_t(all) << 32);
-      if (__any_sync(kAll, most >= best.low_value)) {
-#pragma unroll 1
-        for (int u = 0; u < kAhead; ++u) {
-          float t = top[0];
-          Vec<T> x = v[0];
-#pragma unroll
-          for (int k = 1; k < kAhead; ++k)
-            if (u == k) {
-              t = top[k];
-              x = v[k];
-            }
-          if (!__any_sync(kAll, t >= best.low_value)) continue;
-          const uint32_t at = uint32_t(head + (i0 + u * threads + tid) * W);
-#pragma unroll
-          for (int k = 0; k < W; ++k) best.offer(x.get(k), at + k);
-        }
+      piece_most = fmaxf(piece_most, most);
+      piece_of[piece][threadIdx.x] = piece_most;
+      if (--left == 0) {
+        left = in_piece;
+        piece_most = -INFINITY;
+        ++piece;
       }
     }
     st.raise(fmaxf(st.m, most), c);
@@ -303,68 +307,131 @@ logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
     st.s += s2;
     st.w += w2;
   }
-  if (rank == 0 && warp == 0) {
-    // The elements before the first vector and after the last, fewer than two vectors' worth.
-    const int tail = head + vectors * W, ends = head + cols - tail;
-    const int i = lane < head ? lane : tail + lane - head;
-    const float x = lane < ends ? as_float(from[i]) : -INFINITY;
-    if (TOP) best.offer(x, uint32_t(i));
+  // The elements before the first vector and after the last, fewer than two vectors' worth.
+  const int tail = head + vectors * W, ends = rank == 0 && warp == 0 ? head + cols - tail : 0;
+  const int end_at = lane < head ? lane : tail + lane - head;
+  const float x = lane < ends ? as_float(from[end_at]) : -INFINITY;
+  const float thread_most = st.m;      // of the vectors
+  if (ends > 0) {
     st.raise(fmaxf(st.m, x), c);
     add_term(x, st.base(), c, st.s, st.w);
   }
-  st.join_warp(c);
-  if (lane == 0) {
-    part[0][warp] = st.m;
-    part[1][warp] = st.s;
-    part[2][warp] = st.w;
-  }
-  if (TOP) lists[warp][lane] = best.key;
-  __syncthreads();
-  if (TOP) {
-    // Pairs of warps, then pairs of those.
-    for (int d = 1; d < warps; d *= 2) {
-      const bool on = warp % (2 * d) == 0 && warp + d < warps;
-      if (on) {
-        best.merge(lists[warp + d][31 - lane]);
-        lists[warp][lane] = best.key;
-      }
+  if constexpr (TOP) {
+    const auto together = [] {
+      if (ONE) __syncwarp();
+      else __syncthreads();
+    };
+    const int own = ONE ? threadIdx.x >> 5 : 0, base = threadIdx.x - lane;
+    const int room = ONE ? kFound / kWarps : kFound;
+    uint64_t *const mine = found + own * room, *const list = lists[own];
+    if (tid == 0) founds[own] = 0;
+    if (tid < 32) list[tid] = kNoKey;
+    // ceil(n / w) threads of every one of w warps reach the least of the warps' ceil(n / w)-th largest.
+    const int each = (p.top + warps - 1) / warps;
+    const float reached = __shfl_sync(kAll, sorted_down(thread_most), each - 1);
+    float bound = reached;
+    if constexpr (!ONE) {
+      if (lane == 0) most_of[warp] = reached;
       __syncthreads();
+      for (int w = 0; w < warps; ++w) bound = fminf(bound, most_of[w]);
     }
-  }
-  if (cluster > 1) {
-    cluster_barrier();
-    if (TOP && rank == 0) {
-      // Warp w takes the lists of blocks w, w + warps, ...; then as above.
-      best.key = kNoKey;
-      for (int r = warp; r < cluster; r += warps)
-        best.merge(cluster_u64(in_block(shared_address(&lists[0][31 - lane]), r)));
-      __syncthreads();      // lists[0] has been read
-      lists[warp][lane] = best.key;
-      __syncthreads();
-      for (int d = 1; d < warps; d *= 2) {
-        if (warp % (2 * d) == 0 && warp + d < warps) {
-          best.merge(lists[warp + d][31 - lane]);
-          lists[warp][lane] = best.key;
+    bound = fmaxf(bound, -3.402823466e38f);      // values of -inf are not listed
+    together();
+    const auto note = [&](float v, int at) {
+      if (!(v >= bound)) return;
+      const int to = atomicAdd(&founds[own], 1);
+      if (to < room) mine[to] = key_of(v, uint32_t(at));
+    };
+    const bool some = thread_most >= bound;
+    if constexpr (ONE) {
+      // Most lanes have something: each its own.
+      for (int r0 = 0, piece = 0; some && r0 < rounds; r0 += in_piece, ++piece) {
+        if (!(piece_of[piece][base + lane] >= bound)) continue;
+        for (int r = r0; r < min(r0 + in_piece, rounds); ++r) {
+          Vec<T> w[kAhead];
+          fetch(v0 + r * step, w);
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            if (!(max_of(w[u]) >= bound)) continue;
+            const int at = head + (v0 + r * step + u * threads + tid) * W;
+#pragma unroll
+            for (int k = 0; k < W; ++k) note(w[u].get(k), at + k);
+          }
         }
+      }
+    } else {
+      // Few have: the warp together, a lane a value of the loads of one of its threads in a round.
+      // (Little code: it is run once a row, and has to be fetched.)
+#pragma unroll 1
+      for (int r0 = 0, piece = 0; r0 < rounds; r0 += in_piece, ++piece) {
+        unsigned from_lanes = __ballot_sync(kAll, some && piece_of[piece][base + lane] >= bound);
+        while (from_lanes) {
+          const int l = __ffs(int(from_lanes)) - 1;
+          from_lanes &= from_lanes - 1;
+#pragma unroll 1
+          for (int r = r0; r < min(r0 + in_piece, rounds); ++r) {
+            const int u = lane / W, i = v0 + r * step + u * threads + (tid - lane + l);
+            const int at = head + i * W + lane % W;
+            if (u < kAhead && i < v1) note(as_float(from[at]), at);
+          }
+        }
+      }
+    }
+    if (lane < ends) note(x, end_at);
+    together();
+    int count = founds[own];
+    if (count > room) {
+      // Too many alike: all of the block's part of the row again, and the ends, a list a warp.
+      together();
+      Best best = {scan_whole(from, head + int64_t(v0) * W + 32 * warp, head + int64_t(v1) * W, warps,
+                              p.top)};
+      if (ends > 0) best.add(lane < ends && x > -INFINITY ? key_of(x, uint32_t(end_at)) : kNoKey);
+      mine[32 * warp + lane] = best.key;
+      count = 32 * warps;
+      together();
+    }
+    place(mine, count, list, tid, threads);
+    together();
+  }
+  st.join_warp(c);
+  Stats all = st;
+  if constexpr (!ONE) {
+    if (lane == 0) {
+      part[0][warp] = st.m;
+      part[1][warp] = st.s;
+      part[2][warp] = st.w;
+    }
+    __syncthreads();
+    if (cluster > 1) {
+      cluster_barrier();
+      if (TOP && rank == 0) {
+        // Warp w takes the lists of blocks w, w + warps, ...
+        for (int r = warp; r < cluster; r += warps)
+          if (lane < p.top)
+            found[p.top * r + lane] = cluster_u64(in_block(shared_address(&lists[0][lane]), r));
+        __syncthreads();
+        place(found, p.top * cluster, lists[0], tid, threads);   // (the same or larger keys, and as many)
         __syncthreads();
       }
     }
+    if (rank == 0 && warp == 0) {
+      all = {-INFINITY, 0.0f, 0.0f};
+      for (int i = lane; i < cluster * warps; i += 32) {
+        const int r = i / warps, w = i - r * warps;
+        Stats o;
+        if (cluster == 1) {
+          o = {part[0][w], part[1][w], part[2][w]};
+        } else {
+          o.m = cluster_float(in_block(shared_address(&part[0][w]), r));
+          o.s = cluster_float(in_block(shared_address(&part[1][w]), r));
+          o.w = cluster_float(in_block(shared_address(&part[2][w]), r));
+        }
+        all.join(o, c);
+      }
+      all.join_warp(c);
+    }
   }
   if (rank == 0 && warp == 0) {
-    Stats all = {-INFINITY, 0.0f, 0.0f};
-    for (int i = lane; i < cluster * warps; i += 32) {
-      const int r = i / warps, w = i - r * warps;
-      Stats o;
-      if (cluster == 1) {
-        o = {part[0][w], part[1][w], part[2][w]};
-      } else {
-        o.m = cluster_float(in_block(shared_address(&part[0][w]), r));
-        o.s = cluster_float(in_block(shared_address(&part[1][w]), r));
-        o.w = cluster_float(in_block(shared_address(&part[2][w]), r));
-      }
-      all.join(o, c);
-    }
-    all.join_warp(c);
     const float log_s = logf(all.s);
     const bool bad = !(all.s == all.s), nothing = all.s == 0.0f;
     const float nan = __uint_as_float(0x7FFFFFFFu);
@@ -380,14 +447,15 @@ logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
       }
     }
     if (TOP && lane < p.top) {
-      const bool have = best.key != kNoKey && !bad;
-      const float v = value_of(uint32_t(best.key >> 32));
-      p.top_ids[row * p.top + lane] = have ? int(~uint32_t(best.key)) : -1;
+      const uint64_t key = lists[ONE ? threadIdx.x >> 5 : 0][lane];
+      const bool have = key != kNoKey && !bad;
+      const float v = value_of(uint32_t(key >> 32));
+      p.top_ids[row * p.top + lane] = have ? int(~uint32_t(key)) : -1;
       p.top_logprobs[row * p.top + lane] =
           bad ? nan : have ? (v - all.m) * p.scale - log_s : -INFINITY;
     }
   }
-  if (cluster > 1) cluster_barrier();      // the others' shared memory has been read
+  if (!ONE && cluster > 1) cluster_barrier();      // the others' shared memory has been read
 }
 
 // ---- gradient ------------------------------------------------------------------------------
@@ -517,10 +585,13 @@ int round_threads(int64_t want) {
 template <typename T>
 cudaError_t launch_logprob_as(const LogprobProblem &p, const DeviceInfo &dev, cudaStream_t stream) {
   const int64_t rounds = (p.cols / Vec<T>::kCount + kAhead - 1) / kAhead;     // of one thread
-  const int threads = round_threads(rounds);
+  // Short rows in numbers: a warp each (8192 rows of 1000, bf16: a block of a warp each 19 us, eight
+  // rows a block 6.4 us).
+  const bool one = rounds <= 4 * 32 && p.rows >= 8 * dev.sm_count;
+  const int threads = one ? kMaxThreads : round_threads(rounds);
   // Blocks of a row: twice as many blocks as there are SMs, a round of loads each at least.
   int cluster = 1;
-  while (cluster < kMaxCluster && p.rows * cluster < 2 * dev.sm_count &&
+  while (!one && cluster < kMaxCluster && p.rows * cluster < 2 * dev.sm_count &&
          rounds >= 2 * cluster * threads)
     cluster *= 2;
   cudaLaunchConfig_t cfg = {};
@@ -531,13 +602,16 @@ cudaError_t launch_logprob_as(const LogprobProblem &p, const DeviceInfo &dev, cu
   attr[1].val.clusterDim.x = unsigned(cluster);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(unsigned(p.rows * cluster), 1, 1);
+  const int64_t per = kMaxThreads / 32;
+  cfg.gridDim = dim3(unsigned(one ? (p.rows + per - 1) / per : p.rows * cluster), 1, 1);
   cfg.blockDim = dim3(unsigned(threads), 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return p.top ? cudaLaunchKernelEx(&cfg, logprob_kernel<T, true>, p, cluster)
-               : cudaLaunchKernelEx(&cfg, logprob_kernel<T, false>, p, cluster);
+  const auto kernel = p.top ? (one ? logprob_kernel<T, true, true> : logprob_kernel<T, true, false>)
+                            : (one ? logprob_kernel<T, false, true>
+                                   : logprob_kernel<T, false, false>);
+  return cudaLaunchKernelEx(&cfg, kernel, p, cluster);
 }
 
 template <typename T>
