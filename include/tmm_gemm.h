@@ -531,7 +531,8 @@ size_t gemm_lora_workspace_size(int dtype, int transw, int transa, int transb, i
 /*
  * A linear layer: the product with one matrix for all rows and what follows it, in one kernel's
  * epilogue.  Element types, sums, rounding, alignment, workspaces and waits as for the grouped
- * operators; sizes below 2^29.
+ * operators, except that FP32 operands of up to 16 rows (M) are read in place for y and dx; sizes
+ * below 2^29.
  */
 #define TMM_ACT_NONE 0
 #define TMM_ACT_RELU 1
@@ -592,8 +593,8 @@ size_t gemm_bias_act_grad_workspace_size(int dtype, int transw, int act, int64_t
  *   - chosen[t, j] is the expert with the j-th largest c among them (ties: the lower number);
  *   - weights[t, j] = scale s_j / (the sum of the chosen s), or (renormalise = 0) scale s_j.
  * The choice is that of the scores to 43 bits (those below 2^-126 count as 0); without a bias it is
- * the logits' own order.  The renormalised weights do not underflow: they are right where every score is below FP32's range.  An
- * expert whose logit or bias is -inf is never chosen; where fewer than k are left (none, in a row of
+ * the logits' own order.  The renormalised weights do not underflow: they are right where every score
+ * is below FP32's range.  An expert whose logit or bias is -inf is never chosen; where fewer than k are left (none, in a row of
  * padding), the last chosen are -1 with weight 0, slots of no group for group_rows.  A row with NaN,
  * or under the softmax with +inf, has NaN weights and chooses some k experts, each once.
  * logits: DEVICE, tokens x experts, row stride ld >= experts; chosen, weights: tokens x k, contiguous.

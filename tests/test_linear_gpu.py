@@ -80,6 +80,27 @@ def test_integers_are_exact(dtype, trans, M, N, K):
     assert torch.equal(y.cpu(), (z + res).to(dtype))
 
 
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("N,K", [(1, 1), (128, 31), (129, 33), (260, 1030), (2048, 515), (4100, 64),
+                                 (72, 9000)])
+def test_few_rows_of_fp32_are_exact(N, K, trans):
+    for M in (1, 2, 3, 4, 7, 8, 15, 16, 17):
+        x, w, dy = ints(M, M, K), ints(2, K, N), ints(3, M, N)
+        bias, z = ints(4, N, top=9), ints(5, M, N, top=1)
+        args = on_gpu(x, torch.float32), on_gpu(w, torch.float32, trans)
+        y, pre = checked(tmm.gemm_bias_act, *args, bias.float().cuda(), "relu", dy.float().cuda(),
+                         pre=True)
+        assert torch.equal(pre.cpu(), (x @ w + bias).float())
+        assert torch.equal(y.cpu(), ((x @ w + bias).relu() + dy).float())
+        for kind in ("none", "relu"):
+            g = checked(tmm.gemm_bias_act_grad, dy.float().cuda(), *args, pre=z.float().cuda(),
+                        act=kind, dbias=True)
+            dz = dy * ref.slope(z, kind)
+            assert torch.equal(g.dx.cpu(), (dz @ w.T).float())
+            assert torch.equal(g.dw.cpu(), (x.T @ dz).float())
+            assert torch.equal(g.dbias.cpu(), dz.sum(0).float())
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 @pytest.mark.parametrize("kind", ref.ACTS)
 @pytest.mark.parametrize("M,N,K,trans", [(1, 512, 1024, True), (70, 515, 300, False),

@@ -84,6 +84,14 @@ def test_operands_on_16_byte_boundaries_need_no_workspace(lib, dtype, M, N, K):
     assert lib.gemm_bias_act_workspace_size(dtype, 0, M, N, K, FAR[0] + 2, K, FAR[1], N) > 0
 
 
+@pytest.mark.parametrize("offset,ldw", [(0, 4096), (4, 4099)])
+def test_few_rows_in_fp32_need_no_workspace(lib, offset, ldw):
+    size = lib.gemm_bias_act_workspace_size
+    assert all(size(_abi.TMM_F32, 0, M, 4096, 512, FAR[0] + offset, 512, FAR[1], ldw) == 0
+               for M in (1, 5, 16))
+    assert size(_abi.TMM_F32, 0, 17, 4096, 512, FAR[0] + offset, 512, FAR[1], ldw) >= 6 * 512 * 4096
+
+
 def test_python_refusals():
     import tiled_matrix_multiply_gb300 as tmm
     x = torch.zeros(4, 8)

@@ -24,6 +24,8 @@ def built():
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=str)
 def test_waits_run_out_once_a_call(dtype, M, K, N):
     lib, limit = _abi.load(), 0.1
+    if dtype is torch.float32:
+        M = max(M, 17)      # of fewer rows the FP32 units' kernel waits for nothing
     x, w = torch.ones(M, K, dtype=dtype, device="cuda"), torch.ones(K, N, dtype=dtype, device="cuda")
     want = tmm.gemm_bias_act(x, w)
     tmm.check_device()

@@ -1001,36 +1001,51 @@ size_t sum_of(std::initializer_list<size_t> sizes) {
   return t;
 }
 
-// dz in the workspace: of the type, on 16-byte rows, or (FP32) as planes.
+// dz in the workspace: of the type, on 16-byte rows, or (FP32) as planes.  FP32 of few rows: dx from
+// FP32 values, whose planes dw takes.
 struct GradPlan {
-  bool make_dz;
+  bool make_dz, few, dz_planes;
   int64_t ldz;
   size_t dz_bytes, partial_bytes, bytes;
 };
+// dz as a matrix of the type: what has been made at `made`, or dy itself.
+Stack dz_stack(const LinearGradProblem &p, const GradPlan &g, const void *made) {
+  return g.make_dz ? Stack{made, 1, p.rows, p.N, g.ldz, 0} : p.dy;
+}
 GradPlan plan_grad(const LinearGradProblem &p) {
   GradPlan g = {};
   g.make_dz = p.act != TMM_ACT_NONE && (p.dx || p.dw);
   g.ldz = (p.N + 7) / 8 * 8;
+  g.few = linear_is_few(p.dtype, p.rows);
+  g.dz_planes = p.dtype == TMM_F32 && !g.few;
   if (g.make_dz) {
-    const __int128 n = __int128(p.rows) * g.ldz * (p.dtype == TMM_F32 ? 6 : 2);
+    const __int128 n = __int128(p.rows) * g.ldz * (g.dz_planes ? 6 : p.dtype == TMM_F32 ? 4 : 2);
     g.dz_bytes = n > __int128(INT64_MAX / 4) ? SIZE_MAX : round256(size_t(n));
   }
   g.partial_bytes = p.dbias ? round256(linear_bias_bytes(p.rows, p.N, p.dtype)) : 0;
+  const bool planes = p.dw || (p.dx && !g.few);
   g.bytes = sum_of({g.dz_bytes, g.partial_bytes,
-                    !g.make_dz && (p.dx || p.dw) ? planes_bytes(p.dy, p.dtype) : 0,
-                    p.dx ? planes_bytes(p.w, p.dtype) : 0, p.dw ? planes_bytes(p.x, p.dtype) : 0});
+                    planes && !(g.make_dz && !g.few) ? planes_bytes(dz_stack(p, g, nullptr), p.dtype)
+                                                     : 0,
+                    p.dx && !g.few ? planes_bytes(p.w, p.dtype) : 0,
+                    p.dw ? planes_bytes(p.x, p.dtype) : 0});
   return g;
 }
 
 }  // namespace
 
+// FP32 of up to 16 rows: making planes of the weights takes longer than the sums (4096 x 4096, gelu and
+// residual, 16 rows: 30 us and 44).
+bool linear_is_few(int dtype, int64_t rows) { return dtype == TMM_F32 && rows <= 16; }
+
 size_t linear_workspace_bytes(const LinearProblem &p) {
-  if (p.K == 0) return 0;
+  if (p.K == 0 || linear_is_few(p.dtype, p.rows)) return 0;
   return sum_of({planes_bytes(p.x, p.dtype), planes_bytes(p.w, p.dtype)});
 }
 
 cudaError_t launch_linear(const LinearProblem &p, const DeviceInfo &dev, void *workspace,
                           cudaStream_t stream) {
+  if (linear_is_few(p.dtype, p.rows) && p.K > 0) return launch_linear_few(p, dev, stream);
   char *ws = static_cast<char *>(workspace);
   DenseProblem d = {p.dtype, p.rows, p.N, p.K};
   if (p.K > 0) {
@@ -1061,16 +1076,18 @@ cudaError_t launch_linear_grad(const LinearGradProblem &p, const DeviceInfo &dev
   char *ws = static_cast<char *>(workspace);
   cudaError_t e;
   Planes dz = {}, w = {}, x = {};
+  void *const made = ws;
   if (g.make_dz) {
-    dz = {ws, p.dtype == TMM_F32 ? 3 : 1, p.rows, p.N, g.ldz, p.rows * g.ldz};
+    dz = {made, g.dz_planes ? 3 : 1, p.rows, p.N, g.ldz, p.rows * g.ldz};
     ws += g.dz_bytes;
   }
   if (g.make_dz || p.dbias) {
-    e = launch_linear_slopes(p, const_cast<void *>(dz.data), g.ldz, p.dtype == TMM_F32,
+    e = launch_linear_slopes(p, g.make_dz ? made : nullptr, g.ldz, g.dz_planes,
                              reinterpret_cast<float *>(ws), dev, stream);
     if (e != cudaSuccess) return e;
   }
   ws += g.partial_bytes;
+  const Stack matrix = dz_stack(p, g, made);
   const Stack *from[3];
   Planes to[3], *at[3];
   int count = 0;
@@ -1078,14 +1095,27 @@ cudaError_t launch_linear_grad(const LinearGradProblem &p, const DeviceInfo &dev
     from[count] = &s;
     at[count++] = planes;
   };
-  if (!g.make_dz && (p.dx || p.dw)) need(p.dy, &dz);
-  if (p.dx) need(p.w, &w);
+  if ((p.dw || (p.dx && !g.few)) && !(g.make_dz && !g.few)) need(matrix, &dz);
+  if (p.dx && !g.few) need(p.w, &w);
   if (p.dw) need(p.x, &x);
   if ((e = make_operand_planes(from, to, count, p.dtype, &ws, dev, stream)) != cudaSuccess) return e;
   for (int i = 0; i < count; ++i) *at[i] = to[i];
+  if (p.dx && g.few) {
+    LinearProblem f = {};
+    f.dtype = p.dtype;
+    f.rows = p.rows;
+    f.N = p.K;
+    f.K = p.N;
+    f.x = matrix;
+    f.w = p.w;
+    f.trans_w = !p.trans_w;
+    f.y = p.dx;
+    f.ldy = p.lddx;
+    if ((e = launch_linear_few(f, dev, stream)) != cudaSuccess) return e;
+  }
   DenseProblem d = {};
   d.dtype = p.dtype;
-  if (p.dx) {
+  if (p.dx && !g.few) {
     d.M = p.rows;
     d.N = p.K;
     d.K = p.N;

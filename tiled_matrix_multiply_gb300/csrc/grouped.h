@@ -90,6 +90,10 @@ struct Planes {
   const void *data;
   int64_t count, rows, cols, ld, stride;   // count: matrices of all planes
 };
+// A linear layer of few rows in FP32, on the FP32 units: no planes, no workspace.
+bool linear_is_few(int dtype, int64_t rows);
+cudaError_t launch_linear_few(const LinearProblem &p, const DeviceInfo &dev, cudaStream_t stream);
+
 // Planes of up to four plain operands, in place where the copy engine can read them, else in *ws
 // (which advances past planes_bytes of each), made by one launch.
 size_t planes_bytes(const Stack &s, int dtype);
