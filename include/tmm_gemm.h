@@ -596,7 +596,8 @@ size_t gemm_bias_act_grad_workspace_size(int dtype, int transw, int act, int64_t
  * the logits' own order.  The renormalised weights do not underflow: they are right where every score
  * is below FP32's range.  An expert whose logit or bias is -inf is never chosen; where fewer than k are left (none, in a row of
  * padding), the last chosen are -1 with weight 0, slots of no group for group_rows.  A row with NaN,
- * or under the softmax with +inf, has NaN weights and chooses some k experts, each once.
+ * or under the softmax with +inf, at an expert whose bias is not -inf has NaN weights, and chooses some
+ * k experts, each once.
  * logits: DEVICE, tokens x experts, row stride ld >= experts; chosen, weights: tokens x k, contiguous.
  * 1 <= experts <= 512, groups <= 32 dividing experts, k <= 16 and <= the experts of top_groups
  * groups, tokens below 2^29.  tokens == 0 is a no-op.  Outputs must not overlap inputs or each

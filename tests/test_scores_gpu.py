@@ -97,6 +97,30 @@ def test_route_scores_closer_than_single_precision_tells(score, groups, top_grou
                     group_best=best)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,k,at", [(64, 1, 6, 0), (64, 1, 6, 5), (256, 8, 8, 3), (256, 8, 8, 7),
+                                           (40, 1, 1, 0), (48, 4, 5, 4), (64, 1, 6, (2, 3)),
+                                           (64, 1, 6, (5, 6)), (64, 1, 6, (0, 2, 4))])
+def test_route_pairs_closer_than_single_precision_tells(score, E, groups, k, at):
+    """Scores number `at` and the next of every row are the same up to the rounding of a logit."""
+    T = 200
+    x, bias = normals(E, T, E, std=1.2), normals(3, E, std=0.05)
+    for j in (at,) if isinstance(at, int) else at:
+        s = ref.scores(x, score)
+        order = (s + bias.double()).argsort(1, descending=True)
+        a, b = order[:, j], order[:, j + 1]
+        row = torch.arange(T)
+        d = bias[a].double() - bias[b].double()
+        if score == "sigmoid":
+            x[row, b] = torch.logit((s[row, a] + d).clamp(1e-3, 1 - 1e-6)).float()
+        else:      # e_b (1 - d) = e_a + d (the sum of all but e_b)
+            e = torch.exp(x.double())
+            rest = e.sum(1) - e[row, b]
+            x[row, b] = torch.log(((e[row, a] + d * rest) / (1 - d)).clamp(min=1e-6)).float()
+    check_route(x, k, bias, score=score, groups=groups, top_groups=max(1, groups // 2),
+                group_best=min(groups, 2))
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_masked_experts(dtype, score):
@@ -146,6 +170,38 @@ def test_route_rows_that_are_not_finite():
         if groups == 1:
             assert bool(w[0].isnan().all() and w[2].isnan().all())
             assert bool(w[1].isnan().all()) == (score == "softmax")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_nan_in_a_row_reaches_all_its_weights(dtype, score):
+    nan = float("nan")
+    x = normals(9, 7, 64, dtype=dtype)
+    x[0, 5] = nan
+    x[1] = nan
+    x[2, 3:] = -INF
+    x[2, 1] = nan                  # fewer left than are chosen
+    x[3, 6] = INF
+    x[4, 8:16] = nan               # all of a group
+    x[5, 0] -= 40.0                # beside NaN where the bias is -inf, and the lowest group's
+    x[5, 63] = nan
+    shut = normals(1, 64, std=0.1)
+    shut[63] = -INF
+    for groups, best, bias, renormalise in itertools.product(
+            (1, 8), (1, 2), (None, normals(1, 64, std=0.1), shut), (True, False)):
+        r = tmm.route_rows(x.cuda(), 4, bias=None if bias is None else bias.cuda(), score=score,
+                           groups=groups, top_groups=max(1, groups // 2), group_best=best,
+                           renormalise=renormalise)
+        e, w = r.experts.cpu(), r.weights.cpu()
+        for row in range(7):
+            mine = e[row][e[row] >= 0].tolist()
+            assert len(set(mine)) == len(mine) == (3 if row == 2 else 4)
+            assert bool((w[row][e[row] < 0] == 0).all())
+            bad = row in (0, 1, 2, 4) or (row == 3 and score == "softmax")
+            if row == 5 and (bias is not shut or score == "softmax"):
+                continue
+            got = w[row][e[row] >= 0]
+            assert bool(got.isnan().all() if bad else got.isfinite().all()), (row, groups, best)
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)

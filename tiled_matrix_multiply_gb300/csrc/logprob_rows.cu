@@ -26,7 +26,7 @@
 // Gradient: dl_v = scale (g ([v = t] - p_v) - h p_v (log p_v + entropy) + sum_j e_j ([v = id_j] - p_v))
 // for the gradients g, h and e_j of the row's log probability, entropy and alternatives: one read and
 // one write.
-#include <atomic>
+#include <algorithm>
 #include <cstdint>
 
 #include "row_ops.cuh"

@@ -54,6 +54,98 @@ __device__ __forceinline__ float near_sigmoid(float l) {
 }
 __device__ __forceinline__ float near_exp(float t) { return __expf(t); }
 
+// ---- pairs of FP32 values --------------------------------------------------------------------
+//
+// A value is the sum of two FP32 values that do not overlap, 47 bits (Dekker's and Knuth's exact sums and
+// products).  The FP64 units of this GPU are few and far: a row of 256 sigmoids took them 16 us, with
+// nothing else to do.
+
+struct Two {
+  float h, l;
+};
+__device__ __forceinline__ Two sum_of(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two renewed(float h, float l) {      // |h| >= |l|
+  const float s = __fadd_rn(h, l);
+  return {s, __fsub_rn(l, __fsub_rn(s, h))};
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+  const Two s = sum_of(a.h, b.h), t = sum_of(a.l, b.l);
+  const Two u = renewed(s.h, __fadd_rn(s.l, t.h));
+  return renewed(u.h, __fadd_rn(u.l, t.l));
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+  const float p = __fmul_rn(a.h, b.h);
+  return renewed(p, __fmaf_rn(a.h, b.l, __fmaf_rn(a.l, b.h, __fmaf_rn(a.h, b.h, -p))));
+}
+__device__ __forceinline__ Two one_over(Two b) {
+  const float q = __frcp_rn(b.h);
+  // 1 - q b, exactly but for its last bits.
+  const float r = __fmaf_rn(-q, b.l, __fmaf_rn(-q, b.h, 1.0f));
+  return renewed(q, __fmul_rn(q, r));
+}
+// e^y for y.h from -87 to 88.  y = n ln 2 + r, the first part of ln 2 of nine bits, so that n times it is
+// exact; Taylor's series, whose terms from the seventh on are below 2^-22 of the sum and made in FP32.
+__device__ __forceinline__ Two exp_of(Two y) {
+  const float n = rintf(y.h * 1.44269504f);
+  const float c = -0.00021219444f, p = __fmul_rn(n, c);      // the rest of ln 2
+  const Two tail = {p, __fmaf_rn(n, 1.6465949697480609e-12f, __fmaf_rn(n, c, -p))};
+  const Two r = Two{__fmaf_rn(-n, 0.693359375f, y.h), y.l} + Two{-tail.h, -tail.l};
+  const float x = r.h;
+  float t = 1.0f / 6227020800.0f;
+  t = fmaf(t, x, 1.0f / 479001600.0f);
+  t = fmaf(t, x, 1.0f / 39916800.0f);
+  t = fmaf(t, x, 1.0f / 3628800.0f);
+  t = fmaf(t, x, 1.0f / 362880.0f);
+  t = fmaf(t, x, 1.0f / 40320.0f);
+  t = fmaf(t, x, 1.0f / 5040.0f);
+  Two q = {t, 0.0f};      // 1/6!, 1/5!, ...: their nearest FP32 values, and what these leave
+  q = q * r + Two{1.0f / 720.0f, -3.3631094437103215e-11f};
+  q = q * r + Two{1.0f / 120.0f, -4.34617203337595e-10f};
+  q = q * r + Two{1.0f / 24.0f, -1.2417634698280722e-09f};
+  q = q * r + Two{1.0f / 6.0f, -4.967053879312289e-09f};
+  q = q * r + Two{0.5f, 0.0f};
+  q = q * r + Two{1.0f, 0.0f};
+  q = q * r + Two{1.0f, 0.0f};
+  const float scale = __int_as_float((int(n) + 127) << 23);
+  return {q.h * scale, q.l * scale};
+}
+__device__ __forceinline__ uint64_t key_of(Two v) {
+  return uint64_t(key_of(v.h)) << 32 | key_of(v.l);
+}
+__device__ __forceinline__ Two value_of(uint64_t key) {
+  return {value_of(uint32_t(key >> 32)), value_of(uint32_t(key))};
+}
+__device__ __forceinline__ uint64_t more(uint64_t a, uint64_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint64_t less(uint64_t a, uint64_t b) { return a > b ? b : a; }
+
+// The scores of up to four logits, a call: seldom run, and has to be fetched when it is.
+struct Four {
+  Two v[4];
+};
+__device__ __noinline__ Four scores_of(float l0, float l1, float l2, float l3, float m,
+                                       bool is_sigmoid) {
+  const float l[4] = {l0, l1, l2, l3};
+  Four f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // 1 / (1 + e^-l) of the smaller of e^-l and e^l; e^(l - m).  0 below -87, where FP32 ends.
+    Two y = is_sigmoid ? Two{-fabsf(l[i]), 0.0f} : sum_of(l[i], -m);
+    const bool tiny = y.h < -87.0f;      // (NaN stays)
+    if (tiny) y = {0.0f, 0.0f};
+    Two e = exp_of(y);
+    if (is_sigmoid) {
+      const Two s = one_over(e + Two{1.0f, 0.0f});
+      e = l[i] < 0.0f ? e * s : s;
+    }
+    const float end = is_sigmoid && l[i] > 0.0f ? 1.0f : 0.0f;
+    f.v[i] = tiny ? Two{end, 0.0f} : e;
+  }
+  return f;
+}
+
 // A lane's keys, the largest first (a network of exchanges: Batcher's odd-even merge sort).
 template <int V>
 __device__ __forceinline__ void sort_down(uint32_t (&k)[V]) {
@@ -209,7 +301,9 @@ __device__ __forceinline__ bool group_open(const RouteProblem &p, const Lane<VEC
 // value lies between the lowest and the highest that may be chosen, and 9 bits of the expert's number's
 // complement, so that one reduction finds the best and, of equal ones, the lower number; every lane's
 // keys are sorted first, and the lane that had the best shows its next.  `close`: two values that
-// decide something are within the error of the scores and of a key, and not made from equal inputs.
+// decide something are within the error of the scores and of a key, and not made from equal inputs, or
+// one is not finite.  Two sigmoids alone that are close to each other, by far the most of these, are put
+// in order here (again: 7 us; 16384 x 256, 8 groups: 27.5 us without this, 23.6 with it).
 // l: this lane's logits, -inf where it has none.
 template <typename T, bool VEC, int V>
 __device__ __forceinline__ int choose(const RouteProblem &p, int64_t row, const Lane<VEC> &a,
@@ -218,7 +312,11 @@ __device__ __forceinline__ int choose(const RouteProblem &p, int64_t row, const 
   float c[V], m;
   bool on[V], open = true;
   const float error = make_scores(p, a, l, c, on, m);
-  close = false;
+  float odd = 0.0f;      // NaN where a score is infinite or NaN
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (on[v]) odd += c[v] * 0.0f;
+  close = __any_sync(kAll, odd != 0.0f);
   if (p.groups > 1) {
     float one = -INFINITY, two = -INFINITY;
 #pragma unroll
@@ -229,19 +327,17 @@ __device__ __forceinline__ int choose(const RouteProblem &p, int64_t row, const 
     }
     open = group_open(p, a, one, two, m, error, close);
   }
-  float hi = -INFINITY, below = -INFINITY, odd = 0.0f;      // below: the lowest, negated
+  float hi = -INFINITY, below = -INFINITY;      // below: the lowest, negated
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     on[v] &= open;
     if (on[v]) {
       hi = fmaxf(hi, c[v]);
       below = fmaxf(below, -c[v]);
-      odd += c[v] * 0.0f;      // NaN of an infinity or NaN
     }
   }
   hi = warp_max(hi);
   const float lo = fmaxf(-warp_max(below), hi - 32.0f);      // (values further down share a key)
-  if (__any_sync(kAll, odd != 0.0f)) close = true;
   const float range = hi - lo, step = range > 1e-30f ? 8388600.0f / range : 0.0f;
   const bool some = hi > -INFINITY;
   uint32_t key[V];
@@ -266,15 +362,34 @@ __device__ __forceinline__ int choose(const RouteProblem &p, int64_t row, const 
   // (Keys are made of steps that do not decrease: without a bias only equal ones are in doubt.)
   const float tol =
       p.bias ? (error + 0x1p-22f * fmaxf(fabsf(hi), fabsf(lo))) * step + 1.5f : 0.5f;
-  bool near = lane < p.k && next != 0 && float((mine >> 9) - (next >> 9)) <= tol;
-  if (__any_sync(kAll, near)) {
-    if (near) {
-      // Equal logits with equal biases are equal, and their numbers decide.
-      const T *const at = static_cast<const T *>(p.logits) + row * p.ld;
-      const int x = 511 - int(mine & 511), y = 511 - int(next & 511);
-      near = float(at[x]) != float(at[y]) || (p.bias && p.bias[x] != p.bias[y]);
+  const bool near = lane < p.k && next != 0 && float((mine >> 9) - (next >> 9)) <= tol;
+  const unsigned pairs = __ballot_sync(kAll, near);
+  if (pairs) {
+    const T *const at = static_cast<const T *>(p.logits) + row * p.ld;
+    const int x = 511 - int(mine & 511), y = 511 - int(next & 511);
+    // Equal logits with equal biases are equal, and their numbers decide.
+    const bool doubt = near && (as_float(at[x]) != as_float(at[y]) ||
+                                (p.bias && p.bias[x] != p.bias[y]));
+    // The last one and the one before it are no pair alone if a third is close, which is shown next.
+    const uint32_t third = __reduce_max_sync(kAll, key[0]), last = __shfl_sync(kAll, mine, p.k);
+    const bool three = third != 0 && float((last >> 9) - (third >> 9)) <= tol;
+    if (!p.bias || !p.sigmoid || (pairs & pairs << 1) || (three && (pairs >> (p.k - 1) & 1))) {
+      close |= __any_sync(kAll, doubt);
+    } else {
+      bool swap = false;
+      if (doubt) {
+        const Four f = scores_of(as_float(at[x]), as_float(at[y]), 0.0f, 0.0f, 0.0f, true);
+        const uint64_t a2 = key_of(f.v[0] + Two{p.bias[x], 0.0f});
+        const uint64_t b2 = key_of(f.v[1] + Two{p.bias[y], 0.0f});
+        swap = b2 > a2 || (b2 == a2 && y < x);
+      }
+      const unsigned swaps = __ballot_sync(kAll, swap);
+      const uint32_t before = __shfl_up_sync(kAll, mine, 1);
+      if (swap)
+        mine = next;
+      else if (swaps << 1 >> lane & 1)
+        mine = before;
     }
-    close |= __any_sync(kAll, near);
   }
   return lane < p.k && mine != 0 ? 511 - int(mine & 511) : -1;
 }
@@ -299,99 +414,10 @@ __device__ __forceinline__ void load_logits(const RouteProblem &p, int64_t row, 
   }
 }
 
-// ---- the choice again, in pairs of FP32 values ---------------------------------------------
-//
-// A value is the sum of two FP32 values that do not overlap, 47 bits (Dekker's and Knuth's exact sums and
-// products).  The FP64 units of this GPU are few and far: a row of 256 sigmoids took them 16 us, with
-// nothing else to do.
+// ---- the choice again ----------------------------------------------------------------------
 
-struct Two {
-  float h, l;
-};
-__device__ __forceinline__ Two sum_of(float a, float b) {
-  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
-  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
-}
-__device__ __forceinline__ Two renewed(float h, float l) {      // |h| >= |l|
-  const float s = __fadd_rn(h, l);
-  return {s, __fsub_rn(l, __fsub_rn(s, h))};
-}
-__device__ __forceinline__ Two operator+(Two a, Two b) {
-  const Two s = sum_of(a.h, b.h), t = sum_of(a.l, b.l);
-  const Two u = renewed(s.h, __fadd_rn(s.l, t.h));
-  return renewed(u.h, __fadd_rn(u.l, t.l));
-}
-__device__ __forceinline__ Two operator*(Two a, Two b) {
-  const float p = __fmul_rn(a.h, b.h);
-  return renewed(p, __fmaf_rn(a.h, b.l, __fmaf_rn(a.l, b.h, __fmaf_rn(a.h, b.h, -p))));
-}
-__device__ __forceinline__ Two one_over(Two b) {
-  const float q = __frcp_rn(b.h);
-  // 1 - q b, exactly but for its last bits.
-  const float r = __fmaf_rn(-q, b.l, __fmaf_rn(-q, b.h, 1.0f));
-  return renewed(q, __fmul_rn(q, r));
-}
-// e^y for y.h from -87 to 88.  y = n ln 2 + r, the first part of ln 2 of nine bits, so that n times it is
-// exact; Taylor's series, whose terms from the seventh on are below 2^-22 of the sum and made in FP32.
-__device__ __forceinline__ Two exp_of(Two y) {
-  const float n = rintf(y.h * 1.44269504f);
-  const float c = -0.00021219444f, p = __fmul_rn(n, c);      // the rest of ln 2
-  const Two tail = {p, __fmaf_rn(n, 1.6465949697480609e-12f, __fmaf_rn(n, c, -p))};
-  const Two r = Two{__fmaf_rn(-n, 0.693359375f, y.h), y.l} + Two{-tail.h, -tail.l};
-  const float x = r.h;
-  float t = 1.0f / 6227020800.0f;
-  t = fmaf(t, x, 1.0f / 479001600.0f);
-  t = fmaf(t, x, 1.0f / 39916800.0f);
-  t = fmaf(t, x, 1.0f / 3628800.0f);
-  t = fmaf(t, x, 1.0f / 362880.0f);
-  t = fmaf(t, x, 1.0f / 40320.0f);
-  t = fmaf(t, x, 1.0f / 5040.0f);
-  Two q = {t, 0.0f};      // 1/6!, 1/5!, ...: their nearest FP32 values, and what these leave
-  q = q * r + Two{1.0f / 720.0f, -3.3631094437103215e-11f};
-  q = q * r + Two{1.0f / 120.0f, -4.34617203337595e-10f};
-  q = q * r + Two{1.0f / 24.0f, -1.2417634698280722e-09f};
-  q = q * r + Two{1.0f / 6.0f, -4.967053879312289e-09f};
-  q = q * r + Two{0.5f, 0.0f};
-  q = q * r + Two{1.0f, 0.0f};
-  q = q * r + Two{1.0f, 0.0f};
-  const float scale = __int_as_float((int(n) + 127) << 23);
-  return {q.h * scale, q.l * scale};
-}
-__device__ __forceinline__ uint64_t key_of(Two v) {
-  return uint64_t(key_of(v.h)) << 32 | key_of(v.l);
-}
-__device__ __forceinline__ Two value_of(uint64_t key) {
-  return {value_of(uint32_t(key >> 32)), value_of(uint32_t(key))};
-}
-__device__ __forceinline__ uint64_t more(uint64_t a, uint64_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint64_t less(uint64_t a, uint64_t b) { return a > b ? b : a; }
-
-// The scores of up to four logits, a call: seldom run, and has to be fetched when it is.
-struct Four {
-  Two v[4];
-};
-__device__ __noinline__ Four scores_of(float l0, float l1, float l2, float l3, float m,
-                                       bool is_sigmoid) {
-  const float l[4] = {l0, l1, l2, l3};
-  Four f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // 1 / (1 + e^-l) of the smaller of e^-l and e^l; e^(l - m).  0 below -87, where FP32 ends.
-    Two y = is_sigmoid ? Two{-fabsf(l[i]), 0.0f} : sum_of(l[i], -m);
-    const bool tiny = y.h < -87.0f;      // (NaN stays)
-    if (tiny) y = {0.0f, 0.0f};
-    Two e = exp_of(y);
-    if (is_sigmoid) {
-      const Two s = one_over(e + Two{1.0f, 0.0f});
-      e = l[i] < 0.0f ? e * s : s;
-    }
-    const float end = is_sigmoid && l[i] > 0.0f ? 1.0f : 0.0f;
-    f.v[i] = tiny ? Two{end, 0.0f} : e;
-  }
-  return f;
-}
-
-// `choose` in pairs of values.
+// `choose` in pairs of values: the expert, or -1, plus 1, and kNaN for a row whose weights are NaN.
+constexpr int kNaN = 1 << 16;
 template <typename T, bool VEC, int V>
 __device__ __noinline__ int choose_again(const RouteProblem &p, int64_t row) {
   const int lane = threadIdx.x & 31;
@@ -431,8 +457,10 @@ __device__ __noinline__ int choose_again(const RouteProblem &p, int64_t row) {
       c[v] = fabsf(b[v]) < INFINITY ? c[v] * scale + Two{b[v], 0.0f} : Two{b[v], 0.0f};
   }
   uint64_t key[V], best = 0, second = 0;
+  bool bad = false;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
+    bad |= b[v] != -INFINITY && (l[v] != l[v] || (!p.sigmoid && l[v] == INFINITY));
     key[v] = l[v] == -INFINITY || b[v] == -INFINITY ? 0 : key_of(c[v]);
     second = more(second, less(best, key[v]));
     best = more(best, key[v]);
@@ -491,7 +519,7 @@ __device__ __noinline__ int choose_again(const RouteProblem &p, int64_t row) {
       if (a.has(v) && a.expert(v) == e) key[v] = 0;
     if (lane == j) mine = e;
   }
-  return mine;
+  return mine + 1 + (__any_sync(kAll, bad) ? kNaN : 0);
 }
 
 // The chosen scores of a row over their sum, as lane j has logit x of slot j (-inf: none), 0 where
@@ -525,7 +553,12 @@ route_kernel(const __grid_constant__ RouteProblem p) {
   load_logits<T>(p, row, a, l);
   bool close;
   int e = choose<T>(p, row, a, l, close);
-  if (close) e = choose_again<T, VEC, V>(p, row);
+  bool bad = false;
+  if (close) {
+    const int again = choose_again<T, VEC, V>(p, row);
+    bad = again >= kNaN;
+    e = (again & (kNaN - 1)) - 1;
+  }
   float m = 0.0f, sum = 1.0f;
   if (!p.sigmoid && !p.renormalise) {
     float top = -INFINITY;
@@ -539,7 +572,8 @@ route_kernel(const __grid_constant__ RouteProblem p) {
   }
   const float x =
       e >= 0 ? as_float(static_cast<const T *>(p.logits)[row * p.ld + e]) : -INFINITY;
-  const float w = score_of(p.sigmoid, p.renormalise, x, m, sum);
+  float w = score_of(p.sigmoid, p.renormalise, x, m, sum);
+  if (bad) w = __uint_as_float(0x7FFFFFFFu);
   if (lane < p.k) {
     p.chosen[row * p.k + lane] = e;
     p.weights[row * p.k + lane] = e >= 0 ? p.scale * w : 0.0f;
