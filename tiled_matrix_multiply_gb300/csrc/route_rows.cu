@@ -11,9 +11,14 @@
 //
 // A warp does a row, all of whose values stay in registers: with G groups rounded up to a power of
 // two every group has 32 / G lanes, so that a group's best are a butterfly within its lanes.  The
-// choice is k + 1 rounds of one warp reduction over keys that hold a value and its number.
+// choice is k + 1 rounds of one warp reduction over keys that hold a value and its number.  About 600
+// instructions a row of 256, in chains of reductions and shuffles, are the bound (16384 rows of 256 FP32
+// logits, k = 8: plain 14.4 us, sigmoids and a bias 18, in 8 groups 23; reading takes 2.7).  Neither more
+// rows in flight (40 or 48 warps an SM: within 2 us, either way) nor blocks of another size help (one or
+// two rows a block: 8 experts 17 and 9 us in place of 7; eight: the same).
 // Gradient: w depends on the chosen logits alone, but for the softmax without renormalisation;
-// rows are written whole, 16 bytes a lane, and the chosen few again.
+// rows are written whole, 16 bytes a lane, and the chosen few again (16384 x 256: 6.6 us; writing and
+// reading take 2.8, a block every four rows most of the rest).
 #include <cstdint>
 #include <type_traits>
 
@@ -263,6 +268,7 @@ template <bool VEC>
 __device__ __forceinline__ bool group_open(const RouteProblem &p, const Lane<VEC> &a, float one,
                                            float two, float m, float error, bool &close) {
   const bool bias = p.bias != nullptr;
+  const int lane = threadIdx.x & 31;
 #pragma unroll 1
   for (int d = 1; d < p.lanes; d <<= 1) {
     const float o = __shfl_xor_sync(kAll, one, d), t = __shfl_xor_sync(kAll, two, d);
@@ -280,11 +286,14 @@ __device__ __forceinline__ bool group_open(const RouteProblem &p, const Lane<VEC
       value = one + two;
   }
   const uint32_t key = any ? key_of(value) : 0u;
+  // A group's lanes compare it with every lanes-th group each.
   int rank = 0;
-  for (int h = 0; h < p.groups; ++h) {
+  for (int h = lane & (p.lanes - 1); h - (lane & (p.lanes - 1)) < p.groups; h += p.lanes) {
     const uint32_t other = __shfl_sync(kAll, key, h * p.lanes);
-    rank += other > key || (other == key && h < a.group);
+    rank += h < p.groups && (other > key || (other == key && h < a.group));
   }
+#pragma unroll 1
+  for (int d = 1; d < p.lanes; d <<= 1) rank += __shfl_xor_sync(kAll, rank, d);
   const bool open = key != 0 && rank < p.top_groups;
   if (bias || p.best == 2) {
     // (Values are in the order of their keys.)
