@@ -21,7 +21,8 @@
 // for each how many are larger.  So the pass is the one without alternatives, and the selection comes
 // after it.  Rows of which too many values reach the bound (thousands of equal ones) are read again
 // whole, by lists that are kept sorted.  (With such lists in the pass itself, under thresholds of various
-// kinds, 4096 rows of 131072 with 20 listed took 320 to 520 us, 248 now.)
+// kinds, 4096 rows of 131072 with 20 listed took 320 to 520 us, 213 now; the pass alone takes 161, the
+// memory's time.)
 //
 // Gradient: dl_v = scale (g ([v = t] - p_v) - h p_v (log p_v + entropy) + sum_j e_j ([v = id_j] - p_v))
 // for the gradients g, h and e_j of the row's log probability, entropy and alternatives: one read and
@@ -360,20 +361,38 @@ logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
         }
       }
     } else {
-      // Few have: the warp together, a lane a value of the loads of one of its threads in a round.
+      // Few have: the warp lists their pieces (where the pieces' maxima were, as they have been looked
+      // at), and reads eight threads' at a time, four lanes a thread's loads in a round.
       // (Little code: it is run once a row, and has to be fetched.)
+      unsigned pieces = 0;
 #pragma unroll 1
-      for (int r0 = 0, piece = 0; r0 < rounds; r0 += in_piece, ++piece) {
-        unsigned from_lanes = __ballot_sync(kAll, some && piece_of[piece][base + lane] >= bound);
-        while (from_lanes) {
-          const int l = __ffs(int(from_lanes)) - 1;
-          from_lanes &= from_lanes - 1;
+      for (int i = 0; some && i * in_piece < rounds; ++i)
+        if (piece_of[i][threadIdx.x] >= bound) pieces |= 1u << i;
+      int to = __popc(pieces);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int before = __shfl_up_sync(kAll, to, d);
+        if (lane >= d) to += before;
+      }
+      const int listed = __shfl_sync(kAll, to, 31);
+      to -= __popc(pieces);
+      const auto entry = [&](int i) -> float & { return piece_of[i >> 5][base + (i & 31)]; };
+      for (; pieces; pieces &= pieces - 1)
+        entry(to++) = __int_as_float(lane | (__ffs(int(pieces)) - 1) << 5);
+      __syncwarp();
 #pragma unroll 1
-          for (int r = r0; r < min(r0 + in_piece, rounds); ++r) {
-            const int u = lane / W, i = v0 + r * step + u * threads + (tid - lane + l);
-            const int at = head + i * W + lane % W;
-            if (u < kAhead && i < v1) note(as_float(from[at]), at);
-          }
+      for (int e = lane / kAhead; e < listed; e += 32 / kAhead) {
+        const int which = __float_as_int(entry(e)), r0 = (which >> 5) * in_piece;
+        const int first = v0 + lane % kAhead * threads + (tid - lane) + (which & 31);
+#pragma unroll 1
+        for (int r = r0; r < min(r0 + in_piece, rounds); ++r) {
+          const int i = first + r * step;
+          if (i >= v1) break;
+          Vec<T> w;
+          w.w = __ldg(body + i);
+          if (!(max_of(w) >= bound)) continue;
+#pragma unroll
+          for (int k = 0; k < W; ++k) note(w.get(k), head + i * W + k);
         }
       }
     }
@@ -588,7 +607,10 @@ cudaError_t launch_logprob_as(const LogprobProblem &p, const DeviceInfo &dev, cu
   // Short rows in numbers: a warp each (8192 rows of 1000, bf16: a block of a warp each 19 us, eight
   // rows a block 6.4 us).
   const bool one = rounds <= 4 * 32 && p.rows >= 8 * dev.sm_count;
-  const int threads = one ? kMaxThreads : round_threads(rounds);
+  // With alternatives smaller blocks, whose selections come more evenly (20 listed: 2000 x 8000, bf16, 25
+  // and 20 us, 4096 x 32768 81 and 72, but 4096 x 131072 213 and 228).
+  const bool small = p.top && rounds <= 4 * kMaxThreads && p.rows >= 4 * dev.sm_count;
+  const int threads = one ? kMaxThreads : std::min(small ? 128 : kMaxThreads, round_threads(rounds));
   // Blocks of a row: twice as many blocks as there are SMs, a round of loads each at least.
   int cluster = 1;
   while (!one && cluster < kMaxCluster && p.rows * cluster < 2 * dev.sm_count &&
