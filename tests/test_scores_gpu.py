@@ -305,11 +305,15 @@ def test_route_without_tokens():
 # ---- log probabilities ---------------------------------------------------------------------
 
 
-def check_logprobs(x, tokens=None, top=0, scale=1.0):
-    p = tmm.logprob_rows(x if x.is_cuda else x.cuda(),
-                         None if tokens is None else tokens.cuda(), top=top, scale=scale)
+def check_logprobs(x, tokens=None, top=0, scale=1.0, given=None, times=1):
+    """Of logits x, or of `given` on the GPU, which are x's rows as many times."""
+    given = x.cuda() if given is None else given
+    p = tmm.logprob_rows(given, None if tokens is None else tokens.repeat(times).cuda(), top=top,
+                         scale=scale)
     x = x.cpu()
     want, *how = ref.logprobs(x, tokens, top, scale)
+    want = {k: v.repeat(times, *[1] * (v.dim() - 1)) for k, v in want.items()}
+    how = [v.repeat(times) for v in how]
     lse, lp, ent = ref.logprob_bounds(want, *how, x.shape[1])
     ref.assert_close(p.lse, want["lse"], lse, "lse")
     ref.assert_close(p.entropy, want["entropy"], ent, "entropy")
@@ -408,6 +412,30 @@ def test_alternatives_in_awkward_orders(dtype, kind):
     many = x.repeat(100, 1)
     p, few = tmm.logprob_rows(many.cuda(), top=32), tmm.logprob_rows(x.cuda(), top=32)
     assert torch.equal(p.top_ids, few.top_ids.repeat(100, 1))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("V,ld", [(5, 5), (64, 67), (1000, 1000), (3001, 3008), (8001, 8001)])
+def test_logprobs_of_many_rows(dtype, V, ld):
+    """Rows in numbers, as many as have a warp each and more: the same 26 over and over."""
+    T, times, low = 26, 50, torch.finfo(dtype).min
+    x = normals(V, T, V, std=2.0, dtype=dtype)
+    x[1] = -INF
+    x[2] = low
+    x[3, 2:] = low
+    x[4, 1:] = -INF
+    x[5] = 0.25                                   # all alike
+    x[6] = (torch.arange(V) % 3).to(dtype)
+    x[7] = (torch.arange(V) / 64).to(dtype)
+    x[8] = (-torch.arange(V) / 64).to(dtype)
+    x[9, : V // 2] = -INF
+    tokens = some_tokens(3, T, V)
+    tokens[5::7] = -1
+    v = strided(x.repeat(times, 1), ld, 1 if ld > V else 0)
+    for top in (0, 1, 5, 16, 17, 20, 21, 32):
+        # (Not bit for bit the same at every repeat: where a row's first 16-byte boundary lies decides
+        # which of its values are added together.)
+        check_logprobs(x, tokens, top, given=v, times=times)
 
 
 @pytest.mark.parametrize("scale", [0.25, 1.0, 3.7])

@@ -9,9 +9,10 @@
 // which no logits overflow (rows masked by the type's lowest value) and which keeps log S apart from
 // M until the end.
 //
-// Reading the logits is the bound: each value costs about eight instructions.  A block does a row; where rows are few
-// a cluster of up to eight does, and its first block adds up what the others have in their shared
-// memory.  Sums are added in a fixed order.
+// Reading the logits is the bound, each value costs about eight instructions (4096 x 131072, bf16: 161 us,
+// 6.65 TB/s).  A block does a row; where rows are many and short a warp does, and where they are few a
+// cluster of up to eight blocks, whose first adds up what the others have in their shared memory (32 x
+// 131072: 4.9 us, with 20 listed 11.1).  Sums are added in a fixed order.
 //
 // The most probable: the pass keeps the largest value of every thread, and of each of up to 16 pieces of
 // what it reads.  Of w warps, ceil(n / w) threads each reach the least of the warps' ceil(n / w)-th
@@ -26,7 +27,8 @@
 //
 // Gradient: dl_v = scale (g ([v = t] - p_v) - h p_v (log p_v + entropy) + sum_j e_j ([v = id_j] - p_v))
 // for the gradients g, h and e_j of the row's log probability, entropy and alternatives: one read and
-// one write.
+// one write are the bound (4096 x 65536, bf16, a tenth of the rows without gradients, which are not read:
+// 150 us, 6.80 TB/s; 515 x 50001, FP32: 32 us, 6.4 TB/s).
 #include <algorithm>
 #include <cstdint>
 
@@ -274,7 +276,7 @@ logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
   const int rounds = TOP ? (v1 - v0 + step - 1) / step : 0;
   const int in_piece = TOP ? max(1, (rounds + kPieces - 1) / kPieces) : 1;
   int piece = 0, left = in_piece;
-  float piece_most = -INFINITY;
+  float piece_most = -INFINITY, even = -INFINITY, odd = -INFINITY;      // (of every other vector)
   Vec<T> next[kAhead];
   fetch(v0, next);
   // Every warp makes the same number of rounds, so that its lanes stay together.
@@ -286,6 +288,13 @@ logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
     float most = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) most = fmaxf(most, max_of(v[u]));
+    if (TOP && ONE) {
+#pragma unroll
+      for (int u = 0; u < kAhead; u += 2) {
+        even = fmaxf(even, max_of(v[u]));
+        odd = fmaxf(odd, max_of(v[u + 1]));
+      }
+    }
     if (TOP) {
       piece_most = fmaxf(piece_most, most);
       piece_of[piece][threadIdx.x] = piece_most;
@@ -331,6 +340,14 @@ logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
     const int each = (p.top + warps - 1) / warps;
     const float reached = __shfl_sync(kAll, sorted_down(thread_most), each - 1);
     float bound = reached;
+    if (ONE && p.top > 20) {
+      // Many values reach the least of nearly all of a warp's maxima: 130 of any row that of 32, on the
+      // mean, and 128 have room.  Half as many of each of two maxima a thread: 50 do (8192 x 1000, 32
+      // listed, 61 and 20 us).
+      const int half = (p.top + 1) / 2;
+      bound = fminf(__shfl_sync(kAll, sorted_down(even), half - 1),
+                    __shfl_sync(kAll, sorted_down(odd), half - 1));
+    }
     if constexpr (!ONE) {
       if (lane == 0) most_of[warp] = reached;
       __syncthreads();
@@ -605,8 +622,9 @@ template <typename T>
 cudaError_t launch_logprob_as(const LogprobProblem &p, const DeviceInfo &dev, cudaStream_t stream) {
   const int64_t rounds = (p.cols / Vec<T>::kCount + kAhead - 1) / kAhead;     // of one thread
   // Short rows in numbers: a warp each (8192 rows of 1000, bf16: a block of a warp each 19 us, eight
-  // rows a block 6.4 us).
-  const bool one = rounds <= 4 * 32 && p.rows >= 8 * dev.sm_count;
+  // rows a block 6.4 us; of 8000, no or 5 listed: 38 and 56 by blocks, 27 and 40 by warps, but 2000 rows
+  // with 20 listed 19 and 22).
+  const bool one = rounds <= (p.top <= 16 ? 256 : 128) && p.rows >= 8 * dev.sm_count;
   // With alternatives smaller blocks, whose selections come more evenly (20 listed: 2000 x 8000, bf16, 25
   // and 20 us, 4096 x 32768 81 and 72, but 4096 x 131072 213 and 228).
   const bool small = p.top && rounds <= 4 * kMaxThreads && p.rows >= 4 * dev.sm_count;
