@@ -147,10 +147,11 @@ def logprob_bounds(out, mean, square, log_s, cols):
 
     A term e^t: its argument is two roundings off (of the difference and of the product with c, whose
     own rounding is a third), 3 |t| half steps, and the exponential is within 2^-22.  Sums: a thread
-    adds at most cols / 512 + 32 terms (16 a round of 4 vectors, 8192 columns a round), and 40 more
-    join threads, warps and blocks.
+    of a block adds at most cols / 512 + 32 terms (16 a round of 4 vectors, 8192 columns a round), one
+    of the warp that does a row alone, of up to 8192 columns, cols / 64 + 32 (1024 columns a round); and
+    40 more join threads, warps and blocks.
     """
-    depth = cols / 512 + 72
+    depth = (cols / 64 if cols <= 8192 + 15 else cols / 512) + 72
     s_err = depth * STEP + 3 * mean * STEP + 2.0 ** -22
     w_err = mean * (depth * STEP + 2.0 ** -22) + 4 * square * STEP
     log_err = s_err + 2 * STEP * (1 + log_s.abs())

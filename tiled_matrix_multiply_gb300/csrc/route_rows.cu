@@ -11,8 +11,8 @@
 //
 // A warp does a row, all of whose values stay in registers: with G groups rounded up to a power of
 // two every group has 32 / G lanes, so that a group's best are a butterfly within its lanes.  The
-// choice is k + 1 rounds of one warp reduction over keys that hold a value and its number.  About 600
-// instructions a row of 256, in chains of reductions and shuffles, are the bound (16384 rows of 256 FP32
+// choice is k + 1 rounds of one warp reduction over keys that hold a value and its number.  The instructions
+// of a row (950 at 256 experts in 8 groups), in chains of reductions and shuffles, are the bound (16384 rows of 256 FP32
 // logits, k = 8: plain 14.4 us, sigmoids and a bias 18, in 8 groups 23; reading takes 2.7).  Neither more
 // rows in flight (40 or 48 warps an SM: within 2 us, either way) nor blocks of another size help (one or
 // two rows a block: 8 experts 17 and 9 us in place of 7; eight: the same).
