@@ -650,10 +650,12 @@ int logprob_rows(int dtype, int64_t rows, int64_t cols, const void *logits, int6
  *   dlogits[r, v] = scale (g ([v = t] - p_v) - h p_v (log p_v + H) + sum_j e_j ([v = id_j] - p_v)),
  * t = tokens[r] (outside [0, cols): no such term), g = dlogprob[r], h = dentropy[r], H = entropy[r],
  * e_j = dtop[r, j], id_j = top_ids[r, j] (outside [0, cols): no such term), p_v = e^(x - lse[r]).
- * lse, entropy and top_ids as logprob_rows gave them.  dlogprob (with tokens), dentropy (with
- * entropy) and, by top = 0, dtop may be left out (NULL).  A row without gradients, or with nothing
- * visible (lse = -inf), gets zeros, whatever its logits.  dlogits: of the logits' type, every entry
- * written, rounded once; it may be logits itself (with ldd == ld).  Otherwise as logprob_rows.
+ * lse, entropy and top_ids as logprob_rows gave them.  p_v is right to about 2^-24 |lse| of itself, as
+ * lse is FP32: a row of nothing but FP32's lowest value, which its lse then is, has p_v = 1.  dlogprob
+ * (with tokens), dentropy (with entropy) and, by top = 0, dtop may be left out (NULL).  A row without
+ * gradients, or with nothing visible (lse = -inf), gets zeros, whatever its logits.  dlogits: of the
+ * logits' type, every entry written, rounded once; it may be logits itself (with ldd == ld).
+ * Otherwise as logprob_rows.
  */
 int logprob_rows_grad(int dtype, int64_t rows, int64_t cols, const void *logits, int64_t ld,
                       float scale, const float *lse, const void *tokens, int token_bits,

@@ -340,3 +340,29 @@ def test_results_past_two_billion_values():
     tmm.gemm_bias_act(x, w, residual=y, y=y)
     assert bool((y[-1] == 9).all()) and bool((y[-2] == 1).all()) and bool((y[0] == 1).all())
     tmm.check_device()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_calls_at_once(dtype):
+    """The same calls on several streams, each with its own workspace, give the same bits."""
+    shapes = [(1, 2048, 1030), (40, 1030, 520), (300, 512, 512)]
+    data = [(normals(1, M, K).to(dtype).cuda(), normals(2, K, N).to(dtype).cuda(),
+             normals(3, M, N).to(dtype).cuda()) for M, K, N in shapes]
+
+    def work(stream=None):
+        out = []
+        for x, w, dy in data:
+            y, z = tmm.gemm_bias_act(x, w, act="gelu", pre=True, stream=stream)
+            out += [y, z, *tmm.gemm_bias_act_grad(dy, x, w, pre=dy, act="gelu", dbias=True,
+                                                  stream=stream)]
+        return out
+
+    want = work()
+    streams = [torch.cuda.Stream() for _ in range(5)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [work(s) for _ in range(4) for s in streams]
+    torch.cuda.synchronize()
+    for out in got:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    tmm.check_device()
