@@ -11,11 +11,12 @@
 //
 // A warp does a row, all of whose values stay in registers: with G groups rounded up to a power of
 // two every group has 32 / G lanes, so that a group's best are a butterfly within its lanes.  The
-// choice is k + 1 rounds of one warp reduction over keys that hold a value and its number.  The instructions
-// of a row (950 at 256 experts in 8 groups), in chains of reductions and shuffles, are the bound (16384 rows of 256 FP32
-// logits, k = 8: plain 14.4 us, sigmoids and a bias 18, in 8 groups 23; reading takes 2.7).  Neither more
-// rows in flight (40 or 48 warps an SM: within 2 us, either way) nor blocks of another size help (one or
-// two rows a block: 8 experts 17 and 9 us in place of 7; eight: the same).
+// choice is k + 1 rounds of one warp reduction over keys that hold a value and its number.  The
+// instructions of a row (900 at 256 experts in 8 groups), in chains of reductions and shuffles, are the
+// bound (16384 rows of 256 FP32 logits, k = 8: plain 14 us, sigmoids and a bias 17, in 8 groups 21 to
+// 23; reading takes 2.7).  Neither more rows in flight (40 or 48 warps an SM: within 2 us, either way)
+// nor blocks of another size help (one or two rows a block: 8 experts 17 and 9 us in place of 7; eight:
+// the same).
 // Gradient: w depends on the chosen logits alone, but for the softmax without renormalisation;
 // rows are written whole, 16 bytes a lane, and the chosen few again (16384 x 256: 6.6 us; writing and
 // reading take 2.8, a block every four rows most of the rest).
@@ -53,11 +54,13 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
-// For the choice, which allows for errors of 2^-20: the hardware's exponential and quotient.
+// For the choice, which allows for errors of 2^-20: the hardware's power of two and reciprocal.
+__device__ __forceinline__ float near_exp(float t) { return exp2_approx(t * kLog2e); }
 __device__ __forceinline__ float near_sigmoid(float l) {
-  return __fdividef(1.0f, 1.0f + __expf(-l));
+  float s;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + near_exp(-l)));
+  return s;
 }
-__device__ __forceinline__ float near_exp(float t) { return __expf(t); }
 
 // ---- pairs of FP32 values --------------------------------------------------------------------
 //
@@ -182,8 +185,8 @@ struct Lane {
 template <bool VEC, int V>
 __device__ __forceinline__ Lane<VEC> lane_of(const RouteProblem &p, int lane) {
   Lane<VEC> a;
-  a.group = lane / p.lanes;
-  const int sub = lane - a.group * p.lanes;
+  a.group = lane >> p.lanes_log2;
+  const int sub = lane & (p.lanes - 1);
   a.stride = p.lanes;
   a.sub = VEC ? sub * V : sub;
   a.first = a.group * p.group_size + a.sub;
@@ -702,6 +705,8 @@ cudaError_t launch_route_as(RouteProblem p, cudaStream_t stream) {
   while (across < p.groups) across *= 2;
   p.group_size = p.experts / p.groups;
   p.lanes = 32 / across;
+  p.lanes_log2 = 0;
+  while (1 << p.lanes_log2 < p.lanes) ++p.lanes_log2;
   const int need = (p.group_size + p.lanes - 1) / p.lanes;      // at most 32
   int V = 1;
   while (V < need) V *= 2;

@@ -25,7 +25,7 @@ struct RouteProblem {
   float scale;
   int32_t *chosen;              // tokens x k
   float *weights;               // tokens x k
-  int group_size, lanes, vec_bias;      // set by the launcher: lanes of a group, 16-byte loads
+  int group_size, lanes, lanes_log2, vec_bias;      // set by the launcher: lanes of a group, 16-byte loads
 };
 struct RouteGradProblem {
   int dtype;
