@@ -121,6 +121,17 @@ def test_route_pairs_closer_than_single_precision_tells(score, E, groups, k, at)
                 group_best=min(groups, 2))
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [1.0, 100.0, 5000.0])
+def test_route_groups_of_large_biases_that_cancel(score, size):
+    """The groups' values are small sums of large c, whose roundings are of the size of the differences."""
+    x = normals(11, 500, 32, std=size * 2e-6)
+    bias = torch.tensor([size, -size, -4 * size, -5 * size]).repeat(8)
+    check_route(x, 2, bias, score=score, groups=8, top_groups=3, group_best=2)
+    check_route(x, 5, bias * (1 + torch.arange(32) // 4 % 2), score=score, groups=8, top_groups=3,
+                group_best=2)
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_masked_experts(dtype, score):

@@ -216,16 +216,17 @@ __device__ __forceinline__ void load_bias(const RouteProblem &p, const Lane<VEC>
 }
 
 // In 32 bits, the scores c of this lane's experts (the logits without a bias) and which of them may be
-// chosen; m: the row's maximum, where the scores are the softmax's.  Returns what two
-// scores may be off by together: of the sigmoids, e^-l by 2^-21 of itself (times s (1 - s)) and the
-// quotient by 2^-22; of the softmax, every term by 2^-21, their sum by as many half steps as it has
-// additions (at most 37), in all 2^-18 of the two scores, which are 1 / sum at most each.
+// chosen; m: the row's maximum, where the scores are the softmax's.  Returns what two scores may be off
+// by together: of the sigmoids, e^-l by 2^-22.5 and |l| 2^-23.4 of itself (times s (1 - s), and
+// |l| s (1 - s) < 0.225), 1 + e^-l by 2^-24 and the reciprocal by 2^-23, in all 2.4e-7 each; of the
+// softmax, every term by 2^-21, their sum by as many half steps as it has additions (at most 37), in all
+// 2^-18 of the two scores, which are 1 / sum at most each.
 template <bool VEC, int V>
 __device__ __forceinline__ float make_scores(const RouteProblem &p, const Lane<VEC> &a,
                                              const float (&l)[V], float (&c)[V], bool (&on)[V],
                                              float &m) {
   const float *const bias = p.bias;
-  float error = 0x1p-20f;
+  float error = 0x1.2p-21f;
   m = 0;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -303,7 +304,10 @@ __device__ __forceinline__ bool group_open(const RouteProblem &p, const Lane<VEC
     const uint32_t lo = __reduce_min_sync(kAll, open ? key : ~0u);
     const uint32_t hi = __reduce_max_sync(kAll, open ? 0u : key);
     const float x = value_of(lo), y = value_of(hi);
-    const float tol = bias ? 2.0f * error + 0x1p-21f * fabsf(y) : 0x1p-16f * y + 1e-37f;
+    // With a bias: the scores' errors, and half a step of each of four c and of two sums of them, which
+    // may be far smaller than the c.  Without, a score of e^-87 is off by 87 2^-23.4 of itself.
+    const float size = any && bias ? fabsf(one) + (fabsf(two) < INFINITY ? fabsf(two) : 0.0f) : 0.0f;
+    const float tol = bias ? 2.0f * error + 0x1p-22f * warp_max(size) : 0x1p-15f * y + 1e-37f;
     close |= hi != 0 && x - y <= tol;
   }
   return open;
