@@ -1,6 +1,10 @@
 """A run of the operators together, as a model uses them: a layer of routed experts with a dense
 projection, and an output layer whose log probabilities are learned; forward and backward against
 autograd in 64 bits on the same (rounded) values, and a step captured into a graph."""
+import pathlib
+import subprocess
+import sys
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -94,6 +98,32 @@ def test_single_tokens(T):
         assert torch.equal(one.experts, r.experts[rows]) and torch.equal(one.weights,
                                                                          r.weights[rows])
         assert torch.equal(tmm.logprob_rows(logits[rows], top=2).top_ids, lp.top_ids[rows])
+
+
+FIRST = """
+import torch, tiled_matrix_multiply_gb300 as tmm
+x, w = torch.ones(200, 64, device="cuda"), torch.ones(64, 96, device="cuda")
+tokens = torch.zeros(200, dtype=torch.int64, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    r = tmm.route_rows(x, 4)
+    few = tmm.gemm_bias_act(x[:3], w)
+    y, z = tmm.gemm_bias_act(x.half(), w.half(), act="relu", pre=True)
+    g = tmm.gemm_bias_act_grad(y, x.half(), w.half(), pre=z, act="relu", dbias=True)
+    p = tmm.logprob_rows(x, tokens, top=2)
+graph.replay()
+torch.cuda.synchronize()
+tmm.check_device()
+assert r.experts[0].tolist() == [0, 1, 2, 3] and bool((few == 64).all()) and bool((y == 64).all())
+assert bool((g.dx == 64 * 96).all()) and bool((g.dbias == 64 * 200).all())
+assert p.top_ids[0].tolist() == [0, 1]
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    subprocess.run([sys.executable, "-c", FIRST], check=True, timeout=300,
+                   cwd=pathlib.Path(tmm.__file__).parents[1])
 
 
 def test_the_example_runs(capsys, monkeypatch):

@@ -29,7 +29,9 @@ struct SlopeParams {
   int planes;           // FP32: dz as its three bf16 parts, planes rows * ldz apart
 };
 
-// Lane l has columns first + l W .. + W (VEC), or first + l, + 32, ...: 16 bytes' worth.
+// Lane l has columns first + l W .. + W, 16 bytes' worth, read as vectors (VEC) or one by one; dz's rows
+// are vectors in any case, whose last may have values past N that nothing reads (4096 x 4095, bf16, with
+// the sums: 34 us where values are read and written one by one with 32 lanes side by side, 26 so).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps)
 slopes_kernel(const __grid_constant__ SlopeParams p) {
@@ -39,7 +41,7 @@ slopes_kernel(const __grid_constant__ SlopeParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t first = int64_t(blockIdx.x) * 32 * W;
   const int64_t r0 = blockIdx.y * p.run, r1 = min(r0 + p.run, p.rows);
-  const auto column = [&](int k) { return first + (VEC ? lane * W + k : lane + 32 * k); };
+  const auto column = [&](int k) { return first + lane * W + k; };
   const auto load = [&](const void *m, int64_t ld, int64_t row, Vec<T> &v) {
     const T *const from = static_cast<const T *>(m) + row * ld;
     if (VEC) {
@@ -84,17 +86,10 @@ slopes_kernel(const __grid_constant__ SlopeParams p) {
 #pragma unroll
           for (int k = 0; k < W / 2; ++k) split2(of_pair(d[k]).x, of_pair(d[k]).y, h[k]);
 #pragma unroll
-          for (int pl = 0; pl < 3; ++pl) {
-            uint16_t *const plane = to + pl * p.rows * p.ldz;
-            if (VEC) {
-              if (column(0) < p.N)
-                *reinterpret_cast<uint2 *>(plane + column(0)) = make_uint2(h[0][pl], h[1][pl]);
-            } else {
-#pragma unroll
-              for (int k = 0; k < W; ++k)
-                if (column(k) < p.N) plane[column(k)] = uint16_t(h[k >> 1][pl] >> (16 * (k & 1)));
-            }
-          }
+          for (int pl = 0; pl < 3; ++pl)
+            if (column(0) < p.N)
+              *reinterpret_cast<uint2 *>(to + pl * p.rows * p.ldz + column(0)) =
+                  make_uint2(h[0][pl], h[1][pl]);
           continue;
         }
       Vec<T> out;
@@ -104,20 +99,14 @@ slopes_kernel(const __grid_constant__ SlopeParams p) {
         out.set(2 * k + 1, of_pair(d[k]).y);
       }
       T *const to = static_cast<T *>(p.dz) + row * p.ldz;
-      if (VEC) {
-        if (column(0) < p.N) *reinterpret_cast<uint4 *>(to + column(0)) = out.w;
-      } else {
-#pragma unroll
-        for (int k = 0; k < W; ++k)
-          if (column(k) < p.N) to[column(k)] = reinterpret_cast<const T *>(&out.w)[k];
-      }
+      if (column(0) < p.N) *reinterpret_cast<uint4 *>(to + column(0)) = out.w;
     }
   }
   if (p.sums == nullptr) return;
 #pragma unroll
   for (int k = 0; k < W; ++k) {
     const float2 f = of_pair(sum[k >> 1]);
-    part[warp][VEC ? lane * W + k : lane + 32 * k] = k & 1 ? f.y : f.x;
+    part[warp][lane * W + k] = k & 1 ? f.y : f.x;
   }
   __syncthreads();
   for (int c = threadIdx.x; c < 32 * W; c += 32 * kWarps) {
@@ -176,8 +165,7 @@ cudaError_t launch_as(const LinearGradProblem &g, void *dz, int64_t ldz, bool pl
   p.run = (g.rows + runs - 1) / runs;
   p.sums = g.dbias == nullptr ? nullptr : runs > 1 ? partial : g.dbias;
   const bool vec = g.N * size % 16 == 0 && aligned(p.dy, p.lddy, size) &&
-                   (p.pre == nullptr || aligned(p.pre, p.ld_pre, size)) &&
-                   (dz == nullptr || aligned(dz, ldz, planes ? 2 : size));
+                   (p.pre == nullptr || aligned(p.pre, p.ld_pre, size));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
