@@ -121,6 +121,19 @@ def test_route_pairs_closer_than_single_precision_tells(score, E, groups, k, at)
                 group_best=min(groups, 2))
 
 
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_route_groups_of_equal_sums_go_to_the_lower_number(dtype, bias):
+    """Every group has s(l) + s(-l) = 1, of other l."""
+    l = normals(3, 300, 8, dtype=torch.float32).abs().to(dtype)
+    x = torch.stack([l, -l, torch.full_like(l, -30.0)], 2)
+    x[::2] = x[::2].flip(2)
+    b = torch.zeros(24, device="cuda") if bias else None
+    r = tmm.route_rows(x.view(300, 24).cuda(), 9, bias=b, score="sigmoid", groups=8, top_groups=3,
+                       group_best=2)
+    assert torch.equal(r.experts.cpu().sort(1).values, torch.arange(9).expand(300, 9).int())
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("size", [1.0, 100.0, 5000.0])
 def test_route_groups_of_large_biases_that_cancel(score, size):

@@ -126,6 +126,11 @@ __device__ __forceinline__ uint64_t key_of(Two v) {
 __device__ __forceinline__ Two value_of(uint64_t key) {
   return {value_of(uint32_t(key >> 32)), value_of(uint32_t(key))};
 }
+// To 44 bits, so that sums which are equal in the mathematics (of s(l) and s(-l)) are equal.
+__device__ __forceinline__ Two shortened(Two v) {
+  const float c = 1.5f * 0x1p-20f * __uint_as_float(__float_as_uint(v.h) & 0x7F800000u);
+  return {v.h, __fsub_rn(__fadd_rn(v.l, c), c)};
+}
 __device__ __forceinline__ uint64_t more(uint64_t a, uint64_t b) { return a > b ? a : b; }
 __device__ __forceinline__ uint64_t less(uint64_t a, uint64_t b) { return a > b ? b : a; }
 
@@ -497,7 +502,7 @@ __device__ __noinline__ int choose_again(const RouteProblem &p, int64_t row) {
         x = f.v[0];
         y = f.v[1];
       }
-      const Two s = x + y;
+      const Two s = shortened(x + y);
       value = key_of(fabsf(x.h + y.h) < INFINITY ? s : Two{x.h + y.h, 0.0f});
     } else if (p.best == 2 && one != 0 && !p.bias) {
       value = key_of(scores_of(value_of(one).h, 0.0f, 0.0f, 0.0f, m, p.sigmoid).v[0]);
