@@ -594,10 +594,11 @@ size_t gemm_bias_act_grad_workspace_size(int dtype, int transw, int act, int64_t
  *   - weights[t, j] = scale s_j / (the sum of the chosen s), or (renormalise = 0) scale s_j.
  * The choice is that of the scores to 43 bits (those below 2^-126 count as 0); without a bias it is
  * the logits' own order.  The renormalised weights do not underflow: they are right where every score
- * is below FP32's range.  An expert whose logit or bias is -inf is never chosen; where fewer than k are left (none, in a row of
- * padding), the last chosen are -1 with weight 0, slots of no group for group_rows.  A row with NaN,
- * or under the softmax with +inf, at an expert whose bias is not -inf has NaN weights, and chooses some
- * k experts, each once.
+ * is below FP32's range.  An expert whose logit or bias is -inf is never chosen; where fewer than k are
+ * left (none, in a row of padding), the last chosen are -1 with weight 0, slots of no group for
+ * group_rows.  Under the softmax, which is over all experts, a row with NaN or +inf has NaN weights,
+ * at an expert whose bias is -inf too; under sigmoids a row with NaN at an expert whose bias is not
+ * -inf.  Such a row chooses some k of the experts that may be chosen, each once.
  * logits: DEVICE, tokens x experts, row stride ld >= experts; chosen, weights: tokens x k, contiguous.
  * 1 <= experts <= 512, groups <= 32 dividing experts, k <= 16 and <= the experts of top_groups
  * groups, tokens below 2^29.  tokens == 0 is a no-op.  Outputs must not overlap inputs or each

@@ -1,0 +1,46 @@
+"""Rows of scores with NaN and infinities where no result seems to need them."""
+import itertools
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import tiled_matrix_multiply_gb300 as tmm  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+INF, NAN = math.inf, math.nan
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from tiled_matrix_multiply_gb300 import build
+    build.build()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("odd", [NAN, INF])
+@pytest.mark.parametrize("E,shut", [(64, 63), (64, 0), (60, 17), (512, 300)])
+def test_route_odd_logits_of_experts_shut_by_their_bias(dtype, odd, E, shut):
+    """The softmax is over all experts, so that its scores are NaN; a sigmoid is the expert's own."""
+    gen = torch.Generator().manual_seed(E + shut)
+    x = torch.randn(5, E, generator=gen).to(dtype)
+    x[::2, shut] = odd
+    bias = torch.randn(E, generator=gen) * 0.1
+    bias[shut] = -INF
+    clean = x.clone()
+    clean[:, shut] = 0.0
+    for groups, best, renormalise in itertools.product((1, 4), (1, 2), (True, False)):
+        how = dict(bias=bias.cuda(), groups=groups, top_groups=max(1, groups // 2),
+                   group_best=best, renormalise=renormalise)
+        r = tmm.route_rows(x.cuda(), 4, score="softmax", **how)
+        assert bool(r.weights[::2].isnan().all()), (groups, best, renormalise)
+        assert bool(r.weights[1::2].isfinite().all())
+        for row in r.experts.tolist():
+            assert len(set(row)) == 4 and shut not in row and all(0 <= e < E for e in row)
+        r = tmm.route_rows(x.cuda(), 4, score="sigmoid", **how)
+        want = tmm.route_rows(clean.cuda(), 4, score="sigmoid", **how)
+        assert torch.equal(r.experts, want.experts) and torch.equal(r.weights, want.weights)

@@ -481,7 +481,8 @@ __device__ __noinline__ int choose_again(const RouteProblem &p, int64_t row) {
   bool bad = false;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    bad |= b[v] != -INFINITY && (l[v] != l[v] || (!p.sigmoid && l[v] == INFINITY));
+    // (Of the softmax any expert's logit makes every score NaN, whatever its bias.)
+    bad |= p.sigmoid ? l[v] != l[v] && b[v] != -INFINITY : l[v] != l[v] || l[v] == INFINITY;
     key[v] = l[v] == -INFINITY || b[v] == -INFINITY ? 0 : key_of(c[v]);
     second = more(second, less(best, key[v]));
     best = more(best, key[v]);
