@@ -561,8 +561,9 @@ size_t gemm_bias_act_workspace_size(int dtype, int transw, int64_t M, int64_t N,
  * the gradient of the residual is dy itself.  Any of dx (M x K), dw (K x N, or with transdw = 1
  * stored N x K) and dbias (N FP32) may be NULL.  pre as gemm_bias_act kept it (act none: may be
  * NULL).  dz is FP32 in dbias; in the products it is rounded to the operands' type first, as a
- * layer of its own would hand it on: for sums of many terms that adds about as much to a result's
- * error as the result's own rounding.  relu'(0) = 0.  x is read for dw alone, w for dx alone.
+ * layer of its own would hand it on (in FP16 without that type's range: to eleven bits, and to 2^-39 of
+ * the largest finite |dy|): for sums of many terms that adds about as much to a result's error as the
+ * result's own rounding.  relu'(0) = 0.  x is read for dw alone, w for dx alone.
  */
 int gemm_bias_act_grad(int dtype, int transw, int act, int64_t M, int64_t N, int64_t K,
                        const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *w,

@@ -92,6 +92,7 @@ struct DenseParams {
   void *out;
   int64_t ld_out;
   int vec_out;             // everything of the result's shape on 16-byte rows
+  const float *unscale;    // FP16: what the sums are multiplied by, or NULL
   const void *bias;
   int bias_f32, act;
   const void *residual;
@@ -115,6 +116,16 @@ __device__ __forceinline__ DenseTile tile_at(const DenseParams &p, int t, int la
 
 // ---- results: z = sum + bias, y = act(z) + residual ------------------------------------------
 
+// Sums of an operand that was kept times a power of two (see linear_slopes.cu).
+template <int KIND>
+__device__ __forceinline__ float unscale_of(const DenseParams &p) {
+  return KIND == kF16 && p.unscale ? *p.unscale : 1.0f;
+}
+template <int KIND>
+__device__ __forceinline__ uint64_t with_bias(uint64_t sum, float unscale, float bias) {
+  if (KIND == kF16) return fma2(sum, both(unscale), both(bias));
+  return add2(sum, both(bias));
+}
 template <int KIND>
 __device__ __forceinline__ float bias_at(const DenseParams &p, int n) {
   if (p.bias == nullptr || n >= p.N) return 0.0f;
@@ -205,7 +216,7 @@ __device__ __forceinline__ void finish_four(const DenseParams &p, int64_t row, i
 // each lane: a warp writes 32 neighbours of a row.
 template <int KIND>
 __device__ __forceinline__ void finish_lanes(const DenseParams &p, int64_t row0, int count, int n,
-                                             const float (&v)[16], float bias) {
+                                             const float (&v)[16], float unscale, float bias) {
   using T = typename Kind<KIND>::T;
   if (n >= p.N) return;
   float r[16];
@@ -217,7 +228,8 @@ __device__ __forceinline__ void finish_lanes(const DenseParams &p, int64_t row0,
     r[j] = p.residual && j < count ? float(residual[j * p.ld_residual]) : 0.0f;
   uint64_t z[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) z[j] = add2(pair_of(v[2 * j], v[2 * j + 1]), both(bias));
+  for (int j = 0; j < 8; ++j)
+    z[j] = with_bias<KIND>(pair_of(v[2 * j], v[2 * j + 1]), unscale, bias);
   if (p.pre) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
@@ -331,8 +343,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int64_t
 // values staged in FP32 took 260.
 template <int KIND>
 __device__ __forceinline__ void finish_block(const DenseParams &p, int64_t row0, int nw,
-                                             const uint32_t (&f)[2][8], const float (&bias)[4],
-                                             const uint4 (&residual)[2], uint32_t stage) {
+                                             const uint32_t (&f)[2][8], float unscale,
+                                             const float (&bias)[4], const uint4 (&residual)[2], uint32_t stage) {
   const int lane = threadIdx.x & 31;
   const auto piece = [&](uint32_t at, int row, int c) {      // free of bank conflicts
     return at + uint32_t(row * 64 + ((c ^ (row >> 1 & 3)) << 4));
@@ -342,9 +354,9 @@ __device__ __forceinline__ void finish_block(const DenseParams &p, int64_t row0,
   for (int c = 0; c < 2; ++c)
 #pragma unroll
     for (int m = 0; m < 4; ++m)
-      z[c][m] = add2(pair_of(__uint_as_float(f[m >> 1][4 * c + 2 * (m & 1)]),
-                             __uint_as_float(f[m >> 1][4 * c + 2 * (m & 1) + 1])),
-                     both(bias[m]));
+      z[c][m] = with_bias<KIND>(pair_of(__uint_as_float(f[m >> 1][4 * c + 2 * (m & 1)]),
+                                        __uint_as_float(f[m >> 1][4 * c + 2 * (m & 1) + 1])),
+                                unscale, bias[m]);
   __syncwarp();      // the reads of the block before are done
   if (p.residual) {
 #pragma unroll
@@ -597,6 +609,7 @@ dense_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
     const uint32_t stage = out_stage + uint32_t(warp - kEpi0) * D::kOutStage;
     float *const parts = reinterpret_cast<float *>(smem_raw + (base - raw));
     const bool split = p.ksplit > 1;
+    const float unscale = unscale_of<KIND>(p);
     // Waits for the next sum, and hands it back.
     const auto ready = [&] {
       const bool ok = mbar_wait(bar_tfull + 8 * (q & 1), (q >> 1) & 1u, p.wait_limit_ns);
@@ -621,7 +634,7 @@ dense_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
           for (int j = 0; j < 16; ++j) parts[(c0 + j) * 128 + 32 * quarter + lane] = v[j];
         } else if (c0 < left) {
           finish_lanes<KIND>(p, tile.q0 + c0, min(16, left - c0), nw + lane, v,
-                             bias_at<KIND>(p, nw + lane));
+                             unscale, bias_at<KIND>(p, nw + lane));
         }
       };
       if (!D::kSplit && sums == 1 && n > 0) {
@@ -652,7 +665,7 @@ dense_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
             load_residual(c0 + 4 * kEpiWarps, next);
             tmem_wait(f[0], f[1]);
             if constexpr (!D::kSplit)
-              finish_block<KIND>(p, tile.q0 + c0, nw, f, bias, residual, stage);
+              finish_block<KIND>(p, tile.q0 + c0, nw, f, unscale, bias, residual, stage);
             residual[0] = next[0];
             residual[1] = next[1];
           } else {
@@ -749,12 +762,14 @@ dense_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
       float bias[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) bias[k] = bias_at<KIND>(p, n0 + k);
+      const float unscale = unscale_of<KIND>(p);
 #pragma unroll
       for (int i = 0; i < kShare; ++i) {
         const int c = c0 + (tid >> 5) + i * kEpiWarps;
         if (c >= c1) break;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) z[i][k] += bias[k];
+        for (int k = 0; k < 4; ++k)
+          z[i][k] = KIND == kF16 ? fmaf(z[i][k], unscale, bias[k]) : z[i][k] + bias[k];
         finish_four<KIND>(p, tile.q0 + c, n0, z[i]);
       }
     }
@@ -806,6 +821,7 @@ struct DenseProblem {
   DenseOperand p, q;
   void *out;
   int64_t ld_out;
+  const float *unscale;
   const void *bias;
   int bias_f32, act;
   const void *residual;
@@ -934,6 +950,7 @@ cudaError_t launch_as(const DenseProblem &g, const DenseShape &s, const DeviceIn
   p.idesc = (1u << 4) | (KIND == kF16 ? 0u : (1u << 7) | (1u << 10));
   p.out = g.out;
   p.ld_out = g.ld_out;
+  p.unscale = g.unscale;
   p.bias = g.bias;
   p.bias_f32 = g.bias_f32 || D::kSplit;
   p.act = g.act;
@@ -1005,11 +1022,11 @@ size_t sum_of(std::initializer_list<size_t> sizes) {
 }
 
 // dz in the workspace: of the type, on 16-byte rows, or (FP32) as planes.  FP32 of few rows: dx from
-// FP32 values, whose planes dw takes.
+// FP32 values, whose planes dw takes.  FP16: times a power of two, unless it is dy or 0 (relu).
 struct GradPlan {
-  bool make_dz, few, dz_planes;
+  bool make_dz, few, dz_planes, scaled;
   int64_t ldz;
-  size_t dz_bytes, partial_bytes, bytes;
+  size_t dz_bytes, unscale_bytes, partial_bytes, bytes;
 };
 // dz as a matrix of the type: what has been made at `made`, or dy itself.
 Stack dz_stack(const LinearGradProblem &p, const GradPlan &g, const void *made) {
@@ -1025,9 +1042,11 @@ GradPlan plan_grad(const LinearGradProblem &p) {
     const __int128 n = __int128(p.rows) * g.ldz * (g.dz_planes ? 6 : p.dtype == TMM_F32 ? 4 : 2);
     g.dz_bytes = n > __int128(INT64_MAX / 4) ? SIZE_MAX : round256(size_t(n));
   }
+  g.scaled = g.make_dz && p.dtype == TMM_F16 && p.act != TMM_ACT_RELU;
+  g.unscale_bytes = g.scaled ? round256(linear_unscale_bytes()) : 0;
   g.partial_bytes = p.dbias ? round256(linear_bias_bytes(p.rows, p.N, p.dtype)) : 0;
   const bool planes = p.dw || (p.dx && !g.few);
-  g.bytes = sum_of({g.dz_bytes, g.partial_bytes,
+  g.bytes = sum_of({g.dz_bytes, g.unscale_bytes, g.partial_bytes,
                     planes && !(g.make_dz && !g.few) ? planes_bytes(dz_stack(p, g, nullptr), p.dtype)
                                                      : 0,
                     p.dx && !g.few ? planes_bytes(p.w, p.dtype) : 0,
@@ -1084,8 +1103,10 @@ cudaError_t launch_linear_grad(const LinearGradProblem &p, const DeviceInfo &dev
     dz = {made, g.dz_planes ? 3 : 1, p.rows, p.N, g.ldz, p.rows * g.ldz};
     ws += g.dz_bytes;
   }
+  float *const unscale = g.scaled ? reinterpret_cast<float *>(ws) : nullptr;
+  ws += g.unscale_bytes;
   if (g.make_dz || p.dbias) {
-    e = launch_linear_slopes(p, g.make_dz ? made : nullptr, g.ldz, g.dz_planes,
+    e = launch_linear_slopes(p, g.make_dz ? made : nullptr, g.ldz, g.dz_planes, unscale,
                              reinterpret_cast<float *>(ws), dev, stream);
     if (e != cudaSuccess) return e;
   }
@@ -1118,6 +1139,7 @@ cudaError_t launch_linear_grad(const LinearGradProblem &p, const DeviceInfo &dev
   }
   DenseProblem d = {};
   d.dtype = p.dtype;
+  d.unscale = unscale;
   if (p.dx && !g.few) {
     d.M = p.rows;
     d.N = p.K;

@@ -115,10 +115,13 @@ cudaError_t launch_linear(const LinearProblem &p, const DeviceInfo &dev, void *w
 cudaError_t launch_linear_grad(const LinearGradProblem &p, const DeviceInfo &dev, void *workspace,
                                cudaStream_t stream);
 // dz (rows x N, ldz, of the type, or with `planes` an FP32 value's three bf16 parts; NULL: not written)
-// and dbias; `partial`: linear_bias_bytes of scratch.
+// and dbias; `partial`: linear_bias_bytes of scratch.  `unscale` (FP16; NULL: dz as it is):
+// linear_unscale_bytes, whose first value is left as what the written dz has to be multiplied by.
 size_t linear_bias_bytes(int64_t rows, int64_t N, int dtype);
+size_t linear_unscale_bytes();
 cudaError_t launch_linear_slopes(const LinearGradProblem &p, void *dz, int64_t ldz, bool planes,
-                                 float *partial, const DeviceInfo &dev, cudaStream_t stream);
+                                 float *unscale, float *partial, const DeviceInfo &dev,
+                                 cudaStream_t stream);
 cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void *workspace,
                            cudaStream_t stream);
 cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *workspace,

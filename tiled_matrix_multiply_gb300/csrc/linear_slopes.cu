@@ -5,8 +5,14 @@
 // vectors of columns, eight warps a row each in turn; a thread's columns are its own, so that the
 // sums stay in registers (FP32, of dz before it is rounded) until the eight warps' are added in
 // shared memory.  The runs' sums are added by a second launch: no atomics, a fixed order.
+//
+// In FP16 slopes of up to 1.13 take dy past 65504, and small dy past 2^-14 downwards, where dx and dw may
+// be neither.  So dz is kept times a power of two that brings the largest finite |dy| to between 2^14
+// and 2^15, found by a pass over dy before (peaks_kernel), and the products take it out again: dz is
+// rounded to eleven bits, and to 2^-39 of the largest |dy|.  (relu's dz is dy or 0.)
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "activation.cuh"
 #include "grouped.h"
@@ -27,18 +33,105 @@ struct SlopeParams {
   int64_t rows, N, lddy, ld_pre, ldz, run;
   int act;
   int planes;           // FP32: dz as its three bf16 parts, planes rows * ldz apart
+  const uint32_t *peaks;      // SCALED: the blocks' largest |dy|, as bits
+  int peak_count;
+  float *unscale;             // and what dz is to be multiplied by, written here
 };
+
+// Blocks of the pass over dy at most: two an SM, and no more than a block of slopes_kernel can read soon.
+constexpr int kMaxPeaks = 304;
+constexpr int kPeakStrip = 256;        // columns of a warp's load
+constexpr int kPeakAhead = 8;          // loads of a warp in flight
+
+// The largest finite |dy| of a block's strips of rows, by turns a warp each: a pass that memory bounds
+// (4096 x 4096 8 us; with loads of four rows of one strip in flight, of which there are only two, 40).  VEC:
+// rows start on 16-byte boundaries (a matrix without gaps is one row).
+template <bool VEC>
+__global__ void __launch_bounds__(32 * kWarps)
+peaks_kernel(const uint16_t *__restrict__ dy, int64_t rows, int64_t N, int64_t ld, int64_t strips,
+             int64_t down, int64_t across, uint32_t *__restrict__ peaks) {
+  constexpr int W = kPeakStrip / 32;
+  __shared__ uint32_t part[kWarps];
+  wait_then_start_next();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // Strip s of row r; the warp's next is `down` rows and `across` strips on.
+  const int64_t start = int64_t(blockIdx.x) * kWarps + warp;
+  int64_t r = start < strips ? 0 : start / strips, s = start - r * strips;
+  uint32_t most = 0;      // of the even and the odd columns
+  while (r < rows) {
+    uint4 v[kPeakAhead];
+#pragma unroll
+    for (int u = 0; u < kPeakAhead; ++u) {
+      // (Single values are read with the lanes side by side.)
+      const int64_t c = s * kPeakStrip + (VEC ? lane * W : lane);
+      const uint16_t *const from = dy + r * ld + c;
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (VEC && r < rows && c + W <= N) {
+        v[u] = __ldg(reinterpret_cast<const uint4 *>(from));
+      } else {
+        constexpr int kNext = VEC ? 1 : 32;
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+          if (r < rows && c + kNext * k < N)
+            reinterpret_cast<uint16_t *>(&v[u])[k] = __ldg(from + kNext * k);
+      }
+      r += down;
+      if ((s += across) >= strips) {
+        s -= strips;
+        ++r;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kPeakAhead; ++u) {
+      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        // Infinities and NaN, 0x7C00 and more without their signs, are left out.
+        const uint32_t size = w[k] & 0x7FFF7FFFu, out = (size + 0x04000400u) & 0x80008000u;
+        most = __vmaxu2(most, size & ~(out | (out - (out >> 15))));
+      }
+    }
+  }
+  most = __reduce_max_sync(~0u, max(most & 0xFFFFu, most >> 16));
+  if (lane == 0) part[warp] = most;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kWarps; ++w) most = max(most, part[w]);
+    peaks[blockIdx.x] = most;
+  }
+}
+
+// The power of two that brings the FP16 value of these bits to between 2^14 and 2^15 (1 for 0): 2^-1 to
+// 2^38.
+__device__ __forceinline__ float scale_of(uint32_t bits) {
+  const int power = bits >> 10 ? int(bits >> 10) - 15 : 31 - __clz(int(bits)) - 24;
+  return bits == 0 ? 1.0f : __int_as_float((14 - power + 127) << 23);
+}
 
 // Lane l has columns first + l W .. + W, 16 bytes' worth, read as vectors (VEC) or one by one; dz's rows
 // are vectors in any case, whose last may have values past N that nothing reads (4096 x 4095, bf16, with
 // the sums: 34 us where values are read and written one by one with 32 lanes side by side, 26 so).
-template <typename T, bool VEC>
+// SCALED: dz times a power of two (FP16).
+template <typename T, bool VEC, bool SCALED>
 __global__ void __launch_bounds__(32 * kWarps)
 slopes_kernel(const __grid_constant__ SlopeParams p) {
   constexpr int W = Vec<T>::kCount;
   __shared__ float part[kWarps][32 * W];
   wait_then_start_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t scale = 0;
+  if constexpr (SCALED) {
+    __shared__ uint32_t peak[kWarps];
+    uint32_t most = 0;
+    for (int i = threadIdx.x; i < p.peak_count; i += 32 * kWarps) most = max(most, p.peaks[i]);
+    most = __reduce_max_sync(~0u, most);
+    if (lane == 0) peak[warp] = most;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) most = max(most, peak[w]);
+    const float f = scale_of(most);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.unscale = 1.0f / f;
+    scale = both(f);
+  }
   const int64_t first = int64_t(blockIdx.x) * 32 * W;
   const int64_t r0 = blockIdx.y * p.run, r1 = min(r0 + p.run, p.rows);
   const auto column = [&](int k) { return first + lane * W + k; };
@@ -95,6 +188,7 @@ slopes_kernel(const __grid_constant__ SlopeParams p) {
       Vec<T> out;
 #pragma unroll
       for (int k = 0; k < W / 2; ++k) {
+        if constexpr (SCALED) d[k] = mul2(d[k], scale);
         out.set(2 * k, of_pair(d[k]).x);
         out.set(2 * k + 1, of_pair(d[k]).y);
       }
@@ -149,7 +243,7 @@ bool aligned(const void *p, int64_t ld, int64_t size) {
 
 template <typename T>
 cudaError_t launch_as(const LinearGradProblem &g, void *dz, int64_t ldz, bool planes,
-                      float *partial, cudaStream_t stream) {
+                      float *unscale, float *partial, cudaStream_t stream) {
   const int64_t size = sizeof(T), runs = runs_of(g.rows, g.N, g.dtype);
   SlopeParams p = {};
   p.dy = g.dy.data;
@@ -171,13 +265,31 @@ cudaError_t launch_as(const LinearGradProblem &g, void *dz, int64_t ldz, bool pl
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   const int64_t strip = 32 * Vec<T>::kCount;
-  cfg.gridDim = dim3(unsigned((g.N + strip - 1) / strip), unsigned(runs), 1);
   cfg.blockDim = dim3(32 * kWarps, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e =
-      cudaLaunchKernelEx(&cfg, vec ? slopes_kernel<T, true> : slopes_kernel<T, false>, p);
+  cudaError_t e;
+  if (unscale) {
+    uint32_t *const peaks = reinterpret_cast<uint32_t *>(unscale) + 1;
+    const bool flat = p.lddy == g.N || g.rows == 1;
+    const int64_t rows = flat ? 1 : g.rows, N = flat ? g.rows * g.N : g.N;
+    const int64_t strips = (N + kPeakStrip - 1) / kPeakStrip;
+    p.peaks = peaks;
+    p.peak_count = int(std::min<int64_t>(kMaxPeaks, (rows * strips + kWarps - 1) / kWarps));
+    p.unscale = unscale;
+    const int64_t step = int64_t(p.peak_count) * kWarps, down = step / strips;
+    cfg.gridDim = dim3(unsigned(p.peak_count), 1, 1);
+    const auto kernel = aligned(p.dy, flat ? 0 : p.lddy, 2) ? peaks_kernel<true> : peaks_kernel<false>;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const uint16_t *>(p.dy), rows, N, p.lddy,
+                                strips, down, step - down * strips, peaks)) != cudaSuccess)
+      return e;
+  }
+  cfg.gridDim = dim3(unsigned((g.N + strip - 1) / strip), unsigned(runs), 1);
+  auto kernel = vec ? slopes_kernel<T, true, false> : slopes_kernel<T, false, false>;
+  if constexpr (std::is_same_v<T, __half>)
+    if (unscale) kernel = vec ? slopes_kernel<T, true, true> : slopes_kernel<T, false, true>;
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess || g.dbias == nullptr || runs == 1) return e;
   cfg.gridDim = dim3(unsigned((g.N + 31) / 32), 1, 1);
   cfg.blockDim = dim3(256, 1, 1);
@@ -192,11 +304,15 @@ size_t linear_bias_bytes(int64_t rows, int64_t N, int dtype) {
   return runs > 1 ? size_t(runs) * size_t(N) * sizeof(float) : 0;
 }
 
+size_t linear_unscale_bytes() { return sizeof(uint32_t) * (1 + kMaxPeaks); }
+
 cudaError_t launch_linear_slopes(const LinearGradProblem &p, void *dz, int64_t ldz, bool planes,
-                                 float *partial, const DeviceInfo &, cudaStream_t stream) {
-  if (p.dtype == TMM_BF16) return launch_as<__nv_bfloat16>(p, dz, ldz, planes, partial, stream);
-  if (p.dtype == TMM_F16) return launch_as<__half>(p, dz, ldz, planes, partial, stream);
-  return launch_as<float>(p, dz, ldz, planes, partial, stream);
+                                 float *unscale, float *partial, const DeviceInfo &,
+                                 cudaStream_t stream) {
+  if (p.dtype == TMM_BF16)
+    return launch_as<__nv_bfloat16>(p, dz, ldz, planes, nullptr, partial, stream);
+  if (p.dtype == TMM_F16) return launch_as<__half>(p, dz, ldz, planes, unscale, partial, stream);
+  return launch_as<float>(p, dz, ldz, planes, nullptr, partial, stream);
 }
 
 }  // namespace tmm
