@@ -135,3 +135,28 @@ def test_half_gradients_in_a_graph_follow_new_sizes_of_dy():
         for a, b in zip(got, work()):
             assert torch.equal(a, b)
     tmm.check_device()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("kind", ("relu",) + SMOOTH)
+@pytest.mark.parametrize("M", [4, 40])
+def test_slopes_at_infinities(dtype, kind, M):
+    """1 and 0, as far out."""
+    z = torch.tensor([math.inf, -math.inf, 60000.0, -60000.0]).to(dtype)
+    z = z.repeat(M // 4)[:, None].expand(-1, 24).contiguous().cuda()
+    dy, one = torch.full((M, 24), 3.0, dtype=dtype), torch.eye(24, dtype=dtype)
+    g = tmm.gemm_bias_act_grad(dy.cuda(), None, one.cuda(), pre=z, act=kind, dw=False, dbias=True)
+    want = torch.tensor([3.0, 0.0, 3.0, 0.0]).repeat(M // 4)[:, None].expand(-1, 24)
+    assert torch.equal(g.dx.float().cpu(), want)
+    assert torch.equal(g.dbias.cpu(), want.sum(0))
+
+
+@pytest.mark.parametrize("kind", ("relu",) + SMOOTH)
+def test_half_layer_below_the_range_has_no_gradient(kind):
+    """z = -70000 is kept as -inf; y is 0 there, and so is its slope."""
+    M, N, K = 40, 72, 16
+    x, w = torch.full((M, K), -70.0, dtype=F16).cuda(), torch.full((K, N), 62.5, dtype=F16).cuda()
+    y, z = tmm.gemm_bias_act(x, w, act=kind, pre=True)
+    assert not bool(y.any()) and bool((z == -math.inf).all())
+    g = tmm.gemm_bias_act_grad(torch.ones_like(y), x, w, pre=z, act=kind, dbias=True)
+    assert not any(bool(t.any()) for t in g)

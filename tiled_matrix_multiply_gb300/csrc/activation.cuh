@@ -13,7 +13,7 @@
 //   4096 in bf16 190 us, without activation 154.
 // FAST, for results of 16 bits: exponentials by the hardware's power of two with a rounded argument
 // (relative error 2^-22 and |z| 2^-24, far below 2^-12).  Else the argument's rounding is made up for.
-// Infinities and NaN are the formulas'.
+// Infinities and NaN are the formulas', those of the derivatives at infinities their limits.
 #pragma once
 
 #include <cstdint>
@@ -131,7 +131,8 @@ __device__ __forceinline__ uint64_t activate2(int act, uint64_t z) {
     default: return z;
   }
 }
-// The derivatives at z.
+// The derivatives at z.  They are 0 and 1 but for less than any FP32 value beyond 200 (gelu 64), and so at
+// infinities, which a kept z of FP16 is from 65520 on.
 template <bool FAST>
 __device__ __forceinline__ uint64_t slope2(int act, uint64_t z) {
   float2 f = of_pair(z);
@@ -139,10 +140,13 @@ __device__ __forceinline__ uint64_t slope2(int act, uint64_t z) {
   switch (act) {
     case TMM_ACT_RELU: return pair_of(f.x > 0.0f ? 1.0f : 0.0f, f.y > 0.0f ? 1.0f : 0.0f);
     case TMM_ACT_SILU: {
+      z = pair_of(within(f.x, -200.0f, 200.0f), within(f.y, -200.0f, 200.0f));
       const uint64_t s = logistic<FAST>(mul2(z, minus));
       return mul2(s, fma2(z, fma2(s, minus, one), one));
     }
     case TMM_ACT_GELU: {
+      f = make_float2(within(f.x, -64.0f, 64.0f), within(f.y, -64.0f, 64.0f));
+      z = pair_of(f.x, f.y);
       uint64_t e;
       const float2 tail = of_pair(normal_tail<FAST>(pair_of(fabsf(f.x), fabsf(f.y)), e));
       return fma2(mul2(z, both(0.39894228f)), e,
