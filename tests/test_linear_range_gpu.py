@@ -160,3 +160,15 @@ def test_half_layer_below_the_range_has_no_gradient(kind):
     assert not bool(y.any()) and bool((z == -math.inf).all())
     g = tmm.gemm_bias_act_grad(torch.ones_like(y), x, w, pre=z, act=kind, dbias=True)
     assert not any(bool(t.any()) for t in g)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("kind", ("relu",) + SMOOTH)
+def test_slopes_at_nan_are_nan(dtype, kind):
+    z = torch.ones(20, 24, dtype=dtype)
+    z[7, 3] = math.nan
+    dy, one = torch.ones(20, 24, dtype=dtype), torch.eye(24, dtype=dtype)
+    g = tmm.gemm_bias_act_grad(dy.cuda(), None, one.cuda(), pre=z.cuda(), act=kind, dw=False,
+                               dbias=True)
+    assert bool(g.dx[7].isnan().all()) and bool(g.dbias[3].isnan())
+    assert int(g.dx.isnan().sum()) == 24 and int(g.dbias.isnan().sum()) == 1

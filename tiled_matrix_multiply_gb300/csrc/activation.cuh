@@ -138,7 +138,9 @@ __device__ __forceinline__ uint64_t slope2(int act, uint64_t z) {
   float2 f = of_pair(z);
   const uint64_t one = both(1.0f), minus = both(-1.0f);
   switch (act) {
-    case TMM_ACT_RELU: return pair_of(f.x > 0.0f ? 1.0f : 0.0f, f.y > 0.0f ? 1.0f : 0.0f);
+    case TMM_ACT_RELU:      // (of NaN NaN)
+      return pair_of(f.x > 0.0f ? 1.0f : positive_part(f.x),
+                     f.y > 0.0f ? 1.0f : positive_part(f.y));
     case TMM_ACT_SILU: {
       z = pair_of(within(f.x, -200.0f, 200.0f), within(f.y, -200.0f, 200.0f));
       const uint64_t s = logistic<FAST>(mul2(z, minus));
