@@ -599,8 +599,8 @@ dense_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
         if (n == 0) break;      // (an empty sum: K = 0)
       }
       commit_if<CG>(on, bar_drain, head);
+      if (!warp_wait(bar_drain, 0u, p.wait_limit_ns)) timed_out = true;
     }
-    if (!warp_wait(bar_drain, 0u, p.wait_limit_ns)) timed_out = true;
   } else {
     // ---- results ----
     const int quarter = warp & 3, turn = (warp - kEpi0) >> 2;
@@ -784,6 +784,12 @@ dense_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ 
     const uint64_t t0 = timer_ns();
     while (timer_ns() - t0 < 1000 * 1000) {
     }
+  }
+  if (CG == 2 && warp == 1 && !leader) {
+    // The last arrival from the leader's products, which this block's result warps have all waited for by
+    // now: with the loops above it would be a wait of the whole call.
+    if (!warp_wait(bar_drain, 0u, p.wait_limit_ns) && lane == 0) atomicOr(&g_linear_status, 2u);
+    __syncwarp();
   }
   // Neither block uses tensor memory or the other's barriers.  (Every remote arrival has been waited
   // for, so that the order of execution is enough; a release would wait for the results to reach memory.)
