@@ -1113,7 +1113,7 @@ cudaError_t launch_linear_grad(const LinearGradProblem &p, const DeviceInfo &dev
   ws += g.unscale_bytes;
   if (g.make_dz || p.dbias) {
     e = launch_linear_slopes(p, g.make_dz ? made : nullptr, g.ldz, g.dz_planes, unscale,
-                             reinterpret_cast<float *>(ws), dev, stream);
+                             reinterpret_cast<float *>(ws), stream);
     if (e != cudaSuccess) return e;
   }
   ws += g.partial_bytes;

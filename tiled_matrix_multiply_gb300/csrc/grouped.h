@@ -120,8 +120,7 @@ cudaError_t launch_linear_grad(const LinearGradProblem &p, const DeviceInfo &dev
 size_t linear_bias_bytes(int64_t rows, int64_t N, int dtype);
 size_t linear_unscale_bytes();
 cudaError_t launch_linear_slopes(const LinearGradProblem &p, void *dz, int64_t ldz, bool planes,
-                                 float *unscale, float *partial, const DeviceInfo &dev,
-                                 cudaStream_t stream);
+                                 float *unscale, float *partial, cudaStream_t stream);
 cudaError_t launch_grouped(const GroupedProblem &p, const DeviceInfo &dev, void *workspace,
                            cudaStream_t stream);
 cudaError_t launch_wgrad(const WgradProblem &p, const DeviceInfo &dev, void *workspace,

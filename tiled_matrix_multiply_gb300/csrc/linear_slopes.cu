@@ -230,11 +230,16 @@ runs_kernel(const float *__restrict__ sums, int64_t runs, int64_t N, float *__re
 }
 
 // Runs of rows: three blocks an SM, as many as fit at once, of 32 rows at least (4096 x 4096, gelu, bf16,
-// sums alone: 21 us, by four blocks 23; reading takes the memory 10 us, the erf bounds the rest).
+// sums alone: 19 us, by four blocks 23; reading takes the memory 10 us, and a warp asks for its next rows
+// only after the slopes of these).  Of 4096 rows at most, however wide the matrix: a thread adds an eighth
+// of a run one after another (65536 FP32 rows of 29312 in one run: off by up to 2046 half steps of the
+// sum, in runs by at most 530).  The number of SMs is that of the GPU this is built for and not asked:
+// workspaces and results then depend on the sizes alone.
+constexpr int kSMs = 152, kLongestRun = 4096, kMostRuns = 65535;      // (of a grid's second dimension)
 int64_t runs_of(int64_t rows, int64_t N, int dtype) {
   const int64_t strip = dtype == TMM_F32 ? 128 : 256, strips = (N + strip - 1) / strip;
-  const int64_t want = std::max<int64_t>(1, 3 * 152 / strips);
-  return std::max<int64_t>(1, std::min(want, (rows + 31) / 32));
+  const int64_t want = std::max<int64_t>(3 * kSMs / strips, (rows + kLongestRun - 1) / kLongestRun);
+  return std::max<int64_t>(1, std::min({want, (rows + 31) / 32, int64_t(kMostRuns)}));
 }
 
 bool aligned(const void *p, int64_t ld, int64_t size) {
@@ -307,8 +312,7 @@ size_t linear_bias_bytes(int64_t rows, int64_t N, int dtype) {
 size_t linear_unscale_bytes() { return sizeof(uint32_t) * (1 + kMaxPeaks); }
 
 cudaError_t launch_linear_slopes(const LinearGradProblem &p, void *dz, int64_t ldz, bool planes,
-                                 float *unscale, float *partial, const DeviceInfo &,
-                                 cudaStream_t stream) {
+                                 float *unscale, float *partial, cudaStream_t stream) {
   if (p.dtype == TMM_BF16)
     return launch_as<__nv_bfloat16>(p, dz, ldz, planes, nullptr, partial, stream);
   if (p.dtype == TMM_F16) return launch_as<__half>(p, dz, ldz, planes, unscale, partial, stream);
