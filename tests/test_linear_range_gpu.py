@@ -172,3 +172,20 @@ def test_slopes_at_nan_are_nan(dtype, kind):
                                dbias=True)
     assert bool(g.dx[7].isnan().all()) and bool(g.dbias[3].isnan())
     assert int(g.dx.isnan().sum()) == 24 and int(g.dbias.isnan().sum()) == 1
+
+
+def test_gelu_in_single_precision():
+    """y = max(z, 0) - |z| Phi(-|z|), one term a sum.  Of the tail, in units of 2^-24 of itself: t is off by
+    3 (a denominator's half step, and a reciprocal's whole one), which moves t q(t) by 2.4 times that; q's eight
+    steps by two of the sum of the terms' sizes, 2.4 q, each, 38; the fit by 0.4; z^2 / 2 by its own
+    half step; the exponential by 4 and 3 for its correction; three products by 3.  In all z^2 / 2 + 56.  y is
+    rounded once more, and below 2^-126 the exponential's result is 0."""
+    z = torch.cat([torch.linspace(-13, 13, 20001), torch.logspace(-20, 0, 500),
+                   -torch.logspace(-20, 0, 500)])
+    y = tmm.gemm_bias_act(z[:, None].cuda(), torch.ones(1, 24).cuda(), act="gelu").double().cpu()
+    zd = z.double()
+    tail = 0.5 * torch.erfc(zd.abs() * math.sqrt(0.5))
+    want = zd.clamp(min=0) - zd.abs() * tail
+    bound = (zd.abs() * tail * (zd * zd / 2 + 56) + want.abs()) * 2.0 ** -24 + 16 * 2.0 ** -126
+    off = (y - want[:, None]).abs() / bound[:, None]
+    assert float(off.max()) <= 1, float(off.max())

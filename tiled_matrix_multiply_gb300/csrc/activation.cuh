@@ -7,10 +7,11 @@
 //   gelu_tanh  z/2 (1 + tanh u) = z s(2 u),     u = sqrt(2/pi) (z + 0.044715 z^3)
 //   Phi(-a) = erfc(a / sqrt 2) / 2,  erfc(x) = e^(-x^2) t q(t),  t = 1 / (1 + c x):  x e^(x^2) erfc(x) tends
 //   to a constant, so that t q(t) stands for e^(x^2) erfc(x) with a bounded relative error everywhere.
-//   q is the polynomial whose largest relative error on [0, 10] is the smallest (a linear program over
-//   4001 points): of degree 7 and c = 0.45, 2^-21.7; of degree 8 and c = 0.5, 2^-24.6.  CUDA's erfcf has
-//   three times as many instructions and held the result warps up beyond the products: 8192 x 4096 x
-//   4096 in bf16 190 us, without activation 154.
+//   q is a polynomial whose largest relative error on [0, 10] is as small as FP32 coefficients let it be (a
+//   linear program over 4001 points; its coefficients rounded one after another, the rest fitted again
+//   each time; c the best of a few): of degree 7 and c = 0.432, 2^-23.2; of degree 8 and c = 0.4875,
+//   2^-25.4.  CUDA's erfcf has three times as many instructions and held the result warps up beyond the
+//   products: 8192 x 4096 x 4096 in bf16 190 us, without activation 154.
 // FAST, for results of 16 bits: exponentials by the hardware's power of two with a rounded argument
 // (relative error 2^-22 and |z| 2^-24, far below 2^-12).  Else the argument's rounding is made up for.
 // Infinities and NaN are the formulas', those of the derivatives at infinities their limits.
@@ -97,11 +98,12 @@ __device__ __forceinline__ uint64_t logistic(uint64_t v) {
 template <bool FAST>
 __device__ __forceinline__ uint64_t normal_tail(uint64_t a, uint64_t &e) {
   // The coefficients of q / 2, the highest first.
-  constexpr float few[8] = {0.03344145f, -0.120179255f, 0.10451595f, 0.020035585f,
-                            0.09439802f, 0.114010655f,  0.126823675f, 0.126954055f};
-  constexpr float more[9] = {-0.0291917f, 0.14065922f, -0.240339115f, 0.135458545f, -0.010982505f,
-                             0.100426475f, 0.121762545f, 0.14116206f, 0.141044465f};
-  const uint64_t t = reciprocal2(fma2(a, both(FAST ? 0.31819805f : 0.35355339f), both(1.0f)));
+  constexpr float few[8] = {0.0366231166f, -0.151907831f, 0.182719693f, -0.0356251895f,
+                            0.119878531f, 0.103872582f,  0.12260922f,  0.121829927f};
+  constexpr float more[9] = {-0.028188616f, 0.144669294f, -0.270742476f, 0.187449187f, -0.0376035161f,
+                             0.111842997f, 0.117160685f, 0.137906998f,  0.137505442f};
+  // (c / sqrt 2)
+  const uint64_t t = reciprocal2(fma2(a, both(FAST ? 0.305470139f : 0.34471455f), both(1.0f)));
   uint64_t q = both(FAST ? few[0] : more[0]);
 #pragma unroll
   for (int i = 1; i < (FAST ? 8 : 9); ++i) q = fma2(q, t, both(FAST ? few[i] : more[i]));
