@@ -635,7 +635,8 @@ int route_rows_grad(int dtype, int64_t tokens, int64_t experts, int64_t k, const
  * The logits are read once; sums are FP32.  Entries of -inf have probability 0 and are no
  * alternatives; where fewer than `top` others are left the last ids are -1, with -inf.  A row of
  * nothing else has lse and logprob -inf and entropy 0.  A row with NaN or +inf has NaN everywhere, and
- * ids of -1.  Masks of the type's lowest finite value count as that value.
+ * ids of -1; a padding token's logprob is 0 in such a row too.  Masks of the type's lowest finite value
+ * count as that value.
  * logits: DEVICE, rows x cols, row stride ld >= cols, no alignment beyond the type's (any cols).
  * tokens: DEVICE, integers of token_bits (32 or 64) bits, or NULL (logprob NULL too).  scale > 0;
  * 0 <= top <= 32 (0: top_ids and top_logprobs may be NULL); rows and cols below 2^29.  Outputs must

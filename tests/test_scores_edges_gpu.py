@@ -44,3 +44,23 @@ def test_route_odd_logits_of_experts_shut_by_their_bias(dtype, odd, E, shut):
         r = tmm.route_rows(x.cuda(), 4, score="sigmoid", **how)
         want = tmm.route_rows(clean.cuda(), 4, score="sigmoid", **how)
         assert torch.equal(r.experts, want.experts) and torch.equal(r.weights, want.weights)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("T,V", [(3, 9), (3, 9000), (1300, 513)])
+def test_padding_in_rows_that_are_not_finite(dtype, T, V):
+    """A padding token's log probability is 0 whatever its row's logits; the row's other results are NaN."""
+    x = torch.randn(T, V, generator=torch.Generator().manual_seed(1)).to(dtype)
+    x[0, V // 2], x[1, V - 1] = NAN, INF
+    tokens = torch.zeros(T, dtype=torch.int64)
+    tokens[0], tokens[1] = -100, V
+    for top in (0, 3):
+        p = tmm.logprob_rows(x.cuda(), tokens.cuda(), top=top)
+        assert p.logprob[:2].tolist() == [0.0, 0.0] and bool(p.logprob[2:].isfinite().all())
+        assert bool(p.lse[:2].isnan().all() and p.entropy[:2].isnan().all())
+        if top:
+            assert bool(p.top_logprobs[:2].isnan().all()) and bool((p.top_ids[:2] == -1).all())
+    # Without a gradient of their own such rows get zeros.
+    g = torch.ones(T, device="cuda")
+    d = tmm.logprob_rows_grad(x.cuda(), tokens.cuda(), p.lse, dlogprob=g)
+    assert not bool(d[:2].any()) and bool(d.isfinite().all())
