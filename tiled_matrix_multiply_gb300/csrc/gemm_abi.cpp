@@ -870,8 +870,7 @@ int check_outputs(const char *who, const Bytes *r, int outs, int count) {
   return TMM_OK;
 }
 
-int check_route(const char *who, int64_t tokens, int64_t experts, int64_t k, int score,
-                int renormalise) {
+int check_route(const char *who, int64_t experts, int64_t k, int score, int renormalise) {
   if (experts < 1 || experts > tmm::kMaxExperts)
     return fail(TMM_ERR_INVALID_ARG, "%s: need 1 <= experts <= %d (experts=%lld)", who,
                 tmm::kMaxExperts, (long long)experts);
@@ -882,7 +881,6 @@ int check_route(const char *who, int64_t tokens, int64_t experts, int64_t k, int
     return fail(TMM_ERR_INVALID_ARG, "%s: unknown score %d", who, score);
   if (renormalise != 0 && renormalise != 1)
     return fail(TMM_ERR_INVALID_ARG, "%s: renormalise must be 0 or 1", who);
-  (void)tokens;
   return TMM_OK;
 }
 
@@ -905,7 +903,7 @@ int route_rows(int dtype, int64_t tokens, int64_t experts, const void *logits, i
   const char *who = "route_rows";
   int rc;
   if ((rc = check_scores(who, "logits", dtype, tokens, experts, logits, ld)) != TMM_OK ||
-      (rc = check_route(who, tokens, experts, k, score, renormalise)) != TMM_OK ||
+      (rc = check_route(who, experts, k, score, renormalise)) != TMM_OK ||
       (rc = check_scale(who, scale, false)) != TMM_OK)
     return rc;
   if (groups < 1 || groups > tmm::kMaxRouteGroups || experts % groups != 0 || top_groups < 1 ||
@@ -959,7 +957,7 @@ int route_rows_grad(int dtype, int64_t tokens, int64_t experts, int64_t k, const
   int rc;
   if ((rc = check_scores(who, "logits", dtype, tokens, experts, logits, ld)) != TMM_OK ||
       (rc = check_scores(who, "dlogits", dtype, tokens, experts, dlogits, ldd)) != TMM_OK ||
-      (rc = check_route(who, tokens, experts, k, score, renormalise)) != TMM_OK ||
+      (rc = check_route(who, experts, k, score, renormalise)) != TMM_OK ||
       (rc = check_scale(who, scale, false)) != TMM_OK ||
       (rc = check_array(who, "dweights", dweights, tokens)) != TMM_OK ||
       (rc = check_array(who, "chosen", chosen, tokens)) != TMM_OK)
@@ -1078,7 +1076,7 @@ int logprob_rows_grad(int dtype, int64_t rows, int64_t cols, const void *logits,
   p.dtop = top > 0 ? dtop : nullptr;
   p.dlogits = dlogits;
   p.ldd = ldd;
-  const cudaError_t e = tmm::launch_logprob_grad(p, dev, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = tmm::launch_logprob_grad(p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(TMM_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
   return TMM_OK;
 }

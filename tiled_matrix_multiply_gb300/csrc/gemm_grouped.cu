@@ -1938,8 +1938,6 @@ bool in_place(const Stack &s, int dtype) {
   return dtype != TMM_F32 && on16(s, 2);
 }
 
-size_t round256(size_t b) { return (b + 255) / 256 * 256; }
-
 // Bytes of an operand's planes in the workspace (0: read in place), or SIZE_MAX; `gathered`:
 // rows fetched through the row index (0: none).
 size_t plane_bytes(const Stack &s, int dtype, int64_t gathered = 0) {
@@ -1947,15 +1945,6 @@ size_t plane_bytes(const Stack &s, int dtype, int64_t gathered = 0) {
   const __int128 n = __int128(dtype == TMM_F32 ? 6 : 2) * s.count *
                      (gathered ? gathered : s.rows) * round8(s.cols);
   return n > __int128(INT64_MAX / 4) ? SIZE_MAX : round256(size_t(n));
-}
-
-size_t add_sizes(std::initializer_list<size_t> sizes) {
-  size_t t = 0;
-  for (size_t s : sizes) {
-    if (s == SIZE_MAX) return SIZE_MAX;
-    t += s;      // each is at most 2^61, and there are at most five
-  }
-  return t;
 }
 
 // The operand in place, or a job that makes its planes in *ws (which advances past them);

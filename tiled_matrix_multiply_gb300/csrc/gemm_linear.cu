@@ -37,12 +37,12 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
-#include <initializer_list>
 #include <mutex>
 #include <type_traits>
 
 #include "activation.cuh"
 #include "grouped.h"
+#include "row_ops.cuh"
 #include "tensor_core.cuh"
 #include "tmm_gemm.h"
 
@@ -132,16 +132,6 @@ __device__ __forceinline__ float bias_at(const DenseParams &p, int n) {
   if (p.bias_f32) return static_cast<const float *>(p.bias)[n];
   return float(static_cast<const typename Kind<KIND>::T *>(p.bias)[n]);
 }
-template <typename T>
-__device__ __forceinline__ T to_type(float v);
-template <>
-__device__ __forceinline__ float to_type<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 to_type<__nv_bfloat16>(float v) {
-  return __float2bfloat16_rn(v);
-}
-template <>
-__device__ __forceinline__ __half to_type<__half>(float v) { return __float2half_rn(v); }
 template <int KIND>
 __device__ __forceinline__ uint32_t pack_results(float lo, float hi) {
   uint32_t w;
@@ -171,7 +161,7 @@ __device__ __forceinline__ void finish_four(const DenseParams &p, int64_t row, i
     if (!whole) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (n + k < p.N) to[k] = to_type<T>(z[k]);
+        if (n + k < p.N) to[k] = rounded<T>(z[k]);
     } else if constexpr (KIND == kF32) {
       *reinterpret_cast<float4 *>(to) = make_float4(z[0], z[1], z[2], z[3]);
     } else {
@@ -234,7 +224,7 @@ __device__ __forceinline__ void finish_lanes(const DenseParams &p, int64_t row0,
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const float2 f = of_pair(z[j >> 1]);
-      if (j < count) pre[j * p.ld_pre] = to_type<T>(j & 1 ? f.y : f.x);
+      if (j < count) pre[j * p.ld_pre] = rounded<T>(j & 1 ? f.y : f.x);
     }
   }
   activate_pairs<KIND != kF32>(p.act, z);
@@ -242,7 +232,7 @@ __device__ __forceinline__ void finish_lanes(const DenseParams &p, int64_t row0,
   for (int j = 0; j < 16; ++j) {
     const float2 f = of_pair(z[j >> 1]);
     const float y = j & 1 ? f.y : f.x;
-    if (j < count) out[j * p.ld_out] = to_type<T>(p.residual ? y + r[j] : y);
+    if (j < count) out[j * p.ld_out] = rounded<T>(p.residual ? y + r[j] : y);
   }
 }
 
@@ -1016,17 +1006,6 @@ cudaError_t launch_dense(const DenseProblem &p, const DeviceInfo &dev, cudaStrea
   return s.cg == 2 ? launch_as<2, kF32>(p, s, dev, stream) : launch_as<1, kF32>(p, s, dev, stream);
 }
 
-size_t round256(size_t b) { return (b + 255) / 256 * 256; }
-// SIZE_MAX: the count does not fit.
-size_t sum_of(std::initializer_list<size_t> sizes) {
-  size_t t = 0;
-  for (size_t s : sizes) {
-    if (s == SIZE_MAX) return SIZE_MAX;
-    t += s;      // each is at most 2^61, and there are few
-  }
-  return t;
-}
-
 // dz in the workspace: of the type, on 16-byte rows, or (FP32) as planes.  FP32 of few rows: dx from
 // FP32 values, whose planes dw takes.  FP16: times a power of two, unless it is dy or 0 (relu).
 struct GradPlan {
@@ -1052,11 +1031,12 @@ GradPlan plan_grad(const LinearGradProblem &p) {
   g.unscale_bytes = g.scaled ? round256(linear_unscale_bytes()) : 0;
   g.partial_bytes = p.dbias ? round256(linear_bias_bytes(p.rows, p.N, p.dtype)) : 0;
   const bool planes = p.dw || (p.dx && !g.few);
-  g.bytes = sum_of({g.dz_bytes, g.unscale_bytes, g.partial_bytes,
-                    planes && !(g.make_dz && !g.few) ? planes_bytes(dz_stack(p, g, nullptr), p.dtype)
-                                                     : 0,
-                    p.dx && !g.few ? planes_bytes(p.w, p.dtype) : 0,
-                    p.dw ? planes_bytes(p.x, p.dtype) : 0});
+  g.bytes = add_sizes({g.dz_bytes, g.unscale_bytes, g.partial_bytes,
+                       planes && !(g.make_dz && !g.few)
+                           ? planes_bytes(dz_stack(p, g, nullptr), p.dtype)
+                           : 0,
+                       p.dx && !g.few ? planes_bytes(p.w, p.dtype) : 0,
+                       p.dw ? planes_bytes(p.x, p.dtype) : 0});
   return g;
 }
 
@@ -1068,7 +1048,7 @@ bool linear_is_few(int dtype, int64_t rows) { return dtype == TMM_F32 && rows <=
 
 size_t linear_workspace_bytes(const LinearProblem &p) {
   if (p.K == 0 || linear_is_few(p.dtype, p.rows)) return 0;
-  return sum_of({planes_bytes(p.x, p.dtype), planes_bytes(p.w, p.dtype)});
+  return add_sizes({planes_bytes(p.x, p.dtype), planes_bytes(p.w, p.dtype)});
 }
 
 cudaError_t launch_linear(const LinearProblem &p, const DeviceInfo &dev, void *workspace,

@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <initializer_list>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -102,6 +103,16 @@ cudaError_t make_operand_planes(const Stack *const *operands, Planes *planes, in
 cudaError_t linear_device_status(unsigned int *status, bool clear);
 void linear_set_test_hooks(int drop_block, int64_t wait_limit_ns);
 
+// A workspace's parts start on 256-byte boundaries; SIZE_MAX: the count does not fit.
+inline size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+inline size_t add_sizes(std::initializer_list<size_t> sizes) {
+  size_t t = 0;
+  for (size_t s : sizes) {
+    if (s == SIZE_MAX) return SIZE_MAX;
+    t += s;      // each is at most 2^61, and there are at most six
+  }
+  return t;
+}
 // Workspace bytes (0: none needed; SIZE_MAX: the count does not fit in size_t).
 size_t grouped_workspace_bytes(const GroupedProblem &p);
 size_t wgrad_workspace_bytes(const WgradProblem &p);

@@ -687,8 +687,7 @@ cudaError_t launch_logprob(const LogprobProblem &p, const DeviceInfo &dev, cudaS
   return launch_logprob_as<float>(p, dev, stream);
 }
 
-cudaError_t launch_logprob_grad(const LogprobGradProblem &p, const DeviceInfo &,
-                                cudaStream_t stream) {
+cudaError_t launch_logprob_grad(const LogprobGradProblem &p, cudaStream_t stream) {
   if (p.dtype == TMM_BF16) return launch_logprob_grad_as<__nv_bfloat16>(p, stream);
   if (p.dtype == TMM_F16) return launch_logprob_grad_as<__half>(p, stream);
   return launch_logprob_grad_as<float>(p, stream);

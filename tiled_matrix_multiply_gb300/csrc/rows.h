@@ -75,7 +75,6 @@ struct LogprobGradProblem {
   int64_t ldd;
 };
 cudaError_t launch_logprob(const LogprobProblem &p, const DeviceInfo &dev, cudaStream_t stream);
-cudaError_t launch_logprob_grad(const LogprobGradProblem &p, const DeviceInfo &dev,
-                                cudaStream_t stream);
+cudaError_t launch_logprob_grad(const LogprobGradProblem &p, cudaStream_t stream);
 
 }  // namespace tmm
