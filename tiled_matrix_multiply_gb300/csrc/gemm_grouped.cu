@@ -1822,11 +1822,9 @@ constexpr int kRowRanks = 16;            // values of u a block makes
 // first tiles are on their way meanwhile.
 template <typename T, bool TRANS_A, bool VEC>
 __global__ void __launch_bounds__(kRowThreads)
-row_ranks_kernel(const T *__restrict__ x, int64_t ldx, int64_t x_rows,
-                 const int *__restrict__ row_index, const int *__restrict__ offsets, int groups,
-                 const T *__restrict__ a, int64_t lda, int64_t stride_a,
-                 const float *__restrict__ scale, int K, int rank, float *__restrict__ u,
-                 int64_t ldu) {
+row_ranks_kernel(const T *x, int64_t ldx, int64_t x_rows, const int *row_index, const int *offsets,
+                 int groups, const T *a, int64_t lda, int64_t stride_a, const float *scale, int K,
+                 int rank, float *__restrict__ u, int64_t ldu) {
   grid_wait();
   grid_start_next();
   __shared__ float sums[kRowThreads / 32][kRowRanks];

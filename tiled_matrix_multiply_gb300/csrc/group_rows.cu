@@ -30,7 +30,9 @@ __device__ __forceinline__ int key_of(const void *index, int64_t s, int groups) 
   return v >= 0 && v < groups ? int(v) : groups;
 }
 
-// Programmatic dependent launch: wait for the launch before, then let the next one start.
+// Programmatic dependent launch: wait for the launch before, then let the next one start.  (What that
+// launch wrote is no constant of this kernel, which runs already: no __restrict__ for what is read, whose
+// loads could take the read-only path.)
 __device__ __forceinline__ void grid_wait() {
   asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -38,7 +40,7 @@ __device__ __forceinline__ void grid_wait() {
 // h[b][g] for g <= groups.
 template <typename T>
 __global__ void __launch_bounds__(1024)
-count_kernel(const void *__restrict__ index, int64_t slots, int64_t chunk, int groups,
+count_kernel(const void *index, int64_t slots, int64_t chunk, int groups,
              int *__restrict__ counts) {
   __shared__ int h[kMaxGroups + 1];
   grid_wait();
@@ -56,8 +58,8 @@ count_kernel(const void *__restrict__ index, int64_t slots, int64_t chunk, int g
 // (groups + 1 each), then a count per warp and group.
 template <typename T>
 __global__ void __launch_bounds__(1024)
-place_kernel(const void *__restrict__ index, int64_t slots, int64_t chunk, int fan, int groups,
-             const int *__restrict__ counts, int *__restrict__ offsets, int *__restrict__ order,
+place_kernel(const void *index, int64_t slots, int64_t chunk, int fan, int groups,
+             const int *counts, int *__restrict__ offsets, int *__restrict__ order,
              int *__restrict__ rows, int *__restrict__ position) {
   extern __shared__ int sh[];
   const int G = groups + 1;

@@ -111,7 +111,7 @@ few_kernel(const __grid_constant__ FewParams p, int split) {
           const float *const from = p.w + int64_t(begin + at) * p.ldw + n0;
           if (p.vec) {
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (at < run && n0 + 4 * lane < p.N) v = __ldg(reinterpret_cast<const float4 *>(from) + lane);
+            if (at < run && n0 + 4 * lane < p.N) v = reinterpret_cast<const float4 *>(from)[lane];
             w[u][0] = v.x;
             w[u][1] = v.y;
             w[u][2] = v.z;
@@ -119,7 +119,7 @@ few_kernel(const __grid_constant__ FewParams p, int split) {
           } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              w[u][i] = at < run && n0 + lane + 32 * i < p.N ? __ldg(from + lane + 32 * i) : 0.0f;
+              w[u][i] = at < run && n0 + lane + 32 * i < p.N ? from[lane + 32 * i] : 0.0f;
           }
         }
 #pragma unroll
@@ -139,12 +139,12 @@ few_kernel(const __grid_constant__ FewParams p, int split) {
           next[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           if (n >= p.N || k >= run) continue;
           if (p.vec && k + at + 4 <= run) {
-            next[j] = __ldg(reinterpret_cast<const float4 *>(from));
+            next[j] = *reinterpret_cast<const float4 *>(from);
           } else {
-            if (k + at < run) next[j].x = __ldg(from);
-            if (k + at + 1 < run) next[j].y = __ldg(from + 1);
-            if (k + at + 2 < run) next[j].z = __ldg(from + 2);
-            if (k + at + 3 < run) next[j].w = __ldg(from + 3);
+            if (k + at < run) next[j].x = from[0];
+            if (k + at + 1 < run) next[j].y = from[1];
+            if (k + at + 2 < run) next[j].z = from[2];
+            if (k + at + 3 < run) next[j].w = from[3];
           }
         }
       };

@@ -48,8 +48,8 @@ constexpr int kPeakAhead = 8;          // loads of a warp in flight
 // rows start on 16-byte boundaries (a matrix without gaps is one row).
 template <bool VEC>
 __global__ void __launch_bounds__(32 * kWarps)
-peaks_kernel(const uint16_t *__restrict__ dy, int64_t rows, int64_t N, int64_t ld, int64_t strips,
-             int64_t down, int64_t across, uint32_t *__restrict__ peaks) {
+peaks_kernel(const uint16_t *dy, int64_t rows, int64_t N, int64_t ld, int64_t strips,
+             int64_t down, int64_t across, uint32_t *peaks) {
   constexpr int W = kPeakStrip / 32;
   __shared__ uint32_t part[kWarps];
   wait_then_start_next();
@@ -67,13 +67,13 @@ peaks_kernel(const uint16_t *__restrict__ dy, int64_t rows, int64_t N, int64_t l
       const uint16_t *const from = dy + r * ld + c;
       v[u] = make_uint4(0, 0, 0, 0);
       if (VEC && r < rows && c + W <= N) {
-        v[u] = __ldg(reinterpret_cast<const uint4 *>(from));
+        v[u] = *reinterpret_cast<const uint4 *>(from);
       } else {
         constexpr int kNext = VEC ? 1 : 32;
 #pragma unroll
         for (int k = 0; k < W; ++k)
           if (r < rows && c + kNext * k < N)
-            reinterpret_cast<uint16_t *>(&v[u])[k] = __ldg(from + kNext * k);
+            reinterpret_cast<uint16_t *>(&v[u])[k] = from[kNext * k];
       }
       r += down;
       if ((s += across) >= strips) {
@@ -213,7 +213,7 @@ slopes_kernel(const __grid_constant__ SlopeParams p) {
 
 // dbias[n] = the runs' sums, 32 columns a block and eight threads a column.
 __global__ void __launch_bounds__(256)
-runs_kernel(const float *__restrict__ sums, int64_t runs, int64_t N, float *__restrict__ dbias) {
+runs_kernel(const float *sums, int64_t runs, int64_t N, float *dbias) {
   __shared__ float part[8][32];
   wait_then_start_next();
   const int c = threadIdx.x & 31, w = threadIdx.x >> 5;

@@ -268,7 +268,7 @@ logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
       const int i = first + u * threads + tid;
       const uint32_t b = lowest_bits<T>();
       v[u].w = make_uint4(b, b, b, b);
-      if (i < v1) v[u].w = __ldg(body + i);
+      if (i < v1) v[u].w = body[i];
     }
   };
   const int step = kAhead * threads;
@@ -406,7 +406,7 @@ logprob_kernel(const __grid_constant__ LogprobProblem p, int cluster) {
           const int i = first + r * step;
           if (i >= v1) break;
           Vec<T> w;
-          w.w = __ldg(body + i);
+          w.w = body[i];
           if (!(max_of(w) >= bound)) continue;
 #pragma unroll
           for (int k = 0; k < W; ++k) note(w.get(k), head + i * W + k);

@@ -47,7 +47,9 @@ __device__ __forceinline__ float Vec<__nv_bfloat16>::get(int i) const {
 }
 
 // Programmatic dependent launch: the launches before are complete and visible after it, and the
-// next one may start as soon as there is room (it waits in turn).
+// next one may start as soon as there is room (it waits in turn).  What the launches before wrote is no
+// constant of the kernel, which runs already while they do: its inputs are read by plain loads, not
+// by __ldg or through pointers to const that are __restrict__, which may take the read-only path.
 __device__ __forceinline__ void wait_then_start_next() {
   asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
 }
