@@ -27,9 +27,11 @@
 // thread's), sixteen take results out (with eight the results of a tile of one slice took 3.9 us, with
 // sixteen 2.9).  Every wait is bounded (globaltimer); on timeout bit 1 of the status word is set and the
 // kernel runs to its end.
-// Measured (us): 8192 x 4096 x 4096 in bf16 plain 140 (1.96 PFLOP/s; a library's product 138), with gelu,
-// residual and z kept 151 to 159; 512 x 4096 x 4096 17; one row 8.3, where reading the weights takes 5.0;
-// FP32 4096^3 with gelu and residual 492, six bf16 products at the library's rate 428.
+// Measured (us, kernels alone, replayed from a graph): 8192 x 4096 x 4096 in bf16 plain 140 (1.96 PFLOP/s; a
+// library's product 138), with gelu, residual and z kept 151 to 159 (called again and again, which the
+// card's power slows down, 177 to 184); 512 x 4096 x 4096 16 to 17 (a library's 13.3); one row 8.3, where
+// reading the weights takes 5.0; FP32 4096^3 with gelu and residual 492, six bf16 products at the library's
+// rate 428.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -21,7 +21,10 @@
 // complement, so that the larger key is the larger value or the lower number) is put in order by counting
 // for each how many are larger.  So the pass is the one without alternatives, and the selection comes
 // after it.  Rows of which too many values reach the bound (thousands of equal ones) are read again
-// whole, by lists that are kept sorted.  (With such lists in the pass itself, under thresholds of various
+// whole, by lists that are kept sorted: rows of equal logits (4096 x 131072 with 20 listed 2140 us, 32 rows 28),
+// and those whose visible values lie in fewer threads' vectors than the bound is made of, the rest the type's
+// lowest value (40 values far apart: as equal ones; a run of 2 % of the row: 214 and 28; with -inf in place
+// of the lowest value 215 and 10).  (With such lists in the pass itself, under thresholds of various
 // kinds, 4096 rows of 131072 with 20 listed took 320 to 520 us, 213 now; the pass alone takes 161, the
 // memory's time.)
 //

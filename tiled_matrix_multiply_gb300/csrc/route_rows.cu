@@ -11,10 +11,11 @@
 //
 // A warp does a row, all of whose values stay in registers: with G groups rounded up to a power of
 // two every group has 32 / G lanes, so that a group's best are a butterfly within its lanes.  The
-// choice is k + 1 rounds of one warp reduction over keys that hold a value and its number.  The
-// instructions of a row (900 at 256 experts in 8 groups), in chains of reductions and shuffles, are the
-// bound (16384 rows of 256 FP32 logits, k = 8: plain 14 us, sigmoids and a bias 17, in 8 groups 21 to
-// 23; reading takes 2.7).  Neither more rows in flight (40 or 48 warps an SM: within 2 us, either way)
+// choice is k + 1 rounds of one warp reduction over keys that hold a value and its number.  A row's
+// instructions (930 at 256 experts in 8 groups: 13 us of issue slots) and the chains of reductions and
+// shuffles that they stand in, at 43 % of the warps that an SM holds, take the time (16384 rows of 256 FP32
+// logits, k = 8, by replays of a graph: plain 14 us, sigmoids and a bias 17, in 8 groups 21 to 23; reading
+// takes 2.7).  Neither more rows in flight (40 or 48 warps an SM: within 2 us, either way)
 // nor blocks of another size help (one or two rows a block: 8 experts 17 and 9 us in place of 7; eight:
 // the same).
 // Gradient: w depends on the chosen logits alone, but for the softmax without renormalisation;
@@ -562,7 +563,9 @@ __device__ __forceinline__ float score_of(bool is_sigmoid, bool renormalise, flo
   return none ? 0.0f : s / total;
 }
 
-// (64 registers a thread: the 64-bit choice would take 96 and leave fewer rows in flight.)
+// (64 registers a thread for up to 8 values a lane: the choice in pairs would take 96 and leave fewer rows in
+// flight.  As it is it keeps some in memory, 28 to 56 bytes a thread at 8 values and up to 340 at 32, in a row in a
+// thousand.)
 template <typename T, bool VEC, int V>
 __global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 8 : V <= 16 ? 5 : 3)
 route_kernel(const __grid_constant__ RouteProblem p) {

@@ -95,7 +95,8 @@ def route_rows(logits, k, bias=None, score="softmax", groups=1, top_groups=1, gr
     equal groups are chosen, a group's value being the sum of its ``group_best`` (1 or 2) largest c;
     ties go to the lower number.  weights = scale * s / (sum of the chosen s), without
     ``renormalise`` scale * s.  An expert whose logit or bias is -inf is never chosen; where none is
-    left the expert is -1 and its weight 0.
+    left the expert is -1 and its weight 0.  A row with NaN or +inf has NaN weights under the softmax,
+    at whichever expert; under sigmoids one with NaN at an expert whose bias is not -inf.
     """
     if stream is None:
         done = _usual.route(logits, k, bias, _SCORES.get(score, -1), groups, top_groups, group_best,
