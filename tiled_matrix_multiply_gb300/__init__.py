@@ -18,7 +18,8 @@ products whose right-hand matrix is chosen row by row; ``route_rows``
 (``scores.py``) chooses the experts that they are grouped by, ``gemm_bias_act``
 (``linear.py``) is the product with one matrix for all rows, bias, activation
 and residual in its epilogue, and ``logprob_rows`` (``scores.py``) reads the
-last one's logits; each has its gradient beside it.  All are asynchronous on the current torch stream of the operands' device.
+last one's logits; each has its gradient beside it.  All are asynchronous on
+the current torch stream of the operands' device.
 """
 from __future__ import annotations
 

@@ -116,9 +116,10 @@ def gemm_bias_act_grad(dy, x, w, pre=None, act="none", dx=True, dw=True, dbias=F
     """Gradients of ``gemm_bias_act`` from dy (M, N), as ``LinearGrads``.
 
     dz = dy act'(pre); dx = dz w^T, dw = x^T dz, dbias the sum of dz's rows in float32 (the
-    residual's gradient is dy).  dz is rounded to the type's bits, in float16 without its range.  pre: what ``gemm_bias_act`` kept (act "none" needs none).  dx, dw
-    and dbias: True, False, or a tensor for the result; a new dw is laid out as w is.  w may be None
-    without dx, and x without dw.
+    residual's gradient is dy).  dz is rounded to the type's bits for the products, in float16 without
+    that type's range.  pre: what ``gemm_bias_act`` kept (act "none" needs none).  dx, dw and dbias:
+    True, False, or a tensor for the result; a new dw is laid out as w is.  w may be None without dx,
+    and x without dw.
     """
     if dx is True and dw is True and workspace is None and stream is None:
         done = _usual.linear_grad(dy, x, w, pre, _ACTS.get(act, -1), dbias)

@@ -159,8 +159,8 @@ def logprob_rows(logits, tokens=None, top=0, scale=1.0, stream=None):
     """Log probabilities under the softmax of every row of ``scale * logits`` (rows, vocabulary).
 
     tokens: int64 or int32 (rows), each row's given token (outside the vocabulary, padding: its log
-    probability is 0, whatever the row's logits), or None.  top: how many of the most probable tokens to list, at most 32.
-    Returns ``RowLogprobs``.
+    probability is 0, whatever the row's logits), or None.  top: how many of the most probable tokens
+    to list, at most 32.  Returns ``RowLogprobs``.
     """
     if stream is None:
         done = _usual.logprob(logits, tokens, top, scale)
